@@ -498,6 +498,128 @@ spec_status spec_commit_rollback(int32_t B, const spec_state_desc *st,
                                  const spec_accept_out *acc, const int32_t *k, int32_t mode,
                                  int32_t *commit_status, spec_stream_t stream);
 
+/*
+ * The trunk's token mixers (DS4Server issue #98, section "Implementation": gated delta rows of the
+ * verify pass are snapshotted and their accepted rows kept or replayed, rejected attention rows are
+ * dropped): what writes the state that spec_commit_rollback commits, and what reads the KV cache
+ * that it trims. The formulas are the operators' own; the pages give no form.
+ *
+ * Gated delta rule. One recurrent layer, per value head the state S [rec_dk][rec_dv] float32 of
+ * spec_state_desc; a token with query q, key k (rec_dk each), value v (rec_dv), log decay g <= 0
+ * and beta does
+ *     S~ = exp(g) S,   u = beta (v - S~^T k),   S' = S~ + k u^T,   o = scale S'^T q.
+ * That is the commit's replay step with a = exp(g), b = k, c = u. Keys and queries are taken as
+ * they are (a trunk that normalises them does so before).
+ *
+ *   dtype       of q, k, v and out: SPEC_BF16 or SPEC_F32. The state, g and beta are float32.
+ *   key_heads   Hk >= 1, divides rec_heads; value head h uses key head h / (rec_heads / Hk).
+ *   q, k        row t of the call at q + t*q_stride (elements): [Hk][rec_dk], heads contiguous.
+ *   v, out      row t at v + t*v_stride: [rec_heads][rec_dv]. q, k and v may be column ranges of
+ *               one wider row. Strides are at least a row's width.
+ *   log_decay, beta   [rows][rec_heads] float32. -Inf clears the state.
+ */
+typedef struct {
+  spec_dtype dtype;
+  int32_t key_heads;
+  const void *q;
+  const void *k;
+  const void *v;
+  int64_t q_stride, k_stride, v_stride;
+  const float *log_decay;
+  const float *beta;
+  float scale;
+  void *out;
+  int64_t out_stride;
+} spec_delta_desc;
+
+/*
+ * spec_delta_rows -- the verify rows of one recurrent layer: row r of request b is input row
+ * b*R + r, run after the state the request holds, and the call leaves what the commit of the same
+ * mode reads (st and its layouts as for spec_commit_rollback):
+ *   SPEC_COMMIT_SNAPSHOT: from rec_live; slot 0 <- rec_live, slot r+1 <- the state after row r.
+ *   SPEC_COMMIT_REPLAY:   from rec_live; slot 0 <- rec_live, step_a, step_b, step_c of row r <-
+ *                         exp(g), k, u. Replaying them gives the snapshots' bytes.
+ *   SPEC_COMMIT_INDEX:    from slot live_slot[b]; slot (live_slot[b] + r + 1) mod n_slots <- the
+ *                         state after row r. A live_slot outside [0, n_slots): no row runs.
+ * Only the given layer's part of a slot (or of the steps) is written.
+ *   layer    in [0, rec_layers). rec_dk <= 256 (else SPEC_ERR_UNSUPPORTED), rec_dv a multiple of 4.
+ *   R        1..8 rows per request, R <= n_slots - 1.
+ *   n_rows   [B] int32 or NULL (R each): request b runs rows [0, n_rows[b]) (clamped to [0, R]);
+ *            its other rows' outputs are set to zero, their slots and steps left as they are.
+ */
+spec_status spec_delta_rows(int32_t B, int32_t R, const spec_state_desc *st, int32_t layer,
+                            int32_t mode, const spec_delta_desc *d, const int32_t *n_rows,
+                            spec_stream_t stream);
+
+/*
+ * spec_delta_prefill -- the same recurrence over B prompts (or pieces of prompts) of any length:
+ * request b owns the input rows [cu_rows[b], cu_rows[b+1]) and rec_live gets its state after them.
+ *   cu_rows   [B + 1] int32, ascending, cu_rows[0] = 0, cu_rows[B] <= rows; read on the device.
+ *             Requests may be empty: their state is copied.
+ *   rows      rows of q, k, v, log_decay, beta and out. 0 <= rows < 2^31.
+ *   rec_init  the states before, in rec_live's layout; rec_live itself to continue in place; NULL
+ *             for empty states.
+ *   workspace spec_delta_prefill_workspace_bytes(rows, B, st) bytes, 256-byte aligned; no
+ *             initial contents are needed. Of st only the rec_* sizes and rec_live are used.
+ */
+spec_status spec_delta_prefill(int32_t B, const int32_t *cu_rows, int64_t rows,
+                               const spec_state_desc *st, int32_t layer, const spec_delta_desc *d,
+                               const float *rec_init, void *workspace, size_t workspace_bytes,
+                               spec_stream_t stream);
+size_t spec_delta_prefill_workspace_bytes(int64_t rows, int32_t B, const spec_state_desc *st);
+
+/*
+ * Attention of the verify rows of B requests that share a long prefix, one layer:
+ *     o = softmax(scale q K^T) V
+ * over the first prefix_len[b] positions of the shared prefix and then over the request's own
+ * cache (kv, kv_len of spec_state_desc: row r sits at position kv_len[b] + r, already written by
+ * the caller, and sees positions 0..kv_len[b] + r, clipped to kv_capacity). The prefix is read
+ * once for all requests. Masked positions take no part whatever they hold.
+ *
+ *   dtype       of q, out and both caches: SPEC_BF16 or SPEC_F32.
+ *   q_heads     a multiple of kv_heads, at most 64 per KV head; query head h reads KV head
+ *               h / (q_heads / kv_heads). kv_row_bytes = kv_heads * head_dim * element size.
+ *   head_dim    a multiple of 8 up to 256 (else SPEC_ERR_UNSUPPORTED).
+ *   q, out      row b*R + r at q + (b*R + r)*q_stride (elements): [q_heads][head_dim].
+ *   prefix_k, prefix_v   position p at prefix_k + p*prefix_stride (elements):
+ *               [kv_heads][head_dim], or both NULL: no prefix. 16-byte aligned, as is the stride
+ *               in bytes. prefix_capacity < 2^31 positions are there.
+ *   prefix_len  [B] int64 (clamped to [0, prefix_capacity]), or NULL: all of prefix_capacity.
+ *   lse         [B*R][q_heads] float32 or NULL: log sum exp(scale q k) of each row, -Inf where a
+ *               row has nothing to see (its output is zero).
+ */
+typedef struct {
+  spec_dtype dtype;
+  int32_t q_heads, kv_heads, head_dim;
+  const void *q;
+  int64_t q_stride;
+  void *out;
+  int64_t out_stride;
+  float scale;
+  const void *prefix_k;
+  const void *prefix_v;
+  int64_t prefix_capacity;
+  int64_t prefix_stride;
+  const int64_t *prefix_len;
+  float *lse;
+} spec_attn_desc;
+
+/*
+ * spec_prefix_attention -- see spec_attn_desc. layer in [0, kv_layers); R in 1..8; kv_capacity
+ * < 2^31. Of st only the kv* fields are used.
+ *   n_rows    [B] int32 or NULL (R each): rows from n_rows[b] on give zero (lse -Inf).
+ *   workspace spec_prefix_attention_workspace_bytes(B, R, st, d) bytes, 256-byte aligned,
+ *             ZERO-FILLED ONCE before its first use; the error word at byte offset 4 as in the
+ *             conventions above.
+ * B at most 1024. The positions are divided evenly over the SMs whatever the requests' lengths, and
+ * the parts joined in a fixed order: the same call gives the same bytes.
+ */
+spec_status spec_prefix_attention(int32_t B, int32_t R, const spec_state_desc *st, int32_t layer,
+                                  const spec_attn_desc *d, const int32_t *n_rows, void *workspace,
+                                  size_t workspace_bytes, spec_stream_t stream);
+size_t spec_prefix_attention_workspace_bytes(int32_t B, int32_t R, const spec_state_desc *st,
+                                             const spec_attn_desc *d);
+
 /* 1 if this build has the batched tensor-core path for more than 8 verify rows per call. */
 int32_t spec_batched_supported(void);
 

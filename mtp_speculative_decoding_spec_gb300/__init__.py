@@ -13,7 +13,7 @@ from ._abi import (ACCEPT_OUT_DTYPE, COUNTERS_DTYPE, REQ_BAD_FILTER, REQ_BAD_K, 
                    REQ_KV_OVERFLOW, REQ_NO_LOGITS, REQ_NONFINITE, REQ_OK, ROWSTATS_DTYPE,
                    SPEC_BF16, SPEC_COMMIT_INDEX, SPEC_COMMIT_REPLAY, SPEC_COMMIT_SNAPSHOT, SPEC_F32,
                    SPEC_Q4A32,
-                   WIDTH_STATE_DTYPE, spec_state_desc)
+                   WIDTH_STATE_DTYPE, spec_attn_desc, spec_delta_desc, spec_state_desc)
 
 ROWSTATS_BYTES = ROWSTATS_DTYPE.itemsize
 ACCEPT_OUT_BYTES = ACCEPT_OUT_DTYPE.itemsize
@@ -201,6 +201,35 @@ def spec_commit_rollback(B, st, acc, k, mode, commit_status=None, stream=None):
     import ctypes
     _check("spec_commit_rollback", _abi.lib().spec_commit_rollback(
         B, ctypes.byref(st), _ptr(acc), _ptr(k), mode, _ptr(commit_status), _stream(stream)))
+
+
+def spec_delta_rows(B, R, st, layer, mode, desc, n_rows=None, stream=None):
+    """``st`` a ``spec_state_desc``, ``desc`` a ``spec_delta_desc`` (host structs of device
+    pointers)."""
+    _check("spec_delta_rows", _abi.lib().spec_delta_rows(
+        B, R, st, layer, mode, desc, _ptr(n_rows), _stream(stream)))
+
+
+def spec_delta_prefill(B, cu_rows, rows, st, layer, desc, rec_init, workspace, stream=None):
+    _check("spec_delta_prefill", _abi.lib().spec_delta_prefill(
+        B, _ptr(cu_rows), rows, st, layer, desc, _ptr(rec_init), _ptr(workspace),
+        _nbytes(workspace), _stream(stream)))
+
+
+def spec_delta_prefill_workspace_bytes(rows, B, st):
+    return int(_abi.lib().spec_delta_prefill_workspace_bytes(rows, B, st))
+
+
+def spec_prefix_attention(B, R, st, layer, desc, n_rows, workspace, stream=None):
+    """``st`` a ``spec_state_desc``, ``desc`` a ``spec_attn_desc`` (host structs of device
+    pointers)."""
+    _check("spec_prefix_attention", _abi.lib().spec_prefix_attention(
+        B, R, st, layer, desc, _ptr(n_rows), _ptr(workspace), _nbytes(workspace),
+        _stream(stream)))
+
+
+def spec_prefix_attention_workspace_bytes(B, R, st, desc):
+    return int(_abi.lib().spec_prefix_attention_workspace_bytes(B, R, st, desc))
 
 
 def spec_lmhead_verify_noalloc(W, wdt, V, d, H, B, R, temperature, logits, stats, stream=None):

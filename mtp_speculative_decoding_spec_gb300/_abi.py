@@ -21,7 +21,9 @@ EXPORTS = ("spec_workspace_bytes", "spec_status_str", "spec_lmhead_verify",
            "spec_accept", "spec_accept_exact", "spec_accept_filtered", "spec_adapt_width",
            "spec_adapt_width_mirror",
            "spec_draft_argmax_rows", "spec_accept_rows",
-           "spec_commit_rollback",
+           "spec_commit_rollback", "spec_delta_rows", "spec_delta_prefill",
+           "spec_delta_prefill_workspace_bytes", "spec_prefix_attention",
+           "spec_prefix_attention_workspace_bytes",
            "spec_batched_supported", "spec_host_alias", "spec_copy_from_host",
            "spec_lmhead_verify_noalloc", "spec_noalloc_scratch_bytes",
            "spec_noalloc_error_word", "spec_test_verify_stalled",
@@ -68,6 +70,44 @@ class spec_state_desc(ctypes.Structure):
         ("step_c", ctypes.c_void_p),
         ("conv_in", ctypes.c_void_p),
         ("live_slot", ctypes.c_void_p),
+    ]
+
+
+class spec_delta_desc(ctypes.Structure):
+    _fields_ = [
+        ("dtype", ctypes.c_int32),
+        ("key_heads", ctypes.c_int32),
+        ("q", ctypes.c_void_p),
+        ("k", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("q_stride", ctypes.c_int64),
+        ("k_stride", ctypes.c_int64),
+        ("v_stride", ctypes.c_int64),
+        ("log_decay", ctypes.c_void_p),
+        ("beta", ctypes.c_void_p),
+        ("scale", ctypes.c_float),
+        ("out", ctypes.c_void_p),
+        ("out_stride", ctypes.c_int64),
+    ]
+
+
+class spec_attn_desc(ctypes.Structure):
+    _fields_ = [
+        ("dtype", ctypes.c_int32),
+        ("q_heads", ctypes.c_int32),
+        ("kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("q", ctypes.c_void_p),
+        ("q_stride", ctypes.c_int64),
+        ("out", ctypes.c_void_p),
+        ("out_stride", ctypes.c_int64),
+        ("scale", ctypes.c_float),
+        ("prefix_k", ctypes.c_void_p),
+        ("prefix_v", ctypes.c_void_p),
+        ("prefix_capacity", ctypes.c_int64),
+        ("prefix_stride", ctypes.c_int64),
+        ("prefix_len", ctypes.c_void_p),
+        ("lse", ctypes.c_void_p),
     ]
 
 
@@ -126,6 +166,18 @@ def lib():
         L.spec_commit_rollback.argtypes = [i32, ctypes.POINTER(spec_state_desc), vp, vp, i32, vp,
                                            vp]
         L.spec_commit_rollback.restype = i32
+        pst, pdd, pad = (ctypes.POINTER(t) for t in (spec_state_desc, spec_delta_desc,
+                                                     spec_attn_desc))
+        L.spec_delta_rows.argtypes = [i32, i32, pst, i32, i32, pdd, vp, vp]
+        L.spec_delta_rows.restype = i32
+        L.spec_delta_prefill.argtypes = [i32, vp, i64, pst, i32, pdd, vp, vp, sz, vp]
+        L.spec_delta_prefill.restype = i32
+        L.spec_delta_prefill_workspace_bytes.argtypes = [i64, i32, pst]
+        L.spec_delta_prefill_workspace_bytes.restype = sz
+        L.spec_prefix_attention.argtypes = [i32, i32, pst, i32, pad, vp, vp, sz, vp]
+        L.spec_prefix_attention.restype = i32
+        L.spec_prefix_attention_workspace_bytes.argtypes = [i32, i32, pst, pad]
+        L.spec_prefix_attention_workspace_bytes.restype = sz
         L.spec_lmhead_verify_noalloc.argtypes = [vp, i32, i64, i64, vp, i32, i32, vp, vp, vp, vp]
         L.spec_lmhead_verify_noalloc.restype = i32
         L.spec_noalloc_scratch_bytes.argtypes = []

@@ -1,0 +1,358 @@
+// Attention of the verify rows over a shared prefix and each request's own cache: the CUDA-core
+// kernel (fp32 caches, and bf16 head sizes that the tensor-core kernel does not take) and the kernel
+// that joins the partial results of both.
+//
+//   o = sum_p exp(s_p) v_p / sum_p exp(s_p),  s_p = scale q.k_p
+//
+// A partial over a range of positions is (m, l, O) with m the range's largest score, l = sum
+// exp(s - m) and O = sum exp(s - m) v; partials of ranges join as m = max m_i, l = sum e^(m_i-m) l_i,
+// O = sum e^(m_i-m) O_i. Scores are kept in the log2 domain (scale log2(e) folded in once).
+#include <math.h>
+
+#include <cuda_bf16.h>
+
+#include "trunk.cuh"
+
+namespace spec {
+namespace {
+
+__device__ __forceinline__ float to_f(float x) { return x; }
+__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
+
+// Eight elements from 16-byte aligned memory (global or shared), as floats.
+__device__ __forceinline__ void load8(const float* p, float* v) {
+  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+  v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+}
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float* v) {
+  const uint4 a = *reinterpret_cast<const uint4*>(p);
+  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+
+constexpr int kSimtTm = 16;       // rows per tile
+constexpr int kSimtBn = 64;       // positions per block
+constexpr int kSimtThreads = 256;
+constexpr int kMaxD = 256;
+constexpr int kPad = 4;           // floats after a row of Q, K: rows start 16 bytes apart in the banks
+
+// 256 threads over a tile of 16 rows and blocks of 64 positions, all operands fp32 in shared memory.
+// Scores: thread (ty, tx) takes rows 2 ty, 2 ty + 1 and positions tx, tx + 32. Values: thread takes
+// four consecutive dims of four rows. A block in which some row's positions end takes only the
+// positions a row sees, one by one, so what a masked position holds reaches no row.
+template <typename T>
+__global__ void __launch_bounds__(kSimtThreads, 1)
+    attn_simt_kernel(const __grid_constant__ AttnParams p) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  pdl_trigger();
+  pdl_wait();
+  const int D = p.D, ld = D + kPad, tid = threadIdx.x;
+  float* qs = reinterpret_cast<float*>(smem);          // [16][ld]
+  float* ks = qs + kSimtTm * ld;                       // [64][ld]
+  float* vs = ks + kSimtBn * ld;                       // [64][ld]
+  float* ps = vs + kSimtBn * ld;                       // [16][64 + 1]
+  float* row_m = ps + kSimtTm * (kSimtBn + 1);         // running max, the old scale's factor, sum
+  float* row_c = row_m + kSimtTm;
+  float* row_l = row_c + kSimtTm;
+  int* row_lim = reinterpret_cast<int*>(row_l + kSimtTm);
+  int32_t* cum = row_lim + kSimtTm;
+  attn_plan(p, cum);
+  if (blockIdx.x == 0)
+    for (int i = tid; i <= p.items; i += kSimtThreads) p.cum[i] = cum[i];
+  const int64_t W = static_cast<int64_t>(cum[p.items]) * p.Hkv;
+  const int64_t share = (W + gridDim.x - 1) / gridDim.x;
+  int64_t x = share * blockIdx.x;
+  const int64_t x1 = min(W, x + share);
+  const int warp = tid >> 5, lane = tid & 31;
+  const int d0 = (tid & 63) * 4, r0 = (tid >> 6) * 4;  // values: dims and rows of this thread
+  while (x < x1) {
+    const int item = attn_item_of(p, cum, x);
+    const int nb = cum[item + 1] - cum[item];
+    const int64_t rel = x - static_cast<int64_t>(cum[item]) * p.Hkv;
+    const int head = static_cast<int>(rel / nb);
+    const int blk0 = static_cast<int>(rel - static_cast<int64_t>(head) * nb);
+    const int blk1 = static_cast<int>(min(static_cast<int64_t>(nb), blk0 + (x1 - x)));
+    const int slot = blockIdx.x + item * p.Hkv + head;
+    x += blk1 - blk0;
+    __syncthreads();  // the previous piece's shared memory is no longer read
+    if (tid < kSimtTm) {
+      row_lim[tid] = attn_row(p, item, tid).lim;
+      row_m[tid] = -INFINITY;
+      row_l[tid] = 0.f;
+    }
+    for (int i = tid; i < kSimtTm * D; i += kSimtThreads) {
+      const int r = i / D, d = i - r * D;
+      const AttnRow a = attn_row(p, item, r);
+      const int64_t at = (static_cast<int64_t>(a.b) * p.R + a.r) * p.qs +
+                         static_cast<int64_t>(head * p.G + a.g) * D + d;
+      qs[r * ld + d] = a.lim > 0 ? to_f(static_cast<const T*>(p.q)[at]) : 0.f;
+    }
+    const bool pre = item < p.npt;
+    const int b = pre ? 0 : (item - p.npt) / p.nown;
+    const uint8_t* kbase = pre ? p.pk : p.kk + static_cast<int64_t>(b) * p.kreq;
+    const uint8_t* vbase = pre ? p.pv : p.kv + static_cast<int64_t>(b) * p.kreq;
+    const int64_t step = pre ? p.pstride : p.krow;
+    const int64_t hoff = static_cast<int64_t>(head) * D * sizeof(T);
+    __syncthreads();
+    int most = 0, least = 0x7fffffff;  // positions any row sees; positions every running row sees
+    for (int r = 0; r < kSimtTm; ++r) {
+      most = max(most, row_lim[r]);
+      if (row_lim[r] > 0) least = min(least, row_lim[r]);
+    }
+    float acc[4][4] = {};
+    for (int blk = blk0; blk < blk1; ++blk) {
+      const int p0 = blk * kSimtBn;
+      __syncthreads();
+      for (int i = tid; i < kSimtBn * (D / 8); i += kSimtThreads) {
+        const int r = i / (D / 8), d = (i - r * (D / 8)) * 8;
+        float kx[8] = {}, vx[8] = {};
+        if (p0 + r < most) {
+          load8(reinterpret_cast<const T*>(kbase + (p0 + r) * step + hoff) + d, kx);
+          load8(reinterpret_cast<const T*>(vbase + (p0 + r) * step + hoff) + d, vx);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          ks[r * ld + d + j] = kx[j];
+          vs[r * ld + d + j] = vx[j];
+        }
+      }
+      __syncthreads();
+      {
+        float z[2][2] = {};
+        const float* q0 = qs + 2 * warp * ld;
+        const float* k0 = ks + lane * ld;
+        for (int d = 0; d < D; d += 4) {
+          const float4 a0 = *reinterpret_cast<const float4*>(q0 + d);
+          const float4 a1 = *reinterpret_cast<const float4*>(q0 + ld + d);
+          const float4 c0 = *reinterpret_cast<const float4*>(k0 + d);
+          const float4 c1 = *reinterpret_cast<const float4*>(k0 + 32 * ld + d);
+          z[0][0] = fmaf(a0.x, c0.x, fmaf(a0.y, c0.y, fmaf(a0.z, c0.z, fmaf(a0.w, c0.w, z[0][0]))));
+          z[0][1] = fmaf(a0.x, c1.x, fmaf(a0.y, c1.y, fmaf(a0.z, c1.z, fmaf(a0.w, c1.w, z[0][1]))));
+          z[1][0] = fmaf(a1.x, c0.x, fmaf(a1.y, c0.y, fmaf(a1.z, c0.z, fmaf(a1.w, c0.w, z[1][0]))));
+          z[1][1] = fmaf(a1.x, c1.x, fmaf(a1.y, c1.y, fmaf(a1.z, c1.z, fmaf(a1.w, c1.w, z[1][1]))));
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {  // a warp holds both rows' 64 scores: the softmax stays in it
+          const int r = 2 * warp + i, lim = row_lim[r] - p0;
+          const float s0 = lane < lim ? z[i][0] * p.scale_log2 : -INFINITY;
+          const float s1 = lane + 32 < lim ? z[i][1] * p.scale_log2 : -INFINITY;
+          float m = fmaxf(s0, s1);
+          if (s0 != s0 || s1 != s1) m = NAN;
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) {
+            const float other = __shfl_xor_sync(0xffffffffu, m, o);
+            m = (m != m || other != other) ? NAN : fmaxf(m, other);
+          }
+          const float old = row_m[r];
+          m = (old != old || m != m) ? NAN : fmaxf(m, old);
+          const float ref = m == -INFINITY ? 0.f : m;  // nothing seen yet: every weight is 0
+          const float e0 = lane < lim ? exp2f(s0 - ref) : 0.f;
+          const float e1 = lane + 32 < lim ? exp2f(s1 - ref) : 0.f;
+          float l = e0 + e1;
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+          ps[r * (kSimtBn + 1) + lane] = e0;
+          ps[r * (kSimtBn + 1) + lane + 32] = e1;
+          __syncwarp();
+          if (lane == 0) {
+            const float c = exp2f(old - ref);
+            row_c[r] = c;
+            row_l[r] = row_l[r] * c + l;
+            row_m[r] = m;
+          }
+        }
+      }
+      __syncthreads();
+      if (d0 < D) {
+        const bool cut = p0 + kSimtBn > least;  // some running row's positions end in this block
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float c = row_c[r0 + i];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[i][j] *= c;
+        }
+        const int np = min(kSimtBn, most - p0);
+        for (int t = 0; t < np; ++t) {
+          const float4 v = *reinterpret_cast<const float4*>(vs + t * ld + d0);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (cut && p0 + t >= row_lim[r0 + i]) continue;
+            const float w = ps[(r0 + i) * (kSimtBn + 1) + t];
+            acc[i][0] = fmaf(w, v.x, acc[i][0]);
+            acc[i][1] = fmaf(w, v.y, acc[i][1]);
+            acc[i][2] = fmaf(w, v.z, acc[i][2]);
+            acc[i][3] = fmaf(w, v.w, acc[i][3]);
+          }
+        }
+      }
+    }
+    __syncthreads();
+    if (tid < kSimtTm)
+      p.ml[static_cast<int64_t>(slot) * kSimtTm + tid] = make_float2(row_m[tid], row_l[tid]);
+    if (d0 < D) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (row_lim[r0 + i] > 0)
+          *reinterpret_cast<float4*>(p.o + (static_cast<int64_t>(slot) * kSimtTm + r0 + i) * D + d0) =
+              make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+    }
+  }
+}
+
+// One block per output row (verify row, query head): the partials of its prefix unit and of its own
+// unit, warp w taking every fourth one, joined in that order.
+constexpr int kJoinThreads = 128;
+
+template <typename T>
+__global__ void __launch_bounds__(kJoinThreads)
+    attn_join_kernel(const __grid_constant__ AttnParams p, int grid) {
+  __shared__ float sm_m[4], sm_l[4];
+  __shared__ float sm_o[4][kMaxD];
+  pdl_trigger();
+  pdl_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int Hq = p.Hkv * p.G;
+  const int64_t row = blockIdx.x / Hq;
+  const int qh = static_cast<int>(blockIdx.x - row * Hq);
+  const int head = qh / p.G, g = qh - head * p.G;
+  const int b = static_cast<int>(row / p.R), r = static_cast<int>(row - static_cast<int64_t>(b) * p.R);
+  const int64_t W = static_cast<int64_t>(__ldcg(p.cum + p.items)) * p.Hkv;
+  const int64_t share = (W + grid - 1) / grid;
+  int first0 = 0, first1 = 0, count0 = 0, ntot = 0, at0 = 0, at1 = 0;  // slots, the row in its tile
+  const bool runs = r < attn_rows(p, b);
+  const int s = (b * p.R + r) * p.G + g, x = r * p.G + g;
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    if (!runs || (u == 0 && p.npt == 0)) continue;
+    if (u == 0 && attn_prefix(p, b) == 0) continue;
+    const int item = u == 0 ? s / p.tm : p.npt + b * p.nown + x / p.tm;
+    const int c0 = __ldcg(p.cum + item), nb = __ldcg(p.cum + item + 1) - c0;
+    if (nb == 0) continue;
+    const int64_t start = static_cast<int64_t>(c0) * p.Hkv + static_cast<int64_t>(head) * nb;
+    const int cta0 = static_cast<int>(start / share);
+    const int count = static_cast<int>((start + nb - 1) / share) - cta0 + 1;
+    const int first = cta0 + item * p.Hkv + head;
+    ntot += count;
+    if (u == 0) {
+      first0 = first, count0 = count, at0 = s % p.tm;
+    } else {
+      first1 = first, at1 = x % p.tm;
+    }
+  }
+  float m = -INFINITY, l = 0.f;
+  float acc[2][4] = {};
+  const int nv = p.D / 4;
+  for (int i0 = warp; i0 < ntot; i0 += 16) {  // four partials of this warp at a time
+    float2 mlv[4];
+    float4 ov[4][2];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int i = i0 + 4 * j;
+      mlv[j] = make_float2(-INFINITY, 0.f);
+      ov[j][0] = ov[j][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (i < ntot) {
+        const bool pre = i < count0;
+        const int64_t t = static_cast<int64_t>(pre ? first0 + i : first1 + i - count0) * p.tm +
+                          (pre ? at0 : at1);
+        mlv[j] = __ldcg(p.ml + t);
+        const float4* o = reinterpret_cast<const float4*>(p.o + t * p.D);
+        if (lane < nv) ov[j][0] = __ldcg(o + lane);
+        if (lane + 32 < nv) ov[j][1] = __ldcg(o + lane + 32);
+      }
+    }
+    float top = m;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) top = (top != top || mlv[j].x != mlv[j].x) ? NAN : fmaxf(top, mlv[j].x);
+    const float ref = top == -INFINITY ? 0.f : top;
+    const float c = exp2f(m - ref);
+    m = top;
+    l *= c;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int d = 0; d < 4; ++d) acc[h][d] *= c;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (mlv[j].x == -INFINITY) continue;  // nothing seen there
+      const float w = exp2f(mlv[j].x - ref);
+      l = fmaf(w, mlv[j].y, l);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        acc[h][0] = fmaf(w, ov[j][h].x, acc[h][0]);
+        acc[h][1] = fmaf(w, ov[j][h].y, acc[h][1]);
+        acc[h][2] = fmaf(w, ov[j][h].z, acc[h][2]);
+        acc[h][3] = fmaf(w, ov[j][h].w, acc[h][3]);
+      }
+    }
+  }
+  if (lane == 0) {
+    sm_m[warp] = m;
+    sm_l[warp] = l;
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    if (lane + 32 * h < nv)
+      *reinterpret_cast<float4*>(&sm_o[warp][(lane + 32 * h) * 4]) =
+          make_float4(acc[h][0], acc[h][1], acc[h][2], acc[h][3]);
+  __syncthreads();
+  float top = -INFINITY;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) top = (top != top || sm_m[w] != sm_m[w]) ? NAN : fmaxf(top, sm_m[w]);
+  float wt[4], tot = 0.f;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    wt[w] = sm_m[w] == -INFINITY ? 0.f : exp2f(sm_m[w] - top);
+    if (wt[w] != 0.f) tot = fmaf(wt[w], sm_l[w], tot);
+  }
+  const float inv = tot == 0.f ? 0.f : 1.f / tot;
+  T* dst = static_cast<T*>(p.out) + row * p.os + static_cast<int64_t>(qh) * p.D;
+  for (int d = threadIdx.x; d < p.D; d += kJoinThreads) {
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w)
+      if (wt[w] != 0.f) v = fmaf(wt[w], sm_o[w][d], v);
+    v = top == -INFINITY ? 0.f : v * inv;
+    if constexpr (sizeof(T) == 2)
+      dst[d] = __float2bfloat16_rn(v);
+    else
+      dst[d] = v;
+  }
+  if (p.lse && threadIdx.x == 0)
+    p.lse[row * Hq + qh] = top == -INFINITY ? -INFINITY : (top + log2f(tot)) * 0.6931471805599453f;
+}
+
+template <typename T>
+cudaError_t simt_launch(const AttnParams& p, int grid, cudaStream_t stream) {
+  static SmemAllowance allowed;
+  const int floats = (kSimtTm + 2 * kSimtBn) * (p.D + kPad) + kSimtTm * (kSimtBn + 1) + 3 * kSimtTm;
+  const int smem = 4 * (floats + kSimtTm + p.items + 1);
+  const cudaError_t e = allow_dynamic_smem(attn_simt_kernel<T>, smem, allowed);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(attn_simt_kernel<T>, dim3(grid), dim3(kSimtThreads), smem, stream, p);
+}
+
+}  // namespace
+
+int attn_simt_tm() { return kSimtTm; }
+int attn_simt_bn() { return kSimtBn; }
+
+cudaError_t attn_simt_launch(const AttnParams& p, spec_dtype dtype, int grid, cudaStream_t stream) {
+  return dtype == SPEC_BF16 ? simt_launch<__nv_bfloat16>(p, grid, stream)
+                            : simt_launch<float>(p, grid, stream);
+}
+
+cudaError_t attn_join_launch(const AttnParams& p, spec_dtype dtype, int grid, cudaStream_t stream) {
+  const int64_t rows = static_cast<int64_t>(p.B) * p.R * p.Hkv * p.G;
+  if (rows > 0x7fffffff) return cudaErrorInvalidConfiguration;
+  const dim3 g(static_cast<unsigned>(rows));
+  return dtype == SPEC_BF16
+             ? launch_pdl(attn_join_kernel<__nv_bfloat16>, g, dim3(kJoinThreads), 0, stream, p, grid)
+             : launch_pdl(attn_join_kernel<float>, g, dim3(kJoinThreads), 0, stream, p, grid);
+}
+
+}  // namespace spec

@@ -1,0 +1,165 @@
+// Launch parameters of the trunk's token mixers: the gated delta rule and attention over a shared
+// prefix (the files of this folder).
+#pragma once
+
+#include "params.cuh"
+
+namespace spec {
+
+enum : int { DELTA_PREFILL = 3 };  // beside the SPEC_COMMIT_* modes of a verify pass
+
+struct DeltaParams {
+  int B, R, H, Hk, dk, dv, layer, layers, n_slots;
+  int mode;                 // SPEC_COMMIT_* or DELTA_PREFILL
+  const void *q, *k, *v;
+  int64_t qs, ks, vs, os;   // elements between rows
+  const float *g, *beta;    // [rows][H]
+  float scale;
+  void* out;
+  int vec_qk, vec_v, vec_o; // the rows of q and k, of v, of out are whole aligned vectors
+  const int32_t* n_rows;    // [B] or null (a verify pass)
+  const int32_t* cu_rows;   // [B + 1] (prefill)
+  int64_t rows;             // rows of the inputs (prefill)
+  const float* init;        // state before the rows (prefill; null: zeros)
+  float* live;
+  float* slots;
+  const int32_t* live_slot;
+  float *step_a, *step_b, *step_c;
+};
+
+cudaError_t delta_scan_launch(const DeltaParams& p, spec_dtype dtype, int sms, cudaStream_t stream);
+
+// Attention of verify rows over a shared prefix and each request's own cache. The work is cut into
+// units: a tile of `tm` rows and a KV head over the positions of one region. Prefix tiles hold the
+// rows of all requests stacked (s = (b R + r) G + g), own tiles the R G rows of one request. A unit
+// is cut into blocks of `bn` positions, the blocks of all units in a row are dealt out evenly to
+// the grid, and each (CTA, unit) that meet leave one partial (max, sum, unnormalised output) in
+// slot cta + unit. Item = a tile of rows for all KV heads: prefix tiles first, then own tiles.
+struct AttnParams {
+  int B, R, G, Hkv, D;
+  int tm, bn;
+  int npt, nown, items;     // prefix tiles, own tiles per request, npt + B * nown
+  const void* q;
+  int64_t qs;
+  void* out;
+  int64_t os;
+  float scale_log2;         // scale * log2(e)
+  const uint8_t *pk, *pv;   // prefix
+  int64_t pcap, pstride;    // positions, bytes between positions
+  const int64_t* prefix_len;
+  const uint8_t *kk, *kv;   // own caches (of request 0, this layer)
+  int64_t kreq, kcap, krow; // bytes between requests, positions, bytes between positions
+  const int64_t* kv_len;
+  const int32_t* n_rows;
+  float* lse;
+  WsHeader* hdr;
+  int32_t* cum;             // [items + 1]: blocks of one KV head before each item
+  float2* ml;               // [slots][tm]: running max (log2 domain) and sum
+  float* o;                 // [slots][tm][D]
+};
+
+constexpr int kAttnMaxItems = 8192;
+
+// Rows of request b that run.
+__device__ __forceinline__ int attn_rows(const AttnParams& p, int b) {
+  return p.n_rows ? max(0, min(p.n_rows[b], p.R)) : p.R;
+}
+__device__ __forceinline__ int attn_prefix(const AttnParams& p, int b) {
+  if (!p.prefix_len) return static_cast<int>(p.pcap);
+  return static_cast<int>(max(static_cast<int64_t>(0), min(p.prefix_len[b], p.pcap)));
+}
+__device__ __forceinline__ int attn_own(const AttnParams& p, int b, int rows) {
+  return static_cast<int>(
+      min(max(p.kv_len[b], static_cast<int64_t>(0)) + rows, p.kcap));
+}
+
+// cum[0..items] in shared memory, by the whole block (a barrier at the end). Every CTA works it out
+// for itself from the lengths on the device, so no launch comes before and no host reads them.
+__device__ __forceinline__ void attn_plan(const AttnParams& p, int32_t* cum) {
+  const int tid = threadIdx.x, nt = blockDim.x, per = p.R * p.G;
+  for (int i = tid; i < p.items; i += nt) {
+    int n = 0;
+    if (i < p.npt) {
+      const int b0 = i * p.tm / per, b1 = min(p.B - 1, ((i + 1) * p.tm - 1) / per);
+      for (int b = b0; b <= b1; ++b)
+        if (attn_rows(p, b) > 0) n = max(n, attn_prefix(p, b));
+    } else {
+      const int b = (i - p.npt) / p.nown;
+      const int rows = attn_rows(p, b);
+      if (rows > 0) n = attn_own(p, b, rows);
+    }
+    cum[i + 1] = (n + p.bn - 1) / p.bn;
+  }
+  if (tid == 0) cum[0] = 0;
+  __syncthreads();
+  if (tid < 32) {
+    int base = 0;
+    for (int i0 = 1; i0 <= p.items; i0 += 32) {
+      const int i = i0 + tid;
+      int v = i <= p.items ? cum[i] : 0;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, v, o);
+        if (tid >= o) v += x;
+      }
+      v += base;
+      if (i <= p.items) cum[i] = v;
+      base = __shfl_sync(0xffffffffu, v, 31);
+    }
+  }
+  __syncthreads();
+}
+
+// A CTA's piece of one unit.
+struct AttnPiece {
+  int item, head, blk0, blk1, slot;
+};
+
+// The item that holds block x of one KV head's row of blocks scaled by Hkv (x < cum[items] Hkv).
+__device__ __forceinline__ int attn_item_of(const AttnParams& p, const int32_t* cum, int64_t x) {
+  int lo = 0, hi = p.items;  // cum[lo] Hkv <= x < cum[hi] Hkv
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (static_cast<int64_t>(cum[mid]) * p.Hkv <= x)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  return lo;
+}
+
+// Row i of a tile: its request, row and query head in the group, and the positions it sees (0: it
+// does not run, or there is no such row).
+struct AttnRow {
+  int b, r, g, lim;
+};
+__device__ __forceinline__ AttnRow attn_row(const AttnParams& p, int item, int i) {
+  AttnRow a;
+  a.b = a.r = a.g = a.lim = 0;
+  const int per = p.R * p.G;
+  if (item < p.npt) {
+    const int s = item * p.tm + i;
+    if (s >= p.B * per) return a;
+    a.b = s / per;
+    const int x = s - a.b * per;
+    a.r = x / p.G;
+    a.g = x - a.r * p.G;
+    if (a.r < attn_rows(p, a.b)) a.lim = attn_prefix(p, a.b);
+  } else {
+    const int own = item - p.npt;
+    a.b = own / p.nown;
+    const int x = (own - a.b * p.nown) * p.tm + i;
+    if (x >= per) return a;
+    a.r = x / p.G;
+    a.g = x - a.r * p.G;
+    if (a.r < attn_rows(p, a.b)) a.lim = attn_own(p, a.b, a.r + 1);
+  }
+  return a;
+}
+
+cudaError_t attn_simt_launch(const AttnParams& p, spec_dtype dtype, int grid, cudaStream_t stream);
+cudaError_t attn_join_launch(const AttnParams& p, spec_dtype dtype, int grid, cudaStream_t stream);
+int attn_simt_tm();
+int attn_simt_bn();
+
+}  // namespace spec
