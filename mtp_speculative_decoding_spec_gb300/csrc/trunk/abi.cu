@@ -4,7 +4,6 @@
 #include <stdint.h>
 #include <string.h>
 
-#include "host.cuh"
 #include "trunk.cuh"
 
 namespace spec {
@@ -70,7 +69,7 @@ spec_status delta_params(const spec_state_desc* st, int32_t layer, const spec_de
 
 // Attention: the tile sizes of the kernel that takes the call, and the workspace's layout.
 struct AttnPlan {
-  int tm, bn, npt, nown, items, grid;
+  int tc, tm, bn, npt, nown, items, grid;
   size_t cum, ml, o, total;
 };
 
@@ -99,8 +98,9 @@ spec_status attn_plan_of(int32_t B, int32_t R, const spec_state_desc* st, const 
   if (s != SPEC_OK) return s;
   const DevAttr a = dev_attr();
   if (a.sms <= 0) return SPEC_ERR_CUDA;
-  w.tm = attn_simt_tm();
-  w.bn = attn_simt_bn();
+  w.tc = d->dtype == SPEC_BF16 && attn_tc_takes(d->head_dim);
+  w.tm = w.tc ? attn_tc_tm() : attn_simt_tm();
+  w.bn = w.tc ? attn_tc_bn(d->head_dim) : attn_simt_bn();
   const int64_t G = d->q_heads / d->kv_heads, per = R * G;
   const bool prefix = d->prefix_k && d->prefix_capacity > 0;
   const int64_t npt = prefix ? (B * per + w.tm - 1) / w.tm : 0;
@@ -253,9 +253,15 @@ spec_status spec_prefix_attention(int32_t B, int32_t R, const spec_state_desc* s
   p.ml = reinterpret_cast<float2*>(ws + w.ml);
   p.o = reinterpret_cast<float*>(ws + w.o);
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-  cudaError_t ce = attn_simt_launch(p, d->dtype, w.grid, cs);
-  if (ce == cudaSuccess) ce = attn_join_launch(p, d->dtype, w.grid, cs);
-  return ce == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+  if (w.tc) {
+    EncodeTiledFn encode = encode_tiled();
+    if (!encode) return SPEC_ERR_CUDA;
+    s = attn_tc_launch(p, w.grid, encode, cs);
+    if (s != SPEC_OK) return s;
+  } else if (attn_simt_launch(p, d->dtype, w.grid, cs) != cudaSuccess) {
+    return SPEC_ERR_CUDA;
+  }
+  return attn_join_launch(p, d->dtype, w.grid, cs) == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -1,0 +1,558 @@
+// Attention of the verify rows over a shared prefix and each request's own cache on the tcgen05
+// tensor cores: bf16, head_dim 64, 128 or 256. Units, pieces and partials as in trunk.cuh.
+//
+// Per block of kBn positions: S = Q K^T into TMEM (128 rows x kBn), a row's softmax by one thread
+// (TMEM lane = row, no shuffles), the weights as bf16 back into the columns of S, O += P V with P
+// read from TMEM and V as it lies in the cache (rows of positions: the B operand is N-major).
+//   * warp 0 loads: Q by all softmax threads (its rows are gathered), K and V blocks by TMA;
+//   * warp 1 issues the MMAs: S of block i+1 goes out before O of block i, so the tensor pipe works
+//     on one while the softmax works on the other (two S buffers);
+//   * warps 2..5 do the softmax. The reference a row's weights are taken against moves only when the
+//     row's maximum has grown by more than 2^8 (the weights stay below 256 and their sum and O are
+//     fp32, so nothing is lost), which makes rescaling O in TMEM rare.
+// Weights are rounded to bf16 for the tensor cores (2^-9 of each weight, as the outputs are); their
+// sum is taken in fp32 before that.
+//
+// A position that some row does not see has weight 0 in that row, and 0 times what lies there must
+// be 0. In blocks where any running row's positions end, the softmax threads therefore look through
+// V first: non-finite values that no row sees are cleared, and where a row does see one, that
+// row's share of it is added by hand and the value cleared for the tensor cores.
+#include <math.h>
+
+#include <cuda_bf16.h>
+
+#include "trunk.cuh"
+
+#include "tcgen05.cuh"
+
+namespace spec {
+namespace {
+
+constexpr int kTm = 128;
+constexpr int kThreads = 6 * 32;
+constexpr int kSoftThreads = 128;
+constexpr float kLazy = 8.f;
+
+template <int D>
+struct Shape {
+  static constexpr int kBn = D == 256 ? 64 : 128;  // K and V blocks of 16 or 32 KB
+  static constexpr int kStages = D == 64 ? 4 : 2;
+  static constexpr int kQBytes = kTm * D * 2;
+  static constexpr int kTile = kBn * D * 2;
+  static constexpr int kPanel = kBn * 128;          // 64 dims of a block: rows of 128 bytes
+  static constexpr int kFixed = kQBytes + 2 * kStages * kTile;
+};
+
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int x, int y, int z,
+                                            uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// B operand whose rows (K) are 128 bytes of N in the 128-byte swizzle: 8-row groups 1,024 bytes
+// apart, the next 64 of N one panel on.
+__device__ __forceinline__ uint64_t smem_desc_n_major(uint32_t saddr, uint32_t panel) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
+  d |= static_cast<uint64_t>((panel >> 4) & 0x3FFFu) << 16;
+  d |= static_cast<uint64_t>((1024u >> 4) & 0x3FFFu) << 32;
+  d |= static_cast<uint64_t>(1u) << 46;
+  d |= static_cast<uint64_t>(2u) << 61;
+  return d;
+}
+
+// A from TMEM (two bf16 of K per 32-bit column), B from shared memory.
+__device__ __forceinline__ void tc_mma_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                          uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate));
+}
+
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,"
+      "%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+      "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]),
+      "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
+      "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void fence_async_smem() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+__device__ __forceinline__ void bar_soft() {  // the softmax threads only
+  asm volatile("bar.sync 1, 128;" ::: "memory");
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ bool odd_pair(uint32_t w) {  // an Inf or NaN in either half
+  return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
+}
+
+// One piece after another of a CTA's share of the blocks.
+struct Walk {
+  int64_t x, x1;
+  __device__ __forceinline__ bool next(const AttnParams& p, const int32_t* cum, AttnPiece& a) {
+    if (x >= x1) return false;
+    a.item = attn_item_of(p, cum, x);
+    const int nb = cum[a.item + 1] - cum[a.item];
+    const int64_t rel = x - static_cast<int64_t>(cum[a.item]) * p.Hkv;
+    a.head = static_cast<int>(rel / nb);
+    a.blk0 = static_cast<int>(rel - static_cast<int64_t>(a.head) * nb);
+    a.blk1 = static_cast<int>(min(static_cast<int64_t>(nb), a.blk0 + (x1 - x)));
+    a.slot = static_cast<int>(blockIdx.x) + a.item * p.Hkv + a.head;
+    x += a.blk1 - a.blk0;
+    return true;
+  }
+};
+
+struct AttnMaps {
+  CUtensorMap pk, pv, ok, ov;
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_tc_kernel(const __grid_constant__ AttnMaps maps, const __grid_constant__ AttnParams p) {
+  using Sh = Shape<D>;
+  constexpr int BN = Sh::kBn, NS = Sh::kStages;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  uint8_t* sq = smem;
+  uint8_t* sk = sq + Sh::kQBytes;
+  uint8_t* sv = sk + NS * Sh::kTile;
+  uint64_t* kfull = reinterpret_cast<uint64_t*>(smem + Sh::kFixed);
+  uint64_t* kempty = kfull + NS;
+  uint64_t* vfull = kempty + NS;
+  uint64_t* vempty = vfull + NS;
+  uint64_t* sfull = vempty + NS;  // [2]
+  uint64_t* pready = sfull + 2;
+  uint64_t* pvdone = pready + 1;  // [2]: a softmax that skipped waits cannot take one phase for another
+  uint64_t* qready = pvdone + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(qready + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile int* seen_odd = abort_flag + 1;    // a row sees a non-finite V in this block
+  volatile int* o_init = abort_flag + 2;      // O holds something before the piece's first MMA on it
+  int* least_sm = const_cast<int*>(abort_flag + 3);  // [4] per softmax warp
+  int* most_sm = least_sm + 4;
+  int32_t* cum = reinterpret_cast<int32_t*>(smem + Sh::kFixed + 512);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  pdl_trigger();
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(&kfull[s], 1);
+      mbar_init(&kempty[s], 1);
+      mbar_init(&vfull[s], 1);
+      mbar_init(&vempty[s], 1);
+    }
+    mbar_init(&sfull[0], 1);
+    mbar_init(&sfull[1], 1);
+    mbar_init(pready, 4);
+    mbar_init(&pvdone[0], 1);
+    mbar_init(&pvdone[1], 1);
+    mbar_init(qready, 4);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) tmem_alloc(tmem_slot, 512);
+  pdl_wait();
+  attn_plan(p, cum);  // ends with a block barrier
+  if (blockIdx.x == 0)
+    for (int i = threadIdx.x; i <= p.items; i += kThreads) p.cum[i] = cum[i];
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int64_t W = static_cast<int64_t>(cum[p.items]) * p.Hkv;
+  const int64_t share = (W + gridDim.x - 1) / gridDim.x;
+  Walk walk;
+  walk.x = share * blockIdx.x;
+  walk.x1 = min(W, walk.x + share);
+  AttnPiece a;
+  auto give_up = [&]() {
+    atomicOr(&p.hdr->error, ERR_TC_WAIT);
+    *abort_flag = 1;
+  };
+
+  if (warp == 0) {
+    // ------------------------------------------------------------------ TMA producer
+    if (lane == 0) {
+      int it = 0;  // V blocks; K runs one block ahead, as the MMAs take them
+      bool ok = true;
+      while (ok && !*abort_flag && walk.next(p, cum, a)) {
+        const bool pre = a.item < p.npt;
+        const int b = pre ? 0 : (a.item - p.npt) / p.nown;
+        auto load = [&](uint8_t* tiles, uint64_t* full, uint64_t* empty, const CUtensorMap* mp,
+                        const CUtensorMap* mo, int i, int blk) {
+          const int s = i % NS;
+          if (i >= NS && !mbar_wait_bounded(&empty[s], ((i / NS) & 1) ^ 1)) return false;
+          mbar_arrive_expect_tx(&full[s], Sh::kTile);
+          for (int j = 0; j < D / 64; ++j) {
+            uint8_t* dst = tiles + s * Sh::kTile + j * Sh::kPanel;
+            if (pre)
+              tc_tma_load_2d(dst, mp, a.head * D + 64 * j, blk * BN, &full[s]);
+            else
+              tma_load_3d(dst, mo, a.head * D + 64 * j, blk * BN, b, &full[s]);
+          }
+          return true;
+        };
+        const int n = a.blk1 - a.blk0;
+        ok = load(sk, kfull, kempty, &maps.pk, &maps.ok, it, a.blk0);
+        for (int j = 0; ok && j < n; ++j) {
+          if (j + 1 < n) ok = load(sk, kfull, kempty, &maps.pk, &maps.ok, it + j + 1, a.blk0 + j + 1);
+          ok = ok && load(sv, vfull, vempty, &maps.pv, &maps.ov, it + j, a.blk0 + j);
+        }
+        it += n;
+      }
+      if (!ok) give_up();
+      // leave nothing in flight: the last loads of every stage have landed
+      for (int j = max(0, it - NS); j < it; ++j) {
+        mbar_wait_bounded(&kfull[j % NS], (j / NS) & 1);
+        mbar_wait_bounded(&vfull[j % NS], (j / NS) & 1);
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      constexpr uint32_t kIdS = tc_idesc(kTm, BN);
+      constexpr uint32_t kIdO = tc_idesc(kTm, D) | (1u << 16);  // B is N-major
+      const uint64_t qd = smem_desc_sw128(smem_u32(sq));
+      const uint64_t kd0 = smem_desc_sw128(smem_u32(sk));
+      const uint64_t vd0 = smem_desc_n_major(smem_u32(sv), Sh::kPanel);
+      int it = 0, piece = 0;
+      bool ok = true;
+      auto scores = [&](int i) {
+        if (!mbar_wait_bounded(&kfull[i % NS], (i / NS) & 1)) return false;
+        tc_fence_after();
+        const uint64_t kd = desc_advance(kd0, (i % NS) * Sh::kTile);
+        const uint32_t ds = tmem + D + (i & 1) * BN;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          tc_mma(ds, desc_advance(qd, (kk / 4) * (kTm * 128) + (kk % 4) * 32),
+                 desc_advance(kd, (kk / 4) * Sh::kPanel + (kk % 4) * 32), kIdS, kk > 0);
+        tc_commit(&sfull[i & 1]);
+        tc_commit(&kempty[i % NS]);
+        return true;
+      };
+      while (ok && !*abort_flag && walk.next(p, cum, a)) {
+        const int n = a.blk1 - a.blk0;
+        ok = mbar_wait_bounded(qready, piece & 1);
+        tc_fence_after();
+        ok = ok && scores(it);
+        for (int j = 0; ok && j < n; ++j) {
+          const int i = it + j;
+          if (j + 1 < n) ok = scores(i + 1);
+          ok = ok && mbar_wait_bounded(pready, i & 1) &&
+               mbar_wait_bounded(&vfull[i % NS], (i / NS) & 1);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t vd = desc_advance(vd0, (i % NS) * Sh::kTile);
+          const uint32_t ps = tmem + D + (i & 1) * BN;
+          const uint32_t acc0 = j > 0 || *o_init ? 1u : 0u;
+#pragma unroll
+          for (int kk = 0; kk < BN / 16; ++kk)
+            tc_mma_ta(tmem, ps + kk * 8, desc_advance(vd, kk * 2048), kIdO, kk > 0 ? 1u : acc0);
+          tc_commit(&vempty[i % NS]);
+          tc_commit(&pvdone[i & 1]);
+        }
+        it += n;
+        ++piece;
+      }
+      if (!ok) give_up();
+    }
+  } else {
+    // ------------------------------------------------------------------ softmax
+    const int quad = warp & 3, row = quad * 32 + lane, st = threadIdx.x - 64;
+    const uint32_t trow = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+    const float scale = fabsf(p.scale_log2);
+    int it = 0;
+    // A wait that runs out ends all further waiting, not the walk: the softmax warps meet at block
+    // barriers, and so go through the same pieces whatever happens.
+    bool ok = true;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      if (ok && !mbar_wait_bounded(bar, parity)) {
+        give_up();
+        ok = false;
+      }
+      ok = __all_sync(0xffffffffu, ok);
+    };
+    while (walk.next(p, cum, a)) {
+      const AttnRow ar = attn_row(p, a.item, row);
+      // Q: this thread's row, in panels of 64 dims, 16-byte chunks in the 128-byte swizzle; a
+      // negative scale goes into Q's signs
+      {
+        const uint32_t flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;
+        const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.q) +
+                                   (static_cast<int64_t>(ar.b) * p.R + ar.r) * p.qs +
+                                   static_cast<int64_t>(a.head * p.G + ar.g) * D;
+        const bool vec = (reinterpret_cast<uintptr_t>(src) & 15u) == 0;
+#pragma unroll 8
+        for (int c = 0; c < D / 8; ++c) {
+          uint4 v = make_uint4(0u, 0u, 0u, 0u);
+          if (ar.lim > 0) {
+            if (vec) {
+              v = __ldg(reinterpret_cast<const uint4*>(src) + c);
+            } else {
+              const uint16_t* h = reinterpret_cast<const uint16_t*>(src) + c * 8;
+              v.x = h[0] | static_cast<uint32_t>(h[1]) << 16;
+              v.y = h[2] | static_cast<uint32_t>(h[3]) << 16;
+              v.z = h[4] | static_cast<uint32_t>(h[5]) << 16;
+              v.w = h[6] | static_cast<uint32_t>(h[7]) << 16;
+            }
+            v.x ^= flip, v.y ^= flip, v.z ^= flip, v.w ^= flip;
+          }
+          *reinterpret_cast<uint4*>(sq + (c / 8) * (kTm * 128) + row * 128 +
+                                    (((c & 7) ^ (row & 7)) << 4)) = v;
+        }
+      }
+      {
+        const int lo = __reduce_min_sync(0xffffffffu, ar.lim > 0 ? ar.lim : 0x7fffffff);
+        const int hi = __reduce_max_sync(0xffffffffu, ar.lim);
+        if (lane == 0) {
+          least_sm[quad] = lo;
+          most_sm[quad] = hi;
+        }
+        if (st == 0) *o_init = 0;
+      }
+      fence_async_smem();
+      bar_soft();
+      if (lane == 0) mbar_arrive(qready);
+      const int least = min(min(least_sm[0], least_sm[1]), min(least_sm[2], least_sm[3]));
+      const int most = max(max(most_sm[0], most_sm[1]), max(most_sm[2], most_sm[3]));
+      float m = -INFINITY, l = 0.f;
+      for (int blk = a.blk0; blk < a.blk1; ++blk, ++it) {
+        const bool first = blk == a.blk0;
+        const int valid = min(BN, ar.lim - blk * BN);  // positions of the block this row sees
+        wait(&sfull[it & 1], (it >> 1) & 1);
+        tc_fence_after();
+        const uint32_t ts = trow + D + (it & 1) * BN;
+        float v[BN];
+#pragma unroll
+        for (int c = 0; c < BN / 64; ++c) tmem_ld64(ts + 64 * c, v + 64 * c);
+        const bool full = __all_sync(0xffffffffu, valid == BN);
+        if (!full) {
+#pragma unroll
+          for (int j = 0; j < BN; ++j) v[j] = j < valid ? v[j] : -INFINITY;
+        }
+        float mx[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+        for (int j = 4; j < BN; ++j) mx[j & 3] = fmaxf(mx[j & 3], v[j]);
+        const float raw = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        const float top = raw == -INFINITY ? -INFINITY : raw * scale;
+        const bool grow = top > m + kLazy;  // from -Inf: at the first score
+        const float mo = m;
+        if (grow) m = top;
+        const float ref = m == -INFINITY ? 0.f : m;
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        uint32_t w[BN / 2];
+#pragma unroll
+        for (int j = 0; j < BN; j += 2) {
+          float e0 = ex2(fmaf(v[j], scale, -ref)), e1 = ex2(fmaf(v[j + 1], scale, -ref));
+          if (!full) {
+            e0 = j < valid ? e0 : 0.f;
+            e1 = j + 1 < valid ? e1 : 0.f;
+          }
+          sum[j & 3] += e0;
+          sum[(j + 1) & 3] += e1;
+          w[j / 2] = bf16_pair(e0, e1);
+        }
+        const float c = grow ? ex2(mo - ref) : 1.f;  // ex2(-Inf) = 0
+        l = l * c + ((sum[0] + sum[1]) + (sum[2] + sum[3]));
+#pragma unroll
+        for (int j = 0; j < BN / 64; ++j) tmem_st32(ts + 32 * j, w + 32 * j);
+        const bool rescale = !first && __any_sync(0xffffffffu, grow);
+        const bool cut = blk * BN + BN > least;
+        if (rescale || cut) {
+          // O of the blocks before is complete (the MMA of this one waits for this thread)
+          if (!first) wait(&pvdone[(it - 1) & 1], ((it - 1) >> 1) & 1);
+          tc_fence_after();
+        }
+        if (rescale) {
+#pragma unroll 1
+          for (int d = 0; d < D; d += 32) {
+            float o[32];
+            uint32_t u[32];
+            tmem_ld32(trow + d, o);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) u[j] = __float_as_uint(o[j] * c);
+            tmem_st32(trow + d, u);
+          }
+        }
+        if (cut) {
+          const int s = it % NS;
+          wait(&vfull[s], (it / NS) & 1);
+          uint8_t* vt = sv + s * Sh::kTile;
+          if (st == 0) *seen_odd = 0;
+          bar_soft();
+          // a thread looks through 16-byte chunks of positions from the first that a row lacks
+          const int from = max(0, least - blk * BN), nrow = BN - from;
+          for (int i = st; i < nrow * (D / 8); i += kSoftThreads) {
+            const int pos = from + i / (D / 8), ch = i % (D / 8);
+            uint4* at = reinterpret_cast<uint4*>(vt + (ch / 8) * Sh::kPanel + pos * 128 +
+                                                 (((ch & 7) ^ (pos & 7)) << 4));
+            const uint4 x = *at;
+            if (odd_pair(x.x) || odd_pair(x.y) || odd_pair(x.z) || odd_pair(x.w)) {
+              if (blk * BN + pos >= most)
+                *at = make_uint4(0u, 0u, 0u, 0u);
+              else
+                *seen_odd = 1;
+            }
+          }
+          bar_soft();
+          if (*seen_odd) {
+            tmem_st_wait();
+            // Some rows see non-finite values and some do not. Each row adds its own share of those
+            // values to O (zero to begin with), then they are cleared for the tensor cores.
+#pragma unroll 1
+            for (int d = 0; d < D; d += 8) {
+              float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+              if (!first) tmem_ld8(trow + d, o);
+              for (int pos = from; pos < BN; ++pos) {
+                const uint4 x = *reinterpret_cast<const uint4*>(
+                    vt + (d / 64) * Sh::kPanel + pos * 128 + ((((d / 8) & 7) ^ (pos & 7)) << 4));
+                uint32_t pw;  // this position's weight and its neighbour's
+                asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n\t"
+                             "tcgen05.wait::ld.sync.aligned;"
+                             : "=r"(pw)
+                             : "r"(ts + pos / 2)
+                             : "memory");
+                if (pos < valid) {
+                  const uint32_t q4[4] = {x.x, x.y, x.z, x.w};
+                  const float e = __uint_as_float((pos & 1) ? (pw & 0xffff0000u) : (pw << 16));
+#pragma unroll
+                  for (int j = 0; j < 8; ++j) {
+                    const float f =
+                        __uint_as_float((j & 1) ? (q4[j / 2] & 0xffff0000u) : (q4[j / 2] << 16));
+                    if (!(fabsf(f) < INFINITY)) o[j] += e * f;
+                  }
+                }
+                __syncwarp();
+              }
+              __syncwarp();
+              asm volatile(
+                  "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(
+                      trow + d),
+                  "r"(__float_as_uint(o[0])), "r"(__float_as_uint(o[1])), "r"(__float_as_uint(o[2])),
+                  "r"(__float_as_uint(o[3])), "r"(__float_as_uint(o[4])), "r"(__float_as_uint(o[5])),
+                  "r"(__float_as_uint(o[6])), "r"(__float_as_uint(o[7]))
+                  : "memory");
+              tmem_st_wait();
+            }
+            bar_soft();
+            for (int i = st; i < nrow * (D / 8); i += kSoftThreads) {
+              const int pos = from + i / (D / 8), ch = i % (D / 8);
+              uint32_t* at = reinterpret_cast<uint32_t*>(vt + (ch / 8) * Sh::kPanel + pos * 128 +
+                                                         (((ch & 7) ^ (pos & 7)) << 4));
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                uint32_t x = at[j];
+                if ((x & 0x7f80u) == 0x7f80u) x &= 0xffff0000u;
+                if ((x & 0x7f800000u) == 0x7f800000u) x &= 0xffffu;
+                at[j] = x;
+              }
+            }
+            if (st == 0) *o_init = 1;
+          }
+          fence_async_smem();
+          bar_soft();
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(pready);
+      }
+      // the piece's partial
+      wait(&pvdone[(it - 1) & 1], ((it - 1) >> 1) & 1);
+      tc_fence_after();
+      const int64_t at = static_cast<int64_t>(a.slot) * kTm + row;
+      if (ar.lim > 0) p.ml[at] = make_float2(m, l);
+#pragma unroll 1
+      for (int d = 0; d < D; d += 32) {
+        float o[32];
+        tmem_ld32(trow + d, o);
+        if (ar.lim > 0) {
+#pragma unroll
+          for (int j = 0; j < 32; j += 4)
+            *reinterpret_cast<float4*>(p.o + at * D + d + j) = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+        }
+      }
+      tc_fence_before();
+      bar_soft();  // every thread is done with this piece's lengths and Q
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int D>
+spec_status launch_tc(const AttnParams& p, int grid, EncodeTiledFn encode, cudaStream_t stream) {
+  using Sh = Shape<D>;
+  static SmemAllowance allowed;
+  const int smem = Sh::kFixed + 512 + 4 * (p.items + 1) + 1024;
+  if (allow_dynamic_smem(attn_tc_kernel<D>, smem, allowed) != cudaSuccess) return SPEC_ERR_CUDA;
+  AttnMaps m;
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(Sh::kBn), 1};
+  const cuuint32_t es[3] = {1, 1, 1};
+  const cuuint64_t width = static_cast<cuuint64_t>(p.Hkv) * D;
+  const auto map2 = [&](CUtensorMap* t, const uint8_t* base) {
+    const cuuint64_t dim[2] = {width, static_cast<cuuint64_t>(p.pcap)};
+    const cuuint64_t stride[1] = {static_cast<cuuint64_t>(p.pstride)};
+    return encode(t, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<uint8_t*>(base), dim, stride, box,
+                  es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  };
+  const auto map3 = [&](CUtensorMap* t, const uint8_t* base) {
+    const cuuint64_t dim[3] = {width, static_cast<cuuint64_t>(p.kcap), static_cast<cuuint64_t>(p.B)};
+    const cuuint64_t stride[2] = {
+        static_cast<cuuint64_t>(p.krow),
+        static_cast<cuuint64_t>(p.B > 1 ? p.kreq : p.krow * p.kcap)};
+    return encode(t, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint8_t*>(base), dim, stride, box,
+                  es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  };
+  if (map3(&m.ok, p.kk) != CUDA_SUCCESS || map3(&m.ov, p.kv) != CUDA_SUCCESS) return SPEC_ERR_CUDA;
+  m.pk = m.ok;
+  m.pv = m.ov;
+  if (p.npt > 0 && (map2(&m.pk, p.pk) != CUDA_SUCCESS || map2(&m.pv, p.pv) != CUDA_SUCCESS))
+    return SPEC_ERR_CUDA;
+  return launch_pdl(attn_tc_kernel<D>, dim3(grid), dim3(kThreads), smem, stream, m, p) == cudaSuccess
+             ? SPEC_OK
+             : SPEC_ERR_CUDA;
+}
+
+}  // namespace
+
+bool attn_tc_takes(int head_dim) { return head_dim == 64 || head_dim == 128 || head_dim == 256; }
+int attn_tc_tm() { return kTm; }
+int attn_tc_bn(int head_dim) { return head_dim == 256 ? Shape<256>::kBn : Shape<128>::kBn; }
+
+spec_status attn_tc_launch(const AttnParams& p, int grid, EncodeTiledFn encode, cudaStream_t stream) {
+  return p.D == 256   ? launch_tc<256>(p, grid, encode, stream)
+         : p.D == 128 ? launch_tc<128>(p, grid, encode, stream)
+                      : launch_tc<64>(p, grid, encode, stream);
+}
+
+}  // namespace spec

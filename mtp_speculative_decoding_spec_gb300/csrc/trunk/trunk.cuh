@@ -2,6 +2,7 @@
 // prefix (the files of this folder).
 #pragma once
 
+#include "host.cuh"
 #include "params.cuh"
 
 namespace spec {
@@ -161,5 +162,9 @@ cudaError_t attn_simt_launch(const AttnParams& p, spec_dtype dtype, int grid, cu
 cudaError_t attn_join_launch(const AttnParams& p, spec_dtype dtype, int grid, cudaStream_t stream);
 int attn_simt_tm();
 int attn_simt_bn();
+bool attn_tc_takes(int head_dim);  // bf16 only
+spec_status attn_tc_launch(const AttnParams& p, int grid, EncodeTiledFn encode, cudaStream_t stream);
+int attn_tc_tm();
+int attn_tc_bn(int head_dim);
 
 }  // namespace spec
