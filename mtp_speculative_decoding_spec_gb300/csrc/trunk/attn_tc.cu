@@ -1,10 +1,11 @@
 // Attention of the verify rows over a shared prefix and each request's own cache on the tcgen05
 // tensor cores: bf16, head_dim 64, 128 or 256. Units, pieces and partials as in trunk.cuh.
 //
-// Per block of kBn positions: S = Q K^T into TMEM (128 rows x kBn), a row's softmax by one thread
+// Per block of kBn positions: S = Q K^T (Q in TMEM, 128 rows x kBn), a row's softmax by one thread
 // (TMEM lane = row, no shuffles), the weights as bf16 back into the columns of S, O += P V with P
-// read from TMEM and V as it lies in the cache (rows of positions: the B operand is N-major).
-//   * warp 0 loads: Q by all softmax threads (its rows are gathered), K and V blocks by TMA;
+// in TMEM too and V as it lies in the cache (rows of positions: the B operand is N-major).
+//   * warp 0 loads K and V blocks by TMA; Q is gathered by the softmax threads into TMEM, so that
+//     its 128 rows are not read from shared memory again for every block;
 //   * warp 1 issues the MMAs: S of block i+1 goes out before O of block i, so the tensor pipe works
 //     on one while the softmax works on the other (two S buffers);
 //   * warps 2..5 do the softmax. The reference a row's weights are taken against moves only when the
@@ -36,11 +37,13 @@ constexpr float kLazy = 8.f;
 template <int D>
 struct Shape {
   static constexpr int kBn = D == 256 ? 64 : 128;  // K and V blocks of 16 or 32 KB
-  static constexpr int kStages = D == 64 ? 4 : 2;
-  static constexpr int kQBytes = kTm * D * 2;
+  static constexpr int kStages = D == 64 ? 6 : 3;
   static constexpr int kTile = kBn * D * 2;
   static constexpr int kPanel = kBn * 128;          // 64 dims of a block: rows of 128 bytes
-  static constexpr int kFixed = kQBytes + 2 * kStages * kTile;
+  static constexpr int kFixed = 2 * kStages * kTile;
+  // TMEM columns: O, two S buffers, Q (two bf16 a column)
+  static constexpr int kS = D, kQ = D + 2 * kBn;
+  static_assert(kQ + D / 2 <= 512, "TMEM");
 };
 
 __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int x, int y, int z,
@@ -136,8 +139,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
-  uint8_t* sq = smem;
-  uint8_t* sk = sq + Sh::kQBytes;
+  uint8_t* sk = smem;
   uint8_t* sv = sk + NS * Sh::kTile;
   uint64_t* kfull = reinterpret_cast<uint64_t*>(smem + Sh::kFixed);
   uint64_t* kempty = kfull + NS;
@@ -235,7 +237,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       constexpr uint32_t kIdS = tc_idesc(kTm, BN);
       constexpr uint32_t kIdO = tc_idesc(kTm, D) | (1u << 16);  // B is N-major
-      const uint64_t qd = smem_desc_sw128(smem_u32(sq));
       const uint64_t kd0 = smem_desc_sw128(smem_u32(sk));
       const uint64_t vd0 = smem_desc_n_major(smem_u32(sv), Sh::kPanel);
       int it = 0, piece = 0;
@@ -244,11 +245,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!mbar_wait_bounded(&kfull[i % NS], (i / NS) & 1)) return false;
         tc_fence_after();
         const uint64_t kd = desc_advance(kd0, (i % NS) * Sh::kTile);
-        const uint32_t ds = tmem + D + (i & 1) * BN;
+        const uint32_t ds = tmem + Sh::kS + (i & 1) * BN;
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
-          tc_mma(ds, desc_advance(qd, (kk / 4) * (kTm * 128) + (kk % 4) * 32),
-                 desc_advance(kd, (kk / 4) * Sh::kPanel + (kk % 4) * 32), kIdS, kk > 0);
+          tc_mma_ta(ds, tmem + Sh::kQ + kk * 8,
+                    desc_advance(kd, (kk / 4) * Sh::kPanel + (kk % 4) * 32), kIdS, kk > 0);
         tc_commit(&sfull[i & 1]);
         tc_commit(&kempty[i % NS]);
         return true;
@@ -266,7 +267,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
           tc_fence_after();
           const uint64_t vd = desc_advance(vd0, (i % NS) * Sh::kTile);
-          const uint32_t ps = tmem + D + (i & 1) * BN;
+          const uint32_t ps = tmem + Sh::kS + (i & 1) * BN;
           const uint32_t acc0 = j > 0 || *o_init ? 1u : 0u;
 #pragma unroll
           for (int kk = 0; kk < BN / 16; ++kk)
@@ -297,32 +298,37 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     while (walk.next(p, cum, a)) {
       const AttnRow ar = attn_row(p, a.item, row);
-      // Q: this thread's row, in panels of 64 dims, 16-byte chunks in the 128-byte swizzle; a
-      // negative scale goes into Q's signs
+      // Q: this thread's row into its TMEM lane; a negative scale goes into Q's signs
       {
         const uint32_t flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;
         const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.q) +
                                    (static_cast<int64_t>(ar.b) * p.R + ar.r) * p.qs +
                                    static_cast<int64_t>(a.head * p.G + ar.g) * D;
         const bool vec = (reinterpret_cast<uintptr_t>(src) & 15u) == 0;
-#pragma unroll 8
-        for (int c = 0; c < D / 8; ++c) {
-          uint4 v = make_uint4(0u, 0u, 0u, 0u);
-          if (ar.lim > 0) {
-            if (vec) {
-              v = __ldg(reinterpret_cast<const uint4*>(src) + c);
-            } else {
-              const uint16_t* h = reinterpret_cast<const uint16_t*>(src) + c * 8;
-              v.x = h[0] | static_cast<uint32_t>(h[1]) << 16;
-              v.y = h[2] | static_cast<uint32_t>(h[3]) << 16;
-              v.z = h[4] | static_cast<uint32_t>(h[5]) << 16;
-              v.w = h[6] | static_cast<uint32_t>(h[7]) << 16;
+#pragma unroll 1
+        for (int d = 0; d < D; d += 64) {
+          uint32_t w[32];
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            uint4 v = make_uint4(0u, 0u, 0u, 0u);
+            if (ar.lim > 0) {
+              if (vec) {
+                v = __ldg(reinterpret_cast<const uint4*>(src + d) + c);
+              } else {
+                const uint16_t* h = reinterpret_cast<const uint16_t*>(src + d) + c * 8;
+                v.x = h[0] | static_cast<uint32_t>(h[1]) << 16;
+                v.y = h[2] | static_cast<uint32_t>(h[3]) << 16;
+                v.z = h[4] | static_cast<uint32_t>(h[5]) << 16;
+                v.w = h[6] | static_cast<uint32_t>(h[7]) << 16;
+              }
             }
-            v.x ^= flip, v.y ^= flip, v.z ^= flip, v.w ^= flip;
+            w[4 * c] = v.x ^ flip, w[4 * c + 1] = v.y ^ flip;
+            w[4 * c + 2] = v.z ^ flip, w[4 * c + 3] = v.w ^ flip;
           }
-          *reinterpret_cast<uint4*>(sq + (c / 8) * (kTm * 128) + row * 128 +
-                                    (((c & 7) ^ (row & 7)) << 4)) = v;
+          __syncwarp();
+          tmem_st32(trow + Sh::kQ + d / 2, w);
         }
+        tmem_st_wait();
       }
       {
         const int lo = __reduce_min_sync(0xffffffffu, ar.lim > 0 ? ar.lim : 0x7fffffff);
@@ -333,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (st == 0) *o_init = 0;
       }
-      fence_async_smem();
+      tc_fence_before();
       bar_soft();
       if (lane == 0) mbar_arrive(qready);
       const int least = min(min(least_sm[0], least_sm[1]), min(least_sm[2], least_sm[3]));
@@ -344,7 +350,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int valid = min(BN, ar.lim - blk * BN);  // positions of the block this row sees
         wait(&sfull[it & 1], (it >> 1) & 1);
         tc_fence_after();
-        const uint32_t ts = trow + D + (it & 1) * BN;
+        const uint32_t ts = trow + Sh::kS + (it & 1) * BN;
         float v[BN];
 #pragma unroll
         for (int c = 0; c < BN / 64; ++c) tmem_ld64(ts + 64 * c, v + 64 * c);
