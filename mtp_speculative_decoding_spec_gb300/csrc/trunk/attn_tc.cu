@@ -67,13 +67,21 @@ __device__ __forceinline__ uint64_t smem_desc_n_major(uint32_t saddr, uint32_t p
   return d;
 }
 
-// A from TMEM (two bf16 of K per 32-bit column), B from shared memory.
+// A from TMEM (two bf16 of K per 32-bit column), B from shared memory. Called by a whole warp, one
+// lane of which issues: the operands are the same in all lanes and stay in uniform registers.
 __device__ __forceinline__ void tc_mma_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
                                           uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate));
+}
+__device__ __forceinline__ void tc_commit_elect(uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+          smem_u32(bar))
+      : "memory");
 }
 
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
@@ -183,7 +191,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
   const int64_t W = static_cast<int64_t>(cum[p.items]) * p.Hkv;
   const int64_t share = (W + gridDim.x - 1) / gridDim.x;
   Walk walk;
@@ -234,7 +242,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
+    {
       constexpr uint32_t kIdS = tc_idesc(kTm, BN);
       constexpr uint32_t kIdO = tc_idesc(kTm, D) | (1u << 16);  // B is N-major
       const uint64_t kd0 = smem_desc_sw128(smem_u32(sk));
@@ -242,7 +250,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int it = 0, piece = 0;
       bool ok = true;
       auto scores = [&](int i) {
-        if (!mbar_wait_bounded(&kfull[i % NS], (i / NS) & 1)) return false;
+        if (!__all_sync(0xffffffffu, mbar_wait_bounded(&kfull[i % NS], (i / NS) & 1))) return false;
         tc_fence_after();
         const uint64_t kd = desc_advance(kd0, (i % NS) * Sh::kTile);
         const uint32_t ds = tmem + Sh::kS + (i & 1) * BN;
@@ -250,20 +258,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int kk = 0; kk < D / 16; ++kk)
           tc_mma_ta(ds, tmem + Sh::kQ + kk * 8,
                     desc_advance(kd, (kk / 4) * Sh::kPanel + (kk % 4) * 32), kIdS, kk > 0);
-        tc_commit(&sfull[i & 1]);
-        tc_commit(&kempty[i % NS]);
+        tc_commit_elect(&sfull[i & 1]);
+        tc_commit_elect(&kempty[i % NS]);
         return true;
       };
-      while (ok && !*abort_flag && walk.next(p, cum, a)) {
+      while (ok && !__any_sync(0xffffffffu, *abort_flag) && walk.next(p, cum, a)) {
         const int n = a.blk1 - a.blk0;
-        ok = mbar_wait_bounded(qready, piece & 1);
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(qready, piece & 1));
         tc_fence_after();
         ok = ok && scores(it);
         for (int j = 0; ok && j < n; ++j) {
           const int i = it + j;
           if (j + 1 < n) ok = scores(i + 1);
-          ok = ok && mbar_wait_bounded(pready, i & 1) &&
-               mbar_wait_bounded(&vfull[i % NS], (i / NS) & 1);
+          ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(pready, i & 1) &&
+                                                 mbar_wait_bounded(&vfull[i % NS], (i / NS) & 1));
           if (!ok) break;
           tc_fence_after();
           const uint64_t vd = desc_advance(vd0, (i % NS) * Sh::kTile);
@@ -272,13 +280,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int kk = 0; kk < BN / 16; ++kk)
             tc_mma_ta(tmem, ps + kk * 8, desc_advance(vd, kk * 2048), kIdO, kk > 0 ? 1u : acc0);
-          tc_commit(&vempty[i % NS]);
-          tc_commit(&pvdone[i & 1]);
+          tc_commit_elect(&vempty[i % NS]);
+          tc_commit_elect(&pvdone[i & 1]);
         }
         it += n;
         ++piece;
       }
-      if (!ok) give_up();
+      if (!ok && lane == 0) give_up();
     }
   } else {
     // ------------------------------------------------------------------ softmax
