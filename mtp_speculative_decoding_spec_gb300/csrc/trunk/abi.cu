@@ -70,7 +70,7 @@ spec_status delta_params(const spec_state_desc* st, int32_t layer, const spec_de
 // Attention: the tile sizes of the kernel that takes the call, and the workspace's layout.
 struct AttnPlan {
   int tc, tm, bn, npt, nown, items, grid;
-  size_t cum, ml, o, total;
+  size_t units, ml, o, total;
 };
 
 spec_status attn_check(int32_t B, int32_t R, const spec_state_desc* st, const spec_attn_desc* d) {
@@ -114,8 +114,8 @@ spec_status attn_plan_of(int32_t B, int32_t R, const spec_state_desc* st, const 
   w.items = static_cast<int>(items);
   w.grid = a.sms;
   const size_t slots = static_cast<size_t>(w.grid) + static_cast<size_t>(items) * d->kv_heads;
-  w.cum = sizeof(WsHeader);
-  w.ml = w.cum + align_up(4 * static_cast<size_t>(items + 1), 256);
+  w.units = sizeof(WsHeader);
+  w.ml = w.units + align_up(sizeof(int2) * static_cast<size_t>(items) * d->kv_heads, 256);
   w.o = w.ml + align_up(slots * w.tm * sizeof(float2), 256);
   w.total = w.o + align_up(slots * w.tm * d->head_dim * sizeof(float), 256);
   return SPEC_OK;
@@ -249,7 +249,7 @@ spec_status spec_prefix_attention(int32_t B, int32_t R, const spec_state_desc* s
   p.n_rows = n_rows;
   p.lse = d->lse;
   p.hdr = static_cast<WsHeader*>(workspace);
-  p.cum = reinterpret_cast<int32_t*>(ws + w.cum);
+  p.units = reinterpret_cast<int2*>(ws + w.units);
   p.ml = reinterpret_cast<float2*>(ws + w.ml);
   p.o = reinterpret_cast<float*>(ws + w.o);
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);

@@ -39,6 +39,7 @@ constexpr int kSimtTm = 16;       // rows per tile
 constexpr int kSimtBn = 64;       // positions per block
 constexpr int kSimtThreads = 256;
 constexpr int kMaxD = 256;
+constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kPad = 4;           // floats after a row of Q, K: rows start 16 bytes apart in the banks
 
 // 256 threads over a tile of 16 rows and blocks of 64 positions, all operands fp32 in shared memory.
@@ -62,10 +63,9 @@ __global__ void __launch_bounds__(kSimtThreads, 1)
   int* row_lim = reinterpret_cast<int*>(row_l + kSimtTm);
   int32_t* cum = row_lim + kSimtTm;
   attn_plan(p, cum);
-  if (blockIdx.x == 0)
-    for (int i = tid; i <= p.items; i += kSimtThreads) p.cum[i] = cum[i];
   const int64_t W = static_cast<int64_t>(cum[p.items]) * p.Hkv;
   const int64_t share = (W + gridDim.x - 1) / gridDim.x;
+  if (blockIdx.x == 0) attn_write_units(p, cum, share);
   int64_t x = share * blockIdx.x;
   const int64_t x1 = min(W, x + share);
   const int warp = tid >> 5, lane = tid & 31;
@@ -204,60 +204,48 @@ __global__ void __launch_bounds__(kSimtThreads, 1)
   }
 }
 
-// One block per output row (verify row, query head): the partials of its prefix unit and of its own
-// unit, warp w taking every fourth one, joined in that order.
-constexpr int kJoinThreads = 128;
+// One output row (verify row, query head) by NW warps: the partials of its prefix unit and then of its
+// own unit, warp w taking every NW-th of them, joined in that order. Many rows have few partials
+// each and get one warp a row (four rows to a block); few rows have many, and get eight warps.
+constexpr int kJoinMost = 4;  // partials in flight per warp
 
-template <typename T>
-__global__ void __launch_bounds__(kJoinThreads)
-    attn_join_kernel(const __grid_constant__ AttnParams p, int grid) {
-  __shared__ float sm_m[4], sm_l[4];
-  __shared__ float sm_o[4][kMaxD];
+template <typename T, int NW>
+__global__ void __launch_bounds__(NW == 1 ? 128 : 32 * NW)
+    attn_join_kernel(const __grid_constant__ AttnParams p) {
+  __shared__ float sm_m[NW], sm_l[NW];
+  __shared__ float sm_o[NW == 1 ? 1 : NW][NW == 1 ? 1 : kMaxD];
   pdl_trigger();
-  pdl_wait();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, warp = NW == 1 ? 0 : threadIdx.x >> 5;
   const int Hq = p.Hkv * p.G;
-  const int64_t row = blockIdx.x / Hq;
-  const int qh = static_cast<int>(blockIdx.x - row * Hq);
+  const int64_t id = NW == 1 ? static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5) : blockIdx.x;
+  const int64_t row = id / Hq;
+  if (row >= static_cast<int64_t>(p.B) * p.R) return;  // whole warps, and only where NW is 1
+  const int qh = static_cast<int>(id - row * Hq);
   const int head = qh / p.G, g = qh - head * p.G;
-  const int b = static_cast<int>(row / p.R), r = static_cast<int>(row - static_cast<int64_t>(b) * p.R);
-  const int64_t W = static_cast<int64_t>(__ldcg(p.cum + p.items)) * p.Hkv;
-  const int64_t share = (W + grid - 1) / grid;
-  int first0 = 0, first1 = 0, count0 = 0, ntot = 0, at0 = 0, at1 = 0;  // slots, the row in its tile
-  const bool runs = r < attn_rows(p, b);
+  const int b = static_cast<int>(row / p.R), r = static_cast<int>(row) - b * p.R;
   const int s = (b * p.R + r) * p.G + g, x = r * p.G + g;
-#pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    if (!runs || (u == 0 && p.npt == 0)) continue;
-    if (u == 0 && attn_prefix(p, b) == 0) continue;
-    const int item = u == 0 ? s / p.tm : p.npt + b * p.nown + x / p.tm;
-    const int c0 = __ldcg(p.cum + item), nb = __ldcg(p.cum + item + 1) - c0;
-    if (nb == 0) continue;
-    const int64_t start = static_cast<int64_t>(c0) * p.Hkv + static_cast<int64_t>(head) * nb;
-    const int cta0 = static_cast<int>(start / share);
-    const int count = static_cast<int>((start + nb - 1) / share) - cta0 + 1;
-    const int first = cta0 + item * p.Hkv + head;
-    ntot += count;
-    if (u == 0) {
-      first0 = first, count0 = count, at0 = s % p.tm;
-    } else {
-      first1 = first, at1 = x % p.tm;
-    }
-  }
+  pdl_wait();
+  const int rows = attn_rows(p, b);
+  int2 u0 = make_int2(0, 0);
+  if (p.npt > 0) u0 = __ldcg(p.units + (s / p.tm) * p.Hkv + head);
+  int2 u1 = __ldcg(p.units + (p.npt + b * p.nown + x / p.tm) * p.Hkv + head);
+  if (p.npt > 0 && attn_prefix(p, b) == 0) u0.y = 0;
+  if (r >= rows) u0.y = u1.y = 0;
+  const int at0 = s % p.tm, at1 = x % p.tm, ntot = u0.y + u1.y;
   float m = -INFINITY, l = 0.f;
   float acc[2][4] = {};
   const int nv = p.D / 4;
-  for (int i0 = warp; i0 < ntot; i0 += 16) {  // four partials of this warp at a time
-    float2 mlv[4];
-    float4 ov[4][2];
+  for (int i0 = warp; i0 < ntot; i0 += kJoinMost * NW) {
+    float2 mlv[kJoinMost];
+    float4 ov[kJoinMost][2];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int i = i0 + 4 * j;
+    for (int j = 0; j < kJoinMost; ++j) {
+      const int i = i0 + NW * j;
       mlv[j] = make_float2(-INFINITY, 0.f);
       ov[j][0] = ov[j][1] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (i < ntot) {
-        const bool pre = i < count0;
-        const int64_t t = static_cast<int64_t>(pre ? first0 + i : first1 + i - count0) * p.tm +
+        const bool pre = i < u0.y;
+        const int64_t t = static_cast<int64_t>(pre ? u0.x + i : u1.x + i - u0.y) * p.tm +
                           (pre ? at0 : at1);
         mlv[j] = __ldcg(p.ml + t);
         const float4* o = reinterpret_cast<const float4*>(p.o + t * p.D);
@@ -267,7 +255,8 @@ __global__ void __launch_bounds__(kJoinThreads)
     }
     float top = m;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) top = (top != top || mlv[j].x != mlv[j].x) ? NAN : fmaxf(top, mlv[j].x);
+    for (int j = 0; j < kJoinMost; ++j)
+      top = (top != top || mlv[j].x != mlv[j].x) ? NAN : fmaxf(top, mlv[j].x);
     const float ref = top == -INFINITY ? 0.f : top;
     const float c = exp2f(m - ref);
     m = top;
@@ -277,7 +266,7 @@ __global__ void __launch_bounds__(kJoinThreads)
 #pragma unroll
       for (int d = 0; d < 4; ++d) acc[h][d] *= c;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < kJoinMost; ++j) {
       if (mlv[j].x == -INFINITY) continue;  // nothing seen there
       const float w = exp2f(mlv[j].x - ref);
       l = fmaf(w, mlv[j].y, l);
@@ -289,6 +278,25 @@ __global__ void __launch_bounds__(kJoinThreads)
         acc[h][3] = fmaf(w, ov[j][h].w, acc[h][3]);
       }
     }
+  }
+  T* dst = static_cast<T*>(p.out) + row * p.os + static_cast<int64_t>(qh) * p.D;
+  if constexpr (NW == 1) {
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const bool empty = m == -INFINITY;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      if (lane + 32 * h < nv) {
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+          const float v = empty ? 0.f : acc[h][d] * inv;
+          if constexpr (sizeof(T) == 2)
+            dst[(lane + 32 * h) * 4 + d] = __float2bfloat16_rn(v);
+          else
+            dst[(lane + 32 * h) * 4 + d] = v;
+        }
+      }
+    if (p.lse && lane == 0) p.lse[row * Hq + qh] = empty ? -INFINITY : (m + log2f(l)) * kLn2;
+    return;
   }
   if (lane == 0) {
     sm_m[warp] = m;
@@ -302,19 +310,18 @@ __global__ void __launch_bounds__(kJoinThreads)
   __syncthreads();
   float top = -INFINITY;
 #pragma unroll
-  for (int w = 0; w < 4; ++w) top = (top != top || sm_m[w] != sm_m[w]) ? NAN : fmaxf(top, sm_m[w]);
-  float wt[4], tot = 0.f;
+  for (int w = 0; w < NW; ++w) top = (top != top || sm_m[w] != sm_m[w]) ? NAN : fmaxf(top, sm_m[w]);
+  float wt[NW], tot = 0.f;
 #pragma unroll
-  for (int w = 0; w < 4; ++w) {
+  for (int w = 0; w < NW; ++w) {
     wt[w] = sm_m[w] == -INFINITY ? 0.f : exp2f(sm_m[w] - top);
     if (wt[w] != 0.f) tot = fmaf(wt[w], sm_l[w], tot);
   }
   const float inv = tot == 0.f ? 0.f : 1.f / tot;
-  T* dst = static_cast<T*>(p.out) + row * p.os + static_cast<int64_t>(qh) * p.D;
-  for (int d = threadIdx.x; d < p.D; d += kJoinThreads) {
+  for (int d = threadIdx.x; d < p.D; d += 32 * NW) {
     float v = 0.f;
 #pragma unroll
-    for (int w = 0; w < 4; ++w)
+    for (int w = 0; w < NW; ++w)
       if (wt[w] != 0.f) v = fmaf(wt[w], sm_o[w][d], v);
     v = top == -INFINITY ? 0.f : v * inv;
     if constexpr (sizeof(T) == 2)
@@ -323,7 +330,7 @@ __global__ void __launch_bounds__(kJoinThreads)
       dst[d] = v;
   }
   if (p.lse && threadIdx.x == 0)
-    p.lse[row * Hq + qh] = top == -INFINITY ? -INFINITY : (top + log2f(tot)) * 0.6931471805599453f;
+    p.lse[row * Hq + qh] = top == -INFINITY ? -INFINITY : (top + log2f(tot)) * kLn2;
 }
 
 template <typename T>
@@ -346,13 +353,16 @@ cudaError_t attn_simt_launch(const AttnParams& p, spec_dtype dtype, int grid, cu
                             : simt_launch<float>(p, grid, stream);
 }
 
-cudaError_t attn_join_launch(const AttnParams& p, spec_dtype dtype, int grid, cudaStream_t stream) {
+cudaError_t attn_join_launch(const AttnParams& p, spec_dtype dtype, int sms, cudaStream_t stream) {
   const int64_t rows = static_cast<int64_t>(p.B) * p.R * p.Hkv * p.G;
   if (rows > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  const dim3 g(static_cast<unsigned>(rows));
-  return dtype == SPEC_BF16
-             ? launch_pdl(attn_join_kernel<__nv_bfloat16>, g, dim3(kJoinThreads), 0, stream, p, grid)
-             : launch_pdl(attn_join_kernel<float>, g, dim3(kJoinThreads), 0, stream, p, grid);
+  const bool many = rows >= 4 * static_cast<int64_t>(sms);
+  const dim3 g(static_cast<unsigned>(many ? (rows + 3) / 4 : rows)), t(many ? 128 : 256);
+  if (dtype == SPEC_BF16)
+    return many ? launch_pdl(attn_join_kernel<__nv_bfloat16, 1>, g, t, 0, stream, p)
+                : launch_pdl(attn_join_kernel<__nv_bfloat16, 8>, g, t, 0, stream, p);
+  return many ? launch_pdl(attn_join_kernel<float, 1>, g, t, 0, stream, p)
+              : launch_pdl(attn_join_kernel<float, 8>, g, t, 0, stream, p);
 }
 
 }  // namespace spec

@@ -8,16 +8,16 @@
 //     its 128 rows are not read from shared memory again for every block;
 //   * warp 1 issues the MMAs: S of block i+1 goes out before O of block i, so the tensor pipe works
 //     on one while the softmax works on the other (two S buffers);
-//   * warps 2..5 do the softmax. The reference a row's weights are taken against moves only when the
+//   * warps 2..5 do the softmax, warps 6 and 7 watch V (below). The reference a row's weights are taken against moves only when the
 //     row's maximum has grown by more than 2^8 (the weights stay below 256 and their sum and O are
 //     fp32, so nothing is lost), which makes rescaling O in TMEM rare.
 // Weights are rounded to bf16 for the tensor cores (2^-9 of each weight, as the outputs are); their
 // sum is taken in fp32 before that.
 //
 // A position that some row does not see has weight 0 in that row, and 0 times what lies there must
-// be 0. In blocks where any running row's positions end, the softmax threads therefore look through
-// V first: non-finite values that no row sees are cleared, and where a row does see one, that
-// row's share of it is added by hand and the value cleared for the tensor cores.
+// be 0. In blocks where any running row's positions end, two guard warps therefore look through V as
+// it lands, ahead of the softmax: non-finite values that no row sees are cleared, and where a row
+// does see one, that row's share of it is added by hand and the value cleared for the tensor cores.
 #include <math.h>
 
 #include <cuda_bf16.h>
@@ -30,7 +30,7 @@ namespace spec {
 namespace {
 
 constexpr int kTm = 128;
-constexpr int kThreads = 6 * 32;
+constexpr int kThreads = 8 * 32;  // producer, MMA, four softmax and two guard warps
 constexpr int kSoftThreads = 128;
 constexpr float kLazy = 8.f;
 
@@ -46,12 +46,17 @@ struct Shape {
   static_assert(kQ + D / 2 <= 512, "TMEM");
 };
 
-__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int x, int y, int z,
-                                            uint64_t* bar) {
+// A whole block of K or V at once: [panel of 64 dims][position][64 dims], the order of its map's box.
+// Called by a whole warp, one lane issues.
+__device__ __forceinline__ void tma_load_block(void* dst, const CUtensorMap* map, int pos, int panel,
+                                               int b, uint64_t* bar, uint32_t bytes) {
   asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%5], %6;\n\t"
+      "@e cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%7, %2, %3, %4}], [%5];\n\t}" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(pos), "r"(panel), "r"(b), "r"(smem_u32(bar)),
+      "r"(bytes), "r"(0)
       : "memory");
 }
 
@@ -102,9 +107,6 @@ __device__ __forceinline__ void tmem_st_wait() {
 __device__ __forceinline__ void fence_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
-__device__ __forceinline__ void bar_soft() {  // the softmax threads only
-  asm volatile("bar.sync 1, 128;" ::: "memory");
-}
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -153,16 +155,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* kempty = kfull + NS;
   uint64_t* vfull = kempty + NS;
   uint64_t* vempty = vfull + NS;
-  uint64_t* sfull = vempty + NS;  // [2]
+  uint64_t* vok = vempty + NS;    // V has landed and been looked through
+  uint64_t* sfull = vok + NS;     // [2]
   uint64_t* pready = sfull + 2;
   uint64_t* pvdone = pready + 1;  // [2]: a softmax that skipped waits cannot take one phase for another
   uint64_t* qready = pvdone + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(qready + 1);
+  uint64_t* meet = qready + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(meet + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  volatile int* seen_odd = abort_flag + 1;    // a row sees a non-finite V in this block
-  volatile int* o_init = abort_flag + 2;      // O holds something before the piece's first MMA on it
-  int* least_sm = const_cast<int*>(abort_flag + 3);  // [4] per softmax warp
-  int* most_sm = least_sm + 4;
+  volatile int* o_init = abort_flag + 1;      // O holds something before the piece's first MMA on it
+  volatile int* odd = abort_flag + 2;         // [NS][2]: a row sees a non-finite V of the stage
+  int* least_sm = const_cast<int*>(odd + 2 * NS);  // [4] per softmax warp
   int32_t* cum = reinterpret_cast<int32_t*>(smem + Sh::kFixed + 512);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -173,6 +176,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&kempty[s], 1);
       mbar_init(&vfull[s], 1);
       mbar_init(&vempty[s], 1);
+      mbar_init(&vok[s], 2);
     }
     mbar_init(&sfull[0], 1);
     mbar_init(&sfull[1], 1);
@@ -180,20 +184,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&pvdone[0], 1);
     mbar_init(&pvdone[1], 1);
     mbar_init(qready, 4);
+    mbar_init(meet, 4);
     *abort_flag = 0;
     fence_mbar_init();
   }
   if (warp == 1) tmem_alloc(tmem_slot, 512);
   pdl_wait();
   attn_plan(p, cum);  // ends with a block barrier
-  if (blockIdx.x == 0)
-    for (int i = threadIdx.x; i <= p.items; i += kThreads) p.cum[i] = cum[i];
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
   const int64_t W = static_cast<int64_t>(cum[p.items]) * p.Hkv;
   const int64_t share = (W + gridDim.x - 1) / gridDim.x;
+  if (blockIdx.x == 0) attn_write_units(p, cum, share);
   Walk walk;
   walk.x = share * blockIdx.x;
   walk.x1 = min(W, walk.x + share);
@@ -205,40 +209,34 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------------------ TMA producer
-    if (lane == 0) {
-      int it = 0;  // V blocks; K runs one block ahead, as the MMAs take them
-      bool ok = true;
-      while (ok && !*abort_flag && walk.next(p, cum, a)) {
-        const bool pre = a.item < p.npt;
-        const int b = pre ? 0 : (a.item - p.npt) / p.nown;
-        auto load = [&](uint8_t* tiles, uint64_t* full, uint64_t* empty, const CUtensorMap* mp,
-                        const CUtensorMap* mo, int i, int blk) {
-          const int s = i % NS;
-          if (i >= NS && !mbar_wait_bounded(&empty[s], ((i / NS) & 1) ^ 1)) return false;
-          mbar_arrive_expect_tx(&full[s], Sh::kTile);
-          for (int j = 0; j < D / 64; ++j) {
-            uint8_t* dst = tiles + s * Sh::kTile + j * Sh::kPanel;
-            if (pre)
-              tc_tma_load_2d(dst, mp, a.head * D + 64 * j, blk * BN, &full[s]);
-            else
-              tma_load_3d(dst, mo, a.head * D + 64 * j, blk * BN, b, &full[s]);
-          }
-          return true;
-        };
-        const int n = a.blk1 - a.blk0;
-        ok = load(sk, kfull, kempty, &maps.pk, &maps.ok, it, a.blk0);
-        for (int j = 0; ok && j < n; ++j) {
-          if (j + 1 < n) ok = load(sk, kfull, kempty, &maps.pk, &maps.ok, it + j + 1, a.blk0 + j + 1);
-          ok = ok && load(sv, vfull, vempty, &maps.pv, &maps.ov, it + j, a.blk0 + j);
-        }
-        it += n;
+    int it = 0;  // V blocks; K runs one block ahead, as the MMAs take them
+    bool ok = true;
+    while (ok && !__any_sync(0xffffffffu, *abort_flag) && walk.next(p, cum, a)) {
+      const bool pre = a.item < p.npt;
+      const int b = pre ? 0 : (a.item - p.npt) / p.nown, panel = a.head * (D / 64);
+      auto load = [&](uint8_t* tiles, uint64_t* full, uint64_t* empty, const CUtensorMap* map, int i,
+                      int blk) {
+        const int s = i % NS;
+        if (i >= NS && !__all_sync(0xffffffffu, mbar_wait_bounded(&empty[s], ((i / NS) & 1) ^ 1)))
+          return false;
+        tma_load_block(tiles + s * Sh::kTile, map, blk * BN, panel, b, &full[s], Sh::kTile);
+        return true;
+      };
+      const CUtensorMap* mk = pre ? &maps.pk : &maps.ok;
+      const CUtensorMap* mv = pre ? &maps.pv : &maps.ov;
+      const int n = a.blk1 - a.blk0;
+      ok = load(sk, kfull, kempty, mk, it, a.blk0);
+      for (int j = 0; ok && j < n; ++j) {
+        if (j + 1 < n) ok = load(sk, kfull, kempty, mk, it + j + 1, a.blk0 + j + 1);
+        ok = ok && load(sv, vfull, vempty, mv, it + j, a.blk0 + j);
       }
-      if (!ok) give_up();
-      // leave nothing in flight: the last loads of every stage have landed
-      for (int j = max(0, it - NS); j < it; ++j) {
-        mbar_wait_bounded(&kfull[j % NS], (j / NS) & 1);
-        mbar_wait_bounded(&vfull[j % NS], (j / NS) & 1);
-      }
+      it += n;
+    }
+    if (!ok && lane == 0) give_up();
+    // leave nothing in flight: the last loads of every stage have landed
+    for (int j = max(0, it - NS); j < it; ++j) {
+      mbar_wait_bounded(&kfull[j % NS], (j / NS) & 1);
+      mbar_wait_bounded(&vfull[j % NS], (j / NS) & 1);
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------------ MMA issuer
@@ -271,7 +269,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int i = it + j;
           if (j + 1 < n) ok = scores(i + 1);
           ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(pready, i & 1) &&
-                                                 mbar_wait_bounded(&vfull[i % NS], (i / NS) & 1));
+                                                 mbar_wait_bounded(&vok[i % NS], (i / NS) & 1));
           if (!ok) break;
           tc_fence_after();
           const uint64_t vd = desc_advance(vd0, (i % NS) * Sh::kTile);
@@ -288,14 +286,76 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok && lane == 0) give_up();
     }
+  } else if (warp >= 6) {
+    // ------------------------------------------------------------------ guards of V
+    // In a block where some running row's positions end, non-finite values of positions that no
+    // row sees are cleared; those that a row does see are reported to the softmax.
+    const int gw = warp - 6;
+    int it = 0;
+    bool ok = true;
+    while (ok && !__any_sync(0xffffffffu, *abort_flag) && walk.next(p, cum, a)) {
+      int least = 0x7fffffff, most = 0;  // positions every running row sees; positions any row sees
+      for (int i = lane; i < kTm; i += 32) {
+        const int lim = attn_row(p, a.item, i).lim;
+        most = max(most, lim);
+        if (lim > 0) least = min(least, lim);
+      }
+      least = __reduce_min_sync(0xffffffffu, least);
+      most = __reduce_max_sync(0xffffffffu, most);
+      for (int blk = a.blk0; ok && blk < a.blk1; ++blk, ++it) {
+        const int s = it % NS;
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&vfull[s], (it / NS) & 1));
+        bool seen = false;
+        if (blk * BN + BN > least) {
+          uint8_t* vt = sv + s * Sh::kTile;
+          const int from = max(0, least - blk * BN);
+          // The swizzle keeps a position's 128 bytes of a panel together, so each panel is one run of
+          // 16-byte chunks. An exponent of all ones carries into its half's top bit.
+          const int run = (BN - from) * 8;
+          uint32_t any = 0;
+#pragma unroll 1
+          for (int j = 0; j < D / 64; ++j) {
+            const uint8_t* base = vt + j * Sh::kPanel + from * 128;
+#pragma unroll
+            for (int k = 0; k < BN * 8 / 64; ++k) {
+              const uint4 x = lds128(base + min(k * 64 + gw * 32 + lane, run - 1) * 16);
+              any |= (x.x & 0x7f807f80u) + 0x00800080u;
+              any |= (x.y & 0x7f807f80u) + 0x00800080u;
+              any |= (x.z & 0x7f807f80u) + 0x00800080u;
+              any |= (x.w & 0x7f807f80u) + 0x00800080u;
+            }
+          }
+          if (__any_sync(0xffffffffu, any & 0x80008000u)) {
+            for (int j = 0; j < D / 64; ++j)
+              for (int i = gw * 32 + lane; i < run; i += 64) {
+                uint4* at = reinterpret_cast<uint4*>(vt + j * Sh::kPanel + from * 128 + i * 16);
+                const uint4 x = *at;
+                if (odd_pair(x.x) || odd_pair(x.y) || odd_pair(x.z) || odd_pair(x.w)) {
+                  if (blk * BN + from + i / 8 >= most)
+                    *at = make_uint4(0u, 0u, 0u, 0u);
+                  else
+                    seen = true;
+                }
+              }
+            fence_async_smem();
+          }
+        }
+        seen = __any_sync(0xffffffffu, seen);
+        if (lane == 0) {
+          odd[2 * s + gw] = seen;
+          mbar_arrive(&vok[s]);
+        }
+      }
+    }
+    if (!ok && lane == 0) give_up();
   } else {
     // ------------------------------------------------------------------ softmax
     const int quad = warp & 3, row = quad * 32 + lane, st = threadIdx.x - 64;
     const uint32_t trow = tmem + (static_cast<uint32_t>(quad * 32) << 16);
     const float scale = fabsf(p.scale_log2);
     int it = 0;
-    // A wait that runs out ends all further waiting, not the walk: the softmax warps meet at block
-    // barriers, and so go through the same pieces whatever happens.
+    // A wait that runs out ends all further waiting, not the walk: whatever happens, a softmax warp
+    // goes through the same pieces as the others, which it meets at `meet`.
     bool ok = true;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       if (ok && !mbar_wait_bounded(bar, parity)) {
@@ -303,6 +363,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = false;
       }
       ok = __all_sync(0xffffffffu, ok);
+    };
+    uint32_t met = 0;
+    auto bar_soft = [&]() {  // a barrier of the softmax warps, with the limit of every wait
+      __syncwarp();
+      if (lane == 0) mbar_arrive(meet);
+      wait(meet, met & 1);
+      ++met;
     };
     while (walk.next(p, cum, a)) {
       const AttnRow ar = attn_row(p, a.item, row);
@@ -340,18 +407,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       {
         const int lo = __reduce_min_sync(0xffffffffu, ar.lim > 0 ? ar.lim : 0x7fffffff);
-        const int hi = __reduce_max_sync(0xffffffffu, ar.lim);
-        if (lane == 0) {
-          least_sm[quad] = lo;
-          most_sm[quad] = hi;
-        }
+        if (lane == 0) least_sm[quad] = lo;
         if (st == 0) *o_init = 0;
       }
       tc_fence_before();
       bar_soft();
       if (lane == 0) mbar_arrive(qready);
       const int least = min(min(least_sm[0], least_sm[1]), min(least_sm[2], least_sm[3]));
-      const int most = max(max(most_sm[0], most_sm[1]), max(most_sm[2], most_sm[3]));
       float m = -INFINITY, l = 0.f;
       for (int blk = a.blk0; blk < a.blk1; ++blk, ++it) {
         const bool first = blk == a.blk0;
@@ -394,8 +456,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int j = 0; j < BN / 64; ++j) tmem_st32(ts + 32 * j, w + 32 * j);
         const bool rescale = !first && __any_sync(0xffffffffu, grow);
-        const bool cut = blk * BN + BN > least;
-        if (rescale || cut) {
+        const int sg = it % NS;
+        bool by_hand = false;
+        if (blk * BN + BN > least) {
+          wait(&vok[sg], (it / NS) & 1);
+          by_hand = odd[2 * sg] | odd[2 * sg + 1];
+        }
+        if (rescale || by_hand) {
           // O of the blocks before is complete (the MMA of this one waits for this thread)
           if (!first) wait(&pvdone[(it - 1) & 1], ((it - 1) >> 1) & 1);
           tc_fence_after();
@@ -411,81 +478,61 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_st32(trow + d, u);
           }
         }
-        if (cut) {
-          const int s = it % NS;
-          wait(&vfull[s], (it / NS) & 1);
-          uint8_t* vt = sv + s * Sh::kTile;
-          if (st == 0) *seen_odd = 0;
-          bar_soft();
-          // a thread looks through 16-byte chunks of positions from the first that a row lacks
+        if (by_hand) {
+          uint8_t* vt = sv + sg * Sh::kTile;
           const int from = max(0, least - blk * BN), nrow = BN - from;
-          for (int i = st; i < nrow * (D / 8); i += kSoftThreads) {
-            const int pos = from + i / (D / 8), ch = i % (D / 8);
-            uint4* at = reinterpret_cast<uint4*>(vt + (ch / 8) * Sh::kPanel + pos * 128 +
-                                                 (((ch & 7) ^ (pos & 7)) << 4));
-            const uint4 x = *at;
-            if (odd_pair(x.x) || odd_pair(x.y) || odd_pair(x.z) || odd_pair(x.w)) {
-              if (blk * BN + pos >= most)
-                *at = make_uint4(0u, 0u, 0u, 0u);
-              else
-                *seen_odd = 1;
-            }
-          }
-          bar_soft();
-          if (*seen_odd) {
-            tmem_st_wait();
-            // Some rows see non-finite values and some do not. Each row adds its own share of those
-            // values to O (zero to begin with), then they are cleared for the tensor cores.
+          tmem_st_wait();
+          // Some rows see non-finite values and some do not. Each row adds its own share of those
+          // values to O (zero to begin with), then they are cleared for the tensor cores.
 #pragma unroll 1
-            for (int d = 0; d < D; d += 8) {
-              float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-              if (!first) tmem_ld8(trow + d, o);
-              for (int pos = from; pos < BN; ++pos) {
-                const uint4 x = *reinterpret_cast<const uint4*>(
-                    vt + (d / 64) * Sh::kPanel + pos * 128 + ((((d / 8) & 7) ^ (pos & 7)) << 4));
-                uint32_t pw;  // this position's weight and its neighbour's
-                asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n\t"
-                             "tcgen05.wait::ld.sync.aligned;"
-                             : "=r"(pw)
-                             : "r"(ts + pos / 2)
-                             : "memory");
-                if (pos < valid) {
-                  const uint32_t q4[4] = {x.x, x.y, x.z, x.w};
-                  const float e = __uint_as_float((pos & 1) ? (pw & 0xffff0000u) : (pw << 16));
+          for (int d = 0; d < D; d += 8) {
+            float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+            if (!first) tmem_ld8(trow + d, o);
+            for (int pos = from; pos < BN; ++pos) {
+              const uint4 x = *reinterpret_cast<const uint4*>(
+                  vt + (d / 64) * Sh::kPanel + pos * 128 + ((((d / 8) & 7) ^ (pos & 7)) << 4));
+              uint32_t pw;  // this position's weight and its neighbour's
+              asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n\t"
+                           "tcgen05.wait::ld.sync.aligned;"
+                           : "=r"(pw)
+                           : "r"(ts + pos / 2)
+                           : "memory");
+              if (pos < valid) {
+                const uint32_t q4[4] = {x.x, x.y, x.z, x.w};
+                const float e = __uint_as_float((pos & 1) ? (pw & 0xffff0000u) : (pw << 16));
 #pragma unroll
-                  for (int j = 0; j < 8; ++j) {
-                    const float f =
-                        __uint_as_float((j & 1) ? (q4[j / 2] & 0xffff0000u) : (q4[j / 2] << 16));
-                    if (!(fabsf(f) < INFINITY)) o[j] += e * f;
-                  }
+                for (int j = 0; j < 8; ++j) {
+                  const float f =
+                      __uint_as_float((j & 1) ? (q4[j / 2] & 0xffff0000u) : (q4[j / 2] << 16));
+                  if (!(fabsf(f) < INFINITY)) o[j] += e * f;
                 }
-                __syncwarp();
               }
               __syncwarp();
-              asm volatile(
-                  "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(
-                      trow + d),
-                  "r"(__float_as_uint(o[0])), "r"(__float_as_uint(o[1])), "r"(__float_as_uint(o[2])),
-                  "r"(__float_as_uint(o[3])), "r"(__float_as_uint(o[4])), "r"(__float_as_uint(o[5])),
-                  "r"(__float_as_uint(o[6])), "r"(__float_as_uint(o[7]))
-                  : "memory");
-              tmem_st_wait();
             }
-            bar_soft();
-            for (int i = st; i < nrow * (D / 8); i += kSoftThreads) {
-              const int pos = from + i / (D / 8), ch = i % (D / 8);
-              uint32_t* at = reinterpret_cast<uint32_t*>(vt + (ch / 8) * Sh::kPanel + pos * 128 +
-                                                         (((ch & 7) ^ (pos & 7)) << 4));
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                uint32_t x = at[j];
-                if ((x & 0x7f80u) == 0x7f80u) x &= 0xffff0000u;
-                if ((x & 0x7f800000u) == 0x7f800000u) x &= 0xffffu;
-                at[j] = x;
-              }
-            }
-            if (st == 0) *o_init = 1;
+            __syncwarp();
+            asm volatile(
+                "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(
+                    trow + d),
+                "r"(__float_as_uint(o[0])), "r"(__float_as_uint(o[1])), "r"(__float_as_uint(o[2])),
+                "r"(__float_as_uint(o[3])), "r"(__float_as_uint(o[4])), "r"(__float_as_uint(o[5])),
+                "r"(__float_as_uint(o[6])), "r"(__float_as_uint(o[7]))
+                : "memory");
+            tmem_st_wait();
           }
+          bar_soft();
+          for (int i = st; i < nrow * (D / 8); i += kSoftThreads) {
+            const int pos = from + i / (D / 8), ch = i % (D / 8);
+            uint32_t* at = reinterpret_cast<uint32_t*>(vt + (ch / 8) * Sh::kPanel + pos * 128 +
+                                                       (((ch & 7) ^ (pos & 7)) << 4));
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              uint32_t x = at[j];
+              if ((x & 0x7f80u) == 0x7f80u) x &= 0xffff0000u;
+              if ((x & 0x7f800000u) == 0x7f800000u) x &= 0xffffu;
+              at[j] = x;
+            }
+          }
+          if (st == 0) *o_init = 1;
           fence_async_smem();
           bar_soft();
         }
@@ -528,29 +575,25 @@ spec_status launch_tc(const AttnParams& p, int grid, EncodeTiledFn encode, cudaS
   const int smem = Sh::kFixed + 512 + 4 * (p.items + 1) + 1024;
   if (allow_dynamic_smem(attn_tc_kernel<D>, smem, allowed) != cudaSuccess) return SPEC_ERR_CUDA;
   AttnMaps m;
-  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(Sh::kBn), 1};
-  const cuuint32_t es[3] = {1, 1, 1};
-  const cuuint64_t width = static_cast<cuuint64_t>(p.Hkv) * D;
-  const auto map2 = [&](CUtensorMap* t, const uint8_t* base) {
-    const cuuint64_t dim[2] = {width, static_cast<cuuint64_t>(p.pcap)};
-    const cuuint64_t stride[1] = {static_cast<cuuint64_t>(p.pstride)};
-    return encode(t, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<uint8_t*>(base), dim, stride, box,
+  // dims inside a 64-dim panel, positions, panels (64 dims on), requests
+  const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(Sh::kBn), D / 64, 1};
+  const cuuint32_t es[4] = {1, 1, 1, 1};
+  const auto map = [&](CUtensorMap* t, const uint8_t* base, int64_t positions, int64_t step, int64_t reqs,
+                       int64_t req_step) {
+    const cuuint64_t dim[4] = {64, static_cast<cuuint64_t>(positions),
+                               static_cast<cuuint64_t>(p.Hkv) * (D / 64), static_cast<cuuint64_t>(reqs)};
+    const cuuint64_t stride[3] = {static_cast<cuuint64_t>(step), 128, static_cast<cuuint64_t>(req_step)};
+    return encode(t, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<uint8_t*>(base), dim, stride, box,
                   es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
   };
-  const auto map3 = [&](CUtensorMap* t, const uint8_t* base) {
-    const cuuint64_t dim[3] = {width, static_cast<cuuint64_t>(p.kcap), static_cast<cuuint64_t>(p.B)};
-    const cuuint64_t stride[2] = {
-        static_cast<cuuint64_t>(p.krow),
-        static_cast<cuuint64_t>(p.B > 1 ? p.kreq : p.krow * p.kcap)};
-    return encode(t, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint8_t*>(base), dim, stride, box,
-                  es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  };
-  if (map3(&m.ok, p.kk) != CUDA_SUCCESS || map3(&m.ov, p.kv) != CUDA_SUCCESS) return SPEC_ERR_CUDA;
+  const int64_t req = p.B > 1 ? p.kreq : p.krow;
+  if (!map(&m.ok, p.kk, p.kcap, p.krow, p.B, req) || !map(&m.ov, p.kv, p.kcap, p.krow, p.B, req))
+    return SPEC_ERR_CUDA;
   m.pk = m.ok;
   m.pv = m.ov;
-  if (p.npt > 0 && (map2(&m.pk, p.pk) != CUDA_SUCCESS || map2(&m.pv, p.pv) != CUDA_SUCCESS))
+  if (p.npt > 0 && (!map(&m.pk, p.pk, p.pcap, p.pstride, 1, p.pstride) ||
+                    !map(&m.pv, p.pv, p.pcap, p.pstride, 1, p.pstride)))
     return SPEC_ERR_CUDA;
   return launch_pdl(attn_tc_kernel<D>, dim3(grid), dim3(kThreads), smem, stream, m, p) == cudaSuccess
              ? SPEC_OK

@@ -54,7 +54,7 @@ struct AttnParams {
   const int32_t* n_rows;
   float* lse;
   WsHeader* hdr;
-  int32_t* cum;             // [items + 1]: blocks of one KV head before each item
+  int2* units;              // [items * Hkv]: each unit's first slot and number of partials
   float2* ml;               // [slots][tm]: running max (log2 domain) and sum
   float* o;                 // [slots][tm][D]
 };
@@ -111,6 +111,22 @@ __device__ __forceinline__ void attn_plan(const AttnParams& p, int32_t* cum) {
   __syncthreads();
 }
 
+// Each unit's partials, for the join; by CTA 0 of the kernel that computes them.
+__device__ __forceinline__ void attn_write_units(const AttnParams& p, const int32_t* cum,
+                                                 int64_t share) {
+  for (int u = threadIdx.x; u < p.items * p.Hkv; u += blockDim.x) {
+    const int item = u / p.Hkv, head = u - item * p.Hkv;
+    const int nb = cum[item + 1] - cum[item];
+    int2 v = make_int2(0, 0);
+    if (nb > 0) {
+      const int64_t start = static_cast<int64_t>(cum[item]) * p.Hkv + static_cast<int64_t>(head) * nb;
+      const int cta0 = static_cast<int>(start / share);
+      v = make_int2(cta0 + u, static_cast<int>((start + nb - 1) / share) - cta0 + 1);
+    }
+    p.units[u] = v;
+  }
+}
+
 // A CTA's piece of one unit.
 struct AttnPiece {
   int item, head, blk0, blk1, slot;
@@ -159,7 +175,7 @@ __device__ __forceinline__ AttnRow attn_row(const AttnParams& p, int item, int i
 }
 
 cudaError_t attn_simt_launch(const AttnParams& p, spec_dtype dtype, int grid, cudaStream_t stream);
-cudaError_t attn_join_launch(const AttnParams& p, spec_dtype dtype, int grid, cudaStream_t stream);
+cudaError_t attn_join_launch(const AttnParams& p, spec_dtype dtype, int sms, cudaStream_t stream);
 int attn_simt_tm();
 int attn_simt_bn();
 bool attn_tc_takes(int head_dim);  // bf16 only
