@@ -69,7 +69,7 @@ spec_status delta_params(const spec_state_desc* st, int32_t layer, const spec_de
 
 // Attention: the tile sizes of the kernel that takes the call, and the workspace's layout.
 struct AttnPlan {
-  int tc, tm, bn, npt, nown, items, grid;
+  int tc, tm, bn, npt, npi, pair, nown, items, grid;
   size_t units, ml, o, total;
 };
 
@@ -105,15 +105,20 @@ spec_status attn_plan_of(int32_t B, int32_t R, const spec_state_desc* st, const 
   const bool prefix = d->prefix_k && d->prefix_capacity > 0;
   const int64_t npt = prefix ? (B * per + w.tm - 1) / w.tm : 0;
   const int64_t nown = (per + w.tm - 1) / w.tm;
-  const int64_t items = npt + B * nown;
-  const int64_t blocks = npt * ((prefix ? d->prefix_capacity : 0) / w.bn + 1) +
-                         B * nown * (st->kv_capacity / w.bn + 1);
+  // two tiles of rows or more: pairs of CTAs take them two by two and share what they load of the prefix
+  w.pair = w.tc && npt >= 2 && a.sms % 2 == 0;
+  const int64_t npi = w.pair ? (npt + 1) / 2 : npt;
+  const int64_t items = npi + B * nown;
+  const int64_t blocks = npi * ((prefix ? d->prefix_capacity : 0) / w.bn + 1 + kAttnOver) +
+                         B * nown * (st->kv_capacity / w.bn + 1 + kAttnOver);
   if (items > kAttnMaxItems || blocks >= (int64_t(1) << 31)) return SPEC_ERR_UNSUPPORTED;
   w.npt = static_cast<int>(npt);
+  w.npi = static_cast<int>(npi);
   w.nown = static_cast<int>(nown);
   w.items = static_cast<int>(items);
   w.grid = a.sms;
-  const size_t slots = static_cast<size_t>(w.grid) + static_cast<size_t>(items) * d->kv_heads;
+  const size_t slots = 2 * static_cast<size_t>(w.grid) +
+                       static_cast<size_t>(items + (w.pair ? npi : 0)) * d->kv_heads;
   w.units = sizeof(WsHeader);
   w.ml = w.units + align_up(sizeof(int2) * static_cast<size_t>(items) * d->kv_heads, 256);
   w.o = w.ml + align_up(slots * w.tm * sizeof(float2), 256);
@@ -227,6 +232,9 @@ spec_status spec_prefix_attention(int32_t B, int32_t R, const spec_state_desc* s
   p.tm = w.tm;
   p.bn = w.bn;
   p.npt = w.npt;
+  p.npi = w.npi;
+  p.pair = w.pair;
+  p.over = kAttnOver;
   p.nown = w.nown;
   p.items = w.items;
   p.q = d->q;

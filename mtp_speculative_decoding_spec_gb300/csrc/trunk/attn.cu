@@ -63,37 +63,30 @@ __global__ void __launch_bounds__(kSimtThreads, 1)
   int* row_lim = reinterpret_cast<int*>(row_l + kSimtTm);
   int32_t* cum = row_lim + kSimtTm;
   attn_plan(p, cum);
-  const int64_t W = static_cast<int64_t>(cum[p.items]) * p.Hkv;
-  const int64_t share = (W + gridDim.x - 1) / gridDim.x;
-  if (blockIdx.x == 0) attn_write_units(p, cum, share);
-  int64_t x = share * blockIdx.x;
-  const int64_t x1 = min(W, x + share);
+  const AttnShares shares = attn_shares(p, cum);
+  if (blockIdx.x == 0) attn_write_units(p, cum, shares);
+  AttnWalk walk;
+  walk.start(p, shares);
+  AttnPiece a;
   const int warp = tid >> 5, lane = tid & 31;
   const int d0 = (tid & 63) * 4, r0 = (tid >> 6) * 4;  // values: dims and rows of this thread
-  while (x < x1) {
-    const int item = attn_item_of(p, cum, x);
-    const int nb = cum[item + 1] - cum[item];
-    const int64_t rel = x - static_cast<int64_t>(cum[item]) * p.Hkv;
-    const int head = static_cast<int>(rel / nb);
-    const int blk0 = static_cast<int>(rel - static_cast<int64_t>(head) * nb);
-    const int blk1 = static_cast<int>(min(static_cast<int64_t>(nb), blk0 + (x1 - x)));
-    const int slot = blockIdx.x + item * p.Hkv + head;
-    x += blk1 - blk0;
+  while (walk.next(p, cum, shares, a)) {
+    const int head = a.head, slot = a.slot;
     __syncthreads();  // the previous piece's shared memory is no longer read
     if (tid < kSimtTm) {
-      row_lim[tid] = attn_row(p, item, tid).lim;
+      row_lim[tid] = attn_row(p, a.tile, tid).lim;
       row_m[tid] = -INFINITY;
       row_l[tid] = 0.f;
     }
     for (int i = tid; i < kSimtTm * D; i += kSimtThreads) {
       const int r = i / D, d = i - r * D;
-      const AttnRow a = attn_row(p, item, r);
-      const int64_t at = (static_cast<int64_t>(a.b) * p.R + a.r) * p.qs +
-                         static_cast<int64_t>(head * p.G + a.g) * D + d;
-      qs[r * ld + d] = a.lim > 0 ? to_f(static_cast<const T*>(p.q)[at]) : 0.f;
+      const AttnRow ar = attn_row(p, a.tile, r);
+      const int64_t at = (static_cast<int64_t>(ar.b) * p.R + ar.r) * p.qs +
+                         static_cast<int64_t>(head * p.G + ar.g) * D + d;
+      qs[r * ld + d] = ar.lim > 0 ? to_f(static_cast<const T*>(p.q)[at]) : 0.f;
     }
-    const bool pre = item < p.npt;
-    const int b = pre ? 0 : (item - p.npt) / p.nown;
+    const bool pre = a.tile < p.npt;
+    const int b = pre ? 0 : (a.tile - p.npt) / p.nown;
     const uint8_t* kbase = pre ? p.pk : p.kk + static_cast<int64_t>(b) * p.kreq;
     const uint8_t* vbase = pre ? p.pv : p.kv + static_cast<int64_t>(b) * p.kreq;
     const int64_t step = pre ? p.pstride : p.krow;
@@ -105,7 +98,7 @@ __global__ void __launch_bounds__(kSimtThreads, 1)
       if (row_lim[r] > 0) least = min(least, row_lim[r]);
     }
     float acc[4][4] = {};
-    for (int blk = blk0; blk < blk1; ++blk) {
+    for (int blk = a.blk0; blk < a.blk1; ++blk) {
       const int p0 = blk * kSimtBn;
       __syncthreads();
       for (int i = tid; i < kSimtBn * (D / 8); i += kSimtThreads) {
@@ -227,8 +220,10 @@ __global__ void __launch_bounds__(NW == 1 ? 128 : 32 * NW)
   pdl_wait();
   const int rows = attn_rows(p, b);
   int2 u0 = make_int2(0, 0);
-  if (p.npt > 0) u0 = __ldcg(p.units + (s / p.tm) * p.Hkv + head);
-  int2 u1 = __ldcg(p.units + (p.npt + b * p.nown + x / p.tm) * p.Hkv + head);
+  const int t0 = s / p.tm;
+  if (p.npt > 0) u0 = __ldcg(p.units + (t0 >> p.pair) * p.Hkv + head);
+  int2 u1 = __ldcg(p.units + (p.npi + b * p.nown + x / p.tm) * p.Hkv + head);
+  if (p.pair) u0.x += t0 & 1;
   if (p.npt > 0 && attn_prefix(p, b) == 0) u0.y = 0;
   if (r >= rows) u0.y = u1.y = 0;
   const int at0 = s % p.tm, at1 = x % p.tm, ntot = u0.y + u1.y;
@@ -245,7 +240,7 @@ __global__ void __launch_bounds__(NW == 1 ? 128 : 32 * NW)
       ov[j][0] = ov[j][1] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (i < ntot) {
         const bool pre = i < u0.y;
-        const int64_t t = static_cast<int64_t>(pre ? u0.x + i : u1.x + i - u0.y) * p.tm +
+        const int64_t t = static_cast<int64_t>(pre ? u0.x + (i << p.pair) : u1.x + i - u0.y) * p.tm +
                           (pre ? at0 : at1);
         mlv[j] = __ldcg(p.ml + t);
         const float4* o = reinterpret_cast<const float4*>(p.o + t * p.D);

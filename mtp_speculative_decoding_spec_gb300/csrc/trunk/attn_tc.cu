@@ -46,18 +46,29 @@ struct Shape {
   static_assert(kQ + D / 2 <= 512, "TMEM");
 };
 
-// A whole block of K or V at once: [panel of 64 dims][position][64 dims], the order of its map's box.
-// Called by a whole warp, one lane issues.
+// A block of K or V at once: [panel of 64 dims][position][64 dims], the order of its map's box. `both`:
+// to the same place in both CTAs of the pair, with the bytes counted on each one's barrier. Called by
+// a whole warp, one lane of which issues; `expect` are the bytes that this CTA's barrier waits for.
 __device__ __forceinline__ void tma_load_block(void* dst, const CUtensorMap* map, int pos, int panel,
-                                               int b, uint64_t* bar, uint32_t bytes) {
-  asm volatile(
-      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
-      "@e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%5], %6;\n\t"
-      "@e cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%7, %2, %3, %4}], [%5];\n\t}" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(pos), "r"(panel), "r"(b), "r"(smem_u32(bar)),
-      "r"(bytes), "r"(0)
-      : "memory");
+                                               int b, uint64_t* bar, uint32_t expect, bool both) {
+  if (both)
+    asm volatile(
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%5], %6;\n\t"
+        "@e cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        ".multicast::cluster [%0], [%1, {%7, %2, %3, %4}], [%5], %8;\n\t}" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(pos), "r"(panel), "r"(b), "r"(smem_u32(bar)),
+        "r"(expect), "r"(0), "h"(static_cast<uint16_t>(3))
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%5], %6;\n\t"
+        "@e cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%7, %2, %3, %4}], [%5];\n\t}" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(pos), "r"(panel), "r"(b), "r"(smem_u32(bar)),
+        "r"(expect), "r"(0)
+        : "memory");
 }
 
 // B operand whose rows (K) are 128 bytes of N in the 128-byte swizzle: 8-row groups 1,024 bytes
@@ -87,6 +98,18 @@ __device__ __forceinline__ void tc_commit_elect(uint64_t* bar) {
       "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
           smem_u32(bar))
       : "memory");
+}
+
+__device__ __forceinline__ void tc_commit_both(uint64_t* bar) {  // on both CTAs' barriers
+  asm volatile(
+      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+      " [%0], %1;\n\t}" ::"r"(smem_u32(bar)),
+      "h"(static_cast<uint16_t>(3))
+      : "memory");
+}
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
 
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
@@ -120,28 +143,18 @@ __device__ __forceinline__ bool odd_pair(uint32_t w) {  // an Inf or NaN in eith
   return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
 }
 
-// One piece after another of a CTA's share of the blocks.
-struct Walk {
-  int64_t x, x1;
-  __device__ __forceinline__ bool next(const AttnParams& p, const int32_t* cum, AttnPiece& a) {
-    if (x >= x1) return false;
-    a.item = attn_item_of(p, cum, x);
-    const int nb = cum[a.item + 1] - cum[a.item];
-    const int64_t rel = x - static_cast<int64_t>(cum[a.item]) * p.Hkv;
-    a.head = static_cast<int>(rel / nb);
-    a.blk0 = static_cast<int>(rel - static_cast<int64_t>(a.head) * nb);
-    a.blk1 = static_cast<int>(min(static_cast<int64_t>(nb), a.blk0 + (x1 - x)));
-    a.slot = static_cast<int>(blockIdx.x) + a.item * p.Hkv + a.head;
-    x += a.blk1 - a.blk0;
-    return true;
-  }
-};
+template <int D>
+__device__ __forceinline__ const __nv_bfloat16* q_row(const AttnParams& p, const AttnPiece& a,
+                                                      const AttnRow& r) {
+  return static_cast<const __nv_bfloat16*>(p.q) + (static_cast<int64_t>(r.b) * p.R + r.r) * p.qs +
+         static_cast<int64_t>(a.head * p.G + r.g) * D;
+}
 
 struct AttnMaps {
   CUtensorMap pk, pv, ok, ov;
 };
 
-template <int D>
+template <int D, bool kPair>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_tc_kernel(const __grid_constant__ AttnMaps maps, const __grid_constant__ AttnParams p) {
   using Sh = Shape<D>;
@@ -157,15 +170,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* vempty = vfull + NS;
   uint64_t* vok = vempty + NS;    // V has landed and been looked through
   uint64_t* sfull = vok + NS;     // [2]
+  // two each, in turns: the scores of block i+1 are out before the weights of block i are waited for,
+  // so one barrier could run through two phases while its waiter looks away
   uint64_t* pready = sfull + 2;
-  uint64_t* pvdone = pready + 1;  // [2]: a softmax that skipped waits cannot take one phase for another
+  uint64_t* pvdone = pready + 2;
   uint64_t* qready = pvdone + 2;
   uint64_t* meet = qready + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(meet + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  volatile int* o_init = abort_flag + 1;      // O holds something before the piece's first MMA on it
-  volatile int* odd = abort_flag + 2;         // [NS][2]: a row sees a non-finite V of the stage
-  int* least_sm = const_cast<int*>(odd + 2 * NS);  // [4] per softmax warp
+  volatile int* o_init = abort_flag + 1;      // [2] O holds something before the piece's first MMA on it
+  volatile int* odd = abort_flag + 3;         // [NS][2]: a row sees a non-finite V of the stage
+  int* least_sm = const_cast<int*>(odd + 2 * NS);  // [2][4] per softmax warp
   int32_t* cum = reinterpret_cast<int32_t*>(smem + Sh::kFixed + 512);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -173,14 +188,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < NS; ++s) {
       mbar_init(&kfull[s], 1);
-      mbar_init(&kempty[s], 1);
+      mbar_init(&kempty[s], kPair ? 2 : 1);
       mbar_init(&vfull[s], 1);
-      mbar_init(&vempty[s], 1);
+      mbar_init(&vempty[s], kPair ? 2 : 1);
       mbar_init(&vok[s], 2);
     }
     mbar_init(&sfull[0], 1);
     mbar_init(&sfull[1], 1);
-    mbar_init(pready, 4);
+    mbar_init(&pready[0], 4);
+    mbar_init(&pready[1], 4);
     mbar_init(&pvdone[0], 1);
     mbar_init(&pvdone[1], 1);
     mbar_init(qready, 4);
@@ -195,12 +211,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
-  const int64_t W = static_cast<int64_t>(cum[p.items]) * p.Hkv;
-  const int64_t share = (W + gridDim.x - 1) / gridDim.x;
-  if (blockIdx.x == 0) attn_write_units(p, cum, share);
-  Walk walk;
-  walk.x = share * blockIdx.x;
-  walk.x1 = min(W, walk.x + share);
+  const AttnShares shares = attn_shares(p, cum);
+  if (blockIdx.x == 0) attn_write_units(p, cum, shares);
+  if (kPair) cluster_barrier();  // the barriers of both CTAs stand before either one's copies arrive
+  const int rank = kPair ? blockIdx.x & 1 : 0;
+  AttnWalk walk;
+  walk.start(p, shares);
   AttnPiece a;
   auto give_up = [&]() {
     atomicOr(&p.hdr->error, ERR_TC_WAIT);
@@ -211,15 +227,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------------ TMA producer
     int it = 0;  // V blocks; K runs one block ahead, as the MMAs take them
     bool ok = true;
-    while (ok && !__any_sync(0xffffffffu, *abort_flag) && walk.next(p, cum, a)) {
-      const bool pre = a.item < p.npt;
-      const int b = pre ? 0 : (a.item - p.npt) / p.nown, panel = a.head * (D / 64);
+    while (ok && !__any_sync(0xffffffffu, *abort_flag) && walk.next(p, cum, shares, a)) {
+      const bool both = kPair && a.pair, pre = both || a.tile < p.npt;
+      const int b = pre ? 0 : (a.tile - p.npt) / p.nown, panel = a.head * (D / 64);
+      // in pairs, each CTA loads half of the block's panels (of its positions, if it has one panel)
+      const int half = both ? rank * (Sh::kTile / 2) : 0;
+      const int dpos = both && D == 64 ? rank * (BN / 2) : 0, dpan = both && D > 64 ? rank * (D / 128) : 0;
       auto load = [&](uint8_t* tiles, uint64_t* full, uint64_t* empty, const CUtensorMap* map, int i,
                       int blk) {
         const int s = i % NS;
         if (i >= NS && !__all_sync(0xffffffffu, mbar_wait_bounded(&empty[s], ((i / NS) & 1) ^ 1)))
           return false;
-        tma_load_block(tiles + s * Sh::kTile, map, blk * BN, panel, b, &full[s], Sh::kTile);
+        tma_load_block(tiles + s * Sh::kTile + half, map, blk * BN + dpos, panel + dpan, b, &full[s],
+                       Sh::kTile, both);
         return true;
       };
       const CUtensorMap* mk = pre ? &maps.pk : &maps.ok;
@@ -233,10 +253,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       it += n;
     }
     if (!ok && lane == 0) give_up();
-    // leave nothing in flight: the last loads of every stage have landed
+    // leave nothing in flight: the last loads of every stage have landed, and in pairs the other CTA's
+    // arrivals on this one's barriers
     for (int j = max(0, it - NS); j < it; ++j) {
       mbar_wait_bounded(&kfull[j % NS], (j / NS) & 1);
       mbar_wait_bounded(&vfull[j % NS], (j / NS) & 1);
+      if (kPair) {
+        mbar_wait_bounded(&kempty[j % NS], (j / NS) & 1);
+        mbar_wait_bounded(&vempty[j % NS], (j / NS) & 1);
+      }
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------------ MMA issuer
@@ -247,6 +272,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t vd0 = smem_desc_n_major(smem_u32(sv), Sh::kPanel);
       int it = 0, piece = 0;
       bool ok = true;
+      // a stage is free when both CTAs of a pair have read it
+      auto free_stage = [&](uint64_t* bar) {
+        if (kPair && a.pair) {
+          tc_commit_both(bar);
+        } else {
+          tc_commit_elect(bar);
+          if (kPair) tc_commit_elect(bar);
+        }
+      };
       auto scores = [&](int i) {
         if (!__all_sync(0xffffffffu, mbar_wait_bounded(&kfull[i % NS], (i / NS) & 1))) return false;
         tc_fence_after();
@@ -257,10 +291,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_mma_ta(ds, tmem + Sh::kQ + kk * 8,
                     desc_advance(kd, (kk / 4) * Sh::kPanel + (kk % 4) * 32), kIdS, kk > 0);
         tc_commit_elect(&sfull[i & 1]);
-        tc_commit_elect(&kempty[i % NS]);
+        free_stage(&kempty[i % NS]);
         return true;
       };
-      while (ok && !__any_sync(0xffffffffu, *abort_flag) && walk.next(p, cum, a)) {
+      while (ok && !__any_sync(0xffffffffu, *abort_flag) && walk.next(p, cum, shares, a)) {
         const int n = a.blk1 - a.blk0;
         ok = __all_sync(0xffffffffu, mbar_wait_bounded(qready, piece & 1));
         tc_fence_after();
@@ -268,17 +302,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int j = 0; ok && j < n; ++j) {
           const int i = it + j;
           if (j + 1 < n) ok = scores(i + 1);
-          ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(pready, i & 1) &&
+          ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(&pready[i & 1], (i >> 1) & 1) &&
                                                  mbar_wait_bounded(&vok[i % NS], (i / NS) & 1));
           if (!ok) break;
           tc_fence_after();
           const uint64_t vd = desc_advance(vd0, (i % NS) * Sh::kTile);
           const uint32_t ps = tmem + Sh::kS + (i & 1) * BN;
-          const uint32_t acc0 = j > 0 || *o_init ? 1u : 0u;
+          const uint32_t acc0 = j > 0 || o_init[piece & 1] ? 1u : 0u;
 #pragma unroll
           for (int kk = 0; kk < BN / 16; ++kk)
             tc_mma_ta(tmem, ps + kk * 8, desc_advance(vd, kk * 2048), kIdO, kk > 0 ? 1u : acc0);
-          tc_commit_elect(&vempty[i % NS]);
+          free_stage(&vempty[i % NS]);
           tc_commit_elect(&pvdone[i & 1]);
         }
         it += n;
@@ -293,15 +327,27 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int gw = warp - 6;
     int it = 0;
     bool ok = true;
-    while (ok && !__any_sync(0xffffffffu, *abort_flag) && walk.next(p, cum, a)) {
+    while (ok && !__any_sync(0xffffffffu, *abort_flag) && walk.next(p, cum, shares, a)) {
       int least = 0x7fffffff, most = 0;  // positions every running row sees; positions any row sees
       for (int i = lane; i < kTm; i += 32) {
-        const int lim = attn_row(p, a.item, i).lim;
+        const int lim = attn_row(p, a.tile, i).lim;
         most = max(most, lim);
         if (lim > 0) least = min(least, lim);
       }
       least = __reduce_min_sync(0xffffffffu, least);
       most = __reduce_max_sync(0xffffffffu, most);
+      {  // the next piece's queries, towards L2
+        AttnWalk ahead = walk;
+        AttnPiece nx;
+        if (ahead.next(p, cum, shares, nx))
+          for (int i = gw * 32 + lane; i < kTm; i += 64) {
+            const AttnRow r = attn_row(p, nx.tile, i);
+            if (r.lim <= 0) continue;
+            const __nv_bfloat16* src = q_row<D>(p, nx, r);
+            for (int d = 0; d < D; d += 64)
+              asm volatile("prefetch.global.L2 [%0];" ::"l"(src + d));
+          }
+      }
       for (int blk = a.blk0; ok && blk < a.blk1; ++blk, ++it) {
         const int s = it % NS;
         ok = __all_sync(0xffffffffu, mbar_wait_bounded(&vfull[s], (it / NS) & 1));
@@ -371,53 +417,59 @@ __global__ void __launch_bounds__(kThreads, 1)
       wait(meet, met & 1);
       ++met;
     };
-    while (walk.next(p, cum, a)) {
-      const AttnRow ar = attn_row(p, a.item, row);
-      // Q: this thread's row into its TMEM lane; a negative scale goes into Q's signs
-      {
-        const uint32_t flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;
-        const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.q) +
-                                   (static_cast<int64_t>(ar.b) * p.R + ar.r) * p.qs +
-                                   static_cast<int64_t>(a.head * p.G + ar.g) * D;
-        const bool vec = (reinterpret_cast<uintptr_t>(src) & 15u) == 0;
-#pragma unroll 1
-        for (int d = 0; d < D; d += 64) {
-          uint32_t w[32];
+    // Q of a piece: this thread's row into its TMEM lane; a negative scale goes into Q's signs
+    int piece = 0, least = 0;
+    AttnRow ar;
+    auto load_q = [&](const AttnPiece& pc) {
+      ar = attn_row(p, pc.tile, row);
+      const uint32_t flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;
+      const __nv_bfloat16* src = q_row<D>(p, pc, ar);
+      const bool vec = (reinterpret_cast<uintptr_t>(src) & 15u) == 0;
 #pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            uint4 v = make_uint4(0u, 0u, 0u, 0u);
-            if (ar.lim > 0) {
-              if (vec) {
-                v = __ldg(reinterpret_cast<const uint4*>(src + d) + c);
-              } else {
-                const uint16_t* h = reinterpret_cast<const uint16_t*>(src + d) + c * 8;
-                v.x = h[0] | static_cast<uint32_t>(h[1]) << 16;
-                v.y = h[2] | static_cast<uint32_t>(h[3]) << 16;
-                v.z = h[4] | static_cast<uint32_t>(h[5]) << 16;
-                v.w = h[6] | static_cast<uint32_t>(h[7]) << 16;
-              }
+      for (int d = 0; d < D; d += 128) {  // up to 16 loads in flight
+        constexpr int kW = D < 128 ? 32 : 64;
+        uint32_t w[kW];
+#pragma unroll
+        for (int c = 0; c < kW / 4; ++c) {
+          uint4 v = make_uint4(0u, 0u, 0u, 0u);
+          if (ar.lim > 0) {
+            if (vec) {
+              v = __ldg(reinterpret_cast<const uint4*>(src + d) + c);
+            } else {
+              const uint16_t* h = reinterpret_cast<const uint16_t*>(src + d) + c * 8;
+              v.x = h[0] | static_cast<uint32_t>(h[1]) << 16;
+              v.y = h[2] | static_cast<uint32_t>(h[3]) << 16;
+              v.z = h[4] | static_cast<uint32_t>(h[5]) << 16;
+              v.w = h[6] | static_cast<uint32_t>(h[7]) << 16;
             }
-            w[4 * c] = v.x ^ flip, w[4 * c + 1] = v.y ^ flip;
-            w[4 * c + 2] = v.z ^ flip, w[4 * c + 3] = v.w ^ flip;
           }
-          __syncwarp();
-          tmem_st32(trow + Sh::kQ + d / 2, w);
+          w[4 * c] = v.x ^ flip, w[4 * c + 1] = v.y ^ flip;
+          w[4 * c + 2] = v.z ^ flip, w[4 * c + 3] = v.w ^ flip;
         }
-        tmem_st_wait();
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < kW / 32; ++j) tmem_st32(trow + Sh::kQ + d / 2 + 32 * j, w + 32 * j);
       }
-      {
-        const int lo = __reduce_min_sync(0xffffffffu, ar.lim > 0 ? ar.lim : 0x7fffffff);
-        if (lane == 0) least_sm[quad] = lo;
-        if (st == 0) *o_init = 0;
-      }
+      tmem_st_wait();
+      const int lo = __reduce_min_sync(0xffffffffu, ar.lim > 0 ? ar.lim : 0x7fffffff);
+      int* lsm = least_sm + 4 * (piece & 1);
+      if (lane == 0) lsm[quad] = lo;
+      if (st == 0) o_init[piece & 1] = 0;
       tc_fence_before();
       bar_soft();
       if (lane == 0) mbar_arrive(qready);
-      const int least = min(min(least_sm[0], least_sm[1]), min(least_sm[2], least_sm[3]));
+      least = min(min(lsm[0], lsm[1]), min(lsm[2], lsm[3]));
+    };
+    bool more = walk.next(p, cum, shares, a);
+    if (more) load_q(a);
+    while (more) {
+      const int lim = ar.lim, from_all = least;
+      const int64_t at = static_cast<int64_t>(a.slot) * kTm + row;
+      const int blk_end = a.blk1;
       float m = -INFINITY, l = 0.f;
-      for (int blk = a.blk0; blk < a.blk1; ++blk, ++it) {
-        const bool first = blk == a.blk0;
-        const int valid = min(BN, ar.lim - blk * BN);  // positions of the block this row sees
+      for (int blk = a.blk0, blk0 = blk; blk < blk_end; ++blk, ++it) {
+        const bool first = blk == blk0;
+        const int valid = min(BN, lim - blk * BN);  // positions of the block this row sees
         wait(&sfull[it & 1], (it >> 1) & 1);
         tc_fence_after();
         const uint32_t ts = trow + Sh::kS + (it & 1) * BN;
@@ -458,7 +510,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool rescale = !first && __any_sync(0xffffffffu, grow);
         const int sg = it % NS;
         bool by_hand = false;
-        if (blk * BN + BN > least) {
+        if (blk * BN + BN > from_all) {
           wait(&vok[sg], (it / NS) & 1);
           by_hand = odd[2 * sg] | odd[2 * sg + 1];
         }
@@ -480,7 +532,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (by_hand) {
           uint8_t* vt = sv + sg * Sh::kTile;
-          const int from = max(0, least - blk * BN), nrow = BN - from;
+          const int from = max(0, from_all - blk * BN), nrow = BN - from;
           tmem_st_wait();
           // Some rows see non-finite values and some do not. Each row adds its own share of those
           // values to O (zero to begin with), then they are cleared for the tensor cores.
@@ -532,32 +584,37 @@ __global__ void __launch_bounds__(kThreads, 1)
               at[j] = x;
             }
           }
-          if (st == 0) *o_init = 1;
+          if (st == 0) o_init[piece & 1] = 1;
           fence_async_smem();
           bar_soft();
         }
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(pready);
+        if (lane == 0) mbar_arrive(&pready[it & 1]);
+        if (blk + 1 == blk_end) {
+          // every product with this piece's Q is complete: the next one's can take its place, and its
+          // first scores be computed, while this piece's output is written
+          ++piece;
+          more = walk.next(p, cum, shares, a);
+          if (more) load_q(a);
+        }
       }
       // the piece's partial
       wait(&pvdone[(it - 1) & 1], ((it - 1) >> 1) & 1);
       tc_fence_after();
-      const int64_t at = static_cast<int64_t>(a.slot) * kTm + row;
-      if (ar.lim > 0) p.ml[at] = make_float2(m, l);
+      if (lim > 0) p.ml[at] = make_float2(m, l);
 #pragma unroll 1
       for (int d = 0; d < D; d += 32) {
         float o[32];
         tmem_ld32(trow + d, o);
-        if (ar.lim > 0) {
+        if (lim > 0) {
 #pragma unroll
           for (int j = 0; j < 32; j += 4)
             *reinterpret_cast<float4*>(p.o + at * D + d + j) = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
         }
       }
       tc_fence_before();
-      bar_soft();  // every thread is done with this piece's lengths and Q
     }
   }
   tc_fence_before();
@@ -566,20 +623,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
+  if (kPair) cluster_barrier();  // the other CTA's copies and arrivals still come to this one's memory
 }
 
-template <int D>
+template <int D, bool kPair>
 spec_status launch_tc(const AttnParams& p, int grid, EncodeTiledFn encode, cudaStream_t stream) {
   using Sh = Shape<D>;
   static SmemAllowance allowed;
   const int smem = Sh::kFixed + 512 + 4 * (p.items + 1) + 1024;
-  if (allow_dynamic_smem(attn_tc_kernel<D>, smem, allowed) != cudaSuccess) return SPEC_ERR_CUDA;
+  if (allow_dynamic_smem(attn_tc_kernel<D, kPair>, smem, allowed) != cudaSuccess) return SPEC_ERR_CUDA;
   AttnMaps m;
   // dims inside a 64-dim panel, positions, panels (64 dims on), requests
-  const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(Sh::kBn), D / 64, 1};
+  const cuuint32_t whole[4] = {64, static_cast<cuuint32_t>(Sh::kBn), D / 64, 1};
+  const cuuint32_t half[4] = {64, static_cast<cuuint32_t>(D == 64 ? Sh::kBn / 2 : Sh::kBn),
+                              D == 64 ? 1 : D / 128, 1};
   const cuuint32_t es[4] = {1, 1, 1, 1};
   const auto map = [&](CUtensorMap* t, const uint8_t* base, int64_t positions, int64_t step, int64_t reqs,
-                       int64_t req_step) {
+                       int64_t req_step, const cuuint32_t* box) {
     const cuuint64_t dim[4] = {64, static_cast<cuuint64_t>(positions),
                                static_cast<cuuint64_t>(p.Hkv) * (D / 64), static_cast<cuuint64_t>(reqs)};
     const cuuint64_t stride[3] = {static_cast<cuuint64_t>(step), 128, static_cast<cuuint64_t>(req_step)};
@@ -588,16 +648,34 @@ spec_status launch_tc(const AttnParams& p, int grid, EncodeTiledFn encode, cudaS
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
   };
   const int64_t req = p.B > 1 ? p.kreq : p.krow;
-  if (!map(&m.ok, p.kk, p.kcap, p.krow, p.B, req) || !map(&m.ov, p.kv, p.kcap, p.krow, p.B, req))
+  if (!map(&m.ok, p.kk, p.kcap, p.krow, p.B, req, whole) || !map(&m.ov, p.kv, p.kcap, p.krow, p.B, req, whole))
     return SPEC_ERR_CUDA;
   m.pk = m.ok;
   m.pv = m.ov;
-  if (p.npt > 0 && (!map(&m.pk, p.pk, p.pcap, p.pstride, 1, p.pstride) ||
-                    !map(&m.pv, p.pv, p.pcap, p.pstride, 1, p.pstride)))
+  if (p.npt > 0 && (!map(&m.pk, p.pk, p.pcap, p.pstride, 1, p.pstride, kPair ? half : whole) ||
+                    !map(&m.pv, p.pv, p.pcap, p.pstride, 1, p.pstride, kPair ? half : whole)))
     return SPEC_ERR_CUDA;
-  return launch_pdl(attn_tc_kernel<D>, dim3(grid), dim3(kThreads), smem, stream, m, p) == cudaSuccess
-             ? SPEC_OK
-             : SPEC_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = kPair ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, attn_tc_kernel<D, kPair>, m, p) == cudaSuccess ? SPEC_OK
+                                                                                : SPEC_ERR_CUDA;
+}
+
+template <int D>
+spec_status launch_of(const AttnParams& p, int grid, EncodeTiledFn encode, cudaStream_t stream) {
+  return p.pair ? launch_tc<D, true>(p, grid, encode, stream)
+                : launch_tc<D, false>(p, grid, encode, stream);
 }
 
 }  // namespace
@@ -607,9 +685,9 @@ int attn_tc_tm() { return kTm; }
 int attn_tc_bn(int head_dim) { return head_dim == 256 ? Shape<256>::kBn : Shape<128>::kBn; }
 
 spec_status attn_tc_launch(const AttnParams& p, int grid, EncodeTiledFn encode, cudaStream_t stream) {
-  return p.D == 256   ? launch_tc<256>(p, grid, encode, stream)
-         : p.D == 128 ? launch_tc<128>(p, grid, encode, stream)
-                      : launch_tc<64>(p, grid, encode, stream);
+  return p.D == 256   ? launch_of<256>(p, grid, encode, stream)
+         : p.D == 128 ? launch_of<128>(p, grid, encode, stream)
+                      : launch_of<64>(p, grid, encode, stream);
 }
 
 }  // namespace spec

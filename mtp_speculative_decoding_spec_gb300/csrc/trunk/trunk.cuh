@@ -33,13 +33,17 @@ cudaError_t delta_scan_launch(const DeltaParams& p, spec_dtype dtype, int sms, c
 // Attention of verify rows over a shared prefix and each request's own cache. The work is cut into
 // units: a tile of `tm` rows and a KV head over the positions of one region. Prefix tiles hold the
 // rows of all requests stacked (s = (b R + r) G + g), own tiles the R G rows of one request. A unit
-// is cut into blocks of `bn` positions, the blocks of all units in a row are dealt out evenly to
-// the grid, and each (CTA, unit) that meet leave one partial (max, sum, unnormalised output) in
-// slot cta + unit. Item = a tile of rows for all KV heads: prefix tiles first, then own tiles.
+// is cut into blocks of `bn` positions; the blocks of all units in a row are dealt out evenly to
+// the grid, and each (CTA, unit) that meet leave one partial (max, sum, unnormalised output) in a
+// slot of their own. Item = a tile of rows for all KV heads: prefix tiles first, then own tiles.
+// With `pair`, prefix items are two tiles each and go to pairs of CTAs, one tile to a CTA, before the
+// own items go to single CTAs. `over` is what starting a unit costs, in blocks: it counts in the
+// dealing as if the unit began with that many blocks more.
 struct AttnParams {
   int B, R, G, Hkv, D;
   int tm, bn;
-  int npt, nown, items;     // prefix tiles, own tiles per request, npt + B * nown
+  int npt, npi, nown, items;  // prefix tiles and items, own tiles per request, npi + B * nown
+  int pair, over;
   const void* q;
   int64_t qs;
   void* out;
@@ -60,6 +64,7 @@ struct AttnParams {
 };
 
 constexpr int kAttnMaxItems = 8192;
+constexpr int kAttnOver = 2;  // see `over`
 
 // Rows of request b that run.
 __device__ __forceinline__ int attn_rows(const AttnParams& p, int b) {
@@ -74,22 +79,24 @@ __device__ __forceinline__ int attn_own(const AttnParams& p, int b, int rows) {
       min(max(p.kv_len[b], static_cast<int64_t>(0)) + rows, p.kcap));
 }
 
-// cum[0..items] in shared memory, by the whole block (a barrier at the end). Every CTA works it out
-// for itself from the lengths on the device, so no launch comes before and no host reads them.
+// cum[0..items] in shared memory: cost of one KV head before each item, in blocks. By the whole block
+// (a barrier at the end). Every CTA works it out for itself from the lengths on the device, so no
+// launch comes before and no host reads them.
 __device__ __forceinline__ void attn_plan(const AttnParams& p, int32_t* cum) {
   const int tid = threadIdx.x, nt = blockDim.x, per = p.R * p.G;
   for (int i = tid; i < p.items; i += nt) {
     int n = 0;
-    if (i < p.npt) {
-      const int b0 = i * p.tm / per, b1 = min(p.B - 1, ((i + 1) * p.tm - 1) / per);
+    if (i < p.npi) {
+      const int span = p.tm << p.pair;
+      const int b0 = i * span / per, b1 = min(p.B - 1, ((i + 1) * span - 1) / per);
       for (int b = b0; b <= b1; ++b)
         if (attn_rows(p, b) > 0) n = max(n, attn_prefix(p, b));
     } else {
-      const int b = (i - p.npt) / p.nown;
+      const int b = (i - p.npi) / p.nown;
       const int rows = attn_rows(p, b);
       if (rows > 0) n = attn_own(p, b, rows);
     }
-    cum[i + 1] = (n + p.bn - 1) / p.bn;
+    cum[i + 1] = n > 0 ? (n + p.bn - 1) / p.bn + p.over : 0;
   }
   if (tid == 0) cum[0] = 0;
   __syncthreads();
@@ -111,51 +118,121 @@ __device__ __forceinline__ void attn_plan(const AttnParams& p, int32_t* cum) {
   __syncthreads();
 }
 
-// Each unit's partials, for the join; by CTA 0 of the kernel that computes them.
+// How the costs are dealt out: the pairs' part [0, wp), `sp` to each pair of CTAs, and the rest up to
+// w, `s1` to each CTA; where the second part's slots begin.
+struct AttnShares {
+  int64_t wp, w, sp, s1;
+  int u1, base1;
+};
+__device__ __forceinline__ AttnShares attn_shares(const AttnParams& p, const int32_t* cum) {
+  AttnShares s;
+  const int grid = gridDim.x;
+  s.w = static_cast<int64_t>(cum[p.items]) * p.Hkv;
+  s.wp = p.pair ? static_cast<int64_t>(cum[p.npi]) * p.Hkv : 0;
+  s.sp = p.pair ? (s.wp + grid / 2 - 1) / (grid / 2) : 0;
+  s.s1 = (s.w - s.wp + grid - 1) / grid;
+  s.u1 = p.pair ? p.npi * p.Hkv : 0;
+  s.base1 = p.pair ? 2 * (grid / 2 + s.u1) : 0;
+  return s;
+}
+
+// Each unit's first slot and number of partials (the slots of a pair's tile lie two apart, the second
+// tile's one on), for the join; by CTA 0 of the kernel that computes them.
 __device__ __forceinline__ void attn_write_units(const AttnParams& p, const int32_t* cum,
-                                                 int64_t share) {
+                                                 const AttnShares& s) {
   for (int u = threadIdx.x; u < p.items * p.Hkv; u += blockDim.x) {
     const int item = u / p.Hkv, head = u - item * p.Hkv;
-    const int nb = cum[item + 1] - cum[item];
+    const int cost = cum[item + 1] - cum[item];
     int2 v = make_int2(0, 0);
-    if (nb > 0) {
-      const int64_t start = static_cast<int64_t>(cum[item]) * p.Hkv + static_cast<int64_t>(head) * nb;
-      const int cta0 = static_cast<int>(start / share);
-      v = make_int2(cta0 + u, static_cast<int>((start + nb - 1) / share) - cta0 + 1);
+    if (cost > 0) {
+      const int64_t x = static_cast<int64_t>(cum[item]) * p.Hkv + static_cast<int64_t>(head) * cost;
+      const bool pair = u < s.u1;
+      const int64_t at = pair ? x : x - s.wp, share = pair ? s.sp : s.s1;
+      const int c0 = static_cast<int>((at + p.over) / share);
+      v.y = static_cast<int>((at + cost - 1) / share) - c0 + 1;
+      v.x = pair ? 2 * (c0 + u) : s.base1 + c0 + u - s.u1;
     }
     p.units[u] = v;
   }
 }
 
-// A CTA's piece of one unit.
+// A CTA's piece of one unit: its tile of rows (prefix tiles, then own tiles; -1: none, the other CTA
+// of the pair has the last tile), KV head, blocks and slot.
 struct AttnPiece {
-  int item, head, blk0, blk1, slot;
+  int tile, head, blk0, blk1, slot;
+  bool pair;
 };
 
-// The item that holds block x of one KV head's row of blocks scaled by Hkv (x < cum[items] Hkv).
-__device__ __forceinline__ int attn_item_of(const AttnParams& p, const int32_t* cum, int64_t x) {
-  int lo = 0, hi = p.items;  // cum[lo] Hkv <= x < cum[hi] Hkv
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (static_cast<int64_t>(cum[mid]) * p.Hkv <= x)
-      lo = mid;
-    else
-      hi = mid;
+// One piece after another of a CTA's shares.
+struct AttnWalk {
+  int64_t x, x1;
+  bool pair;  // the pairs' part is being walked
+  __device__ __forceinline__ void start(const AttnParams& p, const AttnShares& s) {
+    pair = p.pair;
+    if (pair) {
+      x = s.sp * (blockIdx.x / 2);
+      x1 = min(s.wp, x + s.sp);
+    } else {
+      single(s);
+    }
   }
-  return lo;
-}
+  __device__ __forceinline__ void single(const AttnShares& s) {
+    pair = false;
+    x = s.wp + s.s1 * blockIdx.x;
+    x1 = min(s.w, x + s.s1);
+  }
+  __device__ __forceinline__ bool next(const AttnParams& p, const int32_t* cum, const AttnShares& s,
+                                       AttnPiece& a) {
+    for (;;) {
+      if (x >= x1) {
+        if (!pair) return false;
+        single(s);
+        continue;
+      }
+      int lo = 0, hi = p.items;  // cum[lo] Hkv <= x < cum[hi] Hkv
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (static_cast<int64_t>(cum[mid]) * p.Hkv <= x)
+          lo = mid;
+        else
+          hi = mid;
+      }
+      const int cost = cum[lo + 1] - cum[lo];
+      const int64_t rel = x - static_cast<int64_t>(cum[lo]) * p.Hkv;
+      a.head = static_cast<int>(rel / cost);
+      const int v0 = static_cast<int>(rel - static_cast<int64_t>(a.head) * cost);
+      const int v1 = static_cast<int>(min(static_cast<int64_t>(cost), v0 + (x1 - x)));
+      x += v1 - v0;
+      a.blk0 = max(0, v0 - p.over);
+      a.blk1 = max(0, v1 - p.over);
+      if (a.blk0 == a.blk1) continue;
+      const int u = lo * p.Hkv + a.head;
+      a.pair = pair;
+      a.tile = lo - p.npi + p.npt;
+      a.slot = s.base1 + static_cast<int>(blockIdx.x) + u - s.u1;
+      if (lo < p.npi) a.tile = lo;
+      if (pair) {
+        const int rank = blockIdx.x & 1;
+        a.tile = 2 * lo + rank < p.npt ? 2 * lo + rank : -1;
+        a.slot = 2 * (static_cast<int>(blockIdx.x) / 2 + u) + rank;
+      }
+      return true;
+    }
+  }
+};
 
 // Row i of a tile: its request, row and query head in the group, and the positions it sees (0: it
 // does not run, or there is no such row).
 struct AttnRow {
   int b, r, g, lim;
 };
-__device__ __forceinline__ AttnRow attn_row(const AttnParams& p, int item, int i) {
+__device__ __forceinline__ AttnRow attn_row(const AttnParams& p, int tile, int i) {
   AttnRow a;
   a.b = a.r = a.g = a.lim = 0;
   const int per = p.R * p.G;
-  if (item < p.npt) {
-    const int s = item * p.tm + i;
+  if (tile < 0) return a;
+  if (tile < p.npt) {
+    const int s = tile * p.tm + i;
     if (s >= p.B * per) return a;
     a.b = s / per;
     const int x = s - a.b * per;
@@ -163,7 +240,7 @@ __device__ __forceinline__ AttnRow attn_row(const AttnParams& p, int item, int i
     a.g = x - a.r * p.G;
     if (a.r < attn_rows(p, a.b)) a.lim = attn_prefix(p, a.b);
   } else {
-    const int own = item - p.npt;
+    const int own = tile - p.npt;
     a.b = own / p.nown;
     const int x = (own - a.b * p.nown) * p.tm + i;
     if (x >= per) return a;
