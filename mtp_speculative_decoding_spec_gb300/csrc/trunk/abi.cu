@@ -166,7 +166,8 @@ spec_status spec_delta_rows(int32_t B, int32_t R, const spec_state_desc* st, int
 
 size_t spec_delta_prefill_workspace_bytes(int64_t rows, int32_t B, const spec_state_desc* st) {
   if (rows < 0 || B < 1 || rec_elems(st) == 0) return 0;
-  return 256;
+  return delta_chunk_sizes(st->rec_dk, st->rec_dv) ? delta_chunk_workspace(rows, B, st->rec_heads)
+                                                   : sizeof(WsHeader);
 }
 
 spec_status spec_delta_prefill(int32_t B, const int32_t* cu_rows, int64_t rows,
@@ -188,6 +189,12 @@ spec_status spec_delta_prefill(int32_t B, const int32_t* cu_rows, int64_t rows,
   p.cu_rows = cu_rows;
   p.rows = rows;
   p.init = rec_init;
+  p.hdr = static_cast<WsHeader*>(workspace);
+  if (delta_chunk_takes(p, d->dtype)) {
+    EncodeTiledFn encode = encode_tiled();
+    if (!encode) return SPEC_ERR_CUDA;
+    return delta_chunk_launch(p, workspace, encode, reinterpret_cast<cudaStream_t>(stream));
+  }
   const cudaError_t e = delta_scan_launch(p, d->dtype, a.sms, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }

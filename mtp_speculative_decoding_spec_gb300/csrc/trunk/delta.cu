@@ -90,6 +90,7 @@ __global__ void __launch_bounds__(kScanThreads)
     delta_scan_kernel(const __grid_constant__ DeltaParams p) {
   pdl_trigger();
   pdl_wait();
+  if (p.hdr && blockIdx.x == 0 && threadIdx.x == 0) p.hdr->error = 0;  // no wait here can set it
   const int lane = threadIdx.x & 31;
   const int tiles = (p.dv + 4 * LV - 1) / (4 * LV);
   const int64_t wid = static_cast<int64_t>(blockIdx.x) * (kScanThreads / 32) + (threadIdx.x >> 5);

@@ -26,9 +26,17 @@ struct DeltaParams {
   float* slots;
   const int32_t* live_slot;
   float *step_a, *step_b, *step_c;
+  WsHeader* hdr;            // prefill: the workspace's, its error word cleared by each call
 };
 
 cudaError_t delta_scan_launch(const DeltaParams& p, spec_dtype dtype, int sms, cudaStream_t stream);
+
+constexpr int kDeltaChunkRows = 16;
+bool delta_chunk_sizes(int dk, int dv);
+size_t delta_chunk_workspace(int64_t rows, int B, int H);
+bool delta_chunk_takes(const DeltaParams& p, spec_dtype dtype);
+spec_status delta_chunk_launch(const DeltaParams& p, void* workspace, EncodeTiledFn encode,
+                               cudaStream_t stream);
 
 // Attention of verify rows over a shared prefix and each request's own cache. The work is cut into
 // units: a tile of `tm` rows and a KV head over the positions of one region. Prefix tiles hold the

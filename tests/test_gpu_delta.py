@@ -231,6 +231,7 @@ def run_prefill(spec, x, lens, layers, layer, init, stream=None, ws=None, gap=0)
     spec.spec_delta_prefill(B, cu, rows, s.st, layer, x.desc(spec),
                             {"zero": None, "live": s.live, "other": start}[init], ws, stream)
     torch.cuda.synchronize()
+    assert int(ws[4:8].cpu().numpy().view(np.uint32)[0]) == 0
     return s, start
 
 
