@@ -51,7 +51,7 @@ __device__ __forceinline__ void ldm4t(uint32_t a, uint32_t* r) {
                : "memory");
 }
 __device__ __forceinline__ void mma(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
       "{%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -59,7 +59,7 @@ __device__ __forceinline__ void mma(float* d, const uint32_t* a, uint32_t b0, ui
 }
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {  // an 8 x 8 matrix of 16-bit values
   uint32_t y;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
 __device__ __forceinline__ uint32_t pack(float lo, float hi) {
@@ -262,18 +262,24 @@ __global__ void __launch_bounds__(kPrepThreads)
 }
 
 // ------------------------------------------------------------------------- the chain of chunks
-// Grid (rec_dv / 16, H, B), clusters of blocks of one head, which read the same K, Q, T and scores:
-// each loads a share of them and multicasts it to all. Four compute warps and a producer warp.
-constexpr int kChainThreads = 5 * 32;
-constexpr int kStages = 2;
+// Grid (rec_dv / 16, H, B), in clusters of blocks of one head, which read the same K, Q, T and scores:
+// each loads a share of them and multicasts it to all. Warps 0-3 carry the chain (k S, u, S), warps
+// 4-7 make the outputs beside it (q S, scores times u), warps 8 and 9 load for them.
+//   chain   k S -> r -> | u | S' -> |      | three barriers of the four warps a chunk
+//   output  q S    ...    scores u, store
+// A warp of the chain has two tiles of eight tokens (w and 7 - w: the same work under causality) and a
+// quarter of S's rows. What a phase multiplies by (K, T) is read into registers before the barrier
+// that its other operand waits for.
+constexpr int kChainThreads = 10 * 32;
+constexpr int kCStages = 3, kOStages = 2;
 constexpr int kVTile = kC * kCols * 2;
-constexpr int kStage = 2 * kTile + kRec + kVTile;  // K, Q, record, V
-constexpr int kPieces = 8;                         // two panels of K, of Q, four quarters of the record
+constexpr int kCStage = kTile + kTBytes + kVecBytes + kVTile;  // chain: K, T, vectors, V
+constexpr int kOStage = kTile + kABytes + kVecBytes;           // output: Q, scores, vectors
 constexpr int kSPlane = kCols * 256;               // S^T: two panels of 16 rows of 128 bytes
 constexpr int kUPlane = kCols * 128;               // 16 x 64
 constexpr int kWork = 3 * kSPlane + 8 * kUPlane;   // S, r, u scaled for the state (3 each), u (2)
-constexpr int kChainSmem = kStages * kStage + kWork + 256 + 1024;
-static_assert(kRec % 64 == 0 && kStage % 128 == 0, "copies of whole 16-byte units");
+constexpr int kChainSmem = kCStages * kCStage + kOStages * kOStage + kWork + 256 + 1024;
+static_assert(kCStage % 1024 == 0 && kOStage % 1024 == 0, "swizzled tiles start on 1,024 bytes");
 
 struct ChainMaps {
   CUtensorMap k, q, v;  // [rows][columns], boxes of 64 x 64 (swizzled) and 16 x 64
@@ -311,8 +317,26 @@ __device__ __forceinline__ void bulk_copy(void* dst, const void* src, uint32_t b
         "l"(src), "r"(bytes), "r"(bar)
         : "memory");
 }
+// Arrive on `bar` of every block of the cluster: lanes 0..cs-1 of a warp that is done with a stage.
+__device__ __forceinline__ void arrive_all(uint64_t* bar, int lane, int cs) {
+  __syncwarp();
+  if (lane < cs) {
+    uint32_t remote;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_u32(bar)), "r"(lane));
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(remote)
+                 : "memory");
+  }
+}
 
-__device__ __forceinline__ void bar_compute() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+// Barriers between the groups of warps. Both go through the same chunks whatever happens, so each
+// side's turn always comes.
+enum : int { kBarChain = 1, kBarState = 2, kBarQs = 3, kBarU = 4, kBarUsed = 5 };
+__device__ __forceinline__ void bar_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(int id, int threads) {
+  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
 
 __global__ void __launch_bounds__(kChainThreads, 1)
     delta_chain_kernel(const __grid_constant__ ChainMaps maps, const __grid_constant__ DeltaParams p,
@@ -320,21 +344,27 @@ __global__ void __launch_bounds__(kChainThreads, 1)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
-  // every swizzled tile starts at a multiple of 1,024 bytes: K and Q tiles and T and score planes do
-  // (kStage is padded below), the work planes are 128-byte rows whose count is a multiple of 8
-  uint8_t* work = smem + kStages * kStage;
-  uint64_t* full = reinterpret_cast<uint64_t*>(work + kWork);
-  uint64_t* empty = full + kStages;    // this block's warps are done with the stage
-  uint64_t* pempty = empty + kStages;  // all blocks of the cluster are
+  uint8_t* ostages = smem + kCStages * kCStage;
+  uint8_t* sps = ostages + kOStages * kOStage;  // parts of S
+  uint8_t* rps = sps + 3 * kSPlane;             // of r
+  uint8_t* ups = rps + 3 * kUPlane;             // of e^(G_last - G) u
+  uint8_t* ops = ups + 3 * kUPlane;             // of u
+  uint64_t* cfull = reinterpret_cast<uint64_t*>(sps + kWork);
+  uint64_t* cempty = cfull + kCStages;  // all blocks of the cluster are done with the stage
+  uint64_t* ofull = cempty + kCStages;
+  uint64_t* oempty = ofull + kOStages;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int h = blockIdx.y, b = blockIdx.z, kh = h / (p.H / p.Hk);
   const int col0 = blockIdx.x * kCols, rank = blockIdx.x % cs;
   pdl_trigger();
   if (tid == 0) {
-    for (int s = 0; s < kStages; ++s) {
-      mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 4);
-      mbar_init(&pempty[s], cs);
+    for (int s = 0; s < kCStages; ++s) {
+      mbar_init(&cfull[s], 1);
+      mbar_init(&cempty[s], 4 * cs);
+    }
+    for (int s = 0; s < kOStages; ++s) {
+      mbar_init(&ofull[s], 1);
+      mbar_init(&oempty[s], 4 * cs);
     }
     fence_mbar_init();
   }
@@ -345,63 +375,133 @@ __global__ void __launch_bounds__(kChainThreads, 1)
   const int n = (c1 - c0 + kC - 1) / kC;
   const int64_t elems = static_cast<int64_t>(p.layers) * p.H * p.dk * p.dv;
   const int64_t off = b * elems + (static_cast<int64_t>(p.layer) * p.H + h) * p.dk * p.dv + col0;
+  // fragment coordinates: lane (g, q); an A operand's row and 16-byte piece; B tiles of tokens tl (lanes
+  // 0-15) and tr
+  const int g = lane >> 2, q = lane & 3, w4 = warp & 3, tl = w4, tr = 7 - w4;
+  const int ar = lane & 15, ac = lane >> 4;
+  const int bt = (lane & 16 ? tr : tl) * 8 + (lane & 7), bc = (lane >> 3) & 1;
+  const uint32_t sp = smem_u32(sps), rp = smem_u32(rps), up = smem_u32(ups), op = smem_u32(ops);
+  bool ok = true;
+  auto wait = [&](uint64_t* bar, uint32_t parity) {  // gives up waiting for good, not the walk
+    if (ok && !mbar_wait_bounded(bar, parity)) {
+      atomicOr(&p.hdr->error, ERR_TC_WAIT);
+      ok = false;
+    }
+    ok = __all_sync(0xffffffffu, ok);
+  };
 
-  if (warp == 4) {
-    // ------------------------------------------------------------------ producer
+  if (warp >= 8) {
+    // ------------------------------------------------------------------ loads, for the chain and the outputs
+    const bool chain = warp == 8;
+    const int stages = chain ? kCStages : kOStages;
+    uint64_t* full = chain ? cfull : ofull;
+    uint64_t* empty = chain ? cempty : oempty;
     const uint8_t* base = rec + (static_cast<int64_t>(first_slot(c0, b)) * p.H + h) * kRec;
     const uint16_t mask = static_cast<uint16_t>((1u << cs) - 1);
-    bool ok = true;
     int c = 0;
     for (; c < n; ++c) {
-      const int s = c % kStages;
-      const uint32_t parity = ((c / kStages) & 1) ^ 1;
-      if (c >= kStages) {
-        ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(&empty[s], parity));
-        if (lane < cs) {
-          uint32_t remote;
-          asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
-                       : "=r"(remote)
-                       : "r"(smem_u32(&pempty[s])), "r"(lane));
-          asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(remote)
-                       : "memory");
-        }
-        ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(&pempty[s], parity));
-        if (!ok) break;
-      }
-      uint8_t* st = smem + s * kStage;
+      const int s = c % stages;
+      if (c >= stages) wait(&empty[s], ((c / stages) & 1) ^ 1);
+      if (!ok) break;
       if (lane == 0) {
         const int row = c0 + c * kC;
+        const uint8_t* r = base + static_cast<int64_t>(c) * p.H * kRec;
         const uint32_t bar = smem_u32(&full[s]);
-        mbar_arrive_expect_tx(&full[s], kStage);
-        tma_box(st + 2 * kTile + kRec, &maps.v, h * p.dv + col0, row, bar, 1, 0);
-        for (int i = rank; i < kPieces; i += cs) {
-          if (i < 4) {
-            tma_box(st + (i >> 1) * kTile + (i & 1) * kPlane, i < 2 ? &maps.k : &maps.q,
-                   kh * kDk + (i & 1) * 64, row, bar, cs, mask);
-          } else {
-            bulk_copy(st + 2 * kTile + (i - 4) * (kRec / 4),
-                      base + static_cast<int64_t>(c) * p.H * kRec + (i - 4) * (kRec / 4), kRec / 4, bar,
+        uint8_t* st = chain ? smem + s * kCStage : ostages + s * kOStage;
+        mbar_arrive_expect_tx(&full[s], chain ? kCStage : kOStage);
+        if (chain) tma_box(st + kTile + kTBytes + kVecBytes, &maps.v, h * p.dv + col0, row, bar, 1, 0);
+        // pieces: two panels of K or Q, the planes of T or of the scores, the vectors
+        const int planes = chain ? 3 : 2;
+        for (int i = rank; i < 3 + planes; i += cs) {
+          if (i < 2)
+            tma_box(st + i * kPlane, chain ? &maps.k : &maps.q, kh * kDk + i * 64, row, bar, cs, mask);
+          else if (i < 2 + planes)
+            bulk_copy(st + kTile + (i - 2) * kPlane, r + (chain ? 0 : kTBytes) + (i - 2) * kPlane, kPlane, bar,
                       cs, mask);
-          }
+          else
+            bulk_copy(st + kTile + planes * kPlane, r + kTBytes + kABytes, kVecBytes, bar, cs, mask);
         }
       }
     }
-    if (!ok && lane == 0) atomicOr(&p.hdr->error, ERR_TC_WAIT);
-    for (int j = max(0, c - kStages); j < c; ++j)  // nothing is left in flight
-      mbar_wait_bounded(&full[j % kStages], (j / kStages) & 1);
+    ok = true;
+    for (int j = max(0, c - stages); j < c; ++j) {  // nothing is left in flight
+      wait(&full[j % stages], (j / stages) & 1);
+      wait(&empty[j % stages], (j / stages) & 1);
+    }
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------------ outputs
+    for (int c = 0; c < n; ++c) {
+      const int s = c % kOStages;
+      wait(&ofull[s], (c / kOStages) & 1);
+      const uint8_t* st = ostages + s * kOStage;
+      const uint32_t q32 = smem_u32(st), a32 = q32 + kTile;
+      const float* eg = reinterpret_cast<const float*>(st + kTile + kABytes);
+      const int len = min(kC, c1 - c0 - c * kC);
+      uint32_t qb[8][4];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) ldm4(q32 + (i >> 2) * kPlane + swz(bt, (i & 3) * 2 + bc), qb[i]);
+      bar_sync(kBarState, 256);
+      float x[2][2][4] = {};  // [part][tile]
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        uint32_t a[2][4];
+        const uint32_t sa = sp + (i >> 2) * (kSPlane / 2) + swz(ar, (i & 3) * 2 + ac);
+        ldm4(sa, a[0]);
+        ldm4(sa + kSPlane, a[1]);
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int t = 0; t < 2; ++t) mma(x[j][t], a[j], qb[i][2 * t], qb[i][2 * t + 1]);
+      }
+      bar_arrive(kBarQs, 256);
+      uint32_t ab[4][2][4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i <= tr / 2) {
+          ldm4(a32 + swz(bt, 2 * i + bc), ab[i][0]);
+          ldm4(a32 + kPlane + swz(bt, 2 * i + bc), ab[i][1]);
+        }
+      bar_sync(kBarU, 256);
+      float o[3][2][4] = {};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (i > tr / 2) break;
+        uint32_t u[2][4];
+        ldm4(op + swz(ar, 2 * i + ac), u[0]);
+        ldm4(op + kUPlane + swz(ar, 2 * i + ac), u[1]);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (t == 0 && i > tl / 2) continue;
+          mma(o[0][t], u[0], ab[i][0][2 * t], ab[i][0][2 * t + 1]);
+          mma(o[1][t], u[1], ab[i][0][2 * t], ab[i][0][2 * t + 1]);
+          mma(o[2][t], u[0], ab[i][1][2 * t], ab[i][1][2 * t + 1]);
+        }
+      }
+      bar_arrive(kBarUsed, 256);
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const int tile = t ? tr : tl, tok = tile * 8 + 2 * q;
+        const float e[2] = {p.scale * eg[tok], p.scale * eg[tok + 1]};
+        float y[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          y[k] = fmaf(e[k & 1], x[0][t][k] + x[1][t][k], o[0][t][k] + (o[1][t][k] + o[2][t][k]));
+        const uint32_t w0 = transpose8(pack(y[0], y[1])), w1 = transpose8(pack(y[2], y[3]));
+        if (tile * 8 + g < len) {
+          __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) +
+                               (static_cast<int64_t>(c0) + c * kC + tile * 8 + g) * p.os +
+                               static_cast<int64_t>(h) * p.dv + col0 + 2 * q;
+          *reinterpret_cast<uint32_t*>(dst) = w0;
+          *reinterpret_cast<uint32_t*>(dst + 8) = w1;
+        }
+      }
+      arrive_all(&oempty[s], lane, cs);
+    }
+    if (n > 0) bar_sync(kBarState, 256);  // the chain's last state, which nothing reads
   } else {
-    // ------------------------------------------------------------------ compute
-    // S^T: this warp's rows of S are dims 32 w..32 w + 31; in registers, lane (g, q) of the fragment
-    // has columns col0 + g and + 8 of dims 32 w + 8 t + 2 q and + 1
-    const int g = lane >> 2, q = lane & 3;
-    const uint32_t sp = smem_u32(work);                      // parts of S
-    const uint32_t rp = sp + 3 * kSPlane;                    // of r
-    const uint32_t up = rp + 3 * kUPlane;                    // of e^(G_last - G) u
-    const uint32_t op = up + 3 * kUPlane;                    // of u
-    uint8_t* sps = work;
-    uint8_t* rps = sps + 3 * kSPlane;
-    uint8_t* ups = rps + 3 * kUPlane;
-    uint8_t* ops = ups + 3 * kUPlane;
+    // ------------------------------------------------------------------ chain
+    // S^T: this warp's rows of S are dims 32 w..32 w + 31; lane (g, q) has columns col0 + g and + 8 of dims
+    // 32 w + 8 t + 2 q and + 1
     float S[4][4];
 #pragma unroll
     for (int t = 0; t < 4; ++t)
@@ -423,25 +523,18 @@ __global__ void __launch_bounds__(kChainThreads, 1)
           for (int s = 0; s < 3; ++s) *reinterpret_cast<uint32_t*>(sps + s * kSPlane + at) = w[s];
         }
     };
-    put_state();
-    bar_compute();
-    // token tiles of 8: this warp's are tl and tr; causality gives every warp the same work
-    const int tl = warp, tr = 7 - warp;
-    // lane's row and 16-byte piece of an A operand, and of B tiles of tokens tl (lanes 0-15) and tr
-    const int ar = lane & 15, ac = lane >> 4;
-    const int bt = (lane & 16 ? tr : tl) * 8 + (lane & 7), bc = (lane >> 3) & 1;
-    bool ok = true;
+    if (n > 0) {
+      put_state();
+      bar_arrive(kBarState, 256);
+    }
     for (int c = 0; c < n; ++c) {
-      const int s = c % kStages;
-      if (ok && !mbar_wait_bounded(&full[s], (c / kStages) & 1)) {
-        atomicOr(&p.hdr->error, ERR_TC_WAIT);
-        ok = false;
-      }
-      uint8_t* st = smem + s * kStage;
-      const uint32_t k32 = smem_u32(st), q32 = k32 + kTile, t32 = k32 + 2 * kTile, a32 = t32 + kTBytes;
-      const float* eg = reinterpret_cast<const float*>(st + 2 * kTile + kTBytes + kABytes);
+      const int s = c % kCStages;
+      wait(&cfull[s], (c / kCStages) & 1);
+      uint8_t* st = smem + s * kCStage;
+      const uint32_t k32 = smem_u32(st), t32 = k32 + kTile;
+      const float* eg = reinterpret_cast<const float*>(st + kTile + kTBytes);
       const float* el = eg + kC;
-      const uint8_t* sv = st + 2 * kTile + kRec;
+      const uint8_t* sv = st + kTile + kTBytes + kVecBytes;
       const int len = min(kC, c1 - c0 - c * kC);
       if (len < kC) {
         // rows past the request's end are another's: what they hold must not reach S even times 0
@@ -449,155 +542,144 @@ __global__ void __launch_bounds__(kChainThreads, 1)
           const int r = len + (i >> 4), pc = i & 15;
           *reinterpret_cast<uint4*>(st + (pc >> 3) * kPlane + swz(r, pc & 7)) = make_uint4(0u, 0u, 0u, 0u);
         }
-        bar_compute();
+        bar_sync(kBarChain, 128);
       }
-      // k S and q S of the warp's tokens
-      float xk[2][4] = {}, xq[2][4] = {};
+      uint32_t kb[8][4];
 #pragma unroll
-      for (int i = 0; i < kDk / 16; ++i) {
-        const int pan = i >> 2, pc = (i & 3) * 2;
-        uint32_t a0[4], a1[4], a2[4], kb[4], qb[4];
-        const uint32_t sa = sp + pan * (kSPlane / 2) + swz(ar, pc + ac);
-        ldm4(sa, a0);
-        ldm4(sa + kSPlane, a1);
-        ldm4(sa + 2 * kSPlane, a2);
-        const int bo = pan * kPlane + swz(bt, pc + bc);
-        ldm4(k32 + bo, kb);
-        ldm4(q32 + bo, qb);
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          mma(xk[t], a2, kb[2 * t], kb[2 * t + 1]);
-          mma(xk[t], a1, kb[2 * t], kb[2 * t + 1]);
-          mma(xk[t], a0, kb[2 * t], kb[2 * t + 1]);
-          mma(xq[t], a1, qb[2 * t], qb[2 * t + 1]);
-          mma(xq[t], a0, qb[2 * t], qb[2 * t + 1]);
-        }
-      }
-      // r = v - e^G (k S)
+      for (int i = 0; i < 8; ++i) ldm4(k32 + (i >> 2) * kPlane + swz(bt, (i & 3) * 2 + bc), kb[i]);
+      float v[2][4], ge[2][2], le[2][2];
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
-        const int tile = t ? tr : tl;
+        const int tile = t ? tr : tl, tok = tile * 8 + 2 * q;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {  // columns g, g + 8
-          const uint32_t v = transpose8(
+          const uint32_t x = transpose8(
               *reinterpret_cast<const uint32_t*>(sv + (tile * 8 + g) * (kCols * 2) + 16 * half + 4 * q));
-          const int tok = tile * 8 + 2 * q;
-          const float r0 = tok < len ? fmaf(-eg[tok], xk[t][2 * half], lo_of(v)) : 0.f;
-          const float r1 = tok + 1 < len ? fmaf(-eg[tok + 1], xk[t][2 * half + 1], hi_of(v)) : 0.f;
-          uint32_t w[3];
-          split<3>(r0, r1, w);
-          const int at = swz(g + 8 * half, tile) + 4 * q;
-#pragma unroll
-          for (int i = 0; i < 3; ++i) *reinterpret_cast<uint32_t*>(rps + i * kUPlane + at) = w[i];
+          v[t][2 * half] = lo_of(x);
+          v[t][2 * half + 1] = hi_of(x);
         }
+        ge[t][0] = -eg[tok], ge[t][1] = -eg[tok + 1];
+        le[t][0] = el[tok], le[t][1] = el[tok + 1];
       }
-      bar_compute();
-      // u = T r
-      float u[2][4] = {};
+      bar_sync(kBarChain, 128);  // the parts of S are there
+      // k S of the warp's tokens, the parts of S in sums of their own
+      float x[3][2][4] = {};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (i > tr / 2) break;  // tokens after the tile's
-        uint32_t r[3][4], tb[3][4];
+      for (int i = 0; i < 8; ++i) {
+        uint32_t a[3][4];
+        const uint32_t sa = sp + (i >> 2) * (kSPlane / 2) + swz(ar, (i & 3) * 2 + ac);
 #pragma unroll
-        for (int j = 0; j < 3; ++j) {
-          ldm4(rp + j * kUPlane + swz(ar, 2 * i + ac), r[j]);
-          ldm4(t32 + j * kPlane + swz(bt, 2 * i + bc), tb[j]);
-        }
+        for (int j = 0; j < 3; ++j) ldm4(sa + j * kSPlane, a[j]);
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          if (t == 0 && i > tl / 2) continue;
-          mma(u[t], r[0], tb[2][2 * t], tb[2][2 * t + 1]);
-          mma(u[t], r[2], tb[0][2 * t], tb[0][2 * t + 1]);
-          mma(u[t], r[1], tb[1][2 * t], tb[1][2 * t + 1]);
-          mma(u[t], r[0], tb[1][2 * t], tb[1][2 * t + 1]);
-          mma(u[t], r[1], tb[0][2 * t], tb[0][2 * t + 1]);
-          mma(u[t], r[0], tb[0][2 * t], tb[0][2 * t + 1]);
-        }
+        for (int j = 0; j < 3; ++j)
+#pragma unroll
+          for (int t = 0; t < 2; ++t) mma(x[j][t], a[j], kb[i][2 * t], kb[i][2 * t + 1]);
       }
+      uint32_t tb[4][3][4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i <= tr / 2) {
+#pragma unroll
+          for (int j = 0; j < 3; ++j) ldm4(t32 + j * kPlane + swz(bt, 2 * i + bc), tb[i][j]);
+        }
+      // r = v - e^G (k S)
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         const int tile = t ? tr : tl, tok = tile * 8 + 2 * q;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
+          float r[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int k = 2 * half + e;
+            r[e] = tok + e < len ? fmaf(ge[t][e], x[0][t][k] + (x[1][t][k] + x[2][t][k]), v[t][k]) : 0.f;
+          }
+          uint32_t w[3];
+          split<3>(r[0], r[1], w);
           const int at = swz(g + 8 * half, tile) + 4 * q;
-          uint32_t w[3], x[2];
-          split<3>(el[tok] * u[t][2 * half], el[tok + 1] * u[t][2 * half + 1], w);
-          split<2>(u[t][2 * half], u[t][2 * half + 1], x);
+#pragma unroll
+          for (int i = 0; i < 3; ++i) *reinterpret_cast<uint32_t*>(rps + i * kUPlane + at) = w[i];
+        }
+      }
+      bar_sync(kBarChain, 128);
+      // u = T r, the terms by size in sums of their own
+      float u[3][2][4] = {};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (i > tr / 2) break;  // tokens after the tile's
+        uint32_t r[3][4];
+#pragma unroll
+        for (int j = 0; j < 3; ++j) ldm4(rp + j * kUPlane + swz(ar, 2 * i + ac), r[j]);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {  // T_k r_0, then what is 2^-8 and 2^-16 of it
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            if (t == 0 && i > tl / 2) continue;
+            const uint32_t(&b0)[4] = tb[i][0], (&b1)[4] = tb[i][1], (&b2)[4] = tb[i][2];
+            if (k == 0) {
+              mma(u[0][t], r[0], b0[2 * t], b0[2 * t + 1]);
+              mma(u[1][t], r[1], b0[2 * t], b0[2 * t + 1]);
+              mma(u[2][t], r[2], b0[2 * t], b0[2 * t + 1]);
+            } else {
+              mma(u[1][t], r[0], b1[2 * t], b1[2 * t + 1]);
+              mma(u[2][t], r[1], b1[2 * t], b1[2 * t + 1]);
+              mma(u[2][t], r[0], b2[2 * t], b2[2 * t + 1]);
+            }
+          }
+        }
+      }
+      // for S': K as it lies (tokens down, dims across), transposed on the way: this warp's dims
+      uint32_t kt[4][8];
+      {
+        const int kr = (lane & 7) + ((lane >> 3) & 1) * 8, kc = 4 * (warp & 1) + (lane >> 4);
+        const uint32_t k0 = k32 + (warp >> 1) * kPlane;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          ldm4t(k0 + swz(16 * i + kr, kc), kt[i]);
+          ldm4t(k0 + swz(16 * i + kr, kc + 2), kt[i] + 4);
+        }
+      }
+      const float all = eg[2 * kC];
+      arrive_all(&cempty[s], lane, cs);  // everything of the stage is in registers
+      if (c > 0) bar_sync(kBarUsed, 256);
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const int tile = t ? tr : tl;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const int at = swz(g + 8 * half, tile) + 4 * q, k = 2 * half;
+          const float y0 = u[0][t][k] + (u[1][t][k] + u[2][t][k]);
+          const float y1 = u[0][t][k + 1] + (u[1][t][k + 1] + u[2][t][k + 1]);
+          uint32_t w[3], z[2];
+          split<3>(le[t][0] * y0, le[t][1] * y1, w);
+          split<2>(y0, y1, z);
 #pragma unroll
           for (int i = 0; i < 3; ++i) *reinterpret_cast<uint32_t*>(ups + i * kUPlane + at) = w[i];
 #pragma unroll
-          for (int i = 0; i < 2; ++i) *reinterpret_cast<uint32_t*>(ops + i * kUPlane + at) = x[i];
+          for (int i = 0; i < 2; ++i) *reinterpret_cast<uint32_t*>(ops + i * kUPlane + at) = z[i];
         }
       }
-      bar_compute();
+      bar_arrive(kBarU, 256);
+      bar_sync(kBarChain, 128);
       // S <- e^G_last S + sum over tokens; the sum in accumulators of its own, joined by one rounding
-      {
-        float d[4][4] = {};
-        // B: K as it lies (tokens down, dims across), transposed on the way: dims 32 w.., 16 tokens
-        const int kr = (lane & 7) + ((lane >> 3) & 1) * 8, kc = 4 * (warp & 1) + (lane >> 4);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint32_t a[3][4], k0[4], k1[4];
-#pragma unroll
-          for (int j = 0; j < 3; ++j) ldm4(up + j * kUPlane + swz(ar, 2 * i + ac), a[j]);
-          const uint32_t kb = k32 + (warp >> 1) * kPlane;
-          ldm4t(kb + swz(16 * i + kr, kc), k0);
-          ldm4t(kb + swz(16 * i + kr, kc + 2), k1);
-#pragma unroll
-          for (int j = 2; j >= 0; --j) {
-            mma(d[0], a[j], k0[0], k0[1]);
-            mma(d[1], a[j], k0[2], k0[3]);
-            mma(d[2], a[j], k1[0], k1[1]);
-            mma(d[3], a[j], k1[2], k1[3]);
-          }
-        }
-        const float all = eg[2 * kC];
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) S[t][e] = fmaf(all, S[t][e], d[t][e]);
-      }
-      put_state();
-      bar_compute();
-      // o = scale e^G (q S) + scores u
-      float o[2][4] = {};
+      float d[4][4] = {};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        if (i > tr / 2) break;
-        uint32_t x[2][4], ab[2][4];
+        uint32_t a[3][4];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          ldm4(op + j * kUPlane + swz(ar, 2 * i + ac), x[j]);
-          ldm4(a32 + j * kPlane + swz(bt, 2 * i + bc), ab[j]);
-        }
+        for (int j = 0; j < 3; ++j) ldm4(up + j * kUPlane + swz(ar, 2 * i + ac), a[j]);
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          if (t == 0 && i > tl / 2) continue;
-          mma(o[t], x[1], ab[0][2 * t], ab[0][2 * t + 1]);
-          mma(o[t], x[0], ab[1][2 * t], ab[1][2 * t + 1]);
-          mma(o[t], x[0], ab[0][2 * t], ab[0][2 * t + 1]);
-        }
+        for (int j = 2; j >= 0; --j)
+#pragma unroll
+          for (int t = 0; t < 4; ++t) mma(d[t], a[j], kt[i][2 * t], kt[i][2 * t + 1]);
       }
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        const int tile = t ? tr : tl, tok = tile * 8 + 2 * q;
-        const float e0 = p.scale * eg[tok], e1 = p.scale * eg[tok + 1];
-        uint32_t w[2];
+      for (int t = 0; t < 4; ++t)
 #pragma unroll
-        for (int half = 0; half < 2; ++half)
-          w[half] = transpose8(pack(fmaf(e0, xq[t][2 * half], o[t][2 * half]),
-                                    fmaf(e1, xq[t][2 * half + 1], o[t][2 * half + 1])));
-        if (tile * 8 + g < len) {
-          __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) +
-                               (static_cast<int64_t>(c0) + c * kC + tile * 8 + g) * p.os +
-                               static_cast<int64_t>(h) * p.dv + col0 + 2 * q;
-          *reinterpret_cast<uint32_t*>(dst) = w[0];
-          *reinterpret_cast<uint32_t*>(dst + 8) = w[1];
-        }
-      }
-      if (len < kC) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&empty[s]);
+        for (int e = 0; e < 4; ++e) S[t][e] = fmaf(all, S[t][e], d[t][e]);
+      bar_sync(kBarQs, 256);  // q S has been taken of the state before
+      put_state();
+      bar_arrive(kBarState, 256);
     }
     float* live = p.live + off;
 #pragma unroll
@@ -607,10 +689,52 @@ __global__ void __launch_bounds__(kChainThreads, 1)
         const int dim = 32 * warp + 8 * t + 2 * q + (e & 1), col = g + 8 * (e >> 1);
         live[static_cast<int64_t>(dim) * p.dv + col] = S[t][e];
       }
+    if (n > 0) bar_sync(kBarUsed, 256);  // the outputs' last turn
   }
   // the cluster's copies and arrivals come to this block's memory until all are done
   __syncwarp();
   asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+
+// How many clusters of cs blocks fit on the device at once; asked once per device and size.
+int clusters_at_once(int cs, cudaLaunchConfig_t cfg) {
+  static std::atomic<int> known[64][4];  // zero: not asked yet
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 1;
+  std::atomic<int>& slot = known[dev][cs == 8 ? 3 : cs == 4 ? 2 : cs == 2 ? 1 : 0];
+  int fit = slot.load(std::memory_order_relaxed);
+  if (fit != 0) return fit;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cs;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaOccupancyMaxActiveClusters(&fit, delta_chain_kernel, &cfg) != cudaSuccess || fit < 1) {
+    cudaGetLastError();
+    fit = 1;
+  }
+  slot.store(fit, std::memory_order_relaxed);
+  return fit;
+}
+
+// Blocks of a cluster: the most (up to 8, dividing the head's blocks) with which the grid still runs in
+// as few turns as it can. A larger cluster reads K, Q, T and the scores fewer times; how many of a size
+// fit at once depends on the device's floor plan (16 heads of 8 blocks ran in two turns as clusters of
+// eight where fewer than 16 of those fitted: 1,122 us against ~560 for one turn).
+int cluster_size(int slices, int64_t heads, const cudaLaunchConfig_t& cfg) {
+  int best = 1;
+  int64_t turns = -1;
+  for (int cs = 8; cs >= 1; cs /= 2) {
+    if (slices % cs != 0) continue;
+    const int fit = clusters_at_once(cs, cfg);
+    const int64_t t = (slices / cs * heads + fit - 1) / fit;
+    if (turns < 0 || t < turns) {
+      turns = t;
+      best = cs;
+    }
+  }
+  return best;
 }
 
 }  // namespace
@@ -656,13 +780,12 @@ spec_status delta_chunk_launch(const DeltaParams& p, void* workspace, EncodeTile
       !map(&m.v, p.v, static_cast<int64_t>(p.H) * p.dv, p.vs, kCols, CU_TENSOR_MAP_SWIZZLE_NONE))
     return SPEC_ERR_CUDA;
   const int slices = p.dv / kCols;
-  int cs = 8;
-  while (slices % cs != 0) cs /= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(slices, p.H, p.B);
   cfg.blockDim = dim3(kChainThreads);
   cfg.dynamicSmemBytes = kChainSmem;
   cfg.stream = stream;
+  const int cs = cluster_size(slices, static_cast<int64_t>(p.H) * p.B, cfg);
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
