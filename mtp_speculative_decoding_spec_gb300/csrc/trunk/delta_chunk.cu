@@ -51,8 +51,7 @@ __device__ __forceinline__ void ldm4t(uint32_t a, uint32_t* r) {
                : "memory");
 }
 __device__ __forceinline__ void mma(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
-  asm(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
       "{%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -270,7 +269,10 @@ __global__ void __launch_bounds__(kPrepThreads)
 // A warp of the chain has two tiles of eight tokens (w and 7 - w: the same work under causality) and a
 // quarter of S's rows. What a phase multiplies by (K, T) is read into registers before the barrier
 // that its other operand waits for.
-constexpr int kChainThreads = 10 * 32;
+constexpr int kChainThreads = 12 * 32;  // three groups of four warps; two of the last do nothing
+// Registers a thread: launched with 168 (64,512 in all), then shared out again by group. The chain takes
+// what the loads give: 4 x 32 x (224 + 144 + 64) = 55,296.
+constexpr int kChainRegs = 224, kOutRegs = 144, kLoadRegs = 64;
 constexpr int kCStages = 3, kOStages = 2;
 constexpr int kVTile = kC * kCols * 2;
 constexpr int kCStage = kTile + kTBytes + kVecBytes + kVTile;  // chain: K, T, vectors, V
@@ -317,13 +319,15 @@ __device__ __forceinline__ void bulk_copy(void* dst, const void* src, uint32_t b
         "l"(src), "r"(bytes), "r"(bar)
         : "memory");
 }
-// Arrive on `bar` of every block of the cluster: lanes 0..cs-1 of a warp that is done with a stage.
+// Arrive on `bar` of every block of the cluster: lanes 0..cs-1 of a warp that is done with a stage. Nothing
+// is published but that the stage has been read, so no fence of the cluster's scope (measured at about
+// 1,100 cycles a time) goes with it.
 __device__ __forceinline__ void arrive_all(uint64_t* bar, int lane, int cs) {
   __syncwarp();
   if (lane < cs) {
     uint32_t remote;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_u32(bar)), "r"(lane));
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(remote)
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(remote)
                  : "memory");
   }
 }
@@ -391,6 +395,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
   };
 
   if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLoadRegs));
     // ------------------------------------------------------------------ loads, for the chain and the outputs
     const bool chain = warp == 8;
     const int stages = chain ? kCStages : kOStages;
@@ -399,7 +404,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
     const uint8_t* base = rec + (static_cast<int64_t>(first_slot(c0, b)) * p.H + h) * kRec;
     const uint16_t mask = static_cast<uint16_t>((1u << cs) - 1);
     int c = 0;
-    for (; c < n; ++c) {
+    for (; c < n && warp < 10; ++c) {
       const int s = c % stages;
       if (c >= stages) wait(&empty[s], ((c / stages) & 1) ^ 1);
       if (!ok) break;
@@ -429,6 +434,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       wait(&empty[j % stages], (j / stages) & 1);
     }
   } else if (warp >= 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOutRegs));
     // ------------------------------------------------------------------ outputs
     for (int c = 0; c < n; ++c) {
       const int s = c % kOStages;
@@ -497,8 +503,8 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       }
       arrive_all(&oempty[s], lane, cs);
     }
-    if (n > 0) bar_sync(kBarState, 256);  // the chain's last state, which nothing reads
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kChainRegs));
     // ------------------------------------------------------------------ chain
     // S^T: this warp's rows of S are dims 32 w..32 w + 31; lane (g, q) has columns col0 + g and + 8 of dims
     // 32 w + 8 t + 2 q and + 1
@@ -523,19 +529,16 @@ __global__ void __launch_bounds__(kChainThreads, 1)
           for (int s = 0; s < 3; ++s) *reinterpret_cast<uint32_t*>(sps + s * kSPlane + at) = w[s];
         }
     };
-    if (n > 0) {
-      put_state();
-      bar_arrive(kBarState, 256);
-    }
-    for (int c = 0; c < n; ++c) {
-      const int s = c % kCStages;
-      wait(&cfull[s], (c / kCStages) & 1);
-      uint8_t* st = smem + s * kCStage;
-      const uint32_t k32 = smem_u32(st), t32 = k32 + kTile;
+    // What a chunk's first phase takes from its stage, read while the chunk before ends
+    uint32_t kb[8][4];
+    float v[2][4], ge[2][2], le[2][2];
+    int len = 0;
+    auto open_stage = [&](int c) {
+      wait(&cfull[c % kCStages], (c / kCStages) & 1);
+      uint8_t* st = smem + (c % kCStages) * kCStage;
       const float* eg = reinterpret_cast<const float*>(st + kTile + kTBytes);
-      const float* el = eg + kC;
       const uint8_t* sv = st + kTile + kTBytes + kVecBytes;
-      const int len = min(kC, c1 - c0 - c * kC);
+      len = min(kC, c1 - c0 - c * kC);
       if (len < kC) {
         // rows past the request's end are another's: what they hold must not reach S even times 0
         for (int i = tid; i < (kC - len) * 16; i += 128) {
@@ -544,10 +547,9 @@ __global__ void __launch_bounds__(kChainThreads, 1)
         }
         bar_sync(kBarChain, 128);
       }
-      uint32_t kb[8][4];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) ldm4(k32 + (i >> 2) * kPlane + swz(bt, (i & 3) * 2 + bc), kb[i]);
-      float v[2][4], ge[2][2], le[2][2];
+      for (int i = 0; i < 8; ++i)
+        ldm4(smem_u32(st) + (i >> 2) * kPlane + swz(bt, (i & 3) * 2 + bc), kb[i]);
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         const int tile = t ? tr : tl, tok = tile * 8 + 2 * q;
@@ -559,29 +561,47 @@ __global__ void __launch_bounds__(kChainThreads, 1)
           v[t][2 * half + 1] = hi_of(x);
         }
         ge[t][0] = -eg[tok], ge[t][1] = -eg[tok + 1];
-        le[t][0] = el[tok], le[t][1] = el[tok + 1];
+        le[t][0] = eg[kC + tok], le[t][1] = eg[kC + tok + 1];
       }
+    };
+    if (n > 0) {
+      open_stage(0);
+      put_state();
+    }
+    for (int c = 0; c < n; ++c) {
+      const int s = c % kCStages;
+      uint8_t* st = smem + s * kCStage;
+      const uint32_t k32 = smem_u32(st), t32 = k32 + kTile;
+      const float all = reinterpret_cast<const float*>(st + kTile + kTBytes)[2 * kC];
       bar_sync(kBarChain, 128);  // the parts of S are there
       // k S of the warp's tokens, the parts of S in sums of their own
       float x[3][2][4] = {};
+      {
+        uint32_t a[2][3][4];
+        auto load = [&](int i) {
+          const uint32_t sa = sp + (i >> 2) * (kSPlane / 2) + swz(ar, (i & 3) * 2 + ac);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        uint32_t a[3][4];
-        const uint32_t sa = sp + (i >> 2) * (kSPlane / 2) + swz(ar, (i & 3) * 2 + ac);
+          for (int j = 0; j < 3; ++j) ldm4(sa + j * kSPlane, a[i & 1][j]);
+        };
+        load(0);
 #pragma unroll
-        for (int j = 0; j < 3; ++j) ldm4(sa + j * kSPlane, a[j]);
+        for (int i = 0; i < 8; ++i) {
+          if (i + 1 < 8) load(i + 1);
 #pragma unroll
-        for (int j = 0; j < 3; ++j)
+          for (int j = 0; j < 3; ++j)
 #pragma unroll
-          for (int t = 0; t < 2; ++t) mma(x[j][t], a[j], kb[i][2 * t], kb[i][2 * t + 1]);
-      }
-      uint32_t tb[4][3][4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (i <= tr / 2) {
-#pragma unroll
-          for (int j = 0; j < 3; ++j) ldm4(t32 + j * kPlane + swz(bt, 2 * i + bc), tb[i][j]);
+            for (int t = 0; t < 2; ++t) mma(x[j][t], a[i & 1][j], kb[i][2 * t], kb[i][2 * t + 1]);
         }
+      }
+      bar_arrive(kBarState, 256);  // the outputs' turn at S, when the chain is past its own
+      uint32_t tb[4][3][4];  // the first three here, the last one beside the products of the others
+      auto load_t = [&](int i) {
+#pragma unroll
+        for (int j = 0; j < 3; ++j) ldm4(t32 + j * kPlane + swz(bt, 2 * i + bc), tb[i][j]);
+      };
+#pragma unroll
+      for (int i = 0; i < 3; ++i)
+        if (i <= tr / 2) load_t(i);
       // r = v - e^G (k S)
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
@@ -604,12 +624,18 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       bar_sync(kBarChain, 128);
       // u = T r, the terms by size in sums of their own
       float u[3][2][4] = {};
+      uint32_t ra[2][3][4];
+      auto load_r = [&](int i) {
+#pragma unroll
+        for (int j = 0; j < 3; ++j) ldm4(rp + j * kUPlane + swz(ar, 2 * i + ac), ra[i & 1][j]);
+      };
+      load_r(0);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         if (i > tr / 2) break;  // tokens after the tile's
-        uint32_t r[3][4];
-#pragma unroll
-        for (int j = 0; j < 3; ++j) ldm4(rp + j * kUPlane + swz(ar, 2 * i + ac), r[j]);
+        if (i + 1 < 4 && i + 1 <= tr / 2) load_r(i + 1);
+        if (i == 1 && tr / 2 == 3) load_t(3);
+        const uint32_t(&r)[3][4] = ra[i & 1];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {  // T_k r_0, then what is 2^-8 and 2^-16 of it
 #pragma unroll
@@ -639,7 +665,6 @@ __global__ void __launch_bounds__(kChainThreads, 1)
           ldm4t(k0 + swz(16 * i + kr, kc + 2), kt[i] + 4);
         }
       }
-      const float all = eg[2 * kC];
       arrive_all(&cempty[s], lane, cs);  // everything of the stage is in registers
       if (c > 0) bar_sync(kBarUsed, 256);
 #pragma unroll
@@ -663,23 +688,29 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       bar_sync(kBarChain, 128);
       // S <- e^G_last S + sum over tokens; the sum in accumulators of its own, joined by one rounding
       float d[4][4] = {};
+      {
+        uint32_t a[2][3][4];
+        auto load_u = [&](int i) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint32_t a[3][4];
+          for (int j = 0; j < 3; ++j) ldm4(up + j * kUPlane + swz(ar, 2 * i + ac), a[i & 1][j]);
+        };
+        load_u(0);
 #pragma unroll
-        for (int j = 0; j < 3; ++j) ldm4(up + j * kUPlane + swz(ar, 2 * i + ac), a[j]);
+        for (int i = 0; i < 4; ++i) {
+          if (i + 1 < 4) load_u(i + 1);
 #pragma unroll
-        for (int j = 2; j >= 0; --j)
+          for (int j = 2; j >= 0; --j)
 #pragma unroll
-          for (int t = 0; t < 4; ++t) mma(d[t], a[j], kt[i][2 * t], kt[i][2 * t + 1]);
+            for (int t = 0; t < 4; ++t) mma(d[t], a[i & 1][j], kt[i][2 * t], kt[i][2 * t + 1]);
+        }
       }
+      if (c + 1 < n) open_stage(c + 1);
 #pragma unroll
       for (int t = 0; t < 4; ++t)
 #pragma unroll
         for (int e = 0; e < 4; ++e) S[t][e] = fmaf(all, S[t][e], d[t][e]);
       bar_sync(kBarQs, 256);  // q S has been taken of the state before
-      put_state();
-      bar_arrive(kBarState, 256);
+      if (c + 1 < n) put_state();
     }
     float* live = p.live + off;
 #pragma unroll
