@@ -92,12 +92,64 @@ __device__ __forceinline__ int cu_at(const DeltaParams& p, int b) {
 __device__ __forceinline__ int first_slot(int cu, int b) { return cu / kC + b; }
 
 // ------------------------------------------------------------------------- what needs no state
-// One block per (slot, value head), 128 threads.
+// One block per (slot, value head), 128 threads. (I + A)^-1 by blocks of 16: the diagonal blocks by
+// forward substitution, a column to a thread, then twice
+//   [[P, 0], [B, Q]]^-1 = [[P^-1, 0], [-Q^-1 B P^-1, Q^-1]]
+// in fp32, the inverse taking the place of A.
 constexpr int kPrepThreads = 128;
 constexpr int kLPitch = 68;  // floats between rows of A
+constexpr int kMPitch = 36;  // and of the 32 x 32 product in between
 constexpr int kPrepSmem = 2 * kTile + kABytes + kVecBytes + kC * kLPitch * 4 + 4 * kC * 4;
 
-__global__ void __launch_bounds__(kPrepThreads)
+// Sums of floats kept as two floats (hi + lo, Knuth's exact sum of two): as exact as 48 bits, in fp32
+// operations alone (64-bit floating point runs at a small fraction of their rate here).
+struct Two {
+  float hi, lo;
+};
+__device__ __forceinline__ Two add_two(Two a, Two b) {
+  const float s = __fadd_rn(a.hi, b.hi), t = __fsub_rn(s, a.hi);
+  const float e = __fadd_rn(__fsub_rn(a.hi, __fsub_rn(s, t)), __fsub_rn(b.hi, t));
+  const float l = __fadd_rn(e, __fadd_rn(a.lo, b.lo));
+  const float hi = __fadd_rn(s, l);
+  return Two{hi, __fsub_rn(l, __fsub_rn(hi, s))};
+}
+// e^x for x <= 0. The rounding of x log2(e) costs |x| 2^-24 of the result, which is itself e^-|x|: at
+// most 2^-25 of 1 whatever x.
+__device__ __forceinline__ float exp_neg(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.4426950408889634f));
+  return y;
+}
+
+// c += A B of 16 x 16 blocks in shared memory, by a warp: lane has rows 2 (l / 4) and + 1, columns
+// 4 (l % 4) to + 3.
+__device__ __forceinline__ void mul16(float (&c)[2][4], const float* A, int pa, const float* B, int pb,
+                                      int lane) {
+  const float* a0 = A + 2 * (lane >> 2) * pa;
+  const float* b0 = B + 4 * (lane & 3);
+#pragma unroll
+  for (int k = 0; k < 16; k += 4) {
+    const float4 x = *reinterpret_cast<const float4*>(a0 + k);
+    const float4 y = *reinterpret_cast<const float4*>(a0 + pa + k);
+    const float xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float4 b = *reinterpret_cast<const float4*>(b0 + (k + j) * pb);
+      c[0][0] = fmaf(xs[j], b.x, c[0][0]), c[0][1] = fmaf(xs[j], b.y, c[0][1]);
+      c[0][2] = fmaf(xs[j], b.z, c[0][2]), c[0][3] = fmaf(xs[j], b.w, c[0][3]);
+      c[1][0] = fmaf(ys[j], b.x, c[1][0]), c[1][1] = fmaf(ys[j], b.y, c[1][1]);
+      c[1][2] = fmaf(ys[j], b.z, c[1][2]), c[1][3] = fmaf(ys[j], b.w, c[1][3]);
+    }
+  }
+}
+__device__ __forceinline__ void put16(const float (&c)[2][4], float sign, float* D, int pd, int lane) {
+#pragma unroll
+  for (int r = 0; r < 2; ++r)
+    *reinterpret_cast<float4*>(D + (2 * (lane >> 2) + r) * pd + 4 * (lane & 3)) =
+        make_float4(sign * c[r][0], sign * c[r][1], sign * c[r][2], sign * c[r][3]);
+}
+
+__global__ void __launch_bounds__(kPrepThreads, 3)
     delta_prep_kernel(const __grid_constant__ DeltaParams p, uint8_t* rec) {
   extern __shared__ __align__(128) uint8_t smem[];
   uint8_t* sk = smem;                              // K, Q; then the parts of T
@@ -108,6 +160,7 @@ __global__ void __launch_bounds__(kPrepThreads)
   float* ghi = L + kC * kLPitch;
   float* glo = ghi + kC;
   float* beta = glo + kC;
+  float* M = reinterpret_cast<float*>(smem);       // between K and T
   pdl_trigger();
   pdl_wait();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -129,45 +182,53 @@ __global__ void __launch_bounds__(kPrepThreads)
   {
     const __nv_bfloat16* kp = static_cast<const __nv_bfloat16*>(p.k) + static_cast<int64_t>(kh) * kDk;
     const __nv_bfloat16* qp = static_cast<const __nv_bfloat16*>(p.q) + static_cast<int64_t>(kh) * kDk;
-#pragma unroll 4
-    for (int i = tid; i < kC * 16; i += kPrepThreads) {
-      const int r = i >> 4, c = i & 15;
-      uint4 k = make_uint4(0u, 0u, 0u, 0u), q = k;
-      if (r < len) {
-        k = __ldg(reinterpret_cast<const uint4*>(kp + (row0 + r) * p.ks) + c);
-        q = __ldg(reinterpret_cast<const uint4*>(qp + (row0 + r) * p.qs) + c);
-      }
-      const int at = (c >> 3) * kPlane + swz(r, c & 7);
-      *reinterpret_cast<uint4*>(sk + at) = k;
-      *reinterpret_cast<uint4*>(sq + at) = q;
-    }
-  }
-  if (warp == 0) {
-    // Running sums in 64 bits, kept as two floats each: the difference of two of them is then as exact
-    // as a float, however far they have run. A decay below e^-200 is 0 in fp32 either way.
     const int t0 = 2 * lane, t1 = t0 + 1;
-    float g0 = t0 < len ? p.g[(static_cast<int64_t>(row0) + t0) * p.H + h] : 0.f;
-    float g1 = t1 < len ? p.g[(static_cast<int64_t>(row0) + t1) * p.H + h] : 0.f;
-    g0 = g0 < -200.f ? -200.f : g0;
-    g1 = g1 < -200.f ? -200.f : g1;
-    beta[t0] = t0 < len ? p.beta[(static_cast<int64_t>(row0) + t0) * p.H + h] : 0.f;
-    beta[t1] = t1 < len ? p.beta[(static_cast<int64_t>(row0) + t1) * p.H + h] : 0.f;
-    double s = static_cast<double>(g0) + g1;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const double x = __shfl_up_sync(0xffffffffu, s, o);
-      if (lane >= o) s += x;
+    float g0 = 0.f, g1 = 0.f, b0 = 0.f, b1 = 0.f;
+    if (warp == 0) {
+      const int64_t at = (static_cast<int64_t>(row0) + t0) * p.H + h;
+      if (t0 < len) g0 = p.g[at], b0 = p.beta[at];
+      if (t1 < len) g1 = p.g[at + p.H], b1 = p.beta[at + p.H];
     }
-    const double a = s - g1, last = __shfl_sync(0xffffffffu, s, 31);
-    ghi[t0] = static_cast<float>(a);
-    glo[t0] = static_cast<float>(a - ghi[t0]);
-    ghi[t1] = static_cast<float>(s);
-    glo[t1] = static_cast<float>(s - ghi[t1]);
-    vec[t0] = expf(static_cast<float>(a));
-    vec[t1] = expf(static_cast<float>(s));
-    vec[kC + t0] = t0 < len ? expf(static_cast<float>(last - a)) : 0.f;
-    vec[kC + t1] = t1 < len ? expf(static_cast<float>(last - s)) : 0.f;
-    if (lane == 0) vec[2 * kC] = expf(static_cast<float>(last));
+    uint4 k[8], q[8];  // all loads in flight at once
+    const int c = tid & 15, r0 = tid >> 4;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int r = r0 + 8 * i;
+      k[i] = q[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (r < len) {
+        k[i] = __ldg(reinterpret_cast<const uint4*>(kp + (row0 + r) * p.ks) + c);
+        q[i] = __ldg(reinterpret_cast<const uint4*>(qp + (row0 + r) * p.qs) + c);
+      }
+    }
+    if (warp == 0) {
+      // running sums of the log decays: the difference of two of them is as exact as a float, however
+      // far they have run. A decay below e^-200 is 0 in fp32 either way.
+      g0 = g0 < -200.f ? -200.f : g0;
+      g1 = g1 < -200.f ? -200.f : g1;
+      beta[t0] = b0;
+      beta[t1] = b1;
+      Two s = add_two(Two{g0, 0.f}, Two{g1, 0.f});
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const Two x{__shfl_up_sync(0xffffffffu, s.hi, o), __shfl_up_sync(0xffffffffu, s.lo, o)};
+        if (lane >= o) s = add_two(s, x);
+      }
+      const Two last{__shfl_sync(0xffffffffu, s.hi, 31), __shfl_sync(0xffffffffu, s.lo, 31)};
+      const Two a = lane == 0 ? Two{g0, 0.f} : add_two(s, Two{-g1, 0.f});
+      ghi[t0] = a.hi, glo[t0] = a.lo;
+      ghi[t1] = s.hi, glo[t1] = s.lo;
+      vec[t0] = expf(a.hi);
+      vec[t1] = expf(s.hi);
+      vec[kC + t0] = t0 < len ? expf((last.hi - a.hi) + (last.lo - a.lo)) : 0.f;
+      vec[kC + t1] = t1 < len ? expf((last.hi - s.hi) + (last.lo - s.lo)) : 0.f;
+      if (lane == 0) vec[2 * kC] = expf(last.hi);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int at = (c >> 3) * kPlane + swz(r0 + 8 * i, c & 7);
+      *reinterpret_cast<uint4*>(sk + at) = k[i];
+      *reinterpret_cast<uint4*>(sq + at) = q[i];
+    }
   }
   __syncthreads();
   // K K^T and Q K^T, lower triangle: warp w takes rows 16 w..16 w + 15, column tiles up to them
@@ -198,12 +259,14 @@ __global__ void __launch_bounds__(kPrepThreads)
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         const int i = warp * 16 + (lane >> 2) + 8 * half, j = t * 8 + 2 * (lane & 3);
-        float l[2], a[2];
+        float l[2] = {0.f, 0.f}, a[2] = {0.f, 0.f};
+        if (t <= 2 * warp + 1) {  // the tile reaches the rows' own tokens
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float d = expf((ghi[i] - ghi[j + e]) + (glo[i] - glo[j + e]));
-          l[e] = j + e < i ? beta[i] * d * kk[t][2 * half + e] : 0.f;
-          a[e] = j + e <= i ? p.scale * d * qk[t][2 * half + e] : 0.f;
+          for (int e = 0; e < 2; ++e) {
+            const float d = exp_neg((ghi[i] - ghi[j + e]) + (glo[i] - glo[j + e]));
+            l[e] = j + e < i ? beta[i] * d * kk[t][2 * half + e] : 0.f;
+            a[e] = j + e <= i ? p.scale * d * qk[t][2 * half + e] : 0.f;
+          }
         }
         *reinterpret_cast<float2*>(L + i * kLPitch + j) = make_float2(l[0], l[1]);
         uint32_t w[2];
@@ -215,36 +278,58 @@ __global__ void __launch_bounds__(kPrepThreads)
     }
   }
   __syncthreads();
-  // (I + A)^-1 by forward substitution, a column to a thread in registers, rows above it zero
-  if (warp < 2) {
-    float t[kC];
+  if (warp < 2) {  // diagonal blocks: thread 16 b + c has column c of block b
+    const int blk = tid >> 4, c = tid & 15;
+    float* D = L + blk * 16 * (kLPitch + 1);
+    float t[16];
 #pragma unroll
-    for (int i = 0; i < kC; ++i) {
-      t[i] = i == tid ? 1.f : 0.f;
-      if (i < 32 && warp == 1) continue;
-      float acc[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int i = 0; i < 16; ++i) {
+      float acc[2] = {0.f, 0.f};
 #pragma unroll
-      for (int j = 0; j < i; j += 4) {
-        const float4 x = *reinterpret_cast<const float4*>(L + i * kLPitch + j);
-        acc[0] = fmaf(x.x, t[j], acc[0]);
-        if (j + 1 < i) acc[1] = fmaf(x.y, t[j + 1], acc[1]);
-        if (j + 2 < i) acc[2] = fmaf(x.z, t[j + 2], acc[2]);
-        if (j + 3 < i) acc[3] = fmaf(x.w, t[j + 3], acc[3]);
-      }
-      t[i] -= (acc[0] + acc[1]) + (acc[2] + acc[3]);
+      for (int j = 0; j < i; ++j) acc[j & 1] = fmaf(D[i * kLPitch + j], t[j], acc[j & 1]);
+      t[i] = (i == c ? 1.f : 0.f) - (acc[0] + acc[1]);
     }
-    const float bt = beta[tid];
+    __syncwarp();
 #pragma unroll
-    for (int i = 0; i < kC; ++i) {
-      float x = t[i] * bt;
-      __nv_bfloat16* at = reinterpret_cast<__nv_bfloat16*>(smem + swz(i, tid >> 3) + 2 * (tid & 7));
+    for (int i = 0; i < 16; ++i) D[i * kLPitch + c] = t[i];
+  }
+  __syncthreads();
+  auto block = [&](int i, int j) { return L + i * 16 * kLPitch + j * 16; };
+  if (warp < 2) {  // the two blocks next to the diagonal in the 32 x 32 blocks
+    const int i = 2 * warp + 1;
+    float c[2][4] = {};
+    mul16(c, block(i, i - 1), kLPitch, block(i - 1, i - 1), kLPitch, lane);
+    __syncwarp();
+    put16(c, 1.f, M + warp * 16 * kMPitch, kMPitch, lane);
+    __syncwarp();
+    float d[2][4] = {};
+    mul16(d, block(i, i), kLPitch, M + warp * 16 * kMPitch, kMPitch, lane);
+    put16(d, -1.f, block(i, i - 1), kLPitch, lane);
+  }
+  __syncthreads();
+  {  // the lower left 32 x 32: a 16 x 16 block to a warp
+    const int bi = warp >> 1, bj = warp & 1;
+    float c[2][4] = {};
+    for (int k = bj; k < 2; ++k) mul16(c, block(2 + bi, k), kLPitch, block(k, bj), kLPitch, lane);
+    put16(c, 1.f, M + bi * 16 * kMPitch + bj * 16, kMPitch, lane);
+    __syncthreads();
+    float d[2][4] = {};
+    for (int k = 0; k <= bi; ++k)
+      mul16(d, block(2 + bi, 2 + k), kLPitch, M + k * 16 * kMPitch + bj * 16, kMPitch, lane);
+    put16(d, -1.f, block(2 + bi, bj), kLPitch, lane);
+  }
+  __syncthreads();
+  // T = (I + A)^-1 diag(beta) in three parts
+#pragma unroll 4
+  for (int i = tid; i < kC * kC / 2; i += kPrepThreads) {
+    const int r = i >> 5, j = 2 * (i & 31);
+    const float2 x = *reinterpret_cast<const float2*>(L + r * kLPitch + j);
+    const float2 bt = *reinterpret_cast<const float2*>(beta + j);
+    uint32_t w[3];
+    split<3>(j <= r ? x.x * bt.x : 0.f, j < r ? x.y * bt.y : 0.f, w);
 #pragma unroll
-      for (int s = 0; s < 3; ++s) {
-        const __nv_bfloat16 v = __float2bfloat16_rn(x);
-        at[s * (kPlane / 2)] = v;
-        x -= __bfloat162float(v);
-      }
-    }
+    for (int k = 0; k < 3; ++k)
+      *reinterpret_cast<uint32_t*>(smem + k * kPlane + swz(r, j >> 3) + 2 * (j & 7)) = w[k];
   }
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   __syncthreads();
@@ -256,7 +341,7 @@ __global__ void __launch_bounds__(kPrepThreads)
     asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst + kTBytes),
                  "r"(smem_u32(sa)), "r"(kABytes + kVecBytes)
                  : "memory");
-    asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group 0;" ::: "memory");
+    asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group.read 0;" ::: "memory");
   }
 }
 
@@ -271,8 +356,8 @@ __global__ void __launch_bounds__(kPrepThreads)
 // that its other operand waits for.
 constexpr int kChainThreads = 12 * 32;  // three groups of four warps; two of the last do nothing
 // Registers a thread: launched with 168 (64,512 in all), then shared out again by group. The chain takes
-// what the loads give: 4 x 32 x (224 + 144 + 64) = 55,296.
-constexpr int kChainRegs = 224, kOutRegs = 144, kLoadRegs = 64;
+// what the loads give: 4 x 32 x (224 + 160 + 64) = 57,344.
+constexpr int kChainRegs = 224, kOutRegs = 160, kLoadRegs = 64;
 constexpr int kCStages = 3, kOStages = 2;
 constexpr int kVTile = kC * kCols * 2;
 constexpr int kCStage = kTile + kTBytes + kVecBytes + kVTile;  // chain: K, T, vectors, V
