@@ -28,15 +28,21 @@ namespace {
 constexpr int kC = 64;                 // tokens per chunk
 constexpr int kDk = 128;
 constexpr int kCols = 16;              // columns of S per block
-constexpr int kPlane = kC * 128;       // a 64 x 64 bf16 matrix: rows of 128 bytes, swizzled
-constexpr int kTBytes = 3 * kPlane;    // T in three parts
-constexpr int kABytes = 2 * kPlane;    // scores in two parts
-constexpr int kVecBytes = 1024;        // e^G [64], e^(G_last - G) [64], e^G_last
+constexpr int kPanel = kC * 128;       // 64 dims of K or Q: rows of 128 bytes, swizzled
+constexpr int kTri = 32 * 64 + 32 * 128;  // 64 x 64 up to the diagonal: rows of 32, then of 64 columns
+constexpr int kTBytes = 3 * kTri;      // T in three parts
+constexpr int kABytes = 2 * kTri;      // scores in two parts
+constexpr int kVecBytes = 640;         // e^G [64], e^(G_last - G) [64], e^G_last
 constexpr int kRec = kTBytes + kABytes + kVecBytes;  // one chunk and head of the workspace
 constexpr int kTile = kC * kDk * 2;    // K or Q of a chunk: two panels of 64 dims
 
 // Where 16-byte piece c (0..7) of row r lies in a run of swizzled 128-byte rows.
 __device__ __forceinline__ int swz(int r, int c) { return r * 128 + ((c ^ (r & 7)) << 4); }
+
+// The same in a triangular matrix, whose first 32 rows have four pieces each.
+__device__ __forceinline__ int tri(int r, int c) {
+  return r < 32 ? r * 64 + ((c ^ ((r >> 1) & 3)) << 4) : 32 * 64 + swz(r - 32, c);
+}
 
 __device__ __forceinline__ void ldm4(uint32_t a, uint32_t* r) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -95,11 +101,16 @@ __device__ __forceinline__ int first_slot(int cu, int b) { return cu / kC + b; }
 // One block per (slot, value head), 128 threads. (I + A)^-1 by blocks of 16: the diagonal blocks by
 // forward substitution, a column to a thread, then twice
 //   [[P, 0], [B, Q]]^-1 = [[P^-1, 0], [-Q^-1 B P^-1, Q^-1]]
-// in fp32, the inverse taking the place of A.
+// in fp32, the inverse taking the place of A. Of T and the scores only the 16 x 16 blocks up to the
+// diagonal are made: the chain reads no others. Shared memory is used twice over (Q then A, K and the
+// scores then T), so that four blocks fit on an SM: with so many small phases it is the other blocks
+// that fill a phase's latencies.
 constexpr int kPrepThreads = 128;
 constexpr int kLPitch = 68;  // floats between rows of A
 constexpr int kMPitch = 36;  // and of the 32 x 32 product in between
-constexpr int kPrepSmem = 2 * kTile + kABytes + kVecBytes + kC * kLPitch * 4 + 4 * kC * 4;
+constexpr int kLBytes = kC * kLPitch * 4;
+constexpr int kPrepSmem = kTile + kLBytes + kABytes + kVecBytes + 3 * kC * 4;
+static_assert(2 * kTri <= kTile && kTri <= kABytes, "T's parts take the places of K and the scores");
 
 // Sums of floats kept as two floats (hi + lo, Knuth's exact sum of two): as exact as 48 bits, in fp32
 // operations alone (64-bit floating point runs at a small fraction of their rate here).
@@ -149,18 +160,19 @@ __device__ __forceinline__ void put16(const float (&c)[2][4], float sign, float*
         make_float4(sign * c[r][0], sign * c[r][1], sign * c[r][2], sign * c[r][3]);
 }
 
-__global__ void __launch_bounds__(kPrepThreads, 3)
+__global__ void __launch_bounds__(kPrepThreads, 4)
     delta_prep_kernel(const __grid_constant__ DeltaParams p, uint8_t* rec) {
   extern __shared__ __align__(128) uint8_t smem[];
-  uint8_t* sk = smem;                              // K, Q; then the parts of T
-  uint8_t* sq = smem + kTile;
-  uint8_t* sa = smem + 2 * kTile;                  // scores, vectors
+  uint8_t* sk = smem;                              // K; then M, then T's first two parts
+  uint8_t* sq = smem + kTile;                      // Q; then A and its inverse
+  uint8_t* sa = sq + kLBytes;                      // scores, vectors; then T's third part
   float* vec = reinterpret_cast<float*>(sa + kABytes);
-  float* L = reinterpret_cast<float*>(sa + kABytes + kVecBytes);
-  float* ghi = L + kC * kLPitch;
+  float* L = reinterpret_cast<float*>(sq);
+  float* ghi = reinterpret_cast<float*>(sa + kABytes + kVecBytes);
   float* glo = ghi + kC;
   float* beta = glo + kC;
-  float* M = reinterpret_cast<float*>(smem);       // between K and T
+  float* M = reinterpret_cast<float*>(sk);
+  uint8_t* dst;                                    // this chunk's and head's record
   pdl_trigger();
   pdl_wait();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -179,6 +191,7 @@ __global__ void __launch_bounds__(kPrepThreads, 3)
   const int len = min(kC, c1 - row0);
   if (len <= 0) return;  // the whole block
   const int kh = h / (p.H / p.Hk);
+  dst = rec + (static_cast<int64_t>(slot) * p.H + h) * kRec;
   {
     const __nv_bfloat16* kp = static_cast<const __nv_bfloat16*>(p.k) + static_cast<int64_t>(kh) * kDk;
     const __nv_bfloat16* qp = static_cast<const __nv_bfloat16*>(p.q) + static_cast<int64_t>(kh) * kDk;
@@ -225,7 +238,7 @@ __global__ void __launch_bounds__(kPrepThreads, 3)
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int at = (c >> 3) * kPlane + swz(r0 + 8 * i, c & 7);
+      const int at = (c >> 3) * kPanel + swz(r0 + 8 * i, c & 7);
       *reinterpret_cast<uint4*>(sk + at) = k[i];
       *reinterpret_cast<uint4*>(sq + at) = q[i];
     }
@@ -240,7 +253,7 @@ __global__ void __launch_bounds__(kPrepThreads, 3)
 #pragma unroll
     for (int s = 0; s < kDk / 16; ++s) {
       uint32_t ka[4], qa[4];
-      const int pan = (s >> 2) * kPlane, c = (s & 3) * 2;
+      const int pan = (s >> 2) * kPanel, c = (s & 3) * 2;
       ldm4(k32 + pan + swz(ar, c + ac), ka);
       ldm4(q32 + pan + swz(ar, c + ac), qa);
 #pragma unroll
@@ -254,30 +267,47 @@ __global__ void __launch_bounds__(kPrepThreads, 3)
           mma(qk[2 * t + 1], qa, b[2], b[3]);
         }
     }
+    __syncthreads();  // A takes Q's place
+    float hi2[2], lo2[2], bt2[2];
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const int i = warp * 16 + (lane >> 2) + 8 * half;
+      hi2[half] = ghi[i], lo2[half] = glo[i], bt2[half] = beta[i];
+    }
 #pragma unroll
     for (int t = 0; t < 8; ++t) {
+      if (t > 2 * warp + 1) break;
+      const int j = t * 8 + 2 * (lane & 3);
+      const float2 hj = *reinterpret_cast<const float2*>(ghi + j);
+      const float2 lj = *reinterpret_cast<const float2*>(glo + j);
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
-        const int i = warp * 16 + (lane >> 2) + 8 * half, j = t * 8 + 2 * (lane & 3);
-        float l[2] = {0.f, 0.f}, a[2] = {0.f, 0.f};
-        if (t <= 2 * warp + 1) {  // the tile reaches the rows' own tokens
+        const int i = warp * 16 + (lane >> 2) + 8 * half;
+        const float d[2] = {exp_neg((hi2[half] - hj.x) + (lo2[half] - lj.x)),
+                            exp_neg((hi2[half] - hj.y) + (lo2[half] - lj.y))};
+        float l[2], a[2];
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float d = exp_neg((ghi[i] - ghi[j + e]) + (glo[i] - glo[j + e]));
-            l[e] = j + e < i ? beta[i] * d * kk[t][2 * half + e] : 0.f;
-            a[e] = j + e <= i ? p.scale * d * qk[t][2 * half + e] : 0.f;
-          }
+        for (int e = 0; e < 2; ++e) {
+          l[e] = j + e < i ? bt2[half] * d[e] * kk[t][2 * half + e] : 0.f;
+          a[e] = j + e <= i ? p.scale * d[e] * qk[t][2 * half + e] : 0.f;
         }
         *reinterpret_cast<float2*>(L + i * kLPitch + j) = make_float2(l[0], l[1]);
         uint32_t w[2];
         split<2>(a[0], a[1], w);
-        const int at = swz(i, t) + 4 * (lane & 3);
+        const int at = tri(i, t) + 4 * (lane & 3);
         *reinterpret_cast<uint32_t*>(sa + at) = w[0];
-        *reinterpret_cast<uint32_t*>(sa + kPlane + at) = w[1];
+        *reinterpret_cast<uint32_t*>(sa + kTri + at) = w[1];
       }
     }
   }
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   __syncthreads();
+  if (tid == 0) {  // scores and vectors leave while T is worked out
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst + kTBytes),
+                 "r"(smem_u32(sa)), "r"(kABytes + kVecBytes)
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+  }
   if (warp < 2) {  // diagonal blocks: thread 16 b + c has column c of block b
     const int blk = tid >> 4, c = tid & 15;
     float* D = L + blk * 16 * (kLPitch + 1);
@@ -318,28 +348,31 @@ __global__ void __launch_bounds__(kPrepThreads, 3)
       mul16(d, block(2 + bi, 2 + k), kLPitch, M + k * 16 * kMPitch + bj * 16, kMPitch, lane);
     put16(d, -1.f, block(2 + bi, bj), kLPitch, lane);
   }
+  if (tid == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the scores are out
   __syncthreads();
-  // T = (I + A)^-1 diag(beta) in three parts
-#pragma unroll 4
-  for (int i = tid; i < kC * kC / 2; i += kPrepThreads) {
-    const int r = i >> 5, j = 2 * (i & 31);
-    const float2 x = *reinterpret_cast<const float2*>(L + r * kLPitch + j);
-    const float2 bt = *reinterpret_cast<const float2*>(beta + j);
-    uint32_t w[3];
-    split<3>(j <= r ? x.x * bt.x : 0.f, j < r ? x.y * bt.y : 0.f, w);
+  // T = (I + A)^-1 diag(beta) in three parts, a pair of columns of each block to a thread
 #pragma unroll
-    for (int k = 0; k < 3; ++k)
-      *reinterpret_cast<uint32_t*>(smem + k * kPlane + swz(r, j >> 3) + 2 * (j & 7)) = w[k];
-  }
+  for (int bi = 0; bi < 4; ++bi)
+#pragma unroll
+    for (int bj = 0; bj <= bi; ++bj) {
+      const int r = 16 * bi + (tid >> 3), j = 16 * bj + 2 * (tid & 7);
+      const float2 x = *reinterpret_cast<const float2*>(L + r * kLPitch + j);
+      const float2 bt = *reinterpret_cast<const float2*>(beta + j);
+      uint32_t w[3];
+      split<3>(x.x * bt.x, x.y * bt.y, w);
+      const int at = tri(r, j >> 3) + 2 * (j & 7);
+      *reinterpret_cast<uint32_t*>(sk + at) = w[0];
+      *reinterpret_cast<uint32_t*>(sk + kTri + at) = w[1];
+      *reinterpret_cast<uint32_t*>(sa + at) = w[2];
+    }
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   __syncthreads();
   if (tid == 0) {
-    uint8_t* dst = rec + (static_cast<int64_t>(slot) * p.H + h) * kRec;
     asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst),
-                 "r"(smem_u32(smem)), "r"(kTBytes)
+                 "r"(smem_u32(sk)), "r"(2 * kTri)
                  : "memory");
-    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst + kTBytes),
-                 "r"(smem_u32(sa)), "r"(kABytes + kVecBytes)
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst + 2 * kTri),
+                 "r"(smem_u32(sa)), "r"(kTri)
                  : "memory");
     asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group.read 0;" ::: "memory");
   }
@@ -353,20 +386,24 @@ __global__ void __launch_bounds__(kPrepThreads, 3)
 //   output  q S    ...    scores u, store
 // A warp of the chain has two tiles of eight tokens (w and 7 - w: the same work under causality) and a
 // quarter of S's rows. What a phase multiplies by (K, T) is read into registers before the barrier
-// that its other operand waits for.
+// that its other operand waits for. (S kept in registers as the next chunk's operand, its four partial
+// products meeting in shared memory instead, moves fewer bytes but took 2.16 us a chunk.)
 constexpr int kChainThreads = 12 * 32;  // three groups of four warps; two of the last do nothing
-// Registers a thread: launched with 168 (64,512 in all), then shared out again by group. The chain takes
-// what the loads give: 4 x 32 x (224 + 160 + 64) = 57,344.
+// Registers a thread: launched with 168 (64,512 in all), then shared out again by group, 57,344 in use.
 constexpr int kChainRegs = 224, kOutRegs = 160, kLoadRegs = 64;
-constexpr int kCStages = 3, kOStages = 2;
+constexpr int kCStages = 3, kOStages = 3;
 constexpr int kVTile = kC * kCols * 2;
-constexpr int kCStage = kTile + kTBytes + kVecBytes + kVTile;  // chain: K, T, vectors, V
-constexpr int kOStage = kTile + kABytes + kVecBytes;           // output: Q, scores, vectors
+// Beside K (Q), whose tiles start on 1,024 bytes: T, vectors, V for the chain, scores and vectors for
+// the outputs.
+constexpr int kCRest = kTBytes + kVecBytes + kVTile;
+constexpr int kORest = kABytes + kVecBytes;
 constexpr int kSPlane = kCols * 256;               // S^T: two panels of 16 rows of 128 bytes
 constexpr int kUPlane = kCols * 128;               // 16 x 64
 constexpr int kWork = 3 * kSPlane + 8 * kUPlane;   // S, r, u scaled for the state (3 each), u (2)
-constexpr int kChainSmem = kCStages * kCStage + kOStages * kOStage + kWork + 256 + 1024;
-static_assert(kCStage % 1024 == 0 && kOStage % 1024 == 0, "swizzled tiles start on 1,024 bytes");
+constexpr int kChainSmem =
+    kCStages * (kTile + kCRest) + kOStages * (kTile + kORest) + kWork + 128 + 1024;
+static_assert(kCRest % 128 == 0 && kORest % 128 == 0, "swizzled tiles start on 128 bytes");
+static_assert(kChainSmem <= 227 * 1024, "shared memory of an SM");
 
 struct ChainMaps {
   CUtensorMap k, q, v;  // [rows][columns], boxes of 64 x 64 (swizzled) and 16 x 64
@@ -433,8 +470,10 @@ __global__ void __launch_bounds__(kChainThreads, 1)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
-  uint8_t* ostages = smem + kCStages * kCStage;
-  uint8_t* sps = ostages + kOStages * kOStage;  // parts of S
+  uint8_t* sq = smem + kCStages * kTile;        // after the tiles of K
+  uint8_t* crest = sq + kOStages * kTile;
+  uint8_t* orest = crest + kCStages * kCRest;
+  uint8_t* sps = orest + kOStages * kORest;     // parts of S
   uint8_t* rps = sps + 3 * kSPlane;             // of r
   uint8_t* ups = rps + 3 * kUPlane;             // of e^(G_last - G) u
   uint8_t* ops = ups + 3 * kUPlane;             // of u
@@ -470,6 +509,8 @@ __global__ void __launch_bounds__(kChainThreads, 1)
   const int ar = lane & 15, ac = lane >> 4;
   const int bt = (lane & 16 ? tr : tl) * 8 + (lane & 7), bc = (lane >> 3) & 1;
   const uint32_t sp = smem_u32(sps), rp = smem_u32(rps), up = smem_u32(ups), op = smem_u32(ops);
+  // and of a triangular matrix's step i (tile tl has steps 0 and 1 only: anything in its place past them)
+  auto tri_at = [&](int i) { return tri(bt, bt < 32 ? (2 * i + bc) & 3 : 2 * i + bc); };
   bool ok = true;
   auto wait = [&](uint64_t* bar, uint32_t parity) {  // gives up waiting for good, not the walk
     if (ok && !mbar_wait_bounded(bar, parity)) {
@@ -497,19 +538,19 @@ __global__ void __launch_bounds__(kChainThreads, 1)
         const int row = c0 + c * kC;
         const uint8_t* r = base + static_cast<int64_t>(c) * p.H * kRec;
         const uint32_t bar = smem_u32(&full[s]);
-        uint8_t* st = chain ? smem + s * kCStage : ostages + s * kOStage;
-        mbar_arrive_expect_tx(&full[s], chain ? kCStage : kOStage);
-        if (chain) tma_box(st + kTile + kTBytes + kVecBytes, &maps.v, h * p.dv + col0, row, bar, 1, 0);
+        uint8_t* st = (chain ? smem : sq) + s * kTile;
+        uint8_t* rest = chain ? crest + s * kCRest : orest + s * kORest;
+        mbar_arrive_expect_tx(&full[s], kTile + (chain ? kCRest : kORest));
+        if (chain) tma_box(rest + kTBytes + kVecBytes, &maps.v, h * p.dv + col0, row, bar, 1, 0);
         // pieces: two panels of K or Q, the planes of T or of the scores, the vectors
         const int planes = chain ? 3 : 2;
         for (int i = rank; i < 3 + planes; i += cs) {
           if (i < 2)
-            tma_box(st + i * kPlane, chain ? &maps.k : &maps.q, kh * kDk + i * 64, row, bar, cs, mask);
+            tma_box(st + i * kPanel, chain ? &maps.k : &maps.q, kh * kDk + i * 64, row, bar, cs, mask);
           else if (i < 2 + planes)
-            bulk_copy(st + kTile + (i - 2) * kPlane, r + (chain ? 0 : kTBytes) + (i - 2) * kPlane, kPlane, bar,
-                      cs, mask);
+            bulk_copy(rest + (i - 2) * kTri, r + (chain ? 0 : kTBytes) + (i - 2) * kTri, kTri, bar, cs, mask);
           else
-            bulk_copy(st + kTile + planes * kPlane, r + kTBytes + kABytes, kVecBytes, bar, cs, mask);
+            bulk_copy(rest + planes * kTri, r + kTBytes + kABytes, kVecBytes, bar, cs, mask);
         }
       }
     }
@@ -524,13 +565,13 @@ __global__ void __launch_bounds__(kChainThreads, 1)
     for (int c = 0; c < n; ++c) {
       const int s = c % kOStages;
       wait(&ofull[s], (c / kOStages) & 1);
-      const uint8_t* st = ostages + s * kOStage;
-      const uint32_t q32 = smem_u32(st), a32 = q32 + kTile;
-      const float* eg = reinterpret_cast<const float*>(st + kTile + kABytes);
+      const uint8_t* rest = orest + s * kORest;
+      const uint32_t q32 = smem_u32(sq + s * kTile), a32 = smem_u32(rest);
+      const float* eg = reinterpret_cast<const float*>(rest + kABytes);
       const int len = min(kC, c1 - c0 - c * kC);
       uint32_t qb[8][4];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) ldm4(q32 + (i >> 2) * kPlane + swz(bt, (i & 3) * 2 + bc), qb[i]);
+      for (int i = 0; i < 8; ++i) ldm4(q32 + (i >> 2) * kPanel + swz(bt, (i & 3) * 2 + bc), qb[i]);
       bar_sync(kBarState, 256);
       float x[2][2][4] = {};  // [part][tile]
 #pragma unroll
@@ -549,8 +590,8 @@ __global__ void __launch_bounds__(kChainThreads, 1)
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         if (i <= tr / 2) {
-          ldm4(a32 + swz(bt, 2 * i + bc), ab[i][0]);
-          ldm4(a32 + kPlane + swz(bt, 2 * i + bc), ab[i][1]);
+          ldm4(a32 + tri_at(i), ab[i][0]);
+          ldm4(a32 + kTri + tri_at(i), ab[i][1]);
         }
       bar_sync(kBarU, 256);
       float o[3][2][4] = {};
@@ -620,21 +661,22 @@ __global__ void __launch_bounds__(kChainThreads, 1)
     int len = 0;
     auto open_stage = [&](int c) {
       wait(&cfull[c % kCStages], (c / kCStages) & 1);
-      uint8_t* st = smem + (c % kCStages) * kCStage;
-      const float* eg = reinterpret_cast<const float*>(st + kTile + kTBytes);
-      const uint8_t* sv = st + kTile + kTBytes + kVecBytes;
+      uint8_t* st = smem + (c % kCStages) * kTile;
+      const uint8_t* rest = crest + (c % kCStages) * kCRest;
+      const float* eg = reinterpret_cast<const float*>(rest + kTBytes);
+      const uint8_t* sv = rest + kTBytes + kVecBytes;
       len = min(kC, c1 - c0 - c * kC);
       if (len < kC) {
         // rows past the request's end are another's: what they hold must not reach S even times 0
         for (int i = tid; i < (kC - len) * 16; i += 128) {
           const int r = len + (i >> 4), pc = i & 15;
-          *reinterpret_cast<uint4*>(st + (pc >> 3) * kPlane + swz(r, pc & 7)) = make_uint4(0u, 0u, 0u, 0u);
+          *reinterpret_cast<uint4*>(st + (pc >> 3) * kPanel + swz(r, pc & 7)) = make_uint4(0u, 0u, 0u, 0u);
         }
         bar_sync(kBarChain, 128);
       }
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        ldm4(smem_u32(st) + (i >> 2) * kPlane + swz(bt, (i & 3) * 2 + bc), kb[i]);
+        ldm4(smem_u32(st) + (i >> 2) * kPanel + swz(bt, (i & 3) * 2 + bc), kb[i]);
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         const int tile = t ? tr : tl, tok = tile * 8 + 2 * q;
@@ -655,9 +697,9 @@ __global__ void __launch_bounds__(kChainThreads, 1)
     }
     for (int c = 0; c < n; ++c) {
       const int s = c % kCStages;
-      uint8_t* st = smem + s * kCStage;
-      const uint32_t k32 = smem_u32(st), t32 = k32 + kTile;
-      const float all = reinterpret_cast<const float*>(st + kTile + kTBytes)[2 * kC];
+      const uint8_t* rest = crest + s * kCRest;
+      const uint32_t k32 = smem_u32(smem + s * kTile), t32 = smem_u32(rest);
+      const float all = reinterpret_cast<const float*>(rest + kTBytes)[2 * kC];
       bar_sync(kBarChain, 128);  // the parts of S are there
       // k S of the warp's tokens, the parts of S in sums of their own
       float x[3][2][4] = {};
@@ -682,7 +724,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       uint32_t tb[4][3][4];  // the first three here, the last one beside the products of the others
       auto load_t = [&](int i) {
 #pragma unroll
-        for (int j = 0; j < 3; ++j) ldm4(t32 + j * kPlane + swz(bt, 2 * i + bc), tb[i][j]);
+        for (int j = 0; j < 3; ++j) ldm4(t32 + j * kTri + tri_at(i), tb[i][j]);
       };
 #pragma unroll
       for (int i = 0; i < 3; ++i)
@@ -743,7 +785,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       uint32_t kt[4][8];
       {
         const int kr = (lane & 7) + ((lane >> 3) & 1) * 8, kc = 4 * (warp & 1) + (lane >> 4);
-        const uint32_t k0 = k32 + (warp >> 1) * kPlane;
+        const uint32_t k0 = k32 + (warp >> 1) * kPanel;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           ldm4t(k0 + swz(16 * i + kr, kc), kt[i]);
