@@ -50,7 +50,6 @@ template <typename T>
 __global__ void __launch_bounds__(kSimtThreads, 1)
     attn_simt_kernel(const __grid_constant__ AttnParams p) {
   extern __shared__ __align__(16) uint8_t smem[];
-  pdl_trigger();
   pdl_wait();
   const int D = p.D, ld = D + kPad, tid = threadIdx.x;
   float* qs = reinterpret_cast<float*>(smem);          // [16][ld]
@@ -207,7 +206,6 @@ __global__ void __launch_bounds__(NW == 1 ? 128 : 32 * NW)
     attn_join_kernel(const __grid_constant__ AttnParams p) {
   __shared__ float sm_m[NW], sm_l[NW];
   __shared__ float sm_o[NW == 1 ? 1 : NW][NW == 1 ? 1 : kMaxD];
-  pdl_trigger();
   const int lane = threadIdx.x & 31, warp = NW == 1 ? 0 : threadIdx.x >> 5;
   const int Hq = p.Hkv * p.G;
   const int64_t id = NW == 1 ? static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5) : blockIdx.x;

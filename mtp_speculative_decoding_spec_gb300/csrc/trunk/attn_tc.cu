@@ -184,7 +184,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   int32_t* cum = reinterpret_cast<int32_t*>(smem + Sh::kFixed + 512);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  pdl_trigger();
   if (threadIdx.x == 0) {
     for (int s = 0; s < NS; ++s) {
       mbar_init(&kfull[s], 1);

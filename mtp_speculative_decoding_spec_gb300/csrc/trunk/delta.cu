@@ -11,9 +11,10 @@
 // of 4 LV columns and all dk rows in registers: LV lanes side by side hold four columns each,
 // 32 / LV groups of lanes hold NI consecutive rows each. A row costs two dot products per column,
 // taken together over S~ (o = scale (S~^T q + (k.q) u)), one butterfly over the groups, and
-// the rank-one update; no block barrier, no shared memory. The next row's inputs are loaded while
-// the present one is computed. Bound by the state's bytes when there are many requests (read once,
-// one write per snapshot), by the latency of the row chain when there are few.
+// the rank-one update; no block barrier. Rows come in groups of eight through the warp's own piece of
+// shared memory, the next group's copies in flight while one is computed: a verify pass waits for
+// memory once, not once a row. Bound by the state's bytes when there are many requests (read once, one
+// write per snapshot), by the latency of the row chain when there are few.
 #include <math.h>
 
 #include <cuda_bf16.h>
@@ -62,6 +63,20 @@ __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float x) {
 template <typename T, int N>
 struct Raw {
   alignas(16) T e[N];
+  __device__ __forceinline__ void shared(const T* p) {  // aligned to its own size, at most 16 bytes
+    constexpr int kBytes = N * static_cast<int>(sizeof(T));
+    if constexpr (kBytes >= 16) {
+#pragma unroll
+      for (int i = 0; i < kBytes / 16; ++i)
+        reinterpret_cast<uint4*>(e)[i] = reinterpret_cast<const uint4*>(p)[i];
+    } else if constexpr (kBytes == 8) {
+      *reinterpret_cast<uint2*>(e) = *reinterpret_cast<const uint2*>(p);
+    } else if constexpr (kBytes == 4) {
+      *reinterpret_cast<uint32_t*>(e) = *reinterpret_cast<const uint32_t*>(p);
+    } else {
+      e[0] = p[0];
+    }
+  }
   __device__ __forceinline__ void load(const T* p, bool vec, int have) {
     constexpr int kBytes = N * static_cast<int>(sizeof(T));
     if (vec && have >= N) {
@@ -83,17 +98,32 @@ struct Raw {
   }
 };
 
-constexpr int kScanThreads = 128;
+constexpr int kGroup = 8;  // rows staged at once
+
+template <int kBytes>
+__device__ __forceinline__ void copy_async16(void* dst, const void* src) {
+  static_assert(kBytes == 16, "one vector");
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+
+// A warp's shared memory: q and k of a group (one or two of them in flight), v, decay and beta.
+template <typename T, int NI, int LV>
+struct Staged {
+  static constexpr int kP = 32 / LV * NI;  // dk, filled up to the lanes' rows
+  static constexpr int kQk = kGroup * kP * static_cast<int>(sizeof(T));
+  static constexpr int kV = kGroup * 4 * LV * static_cast<int>(sizeof(T));
+  static constexpr int bytes(int bufs) { return 2 * bufs * kQk + kV + 2 * kGroup * 4; }
+};
 
 template <typename T, int NI, int LV>
-__global__ void __launch_bounds__(kScanThreads)
-    delta_scan_kernel(const __grid_constant__ DeltaParams p) {
-  pdl_trigger();
+__global__ void __launch_bounds__(128, 1) delta_scan_kernel(const __grid_constant__ DeltaParams p, int bufs) {
+  using St = Staged<T, NI, LV>;
+  extern __shared__ __align__(16) uint8_t smem[];
   pdl_wait();
   if (p.hdr && blockIdx.x == 0 && threadIdx.x == 0) p.hdr->error = 0;  // no wait here can set it
   const int lane = threadIdx.x & 31;
   const int tiles = (p.dv + 4 * LV - 1) / (4 * LV);
-  const int64_t wid = static_cast<int64_t>(blockIdx.x) * (kScanThreads / 32) + (threadIdx.x >> 5);
+  const int64_t wid = static_cast<int64_t>(blockIdx.x) * (blockDim.x / 32) + (threadIdx.x >> 5);
   const int tile = static_cast<int>(wid % tiles);
   const int64_t bh = wid / tiles;
   const int h = static_cast<int>(bh % p.H);
@@ -121,24 +151,65 @@ __global__ void __launch_bounds__(kScanThreads)
     R = p.R;
     n = p.n_rows ? max(0, min(p.n_rows[b], p.R)) : p.R;
   }
-  // its state: elements of a request's state (or of a slot), of this layer and head in it
-  const int64_t elems = static_cast<int64_t>(p.layers) * p.H * p.dk * p.dv;
-  const int64_t off = (static_cast<int64_t>(p.layer) * p.H + h) * p.dk * p.dv +
-                      static_cast<int64_t>(i0) * p.dv + col;
   int slot = 0;
-  const float* src;
-  if (prefill) {
-    src = p.init ? p.init + b * elems + off : nullptr;
-  } else if (p.mode == SPEC_COMMIT_INDEX) {
+  if (p.mode == SPEC_COMMIT_INDEX) {
     slot = p.live_slot[b];
     if (slot < 0 || slot >= p.n_slots) {  // no live state: no row runs
       slot = 0;
       n = 0;
     }
-    src = p.slots + (static_cast<int64_t>(b) * p.n_slots + slot) * elems + off;
-  } else {
-    src = p.live + b * elems + off;
   }
+  // the first group's rows and the state, all in flight together
+  uint8_t* mine = smem + (threadIdx.x >> 5) * St::bytes(bufs);
+  uint8_t* sv = mine + 2 * bufs * St::kQk;
+  float* sa = reinterpret_cast<float*>(sv + St::kV);
+  float* sb = sa + kGroup;
+  const T* qp = static_cast<const T*>(p.q) + row0 * p.qs + static_cast<int64_t>(kh) * p.dk;
+  const T* kp = static_cast<const T*>(p.k) + row0 * p.ks + static_cast<int64_t>(kh) * p.dk;
+  const T* vp = static_cast<const T*>(p.v) + row0 * p.vs + static_cast<int64_t>(h) * p.dv;
+  T* op = static_cast<T*>(p.out) + row0 * p.os + static_cast<int64_t>(h) * p.dv + col;
+  Raw<T, 4> vn;  // row lane / LV of the group (in the first 8 LV lanes)
+  float gn = 0.f, bn = 0.f;
+  auto fetch = [&](int r0, int buf) {
+    constexpr int kE = 16 / static_cast<int>(sizeof(T));
+    T* sq = reinterpret_cast<T*>(mine + 2 * buf * St::kQk);
+    T* sk = sq + kGroup * St::kP;
+    if (p.vec_qk) {
+      for (int i = lane; i < kGroup * St::kP / kE; i += 32) {
+        const int r = i / (St::kP / kE), d = (i % (St::kP / kE)) * kE;
+        if (r0 + r < n && d < p.dk) {
+          copy_async16<16>(sq + r * St::kP + d, qp + (r0 + r) * p.qs + d);
+          copy_async16<16>(sk + r * St::kP + d, kp + (r0 + r) * p.ks + d);
+        } else {
+          *reinterpret_cast<uint4*>(sq + r * St::kP + d) = make_uint4(0u, 0u, 0u, 0u);
+          *reinterpret_cast<uint4*>(sk + r * St::kP + d) = make_uint4(0u, 0u, 0u, 0u);
+        }
+      }
+    } else {
+      for (int i = lane; i < kGroup * St::kP; i += 32) {
+        const int r = i / St::kP, d = i % St::kP;
+        const bool there = r0 + r < n && d < p.dk;
+        sq[i] = there ? qp[(r0 + r) * p.qs + d] : from_f<T>(0.f);
+        sk[i] = there ? kp[(r0 + r) * p.ks + d] : from_f<T>(0.f);
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    const int r = r0 + lane / LV;
+    vn.load(vp + r * p.vs + col, p.vec_v, lane < kGroup * LV && r < n && on ? 4 : 0);
+    if (lane < kGroup && r0 + lane < n) {
+      gn = __ldg(p.g + (row0 + r0 + lane) * p.H + h);
+      bn = __ldg(p.beta + (row0 + r0 + lane) * p.H + h);
+    }
+  };
+  if (n > 0) fetch(0, 0);
+  // its state: elements of a request's state (or of a slot), of this layer and head in it
+  const int64_t elems = static_cast<int64_t>(p.layers) * p.H * p.dk * p.dv;
+  const int64_t off = (static_cast<int64_t>(p.layer) * p.H + h) * p.dk * p.dv +
+                      static_cast<int64_t>(i0) * p.dv + col;
+  const float* src = prefill ? (p.init ? p.init + b * elems + off : nullptr)
+                     : p.mode == SPEC_COMMIT_INDEX
+                         ? p.slots + (static_cast<int64_t>(b) * p.n_slots + slot) * elems + off
+                         : p.live + b * elems + off;
   f2 s[NI][2];
 #pragma unroll
   for (int ii = 0; ii < NI; ++ii) {
@@ -152,102 +223,109 @@ __global__ void __launch_bounds__(kScanThreads)
     for (int ii = 0; ii < NI; ++ii) {
       const float2 x = unpair(s[ii][0]), y = unpair(s[ii][1]);
       if (on && ii < have)
-        *reinterpret_cast<float4*>(dst + static_cast<int64_t>(ii) * p.dv) =
-            make_float4(x.x, x.y, y.x, y.y);
+        __stcs(reinterpret_cast<float4*>(dst + static_cast<int64_t>(ii) * p.dv),
+               make_float4(x.x, x.y, y.x, y.y));
     }
   };
+  float* slots = p.slots + static_cast<int64_t>(b) * p.n_slots * elems + off;
   if (p.mode == SPEC_COMMIT_SNAPSHOT || p.mode == SPEC_COMMIT_REPLAY)  // slot 0: before the cycle
-    store_state(p.slots + static_cast<int64_t>(b) * p.n_slots * elems + off);
+    store_state(slots);
 
-  const T* qp = static_cast<const T*>(p.q) + row0 * p.qs + static_cast<int64_t>(kh) * p.dk + i0;
-  const T* kp = static_cast<const T*>(p.k) + row0 * p.ks + static_cast<int64_t>(kh) * p.dk + i0;
-  const T* vp = static_cast<const T*>(p.v) + row0 * p.vs + static_cast<int64_t>(h) * p.dv + col;
-  T* op = static_cast<T*>(p.out) + row0 * p.os + static_cast<int64_t>(h) * p.dv + col;
-  const float* gp = p.g + row0 * p.H + h;
-  const float* bp = p.beta + row0 * p.H + h;
-  Raw<T, NI> qn, kn;
-  Raw<T, 4> vn;
-  float gn = 0.f, bn = 0.f;
-  auto fetch = [&](int64_t r) {
-    qn.load(qp + r * p.qs, p.vec_qk, have);
-    kn.load(kp + r * p.ks, p.vec_qk, have);
-    vn.load(vp + r * p.vs, p.vec_v, on ? 4 : 0);
-    gn = __ldg(gp + r * p.H);
-    bn = __ldg(bp + r * p.H);
-  };
-  if (n > 0) fetch(0);
-  for (int r = 0; r < n; ++r) {
-    const Raw<T, NI> qr = qn, kr = kn;
-    const Raw<T, 4> vr = vn;
-    const float a = expf(gn), beta = bn;
-    if (r + 1 < n) fetch(r + 1);
-    const f2 a2 = pair(a, a);
-    f2 ks0 = 0, ks1 = 0, qs0 = 0, qs1 = 0;
-    float qk = 0.f;
-#pragma unroll
-    for (int ii = 0; ii < NI; ++ii) {
-      const float kf = to_f(kr.e[ii]), qf = to_f(qr.e[ii]);
-      const f2 k2 = pair(kf, kf), q2 = pair(qf, qf);
-      s[ii][0] = mul2(s[ii][0], a2);
-      s[ii][1] = mul2(s[ii][1], a2);
-      ffma2_acc(ks0, k2, s[ii][0]);
-      ffma2_acc(ks1, k2, s[ii][1]);
-      ffma2_acc(qs0, q2, s[ii][0]);
-      ffma2_acc(qs1, q2, s[ii][1]);
-      qk = fmaf(kf, qf, qk);
+  int to = slot;
+  for (int r0 = 0; r0 < n; r0 += kGroup) {
+    const int buf = bufs == 2 ? (r0 / kGroup) & 1 : 0;
+    if (lane < kGroup * LV) *reinterpret_cast<Raw<T, 4>*>(sv + lane * 4 * sizeof(T)) = vn;
+    if (lane < kGroup) {
+      sa[lane] = expf(gn);
+      sb[lane] = bn;
     }
-#pragma unroll
-    for (int o = LV; o < 32; o <<= 1) {
-      ks0 = add2(ks0, __shfl_xor_sync(0xffffffffu, ks0, o));
-      ks1 = add2(ks1, __shfl_xor_sync(0xffffffffu, ks1, o));
-      qs0 = add2(qs0, __shfl_xor_sync(0xffffffffu, qs0, o));
-      qs1 = add2(qs1, __shfl_xor_sync(0xffffffffu, qs1, o));
-      qk += __shfl_xor_sync(0xffffffffu, qk, o);
+    if (r0 + kGroup < n) {  // only with two buffers
+      fetch(r0 + kGroup, buf ^ 1);
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+    } else {
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
     }
-    const float2 ka = unpair(ks0), kb = unpair(ks1), qa = unpair(qs0), qb = unpair(qs1);
-    float u[4];
-    u[0] = beta * (to_f(vr.e[0]) - ka.x);
-    u[1] = beta * (to_f(vr.e[1]) - ka.y);
-    u[2] = beta * (to_f(vr.e[2]) - kb.x);
-    u[3] = beta * (to_f(vr.e[3]) - kb.y);
-    if (lead && on) {
-      T* dst = op + static_cast<int64_t>(r) * p.os;
-      alignas(16) T o4[4];
-      o4[0] = from_f<T>(p.scale * fmaf(qk, u[0], qa.x));
-      o4[1] = from_f<T>(p.scale * fmaf(qk, u[1], qa.y));
-      o4[2] = from_f<T>(p.scale * fmaf(qk, u[2], qb.x));
-      o4[3] = from_f<T>(p.scale * fmaf(qk, u[3], qb.y));
-      if (p.vec_o) {
-        if constexpr (sizeof(T) == 2)
-          *reinterpret_cast<uint2*>(dst) = *reinterpret_cast<const uint2*>(o4);
-        else
-          *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(o4);
-      } else {
+    __syncwarp();
+    const T* sq = reinterpret_cast<const T*>(mine + 2 * buf * St::kQk) + i0;
+    const T* sk = sq + kGroup * St::kP;
+    const int rows = min(kGroup, n - r0);
+    for (int r = 0; r < rows; ++r) {
+      Raw<T, NI> qr, kr;
+      Raw<T, 4> vr;
+      qr.shared(sq + r * St::kP);
+      kr.shared(sk + r * St::kP);
+      vr.shared(reinterpret_cast<const T*>(sv) + (r * LV + lane % LV) * 4);
+      const float a = sa[r], beta = sb[r];
+      const f2 a2 = pair(a, a);
+      f2 ks0 = 0, ks1 = 0, qs0 = 0, qs1 = 0;
+      float qk = 0.f;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) dst[j] = o4[j];
+      for (int ii = 0; ii < NI; ++ii) {
+        const float kf = to_f(kr.e[ii]), qf = to_f(qr.e[ii]);
+        const f2 k2 = pair(kf, kf), q2 = pair(qf, qf);
+        s[ii][0] = mul2(s[ii][0], a2);
+        s[ii][1] = mul2(s[ii][1], a2);
+        ffma2_acc(ks0, k2, s[ii][0]);
+        ffma2_acc(ks1, k2, s[ii][1]);
+        ffma2_acc(qs0, q2, s[ii][0]);
+        ffma2_acc(qs1, q2, s[ii][1]);
+        qk = fmaf(kf, qf, qk);
+      }
+#pragma unroll
+      for (int o = LV; o < 32; o <<= 1) {
+        ks0 = add2(ks0, __shfl_xor_sync(0xffffffffu, ks0, o));
+        ks1 = add2(ks1, __shfl_xor_sync(0xffffffffu, ks1, o));
+        qs0 = add2(qs0, __shfl_xor_sync(0xffffffffu, qs0, o));
+        qs1 = add2(qs1, __shfl_xor_sync(0xffffffffu, qs1, o));
+        qk += __shfl_xor_sync(0xffffffffu, qk, o);
+      }
+      const float2 ka = unpair(ks0), kb = unpair(ks1), qa = unpair(qs0), qb = unpair(qs1);
+      float u[4];
+      u[0] = beta * (to_f(vr.e[0]) - ka.x);
+      u[1] = beta * (to_f(vr.e[1]) - ka.y);
+      u[2] = beta * (to_f(vr.e[2]) - kb.x);
+      u[3] = beta * (to_f(vr.e[3]) - kb.y);
+      if (lead && on) {
+        T* dst = op + static_cast<int64_t>(r0 + r) * p.os;
+        alignas(16) T o4[4];
+        o4[0] = from_f<T>(p.scale * fmaf(qk, u[0], qa.x));
+        o4[1] = from_f<T>(p.scale * fmaf(qk, u[1], qa.y));
+        o4[2] = from_f<T>(p.scale * fmaf(qk, u[2], qb.x));
+        o4[3] = from_f<T>(p.scale * fmaf(qk, u[3], qb.y));
+        if (p.vec_o) {
+          if constexpr (sizeof(T) == 2)
+            *reinterpret_cast<uint2*>(dst) = *reinterpret_cast<const uint2*>(o4);
+          else
+            *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(o4);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) dst[j] = o4[j];
+        }
+      }
+#pragma unroll
+      for (int ii = 0; ii < NI; ++ii) {
+        const float kf = to_f(kr.e[ii]);
+        // scalar products: a packed product and sum come out fused, which rounds once only
+        s[ii][0] = add2(s[ii][0], pair(__fmul_rn(kf, u[0]), __fmul_rn(kf, u[1])));
+        s[ii][1] = add2(s[ii][1], pair(__fmul_rn(kf, u[2]), __fmul_rn(kf, u[3])));
+      }
+      if (p.mode == SPEC_COMMIT_SNAPSHOT || p.mode == SPEC_COMMIT_INDEX) {
+        if (++to == p.n_slots) to = 0;
+        store_state(slots + to * elems);
+      } else if (p.mode == SPEC_COMMIT_REPLAY) {
+        const int64_t lh =
+            ((static_cast<int64_t>(b) * (p.n_slots - 1) + r0 + r) * p.layers + p.layer) * p.H + h;
+        if (lead && on)
+          *reinterpret_cast<float4*>(p.step_c + lh * p.dv + col) = make_float4(u[0], u[1], u[2], u[3]);
+        if (tile == 0 && lane % LV == 0) {
+#pragma unroll
+          for (int ii = 0; ii < NI; ++ii)
+            if (ii < have) p.step_b[lh * p.dk + i0 + ii] = to_f(kr.e[ii]);
+          if (lane == 0) p.step_a[lh] = a;
+        }
       }
     }
-#pragma unroll
-    for (int ii = 0; ii < NI; ++ii) {
-      const float kf = to_f(kr.e[ii]);
-      // scalar products: a packed product and sum come out fused, which rounds once only
-      s[ii][0] = add2(s[ii][0], pair(__fmul_rn(kf, u[0]), __fmul_rn(kf, u[1])));
-      s[ii][1] = add2(s[ii][1], pair(__fmul_rn(kf, u[2]), __fmul_rn(kf, u[3])));
-    }
-    if (p.mode == SPEC_COMMIT_SNAPSHOT || p.mode == SPEC_COMMIT_INDEX) {
-      const int to = (slot + r + 1) % p.n_slots;
-      store_state(p.slots + (static_cast<int64_t>(b) * p.n_slots + to) * elems + off);
-    } else if (p.mode == SPEC_COMMIT_REPLAY) {
-      const int64_t lh = ((static_cast<int64_t>(b) * (p.n_slots - 1) + r) * p.layers + p.layer) * p.H + h;
-      if (lead && on)
-        *reinterpret_cast<float4*>(p.step_c + lh * p.dv + col) = make_float4(u[0], u[1], u[2], u[3]);
-      if (tile == 0 && lane % LV == 0) {
-#pragma unroll
-        for (int ii = 0; ii < NI; ++ii)
-          if (ii < have) p.step_b[lh * p.dk + i0 + ii] = to_f(kr.e[ii]);
-        if (lane == 0) p.step_a[lh] = a;
-      }
-    }
+    __syncwarp();  // the group's rows are read
   }
   if (prefill) {
     store_state(p.live + b * elems + off);
@@ -259,13 +337,20 @@ __global__ void __launch_bounds__(kScanThreads)
 }
 
 template <typename T, int NI, int LV>
-cudaError_t launch_scan(const DeltaParams& p, cudaStream_t stream) {
+cudaError_t launch_scan(const DeltaParams& p, int sms, cudaStream_t stream) {
+  static SmemAllowance allowed;
   const int64_t tiles = (p.dv + 4 * LV - 1) / (4 * LV);
   const int64_t warps = tiles * p.H * p.B;
-  const int64_t blocks = (warps + kScanThreads / 32 - 1) / (kScanThreads / 32);
+  // few warps: one to a block, so that they spread over all SMs
+  const int per = warps <= 8 * static_cast<int64_t>(sms) ? 1 : 4;
+  const int64_t blocks = (warps + per - 1) / per;
   if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  return launch_pdl(delta_scan_kernel<T, NI, LV>, dim3(static_cast<unsigned>(blocks)),
-                    dim3(kScanThreads), 0, stream, p);
+  const int bufs = p.mode == DELTA_PREFILL ? 2 : 1;
+  const int smem = per * Staged<T, NI, LV>::bytes(bufs);
+  const cudaError_t e = allow_dynamic_smem(delta_scan_kernel<T, NI, LV>, smem, allowed);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(delta_scan_kernel<T, NI, LV>, dim3(static_cast<unsigned>(blocks)), dim3(32 * per), smem,
+                    stream, p, bufs);
 }
 
 template <typename T>
@@ -274,14 +359,14 @@ cudaError_t scan_of(const DeltaParams& p, int sms, cudaStream_t stream) {
   // is half as long for the same work in total.
   const int64_t warps = static_cast<int64_t>((p.dv + 15) / 16) * p.H * p.B;
   if (warps < 2 * sms && p.dk <= 128) {
-    if (p.dk <= 16) return launch_scan<T, 1, 2>(p, stream);
-    if (p.dk <= 64) return launch_scan<T, 4, 2>(p, stream);
-    return launch_scan<T, 8, 2>(p, stream);
+    if (p.dk <= 16) return launch_scan<T, 1, 2>(p, sms, stream);
+    if (p.dk <= 64) return launch_scan<T, 4, 2>(p, sms, stream);
+    return launch_scan<T, 8, 2>(p, sms, stream);
   }
-  if (p.dk <= 16) return launch_scan<T, 2, 4>(p, stream);
-  if (p.dk <= 64) return launch_scan<T, 8, 4>(p, stream);
-  if (p.dk <= 128) return launch_scan<T, 16, 4>(p, stream);
-  return launch_scan<T, 16, 2>(p, stream);  // 256 rows: a warp's registers hold 8 columns
+  if (p.dk <= 16) return launch_scan<T, 2, 4>(p, sms, stream);
+  if (p.dk <= 64) return launch_scan<T, 8, 4>(p, sms, stream);
+  if (p.dk <= 128) return launch_scan<T, 16, 4>(p, sms, stream);
+  return launch_scan<T, 16, 2>(p, sms, stream);  // 256 rows: a warp's registers hold 8 columns
 }
 
 }  // namespace

@@ -173,7 +173,6 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
   float* beta = glo + kC;
   float* M = reinterpret_cast<float*>(sk);
   uint8_t* dst;                                    // this chunk's and head's record
-  pdl_trigger();
   pdl_wait();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int slot = blockIdx.x, h = blockIdx.y;
@@ -484,7 +483,6 @@ __global__ void __launch_bounds__(kChainThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int h = blockIdx.y, b = blockIdx.z, kh = h / (p.H / p.Hk);
   const int col0 = blockIdx.x * kCols, rank = blockIdx.x % cs;
-  pdl_trigger();
   if (tid == 0) {
     for (int s = 0; s < kCStages; ++s) {
       mbar_init(&cfull[s], 1);
