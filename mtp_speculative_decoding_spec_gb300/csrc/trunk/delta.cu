@@ -115,20 +115,23 @@ struct Staged {
   static constexpr int bytes(int bufs) { return 2 * bufs * kQk + kV + 2 * kGroup * 4; }
 };
 
+// One warp to a block: no warp needs another, and warps that end make room one by one. Blocks an SM: as
+// many as the state's registers allow. With many requests it is the warps in flight that count (32
+// requests x 8 rows, replay: 29.6 us with eight, 24.1 with twelve).
+template <typename T, int NI>
+constexpr int kScanBlocks = NI >= 16 ? (sizeof(T) == 2 ? 11 : 10) : 16;
+
 template <typename T, int NI, int LV>
-__global__ void __launch_bounds__(128, 1) delta_scan_kernel(const __grid_constant__ DeltaParams p, int bufs) {
+__global__ void __launch_bounds__(32, kScanBlocks<T, NI>)
+    delta_scan_kernel(const __grid_constant__ DeltaParams p, int bufs) {
   using St = Staged<T, NI, LV>;
   extern __shared__ __align__(16) uint8_t smem[];
   pdl_wait();
   if (p.hdr && blockIdx.x == 0 && threadIdx.x == 0) p.hdr->error = 0;  // no wait here can set it
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x;
   const int tiles = (p.dv + 4 * LV - 1) / (4 * LV);
-  const int64_t wid = static_cast<int64_t>(blockIdx.x) * (blockDim.x / 32) + (threadIdx.x >> 5);
-  const int tile = static_cast<int>(wid % tiles);
-  const int64_t bh = wid / tiles;
-  const int h = static_cast<int>(bh % p.H);
-  if (bh / p.H >= p.B) return;  // whole warps; no block barrier follows
-  const int b = static_cast<int>(bh / p.H);
+  const int tile = blockIdx.x % tiles, bh = blockIdx.x / tiles;
+  const int h = bh % p.H, b = bh / p.H;
   const int kh = h / (p.H / p.Hk);
   const int col = tile * 4 * LV + (lane % LV) * 4;
   const int i0 = (lane / LV) * NI;
@@ -160,8 +163,7 @@ __global__ void __launch_bounds__(128, 1) delta_scan_kernel(const __grid_constan
     }
   }
   // the first group's rows and the state, all in flight together
-  uint8_t* mine = smem + (threadIdx.x >> 5) * St::bytes(bufs);
-  uint8_t* sv = mine + 2 * bufs * St::kQk;
+  uint8_t* sv = smem + 2 * bufs * St::kQk;
   float* sa = reinterpret_cast<float*>(sv + St::kV);
   float* sb = sa + kGroup;
   const T* qp = static_cast<const T*>(p.q) + row0 * p.qs + static_cast<int64_t>(kh) * p.dk;
@@ -172,7 +174,7 @@ __global__ void __launch_bounds__(128, 1) delta_scan_kernel(const __grid_constan
   float gn = 0.f, bn = 0.f;
   auto fetch = [&](int r0, int buf) {
     constexpr int kE = 16 / static_cast<int>(sizeof(T));
-    T* sq = reinterpret_cast<T*>(mine + 2 * buf * St::kQk);
+    T* sq = reinterpret_cast<T*>(smem + 2 * buf * St::kQk);
     T* sk = sq + kGroup * St::kP;
     if (p.vec_qk) {
       for (int i = lane; i < kGroup * St::kP / kE; i += 32) {
@@ -246,7 +248,7 @@ __global__ void __launch_bounds__(128, 1) delta_scan_kernel(const __grid_constan
       asm volatile("cp.async.wait_group 0;" ::: "memory");
     }
     __syncwarp();
-    const T* sq = reinterpret_cast<const T*>(mine + 2 * buf * St::kQk) + i0;
+    const T* sq = reinterpret_cast<const T*>(smem + 2 * buf * St::kQk) + i0;
     const T* sk = sq + kGroup * St::kP;
     const int rows = min(kGroup, n - r0);
     for (int r = 0; r < rows; ++r) {
@@ -302,6 +304,8 @@ __global__ void __launch_bounds__(128, 1) delta_scan_kernel(const __grid_constan
           for (int j = 0; j < 4; ++j) dst[j] = o4[j];
         }
       }
+      __syncwarp();  // so that the key is read anew: held since the dot products it would cost registers
+      kr.shared(sk + r * St::kP);
 #pragma unroll
       for (int ii = 0; ii < NI; ++ii) {
         const float kf = to_f(kr.e[ii]);
@@ -337,19 +341,16 @@ __global__ void __launch_bounds__(128, 1) delta_scan_kernel(const __grid_constan
 }
 
 template <typename T, int NI, int LV>
-cudaError_t launch_scan(const DeltaParams& p, int sms, cudaStream_t stream) {
+cudaError_t launch_scan(const DeltaParams& p, cudaStream_t stream) {
   static SmemAllowance allowed;
   const int64_t tiles = (p.dv + 4 * LV - 1) / (4 * LV);
-  const int64_t warps = tiles * p.H * p.B;
-  // few warps: one to a block, so that they spread over all SMs
-  const int per = warps <= 8 * static_cast<int64_t>(sms) ? 1 : 4;
-  const int64_t blocks = (warps + per - 1) / per;
+  const int64_t blocks = tiles * p.H * p.B;
   if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
   const int bufs = p.mode == DELTA_PREFILL ? 2 : 1;
-  const int smem = per * Staged<T, NI, LV>::bytes(bufs);
+  const int smem = Staged<T, NI, LV>::bytes(bufs);
   const cudaError_t e = allow_dynamic_smem(delta_scan_kernel<T, NI, LV>, smem, allowed);
   if (e != cudaSuccess) return e;
-  return launch_pdl(delta_scan_kernel<T, NI, LV>, dim3(static_cast<unsigned>(blocks)), dim3(32 * per), smem,
+  return launch_pdl(delta_scan_kernel<T, NI, LV>, dim3(static_cast<unsigned>(blocks)), dim3(32), smem,
                     stream, p, bufs);
 }
 
@@ -359,14 +360,14 @@ cudaError_t scan_of(const DeltaParams& p, int sms, cudaStream_t stream) {
   // is half as long for the same work in total.
   const int64_t warps = static_cast<int64_t>((p.dv + 15) / 16) * p.H * p.B;
   if (warps < 2 * sms && p.dk <= 128) {
-    if (p.dk <= 16) return launch_scan<T, 1, 2>(p, sms, stream);
-    if (p.dk <= 64) return launch_scan<T, 4, 2>(p, sms, stream);
-    return launch_scan<T, 8, 2>(p, sms, stream);
+    if (p.dk <= 16) return launch_scan<T, 1, 2>(p, stream);
+    if (p.dk <= 64) return launch_scan<T, 4, 2>(p, stream);
+    return launch_scan<T, 8, 2>(p, stream);
   }
-  if (p.dk <= 16) return launch_scan<T, 2, 4>(p, sms, stream);
-  if (p.dk <= 64) return launch_scan<T, 8, 4>(p, sms, stream);
-  if (p.dk <= 128) return launch_scan<T, 16, 4>(p, sms, stream);
-  return launch_scan<T, 16, 2>(p, sms, stream);  // 256 rows: a warp's registers hold 8 columns
+  if (p.dk <= 16) return launch_scan<T, 2, 4>(p, stream);
+  if (p.dk <= 64) return launch_scan<T, 8, 4>(p, stream);
+  if (p.dk <= 128) return launch_scan<T, 16, 4>(p, stream);
+  return launch_scan<T, 16, 2>(p, stream);  // 256 rows: a warp's registers hold 8 columns
 }
 
 }  // namespace
