@@ -43,8 +43,8 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kPad = 4;           // floats after a row of Q, K: rows start 16 bytes apart in the banks
 
 // 256 threads over a tile of 16 rows and blocks of 64 positions, all operands fp32 in shared memory.
-// Scores: thread (ty, tx) takes rows 2 ty, 2 ty + 1 and positions tx, tx + 32. Values: thread takes
-// four consecutive dims of four rows. A block in which some row's positions end takes only the
+// Scores: thread (ty, tx) takes rows 2 ty, 2 ty + 1 and positions tx, tx + 32. Values: a thread takes
+// four consecutive dims of one to four rows. A block in which some row's positions end takes only the
 // positions a row sees, one by one, so what a masked position holds reaches no row.
 template <typename T>
 __global__ void __launch_bounds__(kSimtThreads, 1)
@@ -60,7 +60,8 @@ __global__ void __launch_bounds__(kSimtThreads, 1)
   float* row_c = row_m + kSimtTm;
   float* row_l = row_c + kSimtTm;
   int* row_lim = reinterpret_cast<int*>(row_l + kSimtTm);
-  int32_t* cum = row_lim + kSimtTm;
+  int64_t* row_q = reinterpret_cast<int64_t*>(row_lim + kSimtTm);  // where the row's query lies
+  int32_t* cum = reinterpret_cast<int32_t*>(row_q + kSimtTm);
   attn_plan(p, cum);
   const AttnShares shares = attn_shares(p, cum);
   if (blockIdx.x == 0) attn_write_units(p, cum, shares);
@@ -68,21 +69,27 @@ __global__ void __launch_bounds__(kSimtThreads, 1)
   walk.start(p, shares);
   AttnPiece a;
   const int warp = tid >> 5, lane = tid & 31;
-  const int d0 = (tid & 63) * 4, r0 = (tid >> 6) * 4;  // values: dims and rows of this thread
+  // values: this thread's four dims of `rpt` (1..4) rows from r0; the fewer the dims, the fewer the rows
+  const int nd = D / 4, ng = min(kSimtTm, kSimtThreads / nd), rpt = (kSimtTm + ng - 1) / ng;
+  const int d0 = (tid % nd) * 4, r0 = tid / nd * rpt;
+  const bool holds = tid / nd < ng && r0 < kSimtTm;
   while (walk.next(p, cum, shares, a)) {
     const int head = a.head, slot = a.slot;
     __syncthreads();  // the previous piece's shared memory is no longer read
     if (tid < kSimtTm) {
-      row_lim[tid] = attn_row(p, a.tile, tid).lim;
+      const AttnRow ar = attn_row(p, a.tile, tid);
+      row_lim[tid] = ar.lim;
+      row_q[tid] = (static_cast<int64_t>(ar.b) * p.R + ar.r) * p.qs +
+                   static_cast<int64_t>(head * p.G + ar.g) * D;
       row_m[tid] = -INFINITY;
       row_l[tid] = 0.f;
     }
-    for (int i = tid; i < kSimtTm * D; i += kSimtThreads) {
-      const int r = i / D, d = i - r * D;
-      const AttnRow ar = attn_row(p, a.tile, r);
-      const int64_t at = (static_cast<int64_t>(ar.b) * p.R + ar.r) * p.qs +
-                         static_cast<int64_t>(head * p.G + ar.g) * D + d;
-      qs[r * ld + d] = ar.lim > 0 ? to_f(static_cast<const T*>(p.q)[at]) : 0.f;
+    __syncthreads();
+    {  // 16 threads a row
+      const int r = tid >> 4;
+      const T* src = static_cast<const T*>(p.q) + row_q[r];
+      const bool runs = row_lim[r] > 0;
+      for (int d = tid & 15; d < D; d += 16) qs[r * ld + d] = runs ? to_f(src[d]) : 0.f;
     }
     const bool pre = a.tile < p.npt;
     const int b = pre ? 0 : (a.tile - p.npt) / p.nown;
@@ -160,36 +167,45 @@ __global__ void __launch_bounds__(kSimtThreads, 1)
         }
       }
       __syncthreads();
-      if (d0 < D) {
-        const bool cut = p0 + kSimtBn > least;  // some running row's positions end in this block
+      if (holds) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float c = row_c[r0 + i];
+          if (i >= rpt) break;
+          const float c = row_c[min(r0 + i, kSimtTm - 1)];
 #pragma unroll
           for (int j = 0; j < 4; ++j) acc[i][j] *= c;
         }
         const int np = min(kSimtBn, most - p0);
-        for (int t = 0; t < np; ++t) {
+        const int all = max(0, min(np, least - p0));  // positions that every running row sees
+        auto add = [&](int t, int i, const float4& v) {
+          const float w = ps[min(r0 + i, kSimtTm - 1) * (kSimtBn + 1) + t];
+          acc[i][0] = fmaf(w, v.x, acc[i][0]);
+          acc[i][1] = fmaf(w, v.y, acc[i][1]);
+          acc[i][2] = fmaf(w, v.z, acc[i][2]);
+          acc[i][3] = fmaf(w, v.w, acc[i][3]);
+        };
+#pragma unroll 4
+        for (int t = 0; t < all; ++t) {
           const float4 v = *reinterpret_cast<const float4*>(vs + t * ld + d0);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            if (cut && p0 + t >= row_lim[r0 + i]) continue;
-            const float w = ps[(r0 + i) * (kSimtBn + 1) + t];
-            acc[i][0] = fmaf(w, v.x, acc[i][0]);
-            acc[i][1] = fmaf(w, v.y, acc[i][1]);
-            acc[i][2] = fmaf(w, v.z, acc[i][2]);
-            acc[i][3] = fmaf(w, v.w, acc[i][3]);
-          }
+          for (int i = 0; i < 4; ++i)
+            if (i < rpt) add(t, i, v);
+        }
+        for (int t = all; t < np; ++t) {
+          const float4 v = *reinterpret_cast<const float4*>(vs + t * ld + d0);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (i < rpt && p0 + t < row_lim[min(r0 + i, kSimtTm - 1)]) add(t, i, v);
         }
       }
     }
     __syncthreads();
     if (tid < kSimtTm)
       p.ml[static_cast<int64_t>(slot) * kSimtTm + tid] = make_float2(row_m[tid], row_l[tid]);
-    if (d0 < D) {
+    if (holds) {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        if (row_lim[r0 + i] > 0)
+        if (i < rpt && r0 + i < kSimtTm && row_lim[r0 + i] > 0)
           *reinterpret_cast<float4*>(p.o + (static_cast<int64_t>(slot) * kSimtTm + r0 + i) * D + d0) =
               make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
     }
@@ -330,7 +346,7 @@ template <typename T>
 cudaError_t simt_launch(const AttnParams& p, int grid, cudaStream_t stream) {
   static SmemAllowance allowed;
   const int floats = (kSimtTm + 2 * kSimtBn) * (p.D + kPad) + kSimtTm * (kSimtBn + 1) + 3 * kSimtTm;
-  const int smem = 4 * (floats + kSimtTm + p.items + 1);
+  const int smem = 4 * (floats + 3 * kSimtTm + p.items + 1);
   const cudaError_t e = allow_dynamic_smem(attn_simt_kernel<T>, smem, allowed);
   if (e != cudaSuccess) return e;
   return launch_pdl(attn_simt_kernel<T>, dim3(grid), dim3(kSimtThreads), smem, stream, p);
