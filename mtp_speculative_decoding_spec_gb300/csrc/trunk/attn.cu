@@ -66,7 +66,7 @@ __global__ void __launch_bounds__(kSimtThreads, 1)
   const AttnShares shares = attn_shares(p, cum);
   if (blockIdx.x == 0) attn_write_units(p, cum, shares);
   AttnWalk walk;
-  walk.start(p, shares);
+  walk.start(p, cum, shares);
   AttnPiece a;
   const int warp = tid >> 5, lane = tid & 31;
   // values: this thread's four dims of `rpt` (1..4) rows from r0; the fewer the dims, the fewer the rows

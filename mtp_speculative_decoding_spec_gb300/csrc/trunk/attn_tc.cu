@@ -1,14 +1,14 @@
 // Attention of the verify rows over a shared prefix and each request's own cache on the tcgen05
 // tensor cores: bf16, head_dim 64, 128 or 256. Units, pieces and partials as in trunk.cuh.
 //
-// Per block of kBn positions: S = Q K^T (Q in TMEM, 128 rows x kBn), a row's softmax by one thread
-// (TMEM lane = row, no shuffles), the weights as bf16 back into the columns of S, O += P V with P
+// Per block of kBn positions: S = Q K^T (Q in TMEM, 128 rows x kBn), a row's softmax by two
+// threads (TMEM lane = row, no shuffles), the weights as bf16 back into the columns of S, O += P V with P
 // in TMEM too and V as it lies in the cache (rows of positions: the B operand is N-major).
 //   * warp 0 loads K and V blocks by TMA; Q is gathered by the softmax threads into TMEM, so that
 //     its 128 rows are not read from shared memory again for every block;
 //   * warp 1 issues the MMAs: S of block i+1 goes out before O of block i, so the tensor pipe works
 //     on one while the softmax works on the other (two S buffers);
-//   * warps 2..5 do the softmax, warps 6 and 7 watch V (below). The reference a row's weights are taken against moves only when the
+//   * warps 4..11 do the softmax, two threads a row; warps 2 and 3 watch V (below). The reference a row's weights are taken against moves only when the
 //     row's maximum has grown by more than 2^8 (the weights stay below 256 and their sum and O are
 //     fp32, so nothing is lost), which makes rescaling O in TMEM rare.
 // Weights are rounded to bf16 for the tensor cores (2^-9 of each weight, as the outputs are); their
@@ -30,8 +30,11 @@ namespace spec {
 namespace {
 
 constexpr int kTm = 128;
-constexpr int kThreads = 8 * 32;  // producer, MMA, four softmax and two guard warps
-constexpr int kSoftThreads = 128;
+constexpr int kThreads = 12 * 32;  // producer, MMA and two guard warps, eight softmax warps
+constexpr int kSoftThreads = 256;
+// Registers a thread: launched with 168 (64,512 in all); the first four warps give to the softmax's
+// eight: 128 x 96 + 256 x 200 = 63,488.
+constexpr int kFewRegs = 152, kSoftRegs = 176;
 constexpr float kLazy = 8.f;
 
 template <int D>
@@ -124,6 +127,23 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
       "r"(r[30]), "r"(r[31])
       : "memory");
 }
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+template <int N>
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t* r) {
+  if constexpr (N == 16) {
+    tmem_st16(taddr, r);
+  } else {
+#pragma unroll
+    for (int j = 0; j < N / 32; ++j) tmem_st32(taddr + 32 * j, r + 32 * j);
+  }
+}
 __device__ __forceinline__ void tmem_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
@@ -180,8 +200,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* o_init = abort_flag + 1;      // [2] O holds something before the piece's first MMA on it
   volatile int* odd = abort_flag + 3;         // [NS][2]: a row sees a non-finite V of the stage
-  int* least_sm = const_cast<int*>(odd + 2 * NS);  // [2][4] per softmax warp
-  int32_t* cum = reinterpret_cast<int32_t*>(smem + Sh::kFixed + 512);
+  int* least_sm = const_cast<int*>(odd + 2 * NS);  // [2][4] per quarter of the rows
+  float* xch = reinterpret_cast<float*>(smem + Sh::kFixed + 512);  // [2][2][128] between a row's threads
+  int32_t* cum = reinterpret_cast<int32_t*>(xch + 4 * kTm);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -194,12 +215,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(&sfull[0], 1);
     mbar_init(&sfull[1], 1);
-    mbar_init(&pready[0], 4);
-    mbar_init(&pready[1], 4);
+    mbar_init(&pready[0], 8);
+    mbar_init(&pready[1], 8);
     mbar_init(&pvdone[0], 1);
     mbar_init(&pvdone[1], 1);
-    mbar_init(qready, 4);
-    mbar_init(meet, 4);
+    mbar_init(qready, 8);
+    mbar_init(meet, 8);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -215,12 +236,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (kPair) cluster_barrier();  // the barriers of both CTAs stand before either one's copies arrive
   const int rank = kPair ? blockIdx.x & 1 : 0;
   AttnWalk walk;
-  walk.start(p, shares);
+  walk.start(p, cum, shares);
   AttnPiece a;
   auto give_up = [&]() {
     atomicOr(&p.hdr->error, ERR_TC_WAIT);
     *abort_flag = 1;
   };
+
+  if (warp < 4)
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
+  else
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
 
   if (warp == 0) {
     // ------------------------------------------------------------------ TMA producer
@@ -319,11 +345,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok && lane == 0) give_up();
     }
-  } else if (warp >= 6) {
+  } else if (warp < 4) {
     // ------------------------------------------------------------------ guards of V
     // In a block where some running row's positions end, non-finite values of positions that no
     // row sees are cleared; those that a row does see are reported to the softmax.
-    const int gw = warp - 6;
+    const int gw = warp - 2;
     int it = 0;
     bool ok = true;
     while (ok && !__any_sync(0xffffffffu, *abort_flag) && walk.next(p, cum, shares, a)) {
@@ -395,7 +421,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!ok && lane == 0) give_up();
   } else {
     // ------------------------------------------------------------------ softmax
-    const int quad = warp & 3, row = quad * 32 + lane, st = threadIdx.x - 64;
+    // A row has two threads, in warps of the same lanes of TMEM: each takes half of a block's scores and
+    // half of O's dims. They tell each other the largest score of their halves once a block.
+    constexpr int CW = BN / 2, DH = D / 2;
+    const int quad = warp & 3, half = (warp - 4) >> 2, row = quad * 32 + lane, st = threadIdx.x - 128;
     const uint32_t trow = tmem + (static_cast<uint32_t>(quad * 32) << 16);
     const float scale = fabsf(p.scale_log2);
     int it = 0;
@@ -416,43 +445,41 @@ __global__ void __launch_bounds__(kThreads, 1)
       wait(meet, met & 1);
       ++met;
     };
-    // Q of a piece: this thread's row into its TMEM lane; a negative scale goes into Q's signs
+    // Both threads' numbers of a row. The two warps come here the same number of times whatever happens.
+    auto exchange = [&](float x, int buf) {
+      xch[(buf * 2 + half) * kTm + row] = x;
+      asm volatile("bar.sync %0, 64;" ::"r"(1 + quad) : "memory");
+      return xch[(buf * 2 + (half ^ 1)) * kTm + row];
+    };
+    // Q of a piece: this thread's half of its row into its TMEM lane; a negative scale goes into Q's signs
     int piece = 0, least = 0;
     AttnRow ar;
     auto load_q = [&](const AttnPiece& pc) {
       ar = attn_row(p, pc.tile, row);
       const uint32_t flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;
       const __nv_bfloat16* src = q_row<D>(p, pc, ar);
-      const bool vec = (reinterpret_cast<uintptr_t>(src) & 15u) == 0;
+      uint32_t w[DH / 2];
+      if (__all_sync(0xffffffffu, (reinterpret_cast<uintptr_t>(src) & 15u) == 0)) {
+        const uint4* from = reinterpret_cast<const uint4*>(src + half * DH);
+        uint4 x[DH / 8];
 #pragma unroll
-      for (int d = 0; d < D; d += 128) {  // up to 16 loads in flight
-        constexpr int kW = D < 128 ? 32 : 64;
-        uint32_t w[kW];
+        for (int c = 0; c < DH / 8; ++c) x[c] = __ldg(from + c);
 #pragma unroll
-        for (int c = 0; c < kW / 4; ++c) {
-          uint4 v = make_uint4(0u, 0u, 0u, 0u);
-          if (ar.lim > 0) {
-            if (vec) {
-              v = __ldg(reinterpret_cast<const uint4*>(src + d) + c);
-            } else {
-              const uint16_t* h = reinterpret_cast<const uint16_t*>(src + d) + c * 8;
-              v.x = h[0] | static_cast<uint32_t>(h[1]) << 16;
-              v.y = h[2] | static_cast<uint32_t>(h[3]) << 16;
-              v.z = h[4] | static_cast<uint32_t>(h[5]) << 16;
-              v.w = h[6] | static_cast<uint32_t>(h[7]) << 16;
-            }
-          }
-          w[4 * c] = v.x ^ flip, w[4 * c + 1] = v.y ^ flip;
-          w[4 * c + 2] = v.z ^ flip, w[4 * c + 3] = v.w ^ flip;
-        }
-        __syncwarp();
+        for (int c = 0; c < DH / 8; ++c)
+          w[4 * c] = x[c].x, w[4 * c + 1] = x[c].y, w[4 * c + 2] = x[c].z, w[4 * c + 3] = x[c].w;
+      } else {
+        const uint16_t* from = reinterpret_cast<const uint16_t*>(src + half * DH);
 #pragma unroll
-        for (int j = 0; j < kW / 32; ++j) tmem_st32(trow + Sh::kQ + d / 2 + 32 * j, w + 32 * j);
+        for (int c = 0; c < DH / 2; ++c) w[c] = from[2 * c] | static_cast<uint32_t>(from[2 * c + 1]) << 16;
       }
+      // rows that do not run have read row 0's
+#pragma unroll
+      for (int c = 0; c < DH / 2; ++c) w[c] = ar.lim > 0 ? w[c] ^ flip : 0u;
+      tmem_st<DH / 2>(trow + Sh::kQ + half * (DH / 2), w);
       tmem_st_wait();
       const int lo = __reduce_min_sync(0xffffffffu, ar.lim > 0 ? ar.lim : 0x7fffffff);
       int* lsm = least_sm + 4 * (piece & 1);
-      if (lane == 0) lsm[quad] = lo;
+      if (lane == 0 && half == 0) lsm[quad] = lo;
       if (st == 0) o_init[piece & 1] = 0;
       tc_fence_before();
       bar_soft();
@@ -472,31 +499,36 @@ __global__ void __launch_bounds__(kThreads, 1)
         wait(&sfull[it & 1], (it >> 1) & 1);
         tc_fence_after();
         const uint32_t ts = trow + Sh::kS + (it & 1) * BN;
-        float v[BN];
-#pragma unroll
-        for (int c = 0; c < BN / 64; ++c) tmem_ld64(ts + 64 * c, v + 64 * c);
-        const bool full = __all_sync(0xffffffffu, valid == BN);
+        float v[CW];
+        if constexpr (CW == 64)
+          tmem_ld64(ts + half * CW, v);
+        else
+          tmem_ld32(ts + half * CW, v);
+        const int mine = valid - half * CW;  // of this thread's scores
+        const bool full = __all_sync(0xffffffffu, mine >= CW);
         if (!full) {
 #pragma unroll
-          for (int j = 0; j < BN; ++j) v[j] = j < valid ? v[j] : -INFINITY;
+          for (int j = 0; j < CW; ++j) v[j] = j < mine ? v[j] : -INFINITY;
         }
         float mx[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
-        for (int j = 4; j < BN; ++j) mx[j & 3] = fmaxf(mx[j & 3], v[j]);
-        const float raw = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        for (int j = 4; j < CW; ++j) mx[j & 3] = fmaxf(mx[j & 3], v[j]);
+        float raw = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        // after this both threads have their scores, whose columns the weights overwrite
+        raw = fmaxf(raw, exchange(raw, it & 1));
         const float top = raw == -INFINITY ? -INFINITY : raw * scale;
         const bool grow = top > m + kLazy;  // from -Inf: at the first score
         const float mo = m;
         if (grow) m = top;
         const float ref = m == -INFINITY ? 0.f : m;
         float sum[4] = {0.f, 0.f, 0.f, 0.f};
-        uint32_t w[BN / 2];
+        uint32_t w[CW / 2];
 #pragma unroll
-        for (int j = 0; j < BN; j += 2) {
+        for (int j = 0; j < CW; j += 2) {
           float e0 = ex2(fmaf(v[j], scale, -ref)), e1 = ex2(fmaf(v[j + 1], scale, -ref));
           if (!full) {
-            e0 = j < valid ? e0 : 0.f;
-            e1 = j + 1 < valid ? e1 : 0.f;
+            e0 = j < mine ? e0 : 0.f;
+            e1 = j + 1 < mine ? e1 : 0.f;
           }
           sum[j & 3] += e0;
           sum[(j + 1) & 3] += e1;
@@ -504,8 +536,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const float c = grow ? ex2(mo - ref) : 1.f;  // ex2(-Inf) = 0
         l = l * c + ((sum[0] + sum[1]) + (sum[2] + sum[3]));
-#pragma unroll
-        for (int j = 0; j < BN / 64; ++j) tmem_st32(ts + 32 * j, w + 32 * j);
+        tmem_st<CW / 2>(ts + half * (CW / 2), w);
         const bool rescale = !first && __any_sync(0xffffffffu, grow);
         const int sg = it % NS;
         bool by_hand = false;
@@ -520,7 +551,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (rescale) {
 #pragma unroll 1
-          for (int d = 0; d < D; d += 32) {
+          for (int d = half * DH; d < half * DH + DH; d += 32) {
             float o[32];
             uint32_t u[32];
             tmem_ld32(trow + d, o);
@@ -533,10 +564,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint8_t* vt = sv + sg * Sh::kTile;
           const int from = max(0, from_all - blk * BN), nrow = BN - from;
           tmem_st_wait();
+          bar_soft();  // both halves of the weights are there
           // Some rows see non-finite values and some do not. Each row adds its own share of those
           // values to O (zero to begin with), then they are cleared for the tensor cores.
 #pragma unroll 1
-          for (int d = 0; d < D; d += 8) {
+          for (int d = half * DH; d < half * DH + DH; d += 8) {
             float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
             if (!first) tmem_ld8(trow + d, o);
             for (int pos = from; pos < BN; ++pos) {
@@ -602,9 +634,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       // the piece's partial
       wait(&pvdone[(it - 1) & 1], ((it - 1) >> 1) & 1);
       tc_fence_after();
-      if (lim > 0) p.ml[at] = make_float2(m, l);
+      l += exchange(l, it & 1);  // the buffer that the last block did not use
+      if (lim > 0 && half == 0) p.ml[at] = make_float2(m, l);
 #pragma unroll 1
-      for (int d = 0; d < D; d += 32) {
+      for (int d = half * DH; d < half * DH + DH; d += 32) {
         float o[32];
         tmem_ld32(trow + d, o);
         if (lim > 0) {
@@ -629,7 +662,7 @@ template <int D, bool kPair>
 spec_status launch_tc(const AttnParams& p, int grid, EncodeTiledFn encode, cudaStream_t stream) {
   using Sh = Shape<D>;
   static SmemAllowance allowed;
-  const int smem = Sh::kFixed + 512 + 4 * (p.items + 1) + 1024;
+  const int smem = Sh::kFixed + 512 + 16 * kTm + 4 * (p.items + 1) + 1024;
   if (allow_dynamic_smem(attn_tc_kernel<D, kPair>, smem, allowed) != cudaSuccess) return SPEC_ERR_CUDA;
   AttnMaps m;
   // dims inside a 64-dim panel, positions, panels (64 dims on), requests

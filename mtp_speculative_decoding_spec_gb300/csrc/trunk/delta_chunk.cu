@@ -389,7 +389,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
 // products meeting in shared memory instead, moves fewer bytes but took 2.16 us a chunk.)
 constexpr int kChainThreads = 12 * 32;  // three groups of four warps; two of the last do nothing
 // Registers a thread: launched with 168 (64,512 in all), then shared out again by group, 57,344 in use.
-constexpr int kChainRegs = 224, kOutRegs = 160, kLoadRegs = 64;
+constexpr int kChainRegs = 224, kOutRegs = 168, kLoadRegs = 104;
 constexpr int kCStages = 3, kOStages = 3;
 constexpr int kVTile = kC * kCols * 2;
 // Beside K (Q), whose tiles start on 1,024 bytes: T, vectors, V for the chain, scores and vectors for

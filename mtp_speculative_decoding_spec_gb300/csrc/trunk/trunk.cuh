@@ -171,58 +171,75 @@ struct AttnPiece {
   bool pair;
 };
 
-// One piece after another of a CTA's shares.
+// One piece after another of a CTA's shares. Only the start of a share is looked for; from there on the
+// next unit follows.
 struct AttnWalk {
-  int64_t x, x1;
-  bool pair;  // the pairs' part is being walked
-  __device__ __forceinline__ void start(const AttnParams& p, const AttnShares& s) {
+  int64_t left;        // costs of the share still to walk
+  int item, head, at;  // the unit, and where in its costs
+  bool pair;           // the pairs' part is being walked
+  __device__ __forceinline__ void seek(const AttnParams& p, const int32_t* cum, int64_t x, int64_t x1) {
+    left = x1 - x;
+    if (left <= 0) return;
+    int lo = 0, hi = p.items;  // cum[lo] Hkv <= x < cum[hi] Hkv
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (static_cast<int64_t>(cum[mid]) * p.Hkv <= x)
+        lo = mid;
+      else
+        hi = mid;
+    }
+    const int64_t rel = x - static_cast<int64_t>(cum[lo]) * p.Hkv;
+    item = lo;
+    head = static_cast<int>(rel / (cum[lo + 1] - cum[lo]));
+    at = static_cast<int>(rel - static_cast<int64_t>(head) * (cum[lo + 1] - cum[lo]));
+  }
+  __device__ __forceinline__ void start(const AttnParams& p, const int32_t* cum, const AttnShares& s) {
     pair = p.pair;
     if (pair) {
-      x = s.sp * (blockIdx.x / 2);
-      x1 = min(s.wp, x + s.sp);
+      const int64_t x = s.sp * (blockIdx.x / 2);
+      seek(p, cum, x, min(s.wp, x + s.sp));
     } else {
-      single(s);
+      single(p, cum, s);
     }
   }
-  __device__ __forceinline__ void single(const AttnShares& s) {
+  __device__ __forceinline__ void single(const AttnParams& p, const int32_t* cum, const AttnShares& s) {
     pair = false;
-    x = s.wp + s.s1 * blockIdx.x;
-    x1 = min(s.w, x + s.s1);
+    const int64_t x = s.wp + s.s1 * blockIdx.x;
+    seek(p, cum, x, min(s.w, x + s.s1));
   }
   __device__ __forceinline__ bool next(const AttnParams& p, const int32_t* cum, const AttnShares& s,
                                        AttnPiece& a) {
     for (;;) {
-      if (x >= x1) {
+      if (left <= 0) {
         if (!pair) return false;
-        single(s);
+        single(p, cum, s);
         continue;
       }
-      int lo = 0, hi = p.items;  // cum[lo] Hkv <= x < cum[hi] Hkv
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (static_cast<int64_t>(cum[mid]) * p.Hkv <= x)
-          lo = mid;
-        else
-          hi = mid;
+      const int cost = cum[item + 1] - cum[item];
+      if (at >= cost) {  // the next unit, past items without positions
+        at = 0;
+        if (++head == p.Hkv || cost == 0) {
+          head = 0;
+          ++item;
+        }
+        continue;
       }
-      const int cost = cum[lo + 1] - cum[lo];
-      const int64_t rel = x - static_cast<int64_t>(cum[lo]) * p.Hkv;
-      a.head = static_cast<int>(rel / cost);
-      const int v0 = static_cast<int>(rel - static_cast<int64_t>(a.head) * cost);
-      const int v1 = static_cast<int>(min(static_cast<int64_t>(cost), v0 + (x1 - x)));
-      x += v1 - v0;
+      const int v0 = at, v1 = static_cast<int>(min(static_cast<int64_t>(cost), v0 + left));
+      at = v1;
+      left -= v1 - v0;
       a.blk0 = max(0, v0 - p.over);
       a.blk1 = max(0, v1 - p.over);
       if (a.blk0 == a.blk1) continue;
-      const int u = lo * p.Hkv + a.head;
+      a.head = head;
+      const int u = item * p.Hkv + head;
       a.pair = pair;
-      a.tile = lo - p.npi + p.npt;
-      a.slot = s.base1 + static_cast<int>(blockIdx.x) + u - s.u1;
-      if (lo < p.npi) a.tile = lo;
       if (pair) {
         const int rank = blockIdx.x & 1;
-        a.tile = 2 * lo + rank < p.npt ? 2 * lo + rank : -1;
+        a.tile = 2 * item + rank < p.npt ? 2 * item + rank : -1;
         a.slot = 2 * (static_cast<int>(blockIdx.x) / 2 + u) + rank;
+      } else {
+        a.tile = item < p.npi ? item : item - p.npi + p.npt;
+        a.slot = s.base1 + static_cast<int>(blockIdx.x) + u - s.u1;
       }
       return true;
     }

@@ -173,7 +173,7 @@ def test_register_budget_and_no_spills(spec):
     logs = glob.glob(os.path.join(ROOT, "mtp_speculative_decoding_spec_gb300", "_build", "trunk",
                                   "*.ptxas.log"))
     threads = {"delta_scan_kernel": 32, "delta_prep_kernel": 128, "delta_chain_kernel": 384, "attn_simt_kernel": 256, "attn_join_kernel": 256,
-               "attn_tc_kernel": 256}
+               "attn_tc_kernel": 384}
     seen = 0
     for path in logs:
         name = None
