@@ -388,9 +388,10 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
 // that its other operand waits for. (S kept in registers as the next chunk's operand, its four partial
 // products meeting in shared memory instead, moves fewer bytes but took 2.16 us a chunk.)
 constexpr int kChainThreads = 12 * 32;  // three groups of four warps; two of the last do nothing
-// Registers a thread: launched with 168 (64,512 in all), then shared out again by group, 57,344 in use.
+// Registers a thread: launched with 168 (64,512 in all), then shared out again by group, 63,488 in use.
 constexpr int kChainRegs = 224, kOutRegs = 168, kLoadRegs = 104;
 constexpr int kCStages = 3, kOStages = 3;
+constexpr int kSortMost = 256;  // requests that are put in order
 constexpr int kVTile = kC * kCols * 2;
 // Beside K (Q), whose tiles start on 1,024 bytes: T, vectors, V for the chain, scores and vectors for
 // the outputs.
@@ -481,7 +482,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
   uint64_t* ofull = cempty + kCStages;
   uint64_t* oempty = ofull + kOStages;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int h = blockIdx.y, b = blockIdx.z, kh = h / (p.H / p.Hk);
+  const int h = blockIdx.y, kh = h / (p.H / p.Hk);
   const int col0 = blockIdx.x * kCols, rank = blockIdx.x % cs;
   if (tid == 0) {
     for (int s = 0; s < kCStages; ++s) {
@@ -497,6 +498,22 @@ __global__ void __launch_bounds__(kChainThreads, 1)
   __syncthreads();
   asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
   pdl_wait();
+  // The longest request first: blocks are dealt out in order, and what starts last should be short.
+  int b = blockIdx.z;
+  if (p.B > 1 && p.B <= kSortMost) {
+    int* lens = reinterpret_cast<int*>(sps);
+    int* pick = lens + kSortMost;
+    for (int i = tid; i < p.B; i += kChainThreads) lens[i] = cu_at(p, i + 1) - cu_at(p, i);
+    __syncthreads();
+    for (int i = tid; i < p.B; i += kChainThreads) {
+      int before = 0;
+      for (int j = 0; j < p.B; ++j) before += lens[j] > lens[i] || (lens[j] == lens[i] && j < i);
+      if (before == static_cast<int>(blockIdx.z)) *pick = i;
+    }
+    __syncthreads();
+    b = __shfl_sync(0xffffffffu, *pick, 0);
+    __syncthreads();  // the place is used otherwise from here on
+  }
   const int c0 = cu_at(p, b), c1 = max(c0, cu_at(p, b + 1));
   const int n = (c1 - c0 + kC - 1) / kC;
   const int64_t elems = static_cast<int64_t>(p.layers) * p.H * p.dk * p.dv;
