@@ -69,7 +69,7 @@ spec_status delta_params(const spec_state_desc* st, int32_t layer, const spec_de
 
 // Attention: the tile sizes of the kernel that takes the call, and the workspace's layout.
 struct AttnPlan {
-  int tc, tm, bn, npt, npi, pair, nown, items, grid;
+  int tc, tm, bn, npt, npi, grp, nown, items, grid;
   size_t units, ml, o, total;
 };
 
@@ -105,9 +105,9 @@ spec_status attn_plan_of(int32_t B, int32_t R, const spec_state_desc* st, const 
   const bool prefix = d->prefix_k && d->prefix_capacity > 0;
   const int64_t npt = prefix ? (B * per + w.tm - 1) / w.tm : 0;
   const int64_t nown = (per + w.tm - 1) / w.tm;
-  // two tiles of rows or more: pairs of CTAs take them two by two and share what they load of the prefix
-  w.pair = w.tc && npt >= 2 && a.sms % 2 == 0;
-  const int64_t npi = w.pair ? (npt + 1) / 2 : npt;
+  const int64_t sets = (npt + kAttnGroup - 1) / kAttnGroup;
+  w.grp = w.tc && npt >= 2 ? static_cast<int>((npt + sets - 1) / sets) : 1;
+  const int64_t npi = (npt + w.grp - 1) / w.grp;
   const int64_t items = npi + B * nown;
   const int64_t blocks = npi * ((prefix ? d->prefix_capacity : 0) / w.bn + 1 + kAttnOver) +
                          B * nown * (st->kv_capacity / w.bn + 1 + kAttnOver);
@@ -118,7 +118,7 @@ spec_status attn_plan_of(int32_t B, int32_t R, const spec_state_desc* st, const 
   w.items = static_cast<int>(items);
   w.grid = a.sms;
   const size_t slots = 2 * static_cast<size_t>(w.grid) +
-                       static_cast<size_t>(items + (w.pair ? npi : 0)) * d->kv_heads;
+                       static_cast<size_t>(npi * w.grp + items - npi) * d->kv_heads;
   w.units = sizeof(WsHeader);
   w.ml = w.units + align_up(sizeof(int2) * static_cast<size_t>(items) * d->kv_heads, 256);
   w.o = w.ml + align_up(slots * w.tm * sizeof(float2), 256);
@@ -240,7 +240,7 @@ spec_status spec_prefix_attention(int32_t B, int32_t R, const spec_state_desc* s
   p.bn = w.bn;
   p.npt = w.npt;
   p.npi = w.npi;
-  p.pair = w.pair;
+  p.grp = w.grp;
   p.over = kAttnOver;
   p.nown = w.nown;
   p.items = w.items;

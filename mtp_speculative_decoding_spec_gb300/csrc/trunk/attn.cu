@@ -235,9 +235,9 @@ __global__ void __launch_bounds__(NW == 1 ? 128 : 32 * NW)
   const int rows = attn_rows(p, b);
   int2 u0 = make_int2(0, 0);
   const int t0 = s / p.tm;
-  if (p.npt > 0) u0 = __ldcg(p.units + (t0 >> p.pair) * p.Hkv + head);
+  if (p.npt > 0) u0 = __ldcg(p.units + t0 / p.grp * p.Hkv + head);
   int2 u1 = __ldcg(p.units + (p.npi + b * p.nown + x / p.tm) * p.Hkv + head);
-  if (p.pair) u0.x += t0 & 1;
+  u0.x += t0 % p.grp;
   if (p.npt > 0 && attn_prefix(p, b) == 0) u0.y = 0;
   if (r >= rows) u0.y = u1.y = 0;
   const int at0 = s % p.tm, at1 = x % p.tm, ntot = u0.y + u1.y;
@@ -254,7 +254,7 @@ __global__ void __launch_bounds__(NW == 1 ? 128 : 32 * NW)
       ov[j][0] = ov[j][1] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (i < ntot) {
         const bool pre = i < u0.y;
-        const int64_t t = static_cast<int64_t>(pre ? u0.x + (i << p.pair) : u1.x + i - u0.y) * p.tm +
+        const int64_t t = static_cast<int64_t>(pre ? u0.x + i * p.grp : u1.x + i - u0.y) * p.tm +
                           (pre ? at0 : at1);
         mlv[j] = __ldcg(p.ml + t);
         const float4* o = reinterpret_cast<const float4*>(p.o + t * p.D);
@@ -365,7 +365,7 @@ cudaError_t attn_simt_launch(const AttnParams& p, spec_dtype dtype, int grid, cu
 cudaError_t attn_join_launch(const AttnParams& p, spec_dtype dtype, int sms, cudaStream_t stream) {
   const int64_t rows = static_cast<int64_t>(p.B) * p.R * p.Hkv * p.G;
   if (rows > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  const bool many = rows >= 4 * static_cast<int64_t>(sms);
+  const bool many = rows >= 6 * static_cast<int64_t>(sms);
   const dim3 g(static_cast<unsigned>(many ? (rows + 3) / 4 : rows)), t(many ? 128 : 256);
   if (dtype == SPEC_BF16)
     return many ? launch_pdl(attn_join_kernel<__nv_bfloat16, 1>, g, t, 0, stream, p)

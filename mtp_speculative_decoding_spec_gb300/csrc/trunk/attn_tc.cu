@@ -49,28 +49,17 @@ struct Shape {
   static_assert(kQ + D / 2 <= 512, "TMEM");
 };
 
-// A block of K or V at once: [panel of 64 dims][position][64 dims], the order of its map's box. `both`:
-// to the same place in both CTAs of the pair, with the bytes counted on each one's barrier. Called by
-// a whole warp, one lane of which issues; `expect` are the bytes that this CTA's barrier waits for.
+// A block of K or V at once: [panel of 64 dims][position][64 dims], the order of its map's box. Called
+// by a whole warp, one lane of which issues.
 __device__ __forceinline__ void tma_load_block(void* dst, const CUtensorMap* map, int pos, int panel,
-                                               int b, uint64_t* bar, uint32_t expect, bool both) {
-  if (both)
-    asm volatile(
-        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
-        "@e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%5], %6;\n\t"
-        "@e cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        ".multicast::cluster [%0], [%1, {%7, %2, %3, %4}], [%5], %8;\n\t}" ::"r"(smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(pos), "r"(panel), "r"(b), "r"(smem_u32(bar)),
-        "r"(expect), "r"(0), "h"(static_cast<uint16_t>(3))
-        : "memory");
-  else
-    asm volatile(
+                                               int b, uint64_t* bar, uint32_t bytes) {
+  asm volatile(
         "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
         "@e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%5], %6;\n\t"
         "@e cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
         " [%0], [%1, {%7, %2, %3, %4}], [%5];\n\t}" ::"r"(smem_u32(dst)),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(pos), "r"(panel), "r"(b), "r"(smem_u32(bar)),
-        "r"(expect), "r"(0)
+        "r"(bytes), "r"(0)
         : "memory");
 }
 
@@ -101,18 +90,6 @@ __device__ __forceinline__ void tc_commit_elect(uint64_t* bar) {
       "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
           smem_u32(bar))
       : "memory");
-}
-
-__device__ __forceinline__ void tc_commit_both(uint64_t* bar) {  // on both CTAs' barriers
-  asm volatile(
-      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
-      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
-      " [%0], %1;\n\t}" ::"r"(smem_u32(bar)),
-      "h"(static_cast<uint16_t>(3))
-      : "memory");
-}
-__device__ __forceinline__ void cluster_barrier() {
-  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
 
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
@@ -174,7 +151,7 @@ struct AttnMaps {
   CUtensorMap pk, pv, ok, ov;
 };
 
-template <int D, bool kPair>
+template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_tc_kernel(const __grid_constant__ AttnMaps maps, const __grid_constant__ AttnParams p) {
   using Sh = Shape<D>;
@@ -208,9 +185,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < NS; ++s) {
       mbar_init(&kfull[s], 1);
-      mbar_init(&kempty[s], kPair ? 2 : 1);
+      mbar_init(&kempty[s], 1);
       mbar_init(&vfull[s], 1);
-      mbar_init(&vempty[s], kPair ? 2 : 1);
+      mbar_init(&vempty[s], 1);
       mbar_init(&vok[s], 2);
     }
     mbar_init(&sfull[0], 1);
@@ -233,8 +210,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
   const AttnShares shares = attn_shares(p, cum);
   if (blockIdx.x == 0) attn_write_units(p, cum, shares);
-  if (kPair) cluster_barrier();  // the barriers of both CTAs stand before either one's copies arrive
-  const int rank = kPair ? blockIdx.x & 1 : 0;
   AttnWalk walk;
   walk.start(p, cum, shares);
   AttnPiece a;
@@ -253,18 +228,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     int it = 0;  // V blocks; K runs one block ahead, as the MMAs take them
     bool ok = true;
     while (ok && !__any_sync(0xffffffffu, *abort_flag) && walk.next(p, cum, shares, a)) {
-      const bool both = kPair && a.pair, pre = both || a.tile < p.npt;
+      const bool pre = a.tile < p.npt;
       const int b = pre ? 0 : (a.tile - p.npt) / p.nown, panel = a.head * (D / 64);
-      // in pairs, each CTA loads half of the block's panels (of its positions, if it has one panel)
-      const int half = both ? rank * (Sh::kTile / 2) : 0;
-      const int dpos = both && D == 64 ? rank * (BN / 2) : 0, dpan = both && D > 64 ? rank * (D / 128) : 0;
       auto load = [&](uint8_t* tiles, uint64_t* full, uint64_t* empty, const CUtensorMap* map, int i,
                       int blk) {
         const int s = i % NS;
         if (i >= NS && !__all_sync(0xffffffffu, mbar_wait_bounded(&empty[s], ((i / NS) & 1) ^ 1)))
           return false;
-        tma_load_block(tiles + s * Sh::kTile + half, map, blk * BN + dpos, panel + dpan, b, &full[s],
-                       Sh::kTile, both);
+        tma_load_block(tiles + s * Sh::kTile, map, blk * BN, panel, b, &full[s], Sh::kTile);
         return true;
       };
       const CUtensorMap* mk = pre ? &maps.pk : &maps.ok;
@@ -278,15 +249,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       it += n;
     }
     if (!ok && lane == 0) give_up();
-    // leave nothing in flight: the last loads of every stage have landed, and in pairs the other CTA's
-    // arrivals on this one's barriers
+    // leave nothing in flight: the last loads of every stage have landed
     for (int j = max(0, it - NS); j < it; ++j) {
       mbar_wait_bounded(&kfull[j % NS], (j / NS) & 1);
       mbar_wait_bounded(&vfull[j % NS], (j / NS) & 1);
-      if (kPair) {
-        mbar_wait_bounded(&kempty[j % NS], (j / NS) & 1);
-        mbar_wait_bounded(&vempty[j % NS], (j / NS) & 1);
-      }
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------------ MMA issuer
@@ -297,15 +263,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t vd0 = smem_desc_n_major(smem_u32(sv), Sh::kPanel);
       int it = 0, piece = 0;
       bool ok = true;
-      // a stage is free when both CTAs of a pair have read it
-      auto free_stage = [&](uint64_t* bar) {
-        if (kPair && a.pair) {
-          tc_commit_both(bar);
-        } else {
-          tc_commit_elect(bar);
-          if (kPair) tc_commit_elect(bar);
-        }
-      };
       auto scores = [&](int i) {
         if (!__all_sync(0xffffffffu, mbar_wait_bounded(&kfull[i % NS], (i / NS) & 1))) return false;
         tc_fence_after();
@@ -316,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_mma_ta(ds, tmem + Sh::kQ + kk * 8,
                     desc_advance(kd, (kk / 4) * Sh::kPanel + (kk % 4) * 32), kIdS, kk > 0);
         tc_commit_elect(&sfull[i & 1]);
-        free_stage(&kempty[i % NS]);
+        tc_commit_elect(&kempty[i % NS]);
         return true;
       };
       while (ok && !__any_sync(0xffffffffu, *abort_flag) && walk.next(p, cum, shares, a)) {
@@ -337,7 +294,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int kk = 0; kk < BN / 16; ++kk)
             tc_mma_ta(tmem, ps + kk * 8, desc_advance(vd, kk * 2048), kIdO, kk > 0 ? 1u : acc0);
-          free_stage(&vempty[i % NS]);
+          tc_commit_elect(&vempty[i % NS]);
           tc_commit_elect(&pvdone[i & 1]);
         }
         it += n;
@@ -655,23 +612,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
-  if (kPair) cluster_barrier();  // the other CTA's copies and arrivals still come to this one's memory
 }
 
-template <int D, bool kPair>
+template <int D>
 spec_status launch_tc(const AttnParams& p, int grid, EncodeTiledFn encode, cudaStream_t stream) {
   using Sh = Shape<D>;
   static SmemAllowance allowed;
   const int smem = Sh::kFixed + 512 + 16 * kTm + 4 * (p.items + 1) + 1024;
-  if (allow_dynamic_smem(attn_tc_kernel<D, kPair>, smem, allowed) != cudaSuccess) return SPEC_ERR_CUDA;
+  if (allow_dynamic_smem(attn_tc_kernel<D>, smem, allowed) != cudaSuccess) return SPEC_ERR_CUDA;
   AttnMaps m;
   // dims inside a 64-dim panel, positions, panels (64 dims on), requests
-  const cuuint32_t whole[4] = {64, static_cast<cuuint32_t>(Sh::kBn), D / 64, 1};
-  const cuuint32_t half[4] = {64, static_cast<cuuint32_t>(D == 64 ? Sh::kBn / 2 : Sh::kBn),
-                              D == 64 ? 1 : D / 128, 1};
+  const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(Sh::kBn), D / 64, 1};
   const cuuint32_t es[4] = {1, 1, 1, 1};
   const auto map = [&](CUtensorMap* t, const uint8_t* base, int64_t positions, int64_t step, int64_t reqs,
-                       int64_t req_step, const cuuint32_t* box) {
+                       int64_t req_step) {
     const cuuint64_t dim[4] = {64, static_cast<cuuint64_t>(positions),
                                static_cast<cuuint64_t>(p.Hkv) * (D / 64), static_cast<cuuint64_t>(reqs)};
     const cuuint64_t stride[3] = {static_cast<cuuint64_t>(step), 128, static_cast<cuuint64_t>(req_step)};
@@ -680,34 +634,16 @@ spec_status launch_tc(const AttnParams& p, int grid, EncodeTiledFn encode, cudaS
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
   };
   const int64_t req = p.B > 1 ? p.kreq : p.krow;
-  if (!map(&m.ok, p.kk, p.kcap, p.krow, p.B, req, whole) || !map(&m.ov, p.kv, p.kcap, p.krow, p.B, req, whole))
+  if (!map(&m.ok, p.kk, p.kcap, p.krow, p.B, req) || !map(&m.ov, p.kv, p.kcap, p.krow, p.B, req))
     return SPEC_ERR_CUDA;
   m.pk = m.ok;
   m.pv = m.ov;
-  if (p.npt > 0 && (!map(&m.pk, p.pk, p.pcap, p.pstride, 1, p.pstride, kPair ? half : whole) ||
-                    !map(&m.pv, p.pv, p.pcap, p.pstride, 1, p.pstride, kPair ? half : whole)))
+  if (p.npt > 0 && (!map(&m.pk, p.pk, p.pcap, p.pstride, 1, p.pstride) ||
+                    !map(&m.pv, p.pv, p.pcap, p.pstride, 1, p.pstride)))
     return SPEC_ERR_CUDA;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = 2;
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = kPair ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, attn_tc_kernel<D, kPair>, m, p) == cudaSuccess ? SPEC_OK
-                                                                                : SPEC_ERR_CUDA;
-}
-
-template <int D>
-spec_status launch_of(const AttnParams& p, int grid, EncodeTiledFn encode, cudaStream_t stream) {
-  return p.pair ? launch_tc<D, true>(p, grid, encode, stream)
-                : launch_tc<D, false>(p, grid, encode, stream);
+  return launch_pdl(attn_tc_kernel<D>, dim3(grid), dim3(kThreads), smem, stream, m, p) == cudaSuccess
+             ? SPEC_OK
+             : SPEC_ERR_CUDA;
 }
 
 }  // namespace
@@ -717,9 +653,9 @@ int attn_tc_tm() { return kTm; }
 int attn_tc_bn(int head_dim) { return head_dim == 256 ? Shape<256>::kBn : Shape<128>::kBn; }
 
 spec_status attn_tc_launch(const AttnParams& p, int grid, EncodeTiledFn encode, cudaStream_t stream) {
-  return p.D == 256   ? launch_of<256>(p, grid, encode, stream)
-         : p.D == 128 ? launch_of<128>(p, grid, encode, stream)
-                      : launch_of<64>(p, grid, encode, stream);
+  return p.D == 256   ? launch_tc<256>(p, grid, encode, stream)
+         : p.D == 128 ? launch_tc<128>(p, grid, encode, stream)
+                      : launch_tc<64>(p, grid, encode, stream);
 }
 
 }  // namespace spec

@@ -100,9 +100,7 @@ struct Raw {
 
 constexpr int kGroup = 8;  // rows staged at once
 
-template <int kBytes>
 __device__ __forceinline__ void copy_async16(void* dst, const void* src) {
-  static_assert(kBytes == 16, "one vector");
   asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
 
@@ -180,8 +178,8 @@ __global__ void __launch_bounds__(32, kScanBlocks<T, NI>)
       for (int i = lane; i < kGroup * St::kP / kE; i += 32) {
         const int r = i / (St::kP / kE), d = (i % (St::kP / kE)) * kE;
         if (r0 + r < n && d < p.dk) {
-          copy_async16<16>(sq + r * St::kP + d, qp + (r0 + r) * p.qs + d);
-          copy_async16<16>(sk + r * St::kP + d, kp + (r0 + r) * p.ks + d);
+          copy_async16(sq + r * St::kP + d, qp + (r0 + r) * p.qs + d);
+          copy_async16(sk + r * St::kP + d, kp + (r0 + r) * p.ks + d);
         } else {
           *reinterpret_cast<uint4*>(sq + r * St::kP + d) = make_uint4(0u, 0u, 0u, 0u);
           *reinterpret_cast<uint4*>(sk + r * St::kP + d) = make_uint4(0u, 0u, 0u, 0u);

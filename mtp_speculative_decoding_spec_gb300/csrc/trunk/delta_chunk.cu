@@ -86,9 +86,6 @@ __device__ __forceinline__ void split(float x, float y, uint32_t* w) {
   }
 }
 
-struct Span {  // a chunk's request, first row and number of rows
-  int b, row0, len;
-};
 __device__ __forceinline__ int cu_at(const DeltaParams& p, int b) {
   return static_cast<int>(max(static_cast<int64_t>(0),
                               min(static_cast<int64_t>(p.cu_rows[b]), p.rows)));

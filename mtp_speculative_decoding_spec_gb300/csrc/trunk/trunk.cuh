@@ -44,14 +44,16 @@ spec_status delta_chunk_launch(const DeltaParams& p, void* workspace, EncodeTile
 // is cut into blocks of `bn` positions; the blocks of all units in a row are dealt out evenly to
 // the grid, and each (CTA, unit) that meet leave one partial (max, sum, unnormalised output) in a
 // slot of their own. Item = a tile of rows for all KV heads: prefix tiles first, then own tiles.
-// With `pair`, prefix items are two tiles each and go to pairs of CTAs, one tile to a CTA, before the
-// own items go to single CTAs. `over` is what starting a unit costs, in blocks: it counts in the
-// dealing as if the unit began with that many blocks more.
+// With `grp` > 1, prefix items are `grp` tiles each and are dealt to groups of as many neighbouring
+// CTAs, a tile to a CTA, before the own items are dealt to single CTAs: a group walks the same
+// positions at the same pace, so the prefix comes from HBM once and from L2 for the others. `over` is
+// what starting a unit costs, in blocks: it counts in the dealing as if the unit began with that many
+// blocks more.
 struct AttnParams {
   int B, R, G, Hkv, D;
   int tm, bn;
   int npt, npi, nown, items;  // prefix tiles and items, own tiles per request, npi + B * nown
-  int pair, over;
+  int grp, over;
   const void* q;
   int64_t qs;
   void* out;
@@ -72,7 +74,8 @@ struct AttnParams {
 };
 
 constexpr int kAttnMaxItems = 8192;
-constexpr int kAttnOver = 2;  // see `over`
+constexpr int kAttnOver = 6;    // see `over`
+constexpr int kAttnGroup = 16;  // most of `grp`
 
 // Rows of request b that run.
 __device__ __forceinline__ int attn_rows(const AttnParams& p, int b) {
@@ -95,7 +98,7 @@ __device__ __forceinline__ void attn_plan(const AttnParams& p, int32_t* cum) {
   for (int i = tid; i < p.items; i += nt) {
     int n = 0;
     if (i < p.npi) {
-      const int span = p.tm << p.pair;
+      const int span = p.tm * p.grp;
       const int b0 = i * span / per, b1 = min(p.B - 1, ((i + 1) * span - 1) / per);
       for (int b = b0; b <= b1; ++b)
         if (attn_rows(p, b) > 0) n = max(n, attn_prefix(p, b));
@@ -126,26 +129,55 @@ __device__ __forceinline__ void attn_plan(const AttnParams& p, int32_t* cum) {
   __syncthreads();
 }
 
-// How the costs are dealt out: the pairs' part [0, wp), `sp` to each pair of CTAs, and the rest up to
-// w, `s1` to each CTA; where the second part's slots begin.
+// How the costs are dealt out: the groups' part [0, wp), `sp` to each group, and the rest up to w: `s1`
+// to each of the `in` CTAs in groups, `s2` to each of the others, which have that much more room; where
+// the second part's units and slots begin.
 struct AttnShares {
-  int64_t wp, w, sp, s1;
-  int u1, base1;
+  int64_t wp, w, sp, s1, s2;
+  int in, u1, base1;
+  __device__ __forceinline__ int64_t single_at(int cta) const {  // where a CTA's part of the rest begins
+    return cta < in ? s1 * cta : s1 * in + s2 * (cta - in);
+  }
+  __device__ __forceinline__ int single_cta(int64_t x) const {  // which CTA has place x of the rest
+    return static_cast<int>(x < s1 * in ? x / s1 : in + (x - s1 * in) / s2);
+  }
+  // With so many groups: the shares, and what the CTA with the most then has. A second unit's start
+  // comes on top where the groups' CTAs take some of the rest too.
+  __device__ __forceinline__ int64_t split(const AttnParams& p, int groups, int grid) {
+    in = groups * p.grp;
+    sp = (wp + groups - 1) / groups;
+    const int64_t rest = w - wp, more = rest - sp * (grid - in);
+    s1 = more > 0 ? (more + grid - 1) / grid : 0;
+    s2 = more > 0 ? s1 + sp : in < grid ? (rest + grid - in - 1) / (grid - in) : 0;
+    return s1 > 0 ? sp + s1 + p.over : max(sp, s2);
+  }
 };
 __device__ __forceinline__ AttnShares attn_shares(const AttnParams& p, const int32_t* cum) {
   AttnShares s;
   const int grid = gridDim.x;
   s.w = static_cast<int64_t>(cum[p.items]) * p.Hkv;
-  s.wp = p.pair ? static_cast<int64_t>(cum[p.npi]) * p.Hkv : 0;
-  s.sp = p.pair ? (s.wp + grid / 2 - 1) / (grid / 2) : 0;
-  s.s1 = (s.w - s.wp + grid - 1) / grid;
-  s.u1 = p.pair ? p.npi * p.Hkv : 0;
-  s.base1 = p.pair ? 2 * (grid / 2 + s.u1) : 0;
+  s.wp = s.sp = 0;
+  s.in = 0;
+  int groups = 0;
+  if (p.grp > 1) {
+    // as many groups as the prefix is of the work, so that a CTA has one kind of work, or one more
+    s.wp = static_cast<int64_t>(cum[p.npi]) * p.Hkv;
+    const int64_t all = s.wp * p.grp + s.w - s.wp;
+    const int most = grid / p.grp;
+    groups = all > 0 ? max(1, static_cast<int>(s.wp * grid / all)) : 1;
+    const int64_t fewer = s.split(p, groups, grid);
+    if (groups < most && s.split(p, groups + 1, grid) < fewer) ++groups;
+    s.split(p, groups, grid);
+  } else {
+    s.s1 = s.s2 = (s.w + grid - 1) / grid;
+  }
+  s.u1 = p.grp > 1 ? p.npi * p.Hkv : 0;
+  s.base1 = p.grp * (groups + s.u1);
   return s;
 }
 
-// Each unit's first slot and number of partials (the slots of a pair's tile lie two apart, the second
-// tile's one on), for the join; by CTA 0 of the kernel that computes them.
+// Each unit's first slot and number of partials (the slots of a group's tile lie `grp` apart), for the
+// join; by CTA 0 of the kernel that computes them.
 __device__ __forceinline__ void attn_write_units(const AttnParams& p, const int32_t* cum,
                                                  const AttnShares& s) {
   for (int u = threadIdx.x; u < p.items * p.Hkv; u += blockDim.x) {
@@ -154,21 +186,22 @@ __device__ __forceinline__ void attn_write_units(const AttnParams& p, const int3
     int2 v = make_int2(0, 0);
     if (cost > 0) {
       const int64_t x = static_cast<int64_t>(cum[item]) * p.Hkv + static_cast<int64_t>(head) * cost;
-      const bool pair = u < s.u1;
-      const int64_t at = pair ? x : x - s.wp, share = pair ? s.sp : s.s1;
-      const int c0 = static_cast<int>((at + p.over) / share);
-      v.y = static_cast<int>((at + cost - 1) / share) - c0 + 1;
-      v.x = pair ? 2 * (c0 + u) : s.base1 + c0 + u - s.u1;
+      const int64_t first = x + p.over, last = x + cost - 1;  // places of its first and last block
+      if (u < s.u1) {
+        const int c0 = static_cast<int>(first / s.sp);
+        v = make_int2(p.grp * (c0 + u), static_cast<int>(last / s.sp) - c0 + 1);
+      } else {
+        const int c0 = s.single_cta(first - s.wp);
+        v = make_int2(s.base1 + c0 + u - s.u1, s.single_cta(last - s.wp) - c0 + 1);
+      }
     }
     p.units[u] = v;
   }
 }
 
-// A CTA's piece of one unit: its tile of rows (prefix tiles, then own tiles; -1: none, the other CTA
-// of the pair has the last tile), KV head, blocks and slot.
+// A CTA's piece of one unit: its tile of rows (prefix tiles, then own tiles), KV head, blocks and slot.
 struct AttnPiece {
   int tile, head, blk0, blk1, slot;
-  bool pair;
 };
 
 // One piece after another of a CTA's shares. Only the start of a share is looked for; from there on the
@@ -176,7 +209,7 @@ struct AttnPiece {
 struct AttnWalk {
   int64_t left;        // costs of the share still to walk
   int item, head, at;  // the unit, and where in its costs
-  bool pair;           // the pairs' part is being walked
+  bool group;          // the groups' part is being walked
   __device__ __forceinline__ void seek(const AttnParams& p, const int32_t* cum, int64_t x, int64_t x1) {
     left = x1 - x;
     if (left <= 0) return;
@@ -194,24 +227,25 @@ struct AttnWalk {
     at = static_cast<int>(rel - static_cast<int64_t>(head) * (cum[lo + 1] - cum[lo]));
   }
   __device__ __forceinline__ void start(const AttnParams& p, const int32_t* cum, const AttnShares& s) {
-    pair = p.pair;
-    if (pair) {
-      const int64_t x = s.sp * (blockIdx.x / 2);
+    group = static_cast<int>(blockIdx.x) < s.in;
+    if (group) {
+      const int64_t x = s.sp * (blockIdx.x / p.grp);
       seek(p, cum, x, min(s.wp, x + s.sp));
     } else {
       single(p, cum, s);
     }
   }
   __device__ __forceinline__ void single(const AttnParams& p, const int32_t* cum, const AttnShares& s) {
-    pair = false;
-    const int64_t x = s.wp + s.s1 * blockIdx.x;
-    seek(p, cum, x, min(s.w, x + s.s1));
+    group = false;
+    const int cta = blockIdx.x;
+    const int64_t x = s.wp + s.single_at(cta);
+    seek(p, cum, x, min(s.w, s.wp + s.single_at(cta + 1)));
   }
   __device__ __forceinline__ bool next(const AttnParams& p, const int32_t* cum, const AttnShares& s,
                                        AttnPiece& a) {
     for (;;) {
       if (left <= 0) {
-        if (!pair) return false;
+        if (!group) return false;
         single(p, cum, s);
         continue;
       }
@@ -232,11 +266,11 @@ struct AttnWalk {
       if (a.blk0 == a.blk1) continue;
       a.head = head;
       const int u = item * p.Hkv + head;
-      a.pair = pair;
-      if (pair) {
-        const int rank = blockIdx.x & 1;
-        a.tile = 2 * item + rank < p.npt ? 2 * item + rank : -1;
-        a.slot = 2 * (static_cast<int>(blockIdx.x) / 2 + u) + rank;
+      if (group) {
+        const int at_group = static_cast<int>(blockIdx.x) / p.grp, rank = blockIdx.x - at_group * p.grp;
+        a.tile = item * p.grp + rank;
+        if (a.tile >= p.npt) continue;  // the last group of tiles is not full
+        a.slot = p.grp * (at_group + u) + rank;
       } else {
         a.tile = item < p.npi ? item : item - p.npi + p.npt;
         a.slot = s.base1 + static_cast<int>(blockIdx.x) + u - s.u1;
@@ -255,7 +289,6 @@ __device__ __forceinline__ AttnRow attn_row(const AttnParams& p, int tile, int i
   AttnRow a;
   a.b = a.r = a.g = a.lim = 0;
   const int per = p.R * p.G;
-  if (tile < 0) return a;
   if (tile < p.npt) {
     const int s = tile * p.tm + i;
     if (s >= p.B * per) return a;
