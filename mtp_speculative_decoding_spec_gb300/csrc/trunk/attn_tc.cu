@@ -162,42 +162,41 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* sk = smem;
   uint8_t* sv = sk + NS * Sh::kTile;
   uint64_t* kfull = reinterpret_cast<uint64_t*>(smem + Sh::kFixed);
-  uint64_t* kempty = kfull + NS;
-  uint64_t* vfull = kempty + NS;
-  uint64_t* vempty = vfull + NS;
-  uint64_t* vok = vempty + NS;    // V has landed and been looked through
-  uint64_t* sfull = vok + NS;     // [2]
-  // two each, in turns: the scores of block i+1 are out before the weights of block i are waited for,
-  // so one barrier could run through two phases while its waiter looks away
-  uint64_t* pready = sfull + 2;
-  uint64_t* pvdone = pready + 2;
-  uint64_t* qready = pvdone + 2;
-  uint64_t* meet = qready + 1;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(meet + 1);
+  uint64_t* kdone = kfull + NS;   // the scores are there, and the stage is free
+  uint64_t* vfull = kdone + NS;
+  uint64_t* vdone = vfull + NS;   // O has the block, and the stage is free
+  uint64_t* vok = vdone + NS;     // V has landed and been looked through
+  // P is written and V ok. One to a stage, as all of these: an arrival for block i + NS cannot come
+  // before block i's product is complete, so no barrier takes it for an earlier block's, and none runs
+  // through two phases while its waiter looks away.
+  uint64_t* pready = vok + NS;
+  uint64_t* qready = pready + NS;
+  uint64_t* meet = qready + 1;    // the softmax warps, [0] and [1] of a group, [2] all
+  uint64_t* ofree = meet + 3;     // the piece's O has been read
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ofree + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* o_init = abort_flag + 1;      // [2] O holds something before the piece's first MMA on it
   volatile int* odd = abort_flag + 3;         // [NS][2]: a row sees a non-finite V of the stage
   int* least_sm = const_cast<int*>(odd + 2 * NS);  // [2][4] per quarter of the rows
-  float* xch = reinterpret_cast<float*>(smem + Sh::kFixed + 512);  // [2][2][128] between a row's threads
-  int32_t* cum = reinterpret_cast<int32_t*>(xch + 4 * kTm);
+  float* row_m = reinterpret_cast<float*>(smem + Sh::kFixed + 512);  // [2][128] each group's last reference
+  float2* row_ml = reinterpret_cast<float2*>(row_m + 2 * kTm);       // [2][128] and sum, at a piece's end
+  int32_t* cum = reinterpret_cast<int32_t*>(row_ml + 2 * kTm);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < NS; ++s) {
       mbar_init(&kfull[s], 1);
-      mbar_init(&kempty[s], 1);
+      mbar_init(&kdone[s], 1);
       mbar_init(&vfull[s], 1);
-      mbar_init(&vempty[s], 1);
+      mbar_init(&vdone[s], 1);
       mbar_init(&vok[s], 2);
+      mbar_init(&pready[s], 6);
     }
-    mbar_init(&sfull[0], 1);
-    mbar_init(&sfull[1], 1);
-    mbar_init(&pready[0], 8);
-    mbar_init(&pready[1], 8);
-    mbar_init(&pvdone[0], 1);
-    mbar_init(&pvdone[1], 1);
     mbar_init(qready, 8);
-    mbar_init(meet, 8);
+    mbar_init(&meet[0], 4);
+    mbar_init(&meet[1], 4);
+    mbar_init(&meet[2], 8);
+    mbar_init(ofree, 8);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -233,7 +232,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto load = [&](uint8_t* tiles, uint64_t* full, uint64_t* empty, const CUtensorMap* map, int i,
                       int blk) {
         const int s = i % NS;
-        if (i >= NS && !__all_sync(0xffffffffu, mbar_wait_bounded(&empty[s], ((i / NS) & 1) ^ 1)))
+        if (i >= NS && !mbar_wait_warp(&empty[s], ((i / NS) & 1) ^ 1))
           return false;
         tma_load_block(tiles + s * Sh::kTile, map, blk * BN, panel, b, &full[s], Sh::kTile);
         return true;
@@ -241,18 +240,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       const CUtensorMap* mk = pre ? &maps.pk : &maps.ok;
       const CUtensorMap* mv = pre ? &maps.pv : &maps.ov;
       const int n = a.blk1 - a.blk0;
-      ok = load(sk, kfull, kempty, mk, it, a.blk0);
+      ok = load(sk, kfull, kdone, mk, it, a.blk0);
       for (int j = 0; ok && j < n; ++j) {
-        if (j + 1 < n) ok = load(sk, kfull, kempty, mk, it + j + 1, a.blk0 + j + 1);
-        ok = ok && load(sv, vfull, vempty, mv, it + j, a.blk0 + j);
+        if (j + 1 < n) ok = load(sk, kfull, kdone, mk, it + j + 1, a.blk0 + j + 1);
+        ok = ok && load(sv, vfull, vdone, mv, it + j, a.blk0 + j);
       }
       it += n;
     }
     if (!ok && lane == 0) give_up();
     // leave nothing in flight: the last loads of every stage have landed
     for (int j = max(0, it - NS); j < it; ++j) {
-      mbar_wait_bounded(&kfull[j % NS], (j / NS) & 1);
-      mbar_wait_bounded(&vfull[j % NS], (j / NS) & 1);
+      mbar_wait_warp(&kfull[j % NS], (j / NS) & 1);
+      mbar_wait_warp(&vfull[j % NS], (j / NS) & 1);
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------------ MMA issuer
@@ -264,7 +263,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int it = 0, piece = 0;
       bool ok = true;
       auto scores = [&](int i) {
-        if (!__all_sync(0xffffffffu, mbar_wait_bounded(&kfull[i % NS], (i / NS) & 1))) return false;
+        if (!mbar_wait_warp(&kfull[i % NS], (i / NS) & 1)) return false;
         tc_fence_after();
         const uint64_t kd = desc_advance(kd0, (i % NS) * Sh::kTile);
         const uint32_t ds = tmem + Sh::kS + (i & 1) * BN;
@@ -272,20 +271,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int kk = 0; kk < D / 16; ++kk)
           tc_mma_ta(ds, tmem + Sh::kQ + kk * 8,
                     desc_advance(kd, (kk / 4) * Sh::kPanel + (kk % 4) * 32), kIdS, kk > 0);
-        tc_commit_elect(&sfull[i & 1]);
-        tc_commit_elect(&kempty[i % NS]);
+        tc_commit_elect(&kdone[i % NS]);
         return true;
       };
       while (ok && !__any_sync(0xffffffffu, *abort_flag) && walk.next(p, cum, shares, a)) {
         const int n = a.blk1 - a.blk0;
-        ok = __all_sync(0xffffffffu, mbar_wait_bounded(qready, piece & 1));
+        ok = mbar_wait_warp(qready, piece & 1);
         tc_fence_after();
         ok = ok && scores(it);
         for (int j = 0; ok && j < n; ++j) {
           const int i = it + j;
           if (j + 1 < n) ok = scores(i + 1);
-          ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(&pready[i & 1], (i >> 1) & 1) &&
-                                                 mbar_wait_bounded(&vok[i % NS], (i / NS) & 1));
+          ok = ok && mbar_wait_warp(&pready[i % NS], (i / NS) & 1);
+          if (j == 0 && piece > 0)
+            ok = ok && mbar_wait_warp(ofree, (piece - 1) & 1);
           if (!ok) break;
           tc_fence_after();
           const uint64_t vd = desc_advance(vd0, (i % NS) * Sh::kTile);
@@ -294,8 +293,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int kk = 0; kk < BN / 16; ++kk)
             tc_mma_ta(tmem, ps + kk * 8, desc_advance(vd, kk * 2048), kIdO, kk > 0 ? 1u : acc0);
-          tc_commit_elect(&vempty[i % NS]);
-          tc_commit_elect(&pvdone[i & 1]);
+          tc_commit_elect(&vdone[i % NS]);
         }
         it += n;
         ++piece;
@@ -332,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       for (int blk = a.blk0; ok && blk < a.blk1; ++blk, ++it) {
         const int s = it % NS;
-        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&vfull[s], (it / NS) & 1));
+        ok = mbar_wait_warp(&vfull[s], (it / NS) & 1);
         bool seen = false;
         if (blk * BN + BN > least) {
           uint8_t* vt = sv + s * Sh::kTile;
@@ -372,41 +370,39 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) {
           odd[2 * s + gw] = seen;
           mbar_arrive(&vok[s]);
+          mbar_arrive(&pready[s]);
         }
       }
     }
     if (!ok && lane == 0) give_up();
   } else {
     // ------------------------------------------------------------------ softmax
-    // A row has two threads, in warps of the same lanes of TMEM: each takes half of a block's scores and
-    // half of O's dims. They tell each other the largest score of their halves once a block.
-    constexpr int CW = BN / 2, DH = D / 2;
-    const int quad = warp & 3, half = (warp - 4) >> 2, row = quad * 32 + lane, st = threadIdx.x - 128;
+    // Two groups of four warps, a thread to a row in each, take the blocks in turns: one is in its
+    // exponentials while the other waits for scores or reads them. What a block needs of the one before
+    // is the row's reference, which is known long before that one's weights.
+    constexpr int DH = D / 2;
+    const int quad = warp & 3, half = (warp - 4) >> 2, row = quad * 32 + lane, st = threadIdx.x & 127;
     const uint32_t trow = tmem + (static_cast<uint32_t>(quad * 32) << 16);
     const float scale = fabsf(p.scale_log2);
     int it = 0;
     // A wait that runs out ends all further waiting, not the walk: whatever happens, a softmax warp
-    // goes through the same pieces as the others, which it meets at `meet`.
+    // goes through the same pieces as the others, which it meets at `meet` and at named barriers.
     bool ok = true;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
-      if (ok && !mbar_wait_bounded(bar, parity)) {
-        give_up();
-        ok = false;
-      }
-      ok = __all_sync(0xffffffffu, ok);
+      if (!ok || mbar_wait_warp(bar, parity)) return;
+      if (lane == 0) give_up();
+      ok = false;
     };
-    uint32_t met = 0;
-    auto bar_soft = [&]() {  // a barrier of the softmax warps, with the limit of every wait
+    uint32_t met_all = 0, met_group = 0;
+    auto bar_all = [&]() {  // a barrier of the softmax warps, with the limit of every wait
       __syncwarp();
-      if (lane == 0) mbar_arrive(meet);
-      wait(meet, met & 1);
-      ++met;
+      if (lane == 0) mbar_arrive(&meet[2]);
+      wait(&meet[2], met_all++ & 1);
     };
-    // Both threads' numbers of a row. The two warps come here the same number of times whatever happens.
-    auto exchange = [&](float x, int buf) {
-      xch[(buf * 2 + half) * kTm + row] = x;
-      asm volatile("bar.sync %0, 64;" ::"r"(1 + quad) : "memory");
-      return xch[(buf * 2 + (half ^ 1)) * kTm + row];
+    auto bar_group = [&]() {  // of the group's
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&meet[half]);
+      wait(&meet[half], met_group++ & 1);
     };
     // Q of a piece: this thread's half of its row into its TMEM lane; a negative scale goes into Q's signs
     int piece = 0, least = 0;
@@ -437,9 +433,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int lo = __reduce_min_sync(0xffffffffu, ar.lim > 0 ? ar.lim : 0x7fffffff);
       int* lsm = least_sm + 4 * (piece & 1);
       if (lane == 0 && half == 0) lsm[quad] = lo;
-      if (st == 0) o_init[piece & 1] = 0;
+      if (st == 0 && half == 0) o_init[piece & 1] = 0;
       tc_fence_before();
-      bar_soft();
+      bar_all();
       if (lane == 0) mbar_arrive(qready);
       least = min(min(lsm[0], lsm[1]), min(lsm[2], lsm[3]));
     };
@@ -449,51 +445,65 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int lim = ar.lim, from_all = least;
       const int64_t at = static_cast<int64_t>(a.slot) * kTm + row;
       const int blk_end = a.blk1;
-      float m = -INFINITY, l = 0.f;
-      for (int blk = a.blk0, blk0 = blk; blk < blk_end; ++blk, ++it) {
-        const bool first = blk == blk0;
+      const int n = blk_end - a.blk0, it0 = it;
+      float mg = -INFINITY, l = 0.f;  // of the group's blocks: the last reference, the sum
+      it += (it & 1) ^ half;          // the first of them
+      for (int blk = a.blk0 + it - it0; blk < blk_end; blk += 2, it += 2) {
+        const bool first = it == it0, last = it + 1 == it0 + n;
         const int valid = min(BN, lim - blk * BN);  // positions of the block this row sees
-        wait(&sfull[it & 1], (it >> 1) & 1);
+        wait(&kdone[it % NS], (it / NS) & 1);
         tc_fence_after();
-        const uint32_t ts = trow + Sh::kS + (it & 1) * BN;
-        float v[CW];
-        if constexpr (CW == 64)
-          tmem_ld64(ts + half * CW, v);
-        else
-          tmem_ld32(ts + half * CW, v);
-        const int mine = valid - half * CW;  // of this thread's scores
-        const bool full = __all_sync(0xffffffffu, mine >= CW);
-        if (!full) {
+        const uint32_t ts = trow + Sh::kS + half * BN;
+        const bool full = __all_sync(0xffffffffu, valid >= BN);
+        float v[64], raw = -INFINITY;
 #pragma unroll
-          for (int j = 0; j < CW; ++j) v[j] = j < mine ? v[j] : -INFINITY;
+        for (int c0 = 0; c0 < BN; c0 += 64) {
+          tmem_ld64(ts + c0, v);
+          if (!full) {
+#pragma unroll
+            for (int j = 0; j < 64; ++j) v[j] = c0 + j < valid ? v[j] : -INFINITY;
+          }
+          float mx[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+          for (int j = 4; j < 64; ++j) mx[j & 3] = fmaxf(mx[j & 3], v[j]);
+          raw = fmaxf(raw, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
         }
-        float mx[4] = {v[0], v[1], v[2], v[3]};
-#pragma unroll
-        for (int j = 4; j < CW; ++j) mx[j & 3] = fmaxf(mx[j & 3], v[j]);
-        float raw = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-        // after this both threads have their scores, whose columns the weights overwrite
-        raw = fmaxf(raw, exchange(raw, it & 1));
         const float top = raw == -INFINITY ? -INFINITY : raw * scale;
-        const bool grow = top > m + kLazy;  // from -Inf: at the first score
-        const float mo = m;
-        if (grow) m = top;
+        float mo = -INFINITY;  // the reference after the block before, from the other group
+        if (!first) {
+          asm volatile("bar.sync %0, 64;" ::"r"(1 + 4 * (half ^ 1) + quad) : "memory");
+          mo = row_m[(half ^ 1) * kTm + row];
+        }
+        const bool grow = top > mo + kLazy;  // from -Inf: at the first score
+        const float m = grow ? top : mo;
+        if (!last) {
+          row_m[half * kTm + row] = m;
+          asm volatile("bar.arrive %0, 64;" ::"r"(1 + 4 * half + quad) : "memory");
+        }
         const float ref = m == -INFINITY ? 0.f : m;
         float sum[4] = {0.f, 0.f, 0.f, 0.f};
-        uint32_t w[CW / 2];
 #pragma unroll
-        for (int j = 0; j < CW; j += 2) {
-          float e0 = ex2(fmaf(v[j], scale, -ref)), e1 = ex2(fmaf(v[j + 1], scale, -ref));
-          if (!full) {
-            e0 = j < mine ? e0 : 0.f;
-            e1 = j + 1 < mine ? e1 : 0.f;
+        for (int c0 = 0; c0 < BN; c0 += 32) {
+          // 64 scores stay in registers; of more, all are read again (the columns before are weights by then)
+          float* x = v + (c0 & 32);
+          if (BN > 64) tmem_ld32(ts + c0, x);
+          uint32_t w[16];
+#pragma unroll
+          for (int j = 0; j < 32; j += 2) {
+            float e0 = ex2(fmaf(x[j], scale, -ref)), e1 = ex2(fmaf(x[j + 1], scale, -ref));
+            if (!full) {
+              e0 = c0 + j < valid ? e0 : 0.f;
+              e1 = c0 + j + 1 < valid ? e1 : 0.f;
+            }
+            sum[j & 3] += e0;
+            sum[(j + 1) & 3] += e1;
+            w[j / 2] = bf16_pair(e0, e1);
           }
-          sum[j & 3] += e0;
-          sum[(j + 1) & 3] += e1;
-          w[j / 2] = bf16_pair(e0, e1);
+          tmem_st16(ts + c0 / 2, w);
         }
         const float c = grow ? ex2(mo - ref) : 1.f;  // ex2(-Inf) = 0
-        l = l * c + ((sum[0] + sum[1]) + (sum[2] + sum[3]));
-        tmem_st<CW / 2>(ts + half * (CW / 2), w);
+        l = (mg == m ? l : l * ex2(mg - ref)) + ((sum[0] + sum[1]) + (sum[2] + sum[3]));
+        mg = m;
         const bool rescale = !first && __any_sync(0xffffffffu, grow);
         const int sg = it % NS;
         bool by_hand = false;
@@ -503,12 +513,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (rescale || by_hand) {
           // O of the blocks before is complete (the MMA of this one waits for this thread)
-          if (!first) wait(&pvdone[(it - 1) & 1], ((it - 1) >> 1) & 1);
+          if (!first)
+            wait(&vdone[(it - 1) % NS], ((it - 1) / NS) & 1);
+          else if (piece > 0)
+            wait(ofree, (piece - 1) & 1);  // and the piece's before has been read
           tc_fence_after();
         }
         if (rescale) {
 #pragma unroll 1
-          for (int d = half * DH; d < half * DH + DH; d += 32) {
+          for (int d = 0; d < D; d += 32) {
             float o[32];
             uint32_t u[32];
             tmem_ld32(trow + d, o);
@@ -521,11 +534,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint8_t* vt = sv + sg * Sh::kTile;
           const int from = max(0, from_all - blk * BN), nrow = BN - from;
           tmem_st_wait();
-          bar_soft();  // both halves of the weights are there
           // Some rows see non-finite values and some do not. Each row adds its own share of those
           // values to O (zero to begin with), then they are cleared for the tensor cores.
 #pragma unroll 1
-          for (int d = half * DH; d < half * DH + DH; d += 8) {
+          for (int d = 0; d < D; d += 8) {
             float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
             if (!first) tmem_ld8(trow + d, o);
             for (int pos = from; pos < BN; ++pos) {
@@ -559,8 +571,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 : "memory");
             tmem_st_wait();
           }
-          bar_soft();
-          for (int i = st; i < nrow * (D / 8); i += kSoftThreads) {
+          bar_group();
+          for (int i = st; i < nrow * (D / 8); i += kSoftThreads / 2) {
             const int pos = from + i / (D / 8), ch = i % (D / 8);
             uint32_t* at = reinterpret_cast<uint32_t*>(vt + (ch / 8) * Sh::kPanel + pos * 128 +
                                                        (((ch & 7) ^ (pos & 7)) << 4));
@@ -574,25 +586,32 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (st == 0) o_init[piece & 1] = 1;
           fence_async_smem();
-          bar_soft();
+          bar_group();
         }
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&pready[it & 1]);
-        if (blk + 1 == blk_end) {
-          // every product with this piece's Q is complete: the next one's can take its place, and its
-          // first scores be computed, while this piece's output is written
-          ++piece;
-          more = walk.next(p, cum, shares, a);
-          if (more) load_q(a);
-        }
+        if (lane == 0) mbar_arrive(&pready[it % NS]);
       }
+      it = it0 + n;
+      // every product with this piece's Q is complete: the next one's can take its place, and its first
+      // scores be computed, while this piece's output is written
+      const int lb = it - 1;
+      wait(&kdone[lb % NS], (lb / NS) & 1);
+      ++piece;
+      more = walk.next(p, cum, shares, a);
+      if (more) load_q(a);
       // the piece's partial
-      wait(&pvdone[(it - 1) & 1], ((it - 1) >> 1) & 1);
+      wait(&vdone[lb % NS], (lb / NS) & 1);
       tc_fence_after();
-      l += exchange(l, it & 1);  // the buffer that the last block did not use
-      if (lim > 0 && half == 0) p.ml[at] = make_float2(m, l);
+      row_ml[half * kTm + row] = make_float2(mg, l);
+      asm volatile("bar.sync %0, 64;" ::"r"(9 + quad) : "memory");
+      if (lim > 0 && half == 0) {
+        const float2 other = row_ml[kTm + row];
+        // the reference never falls, so the greater one is the last one's
+        const float m = fmaxf(mg, other.x), ref = m == -INFINITY ? 0.f : m;
+        p.ml[at] = make_float2(m, l * ex2(mg - ref) + other.y * ex2(other.x - ref));
+      }
 #pragma unroll 1
       for (int d = half * DH; d < half * DH + DH; d += 32) {
         float o[32];
@@ -604,6 +623,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(ofree);
     }
   }
   tc_fence_before();
@@ -618,7 +639,7 @@ template <int D>
 spec_status launch_tc(const AttnParams& p, int grid, EncodeTiledFn encode, cudaStream_t stream) {
   using Sh = Shape<D>;
   static SmemAllowance allowed;
-  const int smem = Sh::kFixed + 512 + 16 * kTm + 4 * (p.items + 1) + 1024;
+  const int smem = Sh::kFixed + 512 + 24 * kTm + 4 * (p.items + 1) + 1024;
   if (allow_dynamic_smem(attn_tc_kernel<D>, smem, allowed) != cudaSuccess) return SPEC_ERR_CUDA;
   AttnMaps m;
   // dims inside a 64-dim panel, positions, panels (64 dims on), requests

