@@ -584,7 +584,7 @@ size_t spec_delta_prefill_workspace_bytes(int64_t rows, int32_t B, const spec_st
  *   q, out      row b*R + r at q + (b*R + r)*q_stride (elements): [q_heads][head_dim].
  *   prefix_k, prefix_v   position p at prefix_k + p*prefix_stride (elements):
  *               [kv_heads][head_dim], or both NULL: no prefix. 16-byte aligned, as is the stride
- *               in bytes. prefix_capacity < 2^31 positions are there.
+ *               in bytes. prefix_capacity positions are there, at most 2^31 - 256.
  *   prefix_len  [B] int64 (clamped to [0, prefix_capacity]), or NULL: all of prefix_capacity.
  *   lse         [B*R][q_heads] float32 or NULL: log sum exp(scale q k) of each row, -Inf where a
  *               row has nothing to see (its output is zero).
@@ -606,8 +606,8 @@ typedef struct {
 } spec_attn_desc;
 
 /*
- * spec_prefix_attention -- see spec_attn_desc. layer in [0, kv_layers); R in 1..8; kv_capacity
- * < 2^31. Of st only the kv* fields are used.
+ * spec_prefix_attention -- see spec_attn_desc. layer in [0, kv_layers); R in 1..8; kv_capacity at
+ * most 2^31 - 256. Of st only the kv* fields are used.
  *   n_rows    [B] int32 or NULL (R each): rows from n_rows[b] on give zero (lse -Inf).
  *   workspace spec_prefix_attention_workspace_bytes(B, R, st, d) bytes, 256-byte aligned,
  *             ZERO-FILLED ONCE before its first use; the error word at byte offset 4 as in the

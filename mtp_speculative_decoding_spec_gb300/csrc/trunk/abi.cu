@@ -87,7 +87,7 @@ spec_status attn_check(int32_t B, int32_t R, const spec_state_desc* st, const sp
   if (d->prefix_k && d->prefix_capacity < 0) return SPEC_ERR_INVALID;
   if (B > 1024 || d->head_dim > 256 || d->q_heads / d->kv_heads > 64 || d->kv_heads > 65536)
     return SPEC_ERR_UNSUPPORTED;
-  if (st->kv_capacity >= (int64_t(1) << 31) || (d->prefix_k && d->prefix_capacity >= (int64_t(1) << 31)))
+  if (st->kv_capacity > kAttnMaxPos || (d->prefix_k && d->prefix_capacity > kAttnMaxPos))
     return SPEC_ERR_UNSUPPORTED;
   return SPEC_OK;
 }

@@ -62,7 +62,7 @@ __global__ void __launch_bounds__(kSimtThreads, 1)
   int* row_lim = reinterpret_cast<int*>(row_l + kSimtTm);
   int64_t* row_q = reinterpret_cast<int64_t*>(row_lim + kSimtTm);  // where the row's query lies
   int32_t* cum = reinterpret_cast<int32_t*>(row_q + kSimtTm);
-  attn_plan(p, cum);
+  const AttnReq* req = attn_plan(p, cum);
   const AttnShares shares = attn_shares(p, cum);
   if (blockIdx.x == 0) attn_write_units(p, cum, shares);
   AttnWalk walk;
@@ -77,7 +77,7 @@ __global__ void __launch_bounds__(kSimtThreads, 1)
     const int head = a.head, slot = a.slot;
     __syncthreads();  // the previous piece's shared memory is no longer read
     if (tid < kSimtTm) {
-      const AttnRow ar = attn_row(p, a.tile, tid);
+      const AttnRow ar = attn_row(p, req, a.tile, tid);
       row_lim[tid] = ar.lim;
       row_q[tid] = (static_cast<int64_t>(ar.b) * p.R + ar.r) * p.qs +
                    static_cast<int64_t>(head * p.G + ar.g) * D;
@@ -232,14 +232,14 @@ __global__ void __launch_bounds__(NW == 1 ? 128 : 32 * NW)
   const int b = static_cast<int>(row / p.R), r = static_cast<int>(row) - b * p.R;
   const int s = (b * p.R + r) * p.G + g, x = r * p.G + g;
   pdl_wait();
-  const int rows = attn_rows(p, b);
+  const AttnReq rq = attn_req(p, b);
   int2 u0 = make_int2(0, 0);
   const int t0 = s / p.tm;
   if (p.npt > 0) u0 = __ldcg(p.units + t0 / p.grp * p.Hkv + head);
   int2 u1 = __ldcg(p.units + (p.npi + b * p.nown + x / p.tm) * p.Hkv + head);
   u0.x += t0 % p.grp;
-  if (p.npt > 0 && attn_prefix(p, b) == 0) u0.y = 0;
-  if (r >= rows) u0.y = u1.y = 0;
+  if (rq.prefix == 0) u0.y = 0;
+  if (r >= rq.rows) u0.y = u1.y = 0;
   const int at0 = s % p.tm, at1 = x % p.tm, ntot = u0.y + u1.y;
   float m = -INFINITY, l = 0.f;
   float acc[2][4] = {};
@@ -346,7 +346,7 @@ template <typename T>
 cudaError_t simt_launch(const AttnParams& p, int grid, cudaStream_t stream) {
   static SmemAllowance allowed;
   const int floats = (kSimtTm + 2 * kSimtBn) * (p.D + kPad) + kSimtTm * (kSimtBn + 1) + 3 * kSimtTm;
-  const int smem = 4 * (floats + 3 * kSimtTm + p.items + 1);
+  const int smem = 4 * (floats + 3 * kSimtTm) + static_cast<int>(attn_plan_bytes(p.items, p.B));
   const cudaError_t e = allow_dynamic_smem(attn_simt_kernel<T>, smem, allowed);
   if (e != cudaSuccess) return e;
   return launch_pdl(attn_simt_kernel<T>, dim3(grid), dim3(kSimtThreads), smem, stream, p);

@@ -136,6 +136,17 @@ __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
 }
+// 32 bytes at a time, a whole sector of memory: half the requests of 16-byte pieces a row apart.
+__device__ __forceinline__ void load32(const void* p, uint32_t* r) {
+  asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "l"(p));
+}
+__device__ __forceinline__ void store32(void* p, const float* v) {
+  asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "f"(v[0]), "f"(v[1]),
+               "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+               : "memory");
+}
 __device__ __forceinline__ bool odd_pair(uint32_t w) {  // an Inf or NaN in either half
   return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
 }
@@ -202,7 +213,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (warp == 1) tmem_alloc(tmem_slot, 512);
   pdl_wait();
-  attn_plan(p, cum);  // ends with a block barrier
+  const AttnReq* req = attn_plan(p, cum);  // ends with a block barrier
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -310,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (ok && !__any_sync(0xffffffffu, *abort_flag) && walk.next(p, cum, shares, a)) {
       int least = 0x7fffffff, most = 0;  // positions every running row sees; positions any row sees
       for (int i = lane; i < kTm; i += 32) {
-        const int lim = attn_row(p, a.tile, i).lim;
+        const int lim = attn_row(p, req, a.tile, i).lim;
         most = max(most, lim);
         if (lim > 0) least = min(least, lim);
       }
@@ -321,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         AttnPiece nx;
         if (ahead.next(p, cum, shares, nx))
           for (int i = gw * 32 + lane; i < kTm; i += 64) {
-            const AttnRow r = attn_row(p, nx.tile, i);
+            const AttnRow r = attn_row(p, req, nx.tile, i);
             if (r.lim <= 0) continue;
             const __nv_bfloat16* src = q_row<D>(p, nx, r);
             for (int d = 0; d < D; d += 64)
@@ -408,18 +419,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     int piece = 0, least = 0;
     AttnRow ar;
     auto load_q = [&](const AttnPiece& pc) {
-      ar = attn_row(p, pc.tile, row);
+      ar = attn_row(p, req, pc.tile, row);
       const uint32_t flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;
       const __nv_bfloat16* src = q_row<D>(p, pc, ar);
       uint32_t w[DH / 2];
-      if (__all_sync(0xffffffffu, (reinterpret_cast<uintptr_t>(src) & 15u) == 0)) {
-        const uint4* from = reinterpret_cast<const uint4*>(src + half * DH);
-        uint4 x[DH / 8];
+      if (__all_sync(0xffffffffu, (reinterpret_cast<uintptr_t>(src) & 31u) == 0)) {
 #pragma unroll
-        for (int c = 0; c < DH / 8; ++c) x[c] = __ldg(from + c);
-#pragma unroll
-        for (int c = 0; c < DH / 8; ++c)
-          w[4 * c] = x[c].x, w[4 * c + 1] = x[c].y, w[4 * c + 2] = x[c].z, w[4 * c + 3] = x[c].w;
+        for (int c = 0; c < DH / 16; ++c) load32(src + half * DH + 16 * c, w + 8 * c);
       } else {
         const uint16_t* from = reinterpret_cast<const uint16_t*>(src + half * DH);
 #pragma unroll
@@ -618,8 +624,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld32(trow + d, o);
         if (lim > 0) {
 #pragma unroll
-          for (int j = 0; j < 32; j += 4)
-            *reinterpret_cast<float4*>(p.o + at * D + d + j) = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+          for (int j = 0; j < 32; j += 8) store32(p.o + at * D + d + j, o + j);
         }
       }
       tc_fence_before();
@@ -639,7 +644,7 @@ template <int D>
 spec_status launch_tc(const AttnParams& p, int grid, EncodeTiledFn encode, cudaStream_t stream) {
   using Sh = Shape<D>;
   static SmemAllowance allowed;
-  const int smem = Sh::kFixed + 512 + 24 * kTm + 4 * (p.items + 1) + 1024;
+  const int smem = Sh::kFixed + 512 + 24 * kTm + static_cast<int>(attn_plan_bytes(p.items, p.B)) + 1024;
   if (allow_dynamic_smem(attn_tc_kernel<D>, smem, allowed) != cudaSuccess) return SPEC_ERR_CUDA;
   AttnMaps m;
   // dims inside a 64-dim panel, positions, panels (64 dims on), requests

@@ -85,40 +85,50 @@ struct AttnParams {
 };
 
 constexpr int kAttnMaxItems = 8192;
+constexpr int64_t kAttnMaxPos = (int64_t(1) << 31) - 256;  // a block past the last one still has an int
 constexpr int kAttnOver = 6;    // see `over`
 constexpr int kAttnGroup = 16;  // most of `grp`
 
-// Rows of request b that run.
-__device__ __forceinline__ int attn_rows(const AttnParams& p, int b) {
-  return p.n_rows ? max(0, min(p.n_rows[b], p.R)) : p.R;
+// Of request b: the rows that run, the positions of the prefix it sees and of its own cache before them.
+struct AttnReq {
+  int rows, prefix, base;
+};
+__device__ __forceinline__ AttnReq attn_req(const AttnParams& p, int b) {
+  const int64_t base = p.kv_len[b], prefix = p.prefix_len ? p.prefix_len[b] : p.pcap;
+  AttnReq r;
+  r.rows = p.n_rows ? max(0, min(p.n_rows[b], p.R)) : p.R;
+  r.prefix = static_cast<int>(max(static_cast<int64_t>(0), min(prefix, p.pcap)));
+  r.base = static_cast<int>(max(static_cast<int64_t>(0), min(base, p.kcap)));
+  return r;
 }
-__device__ __forceinline__ int attn_prefix(const AttnParams& p, int b) {
-  if (!p.prefix_len) return static_cast<int>(p.pcap);
-  return static_cast<int>(max(static_cast<int64_t>(0), min(p.prefix_len[b], p.pcap)));
+__device__ __forceinline__ int attn_own(const AttnParams& p, const AttnReq& r, int rows) {
+  return min(r.base + rows, static_cast<int>(p.kcap));
 }
-__device__ __forceinline__ int attn_own(const AttnParams& p, int b, int rows) {
-  return static_cast<int>(
-      min(max(p.kv_len[b], static_cast<int64_t>(0)) + rows, p.kcap));
+__host__ __device__ constexpr size_t attn_plan_bytes(int items, int B) {
+  return sizeof(int32_t) * (items + 1) + sizeof(AttnReq) * B;
 }
 
-// cum[0..items] in shared memory: cost of one KV head before each item, in blocks. By the whole block
-// (a barrier at the end). Every CTA works it out for itself from the lengths on the device, so no
-// launch comes before and no host reads them.
-__device__ __forceinline__ void attn_plan(const AttnParams& p, int32_t* cum) {
+// cum[0..items] in shared memory: cost of one KV head before each item, in blocks; after it the
+// requests' numbers. By the whole block (a barrier at the end). Every CTA works it out for itself from
+// the lengths on the device, so no launch comes before and no host reads them.
+__device__ __forceinline__ AttnReq* attn_plan(const AttnParams& p, int32_t* cum) {
   const int tid = threadIdx.x, nt = blockDim.x, per = p.R * p.G;
-  for (int i = tid; i < p.items; i += nt) {
+  AttnReq* req = reinterpret_cast<AttnReq*>(cum + p.items + 1);
+  const auto cost = [&p](int n) { return n > 0 ? (n + p.bn - 1) / p.bn + p.over : 0; };
+  for (int b = tid; b < p.B; b += nt) {
+    const AttnReq r = attn_req(p, b);
+    req[b] = r;
+    const int c = r.rows > 0 ? cost(attn_own(p, r, r.rows)) : 0;
+    for (int j = 0; j < p.nown; ++j) cum[p.npi + b * p.nown + j + 1] = c;
+  }
+  __syncthreads();
+  for (int i = tid; i < p.npi; i += nt) {
+    const int span = p.tm * p.grp;
+    const int b0 = i * span / per, b1 = min(p.B - 1, ((i + 1) * span - 1) / per);
     int n = 0;
-    if (i < p.npi) {
-      const int span = p.tm * p.grp;
-      const int b0 = i * span / per, b1 = min(p.B - 1, ((i + 1) * span - 1) / per);
-      for (int b = b0; b <= b1; ++b)
-        if (attn_rows(p, b) > 0) n = max(n, attn_prefix(p, b));
-    } else {
-      const int b = (i - p.npi) / p.nown;
-      const int rows = attn_rows(p, b);
-      if (rows > 0) n = attn_own(p, b, rows);
-    }
-    cum[i + 1] = n > 0 ? (n + p.bn - 1) / p.bn + p.over : 0;
+    for (int b = b0; b <= b1; ++b)
+      if (req[b].rows > 0) n = max(n, req[b].prefix);
+    cum[i + 1] = cost(n);
   }
   if (tid == 0) cum[0] = 0;
   __syncthreads();
@@ -138,6 +148,7 @@ __device__ __forceinline__ void attn_plan(const AttnParams& p, int32_t* cum) {
     }
   }
   __syncthreads();
+  return req;
 }
 
 // How the costs are dealt out: the groups' part [0, wp), `sp` to each group, and the rest up to w: `s1`
@@ -296,7 +307,7 @@ struct AttnWalk {
 struct AttnRow {
   int b, r, g, lim;
 };
-__device__ __forceinline__ AttnRow attn_row(const AttnParams& p, int tile, int i) {
+__device__ __forceinline__ AttnRow attn_row(const AttnParams& p, const AttnReq* req, int tile, int i) {
   AttnRow a;
   a.b = a.r = a.g = a.lim = 0;
   const int per = p.R * p.G;
@@ -307,7 +318,7 @@ __device__ __forceinline__ AttnRow attn_row(const AttnParams& p, int tile, int i
     const int x = s - a.b * per;
     a.r = x / p.G;
     a.g = x - a.r * p.G;
-    if (a.r < attn_rows(p, a.b)) a.lim = attn_prefix(p, a.b);
+    if (a.r < req[a.b].rows) a.lim = req[a.b].prefix;
   } else {
     const int own = tile - p.npt;
     a.b = own / p.nown;
@@ -315,7 +326,7 @@ __device__ __forceinline__ AttnRow attn_row(const AttnParams& p, int tile, int i
     if (x >= per) return a;
     a.r = x / p.G;
     a.g = x - a.r * p.G;
-    if (a.r < attn_rows(p, a.b)) a.lim = attn_own(p, a.b, a.r + 1);
+    if (a.r < req[a.b].rows) a.lim = attn_own(p, req[a.b], a.r + 1);
   }
   return a;
 }
