@@ -487,28 +487,36 @@ __global__ void __launch_bounds__(kThreads, 1)
           asm volatile("bar.arrive %0, 64;" ::"r"(1 + 4 * half + quad) : "memory");
         }
         const float ref = m == -INFINITY ? 0.f : m;
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        // A weight is 2^(scale s - ref): two at a time in packed arithmetic. Of 128 scores the last 32 stay
+        // in registers; the others are read again, before weights take their columns.
+        unsigned long long sum[2] = {0ull, 0ull};
+        const unsigned long long scale2 = pack2(__float_as_uint(scale), __float_as_uint(scale));
+        const unsigned long long ref2 = pack2(__float_as_uint(-ref), __float_as_uint(-ref));
 #pragma unroll
         for (int c0 = 0; c0 < BN; c0 += 32) {
-          // 64 scores stay in registers; of more, all are read again (the columns before are weights by then)
-          float* x = v + (c0 & 32);
-          if (BN > 64) tmem_ld32(ts + c0, x);
+          float again[32];
+          const bool kept = BN == 64 || c0 + 32 == BN;
+          if (!kept) tmem_ld32(ts + c0, again);
+          const float* x = kept ? v + (c0 & 32) : again;
           uint32_t w[16];
 #pragma unroll
           for (int j = 0; j < 32; j += 2) {
-            float e0 = ex2(fmaf(x[j], scale, -ref)), e1 = ex2(fmaf(x[j + 1], scale, -ref));
+            unsigned long long y = ref2;
+            ffma2_acc(y, pack2(__float_as_uint(x[j]), __float_as_uint(x[j + 1])), scale2);
+            uint32_t lo, hi;
+            asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(y));
+            float e0 = ex2(__uint_as_float(lo)), e1 = ex2(__uint_as_float(hi));
             if (!full) {
               e0 = c0 + j < valid ? e0 : 0.f;
               e1 = c0 + j + 1 < valid ? e1 : 0.f;
             }
-            sum[j & 3] += e0;
-            sum[(j + 1) & 3] += e1;
+            asm("add.rn.f32x2 %0, %0, %1;" : "+l"(sum[(j / 2) & 1]) : "l"(pack2(__float_as_uint(e0), __float_as_uint(e1))));
             w[j / 2] = bf16_pair(e0, e1);
           }
           tmem_st16(ts + c0 / 2, w);
         }
         const float c = grow ? ex2(mo - ref) : 1.f;  // ex2(-Inf) = 0
-        l = (mg == m ? l : l * ex2(mg - ref)) + ((sum[0] + sum[1]) + (sum[2] + sum[3]));
+        l = (mg == m ? l : l * ex2(mg - ref)) + (sum2(sum[0]) + sum2(sum[1]));
         mg = m;
         const bool rescale = !first && __any_sync(0xffffffffu, grow);
         const int sg = it % NS;

@@ -122,13 +122,14 @@ __device__ __forceinline__ AttnReq* attn_plan(const AttnParams& p, int32_t* cum)
     for (int j = 0; j < p.nown; ++j) cum[p.npi + b * p.nown + j + 1] = c;
   }
   __syncthreads();
-  for (int i = tid; i < p.npi; i += nt) {
+  for (int i = tid >> 5; i < p.npi; i += nt >> 5) {  // a warp to an item
     const int span = p.tm * p.grp;
     const int b0 = i * span / per, b1 = min(p.B - 1, ((i + 1) * span - 1) / per);
     int n = 0;
-    for (int b = b0; b <= b1; ++b)
+    for (int b = b0 + (tid & 31); b <= b1; b += 32)
       if (req[b].rows > 0) n = max(n, req[b].prefix);
-    cum[i + 1] = cost(n);
+    n = __reduce_max_sync(0xffffffffu, n);
+    if ((tid & 31) == 0) cum[i + 1] = cost(n);
   }
   if (tid == 0) cum[0] = 0;
   __syncthreads();
@@ -188,8 +189,13 @@ __device__ __forceinline__ AttnShares attn_shares(const AttnParams& p, const int
     const int most = grid / p.grp;
     groups = all > 0 ? max(1, static_cast<int>(s.wp * grid / all)) : 1;
     const int64_t fewer = s.split(p, groups, grid);
-    if (groups < most && s.split(p, groups + 1, grid) < fewer) ++groups;
-    s.split(p, groups, grid);
+    if (groups < most) {
+      AttnShares more = s;
+      if (more.split(p, groups + 1, grid) < fewer) {
+        s = more;
+        ++groups;
+      }
+    }
   } else {
     s.s1 = s.s2 = (s.w + grid - 1) / grid;
   }
