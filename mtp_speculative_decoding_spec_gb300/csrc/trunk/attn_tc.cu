@@ -132,6 +132,11 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
 __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
@@ -469,10 +474,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int j = 0; j < 64; ++j) v[j] = c0 + j < valid ? v[j] : -INFINITY;
           }
-          float mx[4] = {v[0], v[1], v[2], v[3]};
+          float mx[4] = {raw, v[1], v[2], v[3]};
+          mx[0] = max3(mx[0], v[0], v[4]);
 #pragma unroll
-          for (int j = 4; j < 64; ++j) mx[j & 3] = fmaxf(mx[j & 3], v[j]);
-          raw = fmaxf(raw, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+          for (int j = 5; j + 1 < 64; j += 2) mx[(j / 2) & 3] = max3(mx[(j / 2) & 3], v[j], v[j + 1]);
+          raw = max3(max3(mx[0], mx[1], v[63]), mx[2], mx[3]);
         }
         const float top = raw == -INFINITY ? -INFINITY : raw * scale;
         float mo = -INFINITY;  // the reference after the block before, from the other group
@@ -515,9 +521,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           tmem_st16(ts + c0 / 2, w);
         }
-        const float c = grow ? ex2(mo - ref) : 1.f;  // ex2(-Inf) = 0
-        l = (mg == m ? l : l * ex2(mg - ref)) + (sum2(sum[0]) + sum2(sum[1]));
-        mg = m;
         const bool rescale = !first && __any_sync(0xffffffffu, grow);
         const int sg = it % NS;
         bool by_hand = false;
@@ -534,6 +537,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after();
         }
         if (rescale) {
+          const float c = grow ? ex2(mo - ref) : 1.f;  // ex2(-Inf) = 0
 #pragma unroll 1
           for (int d = 0; d < D; d += 32) {
             float o[32];
@@ -606,6 +610,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&pready[it % NS]);
+        l = (mg == m ? l : l * ex2(mg - ref)) + (sum2(sum[0]) + sum2(sum[1]));
+        mg = m;
       }
       it = it0 + n;
       // every product with this piece's Q is complete: the next one's can take its place, and its first
