@@ -365,7 +365,7 @@ cudaError_t attn_simt_launch(const AttnParams& p, spec_dtype dtype, int grid, cu
 cudaError_t attn_join_launch(const AttnParams& p, spec_dtype dtype, int sms, cudaStream_t stream) {
   const int64_t rows = static_cast<int64_t>(p.B) * p.R * p.Hkv * p.G;
   if (rows > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  const bool many = rows >= 6 * static_cast<int64_t>(sms);
+  const bool many = rows >= 4 * static_cast<int64_t>(sms);
   const dim3 g(static_cast<unsigned>(many ? (rows + 3) / 4 : rows)), t(many ? 128 : 256);
   if (dtype == SPEC_BF16)
     return many ? launch_pdl(attn_join_kernel<__nv_bfloat16, 1>, g, t, 0, stream, p)

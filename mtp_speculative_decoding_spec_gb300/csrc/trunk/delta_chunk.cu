@@ -375,9 +375,10 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
 }
 
 // ------------------------------------------------------------------------- the chain of chunks
-// Grid (rec_dv / 16, H, B), in clusters of blocks of one head, which read the same K, Q, T and scores:
-// each loads a share of them and multicasts it to all. Warps 0-3 carry the chain (k S, u, S), warps
-// 4-7 make the outputs beside it (q S, scores times u), warps 8 and 9 load for them.
+// Grid (rec_dv / 16, H, B). Warps 0-3 carry the chain (k S, u, S), warps 4-7 make the outputs beside it
+// (q S, scores times u), warps 8 and 9 load for them. A head's blocks read the same K, Q, T and scores at
+// about the same time, from L2 all but once (clusters of them with multicast copies: no faster, and slower
+// where not all clusters fit at once).
 //   chain   k S -> r -> | u | S' -> |      | three barriers of the four warps a chunk
 //   output  q S    ...    scores u, store
 // A warp of the chain has two tiles of eight tokens (w and 7 - w: the same work under causality) and a
@@ -406,49 +407,19 @@ struct ChainMaps {
   CUtensorMap k, q, v;  // [rows][columns], boxes of 64 x 64 (swizzled) and 16 x 64
 };
 
-// A box of 64 rows (a run of bytes) to this block, or to the same place in all blocks of the cluster, the
-// bytes counted on each one's barrier.
-__device__ __forceinline__ void tma_box(void* dst, const CUtensorMap* map, int x, int y, uint32_t bar,
-                                        int cs, uint16_t mask) {
-  if (cs > 1)
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        ".multicast::cluster [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar), "h"(mask)
-        : "memory");
-  else
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
-        : "memory");
+__device__ __forceinline__ void tma_box(void* dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+      : "memory");
 }
-__device__ __forceinline__ void bulk_copy(void* dst, const void* src, uint32_t bytes, uint32_t bar,
-                                          int cs, uint16_t mask) {
-  if (cs > 1)
-    asm volatile(
-        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.multicast::cluster"
-        " [%0], [%1], %2, [%3], %4;" ::"r"(smem_u32(dst)),
-        "l"(src), "r"(bytes), "r"(bar), "h"(mask)
-        : "memory");
-  else
-    asm volatile(
-        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-            smem_u32(dst)),
-        "l"(src), "r"(bytes), "r"(bar)
-        : "memory");
-}
-// Arrive on `bar` of every block of the cluster: lanes 0..cs-1 of a warp that is done with a stage. Nothing
-// is published but that the stage has been read, so no fence of the cluster's scope (measured at about
-// 1,100 cycles a time) goes with it.
-__device__ __forceinline__ void arrive_all(uint64_t* bar, int lane, int cs) {
-  __syncwarp();
-  if (lane < cs) {
-    uint32_t remote;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_u32(bar)), "r"(lane));
-    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(remote)
-                 : "memory");
-  }
+__device__ __forceinline__ void bulk_copy(void* dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          smem_u32(dst)),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
 }
 
 // Barriers between the groups of warps. Both go through the same chunks whatever happens, so each
@@ -463,7 +434,7 @@ __device__ __forceinline__ void bar_arrive(int id, int threads) {
 
 __global__ void __launch_bounds__(kChainThreads, 1)
     delta_chain_kernel(const __grid_constant__ ChainMaps maps, const __grid_constant__ DeltaParams p,
-                       const uint8_t* rec, int cs) {
+                       const uint8_t* rec) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -475,25 +446,24 @@ __global__ void __launch_bounds__(kChainThreads, 1)
   uint8_t* ups = rps + 3 * kUPlane;             // of e^(G_last - G) u
   uint8_t* ops = ups + 3 * kUPlane;             // of u
   uint64_t* cfull = reinterpret_cast<uint64_t*>(sps + kWork);
-  uint64_t* cempty = cfull + kCStages;  // all blocks of the cluster are done with the stage
+  uint64_t* cempty = cfull + kCStages;
   uint64_t* ofull = cempty + kCStages;
   uint64_t* oempty = ofull + kOStages;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int h = blockIdx.y, kh = h / (p.H / p.Hk);
-  const int col0 = blockIdx.x * kCols, rank = blockIdx.x % cs;
+  const int col0 = blockIdx.x * kCols;
   if (tid == 0) {
     for (int s = 0; s < kCStages; ++s) {
       mbar_init(&cfull[s], 1);
-      mbar_init(&cempty[s], 4 * cs);
+      mbar_init(&cempty[s], 4);
     }
     for (int s = 0; s < kOStages; ++s) {
       mbar_init(&ofull[s], 1);
-      mbar_init(&oempty[s], 4 * cs);
+      mbar_init(&oempty[s], 4);
     }
     fence_mbar_init();
   }
   __syncthreads();
-  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
   pdl_wait();
   // The longest request first: blocks are dealt out in order, and what starts last should be short.
   int b = blockIdx.z;
@@ -540,7 +510,6 @@ __global__ void __launch_bounds__(kChainThreads, 1)
     uint64_t* full = chain ? cfull : ofull;
     uint64_t* empty = chain ? cempty : oempty;
     const uint8_t* base = rec + (static_cast<int64_t>(first_slot(c0, b)) * p.H + h) * kRec;
-    const uint16_t mask = static_cast<uint16_t>((1u << cs) - 1);
     int c = 0;
     for (; c < n && warp < 10; ++c) {
       const int s = c % stages;
@@ -553,23 +522,20 @@ __global__ void __launch_bounds__(kChainThreads, 1)
         uint8_t* st = (chain ? smem : sq) + s * kTile;
         uint8_t* rest = chain ? crest + s * kCRest : orest + s * kORest;
         mbar_arrive_expect_tx(&full[s], kTile + (chain ? kCRest : kORest));
-        if (chain) tma_box(rest + kTBytes + kVecBytes, &maps.v, h * p.dv + col0, row, bar, 1, 0);
-        // pieces: two panels of K or Q, the planes of T or of the scores, the vectors
-        const int planes = chain ? 3 : 2;
-        for (int i = rank; i < 3 + planes; i += cs) {
-          if (i < 2)
-            tma_box(st + i * kPanel, chain ? &maps.k : &maps.q, kh * kDk + i * 64, row, bar, cs, mask);
-          else if (i < 2 + planes)
-            bulk_copy(rest + (i - 2) * kTri, r + (chain ? 0 : kTBytes) + (i - 2) * kTri, kTri, bar, cs, mask);
-          else
-            bulk_copy(rest + planes * kTri, r + kTBytes + kABytes, kVecBytes, bar, cs, mask);
+        for (int i = 0; i < 2; ++i)
+          tma_box(st + i * kPanel, chain ? &maps.k : &maps.q, kh * kDk + i * 64, row, bar);
+        if (chain) {
+          bulk_copy(rest, r, kTBytes, bar);
+          bulk_copy(rest + kTBytes, r + kTBytes + kABytes, kVecBytes, bar);
+          tma_box(rest + kTBytes + kVecBytes, &maps.v, h * p.dv + col0, row, bar);
+        } else {
+          bulk_copy(rest, r + kTBytes, kABytes + kVecBytes, bar);
         }
       }
     }
     ok = true;
     for (int j = max(0, c - stages); j < c; ++j) {  // nothing is left in flight
       wait(&full[j % stages], (j / stages) & 1);
-      wait(&empty[j % stages], (j / stages) & 1);
     }
   } else if (warp >= 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOutRegs));
@@ -639,7 +605,8 @@ __global__ void __launch_bounds__(kChainThreads, 1)
           *reinterpret_cast<uint32_t*>(dst + 8) = w1;
         }
       }
-      arrive_all(&oempty[s], lane, cs);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&oempty[s]);
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kChainRegs));
@@ -804,7 +771,8 @@ __global__ void __launch_bounds__(kChainThreads, 1)
           ldm4t(k0 + swz(16 * i + kr, kc + 2), kt[i] + 4);
         }
       }
-      arrive_all(&cempty[s], lane, cs);  // everything of the stage is in registers
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&cempty[s]);  // everything of the stage is in registers
       if (c > 0) bar_sync(kBarUsed, 256);
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
@@ -861,50 +829,6 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       }
     if (n > 0) bar_sync(kBarUsed, 256);  // the outputs' last turn
   }
-  // the cluster's copies and arrivals come to this block's memory until all are done
-  __syncwarp();
-  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
-}
-
-// How many clusters of cs blocks fit on the device at once; asked once per device and size.
-int clusters_at_once(int cs, cudaLaunchConfig_t cfg) {
-  static std::atomic<int> known[64][4];  // zero: not asked yet
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 1;
-  std::atomic<int>& slot = known[dev][cs == 8 ? 3 : cs == 4 ? 2 : cs == 2 ? 1 : 0];
-  int fit = slot.load(std::memory_order_relaxed);
-  if (fit != 0) return fit;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = cs;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaOccupancyMaxActiveClusters(&fit, delta_chain_kernel, &cfg) != cudaSuccess || fit < 1) {
-    cudaGetLastError();
-    fit = 1;
-  }
-  slot.store(fit, std::memory_order_relaxed);
-  return fit;
-}
-
-// Blocks of a cluster: the most (up to 8, dividing the head's blocks) with which the grid still runs in
-// as few turns as it can. A larger cluster reads K, Q, T and the scores fewer times; how many of a size
-// fit at once depends on the device's floor plan (16 heads of 8 blocks ran in two turns as clusters of
-// eight where fewer than 16 of those fitted: 1,122 us against ~560 for one turn).
-int cluster_size(int slices, int64_t heads, const cudaLaunchConfig_t& cfg) {
-  int best = 1;
-  int64_t turns = -1;
-  for (int cs = 8; cs >= 1; cs /= 2) {
-    if (slices % cs != 0) continue;
-    const int fit = clusters_at_once(cs, cfg);
-    const int64_t t = (slices / cs * heads + fit - 1) / fit;
-    if (turns < 0 || t < turns) {
-      turns = t;
-      best = cs;
-    }
-  }
-  return best;
 }
 
 }  // namespace
@@ -949,23 +873,8 @@ spec_status delta_chunk_launch(const DeltaParams& p, void* workspace, EncodeTile
       !map(&m.q, p.q, static_cast<int64_t>(p.Hk) * kDk, p.qs, 64, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !map(&m.v, p.v, static_cast<int64_t>(p.H) * p.dv, p.vs, kCols, CU_TENSOR_MAP_SWIZZLE_NONE))
     return SPEC_ERR_CUDA;
-  const int slices = p.dv / kCols;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(slices, p.H, p.B);
-  cfg.blockDim = dim3(kChainThreads);
-  cfg.dynamicSmemBytes = kChainSmem;
-  cfg.stream = stream;
-  const int cs = cluster_size(slices, static_cast<int64_t>(p.H) * p.B, cfg);
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = cs;
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, delta_chain_kernel, m, p, static_cast<const uint8_t*>(rec), cs) ==
-                 cudaSuccess
+  return launch_pdl(delta_chain_kernel, dim3(p.dv / kCols, p.H, p.B), dim3(kChainThreads), kChainSmem, stream,
+                    m, p, static_cast<const uint8_t*>(rec)) == cudaSuccess
              ? SPEC_OK
              : SPEC_ERR_CUDA;
 }

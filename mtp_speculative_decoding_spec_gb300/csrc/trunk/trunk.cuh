@@ -42,7 +42,7 @@ __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity) {
 
 cudaError_t delta_scan_launch(const DeltaParams& p, spec_dtype dtype, int sms, cudaStream_t stream);
 
-constexpr int kDeltaChunkRows = 16;
+constexpr int kDeltaChunkRows = 32;
 bool delta_chunk_sizes(int dk, int dv);
 size_t delta_chunk_workspace(int64_t rows, int B, int H);
 bool delta_chunk_takes(const DeltaParams& p, spec_dtype dtype);
