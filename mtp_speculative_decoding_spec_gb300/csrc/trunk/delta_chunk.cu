@@ -424,7 +424,7 @@ __device__ __forceinline__ void bulk_copy(void* dst, const void* src, uint32_t b
 
 // Barriers between the groups of warps. Both go through the same chunks whatever happens, so each
 // side's turn always comes.
-enum : int { kBarChain = 1, kBarState = 2, kBarQs = 3, kBarU = 4, kBarUsed = 5 };
+enum : int { kBarChain = 1, kBarState = 2, kBarQs = 3, kBarU = 4, kBarUsed = 5, kBarStage = 6 };
 __device__ __forceinline__ void bar_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
@@ -510,6 +510,11 @@ __global__ void __launch_bounds__(kChainThreads, 1)
     uint64_t* full = chain ? cfull : ofull;
     uint64_t* empty = chain ? cempty : oempty;
     const uint8_t* base = rec + (static_cast<int64_t>(first_slot(c0, b)) * p.H + h) * kRec;
+    if (warp == 10)  // waits for the chain's stages in the place of its four warps
+      for (int c = 0; c < n; ++c) {
+        wait(&cfull[c % kCStages], (c / kCStages) & 1);
+        bar_sync(kBarStage, 160);
+      }
     int c = 0;
     for (; c < n && warp < 10; ++c) {
       const int s = c % stages;
@@ -634,18 +639,15 @@ __global__ void __launch_bounds__(kChainThreads, 1)
           for (int s = 0; s < 3; ++s) *reinterpret_cast<uint32_t*>(sps + s * kSPlane + at) = w[s];
         }
     };
-    // What a chunk's first phase takes from its stage, read while the chunk before ends
+    // What a chunk's first phase takes from its stage: K is read between the last products of the chunk
+    // before, as the registers of its other form come free
     uint32_t kb[8][4];
-    float v[2][4], ge[2][2], le[2][2];
+    float v[2][4], ge[2][2];
     int len = 0;
     auto open_stage = [&](int c) {
-      wait(&cfull[c % kCStages], (c / kCStages) & 1);
-      uint8_t* st = smem + (c % kCStages) * kTile;
-      const uint8_t* rest = crest + (c % kCStages) * kCRest;
-      const float* eg = reinterpret_cast<const float*>(rest + kTBytes);
-      const uint8_t* sv = rest + kTBytes + kVecBytes;
       len = min(kC, c1 - c0 - c * kC);
       if (len < kC) {
+        uint8_t* st = smem + (c % kCStages) * kTile;
         // rows past the request's end are another's: what they hold must not reach S even times 0
         for (int i = tid; i < (kC - len) * 16; i += 128) {
           const int r = len + (i >> 4), pc = i & 15;
@@ -653,9 +655,14 @@ __global__ void __launch_bounds__(kChainThreads, 1)
         }
         bar_sync(kBarChain, 128);
       }
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        ldm4(smem_u32(st) + (i >> 2) * kPanel + swz(bt, (i & 3) * 2 + bc), kb[i]);
+    };
+    auto load_k = [&](int c, int i) {
+      ldm4(smem_u32(smem + (c % kCStages) * kTile) + (i >> 2) * kPanel + swz(bt, (i & 3) * 2 + bc), kb[i]);
+    };
+    auto load_rest = [&](int c) {
+      const uint8_t* rest = crest + (c % kCStages) * kCRest;
+      const float* eg = reinterpret_cast<const float*>(rest + kTBytes);
+      const uint8_t* sv = rest + kTBytes + kVecBytes;
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         const int tile = t ? tr : tl, tok = tile * 8 + 2 * q;
@@ -667,18 +674,21 @@ __global__ void __launch_bounds__(kChainThreads, 1)
           v[t][2 * half + 1] = hi_of(x);
         }
         ge[t][0] = -eg[tok], ge[t][1] = -eg[tok + 1];
-        le[t][0] = eg[kC + tok], le[t][1] = eg[kC + tok + 1];
       }
     };
     if (n > 0) {
+      bar_sync(kBarStage, 160);
       open_stage(0);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) load_k(0, i);
+      load_rest(0);
       put_state();
     }
     for (int c = 0; c < n; ++c) {
       const int s = c % kCStages;
       const uint8_t* rest = crest + s * kCRest;
       const uint32_t k32 = smem_u32(smem + s * kTile), t32 = smem_u32(rest);
-      const float all = reinterpret_cast<const float*>(rest + kTBytes)[2 * kC];
+      const float* eg = reinterpret_cast<const float*>(rest + kTBytes);
       bar_sync(kBarChain, 128);  // the parts of S are there
       // k S of the warp's tokens, the parts of S in sums of their own
       float x[3][2][4] = {};
@@ -771,6 +781,13 @@ __global__ void __launch_bounds__(kChainThreads, 1)
           ldm4t(k0 + swz(16 * i + kr, kc + 2), kt[i] + 4);
         }
       }
+      const float all = eg[2 * kC];
+      float le[2][2];
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const int tok = (t ? tr : tl) * 8 + 2 * q;
+        le[t][0] = eg[kC + tok], le[t][1] = eg[kC + tok + 1];
+      }
       __syncwarp();
       if (lane == 0) mbar_arrive(&cempty[s]);  // everything of the stage is in registers
       if (c > 0) bar_sync(kBarUsed, 256);
@@ -792,7 +809,12 @@ __global__ void __launch_bounds__(kChainThreads, 1)
         }
       }
       bar_arrive(kBarU, 256);
-      bar_sync(kBarChain, 128);
+      if (c + 1 < n) {
+        bar_sync(kBarStage, 160);
+        open_stage(c + 1);
+      } else {
+        bar_sync(kBarChain, 128);
+      }
       // S <- e^G_last S + sum over tokens; the sum in accumulators of its own, joined by one rounding
       float d[4][4] = {};
       {
@@ -809,9 +831,13 @@ __global__ void __launch_bounds__(kChainThreads, 1)
           for (int j = 2; j >= 0; --j)
 #pragma unroll
             for (int t = 0; t < 4; ++t) mma(d[t], a[i & 1][j], kt[i][2 * t], kt[i][2 * t + 1]);
+          if (c + 1 < n) {
+            load_k(c + 1, 2 * i);
+            load_k(c + 1, 2 * i + 1);
+          }
         }
       }
-      if (c + 1 < n) open_stage(c + 1);
+      if (c + 1 < n) load_rest(c + 1);
 #pragma unroll
       for (int t = 0; t < 4; ++t)
 #pragma unroll
