@@ -56,6 +56,12 @@ __device__ __forceinline__ void ldm4t(uint32_t a, uint32_t* r) {
                : "r"(a)
                : "memory");
 }
+// The counterpart: a product's results, packed in pairs, to rows of shared memory.
+__device__ __forceinline__ void stm4(uint32_t a, uint32_t r0, uint32_t r1, uint32_t r2, uint32_t r3) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(r0), "r"(r1),
+               "r"(r2), "r"(r3)
+               : "memory");
+}
 __device__ __forceinline__ void mma(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
       "{%0,%1,%2,%3};"
@@ -626,18 +632,22 @@ __global__ void __launch_bounds__(kChainThreads, 1)
         const int dim = 32 * warp + 8 * t + 2 * q + (e & 1), col = g + 8 * (e >> 1);
         S[t][e] = p.init ? p.init[off + static_cast<int64_t>(dim) * p.dv + col] : 0.f;
       }
+    // where a lane's row of four stored matrices lies: columns g and g + 8 (lane / 8, odd), and of two
+    // pieces of 8 dims or tiles of tokens
+    const int mr = (lane & 7) + (lane & 8), mh = lane >> 4;
+    const uint32_t s_at = sp + (warp >> 1) * (kSPlane / 2) + swz(mr, 4 * (warp & 1) + mh);
+    const uint32_t u_at = swz(mr, mh ? tr : tl);
     auto put_state = [&]() {
 #pragma unroll
-      for (int t = 0; t < 4; ++t)
+      for (int t = 0; t < 4; t += 2) {  // dims 32 w + 8 t: panel w / 2, 16-byte piece 4 (w & 1) + t
+        uint32_t w[4][3];
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          uint32_t w[3];
-          split<3>(S[t][2 * half], S[t][2 * half + 1], w);
-          // dim 32 w + 8 t: panel w / 2, 16-byte piece 4 (w & 1) + t
-          const int at = (warp >> 1) * (kSPlane / 2) + swz(g + 8 * half, 4 * (warp & 1) + t) + 4 * q;
+        for (int i = 0; i < 4; ++i)
+          split<3>(S[t + (i >> 1)][2 * (i & 1)], S[t + (i >> 1)][2 * (i & 1) + 1], w[i]);
 #pragma unroll
-          for (int s = 0; s < 3; ++s) *reinterpret_cast<uint32_t*>(sps + s * kSPlane + at) = w[s];
-        }
+        for (int k = 0; k < 3; ++k)
+          stm4((s_at ^ (t << 4)) + k * kSPlane, w[0][k], w[1][k], w[2][k], w[3][k]);
+      }
     };
     // What a chunk's first phase takes from its stage: K is read between the last products of the chunk
     // before, as the registers of its other form come free
@@ -719,23 +729,21 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       for (int i = 0; i < 3; ++i)
         if (i <= tr / 2) load_t(i);
       // r = v - e^G (k S)
+      {
+        uint32_t w[4][3];
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        const int tile = t ? tr : tl, tok = tile * 8 + 2 * q;
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
+        for (int i = 0; i < 4; ++i) {
+          const int t = i >> 1, tok = (t ? tr : tl) * 8 + 2 * q;
           float r[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const int k = 2 * half + e;
+            const int k = 2 * (i & 1) + e;
             r[e] = tok + e < len ? fmaf(ge[t][e], x[0][t][k] + (x[1][t][k] + x[2][t][k]), v[t][k]) : 0.f;
           }
-          uint32_t w[3];
-          split<3>(r[0], r[1], w);
-          const int at = swz(g + 8 * half, tile) + 4 * q;
-#pragma unroll
-          for (int i = 0; i < 3; ++i) *reinterpret_cast<uint32_t*>(rps + i * kUPlane + at) = w[i];
+          split<3>(r[0], r[1], w[i]);
         }
+#pragma unroll
+        for (int k = 0; k < 3; ++k) stm4(rp + u_at + k * kUPlane, w[0][k], w[1][k], w[2][k], w[3][k]);
       }
       bar_sync(kBarChain, 128);
       // u = T r, the terms by size in sums of their own
@@ -791,22 +799,20 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&cempty[s]);  // everything of the stage is in registers
       if (c > 0) bar_sync(kBarUsed, 256);
+      {
+        uint32_t w[4][3], z[4][2];
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        const int tile = t ? tr : tl;
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const int at = swz(g + 8 * half, tile) + 4 * q, k = 2 * half;
+        for (int i = 0; i < 4; ++i) {
+          const int t = i >> 1, k = 2 * (i & 1);
           const float y0 = u[0][t][k] + (u[1][t][k] + u[2][t][k]);
           const float y1 = u[0][t][k + 1] + (u[1][t][k + 1] + u[2][t][k + 1]);
-          uint32_t w[3], z[2];
-          split<3>(le[t][0] * y0, le[t][1] * y1, w);
-          split<2>(y0, y1, z);
-#pragma unroll
-          for (int i = 0; i < 3; ++i) *reinterpret_cast<uint32_t*>(ups + i * kUPlane + at) = w[i];
-#pragma unroll
-          for (int i = 0; i < 2; ++i) *reinterpret_cast<uint32_t*>(ops + i * kUPlane + at) = z[i];
+          split<3>(le[t][0] * y0, le[t][1] * y1, w[i]);
+          split<2>(y0, y1, z[i]);
         }
+#pragma unroll
+        for (int k = 0; k < 3; ++k) stm4(up + u_at + k * kUPlane, w[0][k], w[1][k], w[2][k], w[3][k]);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) stm4(op + u_at + k * kUPlane, z[0][k], z[1][k], z[2][k], z[3][k]);
       }
       bar_arrive(kBarU, 256);
       if (c + 1 < n) {
