@@ -1,16 +1,17 @@
 // Attention of the verify rows over a shared prefix and each request's own cache on the tcgen05
 // tensor cores: bf16, head_dim 64, 128 or 256. Units, pieces and partials as in trunk.cuh.
 //
-// Per block of kBn positions: S = Q K^T (Q in TMEM, 128 rows x kBn), a row's softmax by two
-// threads (TMEM lane = row, no shuffles), the weights as bf16 back into the columns of S, O += P V with P
+// Per block of kBn positions: S = Q K^T (Q in TMEM, 128 rows x kBn), a row's softmax by one thread
+// (TMEM lane = row, no shuffles), the weights as bf16 back into the columns of S, O += P V with P
 // in TMEM too and V as it lies in the cache (rows of positions: the B operand is N-major).
 //   * warp 0 loads K and V blocks by TMA; Q is gathered by the softmax threads into TMEM, so that
 //     its 128 rows are not read from shared memory again for every block;
 //   * warp 1 issues the MMAs: S of block i+1 goes out before O of block i, so the tensor pipe works
 //     on one while the softmax works on the other (two S buffers);
-//   * warps 4..11 do the softmax, two threads a row; warps 2 and 3 watch V (below). The reference a row's weights are taken against moves only when the
-//     row's maximum has grown by more than 2^8 (the weights stay below 256 and their sum and O are
-//     fp32, so nothing is lost), which makes rescaling O in TMEM rare.
+//   * warps 4..7 and 8..11 do the softmax of the blocks in turns; warps 2 and 3 watch V (below). The
+//     reference a row's weights are taken against moves only when the row's maximum has grown by more
+//     than 2^8 (the weights stay below 256 and their sum and O are fp32, so nothing is lost), which makes
+//     rescaling O in TMEM rare.
 // Weights are rounded to bf16 for the tensor cores (2^-9 of each weight, as the outputs are); their
 // sum is taken in fp32 before that.
 //
@@ -18,6 +19,13 @@
 // be 0. In blocks where any running row's positions end, two guard warps therefore look through V as
 // it lands, ahead of the softmax: non-finite values that no row sees are cleared, and where a row
 // does see one, that row's share of it is added by hand and the value cleared for the tensor cores.
+//
+// 16 query heads on 4 KV heads of 256 dims: 256 rows over 63,488 shared positions and 700 own ones each,
+// 191 us with the join = 1.40 PFLOP/s (0.73 of cuBLAS); a block of 64 positions takes about 1,500 cycles
+// against 1,024 of the tensor pipe, the rest the way from a block's scores through its softmax to its
+// second product, which two buffers of S hide in part. Two rows of one request over its own 63,488: 50.5
+// us = 5.2 TB/s (0.76 of a copy), eight single rows over a shared 63,488 60 us = 5.0 TB/s: HBM while the
+// blocks run, and some 18 us of launch, plan, first loads, partials and join around them.
 #include <math.h>
 
 #include <cuda_bf16.h>
@@ -33,13 +41,17 @@ constexpr int kTm = 128;
 constexpr int kThreads = 12 * 32;  // producer, MMA and two guard warps, eight softmax warps
 constexpr int kSoftThreads = 256;
 // Registers a thread: launched with 168 (64,512 in all); the first four warps give to the softmax's
-// eight: 128 x 96 + 256 x 200 = 63,488.
+// eight: 128 x 152 + 256 x 176 = 64,512. (104 and 200 spill in the guards: 214 us for 191.)
 constexpr int kFewRegs = 152, kSoftRegs = 176;
+// Bits that a row's maximum may grow by before its reference moves: 256 rows over 63,488 positions 260 us
+// with 0, 192 with 8.
 constexpr float kLazy = 8.f;
 
 template <int D>
 struct Shape {
-  static constexpr int kBn = D == 256 ? 64 : 128;  // K and V blocks of 16 or 32 KB
+  // K and V blocks of 16 or 32 KB. 128 dims in blocks of 64 positions took 168 us for 151 (256 rows over
+  // 63,488); 256 dims in blocks of 128 do not fit beside two buffers of S.
+  static constexpr int kBn = D == 256 ? 64 : 128;
   static constexpr int kStages = D == 64 ? 6 : 3;
   static constexpr int kTile = kBn * D * 2;
   static constexpr int kPanel = kBn * 128;          // 64 dims of a block: rows of 128 bytes

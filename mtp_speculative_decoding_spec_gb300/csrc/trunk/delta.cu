@@ -14,7 +14,11 @@
 // the rank-one update; no block barrier. Rows come in groups of eight through the warp's own piece of
 // shared memory, the next group's copies in flight while one is computed: a verify pass waits for
 // memory once, not once a row. Bound by the state's bytes when there are many requests (read once, one
-// write per snapshot), by the latency of the row chain when there are few.
+// write per snapshot), by the latency of the row chain when there are few. 16 heads of [128, 128], bf16
+// rows: 32 requests x up to 8 rows, snapshots 40.5 us = 5.4 TB/s (0.80 of a copy's 6.79); replay, which
+// moves a third of that, 26.5 us = 2.7 TB/s, two and a half turns of the warps that fit, each load,
+// row chain and store one after another; 1 x 8 rows, index 6.4 us. (Turns of one set of warps, the next
+// tile's state copied ahead to shared memory: replay 34.5 us, snapshots 45.0.)
 #include <math.h>
 
 #include <cuda_bf16.h>
@@ -115,7 +119,8 @@ struct Staged {
 
 // One warp to a block: no warp needs another, and warps that end make room one by one. Blocks an SM: as
 // many as the state's registers allow. With many requests it is the warps in flight that count (32
-// requests x 8 rows, replay: 29.6 us with eight, 24.1 with twelve).
+// requests x 8 rows of [128, 128]: replay 32.1 us with eight, 26.5 with eleven; snapshots 47.4 and 40.6).
+// Of the tiles with fewer rows a lane, more than 16 do not help (1 x 8 rows, index: 6.4 us, 7.6 with 24).
 template <typename T, int NI>
 constexpr int kScanBlocks = NI >= 16 ? (sizeof(T) == 2 ? 11 : 10) : 16;
 
@@ -354,8 +359,10 @@ cudaError_t launch_scan(const DeltaParams& p, cudaStream_t stream) {
 
 template <typename T>
 cudaError_t scan_of(const DeltaParams& p, int sms, cudaStream_t stream) {
-  // Tiles of 8 columns instead of 16 while 16-column tiles leave SMs without a warp: the row chain
-  // is half as long for the same work in total.
+  // Tiles of 8 columns instead of 16 while 16-column tiles would not give every SM two warps: the row chain
+  // is half as long for the same work in total. 16 heads of [128, 128] x 8 rows, index, tiles of 8 and of
+  // 16 columns: one request 6.4 and 8.8 us, two 7.5 and 8.9, three 9.4 and 9.0, four 10.5 and 9.6; 32
+  // requests, replay, 32.8 and 26.5. A lane's rows follow rec_dk, so that no registers hold nothing.
   const int64_t warps = static_cast<int64_t>((p.dv + 15) / 16) * p.H * p.B;
   if (warps < 2 * sms && p.dk <= 128) {
     if (p.dk <= 16) return launch_scan<T, 1, 2>(p, stream);

@@ -16,6 +16,11 @@
 // chunk. S, u and T are fp32. q, k and v are bf16 as given; S, u, T enter products as sums of three
 // bf16 (24 bits), with the product terms below 2^-24 left out, and sums are fp32: the state is as
 // exact as fp32 arithmetic leaves it. Where only a bf16 output is made, two parts are enough.
+//
+// 16 heads of [128, 128], one prompt of 15,360 rows: 471 us, of which 74 the first kernel (0.25 GB, 3.3
+// TB/s) and 1.65 us a chunk the second; 63,488 rows 1.92 ms. q, k, v and the outputs alone would take 38
+// us: what bounds it is the chain's latency, some 3,300 cycles a chunk in which an SM's sub-core has one
+// warp of the chain and one of the outputs, its matrix instructions (198 of 8.3 cycles) half the time.
 #include <math.h>
 
 #include <cuda_bf16.h>
@@ -383,19 +388,20 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
 // ------------------------------------------------------------------------- the chain of chunks
 // Grid (rec_dv / 16, H, B). Warps 0-3 carry the chain (k S, u, S), warps 4-7 make the outputs beside it
 // (q S, scores times u), warps 8 and 9 load for them. A head's blocks read the same K, Q, T and scores at
-// about the same time, from L2 all but once (clusters of them with multicast copies: no faster, and slower
-// where not all clusters fit at once).
+// about the same time, from L2 all but once (clusters of 2 and 4 with multicast copies took the same
+// time, of 8 885 us against 488: too few of those fit at once).
 //   chain   k S -> r -> | u | S' -> |      | three barriers of the four warps a chunk
 //   output  q S    ...    scores u, store
 // A warp of the chain has two tiles of eight tokens (w and 7 - w: the same work under causality) and a
 // quarter of S's rows. What a phase multiplies by (K, T) is read into registers before the barrier
-// that its other operand waits for. (S kept in registers as the next chunk's operand, its four partial
+// that its other operand waits for. Warp 10 waits for the chain's stages in its place: even over, a
+// wait for a copy costs a warp 100 to 250 cycles, a named barrier 25 (488 -> 472 us). (S kept in registers as the next chunk's operand, its four partial
 // products meeting in shared memory instead, moves fewer bytes but took 2.16 us a chunk.)
-constexpr int kChainThreads = 12 * 32;  // three groups of four warps; two of the last do nothing
+constexpr int kChainThreads = 12 * 32;  // three groups of four warps; the last one does nothing
 // Registers a thread: launched with 168 (64,512 in all), then shared out again by group, 63,488 in use.
 constexpr int kChainRegs = 224, kOutRegs = 168, kLoadRegs = 104;
 constexpr int kCStages = 3, kOStages = 3;
-constexpr int kSortMost = 256;  // requests that are put in order
+constexpr int kSortMost = 256;  // requests that are put in order (their lengths lie in the place of S)
 constexpr int kVTile = kC * kCols * 2;
 // Beside K (Q), whose tiles start on 1,024 bytes: T, vectors, V for the chain, scores and vectors for
 // the outputs.
@@ -471,7 +477,8 @@ __global__ void __launch_bounds__(kChainThreads, 1)
   }
   __syncthreads();
   pdl_wait();
-  // The longest request first: blocks are dealt out in order, and what starts last should be short.
+  // The longest request first: blocks are dealt out in order, and what starts last should be short (prompts
+  // of 0, 1, 77, 1,000 and 2,311 rows: 124 us, 134 in the order given).
   int b = blockIdx.z;
   if (p.B > 1 && p.B <= kSortMost) {
     int* lens = reinterpret_cast<int*>(sps);
@@ -516,7 +523,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
     uint64_t* full = chain ? cfull : ofull;
     uint64_t* empty = chain ? cempty : oempty;
     const uint8_t* base = rec + (static_cast<int64_t>(first_slot(c0, b)) * p.H + h) * kRec;
-    if (warp == 10)  // waits for the chain's stages in the place of its four warps
+    if (warp == 10)
       for (int c = 0; c < n; ++c) {
         wait(&cfull[c % kCStages], (c / kCStages) & 1);
         bar_sync(kBarStage, 160);
@@ -871,7 +878,12 @@ size_t delta_chunk_workspace(int64_t rows, int B, int H) {
   return sizeof(WsHeader) + static_cast<size_t>(rows / kC + B) * H * kRec;
 }
 
-// Below this many tokens a request (on average) a chunk's fixed work outweighs the row scan's.
+// With fewer tokens a request (on average) the row scan takes the call: a chunk costs the same however
+// few of its rows there are, and a block an SM at a time. 16 heads of [128, 128], scan and chunks: one
+// request of 16 rows 8.7 and 12.2 us, of 32 15.3 and 12.2, of 64 28.4 and 12.5; eight of 32 26.0 and
+// 44.6, of 64 48.8 and 45.6; 32 of 16 44.5 and 156, of 32 80.0 and 157, of 64 151 and 160. One request of
+// 15,360 7,549 and 488: with the limit any lower or higher, the worse of its two sides costs more, since
+// the host does not know whether the rows are spread evenly.
 bool delta_chunk_takes(const DeltaParams& p, spec_dtype dtype) {
   return dtype == SPEC_BF16 && delta_chunk_sizes(p.dk, p.dv) && p.vec_qk && p.vec_o &&
          (reinterpret_cast<uintptr_t>(p.v) & 15u) == 0 && p.vs % 8 == 0 && p.H <= 65535 &&

@@ -86,8 +86,12 @@ struct AttnParams {
 
 constexpr int kAttnMaxItems = 8192;
 constexpr int64_t kAttnMaxPos = (int64_t(1) << 31) - 256;  // a block past the last one still has an int
-constexpr int kAttnOver = 6;    // see `over`
-constexpr int kAttnGroup = 16;  // most of `grp`
+// See `over`. 256 rows over a prefix of 15,360 and 700 own positions each, 0, 4 and 6: 100.8, 80.5 and 79.3
+// us (63,488: 195.7, 190.1, 191.6); eight requests of eight rows over 3,000: 30.3, 27.6, 24.8.
+constexpr int kAttnOver = 6;
+// The most of `grp`. 256 rows (8 tiles) over 63,488 positions, groups of 1, 4 and 8: 211, 194 and 192 us;
+// 40 rows of 4 heads (2 tiles) singly and in pairs: 104 and 68 us.
+constexpr int kAttnGroup = 16;
 
 // Of request b: the rows that run, the positions of the prefix it sees and of its own cache before them.
 struct AttnReq {
@@ -341,7 +345,9 @@ cudaError_t attn_simt_launch(const AttnParams& p, spec_dtype dtype, int grid, cu
 cudaError_t attn_join_launch(const AttnParams& p, spec_dtype dtype, int sms, cudaStream_t stream);
 int attn_simt_tm();
 int attn_simt_bn();
-bool attn_tc_takes(int head_dim);  // bf16 only
+// Head sizes of the tensor-core kernel, bf16 alone. On the CUDA cores two rows over 63,488 positions of 256
+// dims take 379 us for 51, 32 rows of 64 dims over 15,360 306 for 20.
+bool attn_tc_takes(int head_dim);
 spec_status attn_tc_launch(const AttnParams& p, int grid, EncodeTiledFn encode, cudaStream_t stream);
 int attn_tc_tm();
 int attn_tc_bn(int head_dim);
