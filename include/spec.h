@@ -25,8 +25,8 @@
  *     returns SPEC_ERR_CUDA. Data-dependent problems never trap: they are written to the
  *     per-request status (spec_accept_out.status) and that request commits nothing.
  *   - Workspace: calls that reduce across thread blocks take a caller-allocated workspace of
- *     at least spec_workspace_bytes() bytes, 256-byte aligned, ZERO-FILLED ONCE before its
- *     first use. Every call leaves it reusable (its counters back at zero). Calls that may run
+ *     at least spec_workspace_bytes() bytes (the token mixers: their own _workspace_bytes()),
+ *     256-byte aligned, ZERO-FILLED ONCE before its first use. Every call leaves it reusable (its counters back at zero). Calls that may run
  *     concurrently (different streams) need separate workspaces. Byte offset 4 of the
  *     workspace holds a 32-bit error word that kernels set (never clear) if an internal
  *     bounded wait gives up; 0 means no error.
@@ -587,7 +587,7 @@ size_t spec_delta_prefill_workspace_bytes(int64_t rows, int32_t B, const spec_st
  *               in bytes. prefix_capacity positions are there, at most 2^31 - 256.
  *   prefix_len  [B] int64 (clamped to [0, prefix_capacity]), or NULL: all of prefix_capacity.
  *   lse         [B*R][q_heads] float32 or NULL: log sum exp(scale q k) of each row, -Inf where a
- *               row has nothing to see (its output is zero).
+ *               row has nothing to see, or sees scores of -Inf alone (its output is zero).
  */
 typedef struct {
   spec_dtype dtype;
