@@ -109,7 +109,7 @@ spec_status attn_plan_of(int32_t B, int32_t R, const spec_state_desc* st, const 
   w.grp = w.tc && npt >= 2 ? static_cast<int>((npt + sets - 1) / sets) : 1;
   const int64_t npi = (npt + w.grp - 1) / w.grp;
   const int64_t items = npi + B * nown;
-  const int64_t blocks = npi * ((prefix ? d->prefix_capacity : 0) / w.bn + 1 + kAttnOver) +
+  const int64_t blocks = npi * ((prefix ? d->prefix_capacity : 0) / w.bn + 1 + kAttnOverPre) +
                          B * nown * (st->kv_capacity / w.bn + 1 + kAttnOver);
   if (items > kAttnMaxItems || blocks >= (int64_t(1) << 31)) return SPEC_ERR_UNSUPPORTED;
   w.npt = static_cast<int>(npt);
@@ -241,7 +241,8 @@ spec_status spec_prefix_attention(int32_t B, int32_t R, const spec_state_desc* s
   p.npt = w.npt;
   p.npi = w.npi;
   p.grp = w.grp;
-  p.over = kAttnOver;
+  p.over[0] = kAttnOverPre;
+  p.over[1] = kAttnOver;
   p.nown = w.nown;
   p.items = w.items;
   p.q = d->q;

@@ -57,14 +57,14 @@ spec_status delta_chunk_launch(const DeltaParams& p, void* workspace, EncodeTile
 // slot of their own. Item = a tile of rows for all KV heads: prefix tiles first, then own tiles.
 // With `grp` > 1, prefix items are `grp` tiles each and are dealt to groups of as many neighbouring
 // CTAs, a tile to a CTA, before the own items are dealt to single CTAs: a group walks the same
-// positions at the same pace, so the prefix comes from HBM once and from L2 for the others. `over` is
-// what starting a unit costs, in blocks: it counts in the dealing as if the unit began with that many
-// blocks more.
+// positions at the same pace, so the prefix comes from HBM once and from L2 for the others. `over`
+// is what starting a prefix unit and an own unit costs, in blocks: it counts in the dealing as if the unit
+// began with that many blocks more (a prefix tile has four times the rows of queries and partials here).
 struct AttnParams {
   int B, R, G, Hkv, D;
   int tm, bn;
   int npt, npi, nown, items;  // prefix tiles and items, own tiles per request, npi + B * nown
-  int grp, over;
+  int grp, over[2];
   const void* q;
   int64_t qs;
   void* out;
@@ -86,9 +86,11 @@ struct AttnParams {
 
 constexpr int kAttnMaxItems = 8192;
 constexpr int64_t kAttnMaxPos = (int64_t(1) << 31) - 256;  // a block past the last one still has an int
-// See `over`. 256 rows over a prefix of 15,360 and 700 own positions each, 0, 4 and 6: 100.8, 80.5 and 79.3
-// us (63,488: 195.7, 190.1, 191.6); eight requests of eight rows over 3,000: 30.3, 27.6, 24.8.
-constexpr int kAttnOver = 6;
+// See `over`; own / prefix units at 0 / 0, 6 / 6, 6 / 10 and 4 / 10, us: 32 x 8 rows with 700 own positions each
+// over a prefix of 2,000 (100 own) 34.0, 33.8, 31.3, 30.6; of 15,360 87.9, 77.0, 75.5, 72.2; of 63,488 195.7,
+// 190.1, 189.0, 190.7; 64 rows over 63,488 76.0, 73.1, 70.3, 70.7; two rows over their own 63,488 52.5, 50.6,
+// 50.4, 51.2.
+constexpr int kAttnOver = 6, kAttnOverPre = 10;
 // The most of `grp`. 256 rows (8 tiles) over 63,488 positions, groups of 1, 4 and 8: 211, 194 and 192 us;
 // 40 rows of 4 heads (2 tiles) singly and in pairs: 104 and 68 us.
 constexpr int kAttnGroup = 16;
@@ -118,11 +120,11 @@ __host__ __device__ constexpr size_t attn_plan_bytes(int items, int B) {
 __device__ __forceinline__ AttnReq* attn_plan(const AttnParams& p, int32_t* cum) {
   const int tid = threadIdx.x, nt = blockDim.x, per = p.R * p.G;
   AttnReq* req = reinterpret_cast<AttnReq*>(cum + p.items + 1);
-  const auto cost = [&p](int n) { return n > 0 ? (n + p.bn - 1) / p.bn + p.over : 0; };
+  const auto cost = [&p](int n, int own) { return n > 0 ? (n + p.bn - 1) / p.bn + p.over[own] : 0; };
   for (int b = tid; b < p.B; b += nt) {
     const AttnReq r = attn_req(p, b);
     req[b] = r;
-    const int c = r.rows > 0 ? cost(attn_own(p, r, r.rows)) : 0;
+    const int c = r.rows > 0 ? cost(attn_own(p, r, r.rows), 1) : 0;
     for (int j = 0; j < p.nown; ++j) cum[p.npi + b * p.nown + j + 1] = c;
   }
   __syncthreads();
@@ -133,7 +135,7 @@ __device__ __forceinline__ AttnReq* attn_plan(const AttnParams& p, int32_t* cum)
     for (int b = b0 + (tid & 31); b <= b1; b += 32)
       if (req[b].rows > 0) n = max(n, req[b].prefix);
     n = __reduce_max_sync(0xffffffffu, n);
-    if ((tid & 31) == 0) cum[i + 1] = cost(n);
+    if ((tid & 31) == 0) cum[i + 1] = cost(n, 0);
   }
   if (tid == 0) cum[0] = 0;
   __syncthreads();
@@ -176,7 +178,7 @@ struct AttnShares {
     const int64_t rest = w - wp, more = rest - sp * (grid - in);
     s1 = more > 0 ? (more + grid - 1) / grid : 0;
     s2 = more > 0 ? s1 + sp : in < grid ? (rest + grid - in - 1) / (grid - in) : 0;
-    return s1 > 0 ? sp + s1 + p.over : max(sp, s2);
+    return s1 > 0 ? sp + s1 + p.over[1] : max(sp, s2);
   }
 };
 __device__ __forceinline__ AttnShares attn_shares(const AttnParams& p, const int32_t* cum) {
@@ -218,7 +220,7 @@ __device__ __forceinline__ void attn_write_units(const AttnParams& p, const int3
     int2 v = make_int2(0, 0);
     if (cost > 0) {
       const int64_t x = static_cast<int64_t>(cum[item]) * p.Hkv + static_cast<int64_t>(head) * cost;
-      const int64_t first = x + p.over, last = x + cost - 1;  // places of its first and last block
+      const int64_t first = x + p.over[item >= p.npi], last = x + cost - 1;  // places of its first and last block
       if (u < s.u1) {
         const int c0 = static_cast<int>(first / s.sp);
         v = make_int2(p.grp * (c0 + u), static_cast<int>(last / s.sp) - c0 + 1);
@@ -293,8 +295,9 @@ struct AttnWalk {
       const int v0 = at, v1 = static_cast<int>(min(static_cast<int64_t>(cost), v0 + left));
       at = v1;
       left -= v1 - v0;
-      a.blk0 = max(0, v0 - p.over);
-      a.blk1 = max(0, v1 - p.over);
+      const int over = p.over[item >= p.npi];
+      a.blk0 = max(0, v0 - over);
+      a.blk1 = max(0, v1 - over);
       if (a.blk0 == a.blk1) continue;
       a.head = head;
       const int u = item * p.Hkv + head;

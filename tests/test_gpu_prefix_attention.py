@@ -147,7 +147,13 @@ CASES = [
     dict(B=9, R=8, Hq=16, Hkv=4, D=256, P=1500, cap=200, kv_len=[11 * i for i in range(9)],
          dtype="bf16", prefix_len=[1500 - 150 * i for i in range(9)]),
     dict(B=9, R=8, Hq=16, Hkv=4, D=128, P=1500, cap=200, kv_len=[11 * i for i in range(9)],
-         dtype="bf16", prefix_len=[1500 - 150 * i for i in range(9)]),
+         dtype="bf16", prefix_len=[1500 - 150 * i for i in range(9)]),    # more tiles of rows than a group of CTAs takes, the last group not full
+    dict(B=17, R=8, Hq=16, Hkv=1, D=64, P=500, cap=40, kv_len=[2 * i for i in range(17)], dtype="bf16"),
+    dict(B=300, R=8, Hq=8, Hkv=2, D=128, P=333, cap=24, kv_len=[i % 17 for i in range(300)],
+         dtype="bf16", prefix_len=[333 - 37 * (i % 10) for i in range(300)],
+         n_rows=[i % 9 for i in range(300)]),
+    dict(B=1024, R=1, Hq=1, Hkv=1, D=256, P=70, cap=9, kv_len=[i % 9 for i in range(1024)],
+         dtype="bf16"),
 ]
 
 
