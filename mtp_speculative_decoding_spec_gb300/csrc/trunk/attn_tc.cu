@@ -54,6 +54,10 @@ struct Shape {
   static constexpr int kBn = D == 256 ? 64 : 128;
   static constexpr int kStages = D == 64 ? 6 : 3;
   static constexpr int kTile = kBn * D * 2;
+  // The product with V starts on the first half of a block's weights. At 128 positions: 142 -> 128 us (256
+  // rows of 128 dims over 63,488); at 64 the tensor pipe, in order, waits for the second half instead of
+  // taking the other buffer's scores: 191 -> 211 us (of 256 dims).
+  static constexpr bool kHalves = kBn == 128;
   static constexpr int kPanel = kBn * 128;          // 64 dims of a block: rows of 128 bytes
   static constexpr int kFixed = 2 * kStages * kTile;
   // TMEM columns: O, two S buffers, Q (two bf16 a column)
@@ -194,11 +198,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* vfull = kdone + NS;
   uint64_t* vdone = vfull + NS;   // O has the block, and the stage is free
   uint64_t* vok = vdone + NS;     // V has landed and been looked through
-  // P is written and V ok. One to a stage, as all of these: an arrival for block i + NS cannot come
+  // P (its first half, where there are halves) is written and V ok; its rest. One to a stage, as all of these: an arrival for block i + NS cannot come
   // before block i's product is complete, so no barrier takes it for an earlier block's, and none runs
   // through two phases while its waiter looks away.
   uint64_t* pready = vok + NS;
-  uint64_t* qready = pready + NS;
+  uint64_t* prest = pready + NS;
+  uint64_t* qready = prest + NS;
   uint64_t* meet = qready + 1;    // the softmax warps, [0] and [1] of a group, [2] all
   uint64_t* ofree = meet + 3;     // the piece's O has been read
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ofree + 1);
@@ -219,6 +224,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&vdone[s], 1);
       mbar_init(&vok[s], 2);
       mbar_init(&pready[s], 6);
+      mbar_init(&prest[s], 4);
     }
     mbar_init(qready, 8);
     mbar_init(&meet[0], 4);
@@ -319,8 +325,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t ps = tmem + Sh::kS + (i & 1) * BN;
           const uint32_t acc0 = j > 0 || o_init[piece & 1] ? 1u : 0u;
 #pragma unroll
-          for (int kk = 0; kk < BN / 16; ++kk)
+          for (int kk = 0; kk < BN / (Sh::kHalves ? 32 : 16); ++kk)
             tc_mma_ta(tmem, ps + kk * 8, desc_advance(vd, kk * 2048), kIdO, kk > 0 ? 1u : acc0);
+          if constexpr (Sh::kHalves) {
+            ok = mbar_wait_warp(&prest[i % NS], (i / NS) & 1);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (int kk = BN / 32; kk < BN / 16; ++kk)
+              tc_mma_ta(tmem, ps + kk * 8, desc_advance(vd, kk * 2048), kIdO, 1u);
+          }
           tc_commit_elect(&vdone[i % NS]);
         }
         it += n;
@@ -505,6 +519,36 @@ __global__ void __launch_bounds__(kThreads, 1)
           asm volatile("bar.arrive %0, 64;" ::"r"(1 + 4 * half + quad) : "memory");
         }
         const float ref = m == -INFINITY ? 0.f : m;
+        const int sg = it % NS;
+        bool by_hand = false;
+        auto settle = [&]() {  // O as this block's product finds it; before its first weights are handed on
+          const bool rescale = !first && __any_sync(0xffffffffu, grow);
+          if (blk * BN + BN > from_all) {
+            wait(&vok[sg], (it / NS) & 1);
+            by_hand = odd[2 * sg] | odd[2 * sg + 1];
+          }
+          if (rescale || by_hand) {
+            // O of the blocks before is complete (the MMA of this one waits for this thread)
+            if (!first)
+              wait(&vdone[(it - 1) % NS], ((it - 1) / NS) & 1);
+            else if (piece > 0)
+              wait(ofree, (piece - 1) & 1);  // and the piece's before has been read
+            tc_fence_after();
+          }
+          if (rescale) {
+            const float c = grow ? ex2(mo - ref) : 1.f;  // ex2(-Inf) = 0
+#pragma unroll 1
+            for (int d = 0; d < D; d += 32) {
+              float o[32];
+              uint32_t u[32];
+              tmem_ld32(trow + d, o);
+#pragma unroll
+              for (int j = 0; j < 32; ++j) u[j] = __float_as_uint(o[j] * c);
+              tmem_st32(trow + d, u);
+            }
+          }
+        };
+        if (Sh::kHalves) settle();
         // A weight is 2^(scale s - ref): two at a time in packed arithmetic. Of 128 scores the last 32 stay
         // in registers; the others are read again, before weights take their columns.
         unsigned long long sum[2] = {0ull, 0ull};
@@ -532,34 +576,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             w[j / 2] = bf16_pair(e0, e1);
           }
           tmem_st16(ts + c0 / 2, w);
-        }
-        const bool rescale = !first && __any_sync(0xffffffffu, grow);
-        const int sg = it % NS;
-        bool by_hand = false;
-        if (blk * BN + BN > from_all) {
-          wait(&vok[sg], (it / NS) & 1);
-          by_hand = odd[2 * sg] | odd[2 * sg + 1];
-        }
-        if (rescale || by_hand) {
-          // O of the blocks before is complete (the MMA of this one waits for this thread)
-          if (!first)
-            wait(&vdone[(it - 1) % NS], ((it - 1) / NS) & 1);
-          else if (piece > 0)
-            wait(ofree, (piece - 1) & 1);  // and the piece's before has been read
-          tc_fence_after();
-        }
-        if (rescale) {
-          const float c = grow ? ex2(mo - ref) : 1.f;  // ex2(-Inf) = 0
-#pragma unroll 1
-          for (int d = 0; d < D; d += 32) {
-            float o[32];
-            uint32_t u[32];
-            tmem_ld32(trow + d, o);
-#pragma unroll
-            for (int j = 0; j < 32; ++j) u[j] = __float_as_uint(o[j] * c);
-            tmem_st32(trow + d, u);
+          if (Sh::kHalves && c0 + 32 == BN / 2 && !by_hand) {  // the first half of the weights
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&pready[sg]);
           }
         }
+        if (!Sh::kHalves) settle();
         if (by_hand) {
           uint8_t* vt = sv + sg * Sh::kTile;
           const int from = max(0, from_all - blk * BN), nrow = BN - from;
@@ -621,7 +645,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&pready[it % NS]);
+        if (lane == 0) {
+          if (!Sh::kHalves || by_hand) mbar_arrive(&pready[sg]);
+          if (Sh::kHalves) mbar_arrive(&prest[sg]);
+        }
         l = (mg == m ? l : l * ex2(mg - ref)) + (sum2(sum[0]) + sum2(sum[1]));
         mg = m;
       }
