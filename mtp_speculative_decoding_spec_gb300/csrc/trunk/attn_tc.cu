@@ -488,10 +488,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int blk = a.blk0 + it - it0; blk < blk_end; blk += 2, it += 2) {
         const bool first = it == it0, last = it + 1 == it0 + n;
         const int valid = min(BN, lim - blk * BN);  // positions of the block this row sees
+        const bool full = __all_sync(0xffffffffu, valid >= BN);
         wait(&kdone[it % NS], (it / NS) & 1);
         tc_fence_after();
         const uint32_t ts = trow + Sh::kS + half * BN;
-        const bool full = __all_sync(0xffffffffu, valid >= BN);
         float v[64], raw = -INFINITY;
 #pragma unroll
         for (int c0 = 0; c0 < BN; c0 += 64) {
