@@ -122,18 +122,29 @@ __global__ void __launch_bounds__(kSimtThreads, 1)
       }
       __syncthreads();
       {
-        float z[2][2] = {};
+        float4 w[2][2] = {};  // four sums a score, every fourth dim in one
         const float* q0 = qs + 2 * warp * ld;
         const float* k0 = ks + lane * ld;
+        const auto dot4 = [](float4& z, const float4& x, const float4& y) {
+          z.x = fmaf(x.x, y.x, z.x), z.y = fmaf(x.y, y.y, z.y);
+          z.z = fmaf(x.z, y.z, z.z), z.w = fmaf(x.w, y.w, z.w);
+        };
+#pragma unroll 4
         for (int d = 0; d < D; d += 4) {
           const float4 a0 = *reinterpret_cast<const float4*>(q0 + d);
           const float4 a1 = *reinterpret_cast<const float4*>(q0 + ld + d);
           const float4 c0 = *reinterpret_cast<const float4*>(k0 + d);
           const float4 c1 = *reinterpret_cast<const float4*>(k0 + 32 * ld + d);
-          z[0][0] = fmaf(a0.x, c0.x, fmaf(a0.y, c0.y, fmaf(a0.z, c0.z, fmaf(a0.w, c0.w, z[0][0]))));
-          z[0][1] = fmaf(a0.x, c1.x, fmaf(a0.y, c1.y, fmaf(a0.z, c1.z, fmaf(a0.w, c1.w, z[0][1]))));
-          z[1][0] = fmaf(a1.x, c0.x, fmaf(a1.y, c0.y, fmaf(a1.z, c0.z, fmaf(a1.w, c0.w, z[1][0]))));
-          z[1][1] = fmaf(a1.x, c1.x, fmaf(a1.y, c1.y, fmaf(a1.z, c1.z, fmaf(a1.w, c1.w, z[1][1]))));
+          dot4(w[0][0], a0, c0);
+          dot4(w[0][1], a0, c1);
+          dot4(w[1][0], a1, c0);
+          dot4(w[1][1], a1, c1);
+        }
+        float z[2][2];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float4 y = w[i >> 1][i & 1];
+          z[i >> 1][i & 1] = (y.x + y.y) + (y.z + y.w);
         }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {  // a warp holds both rows' 64 scores: the softmax stays in it
@@ -168,21 +179,17 @@ __global__ void __launch_bounds__(kSimtThreads, 1)
       }
       __syncthreads();
       if (holds) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (i >= rpt) break;
-          const float c = row_c[min(r0 + i, kSimtTm - 1)];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) acc[i][j] *= c;
-        }
+        // a block's sum by itself, joined to the blocks' before by one operation: the error of a long sum
+        // then grows with the square roots of 64 and of the blocks, not of all positions
+        float sum[4][4] = {};
         const int np = min(kSimtBn, most - p0);
         const int all = max(0, min(np, least - p0));  // positions that every running row sees
         auto add = [&](int t, int i, const float4& v) {
           const float w = ps[min(r0 + i, kSimtTm - 1) * (kSimtBn + 1) + t];
-          acc[i][0] = fmaf(w, v.x, acc[i][0]);
-          acc[i][1] = fmaf(w, v.y, acc[i][1]);
-          acc[i][2] = fmaf(w, v.z, acc[i][2]);
-          acc[i][3] = fmaf(w, v.w, acc[i][3]);
+          sum[i][0] = fmaf(w, v.x, sum[i][0]);
+          sum[i][1] = fmaf(w, v.y, sum[i][1]);
+          sum[i][2] = fmaf(w, v.z, sum[i][2]);
+          sum[i][3] = fmaf(w, v.w, sum[i][3]);
         };
 #pragma unroll 4
         for (int t = 0; t < all; ++t) {
@@ -196,6 +203,13 @@ __global__ void __launch_bounds__(kSimtThreads, 1)
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             if (i < rpt && p0 + t < row_lim[min(r0 + i, kSimtTm - 1)]) add(t, i, v);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (i >= rpt) break;
+          const float c = row_c[min(r0 + i, kSimtTm - 1)];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(acc[i][j], c, sum[i][j]);
         }
       }
     }
