@@ -241,8 +241,8 @@ spec_status spec_prefix_attention(int32_t B, int32_t R, const spec_state_desc* s
   p.npt = w.npt;
   p.npi = w.npi;
   p.grp = w.grp;
-  p.over[0] = kAttnOverPre;
-  p.over[1] = kAttnOver;
+  p.over[0] = w.tc ? kAttnOverPre : kAttnSimtOver;
+  p.over[1] = w.tc ? kAttnOver : kAttnSimtOver;
   p.nown = w.nown;
   p.items = w.items;
   p.q = d->q;

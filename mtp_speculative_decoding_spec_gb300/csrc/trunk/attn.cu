@@ -19,44 +19,47 @@ namespace {
 __device__ __forceinline__ float to_f(float x) { return x; }
 __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
 
-// Eight elements from 16-byte aligned memory (global or shared), as floats.
-__device__ __forceinline__ void load8(const float* p, float* v) {
-  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-  v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+// Four elements of shared memory (aligned to their size), as floats.
+__device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
+  const uint2 a = *reinterpret_cast<const uint2*>(p);
+  return make_float4(__uint_as_float(a.x << 16), __uint_as_float(a.x & 0xffff0000u),
+                     __uint_as_float(a.y << 16), __uint_as_float(a.y & 0xffff0000u));
 }
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float* v) {
-  const uint4 a = *reinterpret_cast<const uint4*>(p);
-  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(w[i] << 16);
-    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
+
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
 }
 
 constexpr int kSimtTm = 16;       // rows per tile
-constexpr int kSimtBn = 64;       // positions per block
+constexpr int kSimtBn = 32;       // positions per block: a lane's
 constexpr int kSimtThreads = 256;
 constexpr int kMaxD = 256;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kPad = 4;           // floats after a row of Q, K: rows start 16 bytes apart in the banks
+constexpr int kPad = 16;          // bytes after a row of Q, K, V: rows start 16 bytes apart in the banks
+constexpr int kPsPitch = kSimtTm + 4;  // floats between positions' weights
 
-// 256 threads over a tile of 16 rows and blocks of 64 positions, all operands fp32 in shared memory.
-// Scores: thread (ty, tx) takes rows 2 ty, 2 ty + 1 and positions tx, tx + 32. Values: a thread takes
-// four consecutive dims of one to four rows. A block in which some row's positions end takes only the
-// positions a row sees, one by one, so what a masked position holds reaches no row.
+// 256 threads over a tile of 16 rows and blocks of 32 positions, the next block's K and V on their way to
+// the other of two buffers (as many buffers as fit: 249 us for 222, 4 rows of 16 fp32 heads of 256 dims over
+// 50,000). Scores: a warp takes four rows and half of the dims, a lane a position, so that
+// a piece of K read serves four rows. The halves meet in shared memory, and four warps do the softmax of
+// four rows each. Values: a thread takes four consecutive dims of one, two or four rows. A block in which
+// some row's positions end takes only the positions a row sees, one by one, so what a masked position
+// holds reaches no row.
 template <typename T>
 __global__ void __launch_bounds__(kSimtThreads, 1)
     attn_simt_kernel(const __grid_constant__ AttnParams p) {
   extern __shared__ __align__(16) uint8_t smem[];
   pdl_wait();
-  const int D = p.D, ld = D + kPad, tid = threadIdx.x;
-  float* qs = reinterpret_cast<float*>(smem);          // [16][ld]
-  float* ks = qs + kSimtTm * ld;                       // [64][ld]
-  float* vs = ks + kSimtBn * ld;                       // [64][ld]
-  float* ps = vs + kSimtBn * ld;                       // [16][64 + 1]
-  float* row_m = ps + kSimtTm * (kSimtBn + 1);         // running max, the old scale's factor, sum
+  const int D = p.D, ld = D + kPad / 4, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int pitch = D * static_cast<int>(sizeof(T)) + kPad, tile_bytes = kSimtBn * pitch;
+  uint8_t* kv = smem;                                    // [2][K, V][32][pitch]
+  float* qs = reinterpret_cast<float*>(smem + 4 * tile_bytes);  // [16][ld]
+  float* ps = qs + kSimtTm * ld;                         // [32][20]
+  float* part = ps + kSimtBn * kPsPitch;                 // [16][32] scores over the upper dims
+  float* row_m = part + kSimtTm * kSimtBn;               // running max, the old scale's factor, sum
   float* row_c = row_m + kSimtTm;
   float* row_l = row_c + kSimtTm;
   int* row_lim = reinterpret_cast<int*>(row_l + kSimtTm);
@@ -68,11 +71,13 @@ __global__ void __launch_bounds__(kSimtThreads, 1)
   AttnWalk walk;
   walk.start(p, cum, shares);
   AttnPiece a;
-  const int warp = tid >> 5, lane = tid & 31;
-  // values: this thread's four dims of `rpt` (1..4) rows from r0; the fewer the dims, the fewer the rows
-  const int nd = D / 4, ng = min(kSimtTm, kSimtThreads / nd), rpt = (kSimtTm + ng - 1) / ng;
+  // scores: this warp's rows and dims
+  const int sr = (warp & 3) * 4, sd = (warp >> 2) * (D / 2);
+  // values: this thread's four dims of `rpt` (1, 2 or 4) rows from r0; the fewer the dims, the fewer the rows
+  const int nd = D / 4, ng = min(kSimtTm, kSimtThreads / nd);
+  const int rpt = ng >= 16 ? 1 : ng >= 8 ? 2 : 4;
   const int d0 = (tid % nd) * 4, r0 = tid / nd * rpt;
-  const bool holds = tid / nd < ng && r0 < kSimtTm;
+  const bool holds = r0 < kSimtTm;
   while (walk.next(p, cum, shares, a)) {
     const int head = a.head, slot = a.slot;
     __syncthreads();  // the previous piece's shared memory is no longer read
@@ -84,130 +89,139 @@ __global__ void __launch_bounds__(kSimtThreads, 1)
       row_m[tid] = -INFINITY;
       row_l[tid] = 0.f;
     }
-    __syncthreads();
-    {  // 16 threads a row
-      const int r = tid >> 4;
-      const T* src = static_cast<const T*>(p.q) + row_q[r];
-      const bool runs = row_lim[r] > 0;
-      for (int d = tid & 15; d < D; d += 16) qs[r * ld + d] = runs ? to_f(src[d]) : 0.f;
-    }
     const bool pre = a.tile < p.npt;
     const int b = pre ? 0 : (a.tile - p.npt) / p.nown;
-    const uint8_t* kbase = pre ? p.pk : p.kk + static_cast<int64_t>(b) * p.kreq;
-    const uint8_t* vbase = pre ? p.pv : p.kv + static_cast<int64_t>(b) * p.kreq;
     const int64_t step = pre ? p.pstride : p.krow;
     const int64_t hoff = static_cast<int64_t>(head) * D * sizeof(T);
+    const uint8_t* kbase = (pre ? p.pk : p.kk + static_cast<int64_t>(b) * p.kreq) + hoff;
+    const uint8_t* vbase = (pre ? p.pv : p.kv + static_cast<int64_t>(b) * p.kreq) + hoff;
     __syncthreads();
     int most = 0, least = 0x7fffffff;  // positions any row sees; positions every running row sees
     for (int r = 0; r < kSimtTm; ++r) {
       most = max(most, row_lim[r]);
       if (row_lim[r] > 0) least = min(least, row_lim[r]);
     }
+    const int chunks = D * static_cast<int>(sizeof(T)) / 16;
+    auto fetch = [&](int blk, int buf) {  // positions that some row sees; the others' places hold anything
+      uint8_t* k = kv + 2 * buf * tile_bytes;
+      const int p0 = blk * kSimtBn, np = min(kSimtBn, most - p0);
+      for (int i = tid; i < np * chunks; i += kSimtThreads) {
+        const int r = i / chunks, c = (i - r * chunks) * 16;
+        copy_async16(k + r * pitch + c, kbase + (p0 + r) * step + c);
+        copy_async16(k + tile_bytes + r * pitch + c, vbase + (p0 + r) * step + c);
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    fetch(a.blk0, 0);
+    {  // 16 threads a row
+      const int r = tid >> 4;
+      const T* src = static_cast<const T*>(p.q) + row_q[r];
+      const bool runs = row_lim[r] > 0;
+      for (int d = tid & 15; d < D; d += 16) qs[r * ld + d] = runs ? to_f(src[d]) : 0.f;
+    }
     float acc[4][4] = {};
     for (int blk = a.blk0; blk < a.blk1; ++blk) {
-      const int p0 = blk * kSimtBn;
-      __syncthreads();
-      for (int i = tid; i < kSimtBn * (D / 8); i += kSimtThreads) {
-        const int r = i / (D / 8), d = (i - r * (D / 8)) * 8;
-        float kx[8] = {}, vx[8] = {};
-        if (p0 + r < most) {
-          load8(reinterpret_cast<const T*>(kbase + (p0 + r) * step + hoff) + d, kx);
-          load8(reinterpret_cast<const T*>(vbase + (p0 + r) * step + hoff) + d, vx);
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          ks[r * ld + d + j] = kx[j];
-          vs[r * ld + d + j] = vx[j];
-        }
-      }
-      __syncthreads();
-      {
-        float4 w[2][2] = {};  // four sums a score, every fourth dim in one
-        const float* q0 = qs + 2 * warp * ld;
-        const float* k0 = ks + lane * ld;
-        const auto dot4 = [](float4& z, const float4& x, const float4& y) {
-          z.x = fmaf(x.x, y.x, z.x), z.y = fmaf(x.y, y.y, z.y);
-          z.z = fmaf(x.z, y.z, z.z), z.w = fmaf(x.w, y.w, z.w);
-        };
-#pragma unroll 4
-        for (int d = 0; d < D; d += 4) {
-          const float4 a0 = *reinterpret_cast<const float4*>(q0 + d);
-          const float4 a1 = *reinterpret_cast<const float4*>(q0 + ld + d);
-          const float4 c0 = *reinterpret_cast<const float4*>(k0 + d);
-          const float4 c1 = *reinterpret_cast<const float4*>(k0 + 32 * ld + d);
-          dot4(w[0][0], a0, c0);
-          dot4(w[0][1], a0, c1);
-          dot4(w[1][0], a1, c0);
-          dot4(w[1][1], a1, c1);
-        }
-        float z[2][2];
+      const int p0 = blk * kSimtBn, buf = (blk - a.blk0) & 1;
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+      __syncthreads();  // this block is here, and the other buffer no longer read
+      if (blk + 1 < a.blk1) fetch(blk + 1, buf ^ 1);
+      const T* ks = reinterpret_cast<const T*>(kv + 2 * buf * tile_bytes + lane * pitch) + sd;
+      const T* vs = reinterpret_cast<const T*>(kv + (2 * buf + 1) * tile_bytes);
+      float4 w[4] = {};  // four sums a score, every fourth dim in one
+#pragma unroll 2
+      for (int d = 0; d < D / 2; d += 4) {
+        const float4 y = load4(ks + d);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float4 y = w[i >> 1][i & 1];
-          z[i >> 1][i & 1] = (y.x + y.y) + (y.z + y.w);
+          const float4 x = load4(qs + (sr + i) * ld + sd + d);
+          w[i].x = fmaf(x.x, y.x, w[i].x), w[i].y = fmaf(x.y, y.y, w[i].y);
+          w[i].z = fmaf(x.z, y.z, w[i].z), w[i].w = fmaf(x.w, y.w, w[i].w);
+        }
+      }
+      float z[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) z[i] = (w[i].x + w[i].y) + (w[i].z + w[i].w);
+      if (warp >= 4) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) part[(sr + i) * kSimtBn + lane] = z[i];
+      }
+      __syncthreads();
+      if (warp < 4) {
+        float e[4], m[4], l[4], old[4];  // four rows side by side
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = sr + i;
+          old[i] = row_m[r];
+          e[i] = p0 + lane < row_lim[r] ? (z[i] + part[r * kSimtBn + lane]) * p.scale_log2 : -INFINITY;
+          m[i] = max_nan(e[i], old[i]);
         }
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {  // a warp holds both rows' 64 scores: the softmax stays in it
-          const int r = 2 * warp + i, lim = row_lim[r] - p0;
-          const float s0 = lane < lim ? z[i][0] * p.scale_log2 : -INFINITY;
-          const float s1 = lane + 32 < lim ? z[i][1] * p.scale_log2 : -INFINITY;
-          float m = fmaxf(s0, s1);
-          if (s0 != s0 || s1 != s1) m = NAN;
+        for (int o = 16; o > 0; o >>= 1)
 #pragma unroll
-          for (int o = 16; o > 0; o >>= 1) {
-            const float other = __shfl_xor_sync(0xffffffffu, m, o);
-            m = (m != m || other != other) ? NAN : fmaxf(m, other);
-          }
-          const float old = row_m[r];
-          m = (old != old || m != m) ? NAN : fmaxf(m, old);
-          const float ref = m == -INFINITY ? 0.f : m;  // nothing seen yet: every weight is 0
-          const float e0 = lane < lim ? exp2f(s0 - ref) : 0.f;
-          const float e1 = lane + 32 < lim ? exp2f(s1 - ref) : 0.f;
-          float l = e0 + e1;
+          for (int i = 0; i < 4; ++i) m[i] = max_nan(m[i], __shfl_xor_sync(0xffffffffu, m[i], o));
 #pragma unroll
-          for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-          ps[r * (kSimtBn + 1) + lane] = e0;
-          ps[r * (kSimtBn + 1) + lane + 32] = e1;
-          __syncwarp();
-          if (lane == 0) {
-            const float c = exp2f(old - ref);
-            row_c[r] = c;
-            row_l[r] = row_l[r] * c + l;
-            row_m[r] = m;
+        for (int i = 0; i < 4; ++i) {
+          const float ref = m[i] == -INFINITY ? 0.f : m[i];  // nothing seen yet: every weight is 0
+          e[i] = p0 + lane < row_lim[sr + i] ? exp2f(e[i] - ref) : 0.f;
+          l[i] = e[i];
+          old[i] = exp2f(old[i] - ref);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) l[i] += __shfl_xor_sync(0xffffffffu, l[i], o);
+        if (lane == 0) {  // every lane is past its reading
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            row_c[sr + i] = old[i];
+            row_l[sr + i] = row_l[sr + i] * old[i] + l[i];
+            row_m[sr + i] = m[i];
           }
         }
+        *reinterpret_cast<float4*>(ps + lane * kPsPitch + sr) = make_float4(e[0], e[1], e[2], e[3]);
       }
       __syncthreads();
       if (holds) {
         // a block's sum by itself, joined to the blocks' before by one operation: the error of a long sum
-        // then grows with the square roots of 64 and of the blocks, not of all positions
+        // then grows with the square roots of 32 and of the blocks, not of all positions
         float sum[4][4] = {};
         const int np = min(kSimtBn, most - p0);
         const int all = max(0, min(np, least - p0));  // positions that every running row sees
-        auto add = [&](int t, int i, const float4& v) {
-          const float w = ps[min(r0 + i, kSimtTm - 1) * (kSimtBn + 1) + t];
-          sum[i][0] = fmaf(w, v.x, sum[i][0]);
-          sum[i][1] = fmaf(w, v.y, sum[i][1]);
-          sum[i][2] = fmaf(w, v.z, sum[i][2]);
-          sum[i][3] = fmaf(w, v.w, sum[i][3]);
+        auto add = [&](int i, float x, const float4& v) {
+          sum[i][0] = fmaf(x, v.x, sum[i][0]);
+          sum[i][1] = fmaf(x, v.y, sum[i][1]);
+          sum[i][2] = fmaf(x, v.z, sum[i][2]);
+          sum[i][3] = fmaf(x, v.w, sum[i][3]);
         };
+        const char* vp = reinterpret_cast<const char*>(vs + d0);
+        if (rpt == 4) {
 #pragma unroll 4
-        for (int t = 0; t < all; ++t) {
-          const float4 v = *reinterpret_cast<const float4*>(vs + t * ld + d0);
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (i < rpt) add(t, i, v);
+          for (int t = 0; t < all; ++t) {
+            const float4 v = load4(reinterpret_cast<const T*>(vp + t * pitch));
+            const float4 x = load4(ps + t * kPsPitch + r0);
+            add(0, x.x, v);
+            add(1, x.y, v);
+            add(2, x.z, v);
+            add(3, x.w, v);
+          }
+        } else {
+#pragma unroll 4
+          for (int t = 0; t < all; ++t) {
+            const float4 v = load4(reinterpret_cast<const T*>(vp + t * pitch));
+            add(0, ps[t * kPsPitch + r0], v);
+            if (rpt == 2) add(1, ps[t * kPsPitch + r0 + 1], v);
+          }
         }
         for (int t = all; t < np; ++t) {
-          const float4 v = *reinterpret_cast<const float4*>(vs + t * ld + d0);
+          const float4 v = load4(reinterpret_cast<const T*>(vp + t * pitch));
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            if (i < rpt && p0 + t < row_lim[min(r0 + i, kSimtTm - 1)]) add(t, i, v);
+            if (i < rpt && p0 + t < row_lim[r0 + i]) add(i, ps[t * kPsPitch + r0 + i], v);
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           if (i >= rpt) break;
-          const float c = row_c[min(r0 + i, kSimtTm - 1)];
+          const float c = row_c[r0 + i];
 #pragma unroll
           for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(acc[i][j], c, sum[i][j]);
         }
@@ -219,7 +233,7 @@ __global__ void __launch_bounds__(kSimtThreads, 1)
     if (holds) {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        if (i < rpt && r0 + i < kSimtTm && row_lim[r0 + i] > 0)
+        if (i < rpt && row_lim[r0 + i] > 0)
           *reinterpret_cast<float4*>(p.o + (static_cast<int64_t>(slot) * kSimtTm + r0 + i) * D + d0) =
               make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
     }
@@ -361,8 +375,9 @@ __global__ void __launch_bounds__(NW == 1 ? 128 : 32 * NW)
 template <typename T>
 cudaError_t simt_launch(const AttnParams& p, int grid, cudaStream_t stream) {
   static SmemAllowance allowed;
-  const int floats = (kSimtTm + 2 * kSimtBn) * (p.D + kPad) + kSimtTm * (kSimtBn + 1) + 3 * kSimtTm;
-  const int smem = 4 * (floats + 3 * kSimtTm) + static_cast<int>(attn_plan_bytes(p.items, p.B));
+  const int tiles = 4 * kSimtBn * (p.D * static_cast<int>(sizeof(T)) + kPad);
+  const int floats = kSimtTm * (p.D + kPad / 4) + kSimtBn * kPsPitch + kSimtTm * kSimtBn + 3 * kSimtTm;
+  const int smem = tiles + 4 * (floats + 3 * kSimtTm) + static_cast<int>(attn_plan_bytes(p.items, p.B));
   const cudaError_t e = allow_dynamic_smem(attn_simt_kernel<T>, smem, allowed);
   if (e != cudaSuccess) return e;
   return launch_pdl(attn_simt_kernel<T>, dim3(grid), dim3(kSimtThreads), smem, stream, p);

@@ -104,10 +104,6 @@ struct Raw {
 
 constexpr int kGroup = 8;  // rows staged at once
 
-__device__ __forceinline__ void copy_async16(void* dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
-}
-
 // A warp's shared memory: q and k of a group (one or two of them in flight), v, decay and beta.
 template <typename T, int NI, int LV>
 struct Staged {

@@ -29,6 +29,10 @@ struct DeltaParams {
   WsHeader* hdr;            // prefill: the workspace's, its error word cleared by each call
 };
 
+__device__ __forceinline__ void copy_async16(void* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+
 // A bounded wait by a whole warp, whose branches stay uniform: 38 cycles when the phase is over, 105 when
 // each lane decides for itself.
 __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity) {
@@ -91,6 +95,8 @@ constexpr int64_t kAttnMaxPos = (int64_t(1) << 31) - 256;  // a block past the l
 // 190.1, 189.0, 190.7; 64 rows over 63,488 76.0, 73.1, 70.3, 70.7; two rows over their own 63,488 52.5, 50.6,
 // 50.4, 51.2.
 constexpr int kAttnOver = 6, kAttnOverPre = 10;
+// On CUDA cores: 2 or 4 102.9 us, 6 106.5 (4 x 8 fp32 rows of 128 dims over 3,000 and 2,000 positions).
+constexpr int kAttnSimtOver = 2;
 // The most of `grp`. 256 rows (8 tiles) over 63,488 positions, groups of 1, 4 and 8: 211, 194 and 192 us;
 // 40 rows of 4 heads (2 tiles) singly and in pairs: 104 and 68 us.
 constexpr int kAttnGroup = 16;
