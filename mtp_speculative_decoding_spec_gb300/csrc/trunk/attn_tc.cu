@@ -21,7 +21,7 @@
 // does see one, that row's share of it is added by hand and the value cleared for the tensor cores.
 //
 // 16 query heads on 4 KV heads of 256 dims: 256 rows over 63,488 shared positions and 700 own ones each,
-// 191 us with the join = 1.40 PFLOP/s (0.73 of cuBLAS); a block of 64 positions takes about 1,500 cycles
+// 189 us with the join = 1.42 PFLOP/s (0.73 of cuBLAS); a block of 64 positions takes about 1,450 cycles
 // against 1,024 of the tensor pipe, the rest the way from a block's scores through its softmax to its
 // second product, which two buffers of S hide in part. Two rows of one request over its own 63,488: 50.5
 // us = 5.2 TB/s (0.76 of a copy), eight single rows over a shared 63,488 60 us = 5.0 TB/s: HBM while the

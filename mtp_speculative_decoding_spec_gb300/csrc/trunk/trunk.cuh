@@ -95,7 +95,8 @@ constexpr int64_t kAttnMaxPos = (int64_t(1) << 31) - 256;  // a block past the l
 // 190.1, 189.0, 190.7; 64 rows over 63,488 76.0, 73.1, 70.3, 70.7; two rows over their own 63,488 52.5, 50.6,
 // 50.4, 51.2.
 constexpr int kAttnOver = 6, kAttnOverPre = 10;
-// On CUDA cores: 2 or 4 102.9 us, 6 106.5 (4 x 8 fp32 rows of 128 dims over 3,000 and 2,000 positions).
+// On CUDA cores (blocks of 32 positions): 1 to 4 81-84 us, 6 87 (4 x 8 fp32 rows of 12 heads of 128 dims over
+// 3,000 shared and 2,000 own positions).
 constexpr int kAttnSimtOver = 2;
 // The most of `grp`. 256 rows (8 tiles) over 63,488 positions, groups of 1, 4 and 8: 211, 194 and 192 us;
 // 40 rows of 4 heads (2 tiles) singly and in pairs: 104 and 68 us.
@@ -355,7 +356,8 @@ cudaError_t attn_join_launch(const AttnParams& p, spec_dtype dtype, int sms, cud
 int attn_simt_tm();
 int attn_simt_bn();
 // Head sizes of the tensor-core kernel, bf16 alone. On the CUDA cores two rows over 63,488 positions of 256
-// dims take 379 us for 51, 32 rows of 64 dims over 15,360 306 for 20.
+// dims take 206 us for 51, 32 rows of 64 dims over 15,360 224 for 20; two rows of 64 dims over 258 8.4 for
+// 9.7, which is not worth a limit on lengths that the host does not know.
 bool attn_tc_takes(int head_dim);
 spec_status attn_tc_launch(const AttnParams& p, int grid, EncodeTiledFn encode, cudaStream_t stream);
 int attn_tc_tm();
