@@ -39,7 +39,7 @@ namespace {
 
 constexpr int kTm = 128;
 constexpr int kThreads = 12 * 32;  // producer, MMA and two guard warps, eight softmax warps
-constexpr int kSoftThreads = 256;
+constexpr int kGroupThreads = 128;  // a softmax group
 // Registers a thread: launched with 168 (64,512 in all); the first four warps give to the softmax's
 // eight: 128 x 152 + 256 x 176 = 64,512. (104 and 200 spill in the guards: 214 us for 191.)
 constexpr int kFewRegs = 152, kSoftRegs = 176;
@@ -626,7 +626,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_st_wait();
           }
           bar_group();
-          for (int i = st; i < nrow * (D / 8); i += kSoftThreads / 2) {
+          for (int i = st; i < nrow * (D / 8); i += kGroupThreads) {
             const int pos = from + i / (D / 8), ch = i % (D / 8);
             uint32_t* at = reinterpret_cast<uint32_t*>(vt + (ch / 8) * Sh::kPanel + pos * 128 +
                                                        (((ch & 7) ^ (pos & 7)) << 4));
