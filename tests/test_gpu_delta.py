@@ -235,7 +235,8 @@ def run_prefill(spec, x, lens, layers, layer, init, stream=None, ws=None, gap=0)
     return s, start
 
 
-LENS = [[1], [63], [64], [65], [128], [0, 1, 77, 0, 200], [5, 130, 64, 63, 1, 0], [515], [2, 2, 2]]
+LENS = [[1], [63], [64], [65], [128], [0, 1, 77, 0, 200], [5, 130, 64, 63, 1, 0], [515], [2, 2, 2],
+        [1, 90, 4], [1, 90, 5]]  # either side of 32 rows a request on average
 
 
 @pytest.mark.parametrize("init", ["zero", "live", "other"])
@@ -289,6 +290,21 @@ def test_prefill_rows_past_the_prompts_are_left_alone(spec):
     x = Rows(100 + 28, 2, 1, 128, 128, "bf16")
     run_prefill(spec, x, [90, 10], 1, 0, "zero", gap=28)
     assert torch.isnan(x.out[100:]).all() and not torch.isnan(x.out[:100]).any()
+
+
+def test_prefill_of_many_requests(spec):
+    """More requests than are put in order of length."""
+    lens = [(37 * i) % 90 for i in range(300)]
+    x = Rows(sum(lens), 1, 1, 128, 16, "bf16", seed=4)
+    s, start = run_prefill(spec, x, lens, 1, 0, "other")
+    lo = np.concatenate([[0], np.cumsum(lens)])
+    for b in (0, 1, 2, 90, 157, 255, 256, 299):
+        S0 = npf(start[b, 0])
+        outs, states, _ = x.oracle(S0, int(lo[b]), int(lo[b + 1]))
+        want = states[-1] if lens[b] else S0
+        assert rel(npf(s.live[b, 0]), want) <= state_tol(128), b
+        if lens[b]:
+            assert rel(x.result(int(lo[b]), int(lo[b + 1])), np.stack(outs)) <= out_tol(128, "bf16"), b
 
 
 def test_prefill_twice_is_bitwise_the_same_and_on_another_stream(spec):
