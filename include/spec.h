@@ -587,7 +587,8 @@ size_t spec_delta_prefill_workspace_bytes(int64_t rows, int32_t B, const spec_st
  *               in bytes. prefix_capacity positions are there, at most 2^31 - 256.
  *   prefix_len  [B] int64 (clamped to [0, prefix_capacity]), or NULL: all of prefix_capacity.
  *   lse         [B*R][q_heads] float32 or NULL: log sum exp(scale q k) of each row, -Inf where a
- *               row has nothing to see, or sees scores of -Inf alone (its output is zero).
+ *               row has nothing to see, or sees scores of -Inf alone (its output is zero). A row
+ *               that sees a score that is NaN has NaN in its output and here.
  */
 typedef struct {
   spec_dtype dtype;

@@ -669,7 +669,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float2 other = row_ml[kTm + row];
         // the reference never falls, so the greater one is the last one's
         const float m = fmaxf(mg, other.x), ref = m == -INFINITY ? 0.f : m;
-        p.ml[at] = make_float2(m, l * ex2(mg - ref) + other.y * ex2(other.x - ref));
+        const float sum = l * ex2(mg - ref) + other.y * ex2(other.x - ref);
+        // The maxima pass over scores that are not numbers, the sum does not. The join takes a maximum of
+        // -Inf for a row that saw nothing, so such a partial says NaN there.
+        p.ml[at] = make_float2(sum != sum ? sum : m, sum);
       }
 #pragma unroll 1
       for (int d = half * DH; d < half * DH + DH; d += 32) {
