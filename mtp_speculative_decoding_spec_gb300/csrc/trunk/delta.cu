@@ -66,9 +66,9 @@ __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float x) {
 // one at a time, zero from `have` on.
 template <typename T, int N>
 struct Raw {
-  alignas(16) T e[N];
+  static constexpr int kBytes = N * static_cast<int>(sizeof(T));
+  alignas(kBytes < 16 ? kBytes : 16) T e[N];
   __device__ __forceinline__ void shared(const T* p) {  // aligned to its own size, at most 16 bytes
-    constexpr int kBytes = N * static_cast<int>(sizeof(T));
     if constexpr (kBytes >= 16) {
 #pragma unroll
       for (int i = 0; i < kBytes / 16; ++i)
@@ -81,8 +81,14 @@ struct Raw {
       e[0] = p[0];
     }
   }
+  __device__ __forceinline__ void store_shared(T* p) const {  // neighbours' values begin where these end
+    static_assert(sizeof(Raw) == kBytes && (kBytes == 8 || kBytes == 16), "one aligned store of just this");
+    if constexpr (kBytes == 16)
+      *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(e);
+    else
+      *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(e);
+  }
   __device__ __forceinline__ void load(const T* p, bool vec, int have) {
-    constexpr int kBytes = N * static_cast<int>(sizeof(T));
     if (vec && have >= N) {
       if constexpr (kBytes >= 16) {
 #pragma unroll
@@ -235,7 +241,7 @@ __global__ void __launch_bounds__(32, kScanBlocks<T, NI>)
   int to = slot;
   for (int r0 = 0; r0 < n; r0 += kGroup) {
     const int buf = bufs == 2 ? (r0 / kGroup) & 1 : 0;
-    if (lane < kGroup * LV) *reinterpret_cast<Raw<T, 4>*>(sv + lane * 4 * sizeof(T)) = vn;
+    if (lane < kGroup * LV) vn.store_shared(reinterpret_cast<T*>(sv) + lane * 4);
     if (lane < kGroup) {
       sa[lane] = expf(gn);
       sb[lane] = bn;
