@@ -517,6 +517,9 @@ spec_status spec_commit_rollback(int32_t B, const spec_state_desc *st,
  *   v, out      row t at v + t*v_stride: [rec_heads][rec_dv]. q, k and v may be column ranges of
  *               one wider row. Strides are at least a row's width.
  *   log_decay, beta   [rows][rec_heads] float32. -Inf clears the state.
+ *
+ * Any other value that is not finite reaches its own row and, through the state, the rows after it
+ * in the heads and columns that the formula takes it to; no row before it, no other request.
  */
 typedef struct {
   spec_dtype dtype;

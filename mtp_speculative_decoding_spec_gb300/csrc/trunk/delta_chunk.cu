@@ -17,6 +17,12 @@
 // bf16 (24 bits), with the product terms below 2^-24 left out, and sums are fp32: the state is as
 // exact as fp32 arithmetic leaves it. Where only a bf16 output is made, two parts are enough.
 //
+// What is not finite stays where the recurrence takes it. The matrices are triangular but a product's
+// steps are not: a token's zeros above the diagonal meet up to 15 later tokens, and 0 times NaN is NaN.
+// So r and u enter products with what is not finite in them taken out; u has it again for the state, and
+// the outputs of a column are NaN from its first token with such a u on. Finding out takes a vote of each
+// warp on r and on u: 472 us for 471 (below; with a branch of each thread's own 476 to 485).
+//
 // 16 heads of [128, 128], one prompt of 15,360 rows: 471 us, of which 74 the first kernel (0.25 GB, 3.3
 // TB/s) and 1.65 us a chunk the second; 63,488 rows 1.92 ms. q, k, v and the outputs alone would take 38
 // us: what bounds it is the chain's latency, some 3,300 cycles a chunk in which an SM's sub-core has one
@@ -97,6 +103,28 @@ __device__ __forceinline__ void split(float x, float y, uint32_t* w) {
   }
 }
 
+// An Inf or NaN among four pairs of bf16. An exponent of all ones carries into its half's top bit.
+__device__ __forceinline__ bool any_odd(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  const auto top = [](uint32_t x) { return (x & 0x7f807f80u) + 0x00800080u; };
+  return ((top(a) | top(b) | top(c) | top(d)) & 0x80008000u) != 0;
+}
+// The elements of four pairs that are one (element e of pair i: bit 2 i + e), which are cleared in the
+// N parts of each.
+template <int N>
+__device__ __forceinline__ uint32_t take_odd(uint32_t (&w)[4][N]) {
+  uint32_t odd = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      if ((w[i][0] >> (16 * e) & 0x7f80u) != 0x7f80u) continue;
+      odd |= 1u << (2 * i + e);
+#pragma unroll
+      for (int k = 0; k < N; ++k) w[i][k] &= e ? 0xffffu : 0xffff0000u;
+    }
+  return odd;
+}
+
 __device__ __forceinline__ int cu_at(const DeltaParams& p, int b) {
   return static_cast<int>(max(static_cast<int64_t>(0),
                               min(static_cast<int64_t>(p.cu_rows[b]), p.rows)));
@@ -141,7 +169,9 @@ __device__ __forceinline__ float exp_neg(float x) {
 }
 
 // c += A B of 16 x 16 blocks in shared memory, by a warp: lane has rows 2 (l / 4) and + 1, columns
-// 4 (l % 4) to + 3.
+// 4 (l % 4) to + 3. Lower: A is lower triangular, and what lies above its diagonal is not multiplied, so
+// that a row of B that is not finite stays out of the rows before it.
+template <bool Lower = false>
 __device__ __forceinline__ void mul16(float (&c)[2][4], const float* A, int pa, const float* B, int pb,
                                       int lane) {
   const float* a0 = A + 2 * (lane >> 2) * pa;
@@ -154,10 +184,14 @@ __device__ __forceinline__ void mul16(float (&c)[2][4], const float* A, int pa, 
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const float4 b = *reinterpret_cast<const float4*>(b0 + (k + j) * pb);
-      c[0][0] = fmaf(xs[j], b.x, c[0][0]), c[0][1] = fmaf(xs[j], b.y, c[0][1]);
-      c[0][2] = fmaf(xs[j], b.z, c[0][2]), c[0][3] = fmaf(xs[j], b.w, c[0][3]);
-      c[1][0] = fmaf(ys[j], b.x, c[1][0]), c[1][1] = fmaf(ys[j], b.y, c[1][1]);
-      c[1][2] = fmaf(ys[j], b.z, c[1][2]), c[1][3] = fmaf(ys[j], b.w, c[1][3]);
+      if (!Lower || k + j <= 2 * (lane >> 2)) {
+        c[0][0] = fmaf(xs[j], b.x, c[0][0]), c[0][1] = fmaf(xs[j], b.y, c[0][1]);
+        c[0][2] = fmaf(xs[j], b.z, c[0][2]), c[0][3] = fmaf(xs[j], b.w, c[0][3]);
+      }
+      if (!Lower || k + j <= 2 * (lane >> 2) + 1) {
+        c[1][0] = fmaf(ys[j], b.x, c[1][0]), c[1][1] = fmaf(ys[j], b.y, c[1][1]);
+        c[1][2] = fmaf(ys[j], b.z, c[1][2]), c[1][3] = fmaf(ys[j], b.w, c[1][3]);
+      }
     }
   }
 }
@@ -234,7 +268,8 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
         if (lane >= o) s = add_two(s, x);
       }
       const Two last{__shfl_sync(0xffffffffu, s.hi, 31), __shfl_sync(0xffffffffu, s.lo, 31)};
-      const Two a = lane == 0 ? Two{g0, 0.f} : add_two(s, Two{-g1, 0.f});
+      const Two x{__shfl_up_sync(0xffffffffu, s.hi, 1), __shfl_up_sync(0xffffffffu, s.lo, 1)};
+      const Two a = lane == 0 ? Two{g0, 0.f} : add_two(x, Two{g0, 0.f});
       ghi[t0] = a.hi, glo[t0] = a.lo;
       ghi[t1] = s.hi, glo[t1] = s.lo;
       vec[t0] = expf(a.hi);
@@ -340,7 +375,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
     put16(c, 1.f, M + warp * 16 * kMPitch, kMPitch, lane);
     __syncwarp();
     float d[2][4] = {};
-    mul16(d, block(i, i), kLPitch, M + warp * 16 * kMPitch, kMPitch, lane);
+    mul16<true>(d, block(i, i), kLPitch, M + warp * 16 * kMPitch, kMPitch, lane);
     put16(d, -1.f, block(i, i - 1), kLPitch, lane);
   }
   __syncthreads();
@@ -351,8 +386,8 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
     put16(c, 1.f, M + bi * 16 * kMPitch + bj * 16, kMPitch, lane);
     __syncthreads();
     float d[2][4] = {};
-    for (int k = 0; k <= bi; ++k)
-      mul16(d, block(2 + bi, 2 + k), kLPitch, M + k * 16 * kMPitch + bj * 16, kMPitch, lane);
+    if (bi > 0) mul16(d, block(3, 2), kLPitch, M + bj * 16, kMPitch, lane);
+    mul16<true>(d, block(2 + bi, 2 + bi), kLPitch, M + bi * 16 * kMPitch + bj * 16, kMPitch, lane);
     put16(d, -1.f, block(2 + bi, bj), kLPitch, lane);
   }
   if (tid == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the scores are out
@@ -366,7 +401,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
       const float2 x = *reinterpret_cast<const float2*>(L + r * kLPitch + j);
       const float2 bt = *reinterpret_cast<const float2*>(beta + j);
       uint32_t w[3];
-      split<3>(x.x * bt.x, x.y * bt.y, w);
+      split<3>(j <= r ? x.x * bt.x : 0.f, j < r ? x.y * bt.y : 0.f, w);
       const int at = tri(r, j >> 3) + 2 * (j & 7);
       *reinterpret_cast<uint32_t*>(sk + at) = w[0];
       *reinterpret_cast<uint32_t*>(sk + kTri + at) = w[1];
@@ -411,7 +446,7 @@ constexpr int kSPlane = kCols * 256;               // S^T: two panels of 16 rows
 constexpr int kUPlane = kCols * 128;               // 16 x 64
 constexpr int kWork = 3 * kSPlane + 8 * kUPlane;   // S, r, u scaled for the state (3 each), u (2)
 constexpr int kChainSmem =
-    kCStages * (kTile + kCRest) + kOStages * (kTile + kORest) + kWork + 128 + 1024;
+    kCStages * (kTile + kCRest) + kOStages * (kTile + kORest) + kWork + 128 + 64 + 1024;
 static_assert(kCRest % 128 == 0 && kORest % 128 == 0, "swizzled tiles start on 128 bytes");
 static_assert(kChainSmem <= 227 * 1024, "shared memory of an SM");
 
@@ -461,6 +496,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
   uint64_t* cempty = cfull + kCStages;
   uint64_t* ofull = cempty + kCStages;
   uint64_t* oempty = ofull + kOStages;
+  int* odd_from = reinterpret_cast<int*>(sps + kWork + 128);  // [16] a column's first token with an odd u
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int h = blockIdx.y, kh = h / (p.H / p.Hk);
   const int col0 = blockIdx.x * kCols;
@@ -475,6 +511,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
     }
     fence_mbar_init();
   }
+  if (tid < kCols) odd_from[tid] = kC;
   __syncthreads();
   pdl_wait();
   // The longest request first: blocks are dealt out in order, and what starts last should be short (prompts
@@ -605,6 +642,9 @@ __global__ void __launch_bounds__(kChainThreads, 1)
           mma(o[2][t], u[0], ab[i][1][2 * t], ab[i][1][2 * t + 1]);
         }
       }
+      // The chain lowers these before kBarU alone, and once a column has an odd u all its later ones are.
+      const int from[2] = {odd_from[g], odd_from[g + 8]};
+      const bool odd = __any_sync(0xffffffffu, min(from[0], from[1]) < kC);
       bar_arrive(kBarUsed, 256);
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
@@ -614,6 +654,12 @@ __global__ void __launch_bounds__(kChainThreads, 1)
 #pragma unroll
         for (int k = 0; k < 4; ++k)
           y[k] = fmaf(e[k & 1], x[0][t][k] + x[1][t][k], o[0][t][k] + (o[1][t][k] + o[2][t][k]));
+        if (odd) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (tok + (k & 1) >= from[k >> 1]) y[k] = NAN;
+          __syncwarp();
+        }
         const uint32_t w0 = transpose8(pack(y[0], y[1])), w1 = transpose8(pack(y[2], y[3]));
         if (tile * 8 + g < len) {
           __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) +
@@ -736,6 +782,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       for (int i = 0; i < 3; ++i)
         if (i <= tr / 2) load_t(i);
       // r = v - e^G (k S)
+      float u[3][2][4] = {};
       {
         uint32_t w[4][3];
 #pragma unroll
@@ -749,12 +796,21 @@ __global__ void __launch_bounds__(kChainThreads, 1)
           }
           split<3>(r[0], r[1], w[i]);
         }
+        // the sum that u begins with: 0, or NaN where r is odd, which is then taken out of the products
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          u[2][i >> 1][2 * (i & 1)] = 0.f * lo_of(w[i][0]);
+          u[2][i >> 1][2 * (i & 1) + 1] = 0.f * hi_of(w[i][0]);
+        }
+        if (__any_sync(0xffffffffu, any_odd(w[0][0], w[1][0], w[2][0], w[3][0]))) {
+          take_odd<3>(w);
+          __syncwarp();
+        }
 #pragma unroll
         for (int k = 0; k < 3; ++k) stm4(rp + u_at + k * kUPlane, w[0][k], w[1][k], w[2][k], w[3][k]);
       }
       bar_sync(kBarChain, 128);
       // u = T r, the terms by size in sums of their own
-      float u[3][2][4] = {};
       uint32_t ra[2][3][4];
       auto load_r = [&](int i) {
 #pragma unroll
@@ -815,6 +871,16 @@ __global__ void __launch_bounds__(kChainThreads, 1)
           const float y1 = u[0][t][k + 1] + (u[1][t][k + 1] + u[2][t][k + 1]);
           split<3>(le[t][0] * y0, le[t][1] * y1, w[i]);
           split<2>(y0, y1, z[i]);
+        }
+        if (__any_sync(0xffffffffu, any_odd(z[0][0], z[1][0], z[2][0], z[3][0]))) {
+          const uint32_t m = take_odd<2>(z);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)  // bit 2 (2 tile + half) + token
+            if (m >> i & 1) {
+              w[i >> 1][0] |= i & 1 ? 0x7fc00000u : 0x7fc0u;  // and so is the state from here on
+              atomicMin(&odd_from[g + 8 * (i >> 1 & 1)], (i >> 2 ? tr : tl) * 8 + 2 * q + (i & 1));
+            }
+          __syncwarp();
         }
 #pragma unroll
         for (int k = 0; k < 3; ++k) stm4(up + u_at + k * kUPlane, w[0][k], w[1][k], w[2][k], w[3][k]);
