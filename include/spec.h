@@ -562,8 +562,9 @@ spec_status spec_delta_rows(int32_t B, int32_t R, const spec_state_desc *st, int
  *   rows      rows of q, k, v, log_decay, beta and out. 0 <= rows < 2^31.
  *   rec_init  the states before, in rec_live's layout; rec_live itself to continue in place; NULL
  *             for empty states.
- *   workspace spec_delta_prefill_workspace_bytes(rows, B, st) bytes, 256-byte aligned; no
- *             initial contents are needed. The error word at byte offset 4 is this call's.
+ *   workspace spec_delta_prefill_workspace_bytes(rows, B, st) bytes (256 are enough where dtype
+ *             is SPEC_F32), 256-byte aligned; no initial contents are needed. The error word at
+ *             byte offset 4 is this call's.
  * Of st only the rec_* sizes and rec_live are used.
  */
 spec_status spec_delta_prefill(int32_t B, const int32_t *cu_rows, int64_t rows,

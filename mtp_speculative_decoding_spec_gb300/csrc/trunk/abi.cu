@@ -179,18 +179,19 @@ spec_status spec_delta_prefill(int32_t B, const int32_t* cu_rows, int64_t rows,
   const spec_status s = delta_params(st, layer, d, p);
   if (s != SPEC_OK) return s;
   if (!st->rec_live || !aligned16(st->rec_live) || !aligned16(rec_init)) return SPEC_ERR_INVALID;
-  if (!workspace || !aligned_to(workspace, 256) ||
-      workspace_bytes < spec_delta_prefill_workspace_bytes(rows, B, st))
-    return SPEC_ERR_INVALID;
-  const DevAttr a = dev_attr();
-  if (a.sms <= 0) return SPEC_ERR_CUDA;
   p.B = B;
   p.mode = DELTA_PREFILL;
   p.cu_rows = cu_rows;
   p.rows = rows;
   p.init = rec_init;
   p.hdr = static_cast<WsHeader*>(workspace);
-  if (delta_chunk_takes(p, d->dtype)) {
+  const bool chunks = delta_chunk_takes(p, d->dtype);  // the row scan uses the header alone
+  if (!workspace || !aligned_to(workspace, 256) ||
+      workspace_bytes < (chunks ? delta_chunk_workspace(rows, B, p.H) : sizeof(WsHeader)))
+    return SPEC_ERR_INVALID;
+  const DevAttr a = dev_attr();
+  if (a.sms <= 0) return SPEC_ERR_CUDA;
+  if (chunks) {
     EncodeTiledFn encode = encode_tiled();
     if (!encode) return SPEC_ERR_CUDA;
     return delta_chunk_launch(p, workspace, encode, reinterpret_cast<cudaStream_t>(stream));

@@ -1,0 +1,36 @@
+"""What a call of the trunk's token mixers asks of its caller: workspaces no larger than it uses."""
+
+import numpy as np
+import pytest
+import torch
+
+from test_gpu_delta import Rows, State, npf, out_tol, rel, state_tol
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def spec():
+    from gpu_util import ensure_built
+    ensure_built()
+    import mtp_speculative_decoding_spec_gb300 as spec
+    return spec
+
+
+def test_fp32_prompts_need_the_header_alone(spec):
+    lens, H, d = [90, 0, 41], 2, 128
+    x = Rows(sum(lens), H, H, d, d, "f32", seed=1)
+    s = State(spec, len(lens), 1, H, d, d, 2)
+    start = s.live.clone()
+    cu = torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int32).cuda()
+    assert spec.spec_delta_prefill_workspace_bytes(sum(lens), len(lens), s.st) > 256
+    spec.spec_delta_prefill(len(lens), cu, sum(lens), s.st, 0, x.desc(spec), s.live,
+                            torch.zeros(256, dtype=torch.uint8).cuda())
+    outs, states, _ = x.oracle(npf(start[0, 0]), 0, 90)
+    assert rel(x.result(0, 90), np.stack(outs)) <= out_tol(d, "f32")
+    assert rel(npf(s.live[0, 0]), states[-1]) <= state_tol(d)
+    # chunks are kept in the workspace: what the query says is needed, and refused without
+    y = Rows(sum(lens), H, H, d, d, "bf16", seed=1)
+    with pytest.raises(spec.SpecError, match="SPEC_ERR_INVALID"):
+        spec.spec_delta_prefill(len(lens), cu, sum(lens), s.st, 0, y.desc(spec), s.live,
+                                torch.zeros(256, dtype=torch.uint8).cuda())
