@@ -559,7 +559,8 @@ spec_status spec_delta_rows(int32_t B, int32_t R, const spec_state_desc *st, int
  * request b owns the input rows [cu_rows[b], cu_rows[b+1]) and rec_live gets its state after them.
  *   cu_rows   [B + 1] int32, ascending, cu_rows[0] = 0, cu_rows[B] <= rows; read on the device.
  *             Requests may be empty: their state is copied.
- *   rows      rows of q, k, v, log_decay, beta and out. 0 <= rows < 2^31.
+ *   rows      rows of q, k, v, log_decay, beta and out. 0 <= rows < 2^31; with 0 those six may
+ *             be NULL, and the states are copied.
  *   rec_init  the states before, in rec_live's layout; rec_live itself to continue in place; NULL
  *             for empty states.
  *   workspace spec_delta_prefill_workspace_bytes(rows, B, st) bytes (256 are enough where dtype

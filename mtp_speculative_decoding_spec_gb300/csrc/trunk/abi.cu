@@ -23,13 +23,14 @@ int64_t rec_elems(const spec_state_desc* st) {
   return e * hd;
 }
 
-// Checks shared by both calls, and the parameters they give.
-spec_status delta_params(const spec_state_desc* st, int32_t layer, const spec_delta_desc* d,
+// Checks shared by both calls, and the parameters they give. Without rows no pointer to them is needed.
+spec_status delta_params(const spec_state_desc* st, int32_t layer, const spec_delta_desc* d, bool any_rows,
                          DeltaParams& p) {
   memset(&p, 0, sizeof(p));
   if (!d || rec_elems(st) == 0 || layer < 0 || layer >= st->rec_layers) return SPEC_ERR_INVALID;
   if (d->dtype != SPEC_BF16 && d->dtype != SPEC_F32) return SPEC_ERR_INVALID;
-  if (!d->q || !d->k || !d->v || !d->log_decay || !d->beta || !d->out) return SPEC_ERR_INVALID;
+  if (any_rows && (!d->q || !d->k || !d->v || !d->log_decay || !d->beta || !d->out))
+    return SPEC_ERR_INVALID;
   if (d->key_heads < 1 || st->rec_heads % d->key_heads != 0) return SPEC_ERR_INVALID;
   const size_t e = d->dtype == SPEC_BF16 ? 2 : 4;
   const int64_t wqk = static_cast<int64_t>(d->key_heads) * st->rec_dk;
@@ -138,7 +139,7 @@ spec_status spec_delta_rows(int32_t B, int32_t R, const spec_state_desc* st, int
                             spec_stream_t stream) {
   if (B < 1 || R < 1 || R > kMaxRows) return SPEC_ERR_INVALID;
   DeltaParams p;
-  const spec_status s = delta_params(st, layer, d, p);
+  const spec_status s = delta_params(st, layer, d, true, p);
   if (s != SPEC_OK) return s;
   if (mode != SPEC_COMMIT_SNAPSHOT && mode != SPEC_COMMIT_REPLAY && mode != SPEC_COMMIT_INDEX)
     return SPEC_ERR_INVALID;
@@ -176,7 +177,7 @@ spec_status spec_delta_prefill(int32_t B, const int32_t* cu_rows, int64_t rows,
                                spec_stream_t stream) {
   if (B < 1 || !cu_rows || rows < 0 || rows >= (int64_t(1) << 31)) return SPEC_ERR_INVALID;
   DeltaParams p;
-  const spec_status s = delta_params(st, layer, d, p);
+  const spec_status s = delta_params(st, layer, d, rows > 0, p);
   if (s != SPEC_OK) return s;
   if (!st->rec_live || !aligned16(st->rec_live) || !aligned16(rec_init)) return SPEC_ERR_INVALID;
   p.B = B;

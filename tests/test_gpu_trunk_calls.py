@@ -1,4 +1,5 @@
-"""What a call of the trunk's token mixers asks of its caller: workspaces no larger than it uses."""
+"""What a call of the trunk's token mixers asks of its caller: workspaces no larger than it uses, no
+pointers where there is nothing to read."""
 
 import numpy as np
 import pytest
@@ -34,3 +35,22 @@ def test_fp32_prompts_need_the_header_alone(spec):
     with pytest.raises(spec.SpecError, match="SPEC_ERR_INVALID"):
         spec.spec_delta_prefill(len(lens), cu, sum(lens), s.st, 0, y.desc(spec), s.live,
                                 torch.zeros(256, dtype=torch.uint8).cuda())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("init", [False, True])
+def test_no_rows_at_all_copies_the_states(spec, dtype, init):
+    """Empty tensors have no address: of a call without rows only the states are touched."""
+    B, H, d = 3, 2, 128
+    x = Rows(0, H, H, d, d, dtype)
+    s = State(spec, B, 2, H, d, d, 2)
+    start, before = torch.randn_like(s.live), s.live.clone()
+    desc = x.desc(spec)
+    desc.q = desc.k = desc.v = desc.log_decay = desc.beta = desc.out = None
+    cu = torch.zeros(B + 1, dtype=torch.int32).cuda()
+    ws = torch.empty(spec.spec_delta_prefill_workspace_bytes(0, B, s.st), dtype=torch.uint8).cuda()
+    spec.spec_delta_prefill(B, cu, 0, s.st, 1, desc, start if init else None, ws)
+    want = start[:, 1] if init else torch.zeros_like(start[:, 1])
+    assert torch.equal(s.live[:, 1], want) and torch.equal(s.live[:, 0], before[:, 0])
+    with pytest.raises(spec.SpecError, match="SPEC_ERR_INVALID"):
+        spec.spec_delta_prefill(B, cu, 1, s.st, 1, desc, None, ws)
