@@ -618,8 +618,12 @@ typedef struct {
  *   workspace spec_prefix_attention_workspace_bytes(B, R, st, d) bytes, 256-byte aligned,
  *             ZERO-FILLED ONCE before its first use; the error word at byte offset 4 as in the
  *             conventions above.
- * B at most 1024. The positions are divided evenly over the SMs whatever the requests' lengths, and
- * the parts joined in a fixed order: the same call gives the same bytes.
+ * B at most 1024. With G = q_heads / kv_heads and tiles of 128 rows (bf16, head_dim 64, 128 or 256)
+ * or 16 (the rest), the ceil(B R G / tile) tiles over a prefix and the B ceil(R G / tile) over the own
+ * caches are at most 8,192, and the blocks of 32 positions under them, with eleven more a tile, fewer
+ * than 2^31. A call beyond that is refused as SPEC_ERR_UNSUPPORTED; the workspace query gives 0 for
+ * sizes that a call would be refused for. The positions are divided evenly over the SMs whatever the
+ * requests' lengths, and the parts joined in a fixed order: the same call gives the same bytes.
  */
 spec_status spec_prefix_attention(int32_t B, int32_t R, const spec_state_desc *st, int32_t layer,
                                   const spec_attn_desc *d, const int32_t *n_rows, void *workspace,

@@ -97,8 +97,6 @@ spec_status attn_plan_of(int32_t B, int32_t R, const spec_state_desc* st, const 
                          AttnPlan& w) {
   const spec_status s = attn_check(B, R, st, d);
   if (s != SPEC_OK) return s;
-  const DevAttr a = dev_attr();
-  if (a.sms <= 0) return SPEC_ERR_CUDA;
   w.tc = d->dtype == SPEC_BF16 && attn_tc_takes(d->head_dim);
   w.tm = w.tc ? attn_tc_tm() : attn_simt_tm();
   w.bn = w.tc ? attn_tc_bn(d->head_dim) : attn_simt_bn();
@@ -113,6 +111,8 @@ spec_status attn_plan_of(int32_t B, int32_t R, const spec_state_desc* st, const 
   const int64_t blocks = npi * ((prefix ? d->prefix_capacity : 0) / w.bn + 1 + kAttnOverPre) +
                          B * nown * (st->kv_capacity / w.bn + 1 + kAttnOver);
   if (items > kAttnMaxItems || blocks >= (int64_t(1) << 31)) return SPEC_ERR_UNSUPPORTED;
+  const DevAttr a = dev_attr();
+  if (a.sms <= 0) return SPEC_ERR_CUDA;
   w.npt = static_cast<int>(npt);
   w.npi = static_cast<int>(npi);
   w.nown = static_cast<int>(nown);

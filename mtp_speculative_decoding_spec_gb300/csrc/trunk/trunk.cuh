@@ -88,7 +88,7 @@ struct AttnParams {
   float* o;                 // [slots][tm][D]
 };
 
-constexpr int kAttnMaxItems = 8192;
+constexpr int kAttnMaxItems = 8192;  // four bytes each in shared memory, beside what a block holds
 constexpr int64_t kAttnMaxPos = (int64_t(1) << 31) - 256;  // a block past the last one still has an int
 // See `over`; own / prefix units at 0 / 0, 6 / 6, 6 / 10 and 4 / 10, us: 32 x 8 rows with 700 own positions each
 // over a prefix of 2,000 (100 own) 34.0, 33.8, 31.3, 30.6; of 15,360 87.9, 77.0, 75.5, 72.2; of 63,488 195.7,
