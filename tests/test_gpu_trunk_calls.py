@@ -1,5 +1,5 @@
 """What a call of the trunk's token mixers asks of its caller: workspaces no larger than it uses, no
-pointers where there is nothing to read."""
+pointers where there is nothing to read, and the stream that the caller has made current."""
 
 import numpy as np
 import pytest
@@ -54,3 +54,20 @@ def test_no_rows_at_all_copies_the_states(spec, dtype, init):
     assert torch.equal(s.live[:, 1], want) and torch.equal(s.live[:, 0], before[:, 0])
     with pytest.raises(spec.SpecError, match="SPEC_ERR_INVALID"):
         spec.spec_delta_prefill(B, cu, 1, s.st, 1, desc, None, ws)
+
+
+@pytest.mark.parametrize("raw", [True, False], ids=["raw query", "stream object"])
+def test_calls_run_on_the_current_stream(spec, raw, monkeypatch):
+    """Whichever way torch is asked for it; a stream given is taken as it is."""
+    monkeypatch.setattr(spec, "_raw_stream", None)
+    if not raw:
+        monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream")
+    side, other = torch.cuda.Stream(), torch.cuda.Stream()
+    assert spec._stream(None) == torch.cuda.current_stream().cuda_stream
+    with torch.cuda.stream(side):
+        assert spec._stream(None) == side.cuda_stream
+        with torch.cuda.stream(other):
+            assert spec._stream(None) == other.cuda_stream
+        assert spec._stream(None) == side.cuda_stream
+        assert spec._stream(other) == other.cuda_stream and spec._stream(7) == 7
+    assert spec._stream(None) == torch.cuda.current_stream().cuda_stream
