@@ -26,9 +26,9 @@
  *     per-request status (spec_accept_out.status) and that request commits nothing.
  *   - Workspace: calls that reduce across thread blocks take a caller-allocated workspace of
  *     at least spec_workspace_bytes() bytes (the token mixers: their own _workspace_bytes()),
- *     256-byte aligned, ZERO-FILLED ONCE before its first use. Every call leaves it reusable (its counters back at zero). Calls that may run
- *     concurrently (different streams) need separate workspaces. Byte offset 4 of the
- *     workspace holds a 32-bit error word that kernels set (never clear) if an internal
+ *     256-byte aligned, ZERO-FILLED ONCE before its first use. Every call leaves it reusable
+ *     (its counters back at zero). Calls that may run concurrently (different streams) need
+ *     separate workspaces. Byte offset 4 of the workspace holds a 32-bit error word that kernels set (never clear) if an internal
  *     bounded wait gives up; 0 means no error.
  *   - Limits: 1..8 verify rows per request (k = 0..7 drafts), at most 8 rows in total per
  *     spec_lmhead_verify / spec_draft_argmax call on the GEMV path; hidden size d with

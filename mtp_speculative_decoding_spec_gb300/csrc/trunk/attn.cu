@@ -42,8 +42,8 @@ constexpr int kPad = 16;          // bytes after a row of Q, K, V: rows start 16
 constexpr int kPsPitch = kSimtTm + 4;  // floats between positions' weights
 
 // 256 threads over a tile of 16 rows and blocks of 32 positions, the next block's K and V on their way to
-// the other of two buffers (as many buffers as fit were slower, 249 us for 222). Scores: a warp takes four rows and half of the dims, a lane a position, so that
-// a piece of K read serves four rows. The halves meet in shared memory, and four warps do the softmax of
+// the other of two buffers (as many buffers as fit were slower, 249 us for 222). Scores: a warp takes four
+// rows and half of the dims, a lane a position, so that a piece of K read serves four rows. The halves meet in shared memory, and four warps do the softmax of
 // four rows each. Values: a thread takes four consecutive dims of one, two or four rows. A block in which
 // some row's positions end takes only the positions a row sees, one by one, so what a masked position
 // holds reaches no row. fp32, 4 rows of 16 heads on 4 KV heads of 256 dims over 50,000 positions: 190 us = 2.2

@@ -21,9 +21,9 @@
 // does see one, that row's share of it is added by hand and the value cleared for the tensor cores.
 //
 // 16 query heads on 4 KV heads of 256 dims: 256 rows over 63,488 shared positions and 700 own ones each,
-// 189 us with the join = 1.42 PFLOP/s (0.73 of cuBLAS); a block of 64 positions takes about 1,450 cycles
-// against 1,024 of the tensor pipe, the rest the way from a block's scores through its softmax to its
-// second product, which two buffers of S hide in part. Two rows of one request over its own 63,488: 50.5
+// 190 to 204 us with the join, by GPU and run = 1.42 to 1.32 PFLOP/s (0.73 to 0.68 of cuBLAS); a block of
+// 64 positions takes about 1,450 cycles against 1,024 of the tensor pipe, the rest the way from a block's
+// scores through its softmax to its second product, which two buffers of S hide in part. Two rows of one request over its own 63,488: 50.5
 // us = 5.2 TB/s (0.76 of a copy), eight single rows over a shared 63,488 60 us = 5.0 TB/s: HBM while the
 // blocks run, and some 18 us of launch, plan, first loads, partials and join around them.
 #include <math.h>
@@ -198,9 +198,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* vfull = kdone + NS;
   uint64_t* vdone = vfull + NS;   // O has the block, and the stage is free
   uint64_t* vok = vdone + NS;     // V has landed and been looked through
-  // P (its first half, where there are halves) is written and V ok; its rest. One to a stage, as all of these: an arrival for block i + NS cannot come
-  // before block i's product is complete, so no barrier takes it for an earlier block's, and none runs
-  // through two phases while its waiter looks away.
+  // P (its first half, where there are halves) is written and V ok; its rest. One to a stage, as all of
+  // these: an arrival for block i + NS cannot come before block i's product is complete, so no barrier
+  // takes it for an earlier block's, and none runs through two phases while its waiter looks away.
   uint64_t* pready = vok + NS;
   uint64_t* prest = pready + NS;
   uint64_t* qready = prest + NS;
@@ -572,7 +572,9 @@ __global__ void __launch_bounds__(kThreads, 1)
               e0 = c0 + j < valid ? e0 : 0.f;
               e1 = c0 + j + 1 < valid ? e1 : 0.f;
             }
-            asm("add.rn.f32x2 %0, %0, %1;" : "+l"(sum[(j / 2) & 1]) : "l"(pack2(__float_as_uint(e0), __float_as_uint(e1))));
+            asm("add.rn.f32x2 %0, %0, %1;"
+                : "+l"(sum[(j / 2) & 1])
+                : "l"(pack2(__float_as_uint(e0), __float_as_uint(e1))));
             w[j / 2] = bf16_pair(e0, e1);
           }
           tmem_st16(ts + c0 / 2, w);

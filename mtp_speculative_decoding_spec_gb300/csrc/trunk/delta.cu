@@ -379,7 +379,6 @@ cudaError_t scan_of(const DeltaParams& p, int sms, cudaStream_t stream) {
 
 }  // namespace
 
-// vec_qk: every lane group's NI elements start on a multiple of their own size (at most 16 bytes)
 cudaError_t delta_scan_launch(const DeltaParams& p, spec_dtype dtype, int sms,
                               cudaStream_t stream) {
   return dtype == SPEC_BF16 ? scan_of<__nv_bfloat16>(p, sms, stream) : scan_of<float>(p, sms, stream);

@@ -23,8 +23,8 @@
 // the outputs of a column are NaN from its first token with such a u on. Finding out takes a vote of each
 // warp on r and on u: 472 us for 471 (below; with a branch of each thread's own 476 to 485).
 //
-// 16 heads of [128, 128], one prompt of 15,360 rows: 471 us, of which 74 the first kernel (0.25 GB, 3.3
-// TB/s) and 1.65 us a chunk the second; 63,488 rows 1.92 ms. q, k, v and the outputs alone would take 38
+// 16 heads of [128, 128], one prompt of 15,360 rows: 473 us, of which 75 the first kernel (0.25 GB, 3.3
+// TB/s) and 1.65 us a chunk the second; 63,488 rows 1.93 ms. q, k, v and the outputs alone would take 38
 // us: what bounds it is the chain's latency, some 3,300 cycles a chunk in which an SM's sub-core has one
 // warp of the chain and one of the outputs, its matrix instructions (198 of 8.3 cycles) half the time.
 #include <math.h>
@@ -430,8 +430,9 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
 // A warp of the chain has two tiles of eight tokens (w and 7 - w: the same work under causality) and a
 // quarter of S's rows. What a phase multiplies by (K, T) is read into registers before the barrier
 // that its other operand waits for. Warp 10 waits for the chain's stages in its place: even over, a
-// wait for a copy costs a warp 100 to 250 cycles, a named barrier 25 (488 -> 472 us). (S kept in registers as the next chunk's operand, its four partial
-// products meeting in shared memory instead, moves fewer bytes but took 2.16 us a chunk.)
+// wait for a copy costs a warp 100 to 250 cycles, a named barrier 25 (488 -> 472 us). (S kept in registers
+// as the next chunk's operand, its four partial products meeting in shared memory instead, moves fewer
+// bytes but took 2.16 us a chunk.)
 constexpr int kChainThreads = 12 * 32;  // three groups of four warps; the last one does nothing
 // Registers a thread: launched with 168 (64,512 in all), then shared out again by group, 63,488 in use.
 constexpr int kChainRegs = 224, kOutRegs = 168, kLoadRegs = 104;
@@ -949,7 +950,9 @@ size_t delta_chunk_workspace(int64_t rows, int B, int H) {
 // request of 16 rows 8.7 and 12.2 us, of 32 15.3 and 12.2, of 64 28.4 and 12.5; eight of 32 26.0 and
 // 44.6, of 64 48.8 and 45.6; 32 of 16 44.5 and 156, of 32 80.0 and 157, of 64 151 and 160. One request of
 // 15,360 7,549 and 488: with the limit any lower or higher, the worse of its two sides costs more, since
-// the host does not know whether the rows are spread evenly.
+// the host does not know whether the rows are spread evenly. Where they are not it can be far off: one
+// prompt of 1,000 rows takes 39 us alone, 156 among 30 single tokens (a block an SM for each of them) and
+// 509 among 32, which is the scan's side.
 bool delta_chunk_takes(const DeltaParams& p, spec_dtype dtype) {
   return dtype == SPEC_BF16 && delta_chunk_sizes(p.dk, p.dv) && p.vec_qk && p.vec_o &&
          (reinterpret_cast<uintptr_t>(p.v) & 15u) == 0 && p.vs % 8 == 0 && p.H <= 65535 &&
