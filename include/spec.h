@@ -593,7 +593,8 @@ size_t spec_delta_prefill_workspace_bytes(int64_t rows, int32_t B, const spec_st
  *   prefix_len  [B] int64 (clamped to [0, prefix_capacity]), or NULL: all of prefix_capacity.
  *   lse         [B*R][q_heads] float32 or NULL: log sum exp(scale q k) of each row, -Inf where a
  *               row has nothing to see, or sees scores of -Inf alone (its output is zero). A row
- *               that sees a score that is NaN has NaN in its output and here.
+ *               that sees a score that is NaN has NaN in its output and here. A value that is
+ *               not finite shows in its dim of every other row that sees it, whatever its weight.
  */
 typedef struct {
   spec_dtype dtype;

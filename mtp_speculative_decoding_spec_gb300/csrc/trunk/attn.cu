@@ -245,7 +245,9 @@ __global__ void __launch_bounds__(kSimtThreads, 1)
 // own unit, warp w taking every NW-th of them, joined in that order. Many rows have few partials
 // each and get one warp a row (four rows to a block); few rows have many, and get eight warps. The whole
 // call, 16 query heads of 256 dims over a prefix of 15,360, one warp and eight: 8 verify rows 31.1 and 25.6
-// us, 32 39.4 and 38.3, 48 36.6 and 37.1, 64 39.5 and 42.7, 128 48.3 and 58.8.
+// us, 32 39.4 and 38.3, 48 36.6 and 37.1, 64 39.5 and 42.7, 128 48.3 and 58.8. A partial of weight 0, from
+// a row that saw nothing there or scores of -Inf alone, is added like any: its output is 0, or what is not
+// finite among the values of positions that the row does see.
 constexpr int kJoinMost = 4;  // partials in flight per warp
 
 template <typename T, int NW>
@@ -307,7 +309,6 @@ __global__ void __launch_bounds__(NW == 1 ? 128 : 32 * NW)
       for (int d = 0; d < 4; ++d) acc[h][d] *= c;
 #pragma unroll
     for (int j = 0; j < kJoinMost; ++j) {
-      if (mlv[j].x == -INFINITY) continue;  // nothing seen there
       const float w = exp2f(mlv[j].x - ref);
       l = fmaf(w, mlv[j].y, l);
 #pragma unroll
@@ -351,18 +352,18 @@ __global__ void __launch_bounds__(NW == 1 ? 128 : 32 * NW)
   float top = -INFINITY;
 #pragma unroll
   for (int w = 0; w < NW; ++w) top = (top != top || sm_m[w] != sm_m[w]) ? NAN : fmaxf(top, sm_m[w]);
+  const float ref = top == -INFINITY ? 0.f : top;
   float wt[NW], tot = 0.f;
 #pragma unroll
   for (int w = 0; w < NW; ++w) {
-    wt[w] = sm_m[w] == -INFINITY ? 0.f : exp2f(sm_m[w] - top);
-    if (wt[w] != 0.f) tot = fmaf(wt[w], sm_l[w], tot);
+    wt[w] = exp2f(sm_m[w] - ref);
+    tot = fmaf(wt[w], sm_l[w], tot);
   }
   const float inv = tot == 0.f ? 0.f : 1.f / tot;
   for (int d = threadIdx.x; d < p.D; d += 32 * NW) {
     float v = 0.f;
 #pragma unroll
-    for (int w = 0; w < NW; ++w)
-      if (wt[w] != 0.f) v = fmaf(wt[w], sm_o[w][d], v);
+    for (int w = 0; w < NW; ++w) v = fmaf(wt[w], sm_o[w][d], v);
     v = top == -INFINITY ? 0.f : v * inv;
     if constexpr (sizeof(T) == 2)
       dst[d] = __float2bfloat16_rn(v);

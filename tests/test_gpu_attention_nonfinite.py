@@ -102,3 +102,24 @@ def test_negative_scale(spec, dtype, D):
              seed=4, scale=-(D ** -0.5))
     c.run(spec)
     c.check()
+
+
+@pytest.mark.parametrize("dtype,D", TYPES)
+@pytest.mark.parametrize("B", [2, 80])
+@pytest.mark.parametrize("key", [-INF, -100.0])
+def test_a_value_of_no_weight(spec, dtype, D, B, key):
+    """A position that is seen with a weight of zero, from a score of -Inf or one too small for a
+    float, and holds NaN or an infinity: 0 times that is NaN, in the dims where it lies and whether or
+    not the position is a piece of work by itself."""
+    c = Case(B, 1, 8, 2, D, 1, 300, [(53 * b) % 290 for b in range(B)], dtype, seed=5, scale=1.0)
+    c.q[:] = 1.0
+    c.prefix[0] = key  # the shared position; the own ones score about sqrt(D)
+    c.run(spec)
+    clean, lse = heads(c).clone(), c.lse.clone()
+    assert torch.isfinite(clean).all()
+    c.prefix[1, 0, 5], c.prefix[1, 0, D + 6] = NAN, INF
+    c.run(spec)
+    bad = torch.zeros_like(clean, dtype=torch.bool)
+    bad[:, :4, 5] = bad[:, 4:, 6] = True
+    assert torch.isnan(heads(c)[bad]).all()
+    assert torch.equal(heads(c)[~bad], clean[~bad]) and torch.equal(c.lse, lse)
