@@ -244,10 +244,10 @@ __global__ void __launch_bounds__(kSimtThreads, 1)
 // One output row (verify row, query head) by NW warps: the partials of its prefix unit and then of its
 // own unit, warp w taking every NW-th of them, joined in that order. Many rows have few partials
 // each and get one warp a row (four rows to a block); few rows have many, and get eight warps. The whole
-// call, 16 query heads of 256 dims over a prefix of 15,360, one warp and eight: 8 verify rows 31.1 and 25.6
-// us, 32 39.4 and 38.3, 48 36.6 and 37.1, 64 39.5 and 42.7, 128 48.3 and 58.8. A partial of weight 0, from
-// a row that saw nothing there or scores of -Inf alone, is added like any: its output is 0, or what is not
-// finite among the values of positions that the row does see.
+// call, 16 query heads of 256 dims over a prefix of 15,360, one warp and eight: 8 verify rows 28.9 and 22.2
+// us, 32 32.8 and 30.2, 40 32.7 and 32.8, 48 32.7 and 33.5, 64 33.6 and 36.0, 128 42.6 and 51.9.
+// A partial of weight 0, from a row that saw nothing there or scores of -Inf alone, is added like any:
+// its output is 0, or what is not finite among the values of positions that the row does see.
 constexpr int kJoinMost = 4;  // partials in flight per warp
 
 template <typename T, int NW>
