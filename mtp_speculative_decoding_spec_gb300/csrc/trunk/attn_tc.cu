@@ -275,18 +275,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       const CUtensorMap* mv = pre ? &maps.pv : &maps.ov;
       const int n = a.blk1 - a.blk0;
       ok = load(sk, kfull, kdone, mk, it, a.blk0);
-      for (int j = 0; ok && j < n; ++j) {
+      int j = 0;
+      for (; ok && j < n; ++j) {
         if (j + 1 < n) ok = load(sk, kfull, kdone, mk, it + j + 1, a.blk0 + j + 1);
         ok = ok && load(sv, vfull, vdone, mv, it + j, a.blk0 + j);
       }
-      it += n;
+      it += j;
     }
     if (!ok && lane == 0) give_up();
-    // leave nothing in flight: the last loads of every stage have landed
-    for (int j = max(0, it - NS); j < it; ++j) {
-      mbar_wait_warp(&kfull[j % NS], (j / NS) & 1);
-      mbar_wait_warp(&vfull[j % NS], (j / NS) & 1);
-    }
+    // Leave nothing in flight: the last loads of every stage have landed. Where a wait ran out, V's last
+    // was not sent and one more of K's may have been; what was not sent costs a wait with its limit.
+    for (int j = max(0, it - NS); j < it + !ok; ++j) mbar_wait_warp(&kfull[j % NS], (j / NS) & 1);
+    for (int j = max(0, it - NS - !ok); j < it; ++j) mbar_wait_warp(&vfull[j % NS], (j / NS) & 1);
   } else if (warp == 1) {
     // ------------------------------------------------------------------ MMA issuer
     {
