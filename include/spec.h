@@ -632,6 +632,148 @@ spec_status spec_prefix_attention(int32_t B, int32_t R, const spec_state_desc *s
 size_t spec_prefix_attention_workspace_bytes(int32_t B, int32_t R, const spec_state_desc *st,
                                              const spec_attn_desc *d);
 
+/*
+ * A KV cache in pages (no counterpart on the pages: the cache of a server of many requests, whose
+ * lengths nobody knows in advance). spec_paged_append writes the new rows of a pass into it, with the
+ * norms of queries and keys and the position rotation on the way; spec_paged_attention attends from
+ * them; spec_paged_commit keeps or drops them, as spec_commit_rollback does for contiguous caches.
+ *
+ * spec_paged_cache is a HOST struct of DEVICE pointers. Position p of request b lies on page
+ * page_table[b*table_stride + p / page_size], as its position p % page_size; position i of page g of
+ * layer l is kv_heads*head_dim elements at
+ *     k_pages + l*layer_stride + g*page_stride + i*row   (bytes; row = those elements' bytes)
+ * and its value likewise at v_pages. Both [layers][n_pages][page_size] and [n_pages][layers][..] are
+ * such layouts, and so is a contiguous cache per request (one page each).
+ *   dtype        of the pages and of q, k, v and out: SPEC_BF16 or SPEC_F32.
+ *   head_dim     a multiple of 8 up to 256 (else SPEC_ERR_UNSUPPORTED).
+ *   page_size    positions a page, >= 1. Attention in bf16 runs on the tensor cores where head_dim
+ *                is 64, 128 or 256 and page_size 8, 16, 32, 64 or a multiple of 128, else on the
+ *                CUDA cores.
+ *   k_pages, v_pages, layer_stride, page_stride   multiples of 16 bytes; layers and pages do not overlap.
+ *   page_table   [B][max_pages] int32 in rows of table_stride entries. An entry outside [0, n_pages) is
+ *                a page that is not there: nothing is written to its positions, and no row sees them.
+ *                Requests may share pages that nobody writes to (a common prompt); the pages that rows
+ *                are appended to belong to one request.
+ *   kv_len       [B] int64: P, the positions in the cache before the call's rows. Row r of request b
+ *                sits at position kv_len[b] + r. Negative lengths count as 0.
+ * A request has max_pages * page_size positions, at most 2^31 - 256, and n_pages < 2^31.
+ *
+ * The rows of a call, in all three: request b owns rows [cu_rows[b], cu_rows[b+1]) of `rows`.
+ *   cu_rows   [B + 1] int32, ascending, read on the device (clamped to [0, rows]). Requests may own
+ *             none. Rows that nobody owns (behind the last request's) are left as they are.
+ *   n_rows    [B] int32 or NULL (all): of its rows request b runs the first n_rows[b] (clamped), so a
+ *             verify pass of mixed widths may keep its rows at b*R + r.
+ * B at most 512.
+ */
+typedef struct {
+  spec_dtype dtype;
+  int32_t layers, kv_heads, head_dim;
+  int32_t page_size;
+  int64_t n_pages;
+  void *k_pages;
+  void *v_pages;
+  int64_t layer_stride, page_stride;
+  const int32_t *page_table;
+  int64_t table_stride;
+  int32_t max_pages;
+  int64_t *kv_len;
+} spec_paged_cache;
+
+/*
+ * spec_paged_append -- of every row that runs: each query and key head normed and rotated, queries
+ * to q_out, keys and values to their pages of the given layer. Per head x of head_dim values:
+ *     y = w x / sqrt(mean(x^2) + norm_eps)          (w NULL: y = x)
+ *     of the first rot_dim dims, pairs (a, b) turned by the angle t = pos * inv_freq[i], i < rot_dim/2:
+ *         y_a' = rot_scale (y_a cos t - y_b sin t),   y_b' = rot_scale (y_b cos t + y_a sin t)
+ * in fp32, rounded once; values are copied.
+ *   q_heads          heads of q; 0: no queries (q, q_out unused). k and v both NULL: nothing is written
+ *                    to the cache.
+ *   q, k, v, q_out   row t at q + t*q_stride (elements), heads contiguous; they may be column ranges of
+ *                    one wider row. q_out may be q itself with the same stride. Rows that do not run
+ *                    leave q_out as it is.
+ *   q_norm, k_norm   [head_dim] float32 or NULL.
+ *   rot_dim          even, 0 (no rotation) .. head_dim. Pairs are (i, i + rot_dim/2), or (2i, 2i + 1)
+ *                    with rot_interleaved.
+ *   inv_freq         [rot_dim/2] float32, finite, below 2^24 in size; any table, so any scaling for long
+ *                    contexts. Angles are formed in fixed point from the whole product: positions up to
+ *                    2^31 cost no accuracy.
+ *   rot_scale        factor on cos and sin (1 where the scaling has none).
+ *   pos              [B] int64 or NULL: the rotation's position of each request's first row (after a
+ *                    prefix kept elsewhere); NULL: kv_len[b].
+ *   status           [B] int32 or NULL: SPEC_REQ_KV_OVERFLOW where rows of the request lie past its table
+ *                    or on pages that are not there (those are not written), else SPEC_REQ_OK.
+ * kv_len is not moved: spec_paged_commit does that.
+ */
+typedef struct {
+  int32_t q_heads;
+  const void *q;
+  const void *k;
+  const void *v;
+  int64_t q_stride, k_stride, v_stride;
+  void *q_out;
+  int64_t q_out_stride;
+  const float *q_norm;
+  const float *k_norm;
+  float norm_eps;
+  int32_t rot_dim, rot_interleaved;
+  const float *inv_freq;
+  float rot_scale;
+  const int64_t *pos;
+} spec_append_desc;
+
+spec_status spec_paged_append(int32_t B, const int32_t *cu_rows, int64_t rows,
+                              const spec_paged_cache *c, int32_t layer, const spec_append_desc *d,
+                              const int32_t *n_rows, int32_t *status, spec_stream_t stream);
+
+/*
+ * spec_paged_attention -- o = softmax(scale q K^T) V of every row that runs over the positions
+ * 0 .. kv_len[b] + r of its request (its own, already appended, included) that are there. Any number of
+ * rows a request: verify rows, whole prompts and chunks of prompts, in one call.
+ *   q_heads   a multiple of kv_heads, at most 64 per KV head; query head h reads KV head
+ *             h / (q_heads / kv_heads).
+ *   q, out    row t at q + t*q_stride (elements): [q_heads][head_dim].
+ *   lse       [rows][q_heads] float32 or NULL: log sum exp(scale q k), -Inf where a row has nothing to
+ *             see or scores of -Inf alone (its output is zero). Rows that a request owns and does not
+ *             run give zero and -Inf. Values that are not finite show as in spec_prefix_attention: in
+ *             the rows that see them, and what a masked position holds in none.
+ *   workspace spec_paged_attention_workspace_bytes(B, rows, c, d) bytes, 256-byte aligned, ZERO-FILLED
+ *             ONCE before its first use; the error word at byte offset 4 as in the conventions above.
+ * With G = q_heads / kv_heads and tiles of 128 rows (tensor cores) or 16 (CUDA cores), rows*G / tile + B
+ * is at most 4,096 and 12,288; a call beyond that is refused as SPEC_ERR_UNSUPPORTED, and the workspace
+ * query gives 0 for sizes that a call would be refused for. The positions are divided over the SMs whatever
+ * the requests' lengths and the parts joined in a fixed order: the same call gives the same bytes.
+ */
+typedef struct {
+  int32_t q_heads;
+  const void *q;
+  int64_t q_stride;
+  void *out;
+  int64_t out_stride;
+  float scale;
+  float *lse;
+} spec_paged_attn_desc;
+
+spec_status spec_paged_attention(int32_t B, const int32_t *cu_rows, int64_t rows,
+                                 const spec_paged_cache *c, int32_t layer,
+                                 const spec_paged_attn_desc *d, const int32_t *n_rows, void *workspace,
+                                 size_t workspace_bytes, spec_stream_t stream);
+size_t spec_paged_attention_workspace_bytes(int32_t B, int64_t rows, const spec_paged_cache *c,
+                                            const spec_paged_attn_desc *d);
+
+/*
+ * spec_paged_commit -- spec_commit_rollback's part of a paged cache (a recurrent state beside it is
+ * committed by that call, with kv_layers = 0): with m = acc[b].n_emit (0 if acc[b].status != 0),
+ * rows [P+m, P+k[b]+1) become zero in every layer and kv_len[b] = P + m.
+ *   acc    [B] spec_accept_out, or NULL: request b keeps all of its k[b] rows (a prompt's chunk): kv_len[b]
+ *          = P + k[b], nothing is cleared.
+ *   k      [B] the cycle's draft counts, 0..7 (acc NULL: rows, any number).
+ *   commit_status  [B] int32 or NULL: SPEC_REQ_OK; SPEC_REQ_BAD_K where k[b] is out of range (m is 0 then,
+ *          nothing is cleared and kv_len stays); SPEC_REQ_KV_OVERFLOW where P + k[b] + 1 (acc NULL:
+ *          P + k[b]) exceeds the request's positions (the clearing stops there).
+ */
+spec_status spec_paged_commit(int32_t B, const spec_paged_cache *c, const spec_accept_out *acc,
+                              const int32_t *k, int32_t *commit_status, spec_stream_t stream);
+
 /* 1 if this build has the batched tensor-core path for more than 8 verify rows per call. */
 int32_t spec_batched_supported(void);
 

@@ -13,7 +13,8 @@ from ._abi import (ACCEPT_OUT_DTYPE, COUNTERS_DTYPE, REQ_BAD_FILTER, REQ_BAD_K, 
                    REQ_KV_OVERFLOW, REQ_NO_LOGITS, REQ_NONFINITE, REQ_OK, ROWSTATS_DTYPE,
                    SPEC_BF16, SPEC_COMMIT_INDEX, SPEC_COMMIT_REPLAY, SPEC_COMMIT_SNAPSHOT, SPEC_F32,
                    SPEC_Q4A32,
-                   WIDTH_STATE_DTYPE, spec_attn_desc, spec_delta_desc, spec_state_desc)
+                   WIDTH_STATE_DTYPE, spec_append_desc, spec_attn_desc, spec_delta_desc,
+                   spec_paged_attn_desc, spec_paged_cache, spec_state_desc)
 
 ROWSTATS_BYTES = ROWSTATS_DTYPE.itemsize
 ACCEPT_OUT_BYTES = ACCEPT_OUT_DTYPE.itemsize
@@ -246,6 +247,30 @@ def spec_prefix_attention(B, R, st, layer, desc, n_rows, workspace, stream=None)
 
 def spec_prefix_attention_workspace_bytes(B, R, st, desc):
     return int(_abi.lib().spec_prefix_attention_workspace_bytes(B, R, st, desc))
+
+
+def spec_paged_append(B, cu_rows, rows, cache, layer, desc, n_rows=None, status=None, stream=None):
+    """``cache`` a ``spec_paged_cache``, ``desc`` a ``spec_append_desc`` (host structs of device
+    pointers)."""
+    _check("spec_paged_append", _abi.lib().spec_paged_append(
+        B, _ptr(cu_rows), rows, cache, layer, desc, _ptr(n_rows), _ptr(status), _stream(stream)))
+
+
+def spec_paged_attention(B, cu_rows, rows, cache, layer, desc, n_rows, workspace, stream=None):
+    """``cache`` a ``spec_paged_cache``, ``desc`` a ``spec_paged_attn_desc`` (host structs of device
+    pointers)."""
+    _check("spec_paged_attention", _abi.lib().spec_paged_attention(
+        B, _ptr(cu_rows), rows, cache, layer, desc, _ptr(n_rows), _ptr(workspace),
+        _nbytes(workspace), _stream(stream)))
+
+
+def spec_paged_attention_workspace_bytes(B, rows, cache, desc):
+    return int(_abi.lib().spec_paged_attention_workspace_bytes(B, rows, cache, desc))
+
+
+def spec_paged_commit(B, cache, acc, k, commit_status=None, stream=None):
+    _check("spec_paged_commit", _abi.lib().spec_paged_commit(
+        B, cache, _ptr(acc), _ptr(k), _ptr(commit_status), _stream(stream)))
 
 
 def spec_lmhead_verify_noalloc(W, wdt, V, d, H, B, R, temperature, logits, stats, stream=None):

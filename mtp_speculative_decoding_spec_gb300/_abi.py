@@ -24,6 +24,8 @@ EXPORTS = ("spec_workspace_bytes", "spec_status_str", "spec_lmhead_verify",
            "spec_commit_rollback", "spec_delta_rows", "spec_delta_prefill",
            "spec_delta_prefill_workspace_bytes", "spec_prefix_attention",
            "spec_prefix_attention_workspace_bytes",
+           "spec_paged_append", "spec_paged_attention", "spec_paged_attention_workspace_bytes",
+           "spec_paged_commit",
            "spec_batched_supported", "spec_host_alias", "spec_copy_from_host",
            "spec_lmhead_verify_noalloc", "spec_noalloc_scratch_bytes",
            "spec_noalloc_error_word", "spec_test_verify_stalled",
@@ -111,6 +113,59 @@ class spec_attn_desc(ctypes.Structure):
     ]
 
 
+class spec_paged_cache(ctypes.Structure):
+    _fields_ = [
+        ("dtype", ctypes.c_int32),
+        ("layers", ctypes.c_int32),
+        ("kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("n_pages", ctypes.c_int64),
+        ("k_pages", ctypes.c_void_p),
+        ("v_pages", ctypes.c_void_p),
+        ("layer_stride", ctypes.c_int64),
+        ("page_stride", ctypes.c_int64),
+        ("page_table", ctypes.c_void_p),
+        ("table_stride", ctypes.c_int64),
+        ("max_pages", ctypes.c_int32),
+        ("kv_len", ctypes.c_void_p),
+    ]
+
+
+class spec_append_desc(ctypes.Structure):
+    _fields_ = [
+        ("q_heads", ctypes.c_int32),
+        ("q", ctypes.c_void_p),
+        ("k", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("q_stride", ctypes.c_int64),
+        ("k_stride", ctypes.c_int64),
+        ("v_stride", ctypes.c_int64),
+        ("q_out", ctypes.c_void_p),
+        ("q_out_stride", ctypes.c_int64),
+        ("q_norm", ctypes.c_void_p),
+        ("k_norm", ctypes.c_void_p),
+        ("norm_eps", ctypes.c_float),
+        ("rot_dim", ctypes.c_int32),
+        ("rot_interleaved", ctypes.c_int32),
+        ("inv_freq", ctypes.c_void_p),
+        ("rot_scale", ctypes.c_float),
+        ("pos", ctypes.c_void_p),
+    ]
+
+
+class spec_paged_attn_desc(ctypes.Structure):
+    _fields_ = [
+        ("q_heads", ctypes.c_int32),
+        ("q", ctypes.c_void_p),
+        ("q_stride", ctypes.c_int64),
+        ("out", ctypes.c_void_p),
+        ("out_stride", ctypes.c_int64),
+        ("scale", ctypes.c_float),
+        ("lse", ctypes.c_void_p),
+    ]
+
+
 _lib = None
 
 
@@ -178,6 +233,16 @@ def lib():
         L.spec_prefix_attention.restype = i32
         L.spec_prefix_attention_workspace_bytes.argtypes = [i32, i32, pst, pad]
         L.spec_prefix_attention_workspace_bytes.restype = sz
+        ppc, pap, ppa = (ctypes.POINTER(t) for t in (spec_paged_cache, spec_append_desc,
+                                                     spec_paged_attn_desc))
+        L.spec_paged_append.argtypes = [i32, vp, i64, ppc, i32, pap, vp, vp, vp]
+        L.spec_paged_append.restype = i32
+        L.spec_paged_attention.argtypes = [i32, vp, i64, ppc, i32, ppa, vp, vp, sz, vp]
+        L.spec_paged_attention.restype = i32
+        L.spec_paged_attention_workspace_bytes.argtypes = [i32, i64, ppc, ppa]
+        L.spec_paged_attention_workspace_bytes.restype = sz
+        L.spec_paged_commit.argtypes = [i32, ppc, vp, vp, vp, vp]
+        L.spec_paged_commit.restype = i32
         L.spec_lmhead_verify_noalloc.argtypes = [vp, i32, i64, i64, vp, i32, i32, vp, vp, vp, vp]
         L.spec_lmhead_verify_noalloc.restype = i32
         L.spec_noalloc_scratch_bytes.argtypes = []

@@ -1,0 +1,309 @@
+// Launch parameters of the paged KV cache's calls, and what attention's kernels (trunk/attn.cuh,
+// trunk/attn_tc.cuh) ask of them.
+#pragma once
+
+#include "trunk/trunk.cuh"
+
+namespace spec {
+
+constexpr int kPagedMaxB = 512;
+constexpr int kPagedMaxTiles = 4096, kPagedSimtMaxTiles = 12288;  // four bytes each in shared memory
+
+// One layer of a paged cache.
+struct PagedLayer {
+  uint8_t *k, *v;
+  int64_t page_stride, table_stride;
+  const int32_t* table;
+  int64_t* kv_len;
+  int row_bytes, page_size, n_pages, max_pages;
+};
+
+// Bytes from the layer's first page to a position of request b, or -1 where its page is not there.
+__device__ __forceinline__ int64_t paged_offset(const PagedLayer& c, int b, int pos) {
+  const int j = pos / c.page_size;
+  if (j >= c.max_pages) return -1;
+  const int g = __ldg(c.table + b * c.table_stride + j);
+  if (g < 0 || g >= c.n_pages) return -1;
+  return g * c.page_stride + static_cast<int64_t>(pos - j * c.page_size) * c.row_bytes;
+}
+
+// How many of the requests' ends cu[1..B] lie at or before a row: the request of a row that has one. By a
+// whole warp; B at most 1,024.
+__device__ __forceinline__ int paged_request_of(const int32_t* cu, int B, int64_t row) {
+  const int lane = threadIdx.x & 31;
+  int first = 0;
+  if (B > 32) {
+    const int i = 32 * (lane + 1);
+    first = 32 * __popc(__ballot_sync(0xffffffffu, i <= B && cu[min(i, B)] <= row));
+  }
+  const int i = first + lane + 1;
+  return first + __popc(__ballot_sync(0xffffffffu, i <= B && cu[min(i, B)] <= row));
+}
+
+// Request b's rows: where they begin, how many it owns and how many of them run.
+struct PagedRows {
+  int start, owned, runs;
+};
+__device__ __forceinline__ PagedRows paged_rows(const int32_t* cu, const int32_t* n_rows, int64_t rows, int b) {
+  const int total = static_cast<int>(rows);
+  PagedRows r;
+  r.start = max(0, min(cu[b], total));
+  r.owned = max(r.start, min(cu[b + 1], total)) - r.start;
+  r.runs = n_rows ? max(0, min(n_rows[b], r.owned)) : r.owned;
+  return r;
+}
+
+struct AppendParams {
+  PagedLayer c;
+  int B, Hq, Hkv, D;
+  int nq, nk;            // query heads, and key heads, that are processed (values: as many as keys)
+  int64_t rows;
+  const int32_t *cu_rows, *n_rows;
+  const void *q, *k, *v;
+  void* q_out;
+  int64_t qs, ks, vs, qos;
+  int vec_in, vec_out;   // rows of q, k, v; of q_out are whole 16-byte vectors
+  const float *q_norm, *k_norm;
+  float eps;
+  int rot;
+  const float* inv_freq;
+  float rot_scale;
+  const int64_t* pos;
+  int32_t* status;
+  int tph;               // lanes of a head
+  int iters;             // turns of a warp over a row's heads
+  int per_task;          // of which one task takes so many
+  int tasks_row;
+  int64_t tasks, tasks_warp;
+};
+cudaError_t append_launch(AppendParams& p, spec_dtype dtype, bool interleaved, int sms, cudaStream_t stream);
+
+struct PagedCommitParams {
+  PagedLayer c;
+  int64_t layer_stride;
+  int layers;
+  const spec_accept_out* acc;
+  const int32_t* k;
+  int32_t* status;
+};
+cudaError_t paged_commit_launch(const PagedCommitParams& p, int B, cudaStream_t stream);
+
+// Attention of new rows over a paged cache. A request's rows times the query heads of a KV head, stacked
+// (x = r G + g), are cut into tiles; a unit is a tile and a KV head over the positions that its last row
+// sees. Requests of many tiles over many positions have them in groups of `grp`, as a shared prefix has.
+// Of AttnParams npt, npi, nown and items are not used but for `items`, the most tiles that there can be; a
+// tile's number is its place in the request and the request.
+struct PagedReq {
+  int start, rows, base;  // first row, rows that run, positions before them
+  int g0, s0;             // its first item of `grp` tiles, its first item of a single tile
+};
+struct PagedParams : AttnParams {
+  PagedLayer c;
+  const int32_t* cu_rows;
+  int64_t rows;
+  int group_min;          // positions from which a request's tiles are grouped
+  int4* reqs;             // for the join: first row, rows, g0, s0
+};
+template <>
+inline constexpr bool kPaged<PagedParams> = true;
+
+__device__ __forceinline__ int64_t paged_offset(const PagedParams& p, int b, int pos) {
+  return paged_offset(p.c, b, pos);
+}
+
+// cum[0..items], then the counts of grouped and of all items, then the requests.
+__host__ __device__ inline size_t attn_plan_bytes(const PagedParams& p) {
+  return sizeof(int32_t) * (p.items + 3) + sizeof(PagedReq) * p.B;
+}
+__device__ __forceinline__ int attn_group_items(const PagedParams& p, const int32_t* cum) {
+  return cum[p.items + 1];
+}
+__device__ __forceinline__ int attn_items(const PagedParams& p, const int32_t* cum) { return cum[p.items + 2]; }
+__device__ __forceinline__ const PagedReq* paged_reqs(const PagedParams& p, const int32_t* cum) {
+  return reinterpret_cast<const PagedReq*>(cum + p.items + 3);
+}
+__device__ __forceinline__ int paged_tiles(const PagedParams& p, int rows) { return (rows * p.G + p.tm - 1) / p.tm; }
+__device__ __forceinline__ int paged_groups(const PagedParams& p, int rows, int base) {
+  const int n = paged_tiles(p, rows);
+  return p.grp > 1 && n >= p.grp && base + rows >= p.group_min ? n / p.grp : 0;
+}
+// What a request's tile sees: up to its last row's position.
+__device__ __forceinline__ int paged_sees(const PagedParams& p, const PagedReq& r, int tile) {
+  const int last = min(r.rows, ((tile + 1) * p.tm - 1) / p.G + 1);
+  return static_cast<int>(min(p.kcap, static_cast<int64_t>(r.base) + last));
+}
+
+// As for AttnParams: by the whole block, in shared memory, a barrier at the end. Requests whose tiles would
+// be more than there can be (cu_rows not as documented) have none.
+__device__ __forceinline__ const PagedReq* attn_plan(const PagedParams& p, int32_t* cum) {
+  const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31;
+  PagedReq* req = const_cast<PagedReq*>(paged_reqs(p, cum));
+  for (int b = tid; b < p.B; b += nt) {
+    const PagedRows r = paged_rows(p.cu_rows, p.n_rows, p.rows, b);
+    req[b].start = r.start;
+    req[b].rows = r.runs;
+    req[b].base = static_cast<int>(max(static_cast<int64_t>(0), min(p.kv_len[b], p.kcap)));
+  }
+  __syncthreads();
+  if (tid < 32) {
+    int all = 0, groups = 0, singles = 0;
+    for (int b0 = 0; b0 < p.B; b0 += 32) {
+      const int b = b0 + lane;
+      int n = b < p.B ? paged_tiles(p, req[b].rows) : 0, at = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, at, o);
+        if (lane >= o) at += x;
+      }
+      if (all + at > p.items) n = 0;
+      all = min(p.items + 1, all + __shfl_sync(0xffffffffu, at, 31));
+      if (b < p.B && n == 0) req[b].rows = 0;
+      const int g = b < p.B ? paged_groups(p, req[b].rows, req[b].base) : 0;
+      int cg = g, cs = n - g * p.grp;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, cg, o), y = __shfl_up_sync(0xffffffffu, cs, o);
+        if (lane >= o) {
+          cg += x;
+          cs += y;
+        }
+      }
+      if (b < p.B) {
+        req[b].g0 = groups + cg - g;
+        req[b].s0 = singles + cs - (n - g * p.grp);
+      }
+      groups += __shfl_sync(0xffffffffu, cg, 31);
+      singles += __shfl_sync(0xffffffffu, cs, 31);
+    }
+    for (int b = lane; b < p.B; b += 32) req[b].s0 += groups;
+    if (lane == 0) {
+      cum[0] = 0;
+      cum[p.items + 1] = groups;
+      cum[p.items + 2] = groups + singles;
+    }
+  }
+  __syncthreads();
+  for (int b = tid >> 5; b < p.B; b += nt >> 5) {  // a warp to a request
+    const PagedReq r = req[b];
+    const int n = paged_tiles(p, r.rows), ng = paged_groups(p, r.rows, r.base);
+    for (int i = lane; i < ng; i += 32)
+      cum[r.g0 + i + 1] = (paged_sees(p, r, (i + 1) * p.grp - 1) + p.bn - 1) / p.bn + p.over[0];
+    for (int t = ng * p.grp + lane; t < n; t += 32)
+      cum[r.s0 + t - ng * p.grp + 1] = (paged_sees(p, r, t) + p.bn - 1) / p.bn + p.over[1];
+  }
+  __syncthreads();
+  if (tid < 32) {
+    const int items = cum[p.items + 2];
+    int base = 0;
+    for (int i0 = 1; i0 <= items; i0 += 32) {
+      const int i = i0 + lane;
+      int v = i <= items ? cum[i] : 0;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += x;
+      }
+      v += base;
+      if (i <= items) cum[i] = v;
+      base = __shfl_sync(0xffffffffu, v, 31);
+    }
+  }
+  if (blockIdx.x == 0)
+    for (int b = tid; b < p.B; b += nt) p.reqs[b] = make_int4(req[b].start, req[b].rows, req[b].g0, req[b].s0);
+  __syncthreads();
+  return req;
+}
+
+constexpr int kTileReqBits = 9;
+static_assert(kPagedMaxB <= 1 << kTileReqBits);
+__device__ __forceinline__ int attn_tile_req(const PagedParams&, int tile) {
+  return tile & ((1 << kTileReqBits) - 1);
+}
+// The request of an item: the last whose first one (of its kind) is not after it and that has any there.
+__device__ __forceinline__ int attn_single_tile(const PagedParams& p, const int32_t* cum, int item) {
+  const PagedReq* req = paged_reqs(p, cum);
+  int lo = 0, hi = p.B;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (req[mid].s0 <= item)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  const int t = item - req[lo].s0 + paged_groups(p, req[lo].rows, req[lo].base) * p.grp;
+  return t << kTileReqBits | lo;
+}
+__device__ __forceinline__ int attn_group_tile(const PagedParams& p, const int32_t* cum, int item, int rank) {
+  const PagedReq* req = paged_reqs(p, cum);
+  int lo = 0, hi = p.B;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (req[mid].g0 <= item)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  return ((item - req[lo].g0) * p.grp + rank) << kTileReqBits | lo;
+}
+__device__ __forceinline__ AttnRow attn_row(const PagedParams& p, const PagedReq* req, int tile, int i) {
+  AttnRow a;
+  a.b = attn_tile_req(p, tile);
+  const int x = (tile >> kTileReqBits) * p.tm + i;
+  a.r = x / p.G;
+  a.g = x - a.r * p.G;
+  a.lim = a.r < req[a.b].rows
+              ? static_cast<int>(min(p.kcap, static_cast<int64_t>(req[a.b].base) + a.r + 1))
+              : 0;
+  if (a.lim == 0) a.r = a.g = 0;
+  return a;
+}
+__device__ __forceinline__ int64_t attn_q_row(const PagedParams&, const PagedReq* req, const AttnRow& r) {
+  return static_cast<int64_t>(req[r.b].start) + r.r;
+}
+
+// Only units that more than one CTA has leave partials, and of those a CTA has at most the end of one
+// (its first piece) and the start of another (its last) in each part of the dealing: four slots a CTA.
+__device__ __forceinline__ int2 attn_unit(const PagedParams& p, const AttnShares& s, int u, int c0, int n) {
+  return make_int2(u < s.u1 ? c0 * p.grp : c0, n);
+}
+__device__ __forceinline__ int attn_slot(const PagedParams&, const AttnShares& s, int u, int cta, int blk0) {
+  return 4 * cta + (u < s.u1 ? 0 : 2) + (blk0 == 0);
+}
+__device__ __forceinline__ int attn_join_slot(const PagedParams& p, const AttnJoinRow& j, int i) {
+  // u0: a grouped tile's (its first CTA, and CTAs `grp` on); u1: a single one's
+  return i < j.u0.y ? 4 * (j.u0.x + i * p.grp) + (i == 0) : 4 * (j.u1.x + i) + 2 + (i == 0);
+}
+__device__ __forceinline__ AttnJoinRow attn_join_row(const PagedParams& p, int64_t row, int qh) {
+  AttnJoinRow j;
+  j.u0 = j.u1 = make_int2(0, 0);
+  j.at0 = j.at1 = 0;
+  j.write = false;
+  const int b = paged_request_of(p.cu_rows, p.B, row);
+  if (b >= p.B || row < p.cu_rows[b]) return j;  // nobody's
+  j.write = true;
+  const int4 rq = __ldcg(p.reqs + b);
+  const int r = static_cast<int>(row) - rq.x;
+  if (r < 0 || r >= rq.y) return j;  // does not run: zero
+  const int head = qh / p.G, x = r * p.G + qh - head * p.G, t = x / p.tm;
+  const int base = static_cast<int>(max(static_cast<int64_t>(0), min(p.kv_len[b], p.kcap)));
+  const int grouped = paged_groups(p, rq.y, base) * p.grp;
+  if (t < grouped) {
+    j.u0 = __ldcg(p.units + (rq.z + t / p.grp) * p.Hkv + head);
+    j.u0.x += t % p.grp;
+    j.at0 = x % p.tm;
+    j.write = j.u0.y > 1;  // else it is written already
+  } else {
+    j.u1 = __ldcg(p.units + (rq.w + t - grouped) * p.Hkv + head);
+    j.at1 = x % p.tm;
+    j.write = j.u1.y > 1;
+  }
+  return j;
+}
+__device__ __forceinline__ int64_t attn_join_rows(const PagedParams& p) { return p.rows; }
+
+cudaError_t paged_simt_launch(const PagedParams& p, spec_dtype dtype, int grid, cudaStream_t stream);
+cudaError_t paged_join_launch(const PagedParams& p, spec_dtype dtype, int sms, cudaStream_t stream);
+bool paged_tc_takes(int head_dim, int page_size);
+spec_status paged_tc_launch(const PagedParams& p, int grid, EncodeTiledFn encode, cudaStream_t stream);
+
+}  // namespace spec

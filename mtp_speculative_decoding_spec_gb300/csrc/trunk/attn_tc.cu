@@ -702,7 +702,7 @@ template <int D>
 spec_status launch_tc(const AttnParams& p, int grid, EncodeTiledFn encode, cudaStream_t stream) {
   using Sh = Shape<D>;
   static SmemAllowance allowed;
-  const int smem = Sh::kFixed + 512 + 24 * kTm + static_cast<int>(attn_plan_bytes(p.items, p.B)) + 1024;
+  const int smem = Sh::kFixed + 512 + 24 * kTm + static_cast<int>(attn_plan_bytes(p)) + 1024;
   if (allow_dynamic_smem(attn_tc_kernel<D>, smem, allowed) != cudaSuccess) return SPEC_ERR_CUDA;
   AttnMaps m;
   // dims inside a 64-dim panel, positions, panels (64 dims on), requests

@@ -117,8 +117,8 @@ __device__ __forceinline__ AttnReq attn_req(const AttnParams& p, int b) {
 __device__ __forceinline__ int attn_own(const AttnParams& p, const AttnReq& r, int rows) {
   return min(r.base + rows, static_cast<int>(p.kcap));
 }
-__host__ __device__ constexpr size_t attn_plan_bytes(int items, int B) {
-  return sizeof(int32_t) * (items + 1) + sizeof(AttnReq) * B;
+__host__ __device__ inline size_t attn_plan_bytes(const AttnParams& p) {
+  return sizeof(int32_t) * (p.items + 1) + sizeof(AttnReq) * p.B;
 }
 
 // cum[0..items] in shared memory: cost of one KV head before each item, in blocks; after it the
@@ -165,6 +165,18 @@ __device__ __forceinline__ AttnReq* attn_plan(const AttnParams& p, int32_t* cum)
   return req;
 }
 
+// What the kernels ask of a call's parameters. The paged cache's overloads stand beside its own type: its
+// tiles and items are known on the device only.
+__device__ __forceinline__ int attn_items(const AttnParams& p, const int32_t*) { return p.items; }
+__device__ __forceinline__ int attn_group_items(const AttnParams& p, const int32_t*) { return p.npi; }
+__device__ __forceinline__ int attn_group_tile(const AttnParams& p, const int32_t*, int item, int rank) {
+  const int tile = item * p.grp + rank;
+  return tile < p.npt ? tile : -1;  // the last group of tiles may not be full
+}
+__device__ __forceinline__ int attn_single_tile(const AttnParams& p, const int32_t*, int item) {
+  return item < p.npi ? item : item - p.npi + p.npt;
+}
+
 // How the costs are dealt out: the groups' part [0, wp), `sp` to each group, and the rest up to w: `s1`
 // to each of the `in` CTAs in groups, `s2` to each of the others, which have that much more room; where
 // the second part's units and slots begin.
@@ -179,7 +191,8 @@ struct AttnShares {
   }
   // With so many groups: the shares, and what the CTA with the most then has. A second unit's start
   // comes on top where the groups' CTAs take some of the rest too.
-  __device__ __forceinline__ int64_t split(const AttnParams& p, int groups, int grid) {
+  template <typename P>
+  __device__ __forceinline__ int64_t split(const P& p, int groups, int grid) {
     in = groups * p.grp;
     sp = (wp + groups - 1) / groups;
     const int64_t rest = w - wp, more = rest - sp * (grid - in);
@@ -188,16 +201,17 @@ struct AttnShares {
     return s1 > 0 ? sp + s1 + p.over[1] : max(sp, s2);
   }
 };
-__device__ __forceinline__ AttnShares attn_shares(const AttnParams& p, const int32_t* cum) {
+template <typename P>
+__device__ __forceinline__ AttnShares attn_shares(const P& p, const int32_t* cum) {
   AttnShares s;
-  const int grid = gridDim.x;
-  s.w = static_cast<int64_t>(cum[p.items]) * p.Hkv;
+  const int grid = gridDim.x, npi = attn_group_items(p, cum);
+  s.w = static_cast<int64_t>(cum[attn_items(p, cum)]) * p.Hkv;
   s.wp = s.sp = 0;
   s.in = 0;
   int groups = 0;
   if (p.grp > 1) {
     // as many groups as the prefix is of the work, so that a CTA has one kind of work, or one more
-    s.wp = static_cast<int64_t>(cum[p.npi]) * p.Hkv;
+    s.wp = static_cast<int64_t>(cum[npi]) * p.Hkv;
     const int64_t all = s.wp * p.grp + s.w - s.wp;
     const int most = grid / p.grp;
     groups = all > 0 ? max(1, static_cast<int>(s.wp * grid / all)) : 1;
@@ -212,37 +226,49 @@ __device__ __forceinline__ AttnShares attn_shares(const AttnParams& p, const int
   } else {
     s.s1 = s.s2 = (s.w + grid - 1) / grid;
   }
-  s.u1 = p.grp > 1 ? p.npi * p.Hkv : 0;
+  s.u1 = p.grp > 1 ? npi * p.Hkv : 0;
   s.base1 = p.grp * (groups + s.u1);
   return s;
 }
 
+// Where a unit's partials begin and how many there are (c0: the group, or of the rest the CTA, that has its
+// first block), and the slot of the partial of this CTA's piece.
+__device__ __forceinline__ int2 attn_unit(const AttnParams& p, const AttnShares& s, int u, int c0, int n) {
+  return make_int2(u < s.u1 ? p.grp * (c0 + u) : s.base1 + c0 + u - s.u1, n);
+}
+__device__ __forceinline__ int attn_slot(const AttnParams& p, const AttnShares& s, int u, int cta, int) {
+  return u < s.u1 ? p.grp * (cta / p.grp + u) + cta % p.grp : s.base1 + cta + u - s.u1;
+}
+
 // Each unit's first slot and number of partials (the slots of a group's tile lie `grp` apart), for the
 // join; by CTA 0 of the kernel that computes them.
-__device__ __forceinline__ void attn_write_units(const AttnParams& p, const int32_t* cum,
-                                                 const AttnShares& s) {
-  for (int u = threadIdx.x; u < p.items * p.Hkv; u += blockDim.x) {
+template <typename P>
+__device__ __forceinline__ void attn_write_units(const P& p, const int32_t* cum, const AttnShares& s) {
+  const int npi = attn_group_items(p, cum);
+  for (int u = threadIdx.x; u < attn_items(p, cum) * p.Hkv; u += blockDim.x) {
     const int item = u / p.Hkv, head = u - item * p.Hkv;
     const int cost = cum[item + 1] - cum[item];
     int2 v = make_int2(0, 0);
     if (cost > 0) {
       const int64_t x = static_cast<int64_t>(cum[item]) * p.Hkv + static_cast<int64_t>(head) * cost;
-      const int64_t first = x + p.over[item >= p.npi], last = x + cost - 1;  // places of its first and last block
+      const int64_t first = x + p.over[item >= npi], last = x + cost - 1;  // places of its first and last block
       if (u < s.u1) {
         const int c0 = static_cast<int>(first / s.sp);
-        v = make_int2(p.grp * (c0 + u), static_cast<int>(last / s.sp) - c0 + 1);
+        v = attn_unit(p, s, u, c0, static_cast<int>(last / s.sp) - c0 + 1);
       } else {
         const int c0 = s.single_cta(first - s.wp);
-        v = make_int2(s.base1 + c0 + u - s.u1, s.single_cta(last - s.wp) - c0 + 1);
+        v = attn_unit(p, s, u, c0, s.single_cta(last - s.wp) - c0 + 1);
       }
     }
     p.units[u] = v;
   }
 }
 
-// A CTA's piece of one unit: its tile of rows (prefix tiles, then own tiles), KV head, blocks and slot.
+// A CTA's piece of one unit: its tile of rows (prefix tiles, then own tiles), KV head, blocks and slot;
+// whether these are all of the unit's blocks.
 struct AttnPiece {
   int tile, head, blk0, blk1, slot;
+  bool whole;
 };
 
 // One piece after another of a CTA's shares. Only the start of a share is looked for; from there on the
@@ -251,10 +277,11 @@ struct AttnWalk {
   int64_t left;        // costs of the share still to walk
   int item, head, at;  // the unit, and where in its costs
   bool group;          // the groups' part is being walked
-  __device__ __forceinline__ void seek(const AttnParams& p, const int32_t* cum, int64_t x, int64_t x1) {
+  template <typename P>
+  __device__ __forceinline__ void seek(const P& p, const int32_t* cum, int64_t x, int64_t x1) {
     left = x1 - x;
     if (left <= 0) return;
-    int lo = 0, hi = p.items;  // cum[lo] Hkv <= x < cum[hi] Hkv
+    int lo = 0, hi = attn_items(p, cum);  // cum[lo] Hkv <= x < cum[hi] Hkv
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
       if (static_cast<int64_t>(cum[mid]) * p.Hkv <= x)
@@ -267,7 +294,8 @@ struct AttnWalk {
     head = static_cast<int>(rel / (cum[lo + 1] - cum[lo]));
     at = static_cast<int>(rel - static_cast<int64_t>(head) * (cum[lo + 1] - cum[lo]));
   }
-  __device__ __forceinline__ void start(const AttnParams& p, const int32_t* cum, const AttnShares& s) {
+  template <typename P>
+  __device__ __forceinline__ void start(const P& p, const int32_t* cum, const AttnShares& s) {
     group = static_cast<int>(blockIdx.x) < s.in;
     if (group) {
       const int64_t x = s.sp * (blockIdx.x / p.grp);
@@ -276,14 +304,15 @@ struct AttnWalk {
       single(p, cum, s);
     }
   }
-  __device__ __forceinline__ void single(const AttnParams& p, const int32_t* cum, const AttnShares& s) {
+  template <typename P>
+  __device__ __forceinline__ void single(const P& p, const int32_t* cum, const AttnShares& s) {
     group = false;
     const int cta = blockIdx.x;
     const int64_t x = s.wp + s.single_at(cta);
     seek(p, cum, x, min(s.w, s.wp + s.single_at(cta + 1)));
   }
-  __device__ __forceinline__ bool next(const AttnParams& p, const int32_t* cum, const AttnShares& s,
-                                       AttnPiece& a) {
+  template <typename P>
+  __device__ __forceinline__ bool next(const P& p, const int32_t* cum, const AttnShares& s, AttnPiece& a) {
     for (;;) {
       if (left <= 0) {
         if (!group) return false;
@@ -302,21 +331,20 @@ struct AttnWalk {
       const int v0 = at, v1 = static_cast<int>(min(static_cast<int64_t>(cost), v0 + left));
       at = v1;
       left -= v1 - v0;
-      const int over = p.over[item >= p.npi];
+      const int over = p.over[item >= attn_group_items(p, cum)];
       a.blk0 = max(0, v0 - over);
       a.blk1 = max(0, v1 - over);
       if (a.blk0 == a.blk1) continue;
+      a.whole = a.blk0 == 0 && a.blk1 == cost - over;
       a.head = head;
       const int u = item * p.Hkv + head;
       if (group) {
-        const int at_group = static_cast<int>(blockIdx.x) / p.grp, rank = blockIdx.x - at_group * p.grp;
-        a.tile = item * p.grp + rank;
-        if (a.tile >= p.npt) continue;  // the last group of tiles is not full
-        a.slot = p.grp * (at_group + u) + rank;
+        a.tile = attn_group_tile(p, cum, item, static_cast<int>(blockIdx.x) % p.grp);
+        if (a.tile < 0) continue;
       } else {
-        a.tile = item < p.npi ? item : item - p.npi + p.npt;
-        a.slot = s.base1 + static_cast<int>(blockIdx.x) + u - s.u1;
+        a.tile = attn_single_tile(p, cum, item);
       }
+      a.slot = attn_slot(p, s, u, static_cast<int>(blockIdx.x), a.blk0);
       return true;
     }
   }
@@ -349,6 +377,48 @@ __device__ __forceinline__ AttnRow attn_row(const AttnParams& p, const AttnReq* 
     if (a.r < req[a.b].rows) a.lim = attn_own(p, req[a.b], a.r + 1);
   }
   return a;
+}
+
+// The row of q, out and lse, and the request of a tile of own positions.
+__device__ __forceinline__ int64_t attn_q_row(const AttnParams& p, const AttnReq*, const AttnRow& r) {
+  return static_cast<int64_t>(r.b) * p.R + r.r;
+}
+__device__ __forceinline__ int attn_tile_req(const AttnParams& p, int tile) { return (tile - p.npt) / p.nown; }
+// A paged cache's call: K and V by pages, of which some may not be there; a row whose positions one CTA has
+// all of is written without the join.
+template <typename P>
+constexpr bool kPaged = false;
+
+// One output row of the join: its unit over the prefix and its own (first slot, number of partials), its
+// place in their tiles; whether the row is written, and the slot of a partial.
+struct AttnJoinRow {
+  int2 u0, u1;
+  int at0, at1;
+  bool write;
+};
+__device__ __forceinline__ int attn_join_slot(const AttnParams& p, const AttnJoinRow& j, int i) {
+  return i < j.u0.y ? j.u0.x + i * p.grp : j.u1.x + i - j.u0.y;
+}
+__device__ __forceinline__ AttnJoinRow attn_join_row(const AttnParams& p, int64_t row, int qh) {
+  AttnJoinRow j;
+  const int head = qh / p.G, g = qh - head * p.G;
+  const int b = static_cast<int>(row / p.R), r = static_cast<int>(row) - b * p.R;
+  const int s = (b * p.R + r) * p.G + g, x = r * p.G + g;
+  const AttnReq rq = attn_req(p, b);
+  j.u0 = make_int2(0, 0);
+  const int t0 = s / p.tm;
+  if (p.npt > 0) j.u0 = __ldcg(p.units + t0 / p.grp * p.Hkv + head);
+  j.u1 = __ldcg(p.units + (p.npi + b * p.nown + x / p.tm) * p.Hkv + head);
+  j.u0.x += t0 % p.grp;
+  if (rq.prefix == 0) j.u0.y = 0;
+  if (r >= rq.rows) j.u0.y = j.u1.y = 0;
+  j.at0 = s % p.tm;
+  j.at1 = x % p.tm;
+  j.write = true;
+  return j;
+}
+__device__ __forceinline__ int64_t attn_join_rows(const AttnParams& p) {
+  return static_cast<int64_t>(p.B) * p.R;
 }
 
 cudaError_t attn_simt_launch(const AttnParams& p, spec_dtype dtype, int grid, cudaStream_t stream);
