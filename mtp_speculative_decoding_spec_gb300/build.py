@@ -20,7 +20,7 @@ LIB = os.path.join(HERE, "libspec.so")
 SOURCES = ["gemv.cu", "gemv_tc.cu", "gemv_q4.cu", "gemm_tc.cu", "accept.cu", "commit.cu", "abi.cu",
            "trunk/delta.cu", "trunk/delta_chunk.cu",
            "trunk/attn.cu", "trunk/attn_tc.cu", "trunk/abi.cu",
-           "paged/append.cu", "paged/commit.cu", "paged/attn.cu", "paged/abi.cu"]
+           "paged/append.cu", "paged/commit.cu", "paged/attn.cu", "paged/attn_tc.cu", "paged/abi.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-Xptxas", "-v"]

@@ -74,7 +74,8 @@ spec_status plan_check(int32_t B, int64_t rows, const spec_paged_cache* c, const
     return SPEC_ERR_INVALID;
   const int64_t G = d->q_heads / c->kv_heads;
   if (G > 64) return SPEC_ERR_UNSUPPORTED;
-  w.tc = 0;
+  w.tc = c->dtype == SPEC_BF16 && paged_tc_takes(c->head_dim, c->page_size) &&
+         c->page_stride < (int64_t(1) << 40);  // a tensor map's strides
   w.tm = w.tc ? attn_tc_tm() : attn_simt_tm();
   w.bn = w.tc ? attn_tc_bn(c->head_dim) : attn_simt_bn();
   const int64_t tiles = rows * G / w.tm + B;  // each request's last tile may not be full
@@ -204,7 +205,11 @@ spec_status spec_paged_attention(int32_t B, const int32_t* cu_rows, int64_t rows
   p.tm = w.tm;
   p.bn = w.bn;
   p.items = w.tiles;
-  p.grp = 1;
+  p.grp = w.tc ? kPagedGroup : 1;
+  p.group_min = kPagedGroupMin;
+  for (p.page_shift = 0; w.tc && p.page_shift < 31 && (1 << p.page_shift) < c->page_size; ++p.page_shift) {
+  }
+  if (c->page_size >= w.bn) p.page_shift = 31;
   p.over[0] = w.tc ? kAttnOverPre : kAttnSimtOver;
   p.over[1] = w.tc ? kAttnOver : kAttnSimtOver;
   p.q = d->q;
@@ -224,7 +229,14 @@ spec_status spec_paged_attention(int32_t B, const int32_t* cu_rows, int64_t rows
   p.ml = reinterpret_cast<float2*>(ws + w.ml);
   p.o = reinterpret_cast<float*>(ws + w.o);
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-  if (paged_simt_launch(p, c->dtype, w.grid, cs) != cudaSuccess) return SPEC_ERR_CUDA;
+  if (w.tc) {
+    EncodeTiledFn encode = encode_tiled();
+    if (!encode) return SPEC_ERR_CUDA;
+    s = paged_tc_launch(p, w.grid, encode, cs);
+    if (s != SPEC_OK) return s;
+  } else if (paged_simt_launch(p, c->dtype, w.grid, cs) != cudaSuccess) {
+    return SPEC_ERR_CUDA;
+  }
   return paged_join_launch(p, c->dtype, w.grid, cs) == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }
 

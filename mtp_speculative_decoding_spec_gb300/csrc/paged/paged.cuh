@@ -53,6 +53,10 @@ __device__ __forceinline__ PagedRows paged_rows(const int32_t* cu, const int32_t
   return r;
 }
 
+// Tiles of a request that walk the same positions side by side (152 SMs are 19 eights), and from how many
+// positions on.
+constexpr int kPagedGroup = 8, kPagedGroupMin = 8192;
+
 struct AppendParams {
   PagedLayer c;
   int B, Hq, Hkv, D;
@@ -102,6 +106,7 @@ struct PagedParams : AttnParams {
   const int32_t* cu_rows;
   int64_t rows;
   int group_min;          // positions from which a request's tiles are grouped
+  int page_shift;         // tensor cores: positions (log2) of a block's part on one page, 31 where that is all
   int4* reqs;             // for the join: first row, rows, g0, s0
 };
 template <>
@@ -303,7 +308,12 @@ __device__ __forceinline__ int64_t attn_join_rows(const PagedParams& p) { return
 
 cudaError_t paged_simt_launch(const PagedParams& p, spec_dtype dtype, int grid, cudaStream_t stream);
 cudaError_t paged_join_launch(const PagedParams& p, spec_dtype dtype, int sms, cudaStream_t stream);
-bool paged_tc_takes(int head_dim, int page_size);
+// Page sizes of the tensor-core kernel: a block of its positions is whole pages or lies on one, and a page has
+// at least the eight rows of the operands' swizzle.
+inline bool paged_tc_takes(int head_dim, int page_size) {
+  return attn_tc_takes(head_dim) && (page_size == 8 || page_size == 16 || page_size == 32 || page_size == 64 ||
+                                     page_size % 128 == 0);
+}
 spec_status paged_tc_launch(const PagedParams& p, int grid, EncodeTiledFn encode, cudaStream_t stream);
 
 }  // namespace spec

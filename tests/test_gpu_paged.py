@@ -325,6 +325,10 @@ ATTN = [
          kv_len=[i % 37 for i in range(300)]),
     dict(lens=[1] * 512, D=256, H=1, Hq=1, dtype="bf16", page=64, kv_len=[i % 90 for i in range(512)]),
     dict(lens=[1, 2], D=256, H=4, Hq=16, dtype="bf16", page=64, kv_len=[9000, 5000]),
+    # as many tiles over as many positions as have groups of CTAs walk them, some left over
+    dict(lens=[300, 3, 0, 270], D=64, H=1, Hq=4, dtype="bf16", page=64, kv_len=[8100, 50, 9000, 9001]),
+    dict(lens=[3, 620, 5], D=256, H=1, Hq=2, dtype="bf16", page=16, kv_len=[700, 7900, 9000]),
+    dict(lens=[130], D=128, H=2, Hq=16, dtype="bf16", page=128, kv_len=[8192]),
 ]
 
 

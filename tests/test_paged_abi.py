@@ -165,6 +165,7 @@ def test_call_refusals(spec):
 
 @pytest.mark.parametrize("dtype,D,rows,over", [
     # 8 query heads on 2: G = 4; tiles of 128 rows and of 16, two requests
+    ("bf16", 128, (4096 - 2) * 32, False), ("bf16", 128, (4096 - 1) * 32, True),
     ("bf16", 72, (12288 - 2) * 4, False), ("bf16", 72, (12288 - 1) * 4, True),
     ("f32", 64, (12288 - 2) * 4, False), ("f32", 64, (12288 - 1) * 4, True),
 ])
@@ -181,7 +182,7 @@ def test_register_budget_and_no_spills(spec):
     each, and no kernel spills."""
     logs = glob.glob(os.path.join(ROOT, "mtp_speculative_decoding_spec_gb300", "_build", "paged", "*.ptxas.log"))
     threads = {"append_kernel": 128, "paged_commit_kernel": 256, "attn_simt_kernel": 256,
-               "attn_join_kernel": 256}
+               "attn_join_kernel": 256, "attn_tc_kernel": 384}
     seen = set()
     for path in logs:
         name = None
