@@ -153,9 +153,8 @@ spec_status spec_paged_append(int32_t B, const int32_t* cu_rows, int64_t rows,
   p.vs = d->v_stride;
   p.qos = d->q_out_stride;
   const auto whole = [e](const void* x, int64_t stride) { return aligned16(x) && stride * e % 16 == 0; };
-  p.vec_in = (p.nq == 0 || whole(d->q, d->q_stride)) &&
-             (p.nk == 0 || (whole(d->k, d->k_stride) && whole(d->v, d->v_stride)));
-  p.vec_out = whole(d->q_out, d->q_out_stride);
+  p.whole = (p.nq == 0 || (whole(d->q, d->q_stride) && whole(d->q_out, d->q_out_stride))) &&
+            (p.nk == 0 || (whole(d->k, d->k_stride) && whole(d->v, d->v_stride)));
   p.q_norm = d->q_norm;
   p.k_norm = d->k_norm;
   p.eps = d->norm_eps;

@@ -10,9 +10,11 @@
 // 2^-64 * pos of error, by integer multiplication. Its upper 32 bits, as a signed number of half turns, go
 // to sincospif.
 //
-// A lane holds eight dims of a head, so a head is D / 8 lanes and a warp has 32 / (D / 8) heads at once. The
-// dims of a lane are the same in all heads, so a row's cos and sin are formed once and stay in registers
-// while the warp goes over the row's heads, four loads in flight.
+// A lane holds eight dims of a head, so a head is D / 8 lanes and a warp has 32 / (D / 8) heads at once. A
+// row's angles are formed once, a lane each, and handed round through shared memory. What the arithmetic has
+// to do then is kept short, since it and not the memory would be the bound: with the weights taken into cos
+// and sin, an output is (x / rms) wc + (x' / rms) ws with x' the pair's other end, whose bits come from the
+// lane that has it before anything is done to them (two bf16 a shuffle), in packed fp32.
 #include <cuda_bf16.h>
 
 #include "paged.cuh"
@@ -20,16 +22,28 @@
 namespace spec {
 namespace {
 
-constexpr int kThreads = 128;
-constexpr int kBatch = 4;   // heads of a lane in flight
+constexpr int kThreads = 128, kWarps = kThreads / 32;
+constexpr int kAppendWarps = 16;        // of an SM
+constexpr int64_t kAppendRows = 2;      // rows of a warp, at most
 
 enum : int { ROT_NONE = 0, ROT_SIDE = 1, ROT_HALF = 2, ROT_HALF_ODD = 3 };
+
+template <typename T, int ROT, int STEP>
+constexpr int kMinBlocks = ROT == ROT_HALF_ODD ? 1 : sizeof(T) == 2 && STEP ? 5 : 4;
 
 template <typename T>
 struct Eight;  // eight elements as they lie in memory
 template <>
 struct Eight<__nv_bfloat16> {
+  static constexpr int kBatch = 8;  // heads of a lane in flight
   uint4 w;
+  __device__ __forceinline__ Eight from(int lane, int width, bool any) const {  // another lane's, or zeros
+    Eight o;
+    o.w.x = __shfl_sync(0xffffffffu, w.x, lane, width), o.w.y = __shfl_sync(0xffffffffu, w.y, lane, width);
+    o.w.z = __shfl_sync(0xffffffffu, w.z, lane, width), o.w.w = __shfl_sync(0xffffffffu, w.w, lane, width);
+    if (!any) o.w = make_uint4(0u, 0u, 0u, 0u);
+    return o;
+  }
   __device__ __forceinline__ void get(float* x) const {
     const uint32_t a[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
@@ -71,7 +85,20 @@ struct Eight<__nv_bfloat16> {
 };
 template <>
 struct Eight<float> {
+  static constexpr int kBatch = 4;
   float4 a, b;
+  __device__ __forceinline__ Eight from(int lane, int width, bool any) const {
+    float x[8];
+    get(x);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      x[j] = __shfl_sync(0xffffffffu, x[j], lane, width);
+      if (!any) x[j] = 0.f;
+    }
+    Eight o;
+    o.set(x);
+    return o;
+  }
   __device__ __forceinline__ void get(float* x) const {
     x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
     x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
@@ -118,181 +145,244 @@ __device__ __forceinline__ uint64_t turns_of(float f) {
   return (u >> 31) ? 0 - t : t;
 }
 
-template <typename T, int ROT>
-__global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ AppendParams p) {
-  pdl_wait();
-  const int lane = threadIdx.x & 31;
-  const int64_t warp = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
-  const int tph = p.tph, at = lane & (tph - 1), sub = lane / tph, heads = 32 / tph;
-  const int D = p.D, e0 = 8 * at, half = p.rot / 2;
-  const bool holds = e0 < D;
-  // this lane's weights and frequencies; element j is turned where bit j of `turns` is set
-  float wq[8], wk[8];
+__device__ __forceinline__ unsigned long long pair(float a, float b) {
+  return pack2(__float_as_uint(a), __float_as_uint(b));
+}
+__device__ __forceinline__ unsigned long long mul2(unsigned long long a, unsigned long long b) {
+  unsigned long long r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// Eight consecutive floats of shared memory (32-byte aligned).
+__device__ __forceinline__ void lds8(const float* p, float* x) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    wq[j] = p.q_norm && holds ? p.q_norm[e0 + j] : 1.f;
-    wk[j] = p.k_norm && holds ? p.k_norm[e0 + j] : 1.f;
+  for (int j = 0; j < 8; j += 4) {
+    const float4 v = *reinterpret_cast<const float4*>(p + j);
+    x[j] = v.x, x[j + 1] = v.y, x[j + 2] = v.z, x[j + 3] = v.w;
   }
-  constexpr int NF = ROT == ROT_NONE ? 1 : ROT == ROT_SIDE ? 4 : 8;
-  uint64_t F[NF];
-  uint32_t turns = 0, low = 0;  // low: the element is its pair's first
-  if constexpr (ROT == ROT_SIDE) {
+}
+
+// WHOLE: rows of q, k, v and q_out are whole 16-byte vectors. STEP: elements that a warp's heads take, 0 where
+// D is no power of two and the host's number counts.
+template <typename T, int ROT, bool WHOLE, int STEP>
+__global__ void __launch_bounds__(kThreads, kMinBlocks<T, ROT, STEP>) append_kernel(const __grid_constant__ AppendParams p) {
+  constexpr int kBatch = Eight<T>::kBatch;
+  __shared__ __align__(32) float weights[2][256];       // of queries and keys
+  __shared__ __align__(32) float2 trig[kWarps][128];    // cos and sin of a warp's row
+  pdl_wait();
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  const int tph = p.tph, at = lane & (tph - 1), sub = lane / tph, heads = 32 / tph;
+  const int D = p.D, e0 = 8 * at, half = p.rot / 2, step = STEP ? STEP : heads * D;
+  const bool holds = e0 < D;
+  for (int d = threadIdx.x; d < D; d += kThreads) {
+    weights[0][d] = p.q_norm ? p.q_norm[d] : 1.f;
+    weights[1][d] = p.k_norm ? p.k_norm[d] : 1.f;
+  }
+  uint64_t F[4];  // of angles lane, lane + 32, ...
+  if constexpr (ROT != ROT_NONE) {
+#pragma unroll
+    for (int n = 0; n < 4; ++n) F[n] = lane + 32 * n < half ? turns_of(p.inv_freq[lane + 32 * n]) : 0;
+  }
+  __syncthreads();
+  const float inv_d = 1.f / static_cast<float>(D);
+  // with pairs half of rot_dim apart: the lane that has the other ends, whether there are any
+  const bool low = e0 < half, turned = ROT == ROT_HALF && e0 < p.rot;
+  const int other = low ? at + half / 8 : at - half / 8;
+  const auto angle = [&](int e) { return trig[wid][ROT == ROT_SIDE ? e >> 1 : e < half ? e : e - half]; };
+  // this block's turns of a row: queries' cq, then keys' ck, then values' ck
+  const int i0 = blockIdx.y * p.per_task, i1 = min(p.iters, i0 + p.per_task);
+  const int q1 = min(i1, p.cq), k0 = max(0, i0 - p.cq), k1 = min(i1 - p.cq, p.ck);
+  const int v0 = max(0, i0 - p.cq - p.ck), v1 = i1 - p.cq - p.ck;
+
+  // A few of a row's heads from `src`, at the lane's dims; turn n is there where a + n < a1 and its head < nh.
+  Eight<T> x[kBatch];
+  auto fetch = [&](const T* src, int a, int a1, int nh) {
+#pragma unroll
+    for (int n = 0; n < kBatch; ++n)
+      if (a + n < a1 && holds && (a + n) * heads + sub < nh) x[n].load(src + n * step, WHOLE);
+  };
+  auto write = [&](T* dst, int a, int a1, int nh, bool whole) {
+#pragma unroll
+    for (int n = 0; n < kBatch; ++n)
+      if (a + n < a1 && holds && (a + n) * heads + sub < nh) x[n].store(dst + n * step, whole);
+  };
+  unsigned long long wc[4], ws[4];
+  auto turn_weights = [&](const float* weight) {  // out_j = y_j wc_j + y'_j ws_j, y and y' without weights
+    float w[8], v[8], cs[16];
+    lds8(weight + e0, w);
+    if constexpr (ROT == ROT_SIDE || ROT == ROT_HALF) {
+      const bool on = e0 < p.rot;
+      const float* from = reinterpret_cast<const float*>(trig[wid] + (!on ? 0 : ROT == ROT_SIDE ? e0 / 2 : low ? e0 : e0 - half));
+      lds8(from, cs);
+      if (ROT == ROT_HALF) lds8(from + 8, cs + 8);
+      lds8(ROT == ROT_SIDE ? weight + e0 : weight + (!on ? 0 : low ? e0 + half : e0 - half), v);
+      float c[8], s[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const bool there = ROT == ROT_SIDE ? e0 + j < p.rot : on;
+        c[j] = there ? cs[ROT == ROT_SIDE ? j & ~1 : 2 * j] : 1.f;
+        s[j] = there ? cs[ROT == ROT_SIDE ? j | 1 : 2 * j + 1] : 0.f;
+        if (ROT == ROT_SIDE ? (j & 1) == 0 : low) s[j] = -s[j];
+      }
+#pragma unroll
+      for (int j = 0; j < 8; j += 2) {
+        wc[j / 2] = pair(w[j] * c[j], w[j + 1] * c[j + 1]);
+        ws[j / 2] = ROT == ROT_SIDE ? pair(v[j + 1] * s[j], v[j] * s[j + 1]) : pair(v[j] * s[j], v[j + 1] * s[j + 1]);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; j += 2) wc[j / 2] = pair(w[j], w[j + 1]);
+    }
+  };
+  auto work = [&](Eight<T>& e, bool live, bool norm) {  // one head, by the whole warp
+    float y[8];
+    e.get(y);
+    unsigned long long y2[4], o2[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) y2[j] = live ? pair(y[2 * j], y[2 * j + 1]) : 0ull;
+    if (norm) {
+      unsigned long long sq = mul2(y2[0], y2[0]);
+#pragma unroll
+      for (int j = 1; j < 4; ++j) ffma2_acc(sq, y2[j], y2[j]);
+      float sum = sum2(sq);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1)
+        if (o < tph) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      const float inv = rsqrtf(fmaf(sum, inv_d, p.eps));
+      const unsigned long long inv2 = pair(inv, inv);
+      if constexpr (ROT == ROT_HALF) {
+        float z[8];
+        e.from(other, tph, turned).get(z);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o2[j] = mul2(mul2(pair(z[2 * j], z[2 * j + 1]), inv2), ws[j]);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) y2[j] = mul2(y2[j], inv2);
+    } else if constexpr (ROT == ROT_HALF) {
+      float z[8];
+      e.from(other, tph, turned).get(z);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) o2[j] = mul2(pair(z[2 * j], z[2 * j + 1]), ws[j]);
+    }
+    if constexpr (ROT == ROT_SIDE) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const unsigned long long swapped = y2[j] << 32 | y2[j] >> 32;
+        o2[j] = mul2(e0 + 2 * j < p.rot ? swapped : 0ull, ws[j]);
+        ffma2_acc(o2[j], y2[j], wc[j]);
+      }
+    } else if constexpr (ROT == ROT_HALF) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) ffma2_acc(o2[j], y2[j], wc[j]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) o2[j] = mul2(y2[j], wc[j]);
+    }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      F[j] = 0;
-      if (e0 + 2 * j < p.rot) {
-        F[j] = turns_of(p.inv_freq[(e0 >> 1) + j]);
-        turns |= 3u << (2 * j);
-      }
+      y[2 * j] = __uint_as_float(static_cast<uint32_t>(o2[j]));
+      y[2 * j + 1] = __uint_as_float(static_cast<uint32_t>(o2[j] >> 32));
     }
-  } else if constexpr (ROT != ROT_NONE) {
+    if constexpr (ROT == ROT_HALF_ODD) {
+      // half of rot_dim no multiple of eight: element j's other end is element (j +- half) & 7 of the lane that
+      // far on or back
+      float up[8], down[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      F[j] = 0;
-      if (e0 + j < p.rot) {
-        const bool first = e0 + j < half;
-        F[j] = turns_of(p.inv_freq[e0 + j - (first ? 0 : half)]);
-        turns |= 1u << j;
-        low |= static_cast<uint32_t>(first) << j;
+      for (int j = 0; j < 8; ++j) up[j] = down[j] = y[j];
+#pragma unroll
+      for (int o = 1; o < 8; o <<= 1)
+        if (half & o) {
+          float a[8], b[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) a[j] = up[(j + o) & 7], b[j] = down[(j - o) & 7];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) up[j] = a[j], down[j] = b[j];
+        }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float a = __shfl_sync(0xffffffffu, up[j], at + ((j + half) >> 3), tph);
+        const float b = __shfl_sync(0xffffffffu, down[j], at + ((j - half) >> 3), tph);
+        if (e0 + j < p.rot) {
+          const float2 cs = angle(e0 + j);
+          y[j] = fmaf(e0 + j < half ? -a : b, cs.y, y[j] * cs.x);
+        }
       }
     }
-  }
-  const int nheads = p.nq + 2 * p.nk;
-  const float inv_d = 1.f / static_cast<float>(D);
-  const T* qb = static_cast<const T*>(p.q);
-  const T* kb = static_cast<const T*>(p.k);
-  const T* vb = static_cast<const T*>(p.v);
+    e.set(y);
+  };
 
-  int64_t last_row = -1;
-  bool runs = false;
-  int64_t page_at = -1;  // where the row's keys and values go, in bytes from the layer's first page
-  float c[NF], s[NF];
-  const int64_t t1 = min(p.tasks, (warp + 1) * p.tasks_warp);
-  for (int64_t t = warp * p.tasks_warp; t < t1; ++t) {
-    const int64_t row = t / p.tasks_row;
-    const int i0 = static_cast<int>(t - row * p.tasks_row) * p.per_task, i1 = min(p.iters, i0 + p.per_task);
-    Eight<T> x[kBatch];
-    auto fetch = [&](int i) {
+  const int64_t warp = static_cast<int64_t>(blockIdx.x) * kWarps + wid;
+  const int64_t row1 = min(p.rows, (warp + 1) * p.rows_warp);
+  for (int64_t row = warp * p.rows_warp; row < row1; ++row) {
+    const T* const q = static_cast<const T*>(p.q) + row * p.qs + sub * D + e0;
+    const T* const k = static_cast<const T*>(p.k) + row * p.ks + sub * D + e0;
+    const T* const v = static_cast<const T*>(p.v) + row * p.vs + sub * D + e0;
+    if (i0 < q1)
+      fetch(q + i0 * step, i0, q1, p.nq);
+    else if (k0 < k1)
+      fetch(k + k0 * step, k0, k1, p.nk);
+    else
+      fetch(v + v0 * step, v0, v1, p.nk);
+    const int b = paged_request_of(p.cu_rows, p.B, row);
+    if (b >= p.B) break;  // nobody's, as all after it
+    const PagedRows pr = paged_rows(p.cu_rows, p.n_rows, p.rows, b);
+    const int64_t r = row - pr.start;
+    if (r < 0 || r >= pr.runs) continue;
+    const int64_t P = max(static_cast<int64_t>(0), p.c.kv_len[b]), pos = P + r;
+    // where the row's keys and values go, in bytes from the layer's first page
+    const int64_t page_at = p.nk > 0 && pos < static_cast<int64_t>(p.c.max_pages) * p.c.page_size
+                                ? paged_offset(p.c, b, static_cast<int>(pos))
+                                : -1;
+    if constexpr (ROT != ROT_NONE) {
+      const uint64_t turn = static_cast<uint64_t>(p.pos ? p.pos[b] + r : pos);
+      __syncwarp();  // the row before is done with the table
 #pragma unroll
-      for (int n = 0; n < kBatch; ++n) {
-        const int h = (i + n) * heads + sub;
-        if (i + n >= i1 || h >= nheads || !holds) continue;
-        const T* src = h < p.nq ? qb + row * p.qs + static_cast<int64_t>(h) * D
-                       : h < p.nq + p.nk
-                           ? kb + row * p.ks + static_cast<int64_t>(h - p.nq) * D
-                           : vb + row * p.vs + static_cast<int64_t>(h - p.nq - p.nk) * D;
-        x[n].load(src + e0, p.vec_in);
-      }
-    };
-    fetch(i0);
-    if (row != last_row) {
-      last_row = row;
-      const int b = paged_request_of(p.cu_rows, p.B, row);
-      runs = false;
-      if (b < p.B) {
-        const PagedRows pr = paged_rows(p.cu_rows, p.n_rows, p.rows, b);
-        const int64_t r = row - pr.start;
-        runs = r >= 0 && r < pr.runs;
-        if (runs) {
-          const int64_t P = max(static_cast<int64_t>(0), p.c.kv_len[b]), pos = P + r;
-          const int64_t turn = p.pos ? p.pos[b] + r : pos;
-          page_at = p.nk > 0 && pos < static_cast<int64_t>(p.c.max_pages) * p.c.page_size
-                        ? paged_offset(p.c, b, static_cast<int>(pos))
-                        : -1;
-          if constexpr (ROT != ROT_NONE) {
-#pragma unroll
-            for (int j = 0; j < NF; ++j) {
-              const uint32_t part = static_cast<uint32_t>((F[j] * static_cast<uint64_t>(turn)) >> 32);
-              float sn, cs;
-              sincospif(static_cast<float>(static_cast<int32_t>(part)) * 0x1p-31f, &sn, &cs);
-              c[j] = cs * p.rot_scale;
-              s[j] = sn * p.rot_scale;
-              if (ROT != ROT_SIDE && (low >> j & 1)) s[j] = -s[j];
-            }
-          }
+      for (int n = 0; n < 4; ++n)
+        if (32 * n < half) {
+          const uint32_t part = static_cast<uint32_t>((F[n] * turn) >> 32);
+          float sn, cs;
+          sincospif(static_cast<float>(static_cast<int32_t>(part)) * 0x1p-31f, &sn, &cs);
+          trig[wid][lane + 32 * n] = make_float2(cs * p.rot_scale, sn * p.rot_scale);
         }
+      __syncwarp();
+    }
+    T* const out = static_cast<T*>(p.q_out) + row * p.qos + sub * D + e0;
+    if (i0 < q1) {
+      turn_weights(weights[0]);
+      for (int a = i0; a < q1; a += kBatch) {
+        if (a > i0) fetch(q + a * step, a, q1, p.nq);
+#pragma unroll
+        for (int n = 0; n < kBatch; ++n) {
+          if (a + n >= q1) break;
+          work(x[n], holds && (a + n) * heads + sub < p.nq, p.q_norm != nullptr);
+        }
+        write(out + a * step, a, q1, p.nq, WHOLE);
       }
     }
-    if (!runs) continue;  // the whole warp
-    for (int i = i0; i < i1; i += kBatch) {
-      if (i > i0) fetch(i);
+    T* const kp = reinterpret_cast<T*>(p.c.k + page_at) + sub * D + e0;
+    T* const vp = reinterpret_cast<T*>(p.c.v + page_at) + sub * D + e0;
+    if (k0 < k1) {
+      turn_weights(weights[1]);
+      for (int a = k0; a < k1; a += kBatch) {
+        if (a > k0 || i0 < q1) fetch(k + a * step, a, k1, p.nk);
 #pragma unroll
-      for (int n = 0; n < kBatch; ++n) {
-        if (i + n >= i1) break;  // the whole warp
-        const int h = (i + n) * heads + sub;
-        const bool is_q = h < p.nq, is_k = !is_q && h < p.nq + p.nk, live = h < nheads && holds;
-        if (__any_sync(0xffffffffu, is_q || is_k)) {
-          float y[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) y[j] = 0.f;
-          if (live) x[n].get(y);
-          const bool norm = is_q ? p.q_norm != nullptr : p.k_norm != nullptr;
-          if (__any_sync(0xffffffffu, norm)) {
-            float sum = 0.f;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) sum = fmaf(y[j], y[j], sum);
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1)
-              if (o < tph) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            const float inv = __frsqrt_rn(fmaf(sum, inv_d, p.eps));
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-              if (norm) y[j] *= inv * (is_q ? wq[j] : wk[j]);
-          }
-          if constexpr (ROT == ROT_SIDE) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float a = y[2 * j], b = y[2 * j + 1];
-              if (turns >> (2 * j) & 1) {
-                y[2 * j] = a * c[j] - b * s[j];
-                y[2 * j + 1] = b * c[j] + a * s[j];
-              }
-            }
-          } else if constexpr (ROT == ROT_HALF) {  // half a multiple of 8: eight pairs' other ends in one lane
-            const int from = e0 < half ? at + half / 8 : at - half / 8;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const float o = __shfl_sync(0xffffffffu, y[j], from, tph);
-              if (turns >> j & 1) y[j] = fmaf(o, s[j], y[j] * c[j]);
-            }
-          } else if constexpr (ROT == ROT_HALF_ODD) {
-            // element j's other end is element (j +- half) & 7 of the lane that far on or back
-            float up[8], down[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) up[j] = down[j] = y[j];
-#pragma unroll
-            for (int o = 1; o < 8; o <<= 1)
-              if (half & o) {
-                float a[8], b[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) a[j] = up[(j + o) & 7], b[j] = down[(j - o) & 7];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) up[j] = a[j], down[j] = b[j];
-              }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const float a = __shfl_sync(0xffffffffu, up[j], at + ((j + half) >> 3), tph);
-              const float b = __shfl_sync(0xffffffffu, down[j], at + ((j - half) >> 3), tph);
-              if (turns >> j & 1) y[j] = fmaf(low >> j & 1 ? a : b, s[j], y[j] * c[j]);
-            }
-          }
-          if (is_q || is_k) x[n].set(y);
+        for (int n = 0; n < kBatch; ++n) {
+          if (a + n >= k1) break;
+          work(x[n], holds && (a + n) * heads + sub < p.nk, p.k_norm != nullptr);
         }
-        if (!live) continue;
-        if (is_q) {
-          x[n].store(static_cast<T*>(p.q_out) + row * p.qos + static_cast<int64_t>(h) * D + e0, p.vec_out);
-        } else if (page_at >= 0) {
-          uint8_t* pages = is_k ? p.c.k : p.c.v;
-          const int kh = h - p.nq - (is_k ? 0 : p.nk);
-          x[n].store(reinterpret_cast<T*>(pages + page_at) + static_cast<int64_t>(kh) * D + e0, true);
-        }
+        if (page_at >= 0) write(kp + a * step, a, k1, p.nk, true);
       }
+    }
+    for (int a = v0; a < v1; a += kBatch) {
+      if (a > v0 || i0 < q1 || k0 < k1) fetch(v + a * step, a, v1, p.nk);
+      if (page_at >= 0) write(vp + a * step, a, v1, p.nk, true);
     }
   }
 
   if (p.status) {  // a warp to a request: the pages of its rows
-    const int64_t warps = static_cast<int64_t>(gridDim.x) * (kThreads / 32);
-    for (int64_t b = warp; b < p.B; b += warps) {
+    const int64_t warps = static_cast<int64_t>(gridDim.x) * kWarps;
+    for (int64_t b = blockIdx.y == 0 ? warp : p.B; b < p.B; b += warps) {
       const int n = paged_rows(p.cu_rows, p.n_rows, p.rows, static_cast<int>(b)).runs;
       const int64_t P = max(static_cast<int64_t>(0), p.c.kv_len[b]);
       const int64_t cap = static_cast<int64_t>(p.c.max_pages) * p.c.page_size;
@@ -310,13 +400,19 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
   }
 }
 
+template <typename T, int ROT>
+cudaError_t launch_rot(const AppendParams& p, dim3 grid, cudaStream_t stream) {
+  const bool pow2 = p.tph * 8 == p.D;  // 32 lanes of eight dims are whole heads then
+  if (!p.whole) return launch_pdl(append_kernel<T, ROT, false, 0>, grid, dim3(kThreads), 0, stream, p);
+  return pow2 ? launch_pdl(append_kernel<T, ROT, true, 256>, grid, dim3(kThreads), 0, stream, p)
+              : launch_pdl(append_kernel<T, ROT, true, 0>, grid, dim3(kThreads), 0, stream, p);
+}
+
 template <typename T>
-cudaError_t launch(const AppendParams& p, bool interleaved, unsigned grid, cudaStream_t stream) {
-  const int half = p.rot / 2;
-  if (p.rot == 0) return launch_pdl(append_kernel<T, ROT_NONE>, dim3(grid), dim3(kThreads), 0, stream, p);
-  if (interleaved) return launch_pdl(append_kernel<T, ROT_SIDE>, dim3(grid), dim3(kThreads), 0, stream, p);
-  if (half % 8 == 0) return launch_pdl(append_kernel<T, ROT_HALF>, dim3(grid), dim3(kThreads), 0, stream, p);
-  return launch_pdl(append_kernel<T, ROT_HALF_ODD>, dim3(grid), dim3(kThreads), 0, stream, p);
+cudaError_t launch(const AppendParams& p, bool interleaved, dim3 grid, cudaStream_t stream) {
+  if (p.rot == 0) return launch_rot<T, ROT_NONE>(p, grid, stream);
+  if (interleaved) return launch_rot<T, ROT_SIDE>(p, grid, stream);
+  return p.rot % 16 == 0 ? launch_rot<T, ROT_HALF>(p, grid, stream) : launch_rot<T, ROT_HALF_ODD>(p, grid, stream);
 }
 
 }  // namespace
@@ -325,17 +421,18 @@ cudaError_t append_launch(AppendParams& p, spec_dtype dtype, bool interleaved, i
   p.tph = 1;
   while (p.tph * 8 < p.D) p.tph *= 2;
   const int heads = 32 / p.tph;
-  p.iters = (p.nq + 2 * p.nk + heads - 1) / heads;
-  // A warp takes a row's heads four at a time where there are few rows, so that they spread over the SMs,
-  // and whole rows where there are many, which then form their angles once.
-  const int64_t warps = static_cast<int64_t>(sms) * 16;
+  p.cq = (p.nq + heads - 1) / heads;
+  p.ck = (p.nk + heads - 1) / heads;
+  p.iters = p.cq + 2 * p.ck;
+  // A warp takes some of a row's heads where there are few rows, so that they spread over the SMs, and whole
+  // rows where there are many, which then form their angles once.
+  const int64_t warps = static_cast<int64_t>(sms) * kAppendWarps;
   const int64_t per = (p.rows * p.iters + warps - 1) / warps;
-  p.per_task = static_cast<int>(max(int64_t(1), min(per, static_cast<int64_t>(p.iters))));
-  p.tasks_row = (p.iters + p.per_task - 1) / p.per_task;
-  p.tasks = p.rows * p.tasks_row;
-  p.tasks_warp = max(int64_t(1), (p.tasks + warps - 1) / warps);
-  const int64_t used = max(int64_t(1), (p.tasks + p.tasks_warp - 1) / p.tasks_warp);
-  const unsigned grid = static_cast<unsigned>((used + kThreads / 32 - 1) / (kThreads / 32));
+  p.per_task = static_cast<int>(max(int64_t(1) + p.iters / 65536, min(per, static_cast<int64_t>(p.iters))));
+  const int parts = max(1, (p.iters + p.per_task - 1) / p.per_task);
+  p.rows_warp = max(int64_t(1), min(kAppendRows, p.rows * parts / warps));
+  const int64_t blocks = max(int64_t(1), (p.rows + p.rows_warp * kWarps - 1) / (p.rows_warp * kWarps));
+  const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(parts));
   return dtype == SPEC_BF16 ? launch<__nv_bfloat16>(p, interleaved, grid, stream)
                             : launch<float>(p, interleaved, grid, stream);
 }

@@ -66,7 +66,7 @@ struct AppendParams {
   const void *q, *k, *v;
   void* q_out;
   int64_t qs, ks, vs, qos;
-  int vec_in, vec_out;   // rows of q, k, v; of q_out are whole 16-byte vectors
+  int whole;             // rows of q, k, v and q_out are whole 16-byte vectors
   const float *q_norm, *k_norm;
   float eps;
   int rot;
@@ -75,10 +75,9 @@ struct AppendParams {
   const int64_t* pos;
   int32_t* status;
   int tph;               // lanes of a head
-  int iters;             // turns of a warp over a row's heads
-  int per_task;          // of which one task takes so many
-  int tasks_row;
-  int64_t tasks, tasks_warp;
+  int cq, ck, iters;     // turns of a warp over a row's query heads, its key heads (its values'), all
+  int per_task;          // of which a warp takes so many
+  int64_t rows_warp;     // rows of a warp
 };
 cudaError_t append_launch(AppendParams& p, spec_dtype dtype, bool interleaved, int sms, cudaStream_t stream);
 
