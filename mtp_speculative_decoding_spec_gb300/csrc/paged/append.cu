@@ -23,19 +23,19 @@ namespace spec {
 namespace {
 
 constexpr int kThreads = 128, kWarps = kThreads / 32;
-constexpr int kAppendWarps = 16;        // of an SM
-constexpr int64_t kAppendRows = 2;      // rows of a warp, at most
+constexpr int kAppendWarps = 16;  // of an SM, to deal out few rows
 
 enum : int { ROT_NONE = 0, ROT_SIDE = 1, ROT_HALF = 2, ROT_HALF_ODD = 3 };
 
 template <typename T, int ROT, int STEP>
-constexpr int kMinBlocks = ROT == ROT_HALF_ODD ? 1 : sizeof(T) == 2 && STEP ? 5 : 4;
+constexpr int kMinBlocks = ROT == ROT_HALF_ODD ? 1 : sizeof(T) == 2 && STEP ? 4 : 3;
+template <typename T>
+constexpr int kBatchOf = sizeof(T) == 2 ? 4 : 2;  // heads of a lane side by side
 
 template <typename T>
 struct Eight;  // eight elements as they lie in memory
 template <>
 struct Eight<__nv_bfloat16> {
-  static constexpr int kBatch = 8;  // heads of a lane in flight
   uint4 w;
   __device__ __forceinline__ Eight from(int lane, int width, bool any) const {  // another lane's, or zeros
     Eight o;
@@ -85,7 +85,6 @@ struct Eight<__nv_bfloat16> {
 };
 template <>
 struct Eight<float> {
-  static constexpr int kBatch = 4;
   float4 a, b;
   __device__ __forceinline__ Eight from(int lane, int width, bool any) const {
     float x[8];
@@ -167,9 +166,10 @@ __device__ __forceinline__ void lds8(const float* p, float* x) {
 // D is no power of two and the host's number counts.
 template <typename T, int ROT, bool WHOLE, int STEP>
 __global__ void __launch_bounds__(kThreads, kMinBlocks<T, ROT, STEP>) append_kernel(const __grid_constant__ AppendParams p) {
-  constexpr int kBatch = Eight<T>::kBatch;
+  constexpr int kBatch = kBatchOf<T>;
   __shared__ __align__(32) float weights[2][256];       // of queries and keys
   __shared__ __align__(32) float2 trig[kWarps][128];    // cos and sin of a warp's row
+  __shared__ uint64_t freq[128];                        // turns a position
   pdl_wait();
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
   const int tph = p.tph, at = lane & (tph - 1), sub = lane / tph, heads = 32 / tph;
@@ -179,33 +179,31 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks<T, ROT, STEP>) append_ker
     weights[0][d] = p.q_norm ? p.q_norm[d] : 1.f;
     weights[1][d] = p.k_norm ? p.k_norm[d] : 1.f;
   }
-  uint64_t F[4];  // of angles lane, lane + 32, ...
-  if constexpr (ROT != ROT_NONE) {
-#pragma unroll
-    for (int n = 0; n < 4; ++n) F[n] = lane + 32 * n < half ? turns_of(p.inv_freq[lane + 32 * n]) : 0;
-  }
+  if (ROT != ROT_NONE && threadIdx.x < half) freq[threadIdx.x] = turns_of(p.inv_freq[threadIdx.x]);
   __syncthreads();
   const float inv_d = 1.f / static_cast<float>(D);
   // with pairs half of rot_dim apart: the lane that has the other ends, whether there are any
   const bool low = e0 < half, turned = ROT == ROT_HALF && e0 < p.rot;
-  const int other = low ? at + half / 8 : at - half / 8;
+  const int other = !turned ? at : low ? at + half / 8 : at - half / 8;
   const auto angle = [&](int e) { return trig[wid][ROT == ROT_SIDE ? e >> 1 : e < half ? e : e - half]; };
   // this block's turns of a row: queries' cq, then keys' ck, then values' ck
   const int i0 = blockIdx.y * p.per_task, i1 = min(p.iters, i0 + p.per_task);
   const int q1 = min(i1, p.cq), k0 = max(0, i0 - p.cq), k1 = min(i1 - p.cq, p.ck);
   const int v0 = max(0, i0 - p.cq - p.ck), v1 = i1 - p.cq - p.ck;
 
-  // A few of a row's heads from `src`, at the lane's dims; turn n is there where a + n < a1 and its head < nh.
+  // kBatch of a row's heads, from turn a on, at the lane's dims; turn n is there where a + n < a1 and its head
+  // < nh. What is not there is computed on all the same (straight code: the heads' shuffles overlap), but a
+  // lane's registers reach no lane of another head, and it is not stored.
   Eight<T> x[kBatch];
   auto fetch = [&](const T* src, int a, int a1, int nh) {
 #pragma unroll
     for (int n = 0; n < kBatch; ++n)
-      if (a + n < a1 && holds && (a + n) * heads + sub < nh) x[n].load(src + n * step, WHOLE);
+      if (a + n < a1 && holds && (a + n) * heads + sub < nh) x[n].load(src + (a + n) * step, WHOLE);
   };
-  auto write = [&](T* dst, int a, int a1, int nh, bool whole) {
+  auto write = [&](const Eight<T>* y, T* dst, int a, int a1, int nh, bool whole) {
 #pragma unroll
     for (int n = 0; n < kBatch; ++n)
-      if (a + n < a1 && holds && (a + n) * heads + sub < nh) x[n].store(dst + n * step, whole);
+      if (a + n < a1 && holds && (a + n) * heads + sub < nh) y[n].store(dst + (a + n) * step, whole);
   };
   unsigned long long wc[4], ws[4];
   auto turn_weights = [&](const float* weight) {  // out_j = y_j wc_j + y'_j ws_j, y and y' without weights
@@ -235,100 +233,111 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks<T, ROT, STEP>) append_ker
       for (int j = 0; j < 8; j += 2) wc[j / 2] = pair(w[j], w[j + 1]);
     }
   };
-  auto work = [&](Eight<T>& e, bool live, bool norm) {  // one head, by the whole warp
-    float y[8];
-    e.get(y);
-    unsigned long long y2[4], o2[4];
+  // The heads in x; `next` fetches the ones after them into x once their bits are taken.
+  auto work = [&](Eight<T>* out, bool norm, auto&& next) {
+    Eight<T> mine[kBatch], far[kBatch];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) y2[j] = live ? pair(y[2 * j], y[2 * j + 1]) : 0ull;
+    for (int n = 0; n < kBatch; ++n) {
+      mine[n] = x[n];
+      // (with a norm a lane that is not turned may have its own bits there: they are finite, or its output is
+      // NaN as it is)
+      if (ROT == ROT_HALF) far[n] = x[n].from(other, tph, norm || turned);
+    }
+    next();
+    unsigned long long y2[kBatch][4];
+    float inv[kBatch];
+#pragma unroll
+    for (int n = 0; n < kBatch; ++n) {
+      float y[8];
+      mine[n].get(y);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) y2[n][j] = STEP || holds ? pair(y[2 * j], y[2 * j + 1]) : 0ull;
+    }
     if (norm) {
-      unsigned long long sq = mul2(y2[0], y2[0]);
 #pragma unroll
-      for (int j = 1; j < 4; ++j) ffma2_acc(sq, y2[j], y2[j]);
-      float sum = sum2(sq);
+      for (int n = 0; n < kBatch; ++n) {
+        unsigned long long sq = mul2(y2[n][0], y2[n][0]);
+#pragma unroll
+        for (int j = 1; j < 4; ++j) ffma2_acc(sq, y2[n][j], y2[n][j]);
+        inv[n] = sum2(sq);
+      }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1)
-        if (o < tph) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      const float inv = rsqrtf(fmaf(sum, inv_d, p.eps));
-      const unsigned long long inv2 = pair(inv, inv);
-      if constexpr (ROT == ROT_HALF) {
-        float z[8];
-        e.from(other, tph, turned).get(z);
+        if (o < tph) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) o2[j] = mul2(mul2(pair(z[2 * j], z[2 * j + 1]), inv2), ws[j]);
-      }
+          for (int n = 0; n < kBatch; ++n) inv[n] += __shfl_xor_sync(0xffffffffu, inv[n], o);
+        }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) y2[j] = mul2(y2[j], inv2);
-    } else if constexpr (ROT == ROT_HALF) {
-      float z[8];
-      e.from(other, tph, turned).get(z);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) o2[j] = mul2(pair(z[2 * j], z[2 * j + 1]), ws[j]);
+      for (int n = 0; n < kBatch; ++n) inv[n] = rsqrtf(fmaf(inv[n], inv_d, p.eps));
     }
-    if constexpr (ROT == ROT_SIDE) {
+#pragma unroll
+    for (int n = 0; n < kBatch; ++n) {
+      unsigned long long o2[4];
+      const unsigned long long inv2 = pair(inv[n], inv[n]);
+      float z[8];
+      if (ROT == ROT_HALF) far[n].get(z);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const unsigned long long swapped = y2[j] << 32 | y2[j] >> 32;
-        o2[j] = mul2(e0 + 2 * j < p.rot ? swapped : 0ull, ws[j]);
-        ffma2_acc(o2[j], y2[j], wc[j]);
-      }
-    } else if constexpr (ROT == ROT_HALF) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) ffma2_acc(o2[j], y2[j], wc[j]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) o2[j] = mul2(y2[j], wc[j]);
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      y[2 * j] = __uint_as_float(static_cast<uint32_t>(o2[j]));
-      y[2 * j + 1] = __uint_as_float(static_cast<uint32_t>(o2[j] >> 32));
-    }
-    if constexpr (ROT == ROT_HALF_ODD) {
-      // half of rot_dim no multiple of eight: element j's other end is element (j +- half) & 7 of the lane that
-      // far on or back
-      float up[8], down[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) up[j] = down[j] = y[j];
-#pragma unroll
-      for (int o = 1; o < 8; o <<= 1)
-        if (half & o) {
-          float a[8], b[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) a[j] = up[(j + o) & 7], b[j] = down[(j - o) & 7];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) up[j] = a[j], down[j] = b[j];
+        unsigned long long z2 = ROT == ROT_HALF ? pair(z[2 * j], z[2 * j + 1]) : 0ull;
+        if (norm) {
+          y2[n][j] = mul2(y2[n][j], inv2);
+          if (ROT == ROT_HALF) z2 = mul2(z2, inv2);
         }
+        if (ROT == ROT_SIDE && e0 + 2 * j < p.rot) z2 = y2[n][j] << 32 | y2[n][j] >> 32;
+        o2[j] = mul2(y2[n][j], wc[j]);
+        if (ROT == ROT_SIDE || ROT == ROT_HALF) ffma2_acc(o2[j], z2, ws[j]);
+      }
+      float y[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float a = __shfl_sync(0xffffffffu, up[j], at + ((j + half) >> 3), tph);
-        const float b = __shfl_sync(0xffffffffu, down[j], at + ((j - half) >> 3), tph);
-        if (e0 + j < p.rot) {
-          const float2 cs = angle(e0 + j);
-          y[j] = fmaf(e0 + j < half ? -a : b, cs.y, y[j] * cs.x);
+      for (int j = 0; j < 4; ++j) {
+        y[2 * j] = __uint_as_float(static_cast<uint32_t>(o2[j]));
+        y[2 * j + 1] = __uint_as_float(static_cast<uint32_t>(o2[j] >> 32));
+      }
+      if constexpr (ROT == ROT_HALF_ODD) {
+        // half of rot_dim no multiple of eight: element j's other end is element (j +- half) & 7 of the lane
+        // that far on or back
+        float up[8], down[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) up[j] = down[j] = y[j];
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1)
+          if (half & o) {
+            float a[8], b[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) a[j] = up[(j + o) & 7], b[j] = down[(j - o) & 7];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) up[j] = a[j], down[j] = b[j];
+          }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float a = __shfl_sync(0xffffffffu, up[j], at + ((j + half) >> 3), tph);
+          const float b = __shfl_sync(0xffffffffu, down[j], at + ((j - half) >> 3), tph);
+          if (e0 + j < p.rot) {
+            const float2 cs = angle(e0 + j);
+            y[j] = fmaf(e0 + j < half ? -a : b, cs.y, y[j] * cs.x);
+          }
         }
       }
+      out[n].set(y);
     }
-    e.set(y);
   };
 
   const int64_t warp = static_cast<int64_t>(blockIdx.x) * kWarps + wid;
-  const int64_t row1 = min(p.rows, (warp + 1) * p.rows_warp);
-  for (int64_t row = warp * p.rows_warp; row < row1; ++row) {
+  const auto one_row = [&](int64_t row) {
     const T* const q = static_cast<const T*>(p.q) + row * p.qs + sub * D + e0;
     const T* const k = static_cast<const T*>(p.k) + row * p.ks + sub * D + e0;
     const T* const v = static_cast<const T*>(p.v) + row * p.vs + sub * D + e0;
     if (i0 < q1)
-      fetch(q + i0 * step, i0, q1, p.nq);
+      fetch(q, i0, q1, p.nq);
     else if (k0 < k1)
-      fetch(k + k0 * step, k0, k1, p.nk);
+      fetch(k, k0, k1, p.nk);
     else
-      fetch(v + v0 * step, v0, v1, p.nk);
+      fetch(v, v0, v1, p.nk);
     const int b = paged_request_of(p.cu_rows, p.B, row);
-    if (b >= p.B) break;  // nobody's, as all after it
+    if (b >= p.B) return;  // nobody's
     const PagedRows pr = paged_rows(p.cu_rows, p.n_rows, p.rows, b);
     const int64_t r = row - pr.start;
-    if (r < 0 || r >= pr.runs) continue;
+    if (r < 0 || r >= pr.runs) return;
     const int64_t P = max(static_cast<int64_t>(0), p.c.kv_len[b]), pos = P + r;
     // where the row's keys and values go, in bytes from the layer's first page
     const int64_t page_at = p.nk > 0 && pos < static_cast<int64_t>(p.c.max_pages) * p.c.page_size
@@ -336,49 +345,56 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks<T, ROT, STEP>) append_ker
                                 : -1;
     if constexpr (ROT != ROT_NONE) {
       const uint64_t turn = static_cast<uint64_t>(p.pos ? p.pos[b] + r : pos);
-      __syncwarp();  // the row before is done with the table
-#pragma unroll
-      for (int n = 0; n < 4; ++n)
-        if (32 * n < half) {
-          const uint32_t part = static_cast<uint32_t>((F[n] * turn) >> 32);
-          float sn, cs;
-          sincospif(static_cast<float>(static_cast<int32_t>(part)) * 0x1p-31f, &sn, &cs);
-          trig[wid][lane + 32 * n] = make_float2(cs * p.rot_scale, sn * p.rot_scale);
-        }
+#pragma unroll 1
+      for (int n = lane; n < half; n += 32) {
+        const uint32_t part = static_cast<uint32_t>((freq[n] * turn) >> 32);
+        float sn, cs;
+        sincospif(static_cast<float>(static_cast<int32_t>(part)) * 0x1p-31f, &sn, &cs);
+        trig[wid][n] = make_float2(cs * p.rot_scale, sn * p.rot_scale);
+      }
       __syncwarp();
     }
     T* const out = static_cast<T*>(p.q_out) + row * p.qos + sub * D + e0;
     if (i0 < q1) {
       turn_weights(weights[0]);
+#pragma unroll 1
       for (int a = i0; a < q1; a += kBatch) {
-        if (a > i0) fetch(q + a * step, a, q1, p.nq);
-#pragma unroll
-        for (int n = 0; n < kBatch; ++n) {
-          if (a + n >= q1) break;
-          work(x[n], holds && (a + n) * heads + sub < p.nq, p.q_norm != nullptr);
-        }
-        write(out + a * step, a, q1, p.nq, WHOLE);
+        Eight<T> y[kBatch];
+        work(y, p.q_norm != nullptr, [&] {
+          if (a + kBatch < q1)
+            fetch(q, a + kBatch, q1, p.nq);
+          else if (k0 < k1)
+            fetch(k, k0, k1, p.nk);
+        });
+        write(y, out, a, q1, p.nq, WHOLE);
       }
     }
     T* const kp = reinterpret_cast<T*>(p.c.k + page_at) + sub * D + e0;
     T* const vp = reinterpret_cast<T*>(p.c.v + page_at) + sub * D + e0;
     if (k0 < k1) {
       turn_weights(weights[1]);
+#pragma unroll 1
       for (int a = k0; a < k1; a += kBatch) {
-        if (a > k0 || i0 < q1) fetch(k + a * step, a, k1, p.nk);
-#pragma unroll
-        for (int n = 0; n < kBatch; ++n) {
-          if (a + n >= k1) break;
-          work(x[n], holds && (a + n) * heads + sub < p.nk, p.k_norm != nullptr);
-        }
-        if (page_at >= 0) write(kp + a * step, a, k1, p.nk, true);
+        Eight<T> y[kBatch];
+        work(y, p.k_norm != nullptr, [&] {
+          if (a + kBatch < k1)
+            fetch(k, a + kBatch, k1, p.nk);
+          else if (v0 < v1)
+            fetch(v, v0, v1, p.nk);
+        });
+        if (page_at >= 0) write(y, kp, a, k1, p.nk, true);
       }
     }
+#pragma unroll 1
     for (int a = v0; a < v1; a += kBatch) {
-      if (a > v0 || i0 < q1 || k0 < k1) fetch(v + a * step, a, v1, p.nk);
-      if (page_at >= 0) write(vp + a * step, a, v1, p.nk, true);
+      Eight<T> y[kBatch];
+#pragma unroll
+      for (int n = 0; n < kBatch; ++n) y[n] = x[n];
+      if (a + kBatch < v1) fetch(v, a + kBatch, v1, p.nk);
+      if (page_at >= 0) write(y, vp, a, v1, p.nk, true);
     }
-  }
+  };
+  if (warp < p.rows) one_row(warp);
 
   if (p.status) {  // a warp to a request: the pages of its rows
     const int64_t warps = static_cast<int64_t>(gridDim.x) * kWarps;
@@ -424,14 +440,13 @@ cudaError_t append_launch(AppendParams& p, spec_dtype dtype, bool interleaved, i
   p.cq = (p.nq + heads - 1) / heads;
   p.ck = (p.nk + heads - 1) / heads;
   p.iters = p.cq + 2 * p.ck;
-  // A warp takes some of a row's heads where there are few rows, so that they spread over the SMs, and whole
-  // rows where there are many, which then form their angles once.
+  // A warp takes some of a row's heads where there are few rows, so that they spread over the SMs, and a whole
+  // row where there are many, which then forms its angles once (two rows to a warp: 70 us for 67).
   const int64_t warps = static_cast<int64_t>(sms) * kAppendWarps;
   const int64_t per = (p.rows * p.iters + warps - 1) / warps;
   p.per_task = static_cast<int>(max(int64_t(1) + p.iters / 65536, min(per, static_cast<int64_t>(p.iters))));
   const int parts = max(1, (p.iters + p.per_task - 1) / p.per_task);
-  p.rows_warp = max(int64_t(1), min(kAppendRows, p.rows * parts / warps));
-  const int64_t blocks = max(int64_t(1), (p.rows + p.rows_warp * kWarps - 1) / (p.rows_warp * kWarps));
+  const int64_t blocks = max(int64_t(1), (p.rows + kWarps - 1) / kWarps);
   const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(parts));
   return dtype == SPEC_BF16 ? launch<__nv_bfloat16>(p, interleaved, grid, stream)
                             : launch<float>(p, interleaved, grid, stream);

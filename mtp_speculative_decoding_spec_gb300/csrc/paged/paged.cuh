@@ -77,7 +77,6 @@ struct AppendParams {
   int tph;               // lanes of a head
   int cq, ck, iters;     // turns of a warp over a row's query heads, its key heads (its values'), all
   int per_task;          // of which a warp takes so many
-  int64_t rows_warp;     // rows of a warp
 };
 cudaError_t append_launch(AppendParams& p, spec_dtype dtype, bool interleaved, int sms, cudaStream_t stream);
 
