@@ -63,7 +63,7 @@ bool rows_ok(const int32_t* cu_rows, int64_t rows, const int32_t* n_rows) {
 // Attention: the tile sizes of the kernel that takes the call, and the workspace's layout.
 struct PagedPlan {
   int tc, tm, bn, tiles, grid;
-  size_t reqs, units, ml, o, total;
+  size_t ml, o, total;
 };
 
 spec_status plan_check(int32_t B, int64_t rows, const spec_paged_cache* c, const spec_paged_attn_desc* d,
@@ -77,7 +77,7 @@ spec_status plan_check(int32_t B, int64_t rows, const spec_paged_cache* c, const
   w.tc = c->dtype == SPEC_BF16 && paged_tc_takes(c->head_dim, c->page_size) &&
          c->page_stride < (int64_t(1) << 40);  // a tensor map's strides
   w.tm = w.tc ? attn_tc_tm() : attn_simt_tm();
-  w.bn = w.tc ? attn_tc_bn(c->head_dim) : attn_simt_bn();
+  w.bn = w.tc ? paged_tc_bn() : attn_simt_bn();
   const int64_t tiles = rows * G / w.tm + B;  // each request's last tile may not be full
   if (tiles > (w.tc ? kPagedMaxTiles : kPagedSimtMaxTiles)) return SPEC_ERR_UNSUPPORTED;
   const int64_t cap = static_cast<int64_t>(c->max_pages) * c->page_size;
@@ -92,11 +92,9 @@ spec_status plan_of(int32_t B, int64_t rows, const spec_paged_cache* c, const sp
   if (s != SPEC_OK) return s;
   const DevAttr a = dev_attr();
   if (a.sms <= 0) return SPEC_ERR_CUDA;
-  w.grid = a.sms;
+  w.grid = min(a.sms, kPagedMaxCtas);
   const size_t slots = 4 * static_cast<size_t>(w.grid);
-  w.reqs = sizeof(WsHeader);
-  w.units = w.reqs + align_up(sizeof(int4) * B, 256);
-  w.ml = w.units + align_up(sizeof(int2) * static_cast<size_t>(w.tiles) * c->kv_heads, 256);
+  w.ml = sizeof(WsHeader) + align_up(2 * w.grid * sizeof(PagedSplit), 256);
   w.o = w.ml + align_up(slots * w.tm * sizeof(float2), 256);
   w.total = w.o + align_up(slots * w.tm * c->head_dim * sizeof(float), 256);
   return SPEC_OK;
@@ -223,8 +221,7 @@ spec_status spec_paged_attention(int32_t B, const int32_t* cu_rows, int64_t rows
   p.cu_rows = cu_rows;
   p.rows = rows;
   p.hdr = static_cast<WsHeader*>(workspace);
-  p.reqs = reinterpret_cast<int4*>(ws + w.reqs);
-  p.units = reinterpret_cast<int2*>(ws + w.units);
+  p.splits = reinterpret_cast<PagedSplit*>(ws + sizeof(WsHeader));
   p.ml = reinterpret_cast<float2*>(ws + w.ml);
   p.o = reinterpret_cast<float*>(ws + w.o);
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);

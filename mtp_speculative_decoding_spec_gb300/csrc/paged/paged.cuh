@@ -2,6 +2,8 @@
 // trunk/attn_tc.cuh) ask of them.
 #pragma once
 
+#include <cuda_bf16.h>
+
 #include "trunk/trunk.cuh"
 
 namespace spec {
@@ -53,6 +55,8 @@ __device__ __forceinline__ PagedRows paged_rows(const int32_t* cu, const int32_t
   return r;
 }
 
+constexpr int kPagedMaxCtas = 512;
+
 // Tiles of a request that walk the same positions side by side (152 SMs are 19 eights), and from how many
 // positions on.
 constexpr int kPagedGroup = 8, kPagedGroupMin = 8192;
@@ -99,13 +103,14 @@ struct PagedReq {
   int start, rows, base;  // first row, rows that run, positions before them
   int g0, s0;             // its first item of `grp` tiles, its first item of a single tile
 };
+struct PagedSplit;
 struct PagedParams : AttnParams {
   PagedLayer c;
   const int32_t* cu_rows;
   int64_t rows;
   int group_min;          // positions from which a request's tiles are grouped
   int page_shift;         // tensor cores: positions (log2) of a block's part on one page, 31 where that is all
-  int4* reqs;             // for the join: first row, rows, g0, s0
+  PagedSplit* splits;     // [2 CTAs]
 };
 template <>
 inline constexpr bool kPaged<PagedParams> = true;
@@ -138,9 +143,10 @@ __device__ __forceinline__ int paged_sees(const PagedParams& p, const PagedReq& 
 
 // As for AttnParams: by the whole block, in shared memory, a barrier at the end. Requests whose tiles would
 // be more than there can be (cu_rows not as documented) have none.
-__device__ __forceinline__ const PagedReq* attn_plan(const PagedParams& p, int32_t* cum) {
+static __device__ __noinline__ const PagedReq* attn_plan(const PagedParams& p, int32_t* cum) {
   const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31;
   PagedReq* req = const_cast<PagedReq*>(paged_reqs(p, cum));
+#pragma unroll 1
   for (int b = tid; b < p.B; b += nt) {
     const PagedRows r = paged_rows(p.cu_rows, p.n_rows, p.rows, b);
     req[b].start = r.start;
@@ -150,6 +156,7 @@ __device__ __forceinline__ const PagedReq* attn_plan(const PagedParams& p, int32
   __syncthreads();
   if (tid < 32) {
     int all = 0, groups = 0, singles = 0;
+#pragma unroll 1
     for (int b0 = 0; b0 < p.B; b0 += 32) {
       const int b = b0 + lane;
       int n = b < p.B ? paged_tiles(p, req[b].rows) : 0, at = n;
@@ -178,6 +185,7 @@ __device__ __forceinline__ const PagedReq* attn_plan(const PagedParams& p, int32
       groups += __shfl_sync(0xffffffffu, cg, 31);
       singles += __shfl_sync(0xffffffffu, cs, 31);
     }
+#pragma unroll 1
     for (int b = lane; b < p.B; b += 32) req[b].s0 += groups;
     if (lane == 0) {
       cum[0] = 0;
@@ -186,11 +194,14 @@ __device__ __forceinline__ const PagedReq* attn_plan(const PagedParams& p, int32
     }
   }
   __syncthreads();
+#pragma unroll 1
   for (int b = tid >> 5; b < p.B; b += nt >> 5) {  // a warp to a request
     const PagedReq r = req[b];
     const int n = paged_tiles(p, r.rows), ng = paged_groups(p, r.rows, r.base);
+#pragma unroll 1
     for (int i = lane; i < ng; i += 32)
       cum[r.g0 + i + 1] = (paged_sees(p, r, (i + 1) * p.grp - 1) + p.bn - 1) / p.bn + p.over[0];
+#pragma unroll 1
     for (int t = ng * p.grp + lane; t < n; t += 32)
       cum[r.s0 + t - ng * p.grp + 1] = (paged_sees(p, r, t) + p.bn - 1) / p.bn + p.over[1];
   }
@@ -198,6 +209,7 @@ __device__ __forceinline__ const PagedReq* attn_plan(const PagedParams& p, int32
   if (tid < 32) {
     const int items = cum[p.items + 2];
     int base = 0;
+#pragma unroll 1
     for (int i0 = 1; i0 <= items; i0 += 32) {
       const int i = i0 + lane;
       int v = i <= items ? cum[i] : 0;
@@ -211,8 +223,6 @@ __device__ __forceinline__ const PagedReq* attn_plan(const PagedParams& p, int32
       base = __shfl_sync(0xffffffffu, v, 31);
     }
   }
-  if (blockIdx.x == 0)
-    for (int b = tid; b < p.B; b += nt) p.reqs[b] = make_int4(req[b].start, req[b].rows, req[b].g0, req[b].s0);
   __syncthreads();
   return req;
 }
@@ -226,6 +236,7 @@ __device__ __forceinline__ int attn_tile_req(const PagedParams&, int tile) {
 __device__ __forceinline__ int attn_single_tile(const PagedParams& p, const int32_t* cum, int item) {
   const PagedReq* req = paged_reqs(p, cum);
   int lo = 0, hi = p.B;
+#pragma unroll 1
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
     if (req[mid].s0 <= item)
@@ -239,6 +250,7 @@ __device__ __forceinline__ int attn_single_tile(const PagedParams& p, const int3
 __device__ __forceinline__ int attn_group_tile(const PagedParams& p, const int32_t* cum, int item, int rank) {
   const PagedReq* req = paged_reqs(p, cum);
   int lo = 0, hi = p.B;
+#pragma unroll 1
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
     if (req[mid].g0 <= item)
@@ -266,52 +278,39 @@ __device__ __forceinline__ int64_t attn_q_row(const PagedParams&, const PagedReq
 
 // Only units that more than one CTA has leave partials, and of those a CTA has at most the end of one
 // (its first piece) and the start of another (its last) in each part of the dealing: four slots a CTA.
-__device__ __forceinline__ int2 attn_unit(const PagedParams& p, const AttnShares& s, int u, int c0, int n) {
-  return make_int2(u < s.u1 ? c0 * p.grp : c0, n);
-}
 __device__ __forceinline__ int attn_slot(const PagedParams&, const AttnShares& s, int u, int cta, int blk0) {
   return 4 * cta + (u < s.u1 ? 0 : 2) + (blk0 == 0);
 }
-__device__ __forceinline__ int attn_join_slot(const PagedParams& p, const AttnJoinRow& j, int i) {
-  // u0: a grouped tile's (its first CTA, and CTAs `grp` on); u1: a single one's
-  return i < j.u0.y ? 4 * (j.u0.x + i * p.grp) + (i == 0) : 4 * (j.u1.x + i) + 2 + (i == 0);
+
+// What the join has to know of a unit that begins in a CTA's share and ends in another's: its number of
+// partials, the CTAs between them, its tile and head. A CTA writes its two (of the groups' part and of the
+// rest), by one thread: clear() first, then every piece.
+struct PagedSplit {
+  int n, step, tile, head;
+};
+__device__ __forceinline__ void paged_splits_clear(const PagedParams& p) {
+  for (int i = 0; i < 2; ++i) *reinterpret_cast<int4*>(p.splits + 2 * blockIdx.x + i) = make_int4(0, 1, 0, 0);
 }
-__device__ __forceinline__ AttnJoinRow attn_join_row(const PagedParams& p, int64_t row, int qh) {
-  AttnJoinRow j;
-  j.u0 = j.u1 = make_int2(0, 0);
-  j.at0 = j.at1 = 0;
-  j.write = false;
-  const int b = paged_request_of(p.cu_rows, p.B, row);
-  if (b >= p.B || row < p.cu_rows[b]) return j;  // nobody's
-  j.write = true;
-  const int4 rq = __ldcg(p.reqs + b);
-  const int r = static_cast<int>(row) - rq.x;
-  if (r < 0 || r >= rq.y) return j;  // does not run: zero
-  const int head = qh / p.G, x = r * p.G + qh - head * p.G, t = x / p.tm;
-  const int base = static_cast<int>(max(static_cast<int64_t>(0), min(p.kv_len[b], p.kcap)));
-  const int grouped = paged_groups(p, rq.y, base) * p.grp;
-  if (t < grouped) {
-    j.u0 = __ldcg(p.units + (rq.z + t / p.grp) * p.Hkv + head);
-    j.u0.x += t % p.grp;
-    j.at0 = x % p.tm;
-    j.write = j.u0.y > 1;  // else it is written already
-  } else {
-    j.u1 = __ldcg(p.units + (rq.w + t - grouped) * p.Hkv + head);
-    j.at1 = x % p.tm;
-    j.write = j.u1.y > 1;
-  }
-  return j;
+__device__ __forceinline__ void paged_split(const PagedParams& p, const int32_t* cum, const AttnShares& s,
+                                            const AttnWalk& walk, const AttnPiece& a) {
+  if (a.whole || a.blk0 > 0) return;
+  const int cta = blockIdx.x, cost = cum[walk.item + 1] - cum[walk.item];
+  // the place of its last block
+  const int64_t last = static_cast<int64_t>(cum[walk.item]) * p.Hkv + static_cast<int64_t>(a.head + 1) * cost - 1;
+  const bool group = walk.item * p.Hkv + a.head < s.u1;
+  const int n = group ? static_cast<int>(last / s.sp) - cta / p.grp + 1 : s.single_cta(last - s.wp) - cta + 1;
+  *reinterpret_cast<int4*>(p.splits + 2 * cta + !group) = make_int4(n, group ? p.grp : 1, a.tile, a.head);
 }
-__device__ __forceinline__ int64_t attn_join_rows(const PagedParams& p) { return p.rows; }
 
 cudaError_t paged_simt_launch(const PagedParams& p, spec_dtype dtype, int grid, cudaStream_t stream);
-cudaError_t paged_join_launch(const PagedParams& p, spec_dtype dtype, int sms, cudaStream_t stream);
+cudaError_t paged_join_launch(const PagedParams& p, spec_dtype dtype, int grid, cudaStream_t stream);
 // Page sizes of the tensor-core kernel: a block of its positions is whole pages or lies on one, and a page has
 // at least the eight rows of the operands' swizzle.
 inline bool paged_tc_takes(int head_dim, int page_size) {
   return attn_tc_takes(head_dim) && (page_size == 8 || page_size == 16 || page_size == 32 || page_size == 64 ||
                                      page_size % 128 == 0);
 }
+int paged_tc_bn();
 spec_status paged_tc_launch(const PagedParams& p, int grid, EncodeTiledFn encode, cudaStream_t stream);
 
 }  // namespace spec

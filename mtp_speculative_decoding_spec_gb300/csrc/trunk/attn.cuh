@@ -71,7 +71,7 @@ __global__ void __launch_bounds__(kSimtThreads, 1) attn_simt_kernel(const __grid
   int32_t* cum = reinterpret_cast<int32_t*>(row_q + kSimtTm);
   const auto* req = attn_plan(p, cum);
   const AttnShares shares = attn_shares(p, cum);
-  if (blockIdx.x == 0) attn_write_units(p, cum, shares);
+  if (!kPaged<P> && blockIdx.x == 0) attn_write_units(p, cum, shares);
   AttnWalk walk;
   walk.start(p, cum, shares);
   AttnPiece a;
@@ -82,7 +82,11 @@ __global__ void __launch_bounds__(kSimtThreads, 1) attn_simt_kernel(const __grid
   const int rpt = ng >= 16 ? 1 : ng >= 8 ? 2 : 4;
   const int d0 = (tid % nd) * 4, r0 = tid / nd * rpt;
   const bool holds = r0 < kSimtTm;
+  if constexpr (kPaged<P>)
+    if (tid == 0) paged_splits_clear(p);
   while (walk.next(p, cum, shares, a)) {
+    if constexpr (kPaged<P>)
+      if (tid == 0) paged_split(p, cum, shares, walk, a);
     const int head = a.head, slot = a.slot;
     __syncthreads();  // the previous piece's shared memory is no longer read
     if (tid < kSimtTm) {
@@ -273,127 +277,6 @@ __global__ void __launch_bounds__(kSimtThreads, 1) attn_simt_kernel(const __grid
   }
 }
 
-// One output row (verify row, query head) by NW warps: the partials of its prefix unit and then of its
-// own unit, warp w taking every NW-th of them, joined in that order. Many rows have few partials
-// each and get one warp a row (four rows to a block); few rows have many, and get eight warps. The whole
-// call, 16 query heads of 256 dims over a prefix of 15,360, one warp and eight: 8 verify rows 28.9 and 22.2
-// us, 32 32.8 and 30.2, 40 32.7 and 32.8, 48 32.7 and 33.5, 64 33.6 and 36.0, 128 42.6 and 51.9.
-// A partial of weight 0, from a row that saw nothing there or scores of -Inf alone, is added like any:
-// its output is 0, or what is not finite among the values of positions that the row does see.
-constexpr int kJoinMost = 4;  // partials in flight per warp
-
-template <typename P, typename T, int NW>
-__global__ void __launch_bounds__(NW == 1 ? 128 : 32 * NW) attn_join_kernel(const __grid_constant__ P p) {
-  __shared__ float sm_m[NW], sm_l[NW];
-  __shared__ float sm_o[NW == 1 ? 1 : NW][NW == 1 ? 1 : kMaxD];
-  const int lane = threadIdx.x & 31, warp = NW == 1 ? 0 : threadIdx.x >> 5;
-  const int Hq = p.Hkv * p.G;
-  const int64_t id = NW == 1 ? static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5) : blockIdx.x;
-  const int64_t row = id / Hq;
-  if (row >= attn_join_rows(p)) return;  // whole warps, and only where NW is 1
-  const int qh = static_cast<int>(id - row * Hq);
-  pdl_wait();
-  const AttnJoinRow jr = attn_join_row(p, row, qh);
-  if (!jr.write) return;  // the whole warp, and the block where it has one row
-  const int ntot = jr.u0.y + jr.u1.y;
-  float m = -INFINITY, l = 0.f;
-  float acc[2][4] = {};
-  const int nv = p.D / 4;
-  for (int i0 = warp; i0 < ntot; i0 += kJoinMost * NW) {
-    float2 mlv[kJoinMost];
-    float4 ov[kJoinMost][2];
-#pragma unroll
-    for (int j = 0; j < kJoinMost; ++j) {
-      const int i = i0 + NW * j;
-      mlv[j] = make_float2(-INFINITY, 0.f);
-      ov[j][0] = ov[j][1] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (i < ntot) {
-        const int64_t t = static_cast<int64_t>(attn_join_slot(p, jr, i)) * p.tm + (i < jr.u0.y ? jr.at0 : jr.at1);
-        mlv[j] = __ldcg(p.ml + t);
-        const float4* o = reinterpret_cast<const float4*>(p.o + t * p.D);
-        if (lane < nv) ov[j][0] = __ldcg(o + lane);
-        if (lane + 32 < nv) ov[j][1] = __ldcg(o + lane + 32);
-      }
-    }
-    float top = m;
-#pragma unroll
-    for (int j = 0; j < kJoinMost; ++j)
-      top = (top != top || mlv[j].x != mlv[j].x) ? NAN : fmaxf(top, mlv[j].x);
-    const float ref = top == -INFINITY ? 0.f : top;
-    const float c = exp2f(m - ref);
-    m = top;
-    l *= c;
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int d = 0; d < 4; ++d) acc[h][d] *= c;
-#pragma unroll
-    for (int j = 0; j < kJoinMost; ++j) {
-      const float w = exp2f(mlv[j].x - ref);
-      l = fmaf(w, mlv[j].y, l);
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        acc[h][0] = fmaf(w, ov[j][h].x, acc[h][0]);
-        acc[h][1] = fmaf(w, ov[j][h].y, acc[h][1]);
-        acc[h][2] = fmaf(w, ov[j][h].z, acc[h][2]);
-        acc[h][3] = fmaf(w, ov[j][h].w, acc[h][3]);
-      }
-    }
-  }
-  T* dst = static_cast<T*>(p.out) + row * p.os + static_cast<int64_t>(qh) * p.D;
-  if constexpr (NW == 1) {
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    const bool empty = m == -INFINITY;
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-      if (lane + 32 * h < nv) {
-#pragma unroll
-        for (int d = 0; d < 4; ++d) {
-          const float v = empty ? 0.f : acc[h][d] * inv;
-          if constexpr (sizeof(T) == 2)
-            dst[(lane + 32 * h) * 4 + d] = __float2bfloat16_rn(v);
-          else
-            dst[(lane + 32 * h) * 4 + d] = v;
-        }
-      }
-    if (p.lse && lane == 0) p.lse[row * Hq + qh] = empty ? -INFINITY : (m + log2f(l)) * kLn2;
-    return;
-  }
-  if (lane == 0) {
-    sm_m[warp] = m;
-    sm_l[warp] = l;
-  }
-#pragma unroll
-  for (int h = 0; h < 2; ++h)
-    if (lane + 32 * h < nv)
-      *reinterpret_cast<float4*>(&sm_o[warp][(lane + 32 * h) * 4]) =
-          make_float4(acc[h][0], acc[h][1], acc[h][2], acc[h][3]);
-  __syncthreads();
-  float top = -INFINITY;
-#pragma unroll
-  for (int w = 0; w < NW; ++w) top = (top != top || sm_m[w] != sm_m[w]) ? NAN : fmaxf(top, sm_m[w]);
-  const float ref = top == -INFINITY ? 0.f : top;
-  float wt[NW], tot = 0.f;
-#pragma unroll
-  for (int w = 0; w < NW; ++w) {
-    wt[w] = exp2f(sm_m[w] - ref);
-    tot = fmaf(wt[w], sm_l[w], tot);
-  }
-  const float inv = tot == 0.f ? 0.f : 1.f / tot;
-  for (int d = threadIdx.x; d < p.D; d += 32 * NW) {
-    float v = 0.f;
-#pragma unroll
-    for (int w = 0; w < NW; ++w) v = fmaf(wt[w], sm_o[w][d], v);
-    v = top == -INFINITY ? 0.f : v * inv;
-    if constexpr (sizeof(T) == 2)
-      dst[d] = __float2bfloat16_rn(v);
-    else
-      dst[d] = v;
-  }
-  if (p.lse && threadIdx.x == 0)
-    p.lse[row * Hq + qh] = top == -INFINITY ? -INFINITY : (top + log2f(tot)) * kLn2;
-}
-
 template <typename P, typename T>
 cudaError_t simt_launch(const P& p, int grid, cudaStream_t stream) {
   static SmemAllowance allowed;
@@ -403,19 +286,6 @@ cudaError_t simt_launch(const P& p, int grid, cudaStream_t stream) {
   const cudaError_t e = allow_dynamic_smem(attn_simt_kernel<P, T>, smem, allowed);
   if (e != cudaSuccess) return e;
   return launch_pdl(attn_simt_kernel<P, T>, dim3(grid), dim3(kSimtThreads), smem, stream, p);
-}
-
-template <typename P>
-cudaError_t join_launch(const P& p, int64_t rows, spec_dtype dtype, int sms, cudaStream_t stream) {
-  rows *= p.Hkv * p.G;
-  if (rows > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  const bool many = rows >= 4 * static_cast<int64_t>(sms);  // both sides measured at the kernel
-  const dim3 g(static_cast<unsigned>(many ? (rows + 3) / 4 : rows)), t(many ? 128 : 256);
-  if (dtype == SPEC_BF16)
-    return many ? launch_pdl(attn_join_kernel<P, __nv_bfloat16, 1>, g, t, 0, stream, p)
-                : launch_pdl(attn_join_kernel<P, __nv_bfloat16, 8>, g, t, 0, stream, p);
-  return many ? launch_pdl(attn_join_kernel<P, float, 1>, g, t, 0, stream, p)
-              : launch_pdl(attn_join_kernel<P, float, 8>, g, t, 0, stream, p);
 }
 
 }  // namespace spec

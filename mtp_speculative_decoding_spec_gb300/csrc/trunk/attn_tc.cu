@@ -7,7 +7,7 @@ namespace {
 
 template <int D>
 spec_status launch_tc(const AttnParams& p, int grid, EncodeTiledFn encode, cudaStream_t stream) {
-  using Sh = Shape<D>;
+  using Sh = Shape<D, false>;
   AttnMaps m;
   // dims inside a 64-dim panel, positions, panels (64 dims on), requests
   const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(Sh::kBn), D / 64, 1};
@@ -36,7 +36,7 @@ spec_status launch_tc(const AttnParams& p, int grid, EncodeTiledFn encode, cudaS
 
 bool attn_tc_takes(int head_dim) { return head_dim == 64 || head_dim == 128 || head_dim == 256; }
 int attn_tc_tm() { return kTm; }
-int attn_tc_bn(int head_dim) { return head_dim == 256 ? Shape<256>::kBn : Shape<128>::kBn; }
+int attn_tc_bn(int head_dim) { return head_dim == 256 ? Shape<256, false>::kBn : Shape<128, false>::kBn; }
 
 spec_status attn_tc_launch(const AttnParams& p, int grid, EncodeTiledFn encode, cudaStream_t stream) {
   return p.D == 256   ? launch_tc<256>(p, grid, encode, stream)

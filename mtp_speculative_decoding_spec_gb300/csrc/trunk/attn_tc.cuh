@@ -7,8 +7,8 @@
 // in TMEM too and V as it lies in the cache (rows of positions: the B operand is N-major).
 //   * warp 0 loads K and V blocks by TMA; Q is gathered by the softmax threads into TMEM, so that
 //     its 128 rows are not read from shared memory again for every block;
-//   * warp 1 issues the MMAs: S of block i+1 goes out before O of block i, so the tensor pipe works
-//     on one while the softmax works on the other (two S buffers);
+//   * warp 1 issues the MMAs: S of the blocks after i goes out before O of block i, so the tensor pipe works
+//     on them while the softmax works on the others (two S buffers, or four);
 //   * warps 4..7 and 8..11 do the softmax of the blocks in turns; warps 2 and 3 watch V (below). The
 //     reference a row's weights are taken against moves only when the row's maximum has grown by more
 //     than 2^8 (the weights stay below 256 and their sum and O are fp32, so nothing is lost), which makes
@@ -43,7 +43,7 @@ constexpr int kTm = 128;
 constexpr int kTcThreads = 12 * 32;  // producer, MMA and two guard warps, eight softmax warps
 constexpr int kGroupThreads = 128;  // a softmax group
 template <typename P>
-constexpr int kTcSmall = kPaged<P> ? 640 : 512;  // bytes of barriers and flags
+constexpr int kTcSmall = kPaged<P> ? 1280 : 512;  // bytes of barriers and flags
 // Registers a thread: launched with 168 (64,512 in all); the first four warps give to the softmax's
 // eight: 128 x 152 + 256 x 176 = 64,512. (104 and 200 spill in the guards: 214 us for 191.)
 constexpr int kFewRegs = 152, kSoftRegs = 176;
@@ -51,65 +51,76 @@ constexpr int kFewRegs = 152, kSoftRegs = 176;
 // with 0, 192 with 8.
 constexpr float kLazy = 8.f;
 
-template <int D>
+// A batch of products alone takes some 500 cycles more than the same products among others, so a block's way
+// from its scores through its softmax to its product and the next scores in its place is long, and what
+// hides it is blocks on their way: as many buffers of scores as tensor memory has room for.
+template <int D, bool PAGED>
 struct Shape {
-  // K and V blocks of 16 or 32 KB. 128 dims in blocks of 64 positions took 168 us for 151 (256 rows over
-  // 63,488); 256 dims in blocks of 128 do not fit beside two buffers of S.
-  static constexpr int kBn = D == 256 ? 64 : 128;
-  static constexpr int kStages = D == 64 ? 6 : 3;
+  // Verify rows: K and V blocks of 16 or 32 KB. 128 dims in blocks of 64 positions took 168 us for 151 (256
+  // rows over 63,488); 256 dims in blocks of 128 do not fit beside two buffers of S.
+  static constexpr int kBn = D == 256 || PAGED ? 64 : 128;
+  static constexpr int kBuf = D != 256 && PAGED ? 4 : 2;
   static constexpr int kTile = kBn * D * 2;
+  static constexpr int kStages = PAGED ? (D == 256 ? 3 : D == 128 ? 6 : 8) : D == 64 ? 6 : 3;
   // The product with V starts on the first half of a block's weights. At 128 positions: 142 -> 128 us (256
   // rows of 128 dims over 63,488); at 64 the tensor pipe, in order, waits for the second half instead of
   // taking the other buffer's scores: 191 -> 211 us (of 256 dims).
   static constexpr bool kHalves = kBn == 128;
-  static constexpr int kPanel = kBn * 128;          // 64 dims of a block: rows of 128 bytes
   static constexpr int kFixed = 2 * kStages * kTile;
-  // TMEM columns: O, two S buffers, Q (two bf16 a column)
-  static constexpr int kS = D, kQ = D + 2 * kBn;
+  // TMEM columns: O, the S buffers, Q (two bf16 a column)
+  static constexpr int kS = D, kQ = D + kBuf * kBn;
   static_assert(kQ + D / 2 <= 512, "TMEM");
+  static_assert(kStages > kBuf, "K runs kBuf - 1 blocks ahead");
 };
 
-// A block of K or V at once: [panel of 64 dims][position][64 dims], the order of its map's box. Called
-// by a whole warp, one lane of which issues.
+// A block of K or V in shared memory: for each panel of 64 dims rows of 128 bytes, eight positions to 1,024
+// bytes (the swizzle's atom). A contiguous cache's box is [panel][position][64 dims], a page's [eight
+// positions][panel][8][64]: then a page of any size lies in one piece, and its neighbour after it.
+template <typename P, int D>
+struct Place {
+  static constexpr int kGroup = kPaged<P> ? D / 64 * 1024 : 1024;               // from eight positions to the next
+  static constexpr int kPanel = kPaged<P> ? 1024 : Shape<D, false>::kBn * 128;  // from a panel to the next
+  static __device__ __forceinline__ int at(int pos) { return (pos >> 3) * kGroup + (pos & 7) * 128; }
+};
+
+// A block of K or V at once, in the order of its map's box.
 __device__ __forceinline__ void tma_load_block(void* dst, const CUtensorMap* map, int pos, int panel,
-                                               int b, uint64_t* bar, uint32_t bytes) {
+                                               int b, uint64_t* bar) {
   asm volatile(
-        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
-        "@e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%5], %6;\n\t"
-        "@e cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%7, %2, %3, %4}], [%5];\n\t}" ::"r"(smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(pos), "r"(panel), "r"(b), "r"(smem_u32(bar)),
-        "r"(bytes), "r"(0)
-        : "memory");
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%6, %2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(pos), "r"(panel), "r"(b), "r"(smem_u32(bar)), "r"(0)
+      : "memory");
 }
 
-// B operand whose rows (K) are 128 bytes of N in the 128-byte swizzle: 8-row groups 1,024 bytes
+// B operand whose rows (K) are 128 bytes of N in the 128-byte swizzle: 8-row groups `group` bytes
 // apart, the next 64 of N one panel on.
-__device__ __forceinline__ uint64_t smem_desc_n_major(uint32_t saddr, uint32_t panel) {
+__device__ __forceinline__ uint64_t smem_desc_n_major(uint32_t saddr, uint32_t panel, uint32_t group) {
   uint64_t d = 0;
   d |= static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
   d |= static_cast<uint64_t>((panel >> 4) & 0x3FFFu) << 16;
-  d |= static_cast<uint64_t>((1024u >> 4) & 0x3FFFu) << 32;
+  d |= static_cast<uint64_t>((group >> 4) & 0x3FFFu) << 32;
   d |= static_cast<uint64_t>(1u) << 46;
   d |= static_cast<uint64_t>(2u) << 61;
   return d;
 }
+// And whose rows (N) are 128 bytes of K, as smem_desc_sw128's.
+__device__ __forceinline__ uint64_t smem_desc_k_major(uint32_t saddr, uint32_t group) {
+  return smem_desc_sw128(saddr) + (static_cast<uint64_t>((group - 1024u) >> 4) << 32);
+}
 
-// A from TMEM (two bf16 of K per 32-bit column), B from shared memory. Called by a whole warp, one
-// lane of which issues: the operands are the same in all lanes and stay in uniform registers.
+// A from TMEM (two bf16 of K per 32-bit column), B from shared memory.
 __device__ __forceinline__ void tc_mma_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
                                           uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate));
 }
-__device__ __forceinline__ void tc_commit_elect(uint64_t* bar) {
-  asm volatile(
-      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
-      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
-          smem_u32(bar))
-      : "memory");
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}" : "=r"(r));
+  return r != 0;
 }
 
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
@@ -204,62 +215,22 @@ struct AttnMaps {
   CUtensorMap pk, pv, ok, ov;  // K and V of the prefix, of the own caches (the paged cache: ok and ov)
 };
 
-// The pages of a block of positions, a lane each: the table's entries come 32 at a time, the next 32 already
-// on their way, so that a block's loads do not wait for its part of the table.
-struct PageWindow {
-  int n = 1;         // pages a block meets
-  int first = -1, b = -1, cur = 0, next = 0;
-  template <typename P>
-  __device__ __forceinline__ PageWindow(const P& p, int bn) {
-    if constexpr (kPaged<P>) n = p.c.page_size >= bn ? 1 : bn / p.c.page_size;
-  }
-  template <typename P>
-  __device__ __forceinline__ int entry(const P& p, int j) const {
-    return j < p.c.max_pages ? __ldg(p.c.table + static_cast<int64_t>(b) * p.c.table_stride + j) : -1;
-  }
-  // This lane's page (n_pages: it is not there) of the block at `pos`, and the position in it.
-  template <typename P>
-  __device__ __forceinline__ int of(const P& p, int req, int pos, int bn, int& at) {
-    const int lane = threadIdx.x & 31;
-    const int j = pos / p.c.page_size, w = j & ~31;
-    at = pos - j * p.c.page_size;
-    if (w != first || req != b) {
-      const bool ahead = req == b && w == first + 32;
-      b = req;
-      cur = ahead ? next : entry(p, w + lane);
-      next = entry(p, w + 32 + lane);
-      first = w;
-    }
-    const int g = __shfl_sync(0xffffffffu, cur, (j & 31) + (lane & (n - 1)));  // n divides 32: no page is past it
-    return static_cast<unsigned>(g) < static_cast<unsigned>(p.c.n_pages) ? g : p.c.n_pages;
-  }
-};
-
-// A block of K or V in its pages, in the order [panel of 64 dims][position][64 dims]: one box where a page has
-// it all, else one per page and panel, a lane each (at most 32 of them: a page has 8 positions or more). A
-// page's number past the last reads zeros.
-template <int D, int BN>
-__device__ __forceinline__ void paged_load_block(uint8_t* dst, const CUtensorMap* map, int panel, int page, int at,
-                                                 int n, uint64_t* bar, uint32_t bytes) {
-  const int lane = threadIdx.x & 31;
-  if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
-  __syncwarp();
-  const int sub = lane & (n - 1), pan = lane / n;
-  if (n == 1 ? lane == 0 : pan < D / 64)
-    asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
-            smem_u32(dst + (n == 1 ? 0 : pan * BN * 128 + sub * (BN / n) * 128))),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(at), "r"(panel + (n == 1 ? 0 : pan)), "r"(page),
-        "r"(smem_u32(bar))
-        : "memory");
+// A page's part of a block of K or V. A page's number past the last reads zeros.
+__device__ __forceinline__ void tma_load_page(void* dst, const CUtensorMap* map, int panel, int eight, int page,
+                                              uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(panel), "r"(eight), "r"(page), "r"(smem_u32(bar))
+      : "memory");
 }
 
 template <typename P, int D>
 __global__ void __launch_bounds__(kTcThreads, 1)
     attn_tc_kernel(const __grid_constant__ AttnMaps maps, const __grid_constant__ P p) {
-  using Sh = Shape<D>;
-  constexpr int BN = Sh::kBn, NS = Sh::kStages;
+  using Sh = Shape<D, kPaged<P>>;
+  using Pl = Place<P, D>;
+  constexpr int BN = Sh::kBn, NS = Sh::kStages, NB = Sh::kBuf;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -286,6 +257,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   // [2 NS] of a K block, which of its pages are not there. Written when the block's stage is free, which may
   // be before every warp has read an earlier block's word: two stages' worth.
   volatile uint32_t* gone = reinterpret_cast<volatile uint32_t*>(least_sm + 8);
+  int* pages = const_cast<int*>(reinterpret_cast<volatile int*>(gone + 2 * NS));  // [128] of the table's entries
   float* row_m = reinterpret_cast<float*>(smem + Sh::kFixed + kTcSmall<P>);  // [2][128] each group's last reference
   float2* row_ml = reinterpret_cast<float2*>(row_m + 2 * kTm);       // [2][128] and sum, at a piece's end
   int32_t* cum = reinterpret_cast<int32_t*>(row_ml + 2 * kTm);
@@ -317,7 +289,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
   const AttnShares shares = attn_shares(p, cum);
-  if (blockIdx.x == 0) attn_write_units(p, cum, shares);
+  if (!kPaged<P> && blockIdx.x == 0) attn_write_units(p, cum, shares);
   AttnWalk walk;
   walk.start(p, cum, shares);
   AttnPiece a;
@@ -333,116 +305,188 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------------------ TMA producer
-    int it = 0;  // V blocks; K runs one block ahead, as the MMAs take them
+    // One elected thread waits and issues, as below; the others help it to the page table's entries.
+    const bool leader = elect_one();
+    int gi = 0, ks = 0, kp = 1, ki = 0, vs = 0, vp = 1, vi = 0;  // the next K and V blocks: stage, its phase, number
     bool ok = true;
-    PageWindow pages(p, BN);
-    int k_page = 0, v_page = 0, k_at = 0, v_at = 0;  // this lane's page of the K and V blocks, where in it
-    while (ok && !__any_sync(0xffffffffu, *abort_flag) && walk.next(p, cum, shares, a)) {
-      const bool pre = a.tile < p.npt;
-      const int b = pre ? 0 : attn_tile_req(p, a.tile), panel = a.head * (D / 64);
-      auto load = [&](uint8_t* tiles, uint64_t* full, uint64_t* empty, const CUtensorMap* map, int i,
-                      int blk) {
-        const int s = i % NS;
-        if (i >= NS && !mbar_wait_warp(&empty[s], ((i / NS) & 1) ^ 1))
-          return false;
-        if constexpr (kPaged<P>) {
-          const bool is_k = tiles == sk;
-          if (is_k) {
-            v_page = k_page;
-            v_at = k_at;
-            k_page = pages.of(p, b, blk * BN, BN, k_at);
-            const uint32_t lost = __ballot_sync(0xffffffffu, k_page == p.c.n_pages && lane < pages.n);
-            if (lane == 0) gone[i % (2 * NS)] = lost;
+    // K runs as far ahead as the MMAs take it
+    auto next_k = [&](int left_k, int left_v) { return left_k > 0 && left_k > left_v - NB; };
+    auto room = [&](uint64_t* empty, int s, int phase, int i) { return i < NS || mbar_wait_bounded(&empty[s], phase); };
+#pragma unroll 1
+    while (__all_sync(0xffffffffu, ok && !*abort_flag) && walk.next(p, cum, shares, a)) {
+      const int panel = a.head * (D / 64), blk0 = a.blk0, blk1 = a.blk1;
+      int left_k = blk1 - blk0, left_v = left_k;
+      if constexpr (kPaged<P>) {
+        const int b = attn_tile_req(p, a.tile), ps = p.c.page_size;
+        const int32_t* table = p.c.table + static_cast<int64_t>(b) * p.c.table_stride;
+        const auto entry = [&](int j) { return j < p.c.max_pages ? __ldg(table + j) : -1; };
+        const int per = ps >= BN ? 1 : BN / ps, bytes = Sh::kTile / per;  // pages of a block
+        int kj = blk0 * BN / ps, k_at = blk0 * BN - kj * ps, vj = kj, v_at = k_at;
+        // entries 32 at a time, the next ones on their way; a ring of four times as many, for V behind K
+        int e = entry((kj & ~31) + lane);
+#pragma unroll 1
+        for (int w = kj & ~31; left_v > 0; w += 32) {
+          __syncwarp();
+          pages[(w + lane) & 127] = static_cast<unsigned>(e) < static_cast<unsigned>(p.c.n_pages) ? e : p.c.n_pages;
+          e = entry(w + 32 + lane);
+          __syncwarp();
+          if (leader) {
+#pragma unroll 1
+            while (ok && left_v > 0) {
+              if (next_k(left_k, left_v)) {
+                if (kj + per > w + 32) break;
+                ok = room(kdone, ks, kp, ki);
+                if (!ok) break;
+                uint32_t lost = 0;
+#pragma unroll 1
+                for (int m = 0; m < per; ++m)
+                  lost |= static_cast<uint32_t>(pages[(kj + m) & 127] == p.c.n_pages) << m;
+                gone[gi] = lost;  // seen with the block: the scores' wait for it comes before the softmax's for them
+                if (++gi == 2 * NS) gi = 0;
+                mbar_arrive_expect_tx(&kfull[ks], Sh::kTile);
+#pragma unroll 1
+                for (int m = 0; m < per; ++m)
+                  tma_load_page(sk + ks * Sh::kTile + m * bytes, &maps.ok, panel, k_at >> 3, pages[(kj + m) & 127],
+                                &kfull[ks]);
+                k_at += BN;
+                if (k_at >= ps) kj += per, k_at = 0;
+                if (++ks == NS) ks = 0, kp ^= 1;
+                ++ki;
+                --left_k;
+              } else {
+                ok = room(vdone, vs, vp, vi);
+                if (!ok) break;
+                mbar_arrive_expect_tx(&vfull[vs], Sh::kTile);
+#pragma unroll 1
+                for (int m = 0; m < per; ++m)
+                  tma_load_page(sv + vs * Sh::kTile + m * bytes, &maps.ov, panel, v_at >> 3, pages[(vj + m) & 127],
+                                &vfull[vs]);
+                v_at += BN;
+                if (v_at >= ps) vj += per, v_at = 0;
+                if (++vs == NS) vs = 0, vp ^= 1;
+                ++vi;
+                --left_v;
+              }
+            }
           }
-          // K runs a block ahead of V, but for a piece's first
-          const bool same = is_k || blk + 1 == a.blk1;
-          paged_load_block<D, BN>(tiles + s * Sh::kTile, map, panel, same ? k_page : v_page, same ? k_at : v_at,
-                                  pages.n, &full[s], Sh::kTile);
-        } else {
-          tma_load_block(tiles + s * Sh::kTile, map, blk * BN, panel, b, &full[s], Sh::kTile);
+          left_v = __reduce_min_sync(0xffffffffu, leader ? (ok ? left_v : 0) : 0x7fffffff);
         }
-        return true;
-      };
-      const CUtensorMap* mk = pre ? &maps.pk : &maps.ok;
-      const CUtensorMap* mv = pre ? &maps.pv : &maps.ov;
-      const int n = a.blk1 - a.blk0;
-      ok = load(sk, kfull, kdone, mk, it, a.blk0);
-      int j = 0;
-      for (; ok && j < n; ++j) {
-        if (j + 1 < n) ok = load(sk, kfull, kdone, mk, it + j + 1, a.blk0 + j + 1);
-        ok = ok && load(sv, vfull, vdone, mv, it + j, a.blk0 + j);
+      } else if (leader) {
+        const bool pre = a.tile < p.npt;
+        const int b = pre ? 0 : attn_tile_req(p, a.tile);
+        const CUtensorMap* mk = pre ? &maps.pk : &maps.ok;
+        const CUtensorMap* mv = pre ? &maps.pv : &maps.ov;
+#pragma unroll 1
+        while (ok && left_v > 0) {
+          const bool is_k = next_k(left_k, left_v);
+          ok = is_k ? room(kdone, ks, kp, ki) : room(vdone, vs, vp, vi);
+          if (!ok) break;
+          mbar_arrive_expect_tx(is_k ? &kfull[ks] : &vfull[vs], Sh::kTile);
+          if (is_k) {
+            tma_load_block(sk + ks * Sh::kTile, mk, (blk1 - left_k) * BN, panel, b, &kfull[ks]);
+            if (++ks == NS) ks = 0, kp ^= 1;
+            ++ki;
+            --left_k;
+          } else {
+            tma_load_block(sv + vs * Sh::kTile, mv, (blk1 - left_v) * BN, panel, b, &vfull[vs]);
+            if (++vs == NS) vs = 0, vp ^= 1;
+            ++vi;
+            --left_v;
+          }
+        }
       }
-      it += j;
     }
-    if (!ok && lane == 0) give_up();
-    // Leave nothing in flight: the last loads of every stage have landed. Where a wait ran out, V's last
-    // was not sent and one more of K's may have been; what was not sent costs a wait with its limit.
-    for (int j = max(0, it - NS); j < it + !ok; ++j) mbar_wait_warp(&kfull[j % NS], (j / NS) & 1);
-    for (int j = max(0, it - NS - !ok); j < it; ++j) mbar_wait_warp(&vfull[j % NS], (j / NS) & 1);
+    if (leader) {
+      if (!ok) give_up();
+      // Leave nothing in flight: the last loads of every stage have landed.
+#pragma unroll 1
+      for (int j = max(0, ki - NS); j < ki; ++j) mbar_wait_bounded(&kfull[j % NS], (j / NS) & 1);
+#pragma unroll 1
+      for (int j = max(0, vi - NS); j < vi; ++j) mbar_wait_bounded(&vfull[j % NS], (j / NS) & 1);
+    }
+    __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------------ MMA issuer
-    {
+    // One elected thread goes through all of it. Its time is part of every block's way, and there the compiler
+    // keeps operands in uniform registers: 9 cycles an MMA, where a warp that elects a thread for each takes 15
+    // alone and 37 beside the softmax's (four moves to uniform registers and a vote each).
+    if (elect_one()) {
       constexpr uint32_t kIdS = tc_idesc(kTm, BN);
       constexpr uint32_t kIdO = tc_idesc(kTm, D) | (1u << 16);  // B is N-major
-      const uint64_t kd0 = smem_desc_sw128(smem_u32(sk));
-      const uint64_t vd0 = smem_desc_n_major(smem_u32(sv), Sh::kPanel);
-      int it = 0, piece = 0;
+      const uint64_t kd0 = smem_desc_k_major(smem_u32(sk), Pl::kGroup);
+      const uint64_t vd0 = smem_desc_n_major(smem_u32(sv), Pl::kPanel, Pl::kGroup);
+      int ks = 0, kp = 0, kb = 0;             // of the next scores: stage, its phase, buffer
+      int vs = 0, vp = 0, vb = 0, piece = 0;  // of the next product
       bool ok = true;
-      auto scores = [&](int i) {
-        if (!mbar_wait_warp(&kfull[i % NS], (i / NS) & 1)) return false;
+      auto scores = [&]() {
+        if (!mbar_wait_bounded(&kfull[ks], kp)) return false;
         tc_fence_after();
-        const uint64_t kd = desc_advance(kd0, (i % NS) * Sh::kTile);
-        const uint32_t ds = tmem + Sh::kS + (i & 1) * BN;
+        const uint64_t kd = desc_advance(kd0, ks * Sh::kTile);
+        const uint32_t ds = tmem + Sh::kS + kb * BN;
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
           tc_mma_ta(ds, tmem + Sh::kQ + kk * 8,
-                    desc_advance(kd, (kk / 4) * Sh::kPanel + (kk % 4) * 32), kIdS, kk > 0);
-        tc_commit_elect(&kdone[i % NS]);
+                    desc_advance(kd, (kk / 4) * Pl::kPanel + (kk % 4) * 32), kIdS, kk > 0);
+        tc_commit(&kdone[ks]);
+        if (++ks == NS) ks = 0, kp ^= 1;
+        kb = kb + 1 == NB ? 0 : kb + 1;
         return true;
       };
-      while (ok && !__any_sync(0xffffffffu, *abort_flag) && walk.next(p, cum, shares, a)) {
+#pragma unroll 1
+      while (ok && !*abort_flag && walk.next(p, cum, shares, a)) {
         const int n = a.blk1 - a.blk0;
-        ok = mbar_wait_warp(qready, piece & 1);
+        ok = mbar_wait_bounded(qready, piece & 1);
         tc_fence_after();
-        ok = ok && scores(it);
+#pragma unroll 1
+        for (int j = 0; ok && j < min(n, NB - 1); ++j) ok = scores();
+#pragma unroll 1
         for (int j = 0; ok && j < n; ++j) {
-          const int i = it + j;
-          if (j + 1 < n) ok = scores(i + 1);
-          ok = ok && mbar_wait_warp(&pready[i % NS], (i / NS) & 1);
-          if (j == 0 && piece > 0)
-            ok = ok && mbar_wait_warp(ofree, (piece - 1) & 1);
+          if (j + NB - 1 < n) ok = scores();
+          ok = ok && mbar_wait_bounded(&pready[vs], vp);
+          uint32_t acc0 = 1;
+          if (j == 0) {
+            if (piece > 0) ok = ok && mbar_wait_bounded(ofree, (piece - 1) & 1);
+            acc0 = o_init[piece & 1] ? 1u : 0u;
+          }
           if (!ok) break;
           tc_fence_after();
-          const uint64_t vd = desc_advance(vd0, (i % NS) * Sh::kTile);
-          const uint32_t ps = tmem + Sh::kS + (i & 1) * BN;
-          const uint32_t acc0 = j > 0 || o_init[piece & 1] ? 1u : 0u;
+          const uint64_t vd = desc_advance(vd0, vs * Sh::kTile);
+          const uint32_t ps = tmem + Sh::kS + vb * BN;
 #pragma unroll
           for (int kk = 0; kk < BN / (Sh::kHalves ? 32 : 16); ++kk)
-            tc_mma_ta(tmem, ps + kk * 8, desc_advance(vd, kk * 2048), kIdO, kk > 0 ? 1u : acc0);
+            tc_mma_ta(tmem, ps + kk * 8, desc_advance(vd, kk * 2 * Pl::kGroup), kIdO, kk > 0 ? 1u : acc0);
           if constexpr (Sh::kHalves) {
-            ok = mbar_wait_warp(&prest[i % NS], (i / NS) & 1);
+            ok = mbar_wait_bounded(&prest[vs], vp);
             if (!ok) break;
             tc_fence_after();
 #pragma unroll
             for (int kk = BN / 32; kk < BN / 16; ++kk)
-              tc_mma_ta(tmem, ps + kk * 8, desc_advance(vd, kk * 2048), kIdO, 1u);
+              tc_mma_ta(tmem, ps + kk * 8, desc_advance(vd, kk * 2 * Pl::kGroup), kIdO, 1u);
           }
-          tc_commit_elect(&vdone[i % NS]);
+          tc_commit(&vdone[vs]);
+          if (++vs == NS) vs = 0, vp ^= 1;
+          vb = vb + 1 == NB ? 0 : vb + 1;
         }
-        it += n;
         ++piece;
       }
-      if (!ok && lane == 0) give_up();
+      if (!ok) give_up();
     }
+    __syncwarp();
   } else if (warp < 4) {
     // ------------------------------------------------------------------ guards of V
     // In a block where some running row's positions end, non-finite values of positions that no
     // row sees are cleared; those that a row does see are reported to the softmax.
     const int gw = warp - 2;
+    if constexpr (kPaged<P>)
+      if (gw == 0 && lane == 0) paged_splits_clear(p);
     int it = 0;
     bool ok = true;
+#pragma unroll 1
     while (ok && !__any_sync(0xffffffffu, *abort_flag) && walk.next(p, cum, shares, a)) {
+      if constexpr (kPaged<P>)
+        if (gw == 0 && lane == 0) paged_split(p, cum, shares, walk, a);
       int least = 0x7fffffff, most = 0;  // positions every running row sees; positions any row sees
+#pragma unroll 1
       for (int i = lane; i < kTm; i += 32) {
         const int lim = attn_row(p, req, a.tile, i).lim;
         most = max(most, lim);
@@ -454,31 +498,36 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         AttnWalk ahead = walk;
         AttnPiece nx;
         if (ahead.next(p, cum, shares, nx))
+#pragma unroll 1
           for (int i = gw * 32 + lane; i < kTm; i += 64) {
             const AttnRow r = attn_row(p, req, nx.tile, i);
             if (r.lim <= 0) continue;
             const __nv_bfloat16* src = q_row<D>(p, req, nx, r);
+#pragma unroll 1
             for (int d = 0; d < D; d += 64)
               asm volatile("prefetch.global.L2 [%0];" ::"l"(src + d));
           }
       }
-      for (int blk = a.blk0; ok && blk < a.blk1; ++blk, ++it) {
+#pragma unroll 1
+      const int blk1 = a.blk1;
+#pragma unroll 1
+      for (int blk = a.blk0; ok && blk < blk1; ++blk, ++it) {
         const int s = it % NS;
         ok = mbar_wait_warp(&vfull[s], (it / NS) & 1);
         bool seen = false;
         if (blk * BN + BN > least) {
           uint8_t* vt = sv + s * Sh::kTile;
           const int from = max(0, least - blk * BN);
-          // The swizzle keeps a position's 128 bytes of a panel together, so each panel is one run of
-          // 16-byte chunks. An exponent of all ones carries into its half's top bit.
+          // The swizzle keeps a position's 128 bytes of a panel together. An exponent of all ones carries
+          // into its half's top bit.
           const int run = (BN - from) * 8;
           uint32_t any = 0;
 #pragma unroll 1
           for (int j = 0; j < D / 64; ++j) {
-            const uint8_t* base = vt + j * Sh::kPanel + from * 128;
 #pragma unroll
             for (int k = 0; k < BN * 8 / 64; ++k) {
-              const uint4 x = lds128(base + min(k * 64 + gw * 32 + lane, run - 1) * 16);
+              const int i = min(k * 64 + gw * 32 + lane, run - 1);
+              const uint4 x = lds128(vt + j * Pl::kPanel + Pl::at(from + i / 8) + i % 8 * 16);
               any |= (x.x & 0x7f807f80u) + 0x00800080u;
               any |= (x.y & 0x7f807f80u) + 0x00800080u;
               any |= (x.z & 0x7f807f80u) + 0x00800080u;
@@ -486,9 +535,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
           }
           if (__any_sync(0xffffffffu, any & 0x80008000u)) {
+#pragma unroll 1
             for (int j = 0; j < D / 64; ++j)
+#pragma unroll 1
               for (int i = gw * 32 + lane; i < run; i += 64) {
-                uint4* at = reinterpret_cast<uint4*>(vt + j * Sh::kPanel + from * 128 + i * 16);
+                uint4* at = reinterpret_cast<uint4*>(vt + j * Pl::kPanel + Pl::at(from + i / 8) + i % 8 * 16);
                 const uint4 x = *at;
                 if (odd_pair(x.x) || odd_pair(x.y) || odd_pair(x.z) || odd_pair(x.w)) {
                   if (blk * BN + from + i / 8 >= most)
@@ -517,7 +568,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     constexpr int DH = D / 2;
     const int quad = warp & 3, half = (warp - 4) >> 2, row = quad * 32 + lane, st = threadIdx.x & 127;
     const uint32_t trow = tmem + (static_cast<uint32_t>(quad * 32) << 16);
-    const float scale = fabsf(p.scale_log2);
+    const float scale = fmaxf(fabsf(p.scale_log2), 1e-45f);  // so that a masked score is -Inf whatever the scale
     int it = 0;
     // A wait that runs out ends all further waiting, not the walk: whatever happens, a softmax warp
     // goes through the same pieces as the others, which it meets at `meet` and at named barriers.
@@ -547,21 +598,30 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const __nv_bfloat16* src = q_row<D>(p, req, pc, ar);
       // (the paged call keeps more of the piece before: half of a long row at a time, or registers spill)
       constexpr int W = kPaged<P> && D == 256 ? DH / 4 : DH / 2;
+      const uint32_t tq = trow + Sh::kQ + half * (DH / 2);
+      // rows that do not run have read row 0's
+      if (__all_sync(0xffffffffu, (reinterpret_cast<uintptr_t>(src) & 31u) == 0)) {
 #pragma unroll
-      for (int part = 0; part < DH / 2; part += W) {
-        uint32_t w[W];
-        if (__all_sync(0xffffffffu, (reinterpret_cast<uintptr_t>(src) & 31u) == 0)) {
+        for (int part = 0; part < DH / 2; part += W) {
+          uint32_t w[W];
 #pragma unroll
           for (int c = 0; c < W / 8; ++c) load32(src + half * DH + 2 * part + 16 * c, w + 8 * c);
-        } else {
-          const uint16_t* from = reinterpret_cast<const uint16_t*>(src + half * DH + 2 * part);
 #pragma unroll
-          for (int c = 0; c < W; ++c) w[c] = from[2 * c] | static_cast<uint32_t>(from[2 * c + 1]) << 16;
+          for (int c = 0; c < W; ++c) w[c] = ar.lim > 0 ? w[c] ^ flip : 0u;
+          tmem_st<W>(tq + part, w);
         }
-        // rows that do not run have read row 0's
+      } else {
+        const uint16_t* from = reinterpret_cast<const uint16_t*>(src + half * DH);
+#pragma unroll 1
+        for (int part = 0; part < DH / 2; part += 16) {
+          uint32_t w[16];
 #pragma unroll
-        for (int c = 0; c < W; ++c) w[c] = ar.lim > 0 ? w[c] ^ flip : 0u;
-        tmem_st<W>(trow + Sh::kQ + half * (DH / 2) + part, w);
+          for (int c = 0; c < 16; ++c) {
+            w[c] = from[2 * (part + c)] | static_cast<uint32_t>(from[2 * (part + c) + 1]) << 16;
+            w[c] = ar.lim > 0 ? w[c] ^ flip : 0u;
+          }
+          tmem_st16(tq + part, w);
+        }
       }
       tmem_st_wait();
       const int lo = __reduce_min_sync(0xffffffffu, ar.lim > 0 ? ar.lim : 0x7fffffff);
@@ -573,20 +633,100 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       if (lane == 0) mbar_arrive(qready);
       least = min(min(lsm[0], lsm[1]), min(lsm[2], lsm[3]));
     };
+    int lim = 0, slot = 0, tile = 0, head = 0;  // of the piece in work
+    bool whole = false;
+    float mg = -INFINITY, l = 0.f;  // of the group's blocks of it: the last reference, the sum
+    auto output = [&]() {  // what the piece has come to
+      const int lb = it - 1;
+      wait(&vdone[lb % NS], (lb / NS) & 1);
+      tc_fence_after();
+      row_ml[half * kTm + row] = make_float2(mg, l);
+      asm volatile("bar.sync %0, 64;" ::"r"(9 + quad) : "memory");
+      const float2 other = row_ml[(half ^ 1) * kTm + row];
+      // the reference never falls, so the greater one is the last one's
+      const float m = fmaxf(mg, other.x), ref = m == -INFINITY ? 0.f : m;
+      // in the groups' order, whichever of them asks
+      const float w0 = half == 0 ? l * ex2(mg - ref) : other.y * ex2(other.x - ref);
+      const float w1 = half == 0 ? other.y * ex2(other.x - ref) : l * ex2(mg - ref);
+      const float sum = w0 + w1;
+      if (whole) {
+        // All that the row sees: its output itself. Nothing seen, or scores of -Inf alone: zero.
+        const bool empty = m == -INFINITY && sum == sum;
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        const AttnRow out_row = attn_row(p, req, tile, row);
+        const int64_t q_at = attn_q_row(p, req, out_row);
+        const int q_head = head * p.G + out_row.g;
+        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + q_at * p.os + static_cast<int64_t>(q_head) * D;
+        if (p.lse && lim > 0 && half == 0)
+          p.lse[q_at * (p.Hkv * p.G) + q_head] =
+              empty ? -INFINITY : (m + log2f(sum)) * 0.6931471805599453f;
+        if (__all_sync(0xffffffffu, (reinterpret_cast<uintptr_t>(dst) & 31u) == 0)) {
+#pragma unroll 1
+          for (int d = half * DH; d < half * DH + DH; d += 32) {
+            float o[32];
+            tmem_ld32(trow + d, o);
+            uint32_t w[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              w[j] = empty ? 0u : bf16_pair(o[2 * j] * inv, o[2 * j + 1] * inv);
+            if (lim > 0) {
+              store32(dst + d, w);
+              store32(dst + d + 16, w + 8);
+            }
+          }
+        } else {
+#pragma unroll 1
+          for (int d = half * DH; d < half * DH + DH; d += 8) {
+            float o[8];
+            tmem_ld8(trow + d, o);
+            if (lim > 0) {
+#pragma unroll
+              for (int j = 0; j < 8; ++j) dst[d + j] = __float2bfloat16_rn(empty ? 0.f : o[j] * inv);
+            }
+          }
+        }
+      } else {
+        const int64_t at = static_cast<int64_t>(slot) * kTm + row;
+        // The maxima pass over scores that are not numbers, the sum does not. The join takes a maximum of
+        // -Inf for a row that saw nothing, so such a partial says NaN there.
+        if (lim > 0 && half == 0) p.ml[at] = make_float2(sum != sum ? sum : m, sum);
+#pragma unroll 1
+        for (int d = half * DH; d < half * DH + DH; d += 32) {
+          float o[32];
+          tmem_ld32(trow + d, o);
+          if (lim > 0) {
+#pragma unroll
+            for (int j = 0; j < 32; j += 8) store32(p.o + at * D + d + j, o + j);
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(ofree);
+    };
     bool more = walk.next(p, cum, shares, a);
-    if (more) load_q(a);
-    while (more) {
-      const int lim = ar.lim, from_all = least, slot = a.slot;
-      const int blk_end = a.blk1;
+    for (;;) {
+      if (more) load_q(a);
+      if (piece > 0) output();  // of the piece before, while this one's first scores are computed
+      if (!more) break;
+      lim = ar.lim, slot = a.slot, tile = a.tile, head = a.head;
+      whole = kPaged<P> && a.whole;
+      const int from_all = least, blk_end = a.blk1;
       const int n = blk_end - a.blk0, it0 = it;
-      const bool whole = kPaged<P> && a.whole;
-      const int tile = a.tile, head = a.head;
-      float mg = -INFINITY, l = 0.f;  // of the group's blocks: the last reference, the sum
+      mg = -INFINITY, l = 0.f;
       it += (it & 1) ^ half;          // the first of them
+#pragma unroll 1
       for (int blk = a.blk0 + it - it0; blk < blk_end; blk += 2, it += 2) {
         const bool first = it == it0, last = it + 1 == it0 + n;
         const int valid = min(BN, lim - blk * BN);  // positions of the block this row sees
         bool full = __all_sync(0xffffffffu, valid >= BN);
+        float mo = -INFINITY;  // the reference after the block before, from the other group
+        const auto others = [&]() {
+          if (first) return;
+          asm volatile("bar.sync %0, 64;" ::"r"(1 + 4 * (half ^ 1) + quad) : "memory");
+          mo = row_m[(half ^ 1) * kTm + row];
+        };
+        if (kPaged<P>) others();  // while the scores are on their way (verify rows: registers spill)
         wait(&kdone[it % NS], (it / NS) & 1);
         uint32_t lost = 0;  // pages of the block that are not there
         if constexpr (kPaged<P>) {
@@ -594,23 +734,26 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           full = full && lost == 0;
         }
         tc_fence_after();
-        const uint32_t ts = trow + Sh::kS + half * BN;
+        const uint32_t ts = trow + Sh::kS + (it % NB) * BN;
+        const auto mask = [&](float* x, int c0) {  // 32 scores
+          if constexpr (kPaged<P>) {
+            __syncwarp();  // (and with it a branch: a block that every row sees pays for no selects)
+            const uint32_t bits = seen_bits(p, valid, lost, c0);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) x[j] = bits >> j & 1 ? x[j] : -INFINITY;
+            __syncwarp();
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) x[j] = c0 + j < valid ? x[j] : -INFINITY;
+          }
+        };
         float v[64], raw = -INFINITY;
 #pragma unroll
         for (int c0 = 0; c0 < BN; c0 += 64) {
           tmem_ld64(ts + c0, v);
           if (!full) {
-            if constexpr (kPaged<P>) {
-#pragma unroll
-              for (int h = 0; h < 64; h += 32) {
-                const uint32_t bits = seen_bits(p, valid, lost, c0 + h);
-#pragma unroll
-                for (int j = 0; j < 32; ++j) v[h + j] = bits >> j & 1 ? v[h + j] : -INFINITY;
-              }
-            } else {
-#pragma unroll
-              for (int j = 0; j < 64; ++j) v[j] = c0 + j < valid ? v[j] : -INFINITY;
-            }
+            mask(v, c0);
+            mask(v + 32, c0 + 32);
           }
           float mx[4] = {raw, v[1], v[2], v[3]};
           mx[0] = max3(mx[0], v[0], v[4]);
@@ -619,11 +762,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           raw = max3(max3(mx[0], mx[1], v[63]), mx[2], mx[3]);
         }
         const float top = raw == -INFINITY ? -INFINITY : raw * scale;
-        float mo = -INFINITY;  // the reference after the block before, from the other group
-        if (!first) {
-          asm volatile("bar.sync %0, 64;" ::"r"(1 + 4 * (half ^ 1) + quad) : "memory");
-          mo = row_m[(half ^ 1) * kTm + row];
-        }
+        if (!kPaged<P>) others();
         const bool grow = top > mo + kLazy;  // from -Inf: at the first score
         const float m = grow ? top : mo;
         if (!last) {
@@ -661,8 +800,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
         };
         if (Sh::kHalves) settle();
-        // A weight is 2^(scale s - ref): two at a time in packed arithmetic. Of 128 scores the last 32 stay
-        // in registers; the others are read again, before weights take their columns.
+        // A weight is 2^(scale s - ref): two at a time in packed arithmetic. A masked score is -Inf. Of 128
+        // scores the last 32 stay in registers; the others are read again, before weights take their columns.
         unsigned long long sum[2] = {0ull, 0ull};
         const unsigned long long scale2 = pack2(__float_as_uint(scale), __float_as_uint(scale));
         const unsigned long long ref2 = pack2(__float_as_uint(-ref), __float_as_uint(-ref));
@@ -670,11 +809,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         for (int c0 = 0; c0 < BN; c0 += 32) {
           float again[32];
           const bool kept = BN == 64 || c0 + 32 == BN;
-          if (!kept) tmem_ld32(ts + c0, again);
+          if (!kept) {
+            tmem_ld32(ts + c0, again);
+            if (!full) mask(again, c0);
+          }
           const float* x = kept ? v + (c0 & 32) : again;
-          uint32_t bits = 0;
-          if constexpr (kPaged<P>)
-            if (!full) bits = seen_bits(p, valid, lost, c0);
           uint32_t w[16];
 #pragma unroll
           for (int j = 0; j < 32; j += 2) {
@@ -682,11 +821,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             ffma2_acc(y, pack2(__float_as_uint(x[j]), __float_as_uint(x[j + 1])), scale2);
             uint32_t lo, hi;
             asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(y));
-            float e0 = ex2(__uint_as_float(lo)), e1 = ex2(__uint_as_float(hi));
-            if (!full) {
-              e0 = (kPaged<P> ? bits >> j & 1 : c0 + j < valid) ? e0 : 0.f;
-              e1 = (kPaged<P> ? bits >> (j + 1) & 1 : c0 + j + 1 < valid) ? e1 : 0.f;
-            }
+            const float e0 = ex2(__uint_as_float(lo)), e1 = ex2(__uint_as_float(hi));
             asm("add.rn.f32x2 %0, %0, %1;"
                 : "+l"(sum[(j / 2) & 1])
                 : "l"(pack2(__float_as_uint(e0), __float_as_uint(e1))));
@@ -711,9 +846,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           for (int d = 0; d < D; d += 8) {
             float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
             if (!first) tmem_ld8(trow + d, o);
+#pragma unroll 1
             for (int pos = from; pos < BN; ++pos) {
               const uint4 x = *reinterpret_cast<const uint4*>(
-                  vt + (d / 64) * Sh::kPanel + pos * 128 + ((((d / 8) & 7) ^ (pos & 7)) << 4));
+                  vt + (d / 64) * Pl::kPanel + Pl::at(pos) + ((((d / 8) & 7) ^ (pos & 7)) << 4));
               uint32_t pw;  // this position's weight and its neighbour's
               asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n\t"
                            "tcgen05.wait::ld.sync.aligned;"
@@ -743,9 +879,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             tmem_st_wait();
           }
           bar_group();
+#pragma unroll 1
           for (int i = st; i < nrow * (D / 8); i += kGroupThreads) {
             const int pos = from + i / (D / 8), ch = i % (D / 8);
-            uint32_t* at = reinterpret_cast<uint32_t*>(vt + (ch / 8) * Sh::kPanel + pos * 128 +
+            uint32_t* at = reinterpret_cast<uint32_t*>(vt + (ch / 8) * Pl::kPanel + Pl::at(pos) +
                                                        (((ch & 7) ^ (pos & 7)) << 4));
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -770,74 +907,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         mg = m;
       }
       it = it0 + n;
-      // every product with this piece's Q is complete: the next one's can take its place, and its first
-      // scores be computed, while this piece's output is written
-      const int lb = it - 1;
-      wait(&kdone[lb % NS], (lb / NS) & 1);
+      // every product with this piece's Q is complete: the next one's can take its place
+      wait(&kdone[(it - 1) % NS], ((it - 1) / NS) & 1);
       ++piece;
       more = walk.next(p, cum, shares, a);
-      if (more) load_q(a);
-      // the piece's partial
-      wait(&vdone[lb % NS], (lb / NS) & 1);
-      tc_fence_after();
-      row_ml[half * kTm + row] = make_float2(mg, l);
-      asm volatile("bar.sync %0, 64;" ::"r"(9 + quad) : "memory");
-      const float2 other = row_ml[(half ^ 1) * kTm + row];
-      // the reference never falls, so the greater one is the last one's
-      const float m = fmaxf(mg, other.x), ref = m == -INFINITY ? 0.f : m;
-      // in the groups' order, whichever of them asks
-      const float w0 = half == 0 ? l * ex2(mg - ref) : other.y * ex2(other.x - ref);
-      const float w1 = half == 0 ? other.y * ex2(other.x - ref) : l * ex2(mg - ref);
-      const float sum = w0 + w1;
-      if (whole) {
-        // All that the row sees: its output itself. Nothing seen, or scores of -Inf alone: zero.
-        const bool empty = m == -INFINITY && sum == sum;
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        const AttnRow out_row = attn_row(p, req, tile, row);
-        const int64_t q_at = attn_q_row(p, req, out_row);
-        const int q_head = head * p.G + out_row.g;
-        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + q_at * p.os + static_cast<int64_t>(q_head) * D;
-        if (p.lse && lim > 0 && half == 0)
-          p.lse[q_at * (p.Hkv * p.G) + q_head] =
-              empty ? -INFINITY : (m + log2f(sum)) * 0.6931471805599453f;
-        const bool aligned = __all_sync(0xffffffffu, (reinterpret_cast<uintptr_t>(dst) & 31u) == 0);
-#pragma unroll 1
-        for (int d = half * DH; d < half * DH + DH; d += 32) {
-          float o[32];
-          tmem_ld32(trow + d, o);
-          uint32_t w[16];
-#pragma unroll
-          for (int j = 0; j < 16; ++j)
-            w[j] = empty ? 0u : bf16_pair(o[2 * j] * inv, o[2 * j + 1] * inv);
-          if (lim > 0) {
-            if (aligned) {
-              store32(dst + d, w);
-              store32(dst + d + 16, w + 8);
-            } else {
-              uint16_t* to = reinterpret_cast<uint16_t*>(dst + d);
-#pragma unroll
-              for (int j = 0; j < 32; ++j) to[j] = static_cast<uint16_t>(w[j / 2] >> (16 * (j & 1)));
-            }
-          }
-        }
-      } else {
-        const int64_t at = static_cast<int64_t>(slot) * kTm + row;
-        // The maxima pass over scores that are not numbers, the sum does not. The join takes a maximum of
-        // -Inf for a row that saw nothing, so such a partial says NaN there.
-        if (lim > 0 && half == 0) p.ml[at] = make_float2(sum != sum ? sum : m, sum);
-#pragma unroll 1
-        for (int d = half * DH; d < half * DH + DH; d += 32) {
-          float o[32];
-          tmem_ld32(trow + d, o);
-          if (lim > 0) {
-#pragma unroll
-            for (int j = 0; j < 32; j += 8) store32(p.o + at * D + d + j, o + j);
-          }
-        }
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(ofree);
     }
   }
   tc_fence_before();
@@ -852,7 +925,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 // Dynamic shared memory of a call, and its launch.
 template <typename P, int D>
 spec_status tc_launch(const P& p, const AttnMaps& m, int grid, cudaStream_t stream) {
-  using Sh = Shape<D>;
+  using Sh = Shape<D, kPaged<P>>;
   static SmemAllowance allowed;
   const int smem = Sh::kFixed + kTcSmall<P> + 24 * kTm + static_cast<int>(attn_plan_bytes(p)) + 1024;
   if (allow_dynamic_smem(attn_tc_kernel<P, D>, smem, allowed) != cudaSuccess) return SPEC_ERR_CUDA;

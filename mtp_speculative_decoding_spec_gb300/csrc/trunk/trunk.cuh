@@ -38,6 +38,7 @@ __device__ __forceinline__ void copy_async16(void* dst, const void* src) {
 __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity) {
   if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
   const uint64_t t0 = globaltimer_ns();
+#pragma unroll 1
   for (uint32_t n = 1;; ++n) {
     if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
     if ((n & 63u) == 0 && __any_sync(0xffffffffu, globaltimer_ns() - t0 > 2000000000ull)) return false;
@@ -124,21 +125,25 @@ __host__ __device__ inline size_t attn_plan_bytes(const AttnParams& p) {
 // cum[0..items] in shared memory: cost of one KV head before each item, in blocks; after it the
 // requests' numbers. By the whole block (a barrier at the end). Every CTA works it out for itself from
 // the lengths on the device, so no launch comes before and no host reads them.
-__device__ __forceinline__ AttnReq* attn_plan(const AttnParams& p, int32_t* cum) {
+static __device__ __forceinline__ AttnReq* attn_plan(const AttnParams& p, int32_t* cum) {
   const int tid = threadIdx.x, nt = blockDim.x, per = p.R * p.G;
   AttnReq* req = reinterpret_cast<AttnReq*>(cum + p.items + 1);
   const auto cost = [&p](int n, int own) { return n > 0 ? (n + p.bn - 1) / p.bn + p.over[own] : 0; };
+#pragma unroll 1
   for (int b = tid; b < p.B; b += nt) {
     const AttnReq r = attn_req(p, b);
     req[b] = r;
     const int c = r.rows > 0 ? cost(attn_own(p, r, r.rows), 1) : 0;
+#pragma unroll 1
     for (int j = 0; j < p.nown; ++j) cum[p.npi + b * p.nown + j + 1] = c;
   }
   __syncthreads();
+#pragma unroll 1
   for (int i = tid >> 5; i < p.npi; i += nt >> 5) {  // a warp to an item
     const int span = p.tm * p.grp;
     const int b0 = i * span / per, b1 = min(p.B - 1, ((i + 1) * span - 1) / per);
     int n = 0;
+#pragma unroll 1
     for (int b = b0 + (tid & 31); b <= b1; b += 32)
       if (req[b].rows > 0) n = max(n, req[b].prefix);
     n = __reduce_max_sync(0xffffffffu, n);
@@ -148,6 +153,7 @@ __device__ __forceinline__ AttnReq* attn_plan(const AttnParams& p, int32_t* cum)
   __syncthreads();
   if (tid < 32) {
     int base = 0;
+#pragma unroll 1
     for (int i0 = 1; i0 <= p.items; i0 += 32) {
       const int i = i0 + tid;
       int v = i <= p.items ? cum[i] : 0;
@@ -231,21 +237,18 @@ __device__ __forceinline__ AttnShares attn_shares(const P& p, const int32_t* cum
   return s;
 }
 
-// Where a unit's partials begin and how many there are (c0: the group, or of the rest the CTA, that has its
-// first block), and the slot of the partial of this CTA's piece.
-__device__ __forceinline__ int2 attn_unit(const AttnParams& p, const AttnShares& s, int u, int c0, int n) {
-  return make_int2(u < s.u1 ? p.grp * (c0 + u) : s.base1 + c0 + u - s.u1, n);
-}
+// The slot of the partial of a CTA's piece of unit u.
 __device__ __forceinline__ int attn_slot(const AttnParams& p, const AttnShares& s, int u, int cta, int) {
   return u < s.u1 ? p.grp * (cta / p.grp + u) + cta % p.grp : s.base1 + cta + u - s.u1;
 }
 
 // Each unit's first slot and number of partials (the slots of a group's tile lie `grp` apart), for the
 // join; by CTA 0 of the kernel that computes them.
-template <typename P>
-__device__ __forceinline__ void attn_write_units(const P& p, const int32_t* cum, const AttnShares& s) {
-  const int npi = attn_group_items(p, cum);
-  for (int u = threadIdx.x; u < attn_items(p, cum) * p.Hkv; u += blockDim.x) {
+static __device__ __forceinline__ void attn_write_units(const AttnParams& p, const int32_t* cum,
+                                                 const AttnShares& s) {
+  const int npi = p.npi;
+#pragma unroll 1
+  for (int u = threadIdx.x; u < p.items * p.Hkv; u += blockDim.x) {
     const int item = u / p.Hkv, head = u - item * p.Hkv;
     const int cost = cum[item + 1] - cum[item];
     int2 v = make_int2(0, 0);
@@ -254,10 +257,10 @@ __device__ __forceinline__ void attn_write_units(const P& p, const int32_t* cum,
       const int64_t first = x + p.over[item >= npi], last = x + cost - 1;  // places of its first and last block
       if (u < s.u1) {
         const int c0 = static_cast<int>(first / s.sp);
-        v = attn_unit(p, s, u, c0, static_cast<int>(last / s.sp) - c0 + 1);
+        v = make_int2(p.grp * (c0 + u), static_cast<int>(last / s.sp) - c0 + 1);
       } else {
         const int c0 = s.single_cta(first - s.wp);
-        v = attn_unit(p, s, u, c0, s.single_cta(last - s.wp) - c0 + 1);
+        v = make_int2(s.base1 + c0 + u - s.u1, s.single_cta(last - s.wp) - c0 + 1);
       }
     }
     p.units[u] = v;
@@ -282,6 +285,7 @@ struct AttnWalk {
     left = x1 - x;
     if (left <= 0) return;
     int lo = 0, hi = attn_items(p, cum);  // cum[lo] Hkv <= x < cum[hi] Hkv
+#pragma unroll 1
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
       if (static_cast<int64_t>(cum[mid]) * p.Hkv <= x)
@@ -313,6 +317,7 @@ struct AttnWalk {
   }
   template <typename P>
   __device__ __forceinline__ bool next(const P& p, const int32_t* cum, const AttnShares& s, AttnPiece& a) {
+#pragma unroll 1
     for (;;) {
       if (left <= 0) {
         if (!group) return false;
@@ -388,38 +393,6 @@ __device__ __forceinline__ int attn_tile_req(const AttnParams& p, int tile) { re
 // all of is written without the join.
 template <typename P>
 constexpr bool kPaged = false;
-
-// One output row of the join: its unit over the prefix and its own (first slot, number of partials), its
-// place in their tiles; whether the row is written, and the slot of a partial.
-struct AttnJoinRow {
-  int2 u0, u1;
-  int at0, at1;
-  bool write;
-};
-__device__ __forceinline__ int attn_join_slot(const AttnParams& p, const AttnJoinRow& j, int i) {
-  return i < j.u0.y ? j.u0.x + i * p.grp : j.u1.x + i - j.u0.y;
-}
-__device__ __forceinline__ AttnJoinRow attn_join_row(const AttnParams& p, int64_t row, int qh) {
-  AttnJoinRow j;
-  const int head = qh / p.G, g = qh - head * p.G;
-  const int b = static_cast<int>(row / p.R), r = static_cast<int>(row) - b * p.R;
-  const int s = (b * p.R + r) * p.G + g, x = r * p.G + g;
-  const AttnReq rq = attn_req(p, b);
-  j.u0 = make_int2(0, 0);
-  const int t0 = s / p.tm;
-  if (p.npt > 0) j.u0 = __ldcg(p.units + t0 / p.grp * p.Hkv + head);
-  j.u1 = __ldcg(p.units + (p.npi + b * p.nown + x / p.tm) * p.Hkv + head);
-  j.u0.x += t0 % p.grp;
-  if (rq.prefix == 0) j.u0.y = 0;
-  if (r >= rq.rows) j.u0.y = j.u1.y = 0;
-  j.at0 = s % p.tm;
-  j.at1 = x % p.tm;
-  j.write = true;
-  return j;
-}
-__device__ __forceinline__ int64_t attn_join_rows(const AttnParams& p) {
-  return static_cast<int64_t>(p.B) * p.R;
-}
 
 cudaError_t attn_simt_launch(const AttnParams& p, spec_dtype dtype, int grid, cudaStream_t stream);
 cudaError_t attn_join_launch(const AttnParams& p, spec_dtype dtype, int sms, cudaStream_t stream);

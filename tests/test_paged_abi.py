@@ -182,7 +182,7 @@ def test_register_budget_and_no_spills(spec):
     each, and no kernel spills."""
     logs = glob.glob(os.path.join(ROOT, "mtp_speculative_decoding_spec_gb300", "_build", "paged", "*.ptxas.log"))
     threads = {"append_kernel": 128, "paged_commit_kernel": 256, "attn_simt_kernel": 256,
-               "attn_join_kernel": 256, "attn_tc_kernel": 384}
+               "attn_tc_kernel": 384, "paged_join_kernel": 256}
     seen = set()
     for path in logs:
         name = None
