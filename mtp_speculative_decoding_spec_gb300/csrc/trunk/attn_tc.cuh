@@ -5,11 +5,11 @@
 // Per block of kBn positions: S = Q K^T (Q in TMEM, 128 rows x kBn), a row's softmax by one thread
 // (TMEM lane = row, no shuffles), the weights as bf16 back into the columns of S, O += P V with P
 // in TMEM too and V as it lies in the cache (rows of positions: the B operand is N-major).
-//   * warp 0 loads K and V blocks by TMA; Q is gathered by the softmax threads into TMEM, so that
+//   * warp 0 loads K and V blocks by TMA (a paged cache: warp 3 loads V); Q is gathered by the softmax threads into TMEM, so that
 //     its 128 rows are not read from shared memory again for every block;
 //   * warp 1 issues the MMAs: S of the blocks after i goes out before O of block i, so the tensor pipe works
 //     on them while the softmax works on the others (two S buffers, or four);
-//   * warps 4..7 and 8..11 do the softmax of the blocks in turns; warps 2 and 3 watch V (below). The
+//   * warps 4..7 and 8..11 do the softmax of the blocks in turns; warp 2 (and 3) watch V (below). The
 //     reference a row's weights are taken against moves only when the row's maximum has grown by more
 //     than 2^8 (the weights stay below 256 and their sum and O are fp32, so nothing is lost), which makes
 //     rescaling O in TMEM rare.
@@ -17,7 +17,7 @@
 // sum is taken in fp32 before that.
 //
 // A position that some row does not see has weight 0 in that row, and 0 times what lies there must
-// be 0. In blocks where any running row's positions end, two guard warps therefore look through V as
+// be 0. In blocks where any running row's positions end, guard warps therefore look through V as
 // it lands, ahead of the softmax: non-finite values that no row sees are cleared, and where a row
 // does see one, that row's share of it is added by hand and the value cleared for the tensor cores.
 //
@@ -40,7 +40,11 @@
 namespace spec {
 
 constexpr int kTm = 128;
-constexpr int kTcThreads = 12 * 32;  // producer, MMA and two guard warps, eight softmax warps
+constexpr int kTcThreads = 12 * 32;  // producers and guards (three), MMA, eight softmax warps
+template <int N>
+struct Number {
+  static constexpr int value = N;
+};
 constexpr int kGroupThreads = 128;  // a softmax group
 template <typename P>
 constexpr int kTcSmall = kPaged<P> ? 1280 : 512;  // bytes of barriers and flags
@@ -252,12 +256,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ofree + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* o_init = abort_flag + 1;      // [2] O holds something before the piece's first MMA on it
-  volatile int* odd = abort_flag + 3;         // [NS][2]: a row sees a non-finite V of the stage
+  volatile int* odd = abort_flag + 3;         // [NS][guards]: a row sees a non-finite V of the stage
   int* least_sm = const_cast<int*>(odd + 2 * NS);  // [2][4] per quarter of the rows
   // [2 NS] of a K block, which of its pages are not there. Written when the block's stage is free, which may
   // be before every warp has read an earlier block's word: two stages' worth.
   volatile uint32_t* gone = reinterpret_cast<volatile uint32_t*>(least_sm + 8);
-  int* pages = const_cast<int*>(reinterpret_cast<volatile int*>(gone + 2 * NS));  // [128] of the table's entries
+  // [K, V][64]: 32 of the table's entries
+  int* page_ring = const_cast<int*>(reinterpret_cast<volatile int*>(gone + 2 * NS));
   float* row_m = reinterpret_cast<float*>(smem + Sh::kFixed + kTcSmall<P>);  // [2][128] each group's last reference
   float2* row_ml = reinterpret_cast<float2*>(row_m + 2 * kTm);       // [2][128] and sum, at a piece's end
   int32_t* cum = reinterpret_cast<int32_t*>(row_ml + 2 * kTm);
@@ -269,8 +274,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       mbar_init(&kdone[s], 1);
       mbar_init(&vfull[s], 1);
       mbar_init(&vdone[s], 1);
-      mbar_init(&vok[s], 2);
-      mbar_init(&pready[s], 6);
+      mbar_init(&vok[s], kPaged<P> ? 1 : 2);
+      mbar_init(&pready[s], kPaged<P> ? 5 : 6);
       mbar_init(&prest[s], 4);
     }
     mbar_init(qready, 8);
@@ -303,82 +308,108 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   else
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
 
-  if (warp == 0) {
-    // ------------------------------------------------------------------ TMA producer
-    // One elected thread waits and issues, as below; the others help it to the page table's entries.
-    const bool leader = elect_one();
-    int gi = 0, ks = 0, kp = 1, ki = 0, vs = 0, vp = 1, vi = 0;  // the next K and V blocks: stage, its phase, number
-    bool ok = true;
-    // K runs as far ahead as the MMAs take it
-    auto next_k = [&](int left_k, int left_v) { return left_k > 0 && left_k > left_v - NB; };
-    auto room = [&](uint64_t* empty, int s, int phase, int i) { return i < NS || mbar_wait_bounded(&empty[s], phase); };
+  constexpr int kGuards = kPaged<P> ? 1 : 2;
+  if (warp == 0 || (warp == 3 && kPaged<P>)) {
+    // ------------------------------------------------------------------ TMA producers
+    // One elected thread waits and issues, as below. A wait and a copy take it 300 to 600 cycles.
+    if constexpr (kPaged<P>) {
+      // K by one warp and V by another: one for both was what a block took longest for (2,048 rows of 128
+      // dims over 61,440 positions 1,004 us, 707 so). The other lanes help to the page table's entries.
+      const bool leader = elect_one(), is_k = warp == 0;
+      uint8_t* const tiles = is_k ? sk : sv;
+      uint64_t* const full = is_k ? kfull : vfull;
+      uint64_t* const done = is_k ? kdone : vdone;
+      int gi = 0, s = 0, phase = 1, i = 0;  // the next block: its stage, the stage's phase, its number
+      bool ok = true;
+      auto issue_to = [&]() {  // the stage of the next block, once it is free
+        if (i >= NS && !mbar_wait_bounded(&done[s], phase)) return false;
+        return true;
+      };
+      auto step = [&]() {
+        if (++s == NS) s = 0, phase ^= 1;
+        ++i;
+      };
+      while (__all_sync(0xffffffffu, ok && !*abort_flag) && walk.next(p, cum, shares, a)) {
+        const int panel = a.head * (D / 64), blk0 = a.blk0, blk1 = a.blk1;
+        int left = blk1 - blk0;
+        {
+          const int b = attn_tile_req(p, a.tile), ps = p.c.page_size;
+          const CUtensorMap* map = is_k ? &maps.ok : &maps.ov;
+          const int32_t* table = p.c.table + static_cast<int64_t>(b) * p.c.table_stride;
+          const auto entry = [&](int j) { return j < p.c.max_pages ? __ldg(table + j) : -1; };
+          int* const pages = page_ring + (is_k ? 0 : 64);
+          int j = blk0 * BN / ps, at = blk0 * BN - j * ps;
+          // entries 32 at a time, the next ones on their way
+          int e = entry((j & ~31) + lane);
 #pragma unroll 1
-    while (__all_sync(0xffffffffu, ok && !*abort_flag) && walk.next(p, cum, shares, a)) {
-      const int panel = a.head * (D / 64), blk0 = a.blk0, blk1 = a.blk1;
-      int left_k = blk1 - blk0, left_v = left_k;
-      if constexpr (kPaged<P>) {
-        const int b = attn_tile_req(p, a.tile), ps = p.c.page_size;
-        const int32_t* table = p.c.table + static_cast<int64_t>(b) * p.c.table_stride;
-        const auto entry = [&](int j) { return j < p.c.max_pages ? __ldg(table + j) : -1; };
-        const int per = ps >= BN ? 1 : BN / ps, bytes = Sh::kTile / per;  // pages of a block
-        int kj = blk0 * BN / ps, k_at = blk0 * BN - kj * ps, vj = kj, v_at = k_at;
-        // entries 32 at a time, the next ones on their way; a ring of four times as many, for V behind K
-        int e = entry((kj & ~31) + lane);
+          for (int w = j & ~31; left > 0; w += 32) {
+            __syncwarp();
+            pages[lane] = static_cast<unsigned>(e) < static_cast<unsigned>(p.c.n_pages) ? e : p.c.n_pages;
+            e = entry(w + 32 + lane);
+            __syncwarp();
+            if (leader) {
+              // blocks of whole pages in pages of 8 to 32 positions, or a block and a part of a page
+              const auto blocks = [&](auto number) {
+                constexpr int PER = decltype(number)::value;
 #pragma unroll 1
-        for (int w = kj & ~31; left_v > 0; w += 32) {
-          __syncwarp();
-          pages[(w + lane) & 127] = static_cast<unsigned>(e) < static_cast<unsigned>(p.c.n_pages) ? e : p.c.n_pages;
-          e = entry(w + 32 + lane);
-          __syncwarp();
-          if (leader) {
-#pragma unroll 1
-            while (ok && left_v > 0) {
-              if (next_k(left_k, left_v)) {
-                if (kj + per > w + 32) break;
-                ok = room(kdone, ks, kp, ki);
-                if (!ok) break;
-                uint32_t lost = 0;
-#pragma unroll 1
-                for (int m = 0; m < per; ++m)
-                  lost |= static_cast<uint32_t>(pages[(kj + m) & 127] == p.c.n_pages) << m;
-                gone[gi] = lost;  // seen with the block: the scores' wait for it comes before the softmax's for them
-                if (++gi == 2 * NS) gi = 0;
-                mbar_arrive_expect_tx(&kfull[ks], Sh::kTile);
-#pragma unroll 1
-                for (int m = 0; m < per; ++m)
-                  tma_load_page(sk + ks * Sh::kTile + m * bytes, &maps.ok, panel, k_at >> 3, pages[(kj + m) & 127],
-                                &kfull[ks]);
-                k_at += BN;
-                if (k_at >= ps) kj += per, k_at = 0;
-                if (++ks == NS) ks = 0, kp ^= 1;
-                ++ki;
-                --left_k;
-              } else {
-                ok = room(vdone, vs, vp, vi);
-                if (!ok) break;
-                mbar_arrive_expect_tx(&vfull[vs], Sh::kTile);
-#pragma unroll 1
-                for (int m = 0; m < per; ++m)
-                  tma_load_page(sv + vs * Sh::kTile + m * bytes, &maps.ov, panel, v_at >> 3, pages[(vj + m) & 127],
-                                &vfull[vs]);
-                v_at += BN;
-                if (v_at >= ps) vj += per, v_at = 0;
-                if (++vs == NS) vs = 0, vp ^= 1;
-                ++vi;
-                --left_v;
-              }
+                while (left > 0 && j < w + 32) {
+                  int page[PER];
+                  uint32_t lost = 0;
+#pragma unroll
+                  for (int m = 0; m < PER; ++m) {
+                    page[m] = pages[j - w + m];
+                    lost |= static_cast<uint32_t>(page[m] == p.c.n_pages) << m;
+                  }
+                  ok = issue_to();
+                  if (!ok) break;
+                  if (is_k) {
+                    gone[gi] = lost;  // seen with the block: the scores' wait for it comes before the softmax's for them
+                    if (++gi == 2 * NS) gi = 0;
+                  }
+                  mbar_arrive_expect_tx(&full[s], Sh::kTile);
+#pragma unroll
+                  for (int m = 0; m < PER; ++m)
+                    tma_load_page(tiles + s * Sh::kTile + m * (Sh::kTile / PER), map, panel, at >> 3, page[m], &full[s]);
+                  at += BN;
+                  if (at >= ps) j += PER, at = 0;
+                  step();
+                  --left;
+                }
+              };
+              if (ps >= BN)
+                blocks(Number<1>());
+              else if (ps == 8)
+                blocks(Number<BN / 8>());
+              else if (ps == 16)
+                blocks(Number<BN / 16>());
+              else
+                blocks(Number<BN / 32>());
             }
+            left = __reduce_min_sync(0xffffffffu, leader ? (ok ? left : 0) : 0x7fffffff);
           }
-          left_v = __reduce_min_sync(0xffffffffu, leader ? (ok ? left_v : 0) : 0x7fffffff);
         }
-      } else if (leader) {
+      }
+      if (leader) {
+        if (!ok) give_up();
+        // Leave nothing in flight: the last loads of every stage have landed.
+#pragma unroll 1
+        for (int k = max(0, i - NS); k < i; ++k) mbar_wait_bounded(&full[k % NS], (k / NS) & 1);
+      }
+      __syncwarp();
+    } else if (elect_one()) {
+      int ks = 0, kp = 1, ki = 0, vs = 0, vp = 1, vi = 0;  // the next K and V blocks: stage, its phase, number
+      bool ok = true;
+      auto room = [&](uint64_t* empty, int s, int phase, int i) { return i < NS || mbar_wait_bounded(&empty[s], phase); };
+      while (ok && !*abort_flag && walk.next(p, cum, shares, a)) {
+        const int panel = a.head * (D / 64), blk1 = a.blk1;
+        int left_k = blk1 - a.blk0, left_v = left_k;
         const bool pre = a.tile < p.npt;
         const int b = pre ? 0 : attn_tile_req(p, a.tile);
         const CUtensorMap* mk = pre ? &maps.pk : &maps.ok;
         const CUtensorMap* mv = pre ? &maps.pv : &maps.ov;
 #pragma unroll 1
-        while (ok && left_v > 0) {
-          const bool is_k = next_k(left_k, left_v);
+        while (left_v > 0) {
+          const bool is_k = left_k > 0 && left_k > left_v - NB;  // K runs as far ahead as the MMAs take it
           ok = is_k ? room(kdone, ks, kp, ki) : room(vdone, vs, vp, vi);
           if (!ok) break;
           mbar_arrive_expect_tx(is_k ? &kfull[ks] : &vfull[vs], Sh::kTile);
@@ -395,8 +426,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
         }
       }
-    }
-    if (leader) {
       if (!ok) give_up();
       // Leave nothing in flight: the last loads of every stage have landed.
 #pragma unroll 1
@@ -476,15 +505,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // ------------------------------------------------------------------ guards of V
     // In a block where some running row's positions end, non-finite values of positions that no
     // row sees are cleared; those that a row does see are reported to the softmax.
-    const int gw = warp - 2;
     if constexpr (kPaged<P>)
-      if (gw == 0 && lane == 0) paged_splits_clear(p);
+      if (lane == 0) paged_splits_clear(p);
+    const int gw = warp - 2;
     int it = 0;
     bool ok = true;
 #pragma unroll 1
     while (ok && !__any_sync(0xffffffffu, *abort_flag) && walk.next(p, cum, shares, a)) {
       if constexpr (kPaged<P>)
-        if (gw == 0 && lane == 0) paged_split(p, cum, shares, walk, a);
+        if (lane == 0) paged_split(p, cum, shares, walk, a);
       int least = 0x7fffffff, most = 0;  // positions every running row sees; positions any row sees
 #pragma unroll 1
       for (int i = lane; i < kTm; i += 32) {
@@ -499,7 +528,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         AttnPiece nx;
         if (ahead.next(p, cum, shares, nx))
 #pragma unroll 1
-          for (int i = gw * 32 + lane; i < kTm; i += 64) {
+          for (int i = gw * 32 + lane; i < kTm; i += 32 * kGuards) {
             const AttnRow r = attn_row(p, req, nx.tile, i);
             if (r.lim <= 0) continue;
             const __nv_bfloat16* src = q_row<D>(p, req, nx, r);
@@ -524,9 +553,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           uint32_t any = 0;
 #pragma unroll 1
           for (int j = 0; j < D / 64; ++j) {
-#pragma unroll
-            for (int k = 0; k < BN * 8 / 64; ++k) {
-              const int i = min(k * 64 + gw * 32 + lane, run - 1);
+#pragma unroll 16
+            for (int k = 0; k < BN * 8 / (32 * kGuards); ++k) {
+              const int i = min((k * kGuards + gw) * 32 + lane, run - 1);
               const uint4 x = lds128(vt + j * Pl::kPanel + Pl::at(from + i / 8) + i % 8 * 16);
               any |= (x.x & 0x7f807f80u) + 0x00800080u;
               any |= (x.y & 0x7f807f80u) + 0x00800080u;
@@ -538,7 +567,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll 1
             for (int j = 0; j < D / 64; ++j)
 #pragma unroll 1
-              for (int i = gw * 32 + lane; i < run; i += 64) {
+              for (int i = gw * 32 + lane; i < run; i += 32 * kGuards) {
                 uint4* at = reinterpret_cast<uint4*>(vt + j * Pl::kPanel + Pl::at(from + i / 8) + i % 8 * 16);
                 const uint4 x = *at;
                 if (odd_pair(x.x) || odd_pair(x.y) || odd_pair(x.z) || odd_pair(x.w)) {
@@ -553,7 +582,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         seen = __any_sync(0xffffffffu, seen);
         if (lane == 0) {
-          odd[2 * s + gw] = seen;
+          odd[kGuards * s + gw] = seen;
           mbar_arrive(&vok[s]);
           mbar_arrive(&pready[s]);
         }
@@ -776,7 +805,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           const bool rescale = !first && __any_sync(0xffffffffu, grow);
           if (blk * BN + BN > from_all) {
             wait(&vok[sg], (it / NS) & 1);
-            by_hand = odd[2 * sg] | odd[2 * sg + 1];
+            by_hand = odd[kGuards * sg] | odd[kGuards * sg + kGuards - 1];
           }
           if (rescale || by_hand) {
             // O of the blocks before is complete (the MMA of this one waits for this thread)
