@@ -81,7 +81,8 @@ spec_status plan_check(int32_t B, int64_t rows, const spec_paged_cache* c, const
   const int64_t tiles = rows * G / w.tm + B;  // each request's last tile may not be full
   if (tiles > (w.tc ? kPagedMaxTiles : kPagedSimtMaxTiles)) return SPEC_ERR_UNSUPPORTED;
   const int64_t cap = static_cast<int64_t>(c->max_pages) * c->page_size;
-  if (tiles * (cap / w.bn + 1 + kAttnOverPre) >= (int64_t(1) << 31)) return SPEC_ERR_UNSUPPORTED;
+  // the dealing counts blocks of all heads in 31 bits, grid - 1 more when it rounds up
+  if (tiles * (cap / w.bn + 1 + kAttnOverPre) >= ((int64_t(1) << 31) - 1024) / c->kv_heads) return SPEC_ERR_UNSUPPORTED;
   w.tiles = static_cast<int>(tiles);
   return SPEC_OK;
 }

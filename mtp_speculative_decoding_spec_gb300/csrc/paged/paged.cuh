@@ -135,6 +135,12 @@ __device__ __forceinline__ int paged_groups(const PagedParams& p, int rows, int 
   const int n = paged_tiles(p, rows);
   return p.grp > 1 && n >= p.grp && base + rows >= p.group_min ? n / p.grp : 0;
 }
+__device__ __forceinline__ int64_t attn_div(const PagedParams&, int64_t x, int64_t y) {  // all below 2^31
+  return static_cast<uint32_t>(x) / static_cast<uint32_t>(y);
+}
+__device__ __forceinline__ int attn_part(const PagedParams&, int64_t x, int64_t all, int grid) {
+  return min(grid, static_cast<int>(static_cast<float>(x) / static_cast<float>(all) * static_cast<float>(grid) + 0.01f));
+}
 // What a request's tile sees: up to its last row's position.
 __device__ __forceinline__ int paged_sees(const PagedParams& p, const PagedReq& r, int tile) {
   const int last = min(r.rows, ((tile + 1) * p.tm - 1) / p.G + 1);
@@ -298,7 +304,8 @@ __device__ __forceinline__ void paged_split(const PagedParams& p, const int32_t*
   // the place of its last block
   const int64_t last = static_cast<int64_t>(cum[walk.item]) * p.Hkv + static_cast<int64_t>(a.head + 1) * cost - 1;
   const bool group = walk.item * p.Hkv + a.head < s.u1;
-  const int n = group ? static_cast<int>(last / s.sp) - cta / p.grp + 1 : s.single_cta(last - s.wp) - cta + 1;
+  const int n = group ? static_cast<int>(attn_div(p, last, s.sp)) - cta / p.grp + 1
+                      : s.single_cta(p, last - s.wp) - cta + 1;
   *reinterpret_cast<int4*>(p.splits + 2 * cta + !group) = make_int4(n, group ? p.grp : 1, a.tile, a.head);
 }
 

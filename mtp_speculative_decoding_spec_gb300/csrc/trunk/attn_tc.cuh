@@ -41,13 +41,17 @@ namespace spec {
 
 constexpr int kTm = 128;
 constexpr int kTcThreads = 12 * 32;  // producers and guards (three), MMA, eight softmax warps
+constexpr int kRing = 16;  // pieces of a CTA that its roles are told of ahead
+struct PieceNote {
+  int tile, head, blk0, blk1, slot, whole;  // tile -1: no more
+};
 template <int N>
 struct Number {
   static constexpr int value = N;
 };
 constexpr int kGroupThreads = 128;  // a softmax group
 template <typename P>
-constexpr int kTcSmall = kPaged<P> ? 1280 : 512;  // bytes of barriers and flags
+constexpr int kTcSmall = kPaged<P> ? 1792 : 512;  // bytes of barriers and flags
 // Registers a thread: launched with 168 (64,512 in all); the first four warps give to the softmax's
 // eight: 128 x 152 + 256 x 176 = 64,512. (104 and 200 spill in the guards: 214 us for 191.)
 constexpr int kFewRegs = 152, kSoftRegs = 176;
@@ -263,6 +267,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   volatile uint32_t* gone = reinterpret_cast<volatile uint32_t*>(least_sm + 8);
   // [K, V][64]: 32 of the table's entries
   int* page_ring = const_cast<int*>(reinterpret_cast<volatile int*>(gone + 2 * NS));
+  uint64_t* ring_full = reinterpret_cast<uint64_t*>(page_ring + 128);
+  PieceNote* ring = reinterpret_cast<PieceNote*>(ring_full + kRing);
   float* row_m = reinterpret_cast<float*>(smem + Sh::kFixed + kTcSmall<P>);  // [2][128] each group's last reference
   float2* row_ml = reinterpret_cast<float2*>(row_m + 2 * kTm);       // [2][128] and sum, at a piece's end
   int32_t* cum = reinterpret_cast<int32_t*>(row_ml + 2 * kTm);
@@ -283,6 +289,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     mbar_init(&meet[1], 4);
     mbar_init(&meet[2], 8);
     mbar_init(ofree, 8);
+    if constexpr (kPaged<P>)
+      for (int s = 0; s < kRing; ++s) mbar_init(&ring_full[s], 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -293,14 +301,52 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
-  const AttnShares shares = attn_shares(p, cum);
-  if (!kPaged<P> && blockIdx.x == 0) attn_write_units(p, cum, shares);
-  AttnWalk walk;
-  walk.start(p, cum, shares);
-  AttnPiece a;
   auto give_up = [&]() {
     atomicOr(&p.hdr->error, ERR_TC_WAIT);
     *abort_flag = 1;
+  };
+  AttnShares shares;
+  AttnWalk walk;
+  AttnPiece a;
+  if (!kPaged<P> || warp == 0) {  // (paged: the others are told, below)
+    shares = attn_shares(p, cum);
+    if (!kPaged<P> && blockIdx.x == 0) attn_write_units(p, cum, shares);
+    walk.start(p, cum, shares);
+  }
+  // The next piece. Of a paged cache the K producer's warp, which is ahead of the others by as many blocks as it
+  // has stages, walks for all and leaves what it finds in a ring; a piece has a block at least, so that no role
+  // is further behind than the ring is long: K(i) is loaded after the scores of block i - NS, those come after the
+  // product of i - NS - NB, and that after the softmax.
+  static_assert(!kPaged<P> || NS + NB + 2 <= kRing);
+  int told = 0;
+  auto tell = [&](bool more) {  // by one lane
+    PieceNote& note = ring[told % kRing];
+    note.tile = more ? a.tile : -1;
+    note.head = a.head, note.blk0 = a.blk0, note.blk1 = a.blk1, note.slot = a.slot, note.whole = a.whole;
+    mbar_arrive(&ring_full[told % kRing]);
+  };
+  auto next_piece = [&](bool one = false) {  // by a whole warp, or by one thread
+    if constexpr (!kPaged<P>) {
+      return walk.next(p, cum, shares, a);
+    } else if (warp == 0) {
+      const bool more = walk.next(p, cum, shares, a);
+      if (lane == 0) {
+        if (told == 0) paged_splits_clear(p);
+        if (more) paged_split(p, cum, shares, walk, a);
+        tell(more);
+      }
+      ++told;
+      return more;
+    } else {
+      bool more = mbar_wait_bounded(&ring_full[told % kRing], (told / kRing) & 1);
+      if (!more) give_up();
+      const PieceNote note = ring[told % kRing];
+      ++told;
+      a.tile = note.tile, a.head = note.head, a.blk0 = note.blk0, a.blk1 = note.blk1, a.slot = note.slot;
+      a.whole = note.whole != 0;
+      more = more && note.tile >= 0;
+      return one ? more : static_cast<bool>(__all_sync(0xffffffffu, more));
+    }
   };
 
   if (warp < 4)
@@ -329,9 +375,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (++s == NS) s = 0, phase ^= 1;
         ++i;
       };
-      while (__all_sync(0xffffffffu, ok && !*abort_flag) && walk.next(p, cum, shares, a)) {
+      bool more = true;
+      while (__all_sync(0xffffffffu, ok && !*abort_flag) && (more = next_piece())) {
         const int panel = a.head * (D / 64), blk0 = a.blk0, blk1 = a.blk1;
         int left = blk1 - blk0;
+        if (is_k && told > 1)  // its queries, towards L2: the softmax takes them when it is done with what is before
+#pragma unroll 1
+          for (int row = lane; row < kTm; row += 32) {
+            const AttnRow r = attn_row(p, req, a.tile, row);
+            if (r.lim <= 0) continue;
+            const __nv_bfloat16* src = q_row<D>(p, req, a, r);
+            for (int d = 0; d < D; d += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(src + d));
+          }
         {
           const int b = attn_tile_req(p, a.tile), ps = p.c.page_size;
           const CUtensorMap* map = is_k ? &maps.ok : &maps.ov;
@@ -389,6 +444,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
         }
       }
+      if (is_k && more && lane == 0) tell(false);  // a wait ran out
       if (leader) {
         if (!ok) give_up();
         // Leave nothing in flight: the last loads of every stage have landed.
@@ -400,7 +456,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       int ks = 0, kp = 1, ki = 0, vs = 0, vp = 1, vi = 0;  // the next K and V blocks: stage, its phase, number
       bool ok = true;
       auto room = [&](uint64_t* empty, int s, int phase, int i) { return i < NS || mbar_wait_bounded(&empty[s], phase); };
-      while (ok && !*abort_flag && walk.next(p, cum, shares, a)) {
+      while (ok && !*abort_flag && next_piece()) {
         const int panel = a.head * (D / 64), blk1 = a.blk1;
         int left_k = blk1 - a.blk0, left_v = left_k;
         const bool pre = a.tile < p.npt;
@@ -462,7 +518,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         return true;
       };
 #pragma unroll 1
-      while (ok && !*abort_flag && walk.next(p, cum, shares, a)) {
+      while (ok && !*abort_flag && next_piece(true)) {
         const int n = a.blk1 - a.blk0;
         ok = mbar_wait_bounded(qready, piece & 1);
         tc_fence_after();
@@ -505,15 +561,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // ------------------------------------------------------------------ guards of V
     // In a block where some running row's positions end, non-finite values of positions that no
     // row sees are cleared; those that a row does see are reported to the softmax.
-    if constexpr (kPaged<P>)
-      if (lane == 0) paged_splits_clear(p);
     const int gw = warp - 2;
     int it = 0;
     bool ok = true;
 #pragma unroll 1
-    while (ok && !__any_sync(0xffffffffu, *abort_flag) && walk.next(p, cum, shares, a)) {
-      if constexpr (kPaged<P>)
-        if (lane == 0) paged_split(p, cum, shares, walk, a);
+    while (ok && !__any_sync(0xffffffffu, *abort_flag) && next_piece()) {
       int least = 0x7fffffff, most = 0;  // positions every running row sees; positions any row sees
 #pragma unroll 1
       for (int i = lane; i < kTm; i += 32) {
@@ -523,7 +575,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
       least = __reduce_min_sync(0xffffffffu, least);
       most = __reduce_max_sync(0xffffffffu, most);
-      {  // the next piece's queries, towards L2
+      if constexpr (!kPaged<P>) {  // the next piece's queries, towards L2
         AttnWalk ahead = walk;
         AttnPiece nx;
         if (ahead.next(p, cum, shares, nx))
@@ -733,7 +785,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(ofree);
     };
-    bool more = walk.next(p, cum, shares, a);
+    bool more = next_piece();
     for (;;) {
       if (more) load_q(a);
       if (piece > 0) output();  // of the piece before, while this one's first scores are computed
@@ -939,7 +991,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       // every product with this piece's Q is complete: the next one's can take its place
       wait(&kdone[(it - 1) % NS], ((it - 1) / NS) & 1);
       ++piece;
-      more = walk.next(p, cum, shares, a);
+      more = next_piece();
     }
   }
   tc_fence_before();

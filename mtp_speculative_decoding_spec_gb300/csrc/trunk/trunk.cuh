@@ -183,6 +183,13 @@ __device__ __forceinline__ int attn_single_tile(const AttnParams& p, const int32
   return item < p.npi ? item : item - p.npi + p.npt;
 }
 
+// Quotients of places: 64 bits, or 32 where the host has made sure that they do (a division of 64 bits takes
+// a third of a microsecond, and the dealing has six of them before the first block).
+__device__ __forceinline__ int64_t attn_div(const AttnParams&, int64_t x, int64_t y) { return x / y; }
+__device__ __forceinline__ int attn_part(const AttnParams&, int64_t x, int64_t all, int grid) {
+  return static_cast<int>(x * grid / all);  // of the grid, what x is of all
+}
+
 // How the costs are dealt out: the groups' part [0, wp), `sp` to each group, and the rest up to w: `s1`
 // to each of the `in` CTAs in groups, `s2` to each of the others, which have that much more room; where
 // the second part's units and slots begin.
@@ -192,18 +199,19 @@ struct AttnShares {
   __device__ __forceinline__ int64_t single_at(int cta) const {  // where a CTA's part of the rest begins
     return cta < in ? s1 * cta : s1 * in + s2 * (cta - in);
   }
-  __device__ __forceinline__ int single_cta(int64_t x) const {  // which CTA has place x of the rest
-    return static_cast<int>(x < s1 * in ? x / s1 : in + (x - s1 * in) / s2);
+  template <typename P>
+  __device__ __forceinline__ int single_cta(const P& p, int64_t x) const {  // which CTA has place x of the rest
+    return static_cast<int>(x < s1 * in ? attn_div(p, x, s1) : in + attn_div(p, x - s1 * in, s2));
   }
   // With so many groups: the shares, and what the CTA with the most then has. A second unit's start
   // comes on top where the groups' CTAs take some of the rest too.
   template <typename P>
   __device__ __forceinline__ int64_t split(const P& p, int groups, int grid) {
     in = groups * p.grp;
-    sp = (wp + groups - 1) / groups;
+    sp = attn_div(p, wp + groups - 1, groups);
     const int64_t rest = w - wp, more = rest - sp * (grid - in);
-    s1 = more > 0 ? (more + grid - 1) / grid : 0;
-    s2 = more > 0 ? s1 + sp : in < grid ? (rest + grid - in - 1) / (grid - in) : 0;
+    s1 = more > 0 ? attn_div(p, more + grid - 1, grid) : 0;
+    s2 = more > 0 ? s1 + sp : in < grid ? attn_div(p, rest + grid - in - 1, grid - in) : 0;
     return s1 > 0 ? sp + s1 + p.over[1] : max(sp, s2);
   }
 };
@@ -220,7 +228,7 @@ __device__ __forceinline__ AttnShares attn_shares(const P& p, const int32_t* cum
     s.wp = static_cast<int64_t>(cum[npi]) * p.Hkv;
     const int64_t all = s.wp * p.grp + s.w - s.wp;
     const int most = grid / p.grp;
-    groups = all > 0 ? max(1, static_cast<int>(s.wp * grid / all)) : 1;
+    groups = all > 0 ? max(1, attn_part(p, s.wp, all, grid)) : 1;
     const int64_t fewer = s.split(p, groups, grid);
     if (groups < most) {
       AttnShares more = s;
@@ -230,7 +238,7 @@ __device__ __forceinline__ AttnShares attn_shares(const P& p, const int32_t* cum
       }
     }
   } else {
-    s.s1 = s.s2 = (s.w + grid - 1) / grid;
+    s.s1 = s.s2 = attn_div(p, s.w + grid - 1, grid);
   }
   s.u1 = p.grp > 1 ? npi * p.Hkv : 0;
   s.base1 = p.grp * (groups + s.u1);
@@ -259,8 +267,8 @@ static __device__ __forceinline__ void attn_write_units(const AttnParams& p, con
         const int c0 = static_cast<int>(first / s.sp);
         v = make_int2(p.grp * (c0 + u), static_cast<int>(last / s.sp) - c0 + 1);
       } else {
-        const int c0 = s.single_cta(first - s.wp);
-        v = make_int2(s.base1 + c0 + u - s.u1, s.single_cta(last - s.wp) - c0 + 1);
+        const int c0 = s.single_cta(p, first - s.wp);
+        v = make_int2(s.base1 + c0 + u - s.u1, s.single_cta(p, last - s.wp) - c0 + 1);
       }
     }
     p.units[u] = v;
@@ -295,7 +303,7 @@ struct AttnWalk {
     }
     const int64_t rel = x - static_cast<int64_t>(cum[lo]) * p.Hkv;
     item = lo;
-    head = static_cast<int>(rel / (cum[lo + 1] - cum[lo]));
+    head = static_cast<int>(attn_div(p, rel, cum[lo + 1] - cum[lo]));
     at = static_cast<int>(rel - static_cast<int64_t>(head) * (cum[lo + 1] - cum[lo]));
   }
   template <typename P>
