@@ -82,7 +82,7 @@ spec_status plan_check(int32_t B, int64_t rows, const spec_paged_cache* c, const
   if (tiles > (w.tc ? kPagedMaxTiles : kPagedSimtMaxTiles)) return SPEC_ERR_UNSUPPORTED;
   const int64_t cap = static_cast<int64_t>(c->max_pages) * c->page_size;
   // the dealing counts blocks of all heads in 31 bits, grid - 1 more when it rounds up
-  if (tiles * (cap / w.bn + 1 + kAttnOverPre) >= ((int64_t(1) << 31) - 1024) / c->kv_heads) return SPEC_ERR_UNSUPPORTED;
+  if (tiles * (cap / w.bn + 1 + kPagedOver) >= ((int64_t(1) << 31) - 1024) / c->kv_heads) return SPEC_ERR_UNSUPPORTED;
   w.tiles = static_cast<int>(tiles);
   return SPEC_OK;
 }
@@ -208,8 +208,7 @@ spec_status spec_paged_attention(int32_t B, const int32_t* cu_rows, int64_t rows
   for (p.page_shift = 0; w.tc && p.page_shift < 31 && (1 << p.page_shift) < c->page_size; ++p.page_shift) {
   }
   if (c->page_size >= w.bn) p.page_shift = 31;
-  p.over[0] = w.tc ? kAttnOverPre : kAttnSimtOver;
-  p.over[1] = w.tc ? kAttnOver : kAttnSimtOver;
+  p.over[0] = p.over[1] = w.tc ? kPagedOver : kAttnSimtOver;
   p.q = d->q;
   p.qs = d->q_stride;
   p.out = d->out;

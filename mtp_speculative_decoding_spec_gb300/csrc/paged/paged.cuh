@@ -58,8 +58,16 @@ __device__ __forceinline__ PagedRows paged_rows(const int32_t* cu, const int32_t
 constexpr int kPagedMaxCtas = 512;
 
 // Tiles of a request that walk the same positions side by side (152 SMs are 19 eights), and from how many
-// positions on.
+// positions on. 2,048 rows of 16 heads on 4 of 256 dims over 61,440 positions, groups of 1, 4, 8, 16: 1,469,
+// 1,231, 1,192, 1,197 us; prompts of 1,000 and 2,311 rows among shorter ones 64 to 65 with all of them. From
+// 0, 2,048, 8,192, 32,768 positions on: those prompts 80, 73, 65, 65 us, four times 512 rows over 30,000
+// 364, 364, 364, 485.
 constexpr int kPagedGroup = 8, kPagedGroupMin = 8192;
+
+// `over` on the tensor cores (trunk.cuh), for grouped tiles (4 to 16: no difference) and single ones: 6, 9, 12,
+// 16, 20 the prompts above 70.7, 65.7, 65.3, 63.7, 65.4 us, 32 requests of 8 rows over 15,360 positions 309.5,
+// 312.0, 311.2, 313.5, 316.6.
+constexpr int kPagedOver = 12;
 
 struct AppendParams {
   PagedLayer c;
