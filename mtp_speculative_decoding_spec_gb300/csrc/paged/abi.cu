@@ -17,7 +17,7 @@ spec_status cache_check(int32_t B, const spec_paged_cache* c) {
   if (c->layers < 1 || c->kv_heads < 1 || c->head_dim < 8 || c->head_dim % 8 != 0 || c->page_size < 1 ||
       c->n_pages < 1 || c->max_pages < 1 || c->table_stride < c->max_pages)
     return SPEC_ERR_INVALID;
-  if (B > kPagedMaxB || c->head_dim > 256 || c->kv_heads > 65536 || c->layers > 65536) return SPEC_ERR_UNSUPPORTED;
+  if (B > kPagedMaxB || c->head_dim > 256 || c->kv_heads > kPagedMaxHeads || c->layers > 65536) return SPEC_ERR_UNSUPPORTED;
   if (c->n_pages >= (int64_t(1) << 31) || static_cast<int64_t>(c->max_pages) * c->page_size > kAttnMaxPos)
     return SPEC_ERR_UNSUPPORTED;
   return SPEC_OK;
@@ -208,6 +208,8 @@ spec_status spec_paged_attention(int32_t B, const int32_t* cu_rows, int64_t rows
   for (p.page_shift = 0; w.tc && p.page_shift < 31 && (1 << p.page_shift) < c->page_size; ++p.page_shift) {
   }
   if (c->page_size >= w.bn) p.page_shift = 31;
+  p.unit_more = w.tc ? kPagedUnitMore : -1;
+  p.unit_part = w.tc && c->head_dim >= 128 ? kPagedUnitPart : 0;
   p.over[0] = p.over[1] = w.tc ? kPagedOver : kAttnSimtOver;
   p.q = d->q;
   p.qs = d->q_stride;

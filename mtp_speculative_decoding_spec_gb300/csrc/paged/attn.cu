@@ -42,9 +42,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
   pdl_wait();
   const auto rows_of = [&](int b) { return paged_rows(p.cu_rows, p.n_rows, p.rows, b); };
   for (int i = threadIdx.x; i < 2 * ctas; i += kJoinThreads) {
-    const int4 u = __ldcg(reinterpret_cast<const int4*>(p.splits + i));
-    const int tile = u.z;
-    first[i + 1] = u.x > 0 ? min(p.tm, rows_of(attn_tile_req(p, tile)).runs * p.G - (tile >> kTileReqBits) * p.tm) : 0;
+    first[i + 1] = paged_split_of(__ldcg(reinterpret_cast<const int4*>(p.splits + i))).count;
   }
   if (threadIdx.x == 0) first[0] = 0;
   __syncthreads();
@@ -80,12 +78,12 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
       else
         hi = mid;
     }
-    const int4 u = __ldcg(reinterpret_cast<const int4*>(p.splits + lo));
+    const PagedSplit u = paged_split_of(__ldcg(reinterpret_cast<const int4*>(p.splits + lo)));
     const int at = t - first[lo], c0 = lo >> 1, part = 2 * (lo & 1);
     float m = -INFINITY, l = 0.f;
     float acc[2][4] = {};
 #pragma unroll 1
-    for (int i0 = w0; i0 < u.x; i0 += kInFlight * nw) {
+    for (int i0 = w0; i0 < u.n; i0 += kInFlight * nw) {
       float2 mlv[kInFlight];
       float4 ov[kInFlight][2];
 #pragma unroll
@@ -93,8 +91,8 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
         const int i = i0 + nw * j;
         mlv[j] = make_float2(-INFINITY, 0.f);
         ov[j][0] = ov[j][1] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (i < u.x) {
-          const int64_t s = static_cast<int64_t>(4 * (c0 + i * u.y) + part + (i == 0)) * p.tm + at;
+        if (i < u.n) {
+          const int64_t s = static_cast<int64_t>(4 * (c0 + i * u.step) + part + (i == 0)) * p.tm + at;
           mlv[j] = __ldcg(p.ml + s);
           const float4* o = reinterpret_cast<const float4*>(p.o + s * p.D);
           if (lane < nv) ov[j][0] = __ldcg(o + lane);
@@ -164,9 +162,9 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
     if (!few || warp == 0) {
       const bool empty = m == -INFINITY;  // nothing seen, or scores of -Inf alone: zero
       const float inv = empty || l == 0.f ? 0.f : 1.f / l;
-      const int x = (u.z >> kTileReqBits) * p.tm + at, r = x / p.G;
-      const int64_t row = rows_of(attn_tile_req(p, u.z)).start + r;
-      const int qh = u.w * p.G + x - r * p.G;
+      const int x = u.tile * p.tm + at, r = x / p.G;
+      const int64_t row = static_cast<int64_t>(u.start) + r;
+      const int qh = u.head * p.G + x - r * p.G;
       T* dst = static_cast<T*>(p.out) + row * p.os + static_cast<int64_t>(qh) * p.D;
 #pragma unroll
       for (int h = 0; h < 2; ++h)

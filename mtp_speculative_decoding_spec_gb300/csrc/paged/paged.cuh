@@ -8,7 +8,7 @@
 
 namespace spec {
 
-constexpr int kPagedMaxB = 512;
+constexpr int kPagedMaxB = 512, kPagedMaxHeads = 65536;
 constexpr int kPagedMaxTiles = 4096, kPagedSimtMaxTiles = 12288;  // four bytes each in shared memory
 
 // One layer of a paged cache.
@@ -68,6 +68,13 @@ constexpr int kPagedGroup = 8, kPagedGroupMin = 8192;
 // 16, 20 the prompts above 70.7, 65.7, 65.3, 63.7, 65.4 us, 32 requests of 8 rows over 15,360 positions 309.5,
 // 312.0, 311.2, 313.5, 316.6.
 constexpr int kPagedOver = 12;
+// On the tensor cores, what a whole unit may cost above an equal share of all before units are cut instead: so
+// many blocks, which is what a cut costs, and where a request has no more than a tile and 128 dims or more the
+// share's so-many-th part, since then HBM is the limit and fewer CTAs draw as much. 32 requests of 8 rows over
+// 1,000, 4,000 and 15,360 positions of 256 dims whole and cut: 33, 87, 290 and 38, 94, 309 us; 128 dims over
+// 15,360 158 and 169; 64 dims, which HBM does not limit, 132 and 119; two rows over 2,000 35 and 16. On the CUDA
+// cores nothing is gained (fp32, over 500 positions: 121 both).
+constexpr int kPagedUnitMore = 8, kPagedUnitPart = 4;
 
 struct AppendParams {
   PagedLayer c;
@@ -116,6 +123,7 @@ struct PagedParams : AttnParams {
   PagedLayer c;
   const int32_t* cu_rows;
   int64_t rows;
+  int unit_more, unit_part;  // attn_by_units (-1: never; part 0: none)
   int group_min;          // positions from which a request's tiles are grouped
   int page_shift;         // tensor cores: positions (log2) of a block's part on one page, 31 where that is all
   PagedSplit* splits;     // [2 CTAs]
@@ -127,16 +135,16 @@ __device__ __forceinline__ int64_t paged_offset(const PagedParams& p, int b, int
   return paged_offset(p.c, b, pos);
 }
 
-// cum[0..items], then the counts of grouped and of all items, then the requests.
+// cum[0..items], then the counts of grouped and of all items and the costliest one's cost, then the requests.
 __host__ __device__ inline size_t attn_plan_bytes(const PagedParams& p) {
-  return sizeof(int32_t) * (p.items + 3) + sizeof(PagedReq) * p.B;
+  return sizeof(int32_t) * (p.items + 4) + sizeof(PagedReq) * p.B;
 }
 __device__ __forceinline__ int attn_group_items(const PagedParams& p, const int32_t* cum) {
   return cum[p.items + 1];
 }
 __device__ __forceinline__ int attn_items(const PagedParams& p, const int32_t* cum) { return cum[p.items + 2]; }
 __device__ __forceinline__ const PagedReq* paged_reqs(const PagedParams& p, const int32_t* cum) {
-  return reinterpret_cast<const PagedReq*>(cum + p.items + 3);
+  return reinterpret_cast<const PagedReq*>(cum + p.items + 4);
 }
 __device__ __forceinline__ int paged_tiles(const PagedParams& p, int rows) { return (rows * p.G + p.tm - 1) / p.tm; }
 __device__ __forceinline__ int paged_groups(const PagedParams& p, int rows, int base) {
@@ -148,6 +156,14 @@ __device__ __forceinline__ int64_t attn_div(const PagedParams&, int64_t x, int64
 }
 __device__ __forceinline__ int attn_part(const PagedParams&, int64_t x, int64_t all, int grid) {
   return min(grid, static_cast<int>(static_cast<float>(x) / static_cast<float>(all) * static_cast<float>(grid) + 0.01f));
+}
+// A unit to a CTA, where there are CTAs for all of them and the costliest is no more than `unit_more` above an
+// equal share: then no unit is cut and the join has nothing to do.
+__device__ __forceinline__ bool attn_by_units(const PagedParams& p, const int32_t* cum, int64_t share) {
+  const int items = attn_items(p, cum);
+  const int64_t more = p.unit_more + (p.unit_part > 0 && items <= p.B ? share / p.unit_part : 0);
+  return attn_group_items(p, cum) == 0 && items <= static_cast<int>(gridDim.x) / p.Hkv &&
+         cum[p.items + 3] <= share + more;
 }
 // What a request's tile sees: up to its last row's position.
 __device__ __forceinline__ int paged_sees(const PagedParams& p, const PagedReq& r, int tile) {
@@ -222,11 +238,12 @@ static __device__ __noinline__ const PagedReq* attn_plan(const PagedParams& p, i
   __syncthreads();
   if (tid < 32) {
     const int items = cum[p.items + 2];
-    int base = 0;
+    int base = 0, most = 0;
 #pragma unroll 1
     for (int i0 = 1; i0 <= items; i0 += 32) {
       const int i = i0 + lane;
       int v = i <= items ? cum[i] : 0;
+      most = max(most, v);
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int x = __shfl_up_sync(0xffffffffu, v, o);
@@ -236,6 +253,8 @@ static __device__ __noinline__ const PagedReq* attn_plan(const PagedParams& p, i
       if (i <= items) cum[i] = v;
       base = __shfl_sync(0xffffffffu, v, 31);
     }
+    most = __reduce_max_sync(0xffffffffu, most);
+    if (lane == 0) cum[p.items + 3] = most;
   }
   __syncthreads();
   return req;
@@ -296,14 +315,29 @@ __device__ __forceinline__ int attn_slot(const PagedParams&, const AttnShares& s
   return 4 * cta + (u < s.u1 ? 0 : 2) + (blk0 == 0);
 }
 
-// What the join has to know of a unit that begins in a CTA's share and ends in another's: its number of
-// partials, the CTAs between them, its tile and head. A CTA writes its two (of the groups' part and of the
+// What the join has to know of a unit that begins in a CTA's share and ends in another's, in 16 bytes: its
+// number of partials and the CTAs from one to the next, its request's first row, its place among the request's
+// tiles, its head and its number of rows (x = r G + g). A CTA writes its two (of the groups' part and of the
 // rest), by one thread: clear() first, then every piece.
 struct PagedSplit {
-  int n, step, tile, head;
+  uint16_t n, step;
+  int start, tile;
+  uint16_t head, count;
 };
+static_assert(sizeof(PagedSplit) == 16 && kPagedMaxCtas < 65536 && kPagedMaxHeads <= 65536);
+__device__ __forceinline__ int4 paged_split_bits(const PagedSplit& s) {
+  return make_int4(s.n | static_cast<int>(static_cast<uint32_t>(s.step) << 16), s.start, s.tile,
+                   s.head | static_cast<int>(static_cast<uint32_t>(s.count) << 16));
+}
+__device__ __forceinline__ PagedSplit paged_split_of(const int4& v) {
+  PagedSplit s;
+  s.n = static_cast<uint16_t>(v.x), s.step = static_cast<uint16_t>(static_cast<uint32_t>(v.x) >> 16);
+  s.start = v.y, s.tile = v.z;
+  s.head = static_cast<uint16_t>(v.w), s.count = static_cast<uint16_t>(static_cast<uint32_t>(v.w) >> 16);
+  return s;
+}
 __device__ __forceinline__ void paged_splits_clear(const PagedParams& p) {
-  for (int i = 0; i < 2; ++i) *reinterpret_cast<int4*>(p.splits + 2 * blockIdx.x + i) = make_int4(0, 1, 0, 0);
+  for (int i = 0; i < 2; ++i) *reinterpret_cast<int4*>(p.splits + 2 * blockIdx.x + i) = make_int4(0, 0, 0, 0);
 }
 __device__ __forceinline__ void paged_split(const PagedParams& p, const int32_t* cum, const AttnShares& s,
                                             const AttnWalk& walk, const AttnPiece& a) {
@@ -314,7 +348,12 @@ __device__ __forceinline__ void paged_split(const PagedParams& p, const int32_t*
   const bool group = walk.item * p.Hkv + a.head < s.u1;
   const int n = group ? static_cast<int>(attn_div(p, last, s.sp)) - cta / p.grp + 1
                       : s.single_cta(p, last - s.wp) - cta + 1;
-  *reinterpret_cast<int4*>(p.splits + 2 * cta + !group) = make_int4(n, group ? p.grp : 1, a.tile, a.head);
+  const PagedReq& r = paged_reqs(p, cum)[attn_tile_req(p, a.tile)];
+  PagedSplit out;
+  out.n = static_cast<uint16_t>(n), out.step = static_cast<uint16_t>(group ? p.grp : 1);
+  out.start = r.start, out.tile = a.tile >> kTileReqBits;
+  out.head = static_cast<uint16_t>(a.head), out.count = static_cast<uint16_t>(min(p.tm, r.rows * p.G - out.tile * p.tm));
+  *reinterpret_cast<int4*>(p.splits + 2 * cta + !group) = paged_split_bits(out);
 }
 
 cudaError_t paged_simt_launch(const PagedParams& p, spec_dtype dtype, int grid, cudaStream_t stream);

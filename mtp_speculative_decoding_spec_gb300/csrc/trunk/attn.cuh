@@ -56,6 +56,7 @@ template <typename P, typename T>
 __global__ void __launch_bounds__(kSimtThreads, 1) attn_simt_kernel(const __grid_constant__ P p) {
   extern __shared__ __align__(16) uint8_t smem[];
   pdl_wait();
+  if constexpr (kPaged<P>) pdl_trigger();  // the join's blocks come as these leave, and wait
   const int D = p.D, ld = D + kPad / 4, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int pitch = D * static_cast<int>(sizeof(T)) + kPad, tile_bytes = kSimtBn * pitch;
   uint8_t* kv = smem;                                    // [2][K, V][32][pitch]

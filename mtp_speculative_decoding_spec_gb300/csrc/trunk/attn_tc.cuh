@@ -296,6 +296,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   }
   if (warp == 1) tmem_alloc(tmem_slot, 512);
   pdl_wait();
+  if constexpr (kPaged<P>) pdl_trigger();  // the join's blocks come as these leave, and wait
   const auto* req = attn_plan(p, cum);  // ends with a block barrier
   tc_fence_before();
   __syncthreads();

@@ -190,12 +190,15 @@ __device__ __forceinline__ int attn_part(const AttnParams&, int64_t x, int64_t a
   return static_cast<int>(x * grid / all);  // of the grid, what x is of all
 }
 
+__device__ __forceinline__ bool attn_by_units(const AttnParams&, const int32_t*, int64_t) { return false; }
+
 // How the costs are dealt out: the groups' part [0, wp), `sp` to each group, and the rest up to w: `s1`
 // to each of the `in` CTAs in groups, `s2` to each of the others, which have that much more room; where
 // the second part's units and slots begin.
 struct AttnShares {
   int64_t wp, w, sp, s1, s2;
   int in, u1, base1;
+  bool units;  // instead: a unit to a CTA (a paged cache's call)
   __device__ __forceinline__ int64_t single_at(int cta) const {  // where a CTA's part of the rest begins
     return cta < in ? s1 * cta : s1 * in + s2 * (cta - in);
   }
@@ -242,6 +245,7 @@ __device__ __forceinline__ AttnShares attn_shares(const P& p, const int32_t* cum
   }
   s.u1 = p.grp > 1 ? npi * p.Hkv : 0;
   s.base1 = p.grp * (groups + s.u1);
+  s.units = attn_by_units(p, cum, s.s1);
   return s;
 }
 
@@ -308,8 +312,13 @@ struct AttnWalk {
   }
   template <typename P>
   __device__ __forceinline__ void start(const P& p, const int32_t* cum, const AttnShares& s) {
-    group = static_cast<int>(blockIdx.x) < s.in;
-    if (group) {
+    group = !s.units && static_cast<int>(blockIdx.x) < s.in;
+    if (s.units) {
+      left = at = 0;
+      item = blockIdx.x / p.Hkv;
+      head = blockIdx.x % p.Hkv;
+      if (item < attn_items(p, cum)) left = cum[item + 1] - cum[item];
+    } else if (group) {
       const int64_t x = s.sp * (blockIdx.x / p.grp);
       seek(p, cum, x, min(s.wp, x + s.sp));
     } else {
