@@ -202,6 +202,8 @@ spec_status spec_paged_attention(int32_t B, const int32_t* cu_rows, int64_t rows
   p.D = c->head_dim;
   p.tm = w.tm;
   p.bn = w.bn;
+  while (1 << p.tm_shift < p.tm) ++p.tm_shift;
+  while (1 << p.bn_shift < p.bn) ++p.bn_shift;
   p.items = w.tiles;
   p.grp = w.tc ? kPagedGroup : 1;
   p.group_min = kPagedGroupMin;

@@ -36,34 +36,51 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, const float* v) {
 template <typename T>
 __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_constant__ PagedParams p, int ctas) {
   __shared__ int first[2 * kPagedMaxCtas + 1];  // of the rows before each unit's
+  __shared__ int4 notes[2 * kPagedMaxCtas];
+  __shared__ int sums[kJoinWarps];
   __shared__ float sm_m[kJoinWarps], sm_l[kJoinWarps];
   __shared__ __align__(16) float sm_o[kJoinWarps][kMaxD];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, Hq = p.Hkv * p.G;
   pdl_wait();
   const auto rows_of = [&](int b) { return paged_rows(p.cu_rows, p.n_rows, p.rows, b); };
-  for (int i = threadIdx.x; i < 2 * ctas; i += kJoinThreads) {
-    first[i + 1] = paged_split_of(__ldcg(reinterpret_cast<const int4*>(p.splits + i))).count;
-  }
-  if (threadIdx.x == 0) first[0] = 0;
-  __syncthreads();
-  if (warp == 0) {
-    int base = 0;
-#pragma unroll 1
-    for (int i0 = 1; i0 <= 2 * ctas; i0 += 32) {
-      const int i = i0 + lane;
-      int v = i <= 2 * ctas ? first[i] : 0;
+  PagedRows own = {0, 0, 0};  // the request whose rows this block fills up first, below
+  if (static_cast<int>(blockIdx.x) < p.B) own = rows_of(blockIdx.x);
+  constexpr int kEach = 2 * kPagedMaxCtas / kJoinThreads;
+  int n[kEach], sum = 0;  // a thread's units, and the rows of them and of those before
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int x = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o) v += x;
-      }
-      v += base;
-      if (i <= 2 * ctas) first[i] = v;
-      base = __shfl_sync(0xffffffffu, v, 31);
+  for (int j = 0; j < kEach; ++j) {
+    const int i = threadIdx.x * kEach + j;
+    n[j] = 0;
+    if (i < 2 * ctas) {
+      notes[i] = __ldcg(reinterpret_cast<const int4*>(p.splits + i));
+      n[j] = paged_split_of(notes[i]).count;
     }
+    sum += n[j];
   }
+  int before = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, before, o);
+    if (lane >= o) before += x;
+  }
+  if (lane == 31) sums[warp] = before;
+  before -= sum;
   __syncthreads();
-  const int total = first[2 * ctas];
+  int total = 0;
+#pragma unroll
+  for (int w = 0; w < kJoinWarps; ++w) {
+    if (w < warp) before += sums[w];
+    total += sums[w];
+  }
+  if (total > 0) {
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) {
+      const int i = threadIdx.x * kEach + j;
+      if (i <= 2 * ctas) first[i] = before;
+      before += n[j];
+    }
+    __syncthreads();
+  }
   const bool few = total <= static_cast<int>(gridDim.x);
   const int nw = few ? kJoinWarps : 1, w0 = few ? warp : 0;
   const int nv = p.D / 4;
@@ -78,7 +95,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
       else
         hi = mid;
     }
-    const PagedSplit u = paged_split_of(__ldcg(reinterpret_cast<const int4*>(p.splits + lo)));
+    const PagedSplit u = paged_split_of(notes[lo]);
     const int at = t - first[lo], c0 = lo >> 1, part = 2 * (lo & 1);
     float m = -INFINITY, l = 0.f;
     float acc[2][4] = {};
@@ -180,7 +197,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
   }
 #pragma unroll 1
   for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
-    const PagedRows r = rows_of(b);
+    const PagedRows r = b == static_cast<int>(blockIdx.x) ? own : rows_of(b);
 #pragma unroll 1
     for (int i = r.runs; i < r.owned; ++i) {
       const int64_t row = r.start + i;

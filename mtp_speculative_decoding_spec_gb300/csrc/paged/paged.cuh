@@ -123,6 +123,7 @@ struct PagedParams : AttnParams {
   PagedLayer c;
   const int32_t* cu_rows;
   int64_t rows;
+  int tm_shift, bn_shift;    // log2 of tm and bn
   int unit_more, unit_part;  // attn_by_units (-1: never; part 0: none)
   int group_min;          // positions from which a request's tiles are grouped
   int page_shift;         // tensor cores: positions (log2) of a block's part on one page, 31 where that is all
@@ -146,10 +147,10 @@ __device__ __forceinline__ int attn_items(const PagedParams& p, const int32_t* c
 __device__ __forceinline__ const PagedReq* paged_reqs(const PagedParams& p, const int32_t* cum) {
   return reinterpret_cast<const PagedReq*>(cum + p.items + 4);
 }
-__device__ __forceinline__ int paged_tiles(const PagedParams& p, int rows) { return (rows * p.G + p.tm - 1) / p.tm; }
+__device__ __forceinline__ int paged_tiles(const PagedParams& p, int rows) { return (rows * p.G + p.tm - 1) >> p.tm_shift; }
 __device__ __forceinline__ int paged_groups(const PagedParams& p, int rows, int base) {
   const int n = paged_tiles(p, rows);
-  return p.grp > 1 && n >= p.grp && base + rows >= p.group_min ? n / p.grp : 0;
+  return p.grp > 1 && n >= p.grp && base + rows >= p.group_min ? n / kPagedGroup : 0;
 }
 __device__ __forceinline__ int64_t attn_div(const PagedParams&, int64_t x, int64_t y) {  // all below 2^31
   return static_cast<uint32_t>(x) / static_cast<uint32_t>(y);
@@ -167,7 +168,7 @@ __device__ __forceinline__ bool attn_by_units(const PagedParams& p, const int32_
 }
 // What a request's tile sees: up to its last row's position.
 __device__ __forceinline__ int paged_sees(const PagedParams& p, const PagedReq& r, int tile) {
-  const int last = min(r.rows, ((tile + 1) * p.tm - 1) / p.G + 1);
+  const int last = min(r.rows, (((tile + 1) << p.tm_shift) - 1) / p.G + 1);
   return static_cast<int>(min(p.kcap, static_cast<int64_t>(r.base) + last));
 }
 
@@ -230,10 +231,10 @@ static __device__ __noinline__ const PagedReq* attn_plan(const PagedParams& p, i
     const int n = paged_tiles(p, r.rows), ng = paged_groups(p, r.rows, r.base);
 #pragma unroll 1
     for (int i = lane; i < ng; i += 32)
-      cum[r.g0 + i + 1] = (paged_sees(p, r, (i + 1) * p.grp - 1) + p.bn - 1) / p.bn + p.over[0];
+      cum[r.g0 + i + 1] = (paged_sees(p, r, (i + 1) * p.grp - 1) + p.bn - 1 >> p.bn_shift) + p.over[0];
 #pragma unroll 1
     for (int t = ng * p.grp + lane; t < n; t += 32)
-      cum[r.s0 + t - ng * p.grp + 1] = (paged_sees(p, r, t) + p.bn - 1) / p.bn + p.over[1];
+      cum[r.s0 + t - ng * p.grp + 1] = (paged_sees(p, r, t) + p.bn - 1 >> p.bn_shift) + p.over[1];
   }
   __syncthreads();
   if (tid < 32) {
@@ -296,7 +297,7 @@ __device__ __forceinline__ int attn_group_tile(const PagedParams& p, const int32
 __device__ __forceinline__ AttnRow attn_row(const PagedParams& p, const PagedReq* req, int tile, int i) {
   AttnRow a;
   a.b = attn_tile_req(p, tile);
-  const int x = (tile >> kTileReqBits) * p.tm + i;
+  const int x = ((tile >> kTileReqBits) << p.tm_shift) + i;
   a.r = x / p.G;
   a.g = x - a.r * p.G;
   a.lim = a.r < req[a.b].rows
