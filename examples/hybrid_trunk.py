@@ -2,13 +2,18 @@
 of requests that share a prompt, speculatively: the trunk's token mixers, the LM head with greedy
 acceptance and the commit, all of a cycle on one stream.
 
-    python examples/hybrid_trunk.py [--requests 8] [--prompt 1000] [--drafts 3] [--tokens 64]
+    python examples/hybrid_trunk.py [--requests 8] [--prompt 1000] [--drafts 3] [--tokens 64] [--paged]
 
 What a cycle runs (R = drafts + 1 verify rows a request):
     spec_delta_rows          each delta layer, from the request's live slot into the slots after it
     spec_prefix_attention    the attention layer, over the shared prompt and the request's own cache
     spec_lmhead_verify, spec_accept (one launch up to 8 rows), spec_commit_rollback: the engine
-and the prompt once: spec_delta_prefill per delta layer. Embedding, projections, norms and the
+and the prompt once: spec_delta_prefill per delta layer. With --paged the attention layer's keys and
+values lie in pages, of which the requests share those that the prompt fills, and queries and keys are
+rotated by their positions:
+    spec_paged_append, spec_paged_attention    in place of spec_prefix_attention
+    spec_paged_commit                          beside spec_commit_rollback, by the engine
+Embedding, projections, norms and the
 prompt's own attention are plain torch. The drafts here are the tokens of a run without drafts, each
 wrong with a given probability, so that cycles accept and roll back; greedy decoding must then give
 the tokens of that run.
@@ -29,7 +34,7 @@ from mtp_speculative_decoding_spec_gb300.engine import SpecVerifyEngine  # noqa:
 class HybridTrunk:
     def __init__(self, requests, rows, capacity, dtype=torch.bfloat16, d=512, vocab=4096,
                  delta_layers=3, heads=8, key_heads=4, dk=128, dv=128, q_heads=8, kv_heads=2,
-                 head_dim=128, mode="index", seed=0, device="cuda"):
+                 head_dim=128, mode="index", seed=0, device="cuda", paged=False, page=16, rot=0):
         self.B, self.R, self.cap, self.dt, self.dev = requests, rows, capacity, dtype, device
         self.L, self.H, self.Hk, self.dk, self.dv = delta_layers, heads, key_heads, dk, dv
         self.Hq, self.Hkv, self.D = q_heads, kv_heads, head_dim
@@ -67,6 +72,11 @@ class HybridTrunk:
         st.kv_row_bytes = kv_heads * head_dim * e
         st.kv_request_stride = self.cache.stride(0) * e
         st.kv_len = self.kv_len.data_ptr()
+        self.paged, self.page, self.rot = paged, page, rot
+        if paged:
+            st.kv, st.kv_layers = None, 0
+            self.cu = torch.arange(requests + 1, dtype=torch.int32, device=device)
+            self.inv_freq = 10000.0 ** (-torch.arange(0, max(rot, 2), 2, device=device).float() / max(rot, 2))
         self.prefix = None
         self.ws = torch.zeros(256, dtype=torch.uint8, device=device)
 
@@ -104,6 +114,46 @@ class HybridTrunk:
             d.prefix_capacity, d.prefix_stride = self.prefix.shape[1], self.prefix.stride(1)
         return d
 
+    # ------------------------------------------------------------------ the paged cache
+    def _pages(self, T):
+        """A cache whose requests share the T // page pages that a prompt of T fills, and have pages of
+        their own for its rest and for `capacity` positions more."""
+        shared, own = T // self.page, -(-(T % self.page + self.cap) // self.page)
+        n = shared + self.B * own
+        self.kv_pages = torch.zeros((2, n, self.page, self.Hkv * self.D), dtype=self.dt,
+                                    device=self.dev)
+        mine = shared + torch.arange(self.B * own, dtype=torch.int32, device=self.dev).view(self.B, own)
+        self.table = torch.cat([torch.arange(shared, dtype=torch.int32, device=self.dev).expand(
+            self.B, shared), mine], 1).contiguous()
+        c = self.pc = spec.spec_paged_cache()
+        c.dtype, c.layers, c.kv_heads, c.head_dim = self.wdt, 1, self.Hkv, self.D
+        c.page_size, c.n_pages, c.max_pages = self.page, n, shared + own
+        c.k_pages, c.v_pages = self.kv_pages[0].data_ptr(), self.kv_pages[1].data_ptr()
+        c.page_stride = self.kv_pages.stride(1) * self.kv_pages.element_size()
+        c.layer_stride = n * c.page_stride
+        c.page_table, c.table_stride = self.table.data_ptr(), shared + own
+        c.kv_len = self.kv_len.data_ptr()
+        return shared
+
+    def _append(self, B, rows, k, v, q=None):
+        """New rows, `rows` of each of B requests: keys and values to their pages, queries rotated."""
+        d = spec.spec_append_desc()
+        d.k, d.v, d.k_stride, d.v_stride = k.data_ptr(), v.data_ptr(), k.stride(0), v.stride(0)
+        if q is not None:
+            d.q_heads, d.q, d.q_stride = self.Hq, q.data_ptr(), q.stride(0)
+            d.q_out, d.q_out_stride = d.q, d.q_stride
+        d.rot_dim, d.inv_freq, d.rot_scale = self.rot, self.inv_freq.data_ptr(), 1.0
+        spec.spec_paged_append(B, self.cu[:B + 1] * rows, B * rows, self.pc, 0, d)
+
+    def _attend(self, rows, q, out):
+        d = spec.spec_paged_attn_desc()
+        d.q_heads, d.scale = self.Hq, self.D ** -0.5
+        d.q, d.q_stride, d.out, d.out_stride = q.data_ptr(), q.stride(0), out.data_ptr(), out.stride(0)
+        n = spec.spec_paged_attention_workspace_bytes(self.B, self.B * rows, self.pc, d)
+        if n > self.ws.numel():
+            self.ws = torch.zeros(n, dtype=torch.uint8, device=self.dev)
+        spec.spec_paged_attention(self.B, self.cu * rows, self.B * rows, self.pc, 0, d, None, self.ws)
+
     # ------------------------------------------------------------------ prompt and cycles
     def prefill(self, prompt):
         """The prompt (a list of tokens) once for all requests; every request starts after it."""
@@ -122,13 +172,25 @@ class HybridTrunk:
             spec.spec_delta_prefill(1, cu, T, st, layer, d, None, ws)
             x = x + out @ w["o"]
         h, w = self._norm(x), self.attn
-        self.prefix = torch.stack([h @ w["k"], h @ w["v"]])
+        self.kv_len.zero_()
+        if self.paged:
+            shared = self._pages(T) * self.page
+            k, v = h @ w["k"], h @ w["v"]
+            if shared:
+                self._append(1, shared, k, v)  # by request 0, on the pages that all have
+                self.kv_len.fill_(shared)
+            rest = T - shared
+            if rest:
+                self._append(self.B, rest, k[shared:].repeat(self.B, 1), v[shared:].repeat(self.B, 1))
+                n = torch.full((self.B,), rest, dtype=torch.int32, device=self.dev)
+                spec.spec_paged_commit(self.B, self.pc, None, n)
+        else:
+            self.prefix = torch.stack([h @ w["k"], h @ w["v"]])
         # the attention layer is the last: no later layer reads the prompt's outputs of it
         self.slots.zero_()
         self.slots[:, 0] = state
         self.live.copy_(state.expand_as(self.live))
         self.live_slot.zero_()
-        self.kv_len.zero_()
         self.cache.zero_()
 
     def verify_rows(self, tokens):
@@ -140,6 +202,12 @@ class HybridTrunk:
             spec.spec_delta_rows(B, R, self.st, layer, self.mode, d)
             x = x + out @ w["o"]
         h, w = self._norm(x), self.attn
+        if self.paged:
+            q = h @ w["q"]
+            self._append(B, R, h @ w["k"], h @ w["v"], q)
+            out = torch.empty_like(q)
+            self._attend(R, q, out)
+            return self._norm(x + out @ w["o"])
         at = self.kv_len[:, None] + torch.arange(R, device=self.dev)[None]
         b = torch.arange(B, device=self.dev)[:, None].expand(B, R)
         for i, name in enumerate("kv"):
@@ -163,6 +231,8 @@ def decode(trunk, prompt, n_tokens, drafts_of=None, drafts=0):
                            device=trunk.dev)
     trunk.prefill(prompt[:-1])
     eng.attach_state(trunk.st, trunk.mode)
+    if trunk.paged:
+        eng.attach_paged(trunk.pc)
     eng.set_requests(temps=[0.0] * B, k=[k] * B)
     tokens, cycles = [[] for _ in range(B)], 0
     last = [prompt[-1] + b for b in range(B)]  # each request goes its own way
@@ -204,8 +274,10 @@ def main():
     ap.add_argument("--tokens", type=int, default=64)
     ap.add_argument("--wrong", type=float, default=0.3)
     ap.add_argument("--mode", choices=("snapshot", "replay", "index"), default="index")
+    ap.add_argument("--paged", action="store_true")
     a = ap.parse_args()
-    trunk = HybridTrunk(a.requests, a.drafts + 1, a.tokens + 16, mode=a.mode)
+    trunk = HybridTrunk(a.requests, a.drafts + 1, a.tokens + 16, mode=a.mode, paged=a.paged,
+                        rot=64 if a.paged else 0)
     g = torch.Generator().manual_seed(1)
     prompt = torch.randint(2000, (a.prompt,), generator=g).tolist()
     plain, n0 = decode(trunk, prompt, a.tokens)

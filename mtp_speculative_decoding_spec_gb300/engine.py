@@ -25,7 +25,8 @@ from . import (ACCEPT_OUT_BYTES, COUNTERS_BYTES, ROWSTATS_BYTES, SPEC_F32,
                spec_adapt_width, spec_adapt_width_mirror, spec_host_alias,
                spec_commit_rollback, spec_draft_argmax, spec_graph_capture_begin,
                spec_graph_capture_end, spec_graph_destroy, spec_graph_instantiate,
-               spec_graph_launch, spec_lmhead_verify, spec_verify_accept_greedy,
+               spec_graph_launch, spec_lmhead_verify, spec_paged_commit,
+               spec_verify_accept_greedy,
                spec_width_graph_create, spec_workspace_bytes)
 
 
@@ -79,7 +80,8 @@ class SpecVerifyEngine:
         self.pos = torch.zeros(B, dtype=torch.int64, device=dev)
         self.k = torch.full((B,), k_max, dtype=torch.int32, device=dev)
         self.commit_status = torch.zeros(B, dtype=torch.int32, device=dev)
-        self.state = None
+        self.paged_status = torch.zeros(B, dtype=torch.int32, device=dev)
+        self.state = self.paged = None
         self.dtype_bytes = 4 if wdt == SPEC_F32 else 2  # bytes per hidden-row element
         self.adaptive = adaptive_cost is not None
         self.alpha = alpha
@@ -133,6 +135,11 @@ class SpecVerifyEngine:
     def attach_state(self, desc, mode):
         """A spec_state_desc (device pointers) committed after every acceptance."""
         self.state, self.state_mode = desc, mode
+
+    def attach_paged(self, cache):
+        """A spec_paged_cache (device pointers) committed after every acceptance, alone or beside
+        attach_state's desc (which then has no KV layers of its own)."""
+        self.paged = cache
 
     # ---------------------------------------------------------------- the cycle
     def draft_step(self, i, h, gate=True, k_active=None):
@@ -192,9 +199,12 @@ class SpecVerifyEngine:
         return False
 
     def commit(self, k=None):
+        k = self.k if k is None else k
         if self.state is not None:
-            spec_commit_rollback(self.B, self.state, self.out, self.k if k is None else k,
-                                 self.state_mode, self.commit_status)
+            spec_commit_rollback(self.B, self.state, self.out, k, self.state_mode,
+                                 self.commit_status)
+        if self.paged is not None:
+            spec_paged_commit(self.B, self.paged, self.out, k, self.paged_status)
 
     def adapt(self):
         if self.adaptive:
@@ -219,7 +229,7 @@ class SpecVerifyEngine:
         for i in range(1, w + 1):
             self.draft_step(i, Hd[i - 1], gate=False)
         # the choice after this cycle is cycle n + 2's width: slot s again, on both sides
-        if self.state is None:
+        if self.state is None and self.paged is None:
             # nothing to commit: the width update can share the fused verify's launch
             fused = self.verify_accept(H[:w + 1], R=w + 1, k=k_dev, k_mirror=self.k_seen_dev[s])
         else:

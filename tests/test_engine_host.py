@@ -240,3 +240,27 @@ def test_commit_only_with_attached_state(calls):
     assert _names(calls)[-1] == "spec_commit_rollback"
     a = calls[-1][1]
     assert a[1] is desc and a[2] is e.out and a[4] == spec.SPEC_COMMIT_REPLAY
+
+
+def test_paged_cache_is_committed(calls, monkeypatch):
+    monkeypatch.setattr(eng_mod, "spec_paged_commit",
+                        lambda *a: calls.append(("spec_paged_commit", a)))
+    e = _engine()
+    cache = spec.spec_paged_cache()
+    e.attach_paged(cache)
+    e.verify_cycle(torch.zeros((B * R, d)))
+    assert _names(calls) == ["spec_lmhead_verify", "spec_accept", "spec_paged_commit"]
+    a = calls[-1][1]
+    assert a[0] == B and a[1] is cache and a[2] is e.out and a[3] is e.k and a[4] is e.paged_status
+    calls.clear()
+    e.attach_state(spec.spec_state_desc(), spec.SPEC_COMMIT_SNAPSHOT)
+    e.verify_cycle(torch.zeros((B * R, d)))
+    assert _names(calls)[-2:] == ["spec_commit_rollback", "spec_paged_commit"]
+    calls.clear()
+    # one request at host-scheduled widths: the commit reads this cycle's width before the update overwrites it
+    w = _engine(b=1, adaptive_cost=[1.0] * (K_MAX + 1), width_lag=True, fuse_greedy=True)
+    w.attach_paged(cache)
+    w.set_requests(temps=[0.0], k=[2])
+    w.cycle(torch.zeros((K_MAX + 1, d)), torch.zeros((K_MAX, 1, d)), K_MAX)
+    assert _names(calls)[-3:] == ["spec_verify_accept_greedy", "spec_paged_commit", "spec_adapt_width_mirror"]
+    assert calls[-2][1][3].data_ptr() == w.k_ring[0].data_ptr() == calls[-1][1][3].data_ptr()
