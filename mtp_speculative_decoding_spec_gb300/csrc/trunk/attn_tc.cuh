@@ -5,14 +5,14 @@
 // Per block of kBn positions: S = Q K^T (Q in TMEM, 128 rows x kBn), a row's softmax by one thread
 // (TMEM lane = row, no shuffles), the weights as bf16 back into the columns of S, O += P V with P
 // in TMEM too and V as it lies in the cache (rows of positions: the B operand is N-major).
-//   * warp 0 loads K and V blocks by TMA (a paged cache: warp 3 loads V); Q is gathered by the softmax threads into TMEM, so that
-//     its 128 rows are not read from shared memory again for every block;
+//   * warp 0 loads K and V blocks by TMA (of a paged cache K, and warp 3 V); Q is gathered by the softmax
+//     threads into TMEM, so that its 128 rows are not read from shared memory again for every block;
 //   * warp 1 issues the MMAs: S of the blocks after i goes out before O of block i, so the tensor pipe works
 //     on them while the softmax works on the others (two S buffers, or four);
-//   * warps 4..7 and 8..11 do the softmax of the blocks in turns; warp 2 (and 3) watch V (below). The
-//     reference a row's weights are taken against moves only when the row's maximum has grown by more
-//     than 2^8 (the weights stay below 256 and their sum and O are fp32, so nothing is lost), which makes
-//     rescaling O in TMEM rare.
+//   * warps 4..7 and 8..11 do the softmax of the blocks in turns; warp 2 (and 3 where it loads nothing) watch
+//     V (below). The reference a row's weights are taken against moves only when the row's maximum has grown
+//     by more than 2^8 (the weights stay below 256 and their sum and O are fp32, so nothing is lost), which
+//     makes rescaling O in TMEM rare.
 // Weights are rounded to bf16 for the tensor cores (2^-9 of each weight, as the outputs are); their
 // sum is taken in fp32 before that.
 //
@@ -21,12 +21,18 @@
 // it lands, ahead of the softmax: non-finite values that no row sees are cleared, and where a row
 // does see one, that row's share of it is added by hand and the value cleared for the tensor cores.
 //
-// 16 query heads on 4 KV heads of 256 dims: 256 rows over 63,488 shared positions and 700 own ones each,
-// 190 to 204 us with the join, by GPU and run = 1.42 to 1.32 PFLOP/s (0.73 to 0.68 of cuBLAS); a block of
-// 64 positions takes about 1,450 cycles against 1,024 of the tensor pipe, the rest the way from a block's
-// scores through its softmax to its second product, which two buffers of S hide in part. Two rows of one request over its own 63,488: 50.5
-// us = 5.2 TB/s (0.76 of a copy), eight single rows over a shared 63,488 60 us = 5.0 TB/s: HBM while the
-// blocks run, and some 18 us of launch, plan, first loads, partials and join around them.
+// The code has to be short: an SM that runs five roles fetches all of them, and loops unrolled over a role's
+// stages cost more in fetches than they saved (198 KB of code for both calls, now 120: 32 x 8 rows over 63,488
+// positions 190 -> 176 us).
+//
+// 16 query heads on 4 KV heads of 256 dims, verify rows: 256 rows over 63,488 shared positions and 700 own ones
+// each, 174 to 178 us with the join = 1.52 PFLOP/s (0.79 of cuBLAS); two rows of one request over its own
+// 63,488: 49.5 us = 5.3 TB/s (0.77 of a copy), eight single rows over a shared 63,488 60 us = 5.0 TB/s: HBM
+// while the blocks run, and some 16 us of launch, plan, first loads, partials and join around them. A paged
+// cache: 2,048 rows over 61,440 positions 1,180 to 1,220 us = 1.78 to 1.72 PFLOP/s (0.92 to 0.89), 128 dims 705
+// and 64 dims 665 (half and a quarter of the work: a block's softmax is 128 x 64 exponentials whatever the
+// head's size); 32 requests of 8 rows over 15,360 each 288 us = 6.7 TB/s (0.99 of a copy); two rows over
+// 63,488 55.5 us.
 #pragma once
 
 #include <math.h>
@@ -41,7 +47,7 @@ namespace spec {
 
 constexpr int kTm = 128;
 constexpr int kTcThreads = 12 * 32;  // producers and guards (three), MMA, eight softmax warps
-constexpr int kRing = 16;  // pieces of a CTA that its roles are told of ahead
+constexpr int kRing = 16;  // pieces of a CTA that its roles are told of ahead (a paged cache's call)
 struct PieceNote {
   int tile, head, blk0, blk1, slot, whole;  // tile -1: no more
 };
@@ -51,7 +57,7 @@ struct Number {
 };
 constexpr int kGroupThreads = 128;  // a softmax group
 template <typename P>
-constexpr int kTcSmall = kPaged<P> ? 1792 : 512;  // bytes of barriers and flags
+constexpr int kTcSmall = kPaged<P> ? 1536 : 512;  // bytes of barriers and flags
 // Registers a thread: launched with 168 (64,512 in all); the first four warps give to the softmax's
 // eight: 128 x 152 + 256 x 176 = 64,512. (104 and 200 spill in the guards: 214 us for 191.)
 constexpr int kFewRegs = 152, kSoftRegs = 176;
@@ -265,10 +271,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   // [2 NS] of a K block, which of its pages are not there. Written when the block's stage is free, which may
   // be before every warp has read an earlier block's word: two stages' worth.
   volatile uint32_t* gone = reinterpret_cast<volatile uint32_t*>(least_sm + 8);
-  // [K, V][64]: 32 of the table's entries
+  // [K, V][32] of the table's entries
   int* page_ring = const_cast<int*>(reinterpret_cast<volatile int*>(gone + 2 * NS));
-  uint64_t* ring_full = reinterpret_cast<uint64_t*>(page_ring + 128);
+  uint64_t* ring_full = reinterpret_cast<uint64_t*>(page_ring + 64);
   PieceNote* ring = reinterpret_cast<PieceNote*>(ring_full + kRing);
+  static_assert(8 * (7 * NS + 5) + 4 * (12 + 2 * NS) +
+                        (kPaged<P> ? 4 * (2 * NS + 64) + kRing * (8 + static_cast<int>(sizeof(PieceNote))) : 0) <=
+                    kTcSmall<P>,
+                "barriers and flags");
   float* row_m = reinterpret_cast<float*>(smem + Sh::kFixed + kTcSmall<P>);  // [2][128] each group's last reference
   float2* row_ml = reinterpret_cast<float2*>(row_m + 2 * kTm);       // [2][128] and sum, at a piece's end
   int32_t* cum = reinterpret_cast<int32_t*>(row_ml + 2 * kTm);
@@ -368,14 +378,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       uint64_t* const done = is_k ? kdone : vdone;
       int gi = 0, s = 0, phase = 1, i = 0;  // the next block: its stage, the stage's phase, its number
       bool ok = true;
-      auto issue_to = [&]() {  // the stage of the next block, once it is free
-        if (i >= NS && !mbar_wait_bounded(&done[s], phase)) return false;
-        return true;
-      };
-      auto step = [&]() {
-        if (++s == NS) s = 0, phase ^= 1;
-        ++i;
-      };
       bool more = true;
       while (__all_sync(0xffffffffu, ok && !*abort_flag) && (more = next_piece())) {
         const int panel = a.head * (D / 64), blk0 = a.blk0, blk1 = a.blk1;
@@ -388,61 +390,60 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const __nv_bfloat16* src = q_row<D>(p, req, a, r);
             for (int d = 0; d < D; d += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(src + d));
           }
-        {
-          const int b = attn_tile_req(p, a.tile), ps = p.c.page_size;
-          const CUtensorMap* map = is_k ? &maps.ok : &maps.ov;
-          const int32_t* table = p.c.table + static_cast<int64_t>(b) * p.c.table_stride;
-          const auto entry = [&](int j) { return j < p.c.max_pages ? __ldg(table + j) : -1; };
-          int* const pages = page_ring + (is_k ? 0 : 64);
-          int j = blk0 * BN / ps, at = blk0 * BN - j * ps;
-          // entries 32 at a time, the next ones on their way
-          int e = entry((j & ~31) + lane);
+        const int b = attn_tile_req(p, a.tile), ps = p.c.page_size;
+        const CUtensorMap* map = is_k ? &maps.ok : &maps.ov;
+        const int32_t* table = p.c.table + static_cast<int64_t>(b) * p.c.table_stride;
+        const auto entry = [&](int j) { return j < p.c.max_pages ? __ldg(table + j) : -1; };
+        int* const pages = page_ring + (is_k ? 0 : 32);
+        int j = blk0 * BN / ps, at = blk0 * BN - j * ps;
+        // entries 32 at a time, the next ones on their way
+        int e = entry((j & ~31) + lane);
 #pragma unroll 1
-          for (int w = j & ~31; left > 0; w += 32) {
-            __syncwarp();
-            pages[lane] = static_cast<unsigned>(e) < static_cast<unsigned>(p.c.n_pages) ? e : p.c.n_pages;
-            e = entry(w + 32 + lane);
-            __syncwarp();
-            if (leader) {
-              // blocks of whole pages in pages of 8 to 32 positions, or a block and a part of a page
-              const auto blocks = [&](auto number) {
-                constexpr int PER = decltype(number)::value;
+        for (int w = j & ~31; left > 0; w += 32) {
+          __syncwarp();
+          pages[lane] = static_cast<unsigned>(e) < static_cast<unsigned>(p.c.n_pages) ? e : p.c.n_pages;
+          e = entry(w + 32 + lane);
+          __syncwarp();
+          if (leader) {
+            // blocks of whole pages in pages of 8 to 32 positions, or a block and a part of a page
+            const auto blocks = [&](auto number) {
+              constexpr int PER = decltype(number)::value;
 #pragma unroll 1
-                while (left > 0 && j < w + 32) {
-                  int page[PER];
-                  uint32_t lost = 0;
+              while (left > 0 && j < w + 32) {
+                int page[PER];
+                uint32_t lost = 0;
 #pragma unroll
-                  for (int m = 0; m < PER; ++m) {
-                    page[m] = pages[j - w + m];
-                    lost |= static_cast<uint32_t>(page[m] == p.c.n_pages) << m;
-                  }
-                  ok = issue_to();
-                  if (!ok) break;
-                  if (is_k) {
-                    gone[gi] = lost;  // seen with the block: the scores' wait for it comes before the softmax's for them
-                    if (++gi == 2 * NS) gi = 0;
-                  }
-                  mbar_arrive_expect_tx(&full[s], Sh::kTile);
-#pragma unroll
-                  for (int m = 0; m < PER; ++m)
-                    tma_load_page(tiles + s * Sh::kTile + m * (Sh::kTile / PER), map, panel, at >> 3, page[m], &full[s]);
-                  at += BN;
-                  if (at >= ps) j += PER, at = 0;
-                  step();
-                  --left;
+                for (int m = 0; m < PER; ++m) {
+                  page[m] = pages[j - w + m];
+                  lost |= static_cast<uint32_t>(page[m] == p.c.n_pages) << m;
                 }
-              };
-              if (ps >= BN)
-                blocks(Number<1>());
-              else if (ps == 8)
-                blocks(Number<BN / 8>());
-              else if (ps == 16)
-                blocks(Number<BN / 16>());
-              else
-                blocks(Number<BN / 32>());
-            }
-            left = __reduce_min_sync(0xffffffffu, leader ? (ok ? left : 0) : 0x7fffffff);
+                ok = i < NS || mbar_wait_bounded(&done[s], phase);
+                if (!ok) break;
+                if (is_k) {
+                  gone[gi] = lost;  // seen with the block: the scores' wait for it comes before the softmax's for them
+                  if (++gi == 2 * NS) gi = 0;
+                }
+                mbar_arrive_expect_tx(&full[s], Sh::kTile);
+#pragma unroll
+                for (int m = 0; m < PER; ++m)
+                  tma_load_page(tiles + s * Sh::kTile + m * (Sh::kTile / PER), map, panel, at >> 3, page[m], &full[s]);
+                at += BN;
+                if (at >= ps) j += PER, at = 0;
+                if (++s == NS) s = 0, phase ^= 1;
+                ++i;
+                --left;
+              }
+            };
+            if (ps >= BN)
+              blocks(Number<1>());
+            else if (ps == 8)
+              blocks(Number<BN / 8>());
+            else if (ps == 16)
+              blocks(Number<BN / 16>());
+            else
+              blocks(Number<BN / 32>());
           }
+          left = __reduce_min_sync(0xffffffffu, leader ? (ok ? left : 0) : 0x7fffffff);
         }
       }
       if (is_k && more && lane == 0) tell(false);  // a wait ran out
