@@ -731,7 +731,7 @@ spec_status spec_paged_append(int32_t B, const int32_t *cu_rows, int64_t rows,
  * rows a request: verify rows, whole prompts and chunks of prompts, in one call.
  *   q_heads   a multiple of kv_heads, at most 64 per KV head; query head h reads KV head
  *             h / (q_heads / kv_heads).
- *   q, out    row t at q + t*q_stride (elements): [q_heads][head_dim].
+ *   q, out    row t at q + t*q_stride (elements): [q_heads][head_dim]. out does not overlap q.
  *   lse       [rows][q_heads] float32 or NULL: log sum exp(scale q k), -Inf where a row has nothing to
  *             see or scores of -Inf alone (its output is zero). Rows that a request owns and does not
  *             run give zero and -Inf. Values that are not finite show as in spec_prefix_attention: in
@@ -739,8 +739,9 @@ spec_status spec_paged_append(int32_t B, const int32_t *cu_rows, int64_t rows,
  *   workspace spec_paged_attention_workspace_bytes(B, rows, c, d) bytes, 256-byte aligned, ZERO-FILLED
  *             ONCE before its first use; the error word at byte offset 4 as in the conventions above.
  * With G = q_heads / kv_heads and tiles of 128 rows (tensor cores) or 16 (CUDA cores), rows*G / tile + B
- * is at most 4,096 and 12,288; a call beyond that is refused as SPEC_ERR_UNSUPPORTED, and the workspace
- * query gives 0 for sizes that a call would be refused for. The positions are divided over the SMs whatever
+ * is at most 4,096 and 12,288, and that times kv_heads and the blocks of positions (64 and 32) that a
+ * request has room for, 13 more for each, below 2^31; a call beyond that is refused as
+ * SPEC_ERR_UNSUPPORTED, and the workspace query gives 0 for sizes that a call would be refused for. The positions are divided over the SMs whatever
  * the requests' lengths and the parts joined in a fixed order: the same call gives the same bytes.
  */
 typedef struct {

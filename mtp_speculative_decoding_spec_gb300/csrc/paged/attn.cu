@@ -218,7 +218,9 @@ cudaError_t paged_simt_launch(const PagedParams& p, spec_dtype dtype, int grid, 
 }
 
 cudaError_t paged_join_launch(const PagedParams& p, spec_dtype dtype, int grid, cudaStream_t stream) {
-  const dim3 g(2 * grid), t(kJoinThreads);
+  // Blocks for each CTA of the attention: 2, 3, 4, 6: 1,000 rows beside 31 single tokens 122.7, 111.6, 111.3, 110.8
+  // us, a call with nothing to join 12.8, 13.2, 13.7, 14.9.
+  const dim3 g(3 * grid), t(kJoinThreads);
   return dtype == SPEC_BF16 ? launch_pdl(paged_join_kernel<__nv_bfloat16>, g, t, 0, stream, p, grid)
                             : launch_pdl(paged_join_kernel<float>, g, t, 0, stream, p, grid);
 }
