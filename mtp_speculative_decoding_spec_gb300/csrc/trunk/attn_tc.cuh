@@ -382,14 +382,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       while (__all_sync(0xffffffffu, ok && !*abort_flag) && (more = next_piece())) {
         const int panel = a.head * (D / 64), blk0 = a.blk0, blk1 = a.blk1;
         int left = blk1 - blk0;
-        if (is_k && told > 1)  // its queries, towards L2: the softmax takes them when it is done with what is before
-#pragma unroll 1
-          for (int row = lane; row < kTm; row += 32) {
-            const AttnRow r = attn_row(p, req, a.tile, row);
-            if (r.lim <= 0) continue;
-            const __nv_bfloat16* src = q_row<D>(p, req, a, r);
-            for (int d = 0; d < D; d += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(src + d));
-          }
         const int b = attn_tile_req(p, a.tile), ps = p.c.page_size;
         const CUtensorMap* map = is_k ? &maps.ok : &maps.ov;
         const int32_t* table = p.c.table + static_cast<int64_t>(b) * p.c.table_stride;
