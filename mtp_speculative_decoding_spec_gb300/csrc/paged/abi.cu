@@ -205,7 +205,7 @@ spec_status spec_paged_attention(int32_t B, const int32_t* cu_rows, int64_t rows
   while (1 << p.tm_shift < p.tm) ++p.tm_shift;
   while (1 << p.bn_shift < p.bn) ++p.bn_shift;
   p.items = w.tiles;
-  p.grp = w.tc ? kPagedGroup : 1;
+  p.grp = w.tc && w.grid >= kPagedGroup ? kPagedGroup : 1;
   p.group_min = kPagedGroupMin;
   for (p.page_shift = 0; w.tc && p.page_shift < 31 && (1 << p.page_shift) < c->page_size; ++p.page_shift) {
   }

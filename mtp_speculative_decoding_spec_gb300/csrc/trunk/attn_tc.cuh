@@ -306,7 +306,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   }
   if (warp == 1) tmem_alloc(tmem_slot, 512);
   pdl_wait();
-  if constexpr (kPaged<P>) pdl_trigger();  // the join's blocks come as these leave, and wait
+  if constexpr (kPaged<P>) {
+    pdl_trigger();  // the join's blocks come as these leave, and wait
+    if (threadIdx.x == 0) paged_splits_clear(p);  // whatever becomes of the walk, the join finds no other call's
+  }
   const auto* req = attn_plan(p, cum);  // ends with a block barrier
   tc_fence_before();
   __syncthreads();
@@ -342,7 +345,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     } else if (warp == 0) {
       const bool more = walk.next(p, cum, shares, a);
       if (lane == 0) {
-        if (told == 0) paged_splits_clear(p);
         if (more) paged_split(p, cum, shares, walk, a);
         tell(more);
       }
