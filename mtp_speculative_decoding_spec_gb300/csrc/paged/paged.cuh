@@ -68,13 +68,20 @@ constexpr int kPagedGroup = 8, kPagedGroupMin = 8192;
 // 16, 20 the prompts above 70.7, 65.7, 65.3, 63.7, 65.4 us, 32 requests of 8 rows over 15,360 positions 309.5,
 // 312.0, 311.2, 313.5, 316.6.
 constexpr int kPagedOver = 12;
-// On the tensor cores, what a whole unit may cost above an equal share of all before units are cut instead: so
-// many blocks, which is what a cut costs, and where a request has no more than a tile and 128 dims or more the
-// share's so-many-th part, since then HBM is the limit and fewer CTAs draw as much. 32 requests of 8 rows over
-// 1,000, 4,000 and 15,360 positions of 256 dims whole and cut: 33, 87, 290 and 38, 94, 309 us; 128 dims over
-// 15,360 158 and 169; 64 dims, which HBM does not limit, 132 and 119; two rows over 2,000 35 and 16. On the CUDA
-// cores nothing is gained (fp32, over 500 positions: 121 both).
-constexpr int kPagedUnitMore = 8, kPagedUnitPart = 4;
+// On the tensor cores, what the busiest CTA may have above an equal share, in blocks, before units are cut instead.
+// Where there is a CTA for every unit: what a cut costs, and where a request has no more than a tile and 128 dims
+// or more the share's so-many-th part, since then HBM is the limit and fewer CTAs draw as much. 32 requests of 8
+// rows over 1,000, 4,000 and 15,360 positions of 256 dims whole and cut: 31, 87, 288 and 36, 94, 309 us; 128 dims
+// over 15,360 158 and 169; 64 dims, which HBM does not limit, 132 and 119; two rows over 2,000 35 and 16. Where a
+// CTA has several: also the start and the partials of the units that it would have parts of, and the join. Prompts
+// of 1,000 and 2,311 rows among shorter ones of 128 dims 54 and 64, 2,311 alone 42 and 53, 64 requests of 8 rows
+// over 4,000 of 256 dims 140 and 149; 4,000 rows over 2,000 (28 above the share) 117 and 133. With 20, 32, 40
+// allowed the last 135, 117, 117; working it out for nothing costs 2 us. On the CUDA cores nothing is gained (32
+// fp32 requests over 500 positions: 121 both).
+constexpr int kPagedUnitOne = 8, kPagedUnitPart = 4, kPagedUnitMore = 32;
+// Of so many items (each finds its place by looking at all others), and so many units a CTA, whose cuts are the
+// smaller part then.
+constexpr int kPagedSort = 256, kPagedRounds = 16;
 
 struct AppendParams {
   PagedLayer c;
@@ -136,9 +143,10 @@ __device__ __forceinline__ int64_t paged_offset(const PagedParams& p, int b, int
   return paged_offset(p.c, b, pos);
 }
 
-// cum[0..items], then the counts of grouped and of all items and the costliest one's cost, then the requests.
+// cum[0..items], then the counts of grouped and of all items and what the busiest CTA has with whole units (0: not
+// worked out), then the requests, then the items by cost, where they are few.
 __host__ __device__ inline size_t attn_plan_bytes(const PagedParams& p) {
-  return sizeof(int32_t) * (p.items + 4) + sizeof(PagedReq) * p.B;
+  return sizeof(int32_t) * (p.items + 4) + sizeof(PagedReq) * p.B + sizeof(uint16_t) * kPagedSort;
 }
 __device__ __forceinline__ int attn_group_items(const PagedParams& p, const int32_t* cum) {
   return cum[p.items + 1];
@@ -146,6 +154,9 @@ __device__ __forceinline__ int attn_group_items(const PagedParams& p, const int3
 __device__ __forceinline__ int attn_items(const PagedParams& p, const int32_t* cum) { return cum[p.items + 2]; }
 __device__ __forceinline__ const PagedReq* paged_reqs(const PagedParams& p, const int32_t* cum) {
   return reinterpret_cast<const PagedReq*>(cum + p.items + 4);
+}
+__device__ __forceinline__ uint16_t* paged_order(const PagedParams& p, const int32_t* cum) {
+  return reinterpret_cast<uint16_t*>(const_cast<PagedReq*>(paged_reqs(p, cum)) + p.B);
 }
 __device__ __forceinline__ int paged_tiles(const PagedParams& p, int rows) { return (rows * p.G + p.tm - 1) >> p.tm_shift; }
 __device__ __forceinline__ int paged_groups(const PagedParams& p, int rows, int base) {
@@ -158,13 +169,15 @@ __device__ __forceinline__ int64_t attn_div(const PagedParams&, int64_t x, int64
 __device__ __forceinline__ int attn_part(const PagedParams&, int64_t x, int64_t all, int grid) {
   return min(grid, static_cast<int>(static_cast<float>(x) / static_cast<float>(all) * static_cast<float>(grid) + 0.01f));
 }
-// A unit to a CTA, where there are CTAs for all of them and the costliest is no more than `unit_more` above an
-// equal share: then no unit is cut and the join has nothing to do.
+// Whole units to a CTA, where the busiest one then has no more than `unit_more` above an equal share: no unit is cut
+// and the join has nothing to do.
 __device__ __forceinline__ bool attn_by_units(const PagedParams& p, const int32_t* cum, int64_t share) {
-  const int items = attn_items(p, cum);
-  const int64_t more = p.unit_more + (p.unit_part > 0 && items <= p.B ? share / p.unit_part : 0);
-  return attn_group_items(p, cum) == 0 && items <= static_cast<int>(gridDim.x) / p.Hkv &&
-         cum[p.items + 3] <= share + more;
+  const int worst = cum[p.items + 3], items = attn_items(p, cum);
+  if (worst == 0) return false;
+  int64_t more = p.unit_more;
+  if (items * p.Hkv <= static_cast<int>(gridDim.x))
+    more = kPagedUnitOne + (p.unit_part > 0 && items <= p.B ? share / p.unit_part : 0);
+  return worst <= share + more;
 }
 // What a request's tile sees: up to its last row's position.
 __device__ __forceinline__ int paged_sees(const PagedParams& p, const PagedReq& r, int tile) {
@@ -172,6 +185,10 @@ __device__ __forceinline__ int paged_sees(const PagedParams& p, const PagedReq& 
   return static_cast<int>(min(p.kcap, static_cast<int64_t>(r.base) + last));
 }
 
+// The unit, the costliest first, that a CTA takes in a round.
+__device__ __forceinline__ int paged_unit(int round, int cta, int grid) {
+  return round * grid + (round & 1 ? grid - 1 - cta : cta);
+}
 // As for AttnParams: by the whole block, in shared memory, a barrier at the end. Requests whose tiles would
 // be more than there can be (cu_rows not as documented) have none.
 static __device__ __noinline__ const PagedReq* attn_plan(const PagedParams& p, int32_t* cum) {
@@ -239,12 +256,13 @@ static __device__ __noinline__ const PagedReq* attn_plan(const PagedParams& p, i
   __syncthreads();
   if (tid < 32) {
     const int items = cum[p.items + 2];
-    int base = 0, most = 0;
+    int base = 0, most = 0, least = 0x7fffffff;
 #pragma unroll 1
     for (int i0 = 1; i0 <= items; i0 += 32) {
       const int i = i0 + lane;
       int v = i <= items ? cum[i] : 0;
       most = max(most, v);
+      if (i <= items) least = min(least, v);
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int x = __shfl_up_sync(0xffffffffu, v, o);
@@ -255,9 +273,58 @@ static __device__ __noinline__ const PagedReq* attn_plan(const PagedParams& p, i
       base = __shfl_sync(0xffffffffu, v, 31);
     }
     most = __reduce_max_sync(0xffffffffu, most);
-    if (lane == 0) cum[p.items + 3] = most;
+    least = __reduce_min_sync(0xffffffffu, least);
+    if (lane == 0) {
+      // 0: whole units are not for this call; 1: that is to be worked out, below
+      const int64_t units = static_cast<int64_t>(items) * p.Hkv, grid = gridDim.x;
+      int worst = 0;
+      if (p.unit_more >= 0 && cum[p.items + 1] == 0 && items > 0) {
+        if (units <= grid) {
+          worst = most;
+        } else if (items <= kPagedSort && units <= kPagedRounds * grid) {
+          const int64_t rounds = attn_div(p, units + grid - 1, grid);
+          const int64_t share = attn_div(p, static_cast<int64_t>(base) * p.Hkv + grid - 1, grid);
+          worst = rounds * least <= share + p.unit_more;
+        }
+      }
+      cum[p.items + 3] = worst;
+    }
   }
   __syncthreads();
+  // Whole units, the costliest first, dealt out forth and back over the grid: what the busiest CTA has then.
+  if (cum[p.items + 3] == 1) {
+    const int items = cum[p.items + 2], grid = gridDim.x;
+    uint16_t* order = paged_order(p, cum);
+#pragma unroll 1
+    for (int i = tid; i < items; i += nt) {
+      const int cost = cum[i + 1] - cum[i];
+      int rank = 0, from = 0;
+#pragma unroll 4
+      for (int j = 0; j < items; ++j) {
+        const int to = cum[j + 1], other = to - from;
+        from = to;
+        rank += other > cost || (other == cost && j < i);
+      }
+      order[rank] = static_cast<uint16_t>(i);
+    }
+    __syncthreads();
+    int worst = 0;
+#pragma unroll 1
+    for (int cta = tid; cta < grid; cta += nt) {
+      int sum = 0;
+#pragma unroll 1
+      for (int round = 0; round * grid < items * p.Hkv; ++round) {
+        const int u = paged_unit(round, cta, grid);
+        if (u >= items * p.Hkv) continue;
+        const int item = order[u / p.Hkv];
+        sum += cum[item + 1] - cum[item];
+      }
+      worst = max(worst, sum);
+    }
+    worst = __reduce_max_sync(0xffffffffu, worst);
+    if (lane == 0) atomicMax(cum + p.items + 3, worst);
+    __syncthreads();
+  }
   return req;
 }
 
@@ -293,6 +360,25 @@ __device__ __forceinline__ int attn_group_tile(const PagedParams& p, const int32
       hi = mid;
   }
   return ((item - req[lo].g0) * p.grp + rank) << kTileReqBits | lo;
+}
+// The next whole unit of a CTA (attn_by_units); `round` of them lie behind it.
+__device__ __forceinline__ bool attn_next_unit(const PagedParams& p, const int32_t* cum, int& round, AttnPiece& a) {
+  const int grid = gridDim.x, units = attn_items(p, cum) * p.Hkv;
+#pragma unroll 1
+  while (round * grid < units) {
+    const int u = paged_unit(round++, blockIdx.x, grid);
+    if (u >= units) continue;
+    const int rank = u / p.Hkv, item = units > grid ? paged_order(p, cum)[rank] : rank;
+    a.blk0 = 0;
+    a.blk1 = cum[item + 1] - cum[item] - p.over[1];
+    if (a.blk1 <= 0) continue;
+    a.whole = true;
+    a.head = u - rank * p.Hkv;
+    a.tile = attn_single_tile(p, cum, item);
+    a.slot = 0;
+    return true;
+  }
+  return false;
 }
 __device__ __forceinline__ AttnRow attn_row(const PagedParams& p, const PagedReq* req, int tile, int i) {
   AttnRow a;

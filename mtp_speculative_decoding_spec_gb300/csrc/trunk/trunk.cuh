@@ -198,7 +198,7 @@ __device__ __forceinline__ bool attn_by_units(const AttnParams&, const int32_t*,
 struct AttnShares {
   int64_t wp, w, sp, s1, s2;
   int in, u1, base1;
-  bool units;  // instead: a unit to a CTA (a paged cache's call)
+  bool units;  // instead: whole units to a CTA (a paged cache's call)
   __device__ __forceinline__ int64_t single_at(int cta) const {  // where a CTA's part of the rest begins
     return cta < in ? s1 * cta : s1 * in + s2 * (cta - in);
   }
@@ -286,6 +286,8 @@ struct AttnPiece {
   bool whole;
 };
 
+__device__ __forceinline__ bool attn_next_unit(const AttnParams&, const int32_t*, int&, AttnPiece&) { return false; }
+
 // One piece after another of a CTA's shares. Only the start of a share is looked for; from there on the
 // next unit follows.
 struct AttnWalk {
@@ -314,10 +316,7 @@ struct AttnWalk {
   __device__ __forceinline__ void start(const P& p, const int32_t* cum, const AttnShares& s) {
     group = !s.units && static_cast<int>(blockIdx.x) < s.in;
     if (s.units) {
-      left = at = 0;
-      item = blockIdx.x / p.Hkv;
-      head = blockIdx.x % p.Hkv;
-      if (item < attn_items(p, cum)) left = cum[item + 1] - cum[item];
+      at = 0;
     } else if (group) {
       const int64_t x = s.sp * (blockIdx.x / p.grp);
       seek(p, cum, x, min(s.wp, x + s.sp));
@@ -334,6 +333,7 @@ struct AttnWalk {
   }
   template <typename P>
   __device__ __forceinline__ bool next(const P& p, const int32_t* cum, const AttnShares& s, AttnPiece& a) {
+    if (s.units) return attn_next_unit(p, cum, at, a);
 #pragma unroll 1
     for (;;) {
       if (left <= 0) {

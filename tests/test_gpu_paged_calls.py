@@ -42,6 +42,25 @@ def test_requests_of_like_lengths(spec, D, H, Hq, page, long):  # noqa: F811
     a.check()
 
 
+@pytest.mark.parametrize("D,H,Hq,page,lens,kv_len", [
+    (128, 16, 32, 16, [0, 1, 77, 300, 600], [5, 90, 100, 40, 0]),
+    (64, 8, 16, 64, [700, 3, 650], [0, 200, 100]),
+    (256, 8, 8, 32, [3] * 30, [200 + 7 * b for b in range(30)]),
+    (256, 2, 8, 8, [500, 0, 1, 1, 1, 300] * 3, [30 * b for b in range(18)]),
+    # far more than an equal share, so that units are cut all the same
+    (128, 4, 4, 128, [1] * 39 + [2], [20] * 39 + [4000]),
+    (64, 1, 2, 16, [1] * 255 + [5], [b % 50 for b in range(256)]),
+    (64, 1, 2, 16, [1] * 256 + [5], [b % 50 for b in range(257)]),
+])
+def test_several_units_of_a_cta(spec, D, H, Hq, page, lens, kv_len):  # noqa: F811
+    """More units than SMs, dealt out whole by their costs, or cut; a page that is not there among them."""
+    c = Cache(len(lens), -(-max(p + n for p, n in zip(kv_len, lens)) // page), page, H, D, "bf16", kv_len, seed=26)
+    c.table[2, 0] = -1
+    a = Attn(c, lens, Hq, seed=26)
+    a.run(spec)
+    a.check()
+
+
 def test_a_page_twice_in_a_table(spec):  # noqa: F811
     c = Cache(2, 8, 16, 2, 128, "bf16", [100, 90], seed=22)
     c.table[0, 3] = c.table[0, 1]
