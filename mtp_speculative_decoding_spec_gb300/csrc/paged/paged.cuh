@@ -57,16 +57,17 @@ __device__ __forceinline__ PagedRows paged_rows(const int32_t* cu, const int32_t
 
 constexpr int kPagedMaxCtas = 512;
 
-// Tiles of a request that walk the same positions side by side (152 SMs are 19 eights), and from how many
-// positions on. 2,048 rows of 16 heads on 4 of 256 dims over 61,440 positions, groups of 1, 4, 8, 16: 1,469,
-// 1,231, 1,192, 1,197 us; prompts of 1,000 and 2,311 rows among shorter ones 64 to 65 with all of them. From
-// 0, 2,048, 8,192, 32,768 positions on: those prompts 80, 73, 65, 65 us, four times 512 rows over 30,000
-// 364, 364, 364, 485.
+// Tiles of a request that walk the same positions side by side (152 SMs are 19 eights), and above how many
+// positions that its rows see in the mean. 2,048 rows of 16 heads on 4 of 256 dims over 61,440 positions, groups of
+// 1, 4, 8, 16: 1,469, 1,231, 1,192, 1,197 us. With groups and without: 512 rows over 20,000 four times 259 and 338
+// us (128 dims), 463 and 636 (256); 2,048 over 9,000 143 and 157; prompts of 49,152 from their start 7,588 and 8,658,
+// 13,067 and 15,569; of 16,384 904 and 798, 1,386 and 1,401; of 8,192 273 and 219, 395 and 389; 4,096 rows over 6,000
+// 219 and 210: from the start tiles see so much less than a group's last one, and groups take no whole units.
 constexpr int kPagedGroup = 8, kPagedGroupMin = 8192;
 
-// `over` on the tensor cores (trunk.cuh), for grouped tiles (4 to 16: no difference) and single ones: 6, 9, 12,
-// 16, 20 the prompts above 70.7, 65.7, 65.3, 63.7, 65.4 us, 32 requests of 8 rows over 15,360 positions 309.5,
-// 312.0, 311.2, 313.5, 316.6.
+// `over` on the tensor cores (trunk.cuh), for grouped tiles (4 to 16: no difference) and single ones. All units
+// cut, 6, 9, 12, 16, 20: prompts of 1,000 and 2,311 rows among shorter ones 70.7, 65.7, 65.3, 63.7, 65.4 us, 32
+// requests of 8 rows over 15,360 positions 309.5, 312.0, 311.2, 313.5, 316.6.
 constexpr int kPagedOver = 12;
 // On the tensor cores, what the busiest CTA may have above an equal share, in blocks, before units are cut instead.
 // Where there is a CTA for every unit: what a cut costs, and where a request has no more than a tile and 128 dims
@@ -132,7 +133,7 @@ struct PagedParams : AttnParams {
   int64_t rows;
   int tm_shift, bn_shift;    // log2 of tm and bn
   int unit_more, unit_part;  // attn_by_units (-1: never; part 0: none)
-  int group_min;          // positions from which a request's tiles are grouped
+  int group_min;          // mean positions above which a request's tiles are grouped
   int page_shift;         // tensor cores: positions (log2) of a block's part on one page, 31 where that is all
   PagedSplit* splits;     // [2 CTAs]
 };
@@ -161,7 +162,7 @@ __device__ __forceinline__ uint16_t* paged_order(const PagedParams& p, const int
 __device__ __forceinline__ int paged_tiles(const PagedParams& p, int rows) { return (rows * p.G + p.tm - 1) >> p.tm_shift; }
 __device__ __forceinline__ int paged_groups(const PagedParams& p, int rows, int base) {
   const int n = paged_tiles(p, rows);
-  return p.grp > 1 && n >= p.grp && base + rows >= p.group_min ? n / kPagedGroup : 0;
+  return p.grp > 1 && n >= p.grp && base + rows / 2 > p.group_min ? n / kPagedGroup : 0;
 }
 __device__ __forceinline__ int64_t attn_div(const PagedParams&, int64_t x, int64_t y) {  // all below 2^31
   return static_cast<uint32_t>(x) / static_cast<uint32_t>(y);
