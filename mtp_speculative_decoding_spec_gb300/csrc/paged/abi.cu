@@ -17,7 +17,8 @@ spec_status cache_check(int32_t B, const spec_paged_cache* c) {
   if (c->layers < 1 || c->kv_heads < 1 || c->head_dim < 8 || c->head_dim % 8 != 0 || c->page_size < 1 ||
       c->n_pages < 1 || c->max_pages < 1 || c->table_stride < c->max_pages)
     return SPEC_ERR_INVALID;
-  if (B > kPagedMaxB || c->head_dim > 256 || c->kv_heads > kPagedMaxHeads || c->layers > 65536) return SPEC_ERR_UNSUPPORTED;
+  if (B > kPagedMaxB || c->head_dim > 256 || c->kv_heads > kPagedMaxHeads || c->layers > 65536)
+    return SPEC_ERR_UNSUPPORTED;
   if (c->n_pages >= (int64_t(1) << 31) || static_cast<int64_t>(c->max_pages) * c->page_size > kAttnMaxPos)
     return SPEC_ERR_UNSUPPORTED;
   return SPEC_OK;

@@ -18,7 +18,7 @@
 //
 // HBM bounds it where there are many rows: a prompt of 15,360 rows of 16 + 2 x 4 heads of 256 dims, a quarter
 // rotated, with norms, 65 us = 5.8 TB/s of bytes read and written (0.86 of a copy); 3,389 rows of 16 + 2 x 8 heads
-// of 128, all rotated, 13.4 (11.3 from L2); and latency where there are few: 32 x 8 rows 5.2, one request of two
+// of 128, all rotated, 13.4 (11.3 from L2); and latency where there are few: 32 x 8 rows 4.7, one request of two
 // 2.8 (in a graph).
 #include <cuda_bf16.h>
 
@@ -34,10 +34,15 @@ constexpr int kAppendWarps = 16;
 
 enum : int { ROT_NONE = 0, ROT_SIDE = 1, ROT_HALF = 2, ROT_HALF_ODD = 3 };
 
+// Blocks an SM, which bounds the registers: 15,360 bf16 rows 72 us with three, 65 with four (fp32's registers, and
+// those of pairs that end inside a lane, do not fit so).
 template <typename T, int ROT, int STEP>
 constexpr int kMinBlocks = ROT == ROT_HALF_ODD ? 1 : sizeof(T) == 2 && STEP ? 4 : 3;
-template <typename T>
-constexpr int kBatchOf = sizeof(T) == 2 ? 4 : 2;  // heads of a lane side by side
+// Heads of a lane side by side. Two and four: 15,360 bf16 rows of 16 + 2 x 4 heads of 256 dims 81 and 65 us; where
+// a warp has fewer than two fours of a row's queries (or keys) none is on its way while another is worked on: 8,000
+// rows of 16 + 2 x 8 heads of 64 dims 12.9 and 15.7, 32 x 8 rows of the first 4.7 and 5.2. fp32, one and two:
+// 15,360 rows 141 and 127.
+constexpr int kBatchMany = 4, kBatchFew = 2;
 
 template <typename T>
 struct Eight;  // eight elements as they lie in memory
@@ -169,11 +174,11 @@ __device__ __forceinline__ void lds8(const float* p, float* x) {
   }
 }
 
-// WHOLE: rows of q, k, v and q_out are whole 16-byte vectors. STEP: elements that a warp's heads take, 0 where
-// D is no power of two and the host's number counts.
-template <typename T, int ROT, bool WHOLE, int STEP>
-__global__ void __launch_bounds__(kThreads, kMinBlocks<T, ROT, STEP>) append_kernel(const __grid_constant__ AppendParams p) {
-  constexpr int kBatch = kBatchOf<T>;
+// WHOLE: rows of q, k, v and q_out are whole 16-byte vectors (element by element 15,360 rows take 161 us for 65).
+// STEP: elements that a warp's heads take, 0 where D is no power of two and the host's number counts (73 us for 65).
+template <typename T, int ROT, bool WHOLE, int STEP, int kBatch>
+__global__ void __launch_bounds__(kThreads, kMinBlocks<T, ROT, STEP>)
+    append_kernel(const __grid_constant__ AppendParams p) {
   __shared__ __align__(32) float weights[2][256];       // of queries and keys
   __shared__ __align__(32) float2 trig[kWarps][128];    // cos and sin of a warp's row
   __shared__ uint64_t freq[128];                        // turns a position
@@ -218,7 +223,8 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks<T, ROT, STEP>) append_ker
     lds8(weight + e0, w);
     if constexpr (ROT == ROT_SIDE || ROT == ROT_HALF) {
       const bool on = e0 < p.rot;
-      const float* from = reinterpret_cast<const float*>(trig[wid] + (!on ? 0 : ROT == ROT_SIDE ? e0 / 2 : low ? e0 : e0 - half));
+      const int first = !on ? 0 : ROT == ROT_SIDE ? e0 / 2 : low ? e0 : e0 - half;
+      const float* from = reinterpret_cast<const float*>(trig[wid] + first);
       lds8(from, cs);
       if (ROT == ROT_HALF) lds8(from + 8, cs + 8);
       lds8(ROT == ROT_SIDE ? weight + e0 : weight + (!on ? 0 : low ? e0 + half : e0 - half), v);
@@ -423,12 +429,20 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks<T, ROT, STEP>) append_ker
   }
 }
 
+template <typename T, int ROT, bool WHOLE, int STEP>
+cudaError_t launch_batch(const AppendParams& p, dim3 grid, cudaStream_t stream) {
+  if constexpr (sizeof(T) == 2)
+    if (min(max(p.cq, p.ck), p.per_task) >= 2 * kBatchMany)
+      return launch_pdl(append_kernel<T, ROT, WHOLE, STEP, kBatchMany>, grid, dim3(kThreads), 0, stream, p);
+  return launch_pdl(append_kernel<T, ROT, WHOLE, STEP, kBatchFew>, grid, dim3(kThreads), 0, stream, p);
+}
+
 template <typename T, int ROT>
 cudaError_t launch_rot(const AppendParams& p, dim3 grid, cudaStream_t stream) {
   const bool pow2 = p.tph * 8 == p.D;  // 32 lanes of eight dims are whole heads then
-  if (!p.whole) return launch_pdl(append_kernel<T, ROT, false, 0>, grid, dim3(kThreads), 0, stream, p);
-  return pow2 ? launch_pdl(append_kernel<T, ROT, true, 256>, grid, dim3(kThreads), 0, stream, p)
-              : launch_pdl(append_kernel<T, ROT, true, 0>, grid, dim3(kThreads), 0, stream, p);
+  return !p.whole ? launch_batch<T, ROT, false, 0>(p, grid, stream)
+         : pow2   ? launch_batch<T, ROT, true, 256>(p, grid, stream)
+                  : launch_batch<T, ROT, true, 0>(p, grid, stream);
 }
 
 template <typename T>

@@ -168,7 +168,8 @@ __device__ __forceinline__ int64_t attn_div(const PagedParams&, int64_t x, int64
   return static_cast<uint32_t>(x) / static_cast<uint32_t>(y);
 }
 __device__ __forceinline__ int attn_part(const PagedParams&, int64_t x, int64_t all, int grid) {
-  return min(grid, static_cast<int>(static_cast<float>(x) / static_cast<float>(all) * static_cast<float>(grid) + 0.01f));
+  const float part = static_cast<float>(x) / static_cast<float>(all) * static_cast<float>(grid);
+  return min(grid, static_cast<int>(part + 0.01f));
 }
 // Whole units to a CTA, where the busiest one then has no more than `unit_more` above an equal share: no unit is cut
 // and the join has nothing to do.

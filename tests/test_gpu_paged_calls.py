@@ -7,7 +7,8 @@ import pytest
 import torch
 
 from oracle import paged as o_pg
-from test_gpu_paged import EPS, Attn, Cache, acc_of, cu_of, i32, npf, spec, tol, torch_dt  # noqa: F401
+from test_gpu_paged import (EPS, Attn, Cache, acc_of, cu_of, i32, npf, run_append, spec, tol,  # noqa: F401
+                            torch_dt)
 
 pytestmark = pytest.mark.gpu
 
@@ -59,6 +60,15 @@ def test_several_units_of_a_cta(spec, D, H, Hq, page, lens, kv_len):  # noqa: F8
     a = Attn(c, lens, Hq, seed=26)
     a.run(spec)
     a.check()
+
+
+@pytest.mark.parametrize("dtype,D,rot,pairs,pad", [
+    ("bf16", 64, 64, "half", 0), ("bf16", 64, 64, "side", 0), ("bf16", 64, 20, "half", 0), ("bf16", 64, 0, "half", 0),
+    ("bf16", 40, 16, "half", 0), ("bf16", 64, 32, "half", 3), ("f32", 64, 48, "half", 0)])
+def test_append_of_many_rows(spec, dtype, D, rot, pairs, pad):  # noqa: F811
+    """As many rows as let a warp take several of a row's heads after one another."""
+    c = Cache(3, 80, 16, 1, D, dtype, [3, 7, 40], seed=27)
+    run_append(spec, c, cu_of([1200, 0, 800]), 2005, 32, rot, pairs, True, pad=pad, in_place=pad == 0, seed=27)
 
 
 def test_a_page_twice_in_a_table(spec):  # noqa: F811
