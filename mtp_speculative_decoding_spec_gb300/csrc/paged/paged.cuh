@@ -159,10 +159,12 @@ __device__ __forceinline__ const PagedReq* paged_reqs(const PagedParams& p, cons
 __device__ __forceinline__ uint16_t* paged_order(const PagedParams& p, const int32_t* cum) {
   return reinterpret_cast<uint16_t*>(const_cast<PagedReq*>(paged_reqs(p, cum)) + p.B);
 }
-__device__ __forceinline__ int paged_tiles(const PagedParams& p, int rows) { return (rows * p.G + p.tm - 1) >> p.tm_shift; }
+__device__ __forceinline__ int paged_tiles(const PagedParams& p, int rows) {
+  return (rows * p.G + p.tm - 1) >> p.tm_shift;
+}
 __device__ __forceinline__ int paged_groups(const PagedParams& p, int rows, int base) {
   const int n = paged_tiles(p, rows);
-  return p.grp > 1 && n >= p.grp && base + rows / 2 > p.group_min ? n / kPagedGroup : 0;
+  return p.grp > 1 && n >= p.grp && static_cast<int64_t>(base) + rows / 2 > p.group_min ? n / kPagedGroup : 0;
 }
 __device__ __forceinline__ int64_t attn_div(const PagedParams&, int64_t x, int64_t y) {  // all below 2^31
   return static_cast<uint32_t>(x) / static_cast<uint32_t>(y);

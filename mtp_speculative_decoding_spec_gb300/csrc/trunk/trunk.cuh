@@ -190,6 +190,7 @@ __device__ __forceinline__ int attn_part(const AttnParams&, int64_t x, int64_t a
   return static_cast<int>(x * grid / all);  // of the grid, what x is of all
 }
 
+// Whether units are dealt out whole, where an equal share is so much.
 __device__ __forceinline__ bool attn_by_units(const AttnParams&, const int32_t*, int64_t) { return false; }
 
 // How the costs are dealt out: the groups' part [0, wp), `sp` to each group, and the rest up to w: `s1`
@@ -292,7 +293,7 @@ __device__ __forceinline__ bool attn_next_unit(const AttnParams&, const int32_t*
 // next unit follows.
 struct AttnWalk {
   int64_t left;        // costs of the share still to walk
-  int item, head, at;  // the unit, and where in its costs
+  int item, head, at;  // the unit, and where in its costs (whole units: the rounds behind)
   bool group;          // the groups' part is being walked
   template <typename P>
   __device__ __forceinline__ void seek(const P& p, const int32_t* cum, int64_t x, int64_t x1) {
