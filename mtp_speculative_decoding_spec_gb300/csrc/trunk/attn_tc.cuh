@@ -648,11 +648,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const float scale = fmaxf(fabsf(p.scale_log2), 1e-45f);  // so that a masked score is -Inf whatever the scale
     int it = 0;
     // A wait that runs out ends all further waiting, not the walk: whatever happens, a softmax warp
-    // goes through the same pieces as the others, which it meets at `meet` and at named barriers.
+    // goes through the same pieces as the others, which it meets at `meet` and at named barriers. Of verify rows
+    // each walks for itself, all alike; of a paged cache each waits for the note of a piece with a limit of its
+    // own, so they take the piece if all have its note and otherwise leave together (`agreed`).
     bool ok = true;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       if (!ok || mbar_wait_warp(bar, parity)) return;
       if (lane == 0) give_up();
+      __syncwarp();
       ok = false;
     };
     uint32_t met_all = 0, met_group = 0;
@@ -660,6 +663,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&meet[2]);
       wait(&meet[2], met_all++ & 1);
+    };
+    // Whether every softmax warp says so. A barrier without a limit, which ends: the warps come to it once a
+    // piece and once after the last one, their waits before it have limits, and all go on as it says.
+    auto agreed = [&](bool mine) {
+      __syncwarp();
+      uint32_t all;
+      asm volatile(
+          "{\n\t.reg .pred m, a;\n\tsetp.ne.u32 m, %1, 0;\n\tbar.red.and.pred a, 13, 256, m;\n\t"
+          "selp.u32 %0, 1, 0, a;\n\t}"
+          : "=r"(all)
+          : "r"(static_cast<uint32_t>(mine))
+          : "memory");
+      return all != 0;
     };
     auto bar_group = [&]() {  // of the group's
       __syncwarp();
@@ -669,7 +685,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // Q of a piece: this thread's half of its row into its TMEM lane; a negative scale goes into Q's signs
     int piece = 0, least = 0;
     AttnRow ar;
-    auto load_q = [&](const AttnPiece& pc) {
+    auto fetch_q = [&](const AttnPiece& pc) {
       ar = attn_row(p, req, pc.tile, row);
       const uint32_t flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;
       const __nv_bfloat16* src = q_row<D>(p, req, pc, ar);
@@ -706,9 +722,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       if (lane == 0 && half == 0) lsm[quad] = lo;
       if (st == 0 && half == 0) o_init[piece & 1] = 0;
       tc_fence_before();
-      bar_all();
+    };
+    auto load_q = [&](const AttnPiece& pc, bool more) {  // whether there is a piece
+      if (more) fetch_q(pc);
+      if constexpr (kPaged<P>)
+        more = agreed(more);
+      else if (more)
+        bar_all();
+      if (!more) return false;
       if (lane == 0) mbar_arrive(qready);
+      const int* lsm = least_sm + 4 * (piece & 1);
       least = min(min(lsm[0], lsm[1]), min(lsm[2], lsm[3]));
+      return true;
     };
     int lim = 0, slot = 0, tile = 0, head = 0;  // of the piece in work
     bool whole = false;
@@ -783,7 +808,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     };
     bool more = next_piece();
     for (;;) {
-      if (more) load_q(a);
+      more = load_q(a, more);
       if (piece > 0) output();  // of the piece before, while this one's first scores are computed
       if (!more) break;
       lim = ar.lim, slot = a.slot, tile = a.tile, head = a.head;
