@@ -227,13 +227,20 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks<T, ROT, STEP>)
       const float* from = reinterpret_cast<const float*>(trig[wid] + first);
       lds8(from, cs);
       if (ROT == ROT_HALF) lds8(from + 8, cs + 8);
-      lds8(ROT == ROT_SIDE ? weight + e0 : weight + (!on ? 0 : low ? e0 + half : e0 - half), v);
+      // a dim that is not turned takes nothing of another, whose weight need not be finite
+      if (ROT == ROT_SIDE || on) {
+        lds8(weight + (ROT == ROT_SIDE ? e0 : low ? e0 + half : e0 - half), v);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = 0.f;
+      }
       float c[8], s[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const bool there = ROT == ROT_SIDE ? e0 + j < p.rot : on;
         c[j] = there ? cs[ROT == ROT_SIDE ? j & ~1 : 2 * j] : 1.f;
         s[j] = there ? cs[ROT == ROT_SIDE ? j | 1 : 2 * j + 1] : 0.f;
+        if (ROT == ROT_SIDE && !there) v[j ^ 1] = 0.f;  // pairs are turned both or neither
         if (ROT == ROT_SIDE ? (j & 1) == 0 : low) s[j] = -s[j];
       }
 #pragma unroll

@@ -1,0 +1,53 @@
+"""The paged cache's calls at the edges of what spec.h allows: weights that are not finite, most heads, lengths
+past every position, pages of other sizes, many rows that do not run. Tolerances and helpers as in
+test_gpu_paged."""
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import paged as o_pg
+from test_gpu_paged import EPS, Cache, i32, npf, spec, torch_dt  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------------------------------------- append
+@pytest.mark.parametrize("what", [float("inf"), -float("inf"), float("nan")])
+@pytest.mark.parametrize("dtype,D,rot,pairs", [
+    ("bf16", 128, 64, "half"), ("f32", 64, 32, "half"), ("bf16", 128, 64, "side"), ("f32", 64, 20, "side"),
+    ("bf16", 96, 32, "half"), ("bf16", 64, 20, "half"), ("f32", 64, 0, "half")])
+def test_a_weight_that_is_not_finite_shows_in_its_dim_and_its_pairs(spec, dtype, D, rot, pairs, what):  # noqa: F811
+    """y = w x / rms of its own dim only, so a dim that is not turned shows its own weight alone."""
+    H, Hq, n = 2, 3, 3
+    dt = torch_dt[dtype]
+    half = torch.finfo(dt).eps / 2
+    g = torch.Generator(device="cuda").manual_seed(D + rot)
+    x = torch.randn((n, (Hq + 2 * H) * D), generator=g, device="cuda").to(dt)
+    f = 1e4 ** (-torch.arange(max(rot // 2, 1), device="cuda", dtype=torch.float32) / max(rot // 2, 1))
+    x64 = npf(x).astype(np.float64).reshape(n, Hq + 2 * H, D)
+    for at in sorted({0, 7, max(rot - 1, 0), rot % D, D - 1}):
+        w = [1 + 0.3 * torch.randn(D, generator=g, device="cuda") for _ in range(2)]
+        w[0][at] = w[1][at] = what
+        c = Cache(1, 2, 8, H, D, dtype, [5])
+        out = torch.zeros((n, Hq * D), dtype=dt, device="cuda")
+        d, e = spec.spec_append_desc(), x.element_size()
+        d.q_heads, d.norm_eps, d.rot_dim, d.rot_interleaved, d.rot_scale = Hq, EPS, rot, pairs == "side", 1.0
+        d.q, d.k, d.v = (x.data_ptr() + e * i * D for i in (0, Hq, Hq + H))
+        d.q_stride = d.k_stride = d.v_stride = x.stride(0)
+        d.q_out, d.q_out_stride, d.inv_freq = out.data_ptr(), out.stride(0), f.data_ptr()
+        d.q_norm, d.k_norm = (v.data_ptr() for v in w)
+        spec.spec_paged_append(1, i32([0, n]), n, c.desc(spec), 0, d)
+        got_q, (k, _) = npf(out).astype(np.float64).reshape(n, Hq, D), c.np(0)
+        table = c.table.cpu().numpy()[0]
+        for r in range(n):
+            page, i = o_pg.place(table, 5 + r, 8, c.n_pages)
+            for got, src, v in [(got_q[r], x64[r, :Hq], w[0]), (k[page, i], x64[r, Hq:Hq + H], w[1])]:
+                for h in range(len(got)):
+                    with np.errstate(invalid="ignore"):
+                        want = o_pg.turned(src[h], 5 + r, npf(v), EPS, rot, pairs == "side", npf(f), 1.0)
+                    fin = np.isfinite(want)
+                    assert np.array_equal(got[h][~fin], want[~fin], equal_nan=True), (at, r, h)
+                    top = np.abs(want[fin]).max()
+                    assert (np.abs(got[h][fin] - want[fin]) <=
+                            half * np.abs(want[fin]) + 32 * 2.0 ** -24 * top).all(), (at, r, h)
