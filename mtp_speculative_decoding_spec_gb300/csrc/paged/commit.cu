@@ -37,7 +37,8 @@ __global__ void __launch_bounds__(256) paged_commit_kernel(const __grid_constant
     uint4* to = reinterpret_cast<uint4*>((plane & 1 ? p.c.v : p.c.k) + (plane >> 1) * p.layer_stride + at);
     for (int i = lane; i < vecs; i += 32) to[i] = make_uint4(0u, 0u, 0u, 0u);
   }
-  // every block has read the length
+  // every block has read the length (the stores above are some lanes': the barrier takes whole warps)
+  __syncwarp();
   asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
   if (blockIdx.x == 0 && tid == 0) {
     if (!bad) p.c.kv_len[b] = len;
