@@ -472,8 +472,9 @@ cudaError_t append_launch(AppendParams& p, spec_dtype dtype, bool interleaved, i
   // row where there are many, which then forms its angles once (two rows to a warp: 70 us for 67).
   const int64_t warps = static_cast<int64_t>(sms) * kAppendWarps;
   const int64_t per = (p.rows * p.iters + warps - 1) / warps;
-  p.per_task = static_cast<int>(max(int64_t(1) + p.iters / 65536, min(per, static_cast<int64_t>(p.iters))));
-  const int parts = max(1, (p.iters + p.per_task - 1) / p.per_task);
+  p.per_task = static_cast<int>(max(int64_t(1), min(per, static_cast<int64_t>(p.iters))));
+  // (so a row has no more parts than there are such warps, which a grid's y holds; no rows: the status alone)
+  const int parts = p.rows > 0 ? max(1, (p.iters + p.per_task - 1) / p.per_task) : 1;
   const int64_t blocks = max(int64_t(1), (p.rows + kWarps - 1) / kWarps);
   const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(parts));
   return dtype == SPEC_BF16 ? launch<__nv_bfloat16>(p, interleaved, grid, stream)

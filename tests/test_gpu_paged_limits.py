@@ -51,3 +51,33 @@ def test_a_weight_that_is_not_finite_shows_in_its_dim_and_its_pairs(spec, dtype,
                     top = np.abs(want[fin]).max()
                     assert (np.abs(got[h][fin] - want[fin]) <=
                             half * np.abs(want[fin]) + 32 * 2.0 ** -24 * top).all(), (at, r, h)
+
+
+@pytest.mark.parametrize("Hq,H", [(1, 65535), (65535, 65536), (65536, 65536)])
+@pytest.mark.parametrize("n", [0, 1, 2])
+def test_append_of_the_most_heads(spec, Hq, H, n):  # noqa: F811
+    """131,071 turns of a warp for a row, 196,607 and 196,608: no more parts of one than a grid has. Without rows
+    too, where the call still says that every request is well."""
+    D = 136
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.randn((n, (Hq + 2 * H) * D), generator=g, device="cuda").to(torch.bfloat16)
+    pages = torch.zeros((2, 3, 1, H * D), dtype=torch.bfloat16, device="cuda")
+    table, kv_len = i32([[2, 0]]), torch.zeros(1, dtype=torch.int64, device="cuda")
+    out = torch.zeros((n, Hq * D), dtype=torch.bfloat16, device="cuda")
+    c, d = spec.spec_paged_cache(), spec.spec_append_desc()
+    c.dtype, c.layers, c.kv_heads, c.head_dim = spec.SPEC_BF16, 1, H, D
+    c.page_size, c.n_pages, c.max_pages, c.table_stride = 1, 3, 2, 2
+    c.k_pages, c.v_pages, c.page_stride = pages[0].data_ptr(), pages[1].data_ptr(), H * D * 2
+    c.page_table, c.kv_len = table.data_ptr(), kv_len.data_ptr()
+    d.q_heads, d.rot_dim, d.rot_scale = Hq, 0, 1.0
+    d.q, d.k, d.v = (x.data_ptr() + 2 * i * D for i in (0, Hq, Hq + H))
+    d.q_stride = d.k_stride = d.v_stride = x.stride(0)
+    d.q_out, d.q_out_stride = out.data_ptr(), out.stride(0)
+    status = torch.full((1,), 9, dtype=torch.int32, device="cuda")
+    spec.spec_paged_append(1, i32([0, n]), n, c, 0, d, None, status)
+    # without norms and rotation everything is copied
+    assert status.tolist() == [0] and torch.equal(out, x[:, :Hq * D])
+    at = [2, 0][:n]
+    assert torch.equal(pages[0, at, 0], x[:, Hq * D:(Hq + H) * D])
+    assert torch.equal(pages[1, at, 0], x[:, (Hq + H) * D:])
+    assert not pages[:, [2, 0][n:] + [1]].any()
