@@ -136,8 +136,6 @@ spec_status spec_paged_append(int32_t B, const int32_t* cu_rows, int64_t rows,
   const DevAttr a = dev_attr();
   if (a.sms <= 0) return SPEC_ERR_CUDA;
   p.B = B;
-  p.Hq = d->q_heads;
-  p.Hkv = c->kv_heads;
   p.D = c->head_dim;
   p.nq = d->q_heads;
   p.nk = d->k ? c->kv_heads : 0;

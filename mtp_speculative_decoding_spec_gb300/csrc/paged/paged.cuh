@@ -86,7 +86,7 @@ constexpr int kPagedSort = 256, kPagedRounds = 16;
 
 struct AppendParams {
   PagedLayer c;
-  int B, Hq, Hkv, D;
+  int B, D;
   int nq, nk;            // query heads, and key heads, that are processed (values: as many as keys)
   int64_t rows;
   const int32_t *cu_rows, *n_rows;
