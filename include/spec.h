@@ -647,7 +647,7 @@ size_t spec_prefix_attention_workspace_bytes(int32_t B, int32_t R, const spec_st
  *   dtype        of the pages and of q, k, v and out: SPEC_BF16 or SPEC_F32.
  *   head_dim     a multiple of 8 up to 256 (else SPEC_ERR_UNSUPPORTED).
  *   page_size    positions a page, >= 1. Attention in bf16 runs on the tensor cores where head_dim
- *                is 64, 128 or 256 and page_size 8, 16, 32, 64 or a multiple of 128, else on the
+ *                is 64, 128 or 256 and page_size 8, 16, 32 or a multiple of 64, else on the
  *                CUDA cores.
  *   k_pages, v_pages, layer_stride, page_stride   multiples of 16 bytes; layers and pages do not overlap.
  *   page_table   [B][max_pages] int32 in rows of table_stride entries. An entry outside [0, n_pages) is

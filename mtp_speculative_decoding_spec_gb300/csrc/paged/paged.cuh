@@ -449,13 +449,13 @@ __device__ __forceinline__ void paged_split(const PagedParams& p, const int32_t*
 
 cudaError_t paged_simt_launch(const PagedParams& p, spec_dtype dtype, int grid, cudaStream_t stream);
 cudaError_t paged_join_launch(const PagedParams& p, spec_dtype dtype, int grid, cudaStream_t stream);
+int paged_tc_bn();
 // Page sizes of the tensor-core kernel: a block of its positions is whole pages or lies on one, and a page has
 // at least the eight rows of the operands' swizzle.
 inline bool paged_tc_takes(int head_dim, int page_size) {
-  return attn_tc_takes(head_dim) && (page_size == 8 || page_size == 16 || page_size == 32 || page_size == 64 ||
-                                     page_size % 128 == 0);
+  return attn_tc_takes(head_dim) && page_size % 8 == 0 &&
+         (page_size % paged_tc_bn() == 0 || paged_tc_bn() % page_size == 0);
 }
-int paged_tc_bn();
 spec_status paged_tc_launch(const PagedParams& p, int grid, EncodeTiledFn encode, cudaStream_t stream);
 
 }  // namespace spec

@@ -7,7 +7,7 @@ import pytest
 import torch
 
 from oracle import paged as o_pg
-from test_gpu_paged import EPS, Cache, i32, npf, spec, torch_dt  # noqa: F401
+from test_gpu_paged import EPS, Attn, Cache, i32, npf, spec, torch_dt  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -81,3 +81,30 @@ def test_append_of_the_most_heads(spec, Hq, H, n):  # noqa: F811
     assert torch.equal(pages[0, at, 0], x[:, Hq * D:(Hq + H) * D])
     assert torch.equal(pages[1, at, 0], x[:, (Hq + H) * D:])
     assert not pages[:, [2, 0][n:] + [1]].any()
+
+
+# ---------------------------------------------------------------------------------- attention
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("page,layout", [(192, "pools"), (320, "pages"), (4160, "pools"), (48, "pools")])
+def test_pages_of_whole_blocks(spec, D, page, layout):  # noqa: F811
+    """Pages of three and five blocks of positions, and a cache per request in one page; a page that is not there
+    among several, lengths on either side of pages' ends, what masked positions hold."""
+    lens, kv_len = [5, 130, 0, 3, 70], [page - 2, 0, 4, 2 * page, 300]
+    pages = -(-max(n + P for n, P in zip(lens, kv_len)) // page)
+    c = Cache(5, pages, page, 2, D, "bf16", kv_len, layers=2, layout=layout, seed=41)
+    a = Attn(c, lens, 6, layer=1, seed=41)
+    a.run(spec)
+    a.check()
+    clean = a.out.clone()
+    for b, (n, P) in enumerate(zip(lens, kv_len)):  # behind the last row's position
+        for x in (c.k, c.v):
+            if (P + n) % page:
+                x[1, c.table[b, (P + n) // page].long(), (P + n) % page:] = float("nan")
+    a.run(spec)
+    assert torch.equal(a.out, clean)
+    c.table[3, 1] = -1
+    c.table[4, 0] = c.n_pages
+    for x in (c.k, c.v):
+        x.nan_to_num_(nan=0.5)
+    a.run(spec)
+    a.check()
