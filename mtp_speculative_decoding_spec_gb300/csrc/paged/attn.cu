@@ -32,8 +32,12 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, const float* v) {
 // there is to do is found from the CTAs' notes (PagedSplit), not from the rows: a warp to each row and head
 // of 2,311 rows of 16 heads took 30 us. (The last CTA to come to a unit joining it in the attention kernel
 // saved this launch and took 18 us more at two rows over 63,488 positions: code that each SM fetches anew.)
-// And rows that requests own and do not run become zero.
-template <typename T>
+// And rows that requests own and do not run become zero (Fill): by the blocks of their request, or by all, a warp
+// to a row. Of a request of 8,192 rows (16 heads of 256 dims over 1,000 positions) that runs three, a call by one
+// block 1,232 us, by all 27; 32 requests of 1 to 8 rows 36.2 by theirs (38.1 by one each), 38.7 by all.
+enum class Fill { kNone, kBlocks, kWarps };
+constexpr int kFillRows = 8, kFillRequests = 64;  // of a request in the mean, and requests, for kBlocks
+template <typename T, Fill FILL>
 __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_constant__ PagedParams p, int ctas) {
   __shared__ int first[2 * kPagedMaxCtas + 1];  // of the rows before each unit's
   __shared__ int4 notes[2 * kPagedMaxCtas];
@@ -43,8 +47,21 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, Hq = p.Hkv * p.G;
   pdl_wait();
   const auto rows_of = [&](int b) { return paged_rows(p.cu_rows, p.n_rows, p.rows, b); };
-  PagedRows own = {0, 0, 0};  // the request whose rows this block fills up first, below
-  if (static_cast<int>(blockIdx.x) < p.B) own = rows_of(blockIdx.x);
+  // (here, so that what they wait for comes with the notes)
+  int row = 0, end = 0;  // this block's rows to clear, every parts-th
+  if (const int part = blockIdx.x / p.B; FILL == Fill::kBlocks && part < static_cast<int>(gridDim.x) / p.B) {
+    const PagedRows own = rows_of(blockIdx.x - part * p.B);
+    row = own.start + own.runs + part, end = own.start + own.owned;
+  }
+  const auto idles = [&](int64_t at) {  // by a warp
+    const int b = paged_request_of(p.cu_rows, p.B, at);
+    if (b >= p.B) return false;
+    const PagedRows r = rows_of(b);
+    return at - r.start >= r.runs;
+  };
+  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * kJoinWarps + warp;
+  bool idle = false;
+  if (FILL == Fill::kWarps && row0 < p.rows) idle = idles(row0);
   constexpr int kEach = 2 * kPagedMaxCtas / kJoinThreads;
   int n[kEach], sum = 0;  // a thread's units, and the rows of them and of those before
 #pragma unroll
@@ -195,19 +212,35 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
     }
     if (few) __syncthreads();  // the parts are no longer read
   }
+  const auto clear = [&](int64_t row, int i, int n) {  // by n threads, of which this is i
+    const float zero[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int64_t d = i * 4; d < static_cast<int64_t>(Hq) * p.D; d += n * 4)
+      store4(static_cast<T*>(p.out) + row * p.os + d, zero);
+    if (p.lse)
+      for (int h = i; h < Hq; h += n) p.lse[row * Hq + h] = -INFINITY;
+  };
+  if constexpr (FILL == Fill::kBlocks) {
 #pragma unroll 1
-  for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
-    const PagedRows r = b == static_cast<int>(blockIdx.x) ? own : rows_of(b);
+    for (const int parts = gridDim.x / p.B; row < end; row += parts) clear(row, threadIdx.x, kJoinThreads);
+  }
+  if constexpr (FILL == Fill::kWarps) {
 #pragma unroll 1
-    for (int i = r.runs; i < r.owned; ++i) {
-      const int64_t row = r.start + i;
-      const float zero[4] = {0.f, 0.f, 0.f, 0.f};
-      for (int d = threadIdx.x * 4; d < Hq * p.D; d += kJoinThreads * 4)
-        store4(static_cast<T*>(p.out) + row * p.os + d, zero);
-      if (p.lse)
-        for (int h = threadIdx.x; h < Hq; h += kJoinThreads) p.lse[row * Hq + h] = -INFINITY;
+    for (int64_t t = row0; t < p.rows;) {
+      if (idle) clear(t, lane, 32);
+      t += static_cast<int64_t>(gridDim.x) * kJoinWarps;
+      if (t < p.rows) idle = idles(t);
     }
   }
+}
+
+template <typename T>
+cudaError_t launch_join(const PagedParams& p, dim3 g, int ctas, cudaStream_t stream) {
+  const dim3 t(kJoinThreads);
+  if (!p.n_rows) return launch_pdl(paged_join_kernel<T, Fill::kNone>, g, t, 0, stream, p, ctas);
+  // a block to a request at least, and not so many rows that one request's could be the most of the time
+  if (p.B <= kFillRequests && static_cast<int>(g.x) >= p.B && p.rows <= int64_t(kFillRows) * p.B)
+    return launch_pdl(paged_join_kernel<T, Fill::kBlocks>, g, t, 0, stream, p, ctas);
+  return launch_pdl(paged_join_kernel<T, Fill::kWarps>, g, t, 0, stream, p, ctas);
 }
 
 }  // namespace
@@ -222,9 +255,8 @@ cudaError_t paged_join_launch(const PagedParams& p, spec_dtype dtype, int grid, 
   // us, a call with nothing to join 12.8, 13.2, 13.7, 14.9.
   // And no more than rows and heads (8 and 32 of them: 12.8 and 55.7 us with all blocks, 12.0 and 54.8).
   const int64_t rows = p.rows * p.Hkv * p.G;
-  const dim3 g(static_cast<unsigned>(max(int64_t(1), min(int64_t(3) * grid, rows)))), t(kJoinThreads);
-  return dtype == SPEC_BF16 ? launch_pdl(paged_join_kernel<__nv_bfloat16>, g, t, 0, stream, p, grid)
-                            : launch_pdl(paged_join_kernel<float>, g, t, 0, stream, p, grid);
+  const dim3 g(static_cast<unsigned>(max(int64_t(1), min(int64_t(3) * grid, rows))));
+  return dtype == SPEC_BF16 ? launch_join<__nv_bfloat16>(p, g, grid, stream) : launch_join<float>(p, g, grid, stream);
 }
 
 }  // namespace spec

@@ -108,3 +108,20 @@ def test_pages_of_whole_blocks(spec, D, page, layout):  # noqa: F811
         x.nan_to_num_(nan=0.5)
     a.run(spec)
     a.check()
+
+
+@pytest.mark.parametrize("dtype,D,Hq,pad", [("bf16", 64, 4, 0), ("bf16", 128, 6, 3), ("f32", 64, 4, 0), ("f32", 72, 2, 1)])
+def test_many_rows_that_requests_own_and_do_not_run(spec, dtype, D, Hq, pad):  # noqa: F811
+    """A padded batch: slots of thousands of rows of which a few run, all or none; rows behind and before them."""
+    lens, runs = [6000, 5, 0, 3000, 40, 700], [3, 0, 0, 1, 40, 0]
+    c = Cache(6, 20, 16, 2, D, dtype, [200, 7, 5, 0, 100, 30], seed=42)
+    a = Attn(c, lens, Hq, n_rows=runs, pad=pad, first=9, extra=11, seed=42)
+    a.run(spec)
+    a.check()
+    d, out = a.desc(spec), a.out.clone()  # without lse
+    d.lse = None
+    a.out.fill_(7.0)
+    n = spec.spec_paged_attention_workspace_bytes(6, a.rows, c.desc(spec), d)
+    spec.spec_paged_attention(6, i32(a.cu), a.rows, c.desc(spec), 0, d, i32(runs),
+                              torch.zeros(n, dtype=torch.uint8, device="cuda"))
+    assert torch.equal(a.out, out)
