@@ -134,12 +134,23 @@ class SpecVerifyEngine:
 
     def attach_state(self, desc, mode):
         """A spec_state_desc (device pointers) committed after every acceptance."""
+        self._check_lengths(desc, self.paged)
         self.state, self.state_mode = desc, mode
 
     def attach_paged(self, cache):
         """A spec_paged_cache (device pointers) committed after every acceptance, alone or beside
-        attach_state's desc (which then has no KV layers of its own)."""
+        attach_state's desc, whose KV layers, if it has any, then keep lengths of their own."""
+        self._check_lengths(self.state, cache)
         self.paged = cache
+
+    @staticmethod
+    def _check_lengths(desc, cache):
+        """Each commit moves the lengths of its cache: one kv_len in both would move twice."""
+        if (getattr(desc, "kv_layers", 0) > 0 and cache is not None
+                and desc.kv_len == cache.kv_len):
+            raise ValueError("the state's KV layers and the paged cache share one kv_len, which "
+                             "both commits would move: give the state no KV layers, or lengths "
+                             "of its own")
 
     # ---------------------------------------------------------------- the cycle
     def draft_step(self, i, h, gate=True, k_active=None):
