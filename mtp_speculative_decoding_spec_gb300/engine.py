@@ -135,12 +135,14 @@ class SpecVerifyEngine:
     def attach_state(self, desc, mode):
         """A spec_state_desc (device pointers) committed after every acceptance."""
         self._check_lengths(desc, self.paged)
+        self._drop_width_graph()
         self.state, self.state_mode = desc, mode
 
     def attach_paged(self, cache):
         """A spec_paged_cache (device pointers) committed after every acceptance, alone or beside
         attach_state's desc, whose KV layers, if it has any, then keep lengths of their own."""
         self._check_lengths(self.state, cache)
+        self._drop_width_graph()
         self.paged = cache
 
     @staticmethod
@@ -286,6 +288,13 @@ class SpecVerifyEngine:
                 finally:
                     spec_graph_capture_end(stream)
         self.graph_exec = spec_graph_instantiate(self.graph)
+
+    def _drop_width_graph(self):
+        """The next cycle captures anew: the graph's bodies hold the commits of what was attached."""
+        if self.graph is not None:
+            if self.device.type == "cuda":  # a launch of it may be running
+                torch.cuda.synchronize(self.device)
+            self.close()
 
     def close(self):
         """Release the width graph, if any (the engine's tensors are freed by PyTorch)."""

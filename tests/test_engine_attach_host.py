@@ -40,3 +40,24 @@ def test_a_state_without_kv_layers_or_with_lengths_of_its_own_is_taken(calls, mo
         attach()
     e.verify_cycle(torch.zeros((B * R, d)))
     assert _names(calls)[-2:] == ["spec_commit_rollback", "spec_paged_commit"]
+
+
+def test_what_is_attached_after_a_width_graph_is_committed_too(calls, monkeypatch):  # noqa: F811
+    """The graph's bodies hold the commits: it is captured anew."""
+    monkeypatch.setattr(eng_mod, "spec_paged_commit", lambda *a: calls.append(("spec_paged_commit", a)))
+    st, c = pair(0, None, 4096)
+    e = _engine(b=1, adaptive_cost=[1.0, 1.5, 2.0, 2.5])
+    H, Hd = torch.ones((K_MAX + 1, d)), torch.ones((K_MAX, 1, d))
+    e.cycle(H, Hd, K_MAX)
+    assert e.graph_exec is not None and "spec_paged_commit" not in _names(calls)
+    for attach, name in ((lambda: e.attach_paged(c), "spec_paged_commit"),
+                         (lambda: e.attach_state(st, spec.SPEC_COMMIT_SNAPSHOT), "spec_commit_rollback")):
+        calls.clear()
+        attach()
+        e.cycle(H, Hd, K_MAX)
+        names = _names(calls)
+        assert names[:2] == ["spec_graph_destroy", "spec_width_graph_create"]
+        assert names.count(name) == K_MAX + 1 and names[-1] == "spec_graph_launch"
+        calls.clear()
+        e.cycle(H, Hd, K_MAX)
+        assert _names(calls) == ["spec_graph_launch"]
