@@ -358,13 +358,13 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks<T, ROT, STEP>)
     const PagedRows pr = paged_rows(p.cu_rows, p.n_rows, p.rows, b);
     const int64_t r = row - pr.start;
     if (r < 0 || r >= pr.runs) return;
-    const int64_t P = max(static_cast<int64_t>(0), p.c.kv_len[b]), pos = P + r;
+    const int64_t P = paged_len(p.c, b), pos = P + r;
     // where the row's keys and values go, in bytes from the layer's first page
     const int64_t page_at = p.nk > 0 && pos < static_cast<int64_t>(p.c.max_pages) * p.c.page_size
                                 ? paged_offset(p.c, b, static_cast<int>(pos))
                                 : -1;
     if constexpr (ROT != ROT_NONE) {
-      const uint64_t turn = static_cast<uint64_t>(p.pos ? p.pos[b] + r : pos);
+      const uint64_t turn = static_cast<uint64_t>(p.pos ? p.pos[b] : P) + static_cast<uint64_t>(r);
 #pragma unroll 1
       for (int n = lane; n < half; n += 32) {
         const uint32_t part = static_cast<uint32_t>((freq[n] * turn) >> 32);
@@ -420,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks<T, ROT, STEP>)
     const int64_t warps = static_cast<int64_t>(gridDim.x) * kWarps;
     for (int64_t b = blockIdx.y == 0 ? warp : p.B; b < p.B; b += warps) {
       const int n = paged_rows(p.cu_rows, p.n_rows, p.rows, static_cast<int>(b)).runs;
-      const int64_t P = max(static_cast<int64_t>(0), p.c.kv_len[b]);
+      const int64_t P = paged_len(p.c, static_cast<int>(b));
       const int64_t cap = static_cast<int64_t>(p.c.max_pages) * p.c.page_size;
       bool bad = n > 0 && P + n > cap;
       if (n > 0 && P < cap) {

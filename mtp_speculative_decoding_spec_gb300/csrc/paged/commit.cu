@@ -14,7 +14,7 @@ constexpr unsigned kCommitBlocks = 8;
 __global__ void __launch_bounds__(256) paged_commit_kernel(const __grid_constant__ PagedCommitParams p) {
   pdl_wait();
   const int b = blockIdx.y, tid = threadIdx.x;
-  const int64_t P = max(static_cast<int64_t>(0), p.c.kv_len[b]);
+  const int64_t P = paged_len(p.c, b);
   const int64_t cap = static_cast<int64_t>(p.c.max_pages) * p.c.page_size;
   const int k = p.k[b];
   int64_t len = P, lo = 0, hi = 0;  // the new length, and the positions to clear

@@ -20,6 +20,12 @@ struct PagedLayer {
   int row_bytes, page_size, n_pages, max_pages;
 };
 
+// The positions in the cache before the call's rows: none where negative, and so few that no position of a row
+// overflows (past the table all are alike).
+__device__ __forceinline__ int64_t paged_len(const PagedLayer& c, int b) {
+  return max(static_cast<int64_t>(0), min(c.kv_len[b], static_cast<int64_t>(1) << 62));
+}
+
 // Bytes from the layer's first page to a position of request b, or -1 where its page is not there.
 __device__ __forceinline__ int64_t paged_offset(const PagedLayer& c, int b, int pos) {
   const int j = pos / c.page_size;

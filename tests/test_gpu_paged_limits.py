@@ -7,7 +7,7 @@ import pytest
 import torch
 
 from oracle import paged as o_pg
-from test_gpu_paged import EPS, Attn, Cache, i32, npf, spec, torch_dt  # noqa: F401
+from test_gpu_paged import EPS, Attn, Cache, acc_of, cu_of, i32, npf, run_append, spec, torch_dt  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -125,3 +125,32 @@ def test_many_rows_that_requests_own_and_do_not_run(spec, dtype, D, Hq, pad):  #
     spec.spec_paged_attention(6, i32(a.cu), a.rows, c.desc(spec), 0, d, i32(runs),
                               torch.zeros(n, dtype=torch.uint8, device="cuda"))
     assert torch.equal(a.out, out)
+
+
+# ------------------------------------------------------------------------- lengths past everything
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_lengths_near_the_end_of_their_type(spec, dtype):  # noqa: F811
+    """As any length past the table: nothing is written or cleared and the status says so; rows attend to all that
+    is there."""
+    top = 2 ** 63 - 1
+    lens = [top, top - 1, top - 3, 2 ** 62, 2 ** 31 - 3, 2 ** 32, -2 ** 63, 20]
+    c = Cache(8, 3, 16, 2, 64, dtype, [0] * 8, seed=43)
+    c.kv_len.copy_(torch.tensor(lens, dtype=torch.int64))
+    before = c.store.clone()
+    n = 4
+    run_append(spec, c, cu_of([n] * 8), n * 8, 4, 0, "half", True, seed=43)  # its status too
+    assert all(torch.equal(x[:, c.table[:6].reshape(-1).long()], y[:, c.table[:6].reshape(-1).long()])
+               for x, y in zip(c.store, before))
+    a = Attn(c, [n] * 8, 4, seed=43)
+    a.run(spec)
+    a.check()
+    before = c.store.clone()
+    st = torch.full((8,), 9, dtype=torch.int32, device="cuda")
+    spec.spec_paged_commit(8, c.desc(spec), acc_of(spec, [1] * 8), i32([3] * 8), st)
+    assert st.tolist() == [spec.REQ_KV_OVERFLOW] * 6 + [0, 0]
+    assert (c.kv_len[:6] >= 2 ** 31 - 3).all() and c.kv_len.tolist()[3:] == [x + 1 for x in lens[3:6]] + [1, 21]
+    keep = torch.ones(c.n_pages, dtype=torch.bool, device="cuda")
+    keep[c.table[6:].reshape(-1).long()] = False
+    assert all(torch.equal(x[:, keep], y[:, keep]) for x, y in zip(c.store, before))
+    spec.spec_paged_commit(8, c.desc(spec), None, i32([3] * 8), st)
+    assert st.tolist() == [spec.REQ_KV_OVERFLOW] * 6 + [0, 0] and (c.kv_len[:6] > 0).all()
