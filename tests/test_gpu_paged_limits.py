@@ -154,3 +154,20 @@ def test_lengths_near_the_end_of_their_type(spec, dtype):  # noqa: F811
     assert all(torch.equal(x[:, keep], y[:, keep]) for x, y in zip(c.store, before))
     spec.spec_paged_commit(8, c.desc(spec), None, i32([3] * 8), st)
     assert st.tolist() == [spec.REQ_KV_OVERFLOW] * 6 + [0, 0] and (c.kv_len[:6] > 0).all()
+
+
+# --------------------------------------------------------------------- values of their descriptions
+@pytest.mark.parametrize("pairs", ["half", "side"])
+@pytest.mark.parametrize("dtype,pos", [("f32", [-7, -60000]), ("bf16", [-1, -(2 ** 20)])])
+def test_positions_before_zero_turn_backwards(spec, pairs, dtype, pos):  # noqa: F811
+    c = Cache(2, 3, 16, 2, 64, dtype, [5, 9], seed=44)
+    run_append(spec, c, [0, 3, 7], 7, 4, 64, pairs, True, pos=pos, seed=44)
+
+
+@pytest.mark.parametrize("dtype,D,page", [("bf16", 64, 16), ("bf16", 128, 64), ("bf16", 256, 32), ("f32", 64, 16)])
+def test_a_scale_of_zero_gives_the_mean(spec, dtype, D, page):  # noqa: F811
+    c = Cache(3, -(-200 // page), page, 2, D, dtype, [100, 3, 126], seed=45)
+    c.table[0, 0] = -1
+    a = Attn(c, [5, 1, 40], 4, scale=0.0, n_rows=[5, 1, 38], seed=45)
+    a.run(spec)
+    a.check()
