@@ -648,7 +648,8 @@ size_t spec_prefix_attention_workspace_bytes(int32_t B, int32_t R, const spec_st
  *   head_dim     a multiple of 8 up to 256 (else SPEC_ERR_UNSUPPORTED).
  *   page_size    positions a page, >= 1. Attention in bf16 runs on the tensor cores where head_dim
  *                is 64, 128 or 256 and page_size 8, 16, 32 or a multiple of 64, else on the
- *                CUDA cores.
+ *                CUDA cores, which suit verify rows: long chunks take them longer than products in
+ *                torch would.
  *   k_pages, v_pages, layer_stride, page_stride   multiples of 16 bytes; layers and pages do not overlap.
  *   page_table   [B][max_pages] int32 in rows of table_stride entries. An entry outside [0, n_pages) is
  *                a page that is not there: nothing is written to its positions, and no row sees them.
@@ -699,7 +700,9 @@ typedef struct {
  *                    2^31 cost no accuracy.
  *   rot_scale        factor on cos and sin (1 where the scaling has none).
  *   pos              [B] int64 or NULL: the rotation's position of each request's first row (after a
- *                    prefix kept elsewhere); NULL: kv_len[b].
+ *                    prefix kept elsewhere, or at positions of the caller's own); NULL: kv_len[b].
+ *                    spec_paged_attention sees the pages alone: a caller with a prefix elsewhere
+ *                    attends to that by itself and joins the two outputs by their lse.
  *   status           [B] int32 or NULL: SPEC_REQ_KV_OVERFLOW where rows of the request lie past its table
  *                    or on pages that are not there (those are not written), else SPEC_REQ_OK.
  * kv_len is not moved: spec_paged_commit does that.
@@ -741,8 +744,9 @@ spec_status spec_paged_append(int32_t B, const int32_t *cu_rows, int64_t rows,
  * With G = q_heads / kv_heads and tiles of 128 rows (tensor cores) or 16 (CUDA cores), rows*G / tile + B
  * is at most 4,096 and 12,288, and that times kv_heads and the blocks of positions (64 and 32) that a
  * request has room for, 13 more for each, below 2^31; a call beyond that is refused as
- * SPEC_ERR_UNSUPPORTED, and the workspace query gives 0 for sizes that a call would be refused for. The positions are divided over the SMs whatever
- * the requests' lengths and the parts joined in a fixed order: the same call gives the same bytes.
+ * SPEC_ERR_UNSUPPORTED, and the workspace query gives 0 for sizes that a call would be refused for. The
+ * positions are divided over the SMs whatever the requests' lengths and the parts joined in a fixed order: the
+ * same call gives the same bytes.
  */
 typedef struct {
   int32_t q_heads;

@@ -17,9 +17,10 @@
 // lane that has it before anything is done to them (two bf16 a shuffle), in packed fp32.
 //
 // HBM bounds it where there are many rows: a prompt of 15,360 rows of 16 + 2 x 4 heads of 256 dims, a quarter
-// rotated, with norms, 65 us = 5.8 TB/s of bytes read and written (0.86 of a copy); 3,389 rows of 16 + 2 x 8 heads
-// of 128, all rotated, 13.4 (11.3 from L2); and latency where there are few: 32 x 8 rows 4.7, one request of two
-// 2.8 (in a graph).
+// rotated, with norms, 65 us = 5.8 TB/s of bytes read and written (0.86 of a copy). A few thousand are a round of
+// the warps that fit at once and part of another: 3,389 rows of 16 + 2 x 8 heads of 128, all rotated, on 2,432 warps
+// 13.4 us, and 11.3 with all of it in L2. Latency where there are few: 32 x 8 rows 4.7, one request of two 2.7 (in a
+// graph).
 #include <cuda_bf16.h>
 
 #include "paged.cuh"

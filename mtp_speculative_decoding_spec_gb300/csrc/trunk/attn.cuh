@@ -50,8 +50,11 @@ constexpr int kPsPitch = kSimtTm + 4;  // floats between positions' weights
 // four rows each. Values: a thread takes four consecutive dims of one, two or four rows. A block in which
 // some row's positions end takes only the positions a row sees, one by one, so what a masked position
 // holds reaches no row. fp32, 4 rows of 16 heads on 4 KV heads of 256 dims over 50,000 positions: 190 us = 2.2
-// TB/s, 32 TFLOP/s; bound by shared memory (a piece of K serves four rows, one of V four) and the three
+// TB/s, 17 TFLOP/s; bound by shared memory (a piece of K serves four rows, one of V four) and the three
 // barriers a block. Two rows of 64 dims over 258 positions 8.0 us with the join: two launches' latency.
+// Over pages 10 to 16 TFLOP/s with full tiles (a table's entry for each piece): 2,048 rows over 61,440 of 16 heads on
+// 4 of 256 fp32 dims 157 ms, of 96 bf16 dims 81, two and a half and two times what products in torch take (58, 40);
+// 32 requests of 1 to 8 fp32 rows over 2,000 400 us, two rows over 63,488 337.
 template <typename P, typename T>
 __global__ void __launch_bounds__(kSimtThreads, 1) attn_simt_kernel(const __grid_constant__ P p) {
   extern __shared__ __align__(16) uint8_t smem[];

@@ -29,10 +29,10 @@
 // each, 174 to 178 us with the join = 1.52 PFLOP/s (0.79 of cuBLAS); two rows of one request over its own
 // 63,488: 49.5 us = 5.3 TB/s (0.77 of a copy), eight single rows over a shared 63,488 60 us = 5.0 TB/s: HBM
 // while the blocks run, and some 16 us of launch, plan, first loads, partials and join around them. A paged
-// cache: 2,048 rows over 61,440 positions 1,180 to 1,220 us = 1.78 to 1.72 PFLOP/s (0.92 to 0.89), 128 dims 700
-// and 64 dims 665 (half and a quarter of the work: a block's softmax is 128 x 64 exponentials whatever the
-// head's size); 32 requests of 8 rows over 15,360 each 288 us = 6.7 TB/s (0.99 of a copy); two rows over
-// 63,488 56 us.
+// cache: 2,048 rows over 61,440 positions 1,180 to 1,400 us by the clock that the power limit leaves, single calls
+// the least (1.78 to 1.50 PFLOP/s, 0.92 of cuBLAS's burst to 0.88 of its long loop), 128 dims 700 to 760 and 64 dims
+// 650 (half and a quarter of the work: a block's softmax is 128 x 64 exponentials whatever the head's size); 32
+// requests of 8 rows over 15,360 each 287 us = 6.7 TB/s (0.99 of a copy); two rows over 63,488 55 us.
 #pragma once
 
 #include <math.h>
@@ -261,7 +261,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   uint64_t* pready = vok + NS;
   uint64_t* prest = pready + NS;
   uint64_t* qready = prest + NS;
-  uint64_t* meet = qready + 1;    // the softmax warps, [0] and [1] of a group, [2] all
+  uint64_t* meet = qready + 1;    // the softmax warps, [0] and [1] of a group, [2] all (verify rows)
   uint64_t* ofree = meet + 3;     // the piece's O has been read
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ofree + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
