@@ -171,3 +171,19 @@ def test_a_scale_of_zero_gives_the_mean(spec, dtype, D, page):  # noqa: F811
     a = Attn(c, [5, 1, 40], 4, scale=0.0, n_rows=[5, 1, 38], seed=45)
     a.run(spec)
     a.check()
+
+
+@pytest.mark.parametrize("B,R,Hq,H,D,dtype", [
+    (1, 8, 4, 2, 64, "bf16"), (5, 1, 1, 1, 64, "bf16"), (64, 8, 4, 2, 128, "bf16"), (65, 8, 4, 2, 128, "bf16"),
+    (300, 3, 2, 1, 64, "bf16"), (512, 2, 1, 1, 64, "f32"), (64, 8, 2, 1, 64, "f32")])
+def test_few_rows_of_many_requests_that_do_not_run(spec, B, R, Hq, H, D, dtype):  # noqa: F811
+    """By the blocks of a request up to 64 of them and eight rows each, by a warp to a row above; one request that
+    owns them all among others that own none."""
+    c = Cache(B, 4, 16, H, D, dtype, [b % 37 for b in range(B)], seed=46)
+    a = Attn(c, [R] * B, Hq, n_rows=[(3 * b) % (R + 1) for b in range(B)], first=2, extra=3, seed=46)
+    a.run(spec)
+    a.check()
+    c = Cache(B, 40, 16, H, D, dtype, [b % 37 for b in range(B)], seed=47)
+    a = Attn(c, [0] * (B - 1) + [R * B], Hq, n_rows=[0] * (B - 1) + [2], first=1, seed=47)
+    a.run(spec)
+    a.check()
